@@ -10,7 +10,11 @@
  *     resident 64-chunk pages, followed by the top-k (k <= 1024, normally 512);
  *   - the same score for many prefill queries against dense chunk keys under
  *     the causal chunk limit, followed by the top-k;
- *   - the top-k select itself over caller-provided scores.
+ *   - the top-k select itself over caller-provided scores;
+ *   - the attention that reads the selection: the per-head norm and rotation
+ *     of its queries and cells, and one softmax over the selected chunk cells,
+ *     the first tokens and a sliding window of tokens (also for a tree of
+ *     drafted tokens).
  *
  * Sources (page titles as published):
  *   [FM] "FlashMemory-DeepSeek-V4: Lightning Index Ultra-Long Context via
@@ -39,7 +43,8 @@
  *     host validates every argument before the first launch; on a non-OK
  *     return nothing was enqueued (FM_ERR_CUDA: a launch failed; earlier
  *     launches of the same call may have been enqueued).
- *   - n_h must be 64 and d must be 128 (the C4Indexer's sizes).
+ *   - n_h must be 64 and d must be 128 (the C4Indexer's sizes) unless an entry
+ *     point says otherwise.
  *   - Ties in a top-k are broken by the lower chunk id.  Selected ids are
  *     written in ascending id order and padded with -1 (scores with -inf).
  *   - Kernels never trap and never spin without a bound.  A device-detected
@@ -422,6 +427,117 @@ fm_status fm_index_prefill_scores(const uint16_t* q, const float* w, const int64
 fm_status fm_index_prefill_topk(const uint16_t* q, const float* w, const int64_t* pos, const uint16_t* keys,
                                 int T, int64_t S, int n_h, int d, int ratio, int k, int32_t* idx_out,
                                 float* score_out, void* workspace, size_t workspace_bytes, fm_stream_t stream);
+
+/*
+ * Norm of each query and key head, and the position rotation, in one pass
+ * ([V4] sec. 2: the chunk cells get RMSNorm and the rotary embedding before
+ * they enter the cache; [RM] "Hyperparameters": YaRN).  For a row x of d
+ * elements (one head of token t) and its gain g:
+ *     y = x / sqrt(mean(x^2) + eps) * g
+ * then the pairs (start + 2i, start + 2i + 1), start = d - rope_dim, turn by the
+ * angle pos[t] * theta'_i, with theta'_i the YaRN frequency of fm_query_chain
+ * (base^(-2i/rope_dim), rope_factor, rope_orig_len, rope_beta_fast / _slow;
+ * rope_factor 1 is the plain rotary embedding).  fp32 throughout, the angle's
+ * fraction of a turn in 64-bit fixed point; one rounding, to bf16.
+ *
+ *   pos       [T] int64 token positions
+ *   q         [T, n_q, d] bf16, token stride q_stride_t elements (a slice of a
+ *             fused projection's output will do); q_gain [d] bf16 or NULL (ones)
+ *   q_out     [T, n_q, d] bf16, dense; may be q itself where that is dense
+ *   k         [T, n_k, d] bf16, token stride k_stride_t; k_gain [d] or NULL
+ *   k_out     [T, n_k, d] bf16, dense, or NULL; may be k where that is dense
+ *   k_pool    [P, 64, n_k, d] bf16 cache pages, k_page_stride elements from
+ *             page to page, or NULL.  Token t's key heads go to pool row
+ *             k_cell[t] (page k_cell[t] / 64); a negative k_cell[t] writes
+ *             nothing, one at or past P * 64 writes nothing and is flagged
+ *             FM_DEVERR_PAGE_RANGE.  The cells of one call are distinct.
+ *   T >= 0; n_q, n_k >= 0 (0: that side's pointers are ignored), n_q + n_k <= 4096
+ *   d         a multiple of 8, 8 <= d <= 1024
+ *   rope_dim  even, 0 <= rope_dim <= min(d, 256); 0: norm only
+ *   strides   multiples of 8 elements, q_stride_t >= n_q * d, k_stride_t >=
+ *             n_k * d, k_page_stride >= 64 * n_k * d; q, k, the gains and the
+ *             outputs 16-byte aligned
+ * Errors: FM_ERR_INVALID_ARG for any violated condition, FM_ERR_CUDA for a
+ * launch failure.
+ */
+fm_status fm_qk_norm_rope(const int64_t* pos, int T, int d, int rope_dim, double rope_base, double rope_factor,
+                          double rope_orig_len, double rope_beta_fast, double rope_beta_slow, float eps,
+                          const uint16_t* q, int64_t q_stride_t, int n_q, const uint16_t* q_gain, uint16_t* q_out,
+                          const uint16_t* k, int64_t k_stride_t, int n_k, const uint16_t* k_gain, uint16_t* k_out,
+                          uint16_t* k_pool, int64_t P, int64_t k_page_stride, const int32_t* k_cell,
+                          fm_stream_t stream);
+
+/*
+ * Attention of a CSA layer: one softmax over the selected chunk cells, the
+ * first tokens of the sequence and a sliding window of its last tokens ([V4]
+ * sec. 4: CSA attention over the sliding window and the selected c4 chunks
+ * with an attention sink; [RM] "Two-level recall algorithm": the indexer's
+ * top-512 restricts what is read).  A cell is a latent of 512 elements that is
+ * key and value of every head.  For token t (sequence b = seq[t], position p =
+ * pos[t]) the keys are
+ *   - cell_pool row cells[t, i], for every i < k with cells[t, i] >= 0
+ *     (fm_native_topk_paged_ex's reserve cells, id_mode 1); a cell listed twice
+ *     counts twice;
+ *   - the cached tokens j <= p of sequence b with j < n_sink or j > p - window:
+ *     kv_pool row page_table[b, j / 64] * 64 + j % 64.  A negative table entry
+ *     is a page that is no longer held: its tokens are no keys;
+ * and for head h, with s_j = scale * (q[t, h] . c_j), Z = sum_j exp(s_j):
+ *     out[t, h] = sum_j exp(s_j) c_j / (Z + exp(sink_logit[h]))
+ *     lse[t, h] = log Z
+ * (sink_logit NULL: no second term).  A token without keys gets out = 0 and
+ * lse = -inf.  Rows that are no keys are never read.
+ *
+ *   q           [T, n_h, 512] bf16, 16-byte aligned; 1 <= n_h <= 1024
+ *   kv_pool     [P, 64, 512] bf16 pages, kv_page_stride elements from page to
+ *               page: a multiple of 512, >= 64 * 512 (layers may lie between);
+ *               16-byte aligned; NULL with P = 0
+ *   page_table  [B, R] int32; an entry at or past P is skipped and flagged
+ *               FM_DEVERR_PAGE_RANGE, as is a position at or past R * 64
+ *   seq         [T] int32 rows of page_table, or NULL (token t is row t, T <= B);
+ *               a negative one (and a negative position) sees no cached tokens,
+ *               one at or past B neither, and is flagged
+ *   pos         [T] int64
+ *   window >= 0, n_sink >= 0 (their sum may be zero)
+ *   cell_pool   [Pc, 64, 512] bf16 with cell_page_stride as kv_pool; cells
+ *               [T, k] int32 (dense), 0 <= k <= 1024; an entry at or past Pc * 64 is
+ *               skipped and flagged; k = 0: both ignored
+ *   sink_logit  [n_h] fp32 or NULL;  scale  > 0, 512^-1/2 as a rule
+ *   out         [T, n_h, 512] bf16, 16-byte aligned;  lse_out [T, n_h] fp32 or NULL
+ *   workspace   >= fm_csa_attn_workspace(T, n_h) bytes, 256-byte aligned (may be
+ *               NULL when that is 0): the partial results of tokens whose keys
+ *               are split over several SMs.  Calls that overlap on the GPU need
+ *               a workspace each.
+ * Scores, softmax statistics and sums are fp32; the softmax weights are rounded
+ * to bf16 for the tensor cores' second product.  The result does not depend on
+ * scheduling.
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_WORKSPACE, FM_ERR_CUDA.
+ */
+size_t fm_csa_attn_workspace(int T, int n_h);
+fm_status fm_csa_attn(const uint16_t* q, int T, int n_h, int d, const uint16_t* kv_pool, int64_t P,
+                      int64_t kv_page_stride, const int32_t* page_table, int B, int R, const int32_t* seq,
+                      const int64_t* pos, int64_t window, int n_sink, const uint16_t* cell_pool, int64_t Pc,
+                      int64_t cell_page_stride, const int32_t* cells, int k, const float* sink_logit, float scale,
+                      uint16_t* out, float* lse_out, void* workspace, size_t workspace_bytes, fm_stream_t stream);
+
+/*
+ * fm_csa_attn for a tree of drafted tokens behind a committed cache.  Sequence
+ * b's first tree_base[b] slots hold committed tokens; drafted token i of the
+ * sequence was written to slot tree_base[b] + i, whatever its depth.  Token t's
+ * keys are the selected cells, the committed tokens j < tree_base[b] that
+ * fm_csa_attn's rule for position pos[t] names, and the drafted slots i whose
+ * bit (i & 31 of word i >> 5 of row t) of tree_mask is set: the token itself
+ * and its ancestors.  A drafted token's position is that of its depth.
+ *
+ *   tree_mask  [T, tree_words] uint32, 1 <= tree_words <= 32
+ *   tree_base  [B] int64; a negative one: no cached tokens
+ * Other arguments, outputs, workspace and errors as fm_csa_attn.
+ */
+fm_status fm_csa_attn_tree(const uint16_t* q, int T, int n_h, int d, const uint16_t* kv_pool, int64_t P,
+                           int64_t kv_page_stride, const int32_t* page_table, int B, int R, const int32_t* seq,
+                           const int64_t* pos, int64_t window, int n_sink, const uint16_t* cell_pool, int64_t Pc,
+                           int64_t cell_page_stride, const int32_t* cells, int k, const float* sink_logit, float scale,
+                           const uint32_t* tree_mask, int tree_words, const int64_t* tree_base, uint16_t* out,
+                           float* lse_out, void* workspace, size_t workspace_bytes, fm_stream_t stream);
 
 /*
  * Device status word of the current device: the OR of FM_DEVERR_* bits set by

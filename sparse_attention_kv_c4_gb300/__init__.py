@@ -19,7 +19,8 @@ __all__ = [
     "fm_index_prefill_workspace", "fm_index_prefill_topk", "fm_native_topk_paged_noalloc", "fm_page_recall",
     "fm_native_topk_paged_ex", "fm_memindex_fp8_workspace", "fm_memindex_score_mask_fp8",
     "fm_index_prefill_scores", "fm_retriever_workspace", "fm_retriever_score_mask", "fm_query_chain_workspace",
-    "fm_query_chain", "fm_query_chain_layers_workspace", "fm_query_chain_layers", "LIB_PATH",
+    "fm_query_chain", "fm_query_chain_layers_workspace", "fm_query_chain_layers", "fm_qk_norm_rope",
+    "fm_csa_attn_workspace", "fm_csa_attn", "fm_csa_attn_tree", "LIB_PATH",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -106,6 +107,20 @@ def lib() -> ctypes.CDLL:
             L.fm_query_chain_layers.argtypes = [_I32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32,
                                                 _I32, _D, _D, _D, _D, _D, _F, _VP, _VP, _VP, _VP, _SZ, _VP]
             L.fm_query_chain_layers.restype = ctypes.c_int
+        if hasattr(L, "fm_qk_norm_rope"):
+            _D = ctypes.c_double
+            L.fm_qk_norm_rope.argtypes = [_VP, _I32, _I32, _I32, _D, _D, _D, _D, _D, _F, _VP, _I64, _I32, _VP, _VP, _VP,
+                                          _I64, _I32, _VP, _VP, _VP, _I64, _I64, _VP, _VP]
+            L.fm_qk_norm_rope.restype = ctypes.c_int
+        if hasattr(L, "fm_csa_attn"):
+            L.fm_csa_attn_workspace.argtypes = [_I32, _I32]
+            L.fm_csa_attn_workspace.restype = _SZ
+            head = [_VP, _I32, _I32, _I32, _VP, _I64, _I64, _VP, _I32, _I32, _VP, _VP, _I64, _I32, _VP, _I64, _I64, _VP,
+                    _I32, _VP, _F]
+            tail = [_VP, _VP, _VP, _SZ, _VP]
+            L.fm_csa_attn.argtypes = head + tail
+            L.fm_csa_attn_tree.argtypes = head + [_VP, _I32, _VP] + tail
+            L.fm_csa_attn.restype = L.fm_csa_attn_tree.restype = ctypes.c_int
         if hasattr(L, "fm_page_recall"):
             L.fm_page_recall.argtypes = [_VP, _I32, _I64, _I64, _I64, _I32, _VP, _VP, _VP, _VP]
         for name in ("fm_memindex_score_mask", "fm_topk_select", "fm_native_topk_paged", "fm_index_prefill_topk",
@@ -369,3 +384,151 @@ def fm_page_recall(mask, S: int, kmax: int, pages_out, density_out=None, n_out=N
     B = mask.shape[0]
     _check(lib().fm_page_recall(_ptr(mask), B, S, sink, recent, kmax, _ptr(pages_out), _ptr(density_out),
                                 _ptr(n_out), _stream(stream)))
+
+
+def _arg(t, name: str, dtypes, shape, device=None, rows=False):
+    """Check one tensor argument: its element type, its shape (None: any size)
+    and that it is dense -- or, with rows, dense but for its first stride."""
+    import torch
+    names = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    if t.dtype not in tuple(getattr(torch, n) for n in names):
+        raise ValueError(f"{name}: dtype {t.dtype}, need {' or '.join(names)}")
+    if t.dim() != len(shape) or any(want is not None and want != have for want, have in zip(shape, t.shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {tuple('any' if n is None else n for n in shape)}")
+    dense = 1
+    for i in reversed(range(1 if rows else 0, t.dim())):
+        if t.shape[i] != 1 and t.stride(i) != dense and t.numel():
+            raise ValueError(f"{name}: strides {t.stride()} of shape {tuple(t.shape)}: rows must be dense")
+        dense *= t.shape[i]
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, need {device}")
+
+
+def _stride0(t, dense: int) -> int:
+    """The first stride, or the dense one where a size of one leaves it open."""
+    return t.stride(0) if t.shape[0] > 1 else dense
+
+
+def _current(t, name: str):
+    """The tensor's device, which must be the current one (the streams' device)."""
+    import torch
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+_BF16 = ("bfloat16", "int16", "uint16")  # bf16 tensors, or their bit patterns
+
+
+def fm_qk_norm_rope(pos, q=None, q_gain=None, q_out=None, k=None, k_gain=None, k_out=None, k_pool=None, k_cell=None,
+                    rope_dim: int = 64, eps: float = 1e-6, stream=None, **rope) -> None:
+    """pos [T] int64; q [T,n_q,d] bf16 (any token stride) -> q_out [T,n_q,d];
+    k [T,n_k,d] bf16 (any token stride) -> k_out [T,n_k,d] and/or rows
+    k_cell [T] int32 of k_pool [P,64,n_k*d] (any page stride).  q or k may be
+    None.  RMSNorm per head with q_gain / k_gain [d] (None: ones), then the
+    rotation of the last rope_dim entries (rope: RETRIEVER_ROPE's parameters)."""
+    cfg = dict(RETRIEVER_ROPE, **rope)
+    if len(cfg) != len(RETRIEVER_ROPE):
+        raise TypeError(f"unknown arguments {sorted(set(cfg) - set(RETRIEVER_ROPE))}")
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q or k is needed")
+    dev = _current(one, "q" if q is not None else "k")
+    T, d = one.shape[0], one.shape[-1]
+    _arg(pos, "pos", "int64", (T,), dev)
+    n_q = n_k = 0
+    if q is not None:
+        if q_out is None:
+            raise ValueError("q needs q_out")
+        _arg(q, "q", _BF16, (T, None, d), dev, rows=True)
+        n_q = q.shape[1]
+        _arg(q_out, "q_out", _BF16, (T, n_q, d), dev)
+    if k is not None:
+        if k_out is None and k_pool is None:
+            raise ValueError("k needs k_out or k_pool")
+        _arg(k, "k", _BF16, (T, None, d), dev, rows=True)
+        n_k = k.shape[1]
+        if k_out is not None:
+            _arg(k_out, "k_out", _BF16, (T, n_k, d), dev)
+        if k_pool is not None:
+            if k_cell is None:
+                raise ValueError("k_pool needs k_cell")
+            _arg(k_pool, "k_pool", _BF16, (None, 64, n_k * d), dev, rows=True)
+            _arg(k_cell, "k_cell", "int32", (T,), dev)
+    for g, name in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+        if g is not None:
+            _arg(g, name, _BF16, (d,), dev)
+    P = 0 if k_pool is None else k_pool.shape[0]
+    _check(lib().fm_qk_norm_rope(_ptr(pos), T, d, rope_dim, cfg["rope_base"], cfg["rope_factor"], cfg["rope_orig_len"],
+                                 cfg["rope_beta_fast"], cfg["rope_beta_slow"], float(eps), _ptr(q),
+                                 0 if q is None else _stride0(q, n_q * d), n_q, _ptr(q_gain), _ptr(q_out), _ptr(k),
+                                 0 if k is None else _stride0(k, n_k * d), n_k, _ptr(k_gain), _ptr(k_out),
+                                 _ptr(k_pool), P, 64 * n_k * d if P == 0 else _stride0(k_pool, 64 * n_k * d),
+                                 _ptr(k_cell), _stream(stream)))
+
+
+def fm_csa_attn_workspace(T: int, n_h: int) -> int:
+    return lib().fm_csa_attn_workspace(T, n_h)
+
+
+def _csa_attn_args(q, kv_pool, page_table, pos, out, seq, window, n_sink, cell_pool, cells, sink_logit, scale, lse_out):
+    dev = _current(q, "q")
+    T, n_h, d = q.shape
+    _arg(q, "q", _BF16, (T, n_h, d), dev)
+    _arg(kv_pool, "kv_pool", _BF16, (None, 64, d), dev, rows=True)
+    _arg(page_table, "page_table", "int32", (None, None), dev)
+    _arg(pos, "pos", "int64", (T,), dev)
+    _arg(out, "out", _BF16, (T, n_h, d), dev)
+    if seq is not None:
+        _arg(seq, "seq", "int32", (T,), dev)
+    if (cell_pool is None) != (cells is None):
+        raise ValueError("cell_pool and cells go together")
+    k = 0
+    if cells is not None:
+        _arg(cell_pool, "cell_pool", _BF16, (None, 64, d), dev, rows=True)
+        _arg(cells, "cells", "int32", (T, None), dev)
+        k = cells.shape[1]
+    if sink_logit is not None:
+        _arg(sink_logit, "sink_logit", "float32", (n_h,), dev)
+    if lse_out is not None:
+        _arg(lse_out, "lse_out", "float32", (T, n_h), dev)
+    page = 64 * d
+    return (_ptr(q), T, n_h, d, _ptr(kv_pool), kv_pool.shape[0], _stride0(kv_pool, page), _ptr(page_table),
+            page_table.shape[0], page_table.shape[1], _ptr(seq), _ptr(pos), int(window), n_sink, _ptr(cell_pool),
+            0 if cells is None else cell_pool.shape[0], page if cells is None else _stride0(cell_pool, page),
+            _ptr(cells), k, _ptr(sink_logit), float(d ** -0.5 if scale is None else scale))
+
+
+def _workspace(workspace, dev):
+    if workspace is None:
+        return None, 0
+    _arg(workspace, "workspace", "uint8", (None,), dev)
+    return _ptr(workspace) or None, workspace.numel()
+
+
+def fm_csa_attn(q, kv_pool, page_table, pos, out, window: int, n_sink: int = 0, seq=None, cell_pool=None, cells=None,
+                sink_logit=None, scale=None, lse_out=None, workspace=None, stream=None) -> None:
+    """q [T,n_h,512] bf16, kv_pool [P,64,512] bf16 (any page stride), page_table
+    [B,R] int32, pos [T] int64, seq [T] int32 (None: token t is row t), cells
+    [T,k] int32 rows of cell_pool [Pc,64,512] (both None: none), sink_logit
+    [n_h] fp32 or None, scale (None: 512 ** -0.5) -> out [T,n_h,512] bf16,
+    lse_out [T,n_h] fp32 or None; workspace >= fm_csa_attn_workspace(T, n_h)."""
+    args = _csa_attn_args(q, kv_pool, page_table, pos, out, seq, window, n_sink, cell_pool, cells, sink_logit, scale,
+                          lse_out)
+    ws, ws_bytes = _workspace(workspace, q.device)
+    _check(lib().fm_csa_attn(*args, _ptr(out), _ptr(lse_out), ws, ws_bytes, _stream(stream)))
+
+
+def fm_csa_attn_tree(q, kv_pool, page_table, pos, out, window: int, tree_mask, tree_base, n_sink: int = 0, seq=None,
+                     cell_pool=None, cells=None, sink_logit=None, scale=None, lse_out=None, workspace=None,
+                     stream=None) -> None:
+    """fm_csa_attn for drafted tokens: sequence b's drafted token i is in cache
+    slot tree_base[b] + i (tree_base [B] int64); tree_mask [T, words] int32 or
+    uint32 has bit i & 31 of word i >> 5 set where token t sees it."""
+    args = _csa_attn_args(q, kv_pool, page_table, pos, out, seq, window, n_sink, cell_pool, cells, sink_logit, scale,
+                          lse_out)
+    _arg(tree_mask, "tree_mask", ("int32", "uint32"), (q.shape[0], None), q.device)
+    _arg(tree_base, "tree_base", "int64", (page_table.shape[0],), q.device)
+    ws, ws_bytes = _workspace(workspace, q.device)
+    _check(lib().fm_csa_attn_tree(*args, _ptr(tree_mask), tree_mask.shape[1], _ptr(tree_base), _ptr(out),
+                                  _ptr(lse_out), ws, ws_bytes, _stream(stream)))

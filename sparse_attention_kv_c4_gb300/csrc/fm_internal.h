@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -26,6 +27,21 @@ fm_status make_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const
                     CUtensorMapSwizzle swizzle);
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// YaRN NTK-by-parts frequency of rotary pair i of rope_dim / 2: theta_i =
+// base^(-2i/rope_dim); pairs that turn fewer than beta_slow times over the
+// original context take theta_i / factor, pairs that turn more than beta_fast
+// times keep theta_i, and the ones between blend the two linearly in the
+// number of turns.
+inline double yarn_freq(int i, int rope_dim, double base, double factor, double orig_len, double beta_fast,
+                        double beta_slow) {
+  const double two_pi = 6.283185307179586476925286766559;
+  const double theta = pow(base, -2.0 * (double)i / (double)rope_dim);
+  const double turns = orig_len * theta / two_pi;
+  double gamma = (turns - beta_slow) / (beta_fast - beta_slow);
+  gamma = gamma < 0.0 ? 0.0 : (gamma > 1.0 ? 1.0 : gamma);
+  return (1.0 - gamma) * theta / factor + gamma * theta;
+}
 
 // ---- launchers (arguments already validated) -------------------------------
 struct MemindexArgs {

@@ -485,20 +485,10 @@ __global__ void __launch_bounds__(kNormThreads)
   }
 }
 
-// YaRN NTK-by-parts frequency of rotary pair i: theta_i = base^(-2i/64);
-// pairs that turn fewer than beta_slow times over the original context take
-// theta_i / factor, pairs that turn more than beta_fast times keep theta_i,
-// and the ones between blend the two linearly in the number of turns.
 RopeFreqs yarn_freqs(double base, double factor, double orig_len, double beta_fast, double beta_slow) {
-  const double two_pi = 6.283185307179586476925286766559;
   RopeFreqs r;
-  for (int i = 0; i < kRopeDim / 2; ++i) {
-    const double theta = std::pow(base, -2.0 * (double)i / (double)kRopeDim);
-    const double turns = orig_len * theta / two_pi;
-    double gamma = (turns - beta_slow) / (beta_fast - beta_slow);
-    gamma = gamma < 0.0 ? 0.0 : (gamma > 1.0 ? 1.0 : gamma);
-    r.f[i] = (1.0 - gamma) * theta / factor + gamma * theta;
-  }
+  for (int i = 0; i < kRopeDim / 2; ++i)
+    r.f[i] = yarn_freq(i, kRopeDim, base, factor, orig_len, beta_fast, beta_slow);
   return r;
 }
 

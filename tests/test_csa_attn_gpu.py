@@ -1,0 +1,341 @@
+"""fm_csa_attn / fm_csa_attn_tree against the fp64 formulas, at the sizes, masks
+and layouts where they can go wrong.  Every pool row that is no key of any token
+is NaN, so a read of it shows."""
+import numpy as np
+import pytest
+
+import attn_ref as ref
+
+pytestmark = pytest.mark.gpu
+D, PAGE = ref.D, ref.PAGE
+
+
+@pytest.fixture(scope="module")
+def torch_dev():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch, torch.device("cuda:0")
+
+
+class Batch:
+    """A ragged batch: seqs = [(new tokens, last position)], each with its pages."""
+
+    def __init__(self, seed, seqs, H, k, window, n_sink, Pc=24, sink=True, holes=False, pads=0, tree=False, gap=1,
+                 magnitude=1.0):
+        rng = np.random.default_rng(seed)
+        self.H, self.k, self.window, self.n_sink, self.tree, self.gap = H, k, window, n_sink, tree, gap
+        self.seq, self.pos, masks, base = [], [], [], []
+        for b, (n, last) in enumerate(seqs):
+            base.append(last + 1)
+            if tree:
+                anc, depth = [], []
+                for i in range(n):
+                    par = i - 1 - int(rng.integers(0, 4))
+                    anc.append((anc[par] if par >= 0 else 0) | (1 << i))
+                    depth.append(depth[par] + 1 if par >= 0 else 1)
+                masks += anc
+                self.pos += [last + x for x in depth]
+            else:
+                self.pos += list(range(last - n + 1, last + 1))
+            self.seq += [b] * n
+        for i in range(pads):  # padding rows behind the batch
+            self.seq.append(-1 if i % 2 else 0)
+            self.pos.append(-1 if i % 2 == 0 else 5)
+            masks.append(0)
+        T = self.T = len(self.seq)
+        self.words = max(1, (max(n for n, _ in seqs) + 31) // 32) if tree else 0
+        self.masks, self.base = masks, base
+        B = self.B = len(seqs)
+        self.R = max(last + (n if tree else 0) for n, last in seqs) // PAGE + 2
+        self.P = B * self.R + 3
+        table = rng.permutation(self.P)[:B * self.R].reshape(B, self.R).astype(np.int32)
+        if holes:
+            table[rng.random(table.shape) < 0.3] = -1
+        self.table = table
+        self.q = ref.bf16(magnitude * rng.standard_normal((T, H, D)))
+        self.sink = rng.standard_normal(H).astype(np.float32) if sink else None
+        self.Pc = Pc
+        self.cells = np.full((T, k), -1, np.int32)
+        for t in range(T):
+            n = int(rng.integers(0, k + 1)) if t % 3 else k
+            n = min(n, Pc * PAGE)
+            c = np.sort(rng.choice(Pc * PAGE, n, replace=False))
+            if t % 4 == 3:  # empty entries anywhere, not only at the end
+                where = np.sort(rng.choice(k, n, replace=False))
+                self.cells[t, where] = c
+            else:
+                self.cells[t, :n] = c
+        # pools: NaN wherever nothing reads
+        self.kv = np.full((self.P * PAGE, D), 0x7FC1, np.uint16)
+        self.cp = np.full((max(Pc, 1) * PAGE, D), 0x7FC1, np.uint16)
+        self.rows = [self.token_rows(t) for t in range(T)]
+        used = sorted({r for rows in self.rows for r in rows})
+        self.kv[used] = ref.bf16(rng.standard_normal((len(used), D)))
+        used = np.unique(self.cells[self.cells >= 0])
+        self.cp[used] = ref.bf16(rng.standard_normal((len(used), D)))
+
+    def token_rows(self, t):
+        b, p = self.seq[t], self.pos[t]
+        if b < 0 or p < 0:
+            return []
+        slots = ref.visible(p, self.window, self.n_sink, self.base[b] if self.tree else p + 1)
+        if self.tree:
+            slots += [self.base[b] + i for i in range(32 * self.words) if (self.masks[t] >> i) & 1]
+        return [int(self.table[b, j // PAGE]) * PAGE + j % PAGE for j in slots if self.table[b, j // PAGE] >= 0]
+
+    def device(self, torch, dev):
+        t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)
+
+        def pool(flat, gap):  # pages with gap - 1 pages of NaN between them
+            a = np.full((flat.shape[0] // PAGE, gap, PAGE, D), 0x7FC1, np.uint16)
+            a[:, 0] = flat.reshape(-1, PAGE, D)
+            return t(a.view(np.int16))[:, 0]
+        self.d = dict(q=t(self.q.view(np.int16)), kv_pool=pool(self.kv, self.gap), page_table=t(self.table),
+                      pos=t(np.array(self.pos, np.int64)),
+                      out=torch.full((self.T, self.H, D), 0x7FC1, dtype=torch.int16, device=dev))
+        self.kw = dict(seq=t(np.array(self.seq, np.int32)), window=self.window, n_sink=self.n_sink,
+                       sink_logit=None if self.sink is None else t(self.sink),
+                       lse_out=torch.full((self.T, self.H), float("nan"), device=dev))
+        if self.k:
+            self.kw.update(cell_pool=pool(self.cp, self.gap), cells=t(self.cells))
+        if self.tree:
+            m = np.array([[(x >> (32 * w)) & 0xFFFFFFFF for w in range(self.words)] for x in self.masks], np.uint32)
+            self.kw.update(tree_mask=t(m.view(np.int32)), tree_base=t(np.array(self.base, np.int64)))
+        import sparse_attention_kv_c4_gb300 as fm
+        self.kw["workspace"] = torch.empty(fm.fm_csa_attn_workspace(self.T, self.H), dtype=torch.uint8, device=dev)
+        return self
+
+    def call(self):
+        import sparse_attention_kv_c4_gb300 as fm
+        (fm.fm_csa_attn_tree if self.tree else fm.fm_csa_attn)(**self.d, **self.kw)
+
+    def check(self, torch, tokens=None):
+        import sparse_attention_kv_c4_gb300 as fm
+        torch.cuda.synchronize()
+        assert fm.fm_device_status(reset=True) == 0
+        out = ref.f64(self.d["out"].cpu().numpy().view(np.uint16))
+        lse = self.kw["lse_out"].cpu().numpy().astype(np.float64)
+        for t in range(self.T) if tokens is None else tokens:
+            keys = [self.kv[self.rows[t]], self.cp[self.cells[t][self.cells[t] >= 0]]]
+            w_out, w_lse, tol, ltol = ref.attend(ref.f64(self.q[t]), ref.f64(np.concatenate(keys)), self.sink, D ** -0.5)
+            bad = ~(np.abs(out[t] - w_out) <= tol)
+            assert not bad.any(), f"token {t} pos {self.pos[t]} keys {sum(map(len, keys))}: {bad.sum()} values off, " \
+                f"first head/element {np.argwhere(bad)[:4].tolist()}, worst {np.nanmax(np.abs(out[t] - w_out)):.3g}"
+            both = np.isneginf(w_lse)
+            assert (np.isneginf(lse[t]) == both).all(), f"token {t}: lse of a row without keys"
+            assert (np.abs(lse[t][~both] - w_lse[~both]) <= ltol[~both]).all(), f"token {t}: lse"
+
+
+CASES = [
+    # seqs, H, k, window, n_sink
+    ([(1, 0)], 64, 0, 128, 0),                                   # one token, one key
+    ([(1, 36)], 64, 0, 128, 4),
+    ([(1, 700)], 1, 1, 1, 0),                                    # one head, one cell, itself
+    ([(3, 2), (1, 63), (2, 64), (4, 65)], 20, 37, 63, 1),        # page borders
+    ([(5, 129), (1, 0), (7, 400)], 64, 64, 64, 70),              # first tokens beyond a page
+    ([(2, 500), (1, 20)], 65, 512, 128, 4),                      # a second head block of one head
+    ([(2, 1000)], 128, 1024, 65, 4),                             # the most cells, two head blocks
+    ([(1, 5000)], 64, 0, 5001, 0),                               # a long window, split over SMs
+    ([(1, 3333), (1, 17)], 130, 100, 3000, 130),
+    ([(40, 300)], 64, 130, 0, 0),                                # no tokens at all, cells alone
+    ([(40, 300)], 8, 0, 0, 5),                                   # first tokens alone
+    ([(333, 332)], 16, 48, 128, 4),                              # a prompt from its first token on
+    ([(170, 700), (3, 2)], 64, 72, 130, 3),                      # more tokens than SMs
+]
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+@pytest.mark.parametrize("variant", ["plain", "holes"])
+def test_matches_formula(torch_dev, case, variant):
+    torch, dev = torch_dev
+    holes = variant == "holes"
+    b = Batch(1000 + case, *CASES[case], holes=holes, pads=3 if holes else 0, sink=not holes, gap=3 if holes else 1)
+    b.device(torch, dev).call()
+    b.check(torch)
+
+
+@pytest.mark.parametrize("seqs,H,k,window,n_sink", [
+    ([(1, 0)], 64, 0, 128, 0),
+    ([(16, 700), (5, 3), (16, 64)], 64, 96, 128, 4),
+    ([(61, 900), (33, 62)], 20, 0, 500, 4),
+    ([(70, 130)], 128, 40, 1, 0),
+    ([(2, 4000)], 64, 0, 100000, 0),
+])
+@pytest.mark.parametrize("holes", [False, True])
+def test_tree_matches_formula(torch_dev, seqs, H, k, window, n_sink, holes):
+    torch, dev = torch_dev
+    b = Batch(77 + H + k, seqs, H, k, window, n_sink, tree=True, holes=holes, pads=2)
+    b.device(torch, dev).call()
+    b.check(torch)
+
+
+@pytest.mark.parametrize("magnitude", [2.0 ** -20, 12.0])
+def test_flat_and_sharp_softmax(torch_dev, magnitude):
+    """Scores all but equal, and scores that spread over hundreds: the running
+    maximum moves from tile to tile."""
+    torch, dev = torch_dev
+    b = Batch(5, [(9, 900)], 64, 256, 300, 4, magnitude=magnitude)
+    b.device(torch, dev).call()
+    b.check(torch)
+
+
+def test_rising_scores(torch_dev):
+    """Each key's score is above all before it, by far: every tile moves every
+    head's maximum, and all earlier weights vanish."""
+    torch, dev = torch_dev
+    b = Batch(6, [(2, 600)], 64, 128, 601, 0, sink=False)
+    ramp = ref.bf16(np.linspace(-1, 1, 601)[:, None] * np.ones((1, D)))
+    for j in range(601):
+        b.kv[int(b.table[0, j // PAGE]) * PAGE + j % PAGE] = ramp[j]
+    b.q[:] = ref.bf16(np.full((2, 64, D), 8.0) * (1 + np.arange(64)[None, :, None] / 16))
+    b.device(torch, dev).call()
+    b.check(torch)
+
+
+def test_repeatable_on_another_stream_and_in_a_graph(torch_dev):
+    """The same call gives the same bits, on another stream, captured and
+    replayed on new inputs, and on two streams at once with a workspace each."""
+    torch, dev = torch_dev
+    b = Batch(8, [(1, 3000), (1, 100), (2, 777)], 64, 512, 2000, 4).device(torch, dev)
+    b.call()
+    b.check(torch)
+    want = [b.d["out"].clone(), b.kw["lse_out"].clone()]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for x in (b.d["out"], b.kw["lse_out"]):
+            x.zero_()
+        b.call()
+    s.synchronize()
+    assert torch.equal(want[0], b.d["out"]) and torch.equal(want[1], b.kw["lse_out"])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.call()
+    c = Batch(9, [(1, 3000), (1, 100), (2, 777)], 64, 512, 2000, 4).device(torch, dev)
+    for key in b.d:
+        if key != "out":
+            b.d[key].copy_(c.d[key])
+    for key in ("seq", "cells", "cell_pool", "sink_logit"):
+        b.kw[key].copy_(c.kw[key])
+    g.replay()
+    c.call()
+    torch.cuda.synchronize()
+    assert torch.equal(b.d["out"], c.d["out"]) and torch.equal(b.kw["lse_out"], c.kw["lse_out"])
+    c.check(torch)
+    want = c.d["out"].clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        b.call()
+    c.call()
+    torch.cuda.synchronize()
+    assert torch.equal(b.d["out"], want) and torch.equal(c.d["out"], want)
+
+
+def test_out_of_range_ids_are_skipped_and_flagged(torch_dev):
+    """Bad pages, cells, rows of the table and positions are no keys, and set
+    FM_DEVERR_PAGE_RANGE; the rest of the call is as without them."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    b = Batch(11, [(2, 300), (2, 400)], 64, 64, 200, 4).device(torch, dev)
+    b.call()
+    b.check(torch)
+    table, cells, seq, pos = b.table.copy(), b.cells.copy(), list(b.seq), list(b.pos)
+
+    def again(**new):
+        for name, value in new.items():
+            (b.d if name in b.d else b.kw)[name].copy_(torch.from_numpy(np.asarray(value)).to(dev))
+        b.call()
+        torch.cuda.synchronize()
+        assert fm.fm_device_status(reset=True) == fm.FM_DEVERR_PAGE_RANGE
+        b.rows = [b.token_rows(t) for t in range(b.T)]
+        b.check(torch)
+    # a page at P and one far past it, in the windows
+    b.table[0, 4], b.table[1, 5] = -1, -1
+    bad = b.table.copy()
+    bad[0, 4], bad[1, 5] = b.P, 2 ** 31 - 1
+    again(page_table=bad)
+    # cells at the pool's end and far past it
+    b.cells[0, 3], b.cells[3, 0] = -1, -1
+    bad = b.cells.copy()
+    bad[0, 3], bad[3, 0] = b.Pc * PAGE, 2 ** 31 - 1
+    (b.d["page_table"]).copy_(torch.from_numpy(b.table).to(dev))
+    again(cells=bad)
+    b.kw["cells"].copy_(torch.from_numpy(b.cells).to(dev))
+    # a row at B
+    b.seq = [seq[0], -1, seq[2], seq[3]]
+    again(seq=np.array([seq[0], b.B, seq[2], seq[3]], np.int32))
+    b.kw["seq"].copy_(torch.from_numpy(np.array(b.seq, np.int32)).to(dev))
+    # a position past the table: the tokens past it are no keys
+    far = b.R * PAGE + 40
+    b.pos = [pos[0], pos[1], pos[2], far]
+    b.rows = None
+    b.d["pos"].copy_(torch.from_numpy(np.array(b.pos, np.int64)).to(dev))
+    b.token_rows_plain = b.token_rows
+    slots = [j for j in ref.visible(far, b.window, b.n_sink, b.R * PAGE)]
+    b.kv[[int(b.table[1, j // PAGE]) * PAGE + j % PAGE for j in slots if b.table[1, j // PAGE] >= 0]] = ref.bf16(np.ones((1, D)))
+    b.d["kv_pool"].copy_(torch.from_numpy(b.kv.view(np.int16).reshape(-1, PAGE, D)).to(dev))
+    b.call()
+    torch.cuda.synchronize()
+    assert fm.fm_device_status(reset=True) == fm.FM_DEVERR_PAGE_RANGE
+    b.token_rows = lambda t: ([int(b.table[1, j // PAGE]) * PAGE + j % PAGE for j in slots if b.table[1, j // PAGE] >= 0]
+                              if t == 3 else b.token_rows_plain(t))
+    b.rows = [b.token_rows(t) for t in range(b.T)]
+    b.check(torch)
+
+
+def test_pools_past_32_bit_offsets(torch_dev):
+    """Pages whose byte and element offsets pass 2^32."""
+    torch, dev = torch_dev
+    P = (1 << 32) // (PAGE * D) + 64  # elements past 2^32: 8.6 GB
+    b = Batch(12, [(2, 200)], 64, 128, 150, 4)
+    b.device(torch, dev)
+    big = torch.empty((P, PAGE, D), dtype=torch.int16, device=dev)
+    shift = P - max(b.P, b.Pc)
+    big[shift:shift + b.P] = b.d["kv_pool"]
+    table = torch.from_numpy(np.where(b.table >= 0, b.table + shift, -1).astype(np.int32)).to(dev)
+    b.d.update(kv_pool=big, page_table=table)
+    b.call()
+    b.check(torch)
+    big[shift:shift + b.Pc] = b.kw["cell_pool"]
+    b.device(torch, dev)
+    b.kw.update(cell_pool=big, cells=torch.from_numpy(np.where(b.cells >= 0, b.cells + shift * PAGE, -1).astype(np.int32)).to(dev))
+    b.call()
+    b.check(torch)
+
+
+def test_huge_window_and_position(torch_dev):
+    """A window of 2^62 tokens at a far position walks the table's pages only."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    b = Batch(13, [(1, 300)], 64, 0, 1 << 62, 2 ** 31 - 1).device(torch, dev)
+    b.call()
+    b.check(torch)
+    assert fm.fm_device_status(reset=True) == 0
+
+
+def test_no_sequences_and_nothing_to_do(torch_dev):
+    """No pages, no cells, no table: every row is empty; T = 0 does nothing."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    q = torch.ones((3, 4, D), dtype=torch.bfloat16, device=dev)
+    pool = torch.empty((0, PAGE, D), dtype=torch.bfloat16, device=dev)
+    table = torch.empty((3, 0), dtype=torch.int32, device=dev)
+    pos = torch.tensor([-1, -5, -1], device=dev)
+    out, lse = torch.ones_like(q), torch.zeros((3, 4), device=dev)
+    ws = torch.empty(fm.fm_csa_attn_workspace(3, 4), dtype=torch.uint8, device=dev)
+    fm.fm_csa_attn(q, pool, table, pos, out, 128, lse_out=lse, sink_logit=torch.zeros(4, device=dev), workspace=ws)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    assert fm.fm_device_status(reset=True) == 0
+    fm.fm_csa_attn(q[:0], pool, table, pos[:0], out[:0], 128)
+
+
+def test_wider_pool_views_and_default_rows(torch_dev):
+    """Without seq, token t reads row t of the table; layers interleaved in one
+    pool are reached by the page stride."""
+    torch, dev = torch_dev
+    b = Batch(14, [(1, 90), (1, 130), (1, 3)], 64, 32, 100, 4, gap=5).device(torch, dev)
+    b.kw["seq"] = None
+    b.call()
+    b.check(torch)
