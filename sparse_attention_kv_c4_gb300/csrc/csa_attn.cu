@@ -4,9 +4,31 @@
 // tokens.  A cell c (512 elements) is key and value of every head:
 //     s_j = scale (q_h . c_j),  out_h = sum_j e^{s_j} c_j / (sum_j e^{s_j} + e^{sink_h})
 //
-// One CTA per (token, eight heads), one warp per head: the warp walks the
-// token's keys with the running maximum and sum of the softmax, each lane
-// holding 16 elements of q and of the output in registers.
+// GB300 mapping.  Every token has keys of its own, shared by its heads, so the
+// unit of work is one token's block of 64 heads against tiles of 64 keys
+// (131 kFLOP per key of 1 KB).  A persistent CTA per SM walks its items (token,
+// head block, split of the keys):
+//   scheduler   (warp 2)  each item's key ranges, into a ring of four
+//   q loader    (warp 3)  the item's 64 query rows, eight SWIZZLE_128B chunks
+//               [64 heads x 64 elements] of 8 KB
+//   producer    (warp 0)  each tile's 64 pool rows by TMA tile::gather4: 16 lanes
+//               take four keys each.  The ring holds nine pairs of chunks [64
+//               keys x 64 elements], four pairs to a tile; a key that is none
+//               is row -1, which the copy fills with zeros without a read, and
+//               a zero bit of the tile's mask
+//   MMA issuer  (warp 1)  S = Q C^T: tcgen05 M64 N64, 32 steps of K16;
+//               O^T += C^T P^T: M128 N64, four blocks of 128 elements x four
+//               steps of K16.  The cell tile is read twice from shared memory,
+//               K-major as keys and MN-major as values, and loaded once
+//   softmax     (warps 4-7)  S from TMEM, the running maximum and sum, P in
+//               bf16 to shared memory
+//   epilogue    (warps 8-11)  O^T from TMEM, times 1 / (sum + sink), to out
+// TMEM: O^T 4 x 64 columns, two S buffers of 64.  The output is kept transposed
+// (rows = elements) because 64 rows of heads x 512 columns would fill TMEM.
+//
+// Few tokens: the keys of an item are split over several CTAs, which write
+// unnormalised fp32 outputs with their maximum and sum; csa_merge_kernel joins
+// them in a fixed order.
 #include <cuda_bf16.h>
 
 #include "fm_common.cuh"
@@ -20,30 +42,46 @@ namespace {
 constexpr int kWidth = 512;
 constexpr int kPage = 64;
 constexpr int kMaxCells = 1024;
+constexpr int kHeadsPerItem = 64;
+constexpr int kTileKeys = 64;
+constexpr int kChunkBytes = 64 * 128;           // 64 rows x 64 elements
+constexpr int kPairBytes = 2 * kChunkBytes;
+constexpr int kPairsPerTile = kWidth / 128;     // 4
+constexpr int kPairs = 9;
+constexpr int kQBytes = kHeadsPerItem * kWidth * 2;
+constexpr int kPBytes = kHeadsPerItem * kTileKeys * 2;
+constexpr int kSmemBytes = 1024 + kQBytes + kPairs * kPairBytes + 2 * kPBytes;
+constexpr int kThreads = 384;
+constexpr int kTmemCols = 512;                  // allocations are powers of two
+constexpr int kSCol = 256;                      // the S buffers behind O^T's 256 columns
+constexpr int kInfoSlots = 4;
+constexpr int kInfoReaders = 1 + 1 + 1 + 4 + 4; // producer, issuer, q loader, softmax and epilogue warps
+constexpr int kMaxParts = 256;                  // partial results of one call
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
-  const uint16_t* q;
-  const uint16_t* kv_pool;
   const int32_t* page_table;
   const int32_t* seq;
   const int64_t* pos;
-  const uint16_t* cell_pool;
   const int32_t* cells;
   const float* sink_logit;
   const uint32_t* tree_mask;
   const int64_t* tree_base;
   uint16_t* out;
   float* lse;
+  float* part_o;                         // [parts][64][512] unnormalised outputs
+  float2* part_ml;                       // [parts][64] (maximum in log2 units, sum)
   unsigned int* status;
   int64_t kv_page_rows, cell_page_rows;  // rows (of 512 elements) from page to page
   int64_t window;
   int64_t cell_limit;                    // Pc * 64
   int T, n_h, P, B, R, k, n_sink, tree_words;
+  int head_blocks, splits, items;        // items = T * head_blocks * splits
   float scale;
 };
 
-// A token's keys, in order: k listed cells, n_first first tokens, n_win window
-// tokens from slot low, then the drafted slots from base.
+// A token's keys, in order: the listed cells, n_first first tokens, n_win window
+// tokens from slot low, then n_tree drafted slots from base.
 struct TokenKeys {
   int64_t low, base;
   int b;
@@ -94,80 +132,642 @@ FM_DEV int token_row(const AttnParams& p, int b, int64_t slot) {
   return page < 0 ? -1 : (int)(page * p.kv_page_rows + slot % kPage);
 }
 
-constexpr int kWarps = 8;
+// What the roles know of one item.  Key slots: the four ranges in order, each
+// rounded up to a multiple of four (one gather4 reads one pool).
+struct ItemInfo {
+  int64_t low, base;
+  int t, head_block, part;                 // part: index of the partial result, -1 = whole
+  int tile_begin, tile_end;                // at least one tile
+  int b, n_first, n_win, n_tree;
+  int end_cells, end_first, end_win, end;  // ends of the ranges, in slots
+};
 
-__global__ void __launch_bounds__(32 * kWarps) csa_attn_kernel(const __grid_constant__ AttnParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t t = blockIdx.x;
-  const int h = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  if (h >= p.n_h) return;
-  const TokenKeys tk = token_keys(p, t);
-  float q[16], o[16], m = -INFINITY, l = 0.f;
-  const uint16_t* qrow = p.q + (t * p.n_h + h) * kWidth + 16 * lane;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    q[i] = __uint_as_float((uint32_t)qrow[i] << 16);
-    o[i] = 0.f;
-  }
-  const int n = p.k + tk.n_first + tk.n_win + tk.n_tree;
-  for (int j = 0; j < n; ++j) {
-    const uint16_t* row = nullptr;
-    if (j < p.k) {
-      const int64_t cell = __ldg(p.cells + t * p.k + j);
-      if (cell >= p.cell_limit) atomicOr(p.status, FM_DEV_PAGE_RANGE);
-      if (cell >= 0 && cell < p.cell_limit)
-        row = p.cell_pool + ((cell / kPage) * p.cell_page_rows + cell % kPage) * kWidth;
-    } else {
-      const int i = j - p.k;
-      int64_t slot = i < tk.n_first ? i : tk.low + (i - tk.n_first);
-      bool seen = true;
-      if (i >= tk.n_first + tk.n_win) {
-        const int d = i - tk.n_first - tk.n_win;
-        seen = (__ldg(p.tree_mask + t * p.tree_words + (d >> 5)) >> (d & 31)) & 1u;
-        slot = tk.base + d;
-      }
-      const int r = seen ? token_row(p, tk.b, slot) : -1;
-      if (r >= 0) row = p.kv_pool + (int64_t)r * kWidth;
-    }
-    if (row == nullptr) continue;
-    float c[16], s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 v = *reinterpret_cast<const uint4*>(row + 16 * lane + 8 * i);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        c[8 * i + 2 * e] = __uint_as_float(u[e] << 16);
-        c[8 * i + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s = fmaf(q[i], c[i], s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale;
-    const float mn = fmaxf(m, s);
-    const float f = m == mn ? 1.f : expf(m - mn), w = mn == -INFINITY ? 0.f : expf(s - mn);
-    m = mn;
-    l = l * f + w;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = o[i] * f + w * c[i];
-  }
-  float below = l;
-  if (p.sink_logit != nullptr && l > 0.f) below += expf(p.sink_logit[h] - m);
-  const float inv = l == 0.f ? 0.f : 1.f / below;
-  uint16_t* dst = p.out + (t * p.n_h + h) * kWidth + 16 * lane;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) dst[i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
-  if (p.lse != nullptr && lane == 0) p.lse[t * p.n_h + h] = l == 0.f ? -INFINITY : m + logf(l);
+FM_DEV int up4(int x) { return (x + 3) & ~3; }
+
+FM_DEV void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int x, const int (&row)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+      "%5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]),
+      "r"(row[3])
+      : "memory");
+}
+FM_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
 }
 
-size_t attn_workspace_bytes(int, int) { return 0; }
+// 16 lanes x 64 columns: thread i gets, of columns 8j + 2 (i % 4) + {0, 1}, lane
+// i / 4 in r[4j], r[4j + 1] and lane i / 4 + 8 in r[4j + 2], r[4j + 3].
+FM_DEV void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
 
-fm_status launch_attn(const AttnParams& p, int, void*, cudaStream_t stream) {
-  csa_attn_kernel<<<dim3((unsigned)p.T, (unsigned)((p.n_h + kWarps - 1) / kWarps)), 32 * kWarps, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return set_error(FM_ERR_CUDA, "fm_csa_attn: launch: %s", cudaGetErrorString(e));
+// Descriptor of an MN-major SWIZZLE_128B operand: 64 elements of M or N to a
+// 128-byte row, one row per K; 8-row groups 1024 bytes apart (stride offset),
+// the next 64 elements of M or N a chunk further (leading offset).
+FM_DEV uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(kChunkBytes >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t kAIsMnMajor = 1u << 15;
+
+FM_DEV float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// OR of a predicate over the softmax warps' 128 threads (and a barrier for them).
+FM_DEV bool softmax_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+FM_DEV uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Lane 0 waits, every lane learns the result.
+FM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort, status) ? 1 : 0;
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  // the other lanes' own view of the phase (it is complete: no wait)
+  if (ok) (void)mbar_try_wait(bar, parity);
+  return ok != 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    csa_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_kv,
+                    const __grid_constant__ CUtensorMap tmap_cell, const __grid_constant__ AttnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_smem = smem;
+  uint8_t* ring = smem + kQBytes;
+  uint8_t* p_smem = ring + kPairs * kPairBytes;
+
+  __shared__ __align__(8) uint64_t kv_full[kPairs], kv_empty[kPairs];
+  __shared__ __align__(8) uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
+  __shared__ __align__(8) uint64_t q_full, q_empty, o_full, o_empty, stat_full[2], stat_empty[2];
+  __shared__ __align__(8) uint64_t info_full[kInfoSlots], info_empty[kInfoSlots], drain;
+  __shared__ __align__(8) uint64_t key_mask[4];
+  __shared__ ItemInfo info[kInfoSlots];
+  __shared__ float factor[2][kHeadsPerItem], rescale[kHeadsPerItem];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  volatile int* abort = &abort_flag;
+  unsigned int* status = p.status;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairs; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&stat_full[i], 128);
+      mbar_init(&stat_empty[i], 4);
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    mbar_init(&o_full, 1);
+    mbar_init(&o_empty, 4);
+    for (int i = 0; i < kInfoSlots; ++i) {
+      mbar_init(&info_full[i], 1);
+      mbar_init(&info_empty[i], kInfoReaders);
+    }
+    mbar_init(&drain, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch(&tmap_q);
+    tma_prefetch(&tmap_kv);
+    tma_prefetch(&tmap_cell);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int n_mine = (p.items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+
+  if (warp == 2) {
+    // ------------------------------- scheduler ------------------------------
+    for (int i = 0; i < n_mine; ++i) {
+      const int slot = i % kInfoSlots;
+      const int item = (int)blockIdx.x + i * (int)gridDim.x;
+      const int split = item % p.splits, th = item / p.splits;
+      const int t = th / p.head_blocks;
+      // listed cells up to the last one that is not empty
+      int last = -1;
+      const int32_t* cells = p.cells + (int64_t)t * p.k;
+#pragma unroll 8
+      for (int c = lane; c < p.k; c += 32)
+        if (__ldg(cells + c) >= 0) last = c;
+      const int n_cells = __reduce_max_sync(0xffffffffu, last) + 1;
+      if (!warp_wait(&info_empty[slot], ((i / kInfoSlots) & 1) ^ 1, abort, status)) break;
+      if (lane == 0) {
+        const TokenKeys tk = token_keys(p, t);
+        ItemInfo f;
+        f.low = tk.low;
+        f.base = tk.base;
+        f.t = t;
+        f.head_block = th % p.head_blocks;
+        f.part = p.splits > 1 ? item : -1;
+        f.b = tk.b;
+        f.n_first = tk.n_first;
+        f.n_win = tk.n_win;
+        f.n_tree = tk.n_tree;
+        f.end_cells = up4(n_cells);
+        f.end_first = f.end_cells + up4(tk.n_first);
+        f.end_win = f.end_first + up4(tk.n_win);
+        f.end = f.end_win + tk.n_tree;
+        const int64_t tiles = (f.end + kTileKeys - 1) / kTileKeys;
+        f.tile_begin = (int)(tiles * split / p.splits);
+        f.tile_end = (int)(tiles * (split + 1) / p.splits);
+        // a split without keys still runs one tile, of no keys
+        if (f.tile_end == f.tile_begin) {
+          f.tile_begin = (int)tiles;
+          f.tile_end = (int)tiles + 1;
+        }
+        info[slot] = f;
+        mbar_arrive(&info_full[slot]);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 3) {
+    // ------------------------------- q loader -------------------------------
+    if (lane == 0) {
+      int loaded = 0;
+      for (int i = 0; i < n_mine; ++i) {
+        const int slot = i % kInfoSlots;
+        if (!mbar_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
+        const int t = info[slot].t, h0 = info[slot].head_block * kHeadsPerItem;
+        mbar_arrive(&info_empty[slot]);
+        if (!mbar_wait(&q_empty, (i & 1) ^ 1, abort, status)) break;
+        mbar_arrive_expect_tx(&q_full, kQBytes);
+        for (int c = 0; c < kWidth / 64; ++c) tma_load_3d(q_smem + c * kChunkBytes, &tmap_q, &q_full, 64 * c, h0, t);
+        loaded = i + 1;
+      }
+      if (loaded > 0 && *abort) mbar_wait_drain(&q_full, (loaded - 1) & 1);
+    }
+  } else if (warp == 0) {
+    // ------------------------------- producer -------------------------------
+    uint32_t n = 0, g = 0;  // pairs and tiles issued so far
+    bool ok = true;
+    for (int i = 0; i < n_mine && ok; ++i) {
+      const int slot = i % kInfoSlots;
+      if (!warp_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
+      const ItemInfo f = info[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&info_empty[slot]);
+      for (int tile = f.tile_begin; tile < f.tile_end && ok; ++tile, ++g) {
+        // this lane's four key slots lie in one range
+        int row[4] = {-1, -1, -1, -1};
+        const int s0 = tile * kTileKeys + 4 * lane;
+        const bool from_cells = s0 < f.end_cells;
+        if (lane < 16 && s0 < f.end) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int s = s0 + e;
+            if (from_cells) {
+              const int64_t cell = s < p.k ? __ldg(p.cells + (int64_t)f.t * p.k + s) : -1;
+              if (cell >= p.cell_limit) {
+                atomicOr(status, FM_DEV_PAGE_RANGE);
+              } else if (cell >= 0) {
+                row[e] = (int)((cell / kPage) * p.cell_page_rows + cell % kPage);
+              }
+            } else {
+              int64_t at = -1;
+              if (s < f.end_first) {
+                if (s - f.end_cells < f.n_first) at = s - f.end_cells;
+              } else if (s < f.end_win) {
+                if (s - f.end_first < f.n_win) at = f.low + (s - f.end_first);
+              } else {
+                const int d = s - f.end_win;
+                if ((__ldg(p.tree_mask + (int64_t)f.t * p.tree_words + (d >> 5)) >> (d & 31)) & 1u) at = f.base + d;
+              }
+              if (at >= 0) row[e] = token_row(p, f.b, at);
+            }
+          }
+        }
+        uint32_t nib = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) nib |= row[e] >= 0 ? 1u << e : 0u;
+        const uint32_t lo = __reduce_or_sync(0xffffffffu, lane < 8 ? nib << (4 * lane) : 0u);
+        const uint32_t hi = __reduce_or_sync(0xffffffffu, lane >= 8 && lane < 16 ? nib << (4 * (lane - 8)) : 0u);
+        if (lane == 0) key_mask[g & 3] = ((uint64_t)hi << 32) | lo;
+        const CUtensorMap* map = from_cells ? &tmap_cell : &tmap_kv;
+        for (int j = 0; j < kPairsPerTile; ++j) {
+          const uint32_t at = n % kPairs;
+          if (!warp_wait(&kv_empty[at], ((n / kPairs) & 1) ^ 1, abort, status)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&kv_full[at], kPairBytes);
+          __syncwarp();
+          if (lane < 16) {
+            uint8_t* dst = ring + at * kPairBytes + lane * 512;
+            tma_gather4(dst, map, &kv_full[at], 128 * j, row);
+            tma_gather4(dst + kChunkBytes, map, &kv_full[at], 128 * j + 64, row);
+          }
+          ++n;
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && *abort) {  // let copies in flight land before the CTA exits
+      for (uint32_t x = n > kPairs ? n - kPairs : 0; x < n; ++x) mbar_wait_drain(&kv_full[x % kPairs], (x / kPairs) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------ MMA issuer ------------------------------
+    if (lane == 0) {
+      const uint32_t idesc_s = idesc_bf16_f32(64, kTileKeys);
+      const uint32_t idesc_o = idesc_bf16_f32(128, kHeadsPerItem) | kAIsMnMajor;
+      const uint64_t q_desc = sdesc_sw128(smem_u32(q_smem));
+      const uint64_t k_desc = sdesc_sw128(smem_u32(ring));
+      const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring));
+      const uint64_t p_desc = sdesc_sw128(smem_u32(p_smem));
+      uint32_t n = 0, g = 0;
+      bool ok = true, have = false, first_prev = false, last_prev = false;
+      uint32_t n_prev = 0, o_seq = 0;
+      // O^T += C^T P^T of the previous tile; each pair of chunks is a block of 128 elements
+      auto second = [&]() -> bool {
+        const uint32_t gp = g - 1;
+        if (!mbar_wait(&p_full[gp & 1], (gp >> 1) & 1, abort, status)) return false;
+        if (first_prev && !mbar_wait(&o_empty, (o_seq & 1) ^ 1, abort, status)) return false;
+        tc_fence_after();
+        const uint64_t b = p_desc + (uint64_t)((gp & 1) * (kPBytes >> 4));
+        for (int m = 0; m < kPairsPerTile; ++m) {
+          const uint32_t at = (n_prev + m) % kPairs;
+          const uint64_t a = v_desc + (uint64_t)(at * (kPairBytes >> 4));
+#pragma unroll
+          for (int kk = 0; kk < kTileKeys / 16; ++kk)
+            umma_bf16_ss(tmem + m * kHeadsPerItem, a + kk * (2048 >> 4), b + kk * 2, idesc_o,
+                         first_prev && kk == 0 ? 0u : 1u);
+          umma_commit(&kv_empty[at]);
+        }
+        umma_commit(&pv_done[gp & 1]);
+        if (last_prev) {
+          umma_commit(&o_full);
+          ++o_seq;
+        }
+        return true;
+      };
+      for (int i = 0; i < n_mine && ok; ++i) {
+        const int slot = i % kInfoSlots;
+        if (!mbar_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
+        const int begin = info[slot].tile_begin, end = info[slot].tile_end;
+        mbar_arrive(&info_empty[slot]);
+        for (int tile = begin; tile < end; ++tile) {
+          if (tile == begin && !(ok = mbar_wait(&q_full, i & 1, abort, status))) break;
+          if (!(ok = mbar_wait(&s_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
+          const uint32_t d = tmem + kSCol + (g & 1) * kTileKeys;
+          for (int j = 0; j < kPairsPerTile; ++j) {
+            const uint32_t at = (n + j) % kPairs;
+            if (!(ok = mbar_wait(&kv_full[at], ((n + j) / kPairs) & 1, abort, status))) break;
+            tc_fence_after();
+            const uint64_t a = q_desc + (uint64_t)(j * (kPairBytes >> 4));
+            const uint64_t b = k_desc + (uint64_t)(at * (kPairBytes >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint64_t o = (uint64_t)((kk >> 2) * (kChunkBytes >> 4) + (kk & 3) * 2);
+              umma_bf16_ss(d, a + o, b + o, idesc_s, (j | kk) != 0 ? 1u : 0u);
+            }
+          }
+          if (!ok) break;
+          umma_commit(&s_full[g & 1]);
+          if (tile == end - 1) umma_commit(&q_empty);
+          if (have && !(ok = second())) break;
+          have = true;
+          first_prev = tile == begin;
+          last_prev = tile == end - 1;
+          n_prev = n;
+          n += kPairsPerTile;
+          ++g;
+        }
+      }
+      if (ok && have && !*abort) second();
+      umma_commit(&drain);
+      mbar_wait_drain(&drain, 0);
+    }
+  } else if (warp < 8) {
+    // ------------------------------- softmax --------------------------------
+    // Warp quad w holds heads 16 w .. 16 w + 15 of the block (S's rows in the
+    // first 16 lanes of its quadrant); a thread has two of them, r0 and r0 + 8,
+    // and 16 keys of each.
+    const int quad = warp & 3;
+    const int r0 = quad * 16 + lane / 4;
+    const float c = p.scale * kLog2e;
+    uint32_t g = 0, n = 0;
+    bool dead = false;
+    for (int i = 0; i < n_mine; ++i) {
+      const int slot = i % kInfoSlots;
+      bool ok = !dead && mbar_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status);
+      if (softmax_any(!ok)) break;
+      const int tiles = info[slot].tile_end - info[slot].tile_begin;
+      const int t = info[slot].t, h0 = info[slot].head_block * kHeadsPerItem, part = info[slot].part;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&info_empty[slot]);
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // m in units of S, l of this thread's keys
+      bool left = false;
+      for (int tile = 0; tile < tiles; ++tile, ++g, n += kPairsPerTile) {
+        // the tile's mask came with its first pair of chunks, whose barrier is complete
+        ok = !dead && mbar_wait(&s_full[g & 1], (g >> 1) & 1, abort, status) &&
+             mbar_wait(&kv_full[n % kPairs], (n / kPairs) & 1, abort, status);
+        ok = __all_sync(0xffffffffu, ok);
+        uint32_t raw[32];
+        float top[2] = {-INFINITY, -INFINITY};
+        bool need = false;
+        if (ok) {
+          tc_fence_after();
+          tmem_ld_16x256b_x8(tmem + ((uint32_t)(quad * 32) << 16) + kSCol + (g & 1) * kTileKeys, raw);
+          const uint64_t mask = key_mask[g & 3];
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[g & 1]);
+          if (mask != ~0ull) {
+            const uint32_t lo = (uint32_t)(mask >> (2 * (lane & 3))), hi = (uint32_t)(mask >> (32 + 2 * (lane & 3)));
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if ((((j < 4 ? lo : hi) >> (8 * (j & 3) + e)) & 1u) == 0)
+                  raw[4 * j + e] = raw[4 * j + 2 + e] = 0xFF800000u;  // -inf
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              top[r] = fmaxf(top[r], fmaxf(__uint_as_float(raw[4 * j + 2 * r]), __uint_as_float(raw[4 * j + 2 * r + 1])));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+          }
+          // the maximum in use may be passed by up to 2^8 before the sums so far
+          // are rescaled: the weights' bf16 and the fp32 sums lose nothing by it
+          need = tile > 0 && (top[0] * c > m[0] * c + 8.f || top[1] * c > m[1] * c + 8.f);
+        }
+        if (softmax_any(need || !ok)) {
+          if (softmax_any(!ok)) {
+            left = true;
+            break;
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float f = 1.f;
+            if (top[r] * c > m[r] * c + 8.f) {
+              f = m[r] == -INFINITY ? 0.f : exp2_fast((m[r] - top[r]) * c);
+              m[r] = top[r];
+            }
+            l[r] *= f;
+            if ((lane & 3) == 0) rescale[r0 + 8 * r] = f;
+          }
+          const uint32_t gp = g - 1;
+          ok = mbar_wait(&pv_done[gp & 1], (gp >> 1) & 1, abort, status);
+          if (softmax_any(!ok)) {
+            left = true;
+            break;
+          }
+          tc_fence_after();
+          for (int x = 0; x < 8; ++x) {
+            uint32_t o[32];
+            const uint32_t addr = tmem + ((uint32_t)(quad * 32) << 16) + 32 * x;
+            tmem_ld32(addr, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < 32; ++h)
+              o[h] = __float_as_uint(__uint_as_float(o[h]) * rescale[(x & 1) * 32 + h]);
+            tmem_st32(addr, o);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+        } else if (tile == 0) {
+          m[0] = top[0];
+          m[1] = top[1];
+        }
+        // weights, their sums, and P (bf16) in rows of 128 bytes, swizzled
+        const float mc[2] = {m[0] == -INFINITY ? 0.f : m[0] * c, m[1] == -INFINITY ? 0.f : m[1] * c};
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float a = exp2_fast(fmaf(__uint_as_float(raw[4 * j + 2 * r]), c, -mc[r]));
+            const float b = exp2_fast(fmaf(__uint_as_float(raw[4 * j + 2 * r + 1]), c, -mc[r]));
+            l[r] += a + b;
+            w[2 * j + r] = pack_bf16(a, b);
+          }
+        if (!mbar_wait(&pv_done[g & 1], ((g >> 1) & 1) ^ 1, abort, status)) {
+          dead = true;  // leave together with the others, at the next tile or item
+          continue;
+        }
+        uint8_t* dst = p_smem + (g & 1) * kPBytes + (lane & 3) * 4;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int row = r0 + 8 * r;
+            *reinterpret_cast<uint32_t*>(dst + row * 128 + ((j ^ (row & 7)) << 4)) = w[2 * j + r];
+          }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(&p_full[g & 1]);
+      }
+      if (left) break;
+      if (!dead && !mbar_wait(&stat_empty[i & 1], ((i >> 1) & 1) ^ 1, abort, status)) dead = true;
+      if (dead) continue;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float sum = l[r];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int hl = r0 + 8 * r, h = h0 + hl;
+        if ((lane & 3) == 0) {
+          if (part >= 0) {
+            factor[i & 1][hl] = 1.f;
+            p.part_ml[(int64_t)part * kHeadsPerItem + hl] = make_float2(m[r] * c, sum);
+          } else {
+            float below = sum;
+            if (p.sink_logit != nullptr && h < p.n_h) below += exp2f(fmaf(__ldg(p.sink_logit + h), kLog2e, -m[r] * c));
+            factor[i & 1][hl] = sum == 0.f ? 0.f : 1.f / below;
+            if (p.lse != nullptr && h < p.n_h)
+              p.lse[(int64_t)t * p.n_h + h] = sum == 0.f ? -INFINITY : m[r] * p.scale + logf(sum);
+          }
+        }
+      }
+      mbar_arrive(&stat_full[i & 1]);
+    }
+  } else {
+    // ------------------------------- epilogue -------------------------------
+    const int quad = warp & 3;
+    for (int i = 0; i < n_mine; ++i) {
+      const int slot = i % kInfoSlots;
+      if (!warp_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
+      const int t = info[slot].t, h0 = info[slot].head_block * kHeadsPerItem, part = info[slot].part;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&info_empty[slot]);
+      if (!warp_wait(&stat_full[i & 1], (i >> 1) & 1, abort, status)) break;
+      if (!warp_wait(&o_full, i & 1, abort, status)) break;
+      tc_fence_after();
+      const int heads = min(kHeadsPerItem, p.n_h - h0);
+#pragma unroll 1
+      for (int x = 0; x < 8; ++x) {
+        uint32_t o[32];
+        tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + 32 * x, o);
+        tmem_ld_wait();
+        const int hl0 = (x & 1) * 32, d = (x >> 1) * 128 + quad * 32 + lane;
+        if (part >= 0) {
+          float* dst = p.part_o + ((int64_t)part * kHeadsPerItem + hl0) * kWidth + d;
+#pragma unroll
+          for (int h = 0; h < 32; ++h)
+            if (hl0 + h < heads) dst[h * kWidth] = __uint_as_float(o[h]);
+        } else {
+          uint16_t* dst = p.out + ((int64_t)t * p.n_h + h0 + hl0) * kWidth + d;
+#pragma unroll
+          for (int h = 0; h < 32; ++h)
+            if (hl0 + h < heads)
+              dst[h * kWidth] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[h]) * factor[i & 1][hl0 + h]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&o_empty);
+        mbar_arrive(&stat_empty[i & 1]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the splits of one (token, head): out = sum_s 2^(m_s - M) O_s / (sum_s
+// 2^(m_s - M) l_s + sink), the splits in order.
+__global__ void __launch_bounds__(128) csa_merge_kernel(const __grid_constant__ AttnParams p) {
+  const int64_t th = blockIdx.x;
+  const int h = (int)(th % p.n_h), hl = h % kHeadsPerItem;
+  const int64_t t = th / p.n_h;
+  const int64_t part0 = (t * p.head_blocks + h / kHeadsPerItem) * p.splits;
+  float top = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_ml[(part0 + s) * kHeadsPerItem + hl].x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  const int d = 4 * threadIdx.x;
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = p.part_ml[(part0 + s) * kHeadsPerItem + hl];
+    if (ml.y == 0.f) continue;  // a split without keys
+    const float w = exp2f(ml.x - top);
+    sum = fmaf(w, ml.y, sum);
+    const float4 o = *reinterpret_cast<const float4*>(p.part_o + ((part0 + s) * kHeadsPerItem + hl) * kWidth + d);
+    acc.x = fmaf(w, o.x, acc.x);
+    acc.y = fmaf(w, o.y, acc.y);
+    acc.z = fmaf(w, o.z, acc.z);
+    acc.w = fmaf(w, o.w, acc.w);
+  }
+  float below = sum;
+  if (p.sink_logit != nullptr) below += exp2f(fmaf(p.sink_logit[h], kLog2e, -top));
+  const float f = sum == 0.f ? 0.f : 1.f / below;
+  uint2 v;
+  v.x = pack_bf16(acc.x * f, acc.y * f);
+  v.y = pack_bf16(acc.z * f, acc.w * f);
+  *reinterpret_cast<uint2*>(p.out + th * kWidth + d) = v;
+  if (p.lse != nullptr && threadIdx.x == 0)
+    p.lse[th] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+int head_blocks_of(int n_h) { return (n_h + kHeadsPerItem - 1) / kHeadsPerItem; }
+
+size_t attn_workspace_bytes(int T, int n_h) {
+  const int64_t items = (int64_t)T * head_blocks_of(n_h);
+  if (items == 0 || items > kMaxParts / 2) return 0;  // such calls never split
+  const int64_t parts = kMaxParts / items * items;
+  return (size_t)parts * kHeadsPerItem * (kWidth * sizeof(float) + sizeof(float2));
+}
+
+fm_status launch_attn(AttnParams& p, const uint16_t* q, const uint16_t* kv_pool, const uint16_t* cell_pool, int64_t Pc,
+                      int sms, void* workspace, cudaStream_t stream) {
+  p.head_blocks = head_blocks_of(p.n_h);
+  const int64_t items = (int64_t)p.T * p.head_blocks;
+  if (items * kMaxParts >= (int64_t(1) << 31))
+    return set_error(FM_ERR_INVALID_ARG, "fm_csa_attn: T=%d n_h=%d: too many head blocks", p.T, p.n_h);
+  // tiles that a token can have at most
+  const int64_t held = (int64_t)p.R * kPage;
+  const int64_t slots = (p.window < held ? p.window : held) + (p.n_sink < held ? p.n_sink : held) + p.k +
+                        (p.tree_mask != nullptr ? 32 * p.tree_words : 0) + 12;
+  const int64_t max_tiles = (slots + kTileKeys - 1) / kTileKeys;
+  int64_t splits = items <= kMaxParts / 2 ? (sms < kMaxParts ? sms : kMaxParts) / items : 1;
+  if (splits > max_tiles) splits = max_tiles;
+  if (splits < 1) splits = 1;
+  p.splits = (int)splits;
+  p.items = (int)(items * splits);
+  const size_t parts = (size_t)p.items;
+  p.part_ml = static_cast<float2*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + parts * kHeadsPerItem * sizeof(float2));
+
+  CUtensorMap tq, tkv, tc;
+  const uint64_t qd[3] = {(uint64_t)kWidth, (uint64_t)p.n_h, (uint64_t)p.T};
+  const uint64_t qs[2] = {(uint64_t)kWidth * 2, (uint64_t)kWidth * 2 * p.n_h};
+  const uint32_t qb[3] = {64, kHeadsPerItem, 1};
+  fm_status st = make_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != FM_OK) return st;
+  // a gather reads single rows of the pools; an empty pool gets a map that no row is read through
+  auto pool_map = [&](CUtensorMap* map, const uint16_t* pool, int64_t pages, int64_t page_rows) {
+    const uint64_t d[2] = {(uint64_t)kWidth, pages > 0 ? (uint64_t)((pages - 1) * page_rows + kPage) : 1};
+    const uint64_t s[1] = {(uint64_t)kWidth * 2};
+    const uint32_t b[2] = {64, 1};
+    return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pages > 0 ? pool : q, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if ((st = pool_map(&tkv, kv_pool, p.P, p.kv_page_rows)) != FM_OK) return st;
+  if ((st = pool_map(&tc, cell_pool, p.k > 0 ? Pc : 0, p.cell_page_rows)) != FM_OK) return st;
+  cudaError_t e = cudaFuncSetAttribute(csa_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return set_error(FM_ERR_CUDA, "fm_csa_attn: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  const int grid = p.items < sms ? p.items : sms;
+  csa_attn_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tq, tkv, tc, p);
+  if ((e = cudaGetLastError()) != cudaSuccess)
+    return set_error(FM_ERR_CUDA, "fm_csa_attn: launch: %s", cudaGetErrorString(e));
+  if (p.splits > 1) {
+    csa_merge_kernel<<<(unsigned)((int64_t)p.T * p.n_h), 128, 0, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess)
+      return set_error(FM_ERR_CUDA, "fm_csa_attn: merge launch: %s", cudaGetErrorString(e));
+  }
   return FM_OK;
 }
 
@@ -215,12 +815,9 @@ fm_status csa_attn(const char* who, bool tree, const uint16_t* q, int T, int n_h
   if (st != FM_OK) return st;
   AttnParams p = {};
   if ((st = status_word(&p.status)) != FM_OK) return st;
-  p.q = q;
-  p.kv_pool = kv_pool;
   p.page_table = page_table;
   p.seq = seq;
   p.pos = pos;
-  p.cell_pool = cell_pool;
   p.cells = cells;
   p.sink_logit = sink_logit;
   p.tree_mask = tree ? tree_mask : nullptr;
@@ -240,7 +837,7 @@ fm_status csa_attn(const char* who, bool tree, const uint16_t* q, int T, int n_h
   p.n_sink = n_sink;
   p.tree_words = tree_words;
   p.scale = scale;
-  return launch_attn(p, sms, workspace, stream);
+  return launch_attn(p, q, kv_pool, cell_pool, Pc, sms, workspace, stream);
 }
 
 }  // namespace
