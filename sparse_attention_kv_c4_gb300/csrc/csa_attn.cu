@@ -8,18 +8,20 @@
 // unit of work is one token's block of 64 heads against tiles of 64 keys
 // (131 kFLOP per key of 1 KB).  A persistent CTA per SM walks its items (token,
 // head block, split of the keys):
-//   scheduler   (warp 2)  each item's key ranges, into a ring of four
-//   q loader    (warp 3)  the item's 64 query rows, eight SWIZZLE_128B chunks
-//               [64 heads x 64 elements] of 8 KB
-//   producer    (warp 0)  each tile's 64 pool rows by TMA tile::gather4: 16 lanes
-//               take four keys each.  The ring holds nine pairs of chunks [64
-//               keys x 64 elements], four pairs to a tile; a key that is none
-//               is row -1, which the copy fills with zeros without a read, and
-//               a zero bit of the tile's mask
-//   MMA issuer  (warp 1)  S = Q C^T: tcgen05 M64 N64, 32 steps of K16;
+//   scheduler   (warp 1)  each item's key ranges, into a ring of four, and its
+//               64 query rows by TMA: eight SWIZZLE_128B chunks [64 heads x 64
+//               elements] of 8 KB
+//   producers   (warps 2, 3)  each tile's 64 pool rows by 16-byte cp.async, a
+//               lane per key for the row's address and 16 lanes per row for its
+//               copies, swizzled as TMA would.  The ring holds nine pairs of
+//               chunks [64 keys x 64 elements], four pairs to a tile; a key
+//               that is none is filled with zeros without a read, and is a zero
+//               bit of the tile's mask
+//   MMA issuer  (warp 0)  S = Q C^T: tcgen05 M64 N64, 32 steps of K16;
 //               O^T += C^T P^T: M128 N64, four blocks of 128 elements x four
-//               steps of K16.  The cell tile is read twice from shared memory,
-//               K-major as keys and MN-major as values, and loaded once
+//               steps of K16, whichever has its operands first.  The cell tile
+//               is read twice from shared memory, K-major as keys and MN-major
+//               as values, and loaded once
 //   softmax     (warps 4-7)  S from TMEM, the running maximum and sum, P in
 //               bf16 to shared memory
 //   epilogue    (warps 8-11)  O^T from TMEM, times 1 / (sum + sink), to out
@@ -55,11 +57,14 @@ constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;                  // allocations are powers of two
 constexpr int kSCol = 256;                      // the S buffers behind O^T's 256 columns
 constexpr int kInfoSlots = 4;
-constexpr int kInfoReaders = 1 + 1 + 1 + 4 + 4; // producer, issuer, q loader, softmax and epilogue warps
+constexpr int kInfoReaders = 2 + 1 + 4 + 4;     // producers, issuer, softmax and epilogue warps
+constexpr int kKvArrivals = 64 + 2;             // the producers' copies, and their first lanes
 constexpr int kMaxParts = 256;                  // partial results of one call
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
+  const uint16_t* kv_pool;
+  const uint16_t* cell_pool;
   const int32_t* page_table;
   const int32_t* seq;
   const int64_t* pos;
@@ -132,26 +137,25 @@ FM_DEV int token_row(const AttnParams& p, int b, int64_t slot) {
   return page < 0 ? -1 : (int)(page * p.kv_page_rows + slot % kPage);
 }
 
-// What the roles know of one item.  Key slots: the four ranges in order, each
-// rounded up to a multiple of four (one gather4 reads one pool).
+// What the roles know of one item.  Its key slots are the four ranges in order.
 struct ItemInfo {
   int64_t low, base;
   int t, head_block, part;                 // part: index of the partial result, -1 = whole
   int tile_begin, tile_end;                // at least one tile
-  int b, n_first, n_win, n_tree;
+  int b;
   int end_cells, end_first, end_win, end;  // ends of the ranges, in slots
 };
 
-FM_DEV int up4(int x) { return (x + 3) & ~3; }
-
-FM_DEV void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int x, const int (&row)[4]) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
-      "%5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]),
-      "r"(row[3])
-      : "memory");
+// 16 bytes global -> shared, or 16 zero bytes where there is nothing to read.
+FM_DEV void cp_async16(uint32_t dst, const void* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16u : 0u) : "memory");
 }
+// Arrive on `bar` when this thread's copies so far have landed.
+FM_DEV void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+FM_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+FM_DEV void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 FM_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
@@ -214,6 +218,19 @@ FM_DEV uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Whether the phase with the given parity is complete, without a wait.
+FM_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Lane 0 waits, every lane learns the result.
 FM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
   int ok = 1;
@@ -225,8 +242,7 @@ FM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsig
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    csa_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_kv,
-                    const __grid_constant__ CUtensorMap tmap_cell, const __grid_constant__ AttnParams p) {
+    csa_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_smem = smem;
@@ -237,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
   __shared__ __align__(8) uint64_t q_full, q_empty, o_full, o_empty, stat_full[2], stat_empty[2];
   __shared__ __align__(8) uint64_t info_full[kInfoSlots], info_empty[kInfoSlots], drain;
-  __shared__ __align__(8) uint64_t key_mask[4];
+  __shared__ __align__(8) uint32_t key_mask[4][2];
   __shared__ ItemInfo info[kInfoSlots];
   __shared__ float factor[2][kHeadsPerItem], rescale[kHeadsPerItem];
   __shared__ uint32_t tmem_slot;
@@ -249,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPairs; ++i) {
-      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_full[i], kKvArrivals);
       mbar_init(&kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -272,12 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch(&tmap_q);
-    tma_prefetch(&tmap_kv);
-    tma_prefetch(&tmap_cell);
-  }
-  if (warp == 1) {
+  if (warp == 1 && lane == 0) tma_prefetch(&tmap_q);
+  if (warp == 0) {
     tmem_alloc(&tmem_slot, kTmemCols);
     tmem_relinquish();
   }
@@ -287,13 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   const int n_mine = (p.items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
 
-  if (warp == 2) {
-    // ------------------------------- scheduler ------------------------------
+  if (warp == 1) {
+    // ------------------------- scheduler, q loader --------------------------
+    int loaded = 0;
     for (int i = 0; i < n_mine; ++i) {
       const int slot = i % kInfoSlots;
       const int item = (int)blockIdx.x + i * (int)gridDim.x;
       const int split = item % p.splits, th = item / p.splits;
-      const int t = th / p.head_blocks;
+      const int t = th / p.head_blocks, head_block = th % p.head_blocks;
       // listed cells up to the last one that is not empty
       int last = -1;
       const int32_t* cells = p.cells + (int64_t)t * p.k;
@@ -308,15 +321,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         f.low = tk.low;
         f.base = tk.base;
         f.t = t;
-        f.head_block = th % p.head_blocks;
+        f.head_block = head_block;
         f.part = p.splits > 1 ? item : -1;
         f.b = tk.b;
-        f.n_first = tk.n_first;
-        f.n_win = tk.n_win;
-        f.n_tree = tk.n_tree;
-        f.end_cells = up4(n_cells);
-        f.end_first = f.end_cells + up4(tk.n_first);
-        f.end_win = f.end_first + up4(tk.n_win);
+        f.end_cells = n_cells;
+        f.end_first = f.end_cells + tk.n_first;
+        f.end_win = f.end_first + tk.n_win;
         f.end = f.end_win + tk.n_tree;
         const int64_t tiles = (f.end + kTileKeys - 1) / kTileKeys;
         f.tile_begin = (int)(tiles * split / p.splits);
@@ -330,25 +340,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&info_full[slot]);
       }
       __syncwarp();
-    }
-  } else if (warp == 3) {
-    // ------------------------------- q loader -------------------------------
-    if (lane == 0) {
-      int loaded = 0;
-      for (int i = 0; i < n_mine; ++i) {
-        const int slot = i % kInfoSlots;
-        if (!mbar_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
-        const int t = info[slot].t, h0 = info[slot].head_block * kHeadsPerItem;
-        mbar_arrive(&info_empty[slot]);
-        if (!mbar_wait(&q_empty, (i & 1) ^ 1, abort, status)) break;
+      if (!warp_wait(&q_empty, (i & 1) ^ 1, abort, status)) break;
+      if (lane == 0) {
         mbar_arrive_expect_tx(&q_full, kQBytes);
-        for (int c = 0; c < kWidth / 64; ++c) tma_load_3d(q_smem + c * kChunkBytes, &tmap_q, &q_full, 64 * c, h0, t);
-        loaded = i + 1;
+        for (int c = 0; c < kWidth / 64; ++c)
+          tma_load_3d(q_smem + c * kChunkBytes, &tmap_q, &q_full, 64 * c, head_block * kHeadsPerItem, t);
       }
-      if (loaded > 0 && *abort) mbar_wait_drain(&q_full, (loaded - 1) & 1);
+      __syncwarp();
+      loaded = i + 1;
     }
-  } else if (warp == 0) {
-    // ------------------------------- producer -------------------------------
+    if (lane == 0 && loaded > 0 && *abort) mbar_wait_drain(&q_full, (loaded - 1) & 1);
+  } else if (warp == 2 || warp == 3) {
+    // ------------------------------- producers ------------------------------
+    // Warp w takes the tile's keys 32 w .. 32 w + 31.  Copy i of a pair moves the
+    // rows of keys 2 i and 2 i + 1: lane l < 16 the 16-byte units l of the
+    // first, the others those of the second.
+    const int half = warp - 2, hi = lane >> 4, unit = lane & 15;
+    const uint32_t lane_dst = smem_u32(ring) + half * 32 * 128 + (unit >> 3) * kChunkBytes + hi * 128 +
+                              (((unit & 7) ^ hi) << 4);
     uint32_t n = 0, g = 0;  // pairs and tiles issued so far
     bool ok = true;
     for (int i = 0; i < n_mine && ok; ++i) {
@@ -358,64 +367,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&info_empty[slot]);
       for (int tile = f.tile_begin; tile < f.tile_end && ok; ++tile, ++g) {
-        // this lane's four key slots lie in one range
-        int row[4] = {-1, -1, -1, -1};
-        const int s0 = tile * kTileKeys + 4 * lane;
-        const bool from_cells = s0 < f.end_cells;
-        if (lane < 16 && s0 < f.end) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int s = s0 + e;
-            if (from_cells) {
-              const int64_t cell = s < p.k ? __ldg(p.cells + (int64_t)f.t * p.k + s) : -1;
-              if (cell >= p.cell_limit) {
-                atomicOr(status, FM_DEV_PAGE_RANGE);
-              } else if (cell >= 0) {
-                row[e] = (int)((cell / kPage) * p.cell_page_rows + cell % kPage);
-              }
-            } else {
-              int64_t at = -1;
-              if (s < f.end_first) {
-                if (s - f.end_cells < f.n_first) at = s - f.end_cells;
-              } else if (s < f.end_win) {
-                if (s - f.end_first < f.n_win) at = f.low + (s - f.end_first);
-              } else {
-                const int d = s - f.end_win;
-                if ((__ldg(p.tree_mask + (int64_t)f.t * p.tree_words + (d >> 5)) >> (d & 31)) & 1u) at = f.base + d;
-              }
-              if (at >= 0) row[e] = token_row(p, f.b, at);
-            }
+        // this lane's key: its row's address, or 0
+        const int s = tile * kTileKeys + half * 32 + lane;
+        uint64_t row = 0;
+        if (s < f.end_cells) {
+          const int64_t cell = __ldg(p.cells + (int64_t)f.t * p.k + s);
+          if (cell >= p.cell_limit)
+            atomicOr(status, FM_DEV_PAGE_RANGE);
+          else if (cell >= 0)
+            row = reinterpret_cast<uint64_t>(p.cell_pool + ((cell / kPage) * p.cell_page_rows + cell % kPage) * kWidth);
+        } else if (s < f.end) {
+          int64_t at = s - f.end_cells;
+          if (s >= f.end_win) {
+            const int d = s - f.end_win;
+            at = (__ldg(p.tree_mask + (int64_t)f.t * p.tree_words + (d >> 5)) >> (d & 31)) & 1u ? f.base + d : -1;
+          } else if (s >= f.end_first) {
+            at = f.low + (s - f.end_first);
           }
+          const int64_t r = at >= 0 ? token_row(p, f.b, at) : -1;
+          if (r >= 0) row = reinterpret_cast<uint64_t>(p.kv_pool + r * kWidth);
         }
-        uint32_t nib = 0;
+        const uint32_t mask = __ballot_sync(0xffffffffu, row != 0);
+        if (lane == 0) key_mask[g & 3][half] = mask;
+        uint64_t src[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) nib |= row[e] >= 0 ? 1u << e : 0u;
-        const uint32_t lo = __reduce_or_sync(0xffffffffu, lane < 8 ? nib << (4 * lane) : 0u);
-        const uint32_t hi = __reduce_or_sync(0xffffffffu, lane >= 8 && lane < 16 ? nib << (4 * (lane - 8)) : 0u);
-        if (lane == 0) key_mask[g & 3] = ((uint64_t)hi << 32) | lo;
-        const CUtensorMap* map = from_cells ? &tmap_cell : &tmap_kv;
+        for (int c = 0; c < 16; ++c) src[c] = __shfl_sync(0xffffffffu, row, 2 * c + hi);
         for (int j = 0; j < kPairsPerTile; ++j) {
           const uint32_t at = n % kPairs;
           if (!warp_wait(&kv_empty[at], ((n / kPairs) & 1) ^ 1, abort, status)) {
             ok = false;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(&kv_full[at], kPairBytes);
-          __syncwarp();
-          if (lane < 16) {
-            uint8_t* dst = ring + at * kPairBytes + lane * 512;
-            tma_gather4(dst, map, &kv_full[at], 128 * j, row);
-            tma_gather4(dst + kChunkBytes, map, &kv_full[at], 128 * j + 64, row);
+          const uint32_t dst = lane_dst + at * kPairBytes;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const bool read = src[c] != 0;
+            const uint8_t* from = read ? reinterpret_cast<const uint8_t*>(src[c]) + j * 256 + unit * 16
+                                       : reinterpret_cast<const uint8_t*>(p.pos);  // any address: nothing is read
+            cp_async16((dst ^ ((2 * c & 7) << 4)) + c * 256, from, read);
           }
+          cp_async_arrive(&kv_full[at]);
+          if (lane == 0) mbar_arrive(&kv_full[at]);  // releases the mask
           ++n;
         }
       }
     }
-    __syncwarp();
-    if (lane == 0 && *abort) {  // let copies in flight land before the CTA exits
-      for (uint32_t x = n > kPairs ? n - kPairs : 0; x < n; ++x) mbar_wait_drain(&kv_full[x % kPairs], (x / kPairs) & 1);
-    }
-  } else if (warp == 1) {
+    cp_async_wait_all();
+  } else if (warp == 0) {
     // ------------------------------ MMA issuer ------------------------------
     if (lane == 0) {
       const uint32_t idesc_s = idesc_bf16_f32(64, kTileKeys);
@@ -424,66 +422,81 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t k_desc = sdesc_sw128(smem_u32(ring));
       const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring));
       const uint64_t p_desc = sdesc_sw128(smem_u32(p_smem));
-      uint32_t n = 0, g = 0;
-      bool ok = true, have = false, first_prev = false, last_prev = false;
-      uint32_t n_prev = 0, o_seq = 0;
-      // O^T += C^T P^T of the previous tile; each pair of chunks is a block of 128 elements
-      auto second = [&]() -> bool {
-        const uint32_t gp = g - 1;
-        if (!mbar_wait(&p_full[gp & 1], (gp >> 1) & 1, abort, status)) return false;
-        if (first_prev && !mbar_wait(&o_empty, (o_seq & 1) ^ 1, abort, status)) return false;
-        tc_fence_after();
-        const uint64_t b = p_desc + (uint64_t)((gp & 1) * (kPBytes >> 4));
-        for (int m = 0; m < kPairsPerTile; ++m) {
-          const uint32_t at = (n_prev + m) % kPairs;
-          const uint64_t a = v_desc + (uint64_t)(at * (kPairBytes >> 4));
+      // The next steps are pair `pair` of tile gs's S and all of tile gv's O;
+      // tiles are numbered over all of the CTA's items.
+      uint32_t gs = 0, gv = 0, pair = 0, idle = 0;
+      int item_s = 0, item_v = 0;          // items that the two tiles belong to
+      int left_s = 0, left_v = 0;          // their tiles not yet done (0: not looked up)
+      bool first_v = true;
+      uint64_t t0 = 0;
+      while (item_v < n_mine) {
+        bool progress = false;
+        // O^T += C^T P^T; each pair of chunks is a block of 128 elements
+        if (gv < gs && mbar_test(&p_full[gv & 1], (gv >> 1) & 1) && (!first_v || mbar_test(&o_empty, (item_v & 1) ^ 1))) {
+          const ItemInfo& f = info[item_v % kInfoSlots];
+          if (first_v) left_v = f.tile_end - f.tile_begin;
+          tc_fence_after();
+          const uint64_t b = p_desc + (uint64_t)((gv & 1) * (kPBytes >> 4));
+          for (int m = 0; m < kPairsPerTile; ++m) {
+            const uint32_t at = (gv * kPairsPerTile + m) % kPairs;
+            const uint64_t a = v_desc + (uint64_t)(at * (kPairBytes >> 4));
 #pragma unroll
-          for (int kk = 0; kk < kTileKeys / 16; ++kk)
-            umma_bf16_ss(tmem + m * kHeadsPerItem, a + kk * (2048 >> 4), b + kk * 2, idesc_o,
-                         first_prev && kk == 0 ? 0u : 1u);
-          umma_commit(&kv_empty[at]);
+            for (int kk = 0; kk < kTileKeys / 16; ++kk)
+              umma_bf16_ss(tmem + m * kHeadsPerItem, a + kk * (2048 >> 4), b + kk * 2, idesc_o,
+                           first_v && kk == 0 ? 0u : 1u);
+            umma_commit(&kv_empty[at]);
+          }
+          umma_commit(&pv_done[gv & 1]);
+          ++gv;
+          first_v = false;
+          if (--left_v == 0) {
+            umma_commit(&o_full);
+            mbar_arrive(&info_empty[item_v % kInfoSlots]);
+            ++item_v;
+            first_v = true;
+          }
+          progress = true;
         }
-        umma_commit(&pv_done[gp & 1]);
-        if (last_prev) {
-          umma_commit(&o_full);
-          ++o_seq;
+        if (left_s == 0 && item_s < n_mine && mbar_test(&info_full[item_s % kInfoSlots], (item_s / kInfoSlots) & 1) &&
+            mbar_test(&q_full, item_s & 1)) {
+          left_s = info[item_s % kInfoSlots].tile_end - info[item_s % kInfoSlots].tile_begin;
         }
-        return true;
-      };
-      for (int i = 0; i < n_mine && ok; ++i) {
-        const int slot = i % kInfoSlots;
-        if (!mbar_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
-        const int begin = info[slot].tile_begin, end = info[slot].tile_end;
-        mbar_arrive(&info_empty[slot]);
-        for (int tile = begin; tile < end; ++tile) {
-          if (tile == begin && !(ok = mbar_wait(&q_full, i & 1, abort, status))) break;
-          if (!(ok = mbar_wait(&s_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
-          const uint32_t d = tmem + kSCol + (g & 1) * kTileKeys;
-          for (int j = 0; j < kPairsPerTile; ++j) {
-            const uint32_t at = (n + j) % kPairs;
-            if (!(ok = mbar_wait(&kv_full[at], ((n + j) / kPairs) & 1, abort, status))) break;
-            tc_fence_after();
-            const uint64_t a = q_desc + (uint64_t)(j * (kPairBytes >> 4));
-            const uint64_t b = k_desc + (uint64_t)(at * (kPairBytes >> 4));
+        const uint32_t n = gs * kPairsPerTile + pair, at = n % kPairs;
+        if (left_s > 0 && (pair > 0 || mbar_test(&s_empty[gs & 1], ((gs >> 1) & 1) ^ 1)) &&
+            mbar_test(&kv_full[at], (n / kPairs) & 1)) {
+          fence_proxy_async();  // the copies were written through the generic proxy
+          tc_fence_after();
+          const uint32_t d = tmem + kSCol + (gs & 1) * kTileKeys;
+          const uint64_t a = q_desc + (uint64_t)(pair * (kPairBytes >> 4));
+          const uint64_t b = k_desc + (uint64_t)(at * (kPairBytes >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint64_t o = (uint64_t)((kk >> 2) * (kChunkBytes >> 4) + (kk & 3) * 2);
-              umma_bf16_ss(d, a + o, b + o, idesc_s, (j | kk) != 0 ? 1u : 0u);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t o = (uint64_t)((kk >> 2) * (kChunkBytes >> 4) + (kk & 3) * 2);
+            umma_bf16_ss(d, a + o, b + o, idesc_s, (pair | kk) != 0 ? 1u : 0u);
+          }
+          if (++pair == kPairsPerTile) {
+            umma_commit(&s_full[gs & 1]);
+            pair = 0;
+            ++gs;
+            if (--left_s == 0) {
+              umma_commit(&q_empty);
+              ++item_s;
             }
           }
-          if (!ok) break;
-          umma_commit(&s_full[g & 1]);
-          if (tile == end - 1) umma_commit(&q_empty);
-          if (have && !(ok = second())) break;
-          have = true;
-          first_prev = tile == begin;
-          last_prev = tile == end - 1;
-          n_prev = n;
-          n += kPairsPerTile;
-          ++g;
+          progress = true;
+        }
+        if (progress) {
+          idle = 0;
+        } else if ((++idle & 63) == 0) {  // a bounded wait: mbar_wait's limit
+          if (idle == 64) t0 = globaltimer();
+          if (*abort) break;
+          if (globaltimer() - t0 > FM_WAIT_LIMIT_NS) {
+            *abort = 1;
+            atomicOr(status, FM_DEV_TIMEOUT);
+            break;
+          }
         }
       }
-      if (ok && have && !*abort) second();
       umma_commit(&drain);
       mbar_wait_drain(&drain, 0);
     }
@@ -518,13 +531,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           tc_fence_after();
           tmem_ld_16x256b_x8(tmem + ((uint32_t)(quad * 32) << 16) + kSCol + (g & 1) * kTileKeys, raw);
-          const uint64_t mask = key_mask[g & 3];
+          const uint32_t mask[2] = {key_mask[g & 3][0], key_mask[g & 3][1]};
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_empty[g & 1]);
-          if (mask != ~0ull) {
-            const uint32_t lo = (uint32_t)(mask >> (2 * (lane & 3))), hi = (uint32_t)(mask >> (32 + 2 * (lane & 3)));
+          if ((mask[0] & mask[1]) != 0xffffffffu) {
+            const uint32_t lo = mask[0] >> (2 * (lane & 3)), hi = mask[1] >> (2 * (lane & 3));
 #pragma unroll
             for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -606,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = r0 + 8 * r;
             *reinterpret_cast<uint32_t*>(dst + row * 128 + ((j ^ (row & 7)) << 4)) = w[2 * j + r];
           }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        fence_proxy_async();
         mbar_arrive(&p_full[g & 1]);
       }
       if (left) break;
@@ -676,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
 // Joins the splits of one (token, head): out = sum_s 2^(m_s - M) O_s / (sum_s
@@ -722,8 +735,7 @@ size_t attn_workspace_bytes(int T, int n_h) {
   return (size_t)parts * kHeadsPerItem * (kWidth * sizeof(float) + sizeof(float2));
 }
 
-fm_status launch_attn(AttnParams& p, const uint16_t* q, const uint16_t* kv_pool, const uint16_t* cell_pool, int64_t Pc,
-                      int sms, void* workspace, cudaStream_t stream) {
+fm_status launch_attn(AttnParams& p, const uint16_t* q, int sms, void* workspace, cudaStream_t stream) {
   p.head_blocks = head_blocks_of(p.n_h);
   const int64_t items = (int64_t)p.T * p.head_blocks;
   if (items * kMaxParts >= (int64_t(1) << 31))
@@ -742,25 +754,16 @@ fm_status launch_attn(AttnParams& p, const uint16_t* q, const uint16_t* kv_pool,
   p.part_ml = static_cast<float2*>(workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + parts * kHeadsPerItem * sizeof(float2));
 
-  CUtensorMap tq, tkv, tc;
+  CUtensorMap tq;
   const uint64_t qd[3] = {(uint64_t)kWidth, (uint64_t)p.n_h, (uint64_t)p.T};
   const uint64_t qs[2] = {(uint64_t)kWidth * 2, (uint64_t)kWidth * 2 * p.n_h};
   const uint32_t qb[3] = {64, kHeadsPerItem, 1};
   fm_status st = make_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != FM_OK) return st;
-  // a gather reads single rows of the pools; an empty pool gets a map that no row is read through
-  auto pool_map = [&](CUtensorMap* map, const uint16_t* pool, int64_t pages, int64_t page_rows) {
-    const uint64_t d[2] = {(uint64_t)kWidth, pages > 0 ? (uint64_t)((pages - 1) * page_rows + kPage) : 1};
-    const uint64_t s[1] = {(uint64_t)kWidth * 2};
-    const uint32_t b[2] = {64, 1};
-    return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pages > 0 ? pool : q, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
-  };
-  if ((st = pool_map(&tkv, kv_pool, p.P, p.kv_page_rows)) != FM_OK) return st;
-  if ((st = pool_map(&tc, cell_pool, p.k > 0 ? Pc : 0, p.cell_page_rows)) != FM_OK) return st;
   cudaError_t e = cudaFuncSetAttribute(csa_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return set_error(FM_ERR_CUDA, "fm_csa_attn: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   const int grid = p.items < sms ? p.items : sms;
-  csa_attn_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tq, tkv, tc, p);
+  csa_attn_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tq, p);
   if ((e = cudaGetLastError()) != cudaSuccess)
     return set_error(FM_ERR_CUDA, "fm_csa_attn: launch: %s", cudaGetErrorString(e));
   if (p.splits > 1) {
@@ -815,6 +818,8 @@ fm_status csa_attn(const char* who, bool tree, const uint16_t* q, int T, int n_h
   if (st != FM_OK) return st;
   AttnParams p = {};
   if ((st = status_word(&p.status)) != FM_OK) return st;
+  p.kv_pool = kv_pool;
+  p.cell_pool = cell_pool;
   p.page_table = page_table;
   p.seq = seq;
   p.pos = pos;
@@ -837,7 +842,7 @@ fm_status csa_attn(const char* who, bool tree, const uint16_t* q, int T, int n_h
   p.n_sink = n_sink;
   p.tree_words = tree_words;
   p.scale = scale;
-  return launch_attn(p, q, kv_pool, cell_pool, Pc, sms, workspace, stream);
+  return launch_attn(p, q, sms, workspace, stream);
 }
 
 }  // namespace
