@@ -8,20 +8,19 @@
 // unit of work is one token's block of 64 heads against tiles of 64 keys
 // (131 kFLOP per key of 1 KB).  A persistent CTA per SM walks its items (token,
 // head block, split of the keys):
-//   scheduler   (warp 1)  each item's key ranges, into a ring of four, and its
-//               64 query rows by TMA: eight SWIZZLE_128B chunks [64 heads x 64
-//               elements] of 8 KB
-//   producers   (warps 2, 3)  each tile's 64 pool rows by 16-byte cp.async, a
-//               lane per key for the row's address and 16 lanes per row for its
-//               copies, swizzled as TMA would.  The ring holds nine pairs of
-//               chunks [64 keys x 64 elements], four pairs to a tile; a key
-//               that is none is filled with zeros without a read, and is a zero
-//               bit of the tile's mask
-//   MMA issuer  (warp 0)  S = Q C^T: tcgen05 M64 N64, 32 steps of K16;
-//               O^T += C^T P^T: M128 N64, four blocks of 128 elements x four
-//               steps of K16, whichever has its operands first.  The cell tile
-//               is read twice from shared memory, K-major as keys and MN-major
-//               as values, and loaded once
+//   resolver    (warp 1)  each item's key ranges, and each tile's 64 pool rows
+//               and mask (a key that is none is row -1 and a zero bit)
+//   q loader    (warp 3)  the item's 64 query rows by TMA: eight SWIZZLE_128B
+//               chunks [64 heads x 64 elements] of 8 KB
+//   producers   (warps 12-15)  the rows by 16-byte cp.async, 16 keys to a warp,
+//               swizzled as TMA would (a TMA gather of four rows costs its warp
+//               some 90 cycles to issue, 128 of them a tile).  The ring holds
+//               nine pairs of chunks [64 keys x 64 elements], four pairs to a
+//               tile; a key that is none is filled with zeros without a read
+//   S issuer    (warp 0)  S = Q C^T: tcgen05 M64 N64, 32 steps of K16
+//   O issuer    (warp 2)  O^T += C^T P^T: M128 N64, four blocks of 128 elements x
+//               four steps of K16.  The cell tile is read twice from shared
+//               memory, K-major as keys and MN-major as values, and loaded once
 //   softmax     (warps 4-7)  S from TMEM, the running maximum and sum, P in
 //               bf16 to shared memory
 //   epilogue    (warps 8-11)  O^T from TMEM, times 1 / (sum + sink), to out
@@ -53,12 +52,14 @@ constexpr int kPairs = 9;
 constexpr int kQBytes = kHeadsPerItem * kWidth * 2;
 constexpr int kPBytes = kHeadsPerItem * kTileKeys * 2;
 constexpr int kSmemBytes = 1024 + kQBytes + kPairs * kPairBytes + 2 * kPBytes;
-constexpr int kThreads = 384;
+constexpr int kThreads = 16 * 32;
+constexpr int kProducerWarps = 4;
+constexpr int kKeysPerProducer = kTileKeys / kProducerWarps;
 constexpr int kTmemCols = 512;                  // allocations are powers of two
 constexpr int kSCol = 256;                      // the S buffers behind O^T's 256 columns
 constexpr int kInfoSlots = 4;
-constexpr int kInfoReaders = 2 + 1 + 4 + 4;     // producers, issuer, softmax and epilogue warps
-constexpr int kKvArrivals = 64 + 2;             // the producers' copies, and their first lanes
+constexpr int kInfoReaders = 1 + 2 + 4 + 4;                   // q loader, issuers, softmax and epilogue warps
+constexpr int kKvArrivals = 33 * kProducerWarps;              // the producers' copies, and their first lanes
 constexpr int kMaxParts = 256;                  // partial results of one call
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -122,33 +123,16 @@ FM_DEV TokenKeys token_keys(const AttnParams& p, int64_t t) {
   return r;
 }
 
-// Pool row of a cached token, or -1.
-FM_DEV int token_row(const AttnParams& p, int b, int64_t slot) {
-  const int64_t pg = slot / kPage;
-  if (pg >= p.R) {
-    atomicOr(p.status, FM_DEV_PAGE_RANGE);
-    return -1;
-  }
-  const int page = __ldg(p.page_table + (int64_t)b * p.R + pg);
-  if (page >= p.P) {
-    atomicOr(p.status, FM_DEV_PAGE_RANGE);
-    return -1;
-  }
-  return page < 0 ? -1 : (int)(page * p.kv_page_rows + slot % kPage);
-}
-
-// What the roles know of one item.  Its key slots are the four ranges in order.
+// What the roles know of one item.
 struct ItemInfo {
-  int64_t low, base;
-  int t, head_block, part;                 // part: index of the partial result, -1 = whole
-  int tile_begin, tile_end;                // at least one tile
-  int b;
-  int end_cells, end_first, end_win, end;  // ends of the ranges, in slots
+  int t, head_block;
+  int part;   // index of the partial result, -1 = whole
+  int tiles;  // at least one
 };
 
-// 16 bytes global -> shared, or 16 zero bytes where there is nothing to read.
-FM_DEV void cp_async16(uint32_t dst, const void* src, bool read) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16u : 0u) : "memory");
+// 16 bytes global -> shared, or 16 zero bytes where `bytes` is 0: nothing is read then.
+FM_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // Arrive on `bar` when this thread's copies so far have landed.
 FM_DEV void cp_async_arrive(uint64_t* bar) {
@@ -177,6 +161,25 @@ FM_DEV void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+
+// The same of 32 columns.
+FM_DEV void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit elements: thread i holds row i / 4,
+// columns 2 (i % 4) + {0, 1} of it, before and after.
+FM_DEV uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // Descriptor of an MN-major SWIZZLE_128B operand: 64 elements of M or N to a
@@ -218,27 +221,26 @@ FM_DEV uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Whether the phase with the given parity is complete, without a wait.
-FM_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Lane 0 waits, every lane learns the result.
+// A warp's wait: lane 0 polls, every lane learns the result.
 FM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   int ok = 1;
   if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort, status) ? 1 : 0;
   ok = __shfl_sync(0xffffffffu, ok, 0);
-  // the other lanes' own view of the phase (it is complete: no wait)
-  if (ok) (void)mbar_try_wait(bar, parity);
+  __syncwarp();
   return ok != 0;
+}
+
+// The issuers' warps run as a whole and elect the lane that issues, so that the
+// operands of an MMA stay uniform values.
+FM_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 x;\n\t"
+      "elect.sync x|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -251,11 +253,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   __shared__ __align__(8) uint64_t kv_full[kPairs], kv_empty[kPairs];
   __shared__ __align__(8) uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
-  __shared__ __align__(8) uint64_t q_full, q_empty, o_full, o_empty, stat_full[2], stat_empty[2];
-  __shared__ __align__(8) uint64_t info_full[kInfoSlots], info_empty[kInfoSlots], drain;
-  __shared__ __align__(8) uint32_t key_mask[4][2];
+  __shared__ __align__(8) uint64_t q_full, q_empty, o_full, o_empty[4], stat_full[2], stat_empty[2];
+  __shared__ __align__(8) uint64_t info_full[kInfoSlots], info_empty[kInfoSlots], rows_full[2], rows_empty[2], drain[2];
+  __shared__ __align__(16) int rows[2][kTileKeys];  // key 16 w + 2 c + x at 16 w + 8 x + c
+  __shared__ int rows_cells[2];                     // how many of them are cells
+  __shared__ uint2 key_mask[8];                     // the resolver is up to four tiles ahead of the softmax
   __shared__ ItemInfo info[kInfoSlots];
-  __shared__ float factor[2][kHeadsPerItem], rescale[kHeadsPerItem];
+  __shared__ __align__(8) float factor[2][kHeadsPerItem];
+  __shared__ float rescale[kHeadsPerItem];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
 
@@ -269,22 +274,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
+      mbar_init(&s_full[i], 2);
       mbar_init(&s_empty[i], 4);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&stat_full[i], 128);
+      mbar_init(&stat_full[i], 4);
       mbar_init(&stat_empty[i], 4);
     }
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
     mbar_init(&o_full, 1);
-    mbar_init(&o_empty, 4);
+    for (int i = 0; i < 4; ++i) mbar_init(&o_empty[i], 4);
     for (int i = 0; i < kInfoSlots; ++i) {
       mbar_init(&info_full[i], 1);
       mbar_init(&info_empty[i], kInfoReaders);
     }
-    mbar_init(&drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&rows_full[i], 1);
+      mbar_init(&rows_empty[i], kProducerWarps);
+    }
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -300,13 +310,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_mine = (p.items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
 
   if (warp == 1) {
-    // ------------------------- scheduler, q loader --------------------------
-    int loaded = 0;
-    for (int i = 0; i < n_mine; ++i) {
+    // -------------------------------- resolver ------------------------------
+    bool ok = true;
+    uint32_t g = 0;
+    for (int i = 0; i < n_mine && ok; ++i) {
       const int slot = i % kInfoSlots;
       const int item = (int)blockIdx.x + i * (int)gridDim.x;
       const int split = item % p.splits, th = item / p.splits;
-      const int t = th / p.head_blocks, head_block = th % p.head_blocks;
+      const int t = th / p.head_blocks;
       // listed cells up to the last one that is not empty
       int last = -1;
       const int32_t* cells = p.cells + (int64_t)t * p.k;
@@ -314,192 +325,227 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = lane; c < p.k; c += 32)
         if (__ldg(cells + c) >= 0) last = c;
       const int n_cells = __reduce_max_sync(0xffffffffu, last) + 1;
+      const TokenKeys tk = token_keys(p, t);
+      const int end_first = n_cells + tk.n_first, end_win = end_first + tk.n_win, end = end_win + tk.n_tree;
+      const int64_t tiles = (end + kTileKeys - 1) / kTileKeys;
+      int tile = (int)(tiles * split / p.splits), tile_end = (int)(tiles * (split + 1) / p.splits);
+      if (tile == tile_end) {  // a split without keys still runs one tile, of no keys
+        tile = (int)tiles;
+        tile_end = tile + 1;
+      }
       if (!warp_wait(&info_empty[slot], ((i / kInfoSlots) & 1) ^ 1, abort, status)) break;
       if (lane == 0) {
-        const TokenKeys tk = token_keys(p, t);
-        ItemInfo f;
-        f.low = tk.low;
-        f.base = tk.base;
-        f.t = t;
-        f.head_block = head_block;
-        f.part = p.splits > 1 ? item : -1;
-        f.b = tk.b;
-        f.end_cells = n_cells;
-        f.end_first = f.end_cells + tk.n_first;
-        f.end_win = f.end_first + tk.n_win;
-        f.end = f.end_win + tk.n_tree;
-        const int64_t tiles = (f.end + kTileKeys - 1) / kTileKeys;
-        f.tile_begin = (int)(tiles * split / p.splits);
-        f.tile_end = (int)(tiles * (split + 1) / p.splits);
-        // a split without keys still runs one tile, of no keys
-        if (f.tile_end == f.tile_begin) {
-          f.tile_begin = (int)tiles;
-          f.tile_end = (int)tiles + 1;
-        }
-        info[slot] = f;
+        info[slot] = ItemInfo{t, th % p.head_blocks, p.splits > 1 ? item : -1, tile_end - tile};
         mbar_arrive(&info_full[slot]);
       }
+      // The keys' indexes are read a tile ahead of their use.  Lane l resolves
+      // keys l and l + 32: `raw` is a cell, or a page with `offset` in it, or -1.
+      int raw[2], offset[2];
+      auto fetch = [&](int at_tile) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int s = at_tile * kTileKeys + 32 * x + lane;
+          raw[x] = -1;
+          offset[x] = 0;
+          if (s < n_cells) {
+            raw[x] = __ldg(cells + s);
+          } else if (s < end) {
+            int64_t at = s - n_cells;
+            bool seen = true;
+            if (s >= end_win) {
+              const int d = s - end_win;
+              seen = (__ldg(p.tree_mask + (int64_t)t * p.tree_words + (d >> 5)) >> (d & 31)) & 1u;
+              at = tk.base + d;
+            } else if (s >= end_first) {
+              at = tk.low + (s - end_first);
+            }
+            if (seen && at >= (int64_t)p.R * kPage) {
+              atomicOr(status, FM_DEV_PAGE_RANGE);
+            } else if (seen) {
+              raw[x] = __ldg(p.page_table + (int64_t)tk.b * p.R + at / kPage);
+              offset[x] = (int)(at % kPage);
+            }
+          }
+        }
+      };
+      fetch(tile);
+      for (; tile < tile_end; ++tile, ++g) {
+        int row[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const bool cell = tile * kTileKeys + 32 * x + lane < n_cells;
+          row[x] = -1;
+          if (raw[x] >= 0) {
+            if (raw[x] >= (cell ? p.cell_limit : p.P))
+              atomicOr(status, FM_DEV_PAGE_RANGE);
+            else
+              row[x] = cell ? (raw[x] / kPage) * (int)p.cell_page_rows + raw[x] % kPage
+                            : raw[x] * (int)p.kv_page_rows + offset[x];
+          }
+        }
+        uint2 mask;
+        mask.x = __ballot_sync(0xffffffffu, row[0] >= 0);
+        mask.y = __ballot_sync(0xffffffffu, row[1] >= 0);
+        if (tile + 1 < tile_end) fetch(tile + 1);
+        if (!(ok = warp_wait(&rows_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
+        const int to = (lane >> 4) * 16 + (lane & 1) * 8 + ((lane & 15) >> 1);
+        rows[g & 1][to] = row[0];
+        rows[g & 1][32 + to] = row[1];
+        if (lane == 0) {
+          key_mask[g & 7] = mask;
+          const int left = n_cells - tile * kTileKeys;
+          rows_cells[g & 1] = left < 0 ? 0 : left;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rows_full[g & 1]);
+      }
+    }
+  } else if (warp == 3) {
+    // ------------------------------- q loader -------------------------------
+    int loaded = 0;
+    for (int i = 0; i < n_mine; ++i) {
+      const int slot = i % kInfoSlots;
+      if (!warp_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
+      const int t = info[slot].t, h0 = info[slot].head_block * kHeadsPerItem;
       __syncwarp();
+      if (lane == 0) mbar_arrive(&info_empty[slot]);
       if (!warp_wait(&q_empty, (i & 1) ^ 1, abort, status)) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&q_full, kQBytes);
-        for (int c = 0; c < kWidth / 64; ++c)
-          tma_load_3d(q_smem + c * kChunkBytes, &tmap_q, &q_full, 64 * c, head_block * kHeadsPerItem, t);
+        for (int c = 0; c < kWidth / 64; ++c) tma_load_3d(q_smem + c * kChunkBytes, &tmap_q, &q_full, 64 * c, h0, t);
       }
       __syncwarp();
       loaded = i + 1;
     }
     if (lane == 0 && loaded > 0 && *abort) mbar_wait_drain(&q_full, (loaded - 1) & 1);
-  } else if (warp == 2 || warp == 3) {
+  } else if (warp >= 12) {
     // ------------------------------- producers ------------------------------
-    // Warp w takes the tile's keys 32 w .. 32 w + 31.  Copy i of a pair moves the
-    // rows of keys 2 i and 2 i + 1: lane l < 16 the 16-byte units l of the
+    // Producer w takes the tile's keys 16 w .. 16 w + 15.  Copy c of a pair moves
+    // the rows of keys 2 c and 2 c + 1: lane l < 16 the 16-byte unit l of the
     // first, the others those of the second.
-    const int half = warp - 2, hi = lane >> 4, unit = lane & 15;
-    const uint32_t lane_dst = smem_u32(ring) + half * 32 * 128 + (unit >> 3) * kChunkBytes + hi * 128 +
+    const int me = warp - 12, hi = lane >> 4, unit = lane & 15;
+    const uint32_t lane_dst = smem_u32(ring) + me * kKeysPerProducer * 128 + (unit >> 3) * kChunkBytes + hi * 128 +
                               (((unit & 7) ^ hi) << 4);
-    uint32_t n = 0, g = 0;  // pairs and tiles issued so far
+    uint32_t at = 0, at_phase = 1, g = 0;
     bool ok = true;
     for (int i = 0; i < n_mine && ok; ++i) {
-      const int slot = i % kInfoSlots;
-      if (!warp_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
-      const ItemInfo f = info[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&info_empty[slot]);
-      for (int tile = f.tile_begin; tile < f.tile_end && ok; ++tile, ++g) {
-        // this lane's key: its row's address, or 0
-        const int s = tile * kTileKeys + half * 32 + lane;
-        uint64_t row = 0;
-        if (s < f.end_cells) {
-          const int64_t cell = __ldg(p.cells + (int64_t)f.t * p.k + s);
-          if (cell >= p.cell_limit)
-            atomicOr(status, FM_DEV_PAGE_RANGE);
-          else if (cell >= 0)
-            row = reinterpret_cast<uint64_t>(p.cell_pool + ((cell / kPage) * p.cell_page_rows + cell % kPage) * kWidth);
-        } else if (s < f.end) {
-          int64_t at = s - f.end_cells;
-          if (s >= f.end_win) {
-            const int d = s - f.end_win;
-            at = (__ldg(p.tree_mask + (int64_t)f.t * p.tree_words + (d >> 5)) >> (d & 31)) & 1u ? f.base + d : -1;
-          } else if (s >= f.end_first) {
-            at = f.low + (s - f.end_first);
-          }
-          const int64_t r = at >= 0 ? token_row(p, f.b, at) : -1;
-          if (r >= 0) row = reinterpret_cast<uint64_t>(p.kv_pool + r * kWidth);
-        }
-        const uint32_t mask = __ballot_sync(0xffffffffu, row != 0);
-        if (lane == 0) key_mask[g & 3][half] = mask;
-        uint64_t src[16];
+      int tiles = 1;  // learned from the item's first tile: its rows come after its info
+      for (int tile = 0; tile < tiles; ++tile, ++g) {
+        if (!(ok = warp_wait(&rows_full[g & 1], (g >> 1) & 1, abort, status))) break;
+        if (tile == 0) tiles = info[i % kInfoSlots].tiles;
+        const int4 r0 = *reinterpret_cast<const int4*>(&rows[g & 1][me * 16 + hi * 8]);
+        const int4 r1 = *reinterpret_cast<const int4*>(&rows[g & 1][me * 16 + hi * 8 + 4]);
+        const int cells = rows_cells[g & 1] - me * 16 - hi;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rows_empty[g & 1]);
+        const int row[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+        const uint8_t* src[8];
+        uint32_t bytes[8];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) src[c] = __shfl_sync(0xffffffffu, row, 2 * c + hi);
+        for (int c = 0; c < 8; ++c) {
+          const uint16_t* base = 2 * c < cells ? p.cell_pool : p.kv_pool;
+          bytes[c] = row[c] >= 0 ? 16u : 0u;
+          if (row[c] < 0) base = reinterpret_cast<const uint16_t*>(p.pos);  // any address: nothing is read
+          src[c] = reinterpret_cast<const uint8_t*>(base + (int64_t)(row[c] < 0 ? 0 : row[c]) * kWidth) + unit * 16;
+        }
+#pragma unroll
         for (int j = 0; j < kPairsPerTile; ++j) {
-          const uint32_t at = n % kPairs;
-          if (!warp_wait(&kv_empty[at], ((n / kPairs) & 1) ^ 1, abort, status)) {
-            ok = false;
-            break;
-          }
+          if (!(ok = warp_wait(&kv_empty[at], at_phase, abort, status))) break;
           const uint32_t dst = lane_dst + at * kPairBytes;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const bool read = src[c] != 0;
-            const uint8_t* from = read ? reinterpret_cast<const uint8_t*>(src[c]) + j * 256 + unit * 16
-                                       : reinterpret_cast<const uint8_t*>(p.pos);  // any address: nothing is read
-            cp_async16((dst ^ ((2 * c & 7) << 4)) + c * 256, from, read);
-          }
+          for (int c = 0; c < 8; ++c) cp_async16((dst ^ ((2 * c & 7) << 4)) + c * 256, src[c] + j * 256, bytes[c]);
           cp_async_arrive(&kv_full[at]);
           if (lane == 0) mbar_arrive(&kv_full[at]);  // releases the mask
-          ++n;
+          if (++at == (uint32_t)kPairs) {
+            at = 0;
+            at_phase ^= 1;
+          }
         }
+        if (!ok) break;
       }
     }
     cp_async_wait_all();
   } else if (warp == 0) {
-    // ------------------------------ MMA issuer ------------------------------
-    if (lane == 0) {
-      const uint32_t idesc_s = idesc_bf16_f32(64, kTileKeys);
-      const uint32_t idesc_o = idesc_bf16_f32(128, kHeadsPerItem) | kAIsMnMajor;
-      const uint64_t q_desc = sdesc_sw128(smem_u32(q_smem));
-      const uint64_t k_desc = sdesc_sw128(smem_u32(ring));
-      const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring));
-      const uint64_t p_desc = sdesc_sw128(smem_u32(p_smem));
-      // The next steps are pair `pair` of tile gs's S and all of tile gv's O;
-      // tiles are numbered over all of the CTA's items.
-      uint32_t gs = 0, gv = 0, pair = 0, idle = 0;
-      int item_s = 0, item_v = 0;          // items that the two tiles belong to
-      int left_s = 0, left_v = 0;          // their tiles not yet done (0: not looked up)
-      bool first_v = true;
-      uint64_t t0 = 0;
-      while (item_v < n_mine) {
-        bool progress = false;
-        // O^T += C^T P^T; each pair of chunks is a block of 128 elements
-        if (gv < gs && mbar_test(&p_full[gv & 1], (gv >> 1) & 1) && (!first_v || mbar_test(&o_empty, (item_v & 1) ^ 1))) {
-          const ItemInfo& f = info[item_v % kInfoSlots];
-          if (first_v) left_v = f.tile_end - f.tile_begin;
-          tc_fence_after();
-          const uint64_t b = p_desc + (uint64_t)((gv & 1) * (kPBytes >> 4));
-          for (int m = 0; m < kPairsPerTile; ++m) {
-            const uint32_t at = (gv * kPairsPerTile + m) % kPairs;
-            const uint64_t a = v_desc + (uint64_t)(at * (kPairBytes >> 4));
-#pragma unroll
-            for (int kk = 0; kk < kTileKeys / 16; ++kk)
-              umma_bf16_ss(tmem + m * kHeadsPerItem, a + kk * (2048 >> 4), b + kk * 2, idesc_o,
-                           first_v && kk == 0 ? 0u : 1u);
-            umma_commit(&kv_empty[at]);
-          }
-          umma_commit(&pv_done[gv & 1]);
-          ++gv;
-          first_v = false;
-          if (--left_v == 0) {
-            umma_commit(&o_full);
-            mbar_arrive(&info_empty[item_v % kInfoSlots]);
-            ++item_v;
-            first_v = true;
-          }
-          progress = true;
-        }
-        if (left_s == 0 && item_s < n_mine && mbar_test(&info_full[item_s % kInfoSlots], (item_s / kInfoSlots) & 1) &&
-            mbar_test(&q_full, item_s & 1)) {
-          left_s = info[item_s % kInfoSlots].tile_end - info[item_s % kInfoSlots].tile_begin;
-        }
-        const uint32_t n = gs * kPairsPerTile + pair, at = n % kPairs;
-        if (left_s > 0 && (pair > 0 || mbar_test(&s_empty[gs & 1], ((gs >> 1) & 1) ^ 1)) &&
-            mbar_test(&kv_full[at], (n / kPairs) & 1)) {
+    // ------------------------------- S issuer -------------------------------
+    const bool one = elect_one();
+    const uint32_t idesc = idesc_bf16_f32(64, kTileKeys);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(q_smem));
+    const uint64_t k_desc = sdesc_sw128(smem_u32(ring));
+    uint32_t g = 0, at = 0, at_phase = 0;
+    bool ok = true;
+    for (int i = 0; i < n_mine && ok; ++i) {
+      const int slot = i % kInfoSlots;
+      if (!warp_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
+      const int tiles = info[slot].tiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&info_empty[slot]);
+      if (!warp_wait(&q_full, i & 1, abort, status)) break;
+      for (int tile = 0; tile < tiles && ok; ++tile, ++g) {
+        if (!(ok = warp_wait(&s_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
+        const uint32_t d = tmem + kSCol + (g & 1) * kTileKeys;
+        for (int j = 0; j < kPairsPerTile; ++j) {
+          if (!(ok = warp_wait(&kv_full[at], at_phase, abort, status))) break;
           fence_proxy_async();  // the copies were written through the generic proxy
           tc_fence_after();
-          const uint32_t d = tmem + kSCol + (gs & 1) * kTileKeys;
-          const uint64_t a = q_desc + (uint64_t)(pair * (kPairBytes >> 4));
+          const uint64_t a = q_desc + (uint64_t)(j * (kPairBytes >> 4));
           const uint64_t b = k_desc + (uint64_t)(at * (kPairBytes >> 4));
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint64_t o = (uint64_t)((kk >> 2) * (kChunkBytes >> 4) + (kk & 3) * 2);
-            umma_bf16_ss(d, a + o, b + o, idesc_s, (pair | kk) != 0 ? 1u : 0u);
+            if (one) umma_bf16_ss(d, a + o, b + o, idesc, kk == 0 ? (uint32_t)j : 1u);
           }
-          if (++pair == kPairsPerTile) {
-            umma_commit(&s_full[gs & 1]);
-            pair = 0;
-            ++gs;
-            if (--left_s == 0) {
-              umma_commit(&q_empty);
-              ++item_s;
-            }
+          if (++at == (uint32_t)kPairs) {
+            at = 0;
+            at_phase ^= 1;
           }
-          progress = true;
         }
-        if (progress) {
-          idle = 0;
-        } else if ((++idle & 63) == 0) {  // a bounded wait: mbar_wait's limit
-          if (idle == 64) t0 = globaltimer();
-          if (*abort) break;
-          if (globaltimer() - t0 > FM_WAIT_LIMIT_NS) {
-            *abort = 1;
-            atomicOr(status, FM_DEV_TIMEOUT);
-            break;
-          }
+        if (!ok) break;
+        if (one) {
+          umma_commit(&s_full[g & 1]);
+          mbar_arrive(&s_full[g & 1]);  // passes the mask on
         }
       }
-      umma_commit(&drain);
-      mbar_wait_drain(&drain, 0);
+      if (ok && one) umma_commit(&q_empty);
     }
+    if (one) umma_commit(&drain[0]);
+    if (one) mbar_wait_drain(&drain[0], 0);
+  } else if (warp == 2) {
+    // ------------------------------- O issuer -------------------------------
+    const bool one = elect_one();
+    const uint32_t idesc = idesc_bf16_f32(128, kHeadsPerItem) | kAIsMnMajor;
+    const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring));
+    const uint64_t p_desc = sdesc_sw128(smem_u32(p_smem));
+    uint32_t g = 0, at = 0;
+    bool ok = true;
+    for (int i = 0; i < n_mine && ok; ++i) {
+      const int slot = i % kInfoSlots;
+      if (!warp_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
+      const int tiles = info[slot].tiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&info_empty[slot]);
+      for (int tile = 0; tile < tiles && ok; ++tile, ++g) {
+        if (!(ok = warp_wait(&p_full[g & 1], (g >> 1) & 1, abort, status))) break;
+        tc_fence_after();
+        const uint64_t b = p_desc + (uint64_t)((g & 1) * (kPBytes >> 4));
+        for (int m = 0; m < kPairsPerTile; ++m) {  // a pair of chunks is a block of 128 elements
+          if (tile == 0) {  // the block of the last item has been read
+            if (!(ok = warp_wait(&o_empty[m], (i & 1) ^ 1, abort, status))) break;
+            tc_fence_after();
+          }
+          const uint64_t a = v_desc + (uint64_t)(at * (kPairBytes >> 4));
+#pragma unroll
+          for (int kk = 0; kk < kTileKeys / 16; ++kk)
+            if (one) umma_bf16_ss(tmem + m * kHeadsPerItem, a + kk * (2048 >> 4), b + kk * 2, idesc, kk == 0 ? (uint32_t)tile : 1u);
+          if (one) umma_commit(&kv_empty[at]);
+          if (++at == (uint32_t)kPairs) at = 0;
+        }
+        if (!ok) break;
+        if (one) umma_commit(&pv_done[g & 1]);
+      }
+      if (ok && one) umma_commit(&o_full);
+    }
+    if (one) umma_commit(&drain[1]);
+    if (one) mbar_wait_drain(&drain[1], 0);
   } else if (warp < 8) {
     // ------------------------------- softmax --------------------------------
     // Warp quad w holds heads 16 w .. 16 w + 15 of the block (S's rows in the
@@ -508,36 +554,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3;
     const int r0 = quad * 16 + lane / 4;
     const float c = p.scale * kLog2e;
-    uint32_t g = 0, n = 0;
+    uint32_t g = 0;
     bool dead = false;
     for (int i = 0; i < n_mine; ++i) {
       const int slot = i % kInfoSlots;
-      bool ok = !dead && mbar_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status);
+      bool ok = !dead && warp_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status);
       if (softmax_any(!ok)) break;
-      const int tiles = info[slot].tile_end - info[slot].tile_begin;
+      const int tiles = info[slot].tiles;
       const int t = info[slot].t, h0 = info[slot].head_block * kHeadsPerItem, part = info[slot].part;
       __syncwarp();
       if (lane == 0) mbar_arrive(&info_empty[slot]);
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // m in units of S, l of this thread's keys
       bool left = false;
-      for (int tile = 0; tile < tiles; ++tile, ++g, n += kPairsPerTile) {
-        // the tile's mask came with its first pair of chunks, whose barrier is complete
-        ok = !dead && mbar_wait(&s_full[g & 1], (g >> 1) & 1, abort, status) &&
-             mbar_wait(&kv_full[n % kPairs], (n / kPairs) & 1, abort, status);
-        ok = __all_sync(0xffffffffu, ok);
+      for (int tile = 0; tile < tiles; ++tile, ++g) {
+        ok = !dead && warp_wait(&s_full[g & 1], (g >> 1) & 1, abort, status);
         uint32_t raw[32];
         float top[2] = {-INFINITY, -INFINITY};
         bool need = false;
         if (ok) {
           tc_fence_after();
           tmem_ld_16x256b_x8(tmem + ((uint32_t)(quad * 32) << 16) + kSCol + (g & 1) * kTileKeys, raw);
-          const uint32_t mask[2] = {key_mask[g & 3][0], key_mask[g & 3][1]};
+          const uint2 mask = key_mask[g & 7];
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_empty[g & 1]);
-          if ((mask[0] & mask[1]) != 0xffffffffu) {
-            const uint32_t lo = mask[0] >> (2 * (lane & 3)), hi = mask[1] >> (2 * (lane & 3));
+          if ((mask.x & mask.y) != 0xffffffffu) {
+            const uint32_t lo = mask.x >> (2 * (lane & 3)), hi = mask.y >> (2 * (lane & 3));
 #pragma unroll
             for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -573,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((lane & 3) == 0) rescale[r0 + 8 * r] = f;
           }
           const uint32_t gp = g - 1;
-          ok = mbar_wait(&pv_done[gp & 1], (gp >> 1) & 1, abort, status);
+          ok = warp_wait(&pv_done[gp & 1], (gp >> 1) & 1, abort, status);
           if (softmax_any(!ok)) {
             left = true;
             break;
@@ -607,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             l[r] += a + b;
             w[2 * j + r] = pack_bf16(a, b);
           }
-        if (!mbar_wait(&pv_done[g & 1], ((g >> 1) & 1) ^ 1, abort, status)) {
+        if (!warp_wait(&pv_done[g & 1], ((g >> 1) & 1) ^ 1, abort, status)) {
           dead = true;  // leave together with the others, at the next tile or item
           continue;
         }
@@ -620,10 +663,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint32_t*>(dst + row * 128 + ((j ^ (row & 7)) << 4)) = w[2 * j + r];
           }
         fence_proxy_async();
-        mbar_arrive(&p_full[g & 1]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[g & 1]);
       }
       if (left) break;
-      if (!dead && !mbar_wait(&stat_empty[i & 1], ((i >> 1) & 1) ^ 1, abort, status)) dead = true;
+      if (!dead && !warp_wait(&stat_empty[i & 1], ((i >> 1) & 1) ^ 1, abort, status)) dead = true;
       if (dead) continue;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -644,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      mbar_arrive(&stat_full[i & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&stat_full[i & 1]);
     }
   } else {
     // ------------------------------- epilogue -------------------------------
@@ -659,31 +705,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(&o_full, i & 1, abort, status)) break;
       tc_fence_after();
       const int heads = min(kHeadsPerItem, p.n_h - h0);
+      const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+      if (part >= 0) {
 #pragma unroll 1
-      for (int x = 0; x < 8; ++x) {
-        uint32_t o[32];
-        tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + 32 * x, o);
-        tmem_ld_wait();
-        const int hl0 = (x & 1) * 32, d = (x >> 1) * 128 + quad * 32 + lane;
-        if (part >= 0) {
-          float* dst = p.part_o + ((int64_t)part * kHeadsPerItem + hl0) * kWidth + d;
+        for (int x = 0; x < 8; ++x) {
+          uint32_t o[32];
+          tmem_ld32(lanes + 32 * x, o);
+          tmem_ld_wait();
+          float* dst = p.part_o + ((int64_t)part * kHeadsPerItem + (x & 1) * 32) * kWidth + (x >> 1) * 128 + quad * 32 + lane;
 #pragma unroll
           for (int h = 0; h < 32; ++h)
-            if (hl0 + h < heads) dst[h * kWidth] = __uint_as_float(o[h]);
-        } else {
-          uint16_t* dst = p.out + ((int64_t)t * p.n_h + h0 + hl0) * kWidth + d;
+            if ((x & 1) * 32 + h < heads) dst[h * kWidth] = __uint_as_float(o[h]);
+          tc_fence_before();
+          __syncwarp();
+          if ((x & 1) && lane == 0) mbar_arrive(&o_empty[x >> 1]);
+        }
+      } else {
+        // A warp has 32 elements (TMEM lanes) of every head.  Eight heads at a
+        // time: four 8 x 8 transposes give thread i head i / 4 and elements 8 e +
+        // 2 (i % 4) + {0, 1} for e < 4; a transpose among four threads gives it
+        // elements 8 (i % 4) .. + 7, 16 bytes.
+        uint16_t* dst = p.out + ((int64_t)t * p.n_h + h0 + lane / 4) * kWidth + quad * 32 + (lane & 3) * 8;
+#pragma unroll 1
+        for (int x = 0; x < 8; ++x) {
+          uint32_t a[16], b[16];
+          tmem_ld_16x256b_x4(lanes + 32 * x, a);
+          tmem_ld_16x256b_x4(lanes + (16u << 16) + 32 * x, b);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if ((x & 1) && lane == 0) mbar_arrive(&o_empty[x >> 1]);
 #pragma unroll
-          for (int h = 0; h < 32; ++h)
-            if (hl0 + h < heads)
-              dst[h * kWidth] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[h]) * factor[i & 1][hl0 + h]));
+          for (int j = 0; j < 4; ++j) {
+            const int hl = (x & 1) * 32 + 8 * j;
+            const float2 f = *reinterpret_cast<const float2*>(&factor[i & 1][hl + 2 * (lane & 3)]);
+            uint32_t e[4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              e[r] = transpose_8x8(pack_bf16(__uint_as_float(a[4 * j + 2 * r]) * f.x, __uint_as_float(a[4 * j + 2 * r + 1]) * f.y));
+              e[2 + r] = transpose_8x8(pack_bf16(__uint_as_float(b[4 * j + 2 * r]) * f.x, __uint_as_float(b[4 * j + 2 * r + 1]) * f.y));
+            }
+            // e[k] of lane q is word (k, q): after two exchanges lane q has words (q, 0..3)
+            const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+            for (int r = 0; r < 4; r += 2) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? e[r] : e[r + 1], 1);
+              if (odd)
+                e[r] = got;
+              else
+                e[r + 1] = got;
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? e[r] : e[r + 2], 2);
+              if (high)
+                e[r] = got;
+              else
+                e[r + 2] = got;
+            }
+            if (hl + lane / 4 < heads)
+              *reinterpret_cast<uint4*>(dst + (int64_t)hl * kWidth + (x >> 1) * 128) = make_uint4(e[0], e[1], e[2], e[3]);
+          }
         }
       }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&o_empty);
-        mbar_arrive(&stat_empty[i & 1]);
-      }
+      if (lane == 0) mbar_arrive(&stat_empty[i & 1]);
     }
   }
   tc_fence_before();
