@@ -12,7 +12,7 @@
 //               and mask (a key that is none is row -1 and a zero bit)
 //   q loader    (warp 3)  the item's 64 query rows by TMA: eight SWIZZLE_128B
 //               chunks [64 heads x 64 elements] of 8 KB
-//   producers   (warps 12-15)  the rows by 16-byte cp.async, 16 keys to a warp,
+//   producers   (warps 16-19)  the rows by 16-byte cp.async, 16 keys to a warp,
 //               swizzled as TMA would (a TMA gather of four rows costs its warp
 //               some 90 cycles to issue, 128 of them a tile).  The ring holds
 //               nine pairs of chunks [64 keys x 64 elements], four pairs to a
@@ -21,9 +21,9 @@
 //   O issuer    (warp 2)  O^T += C^T P^T: M128 N64, four blocks of 128 elements x
 //               four steps of K16.  The cell tile is read twice from shared
 //               memory, K-major as keys and MN-major as values, and loaded once
-//   softmax     (warps 4-7)  S from TMEM, the running maximum and sum, P in
-//               bf16 to shared memory
-//   epilogue    (warps 8-11)  O^T from TMEM, times 1 / (sum + sink), to out
+//   softmax     (warps 4-11)  S from TMEM, the running maximum and sum, P in
+//               bf16 to shared memory: 16 heads x 32 keys to a warp
+//   epilogue    (warps 12-15)  O^T from TMEM, times 1 / (sum + sink), to out
 // TMEM: O^T 4 x 64 columns, two S buffers of 64.  The output is kept transposed
 // (rows = elements) because 64 rows of heads x 512 columns would fill TMEM.
 //
@@ -51,14 +51,14 @@ constexpr int kPairsPerTile = kWidth / 128;     // 4
 constexpr int kPairs = 9;
 constexpr int kQBytes = kHeadsPerItem * kWidth * 2;
 constexpr int kPBytes = kHeadsPerItem * kTileKeys * 2;
-constexpr int kSmemBytes = 1024 + kQBytes + kPairs * kPairBytes + 2 * kPBytes;
-constexpr int kThreads = 16 * 32;
+constexpr int kThreads = 20 * 32;
+constexpr int kSoftmaxWarps = 8;
 constexpr int kProducerWarps = 4;
 constexpr int kKeysPerProducer = kTileKeys / kProducerWarps;
 constexpr int kTmemCols = 512;                  // allocations are powers of two
 constexpr int kSCol = 256;                      // the S buffers behind O^T's 256 columns
 constexpr int kInfoSlots = 4;
-constexpr int kInfoReaders = 1 + 2 + 4 + 4;                   // q loader, issuers, softmax and epilogue warps
+constexpr int kInfoReaders = 1 + 2 + kSoftmaxWarps + 4;       // q loader, issuers, softmax and epilogue warps
 constexpr int kKvArrivals = 33 * kProducerWarps;              // the producers' copies, and their first lanes
 constexpr int kMaxParts = 256;                  // partial results of one call
 constexpr float kLog2e = 1.4426950408889634f;
@@ -148,22 +148,8 @@ FM_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
       : "memory");
 }
 
-// 16 lanes x 64 columns: thread i gets, of columns 8j + 2 (i % 4) + {0, 1}, lane
+// 16 lanes x 32 columns: thread i gets, of columns 8j + 2 (i % 4) + {0, 1}, lane
 // i / 4 in r[4j], r[4j + 1] and lane i / 4 + 8 in r[4j + 2], r[4j + 3].
-FM_DEV void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
-// The same of 32 columns.
 FM_DEV void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
@@ -202,16 +188,38 @@ FM_DEV float exp2_fast(float x) {
   return y;
 }
 
-// OR of a predicate over the softmax warps' 128 threads (and a barrier for them).
+// Four 8 x 8 matrices of 16-bit elements to shared memory: x[k] is matrix k, thread
+// i holding row i / 4, columns 2 (i % 4) + {0, 1}; thread i's address is that of row
+// i % 8 of matrix i / 8.
+FM_DEV void store_8x8_x4(uint32_t addr, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x0), "r"(x1),
+               "r"(x2), "r"(x3)
+               : "memory");
+}
+
+// Whether the phase with the given parity is complete, without a wait.
+FM_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// OR of a predicate over the softmax warps' threads (and a barrier for them).
 FM_DEV bool softmax_any(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}\n"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "n"(32 * kSoftmaxWarps)
       : "memory");
   return r != 0;
 }
@@ -243,70 +251,79 @@ FM_DEV bool elect_one() {
   return r != 0;
 }
 
+// What the roles share besides the tiles.
+struct Shared {
+  uint64_t kv_full[kPairs], kv_empty[kPairs];
+  uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
+  uint64_t q_full, q_empty, o_full, o_empty[4], stat_full[2], stat_empty[2];
+  uint64_t info_full[kInfoSlots], info_empty[kInfoSlots], rows_full[2], rows_empty[2], drain[2];
+  uint2 key_mask[8];                     // the resolver is up to four tiles ahead of the softmax
+  ItemInfo info[kInfoSlots];
+  alignas(16) int rows[2][kTileKeys];                // key 16 w + 2 c + x at 16 w + 8 x + c
+  int rows_cells[2];                     // how many of them are cells
+  alignas(16) float factor[2][kHeadsPerItem];
+  float rescale[kHeadsPerItem], top_half[2][kHeadsPerItem], sum_half[kHeadsPerItem];
+  uint32_t tmem_slot;
+  int abort_flag;
+};
+constexpr int kSmemBytes = kQBytes + kPairs * kPairBytes + 2 * kPBytes + (int)sizeof(Shared);
+static_assert(kSmemBytes <= 232448, "227 KB of shared memory to a CTA");
+static_assert(offsetof(Shared, rows) % 16 == 0 && offsetof(Shared, factor) % 8 == 0, "vector accesses");
+
 __global__ void __launch_bounds__(kThreads, 1)
     csa_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ AttnParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* q_smem = smem;
   uint8_t* ring = smem + kQBytes;
   uint8_t* p_smem = ring + kPairs * kPairBytes;
-
-  __shared__ __align__(8) uint64_t kv_full[kPairs], kv_empty[kPairs];
-  __shared__ __align__(8) uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
-  __shared__ __align__(8) uint64_t q_full, q_empty, o_full, o_empty[4], stat_full[2], stat_empty[2];
-  __shared__ __align__(8) uint64_t info_full[kInfoSlots], info_empty[kInfoSlots], rows_full[2], rows_empty[2], drain[2];
-  __shared__ __align__(16) int rows[2][kTileKeys];  // key 16 w + 2 c + x at 16 w + 8 x + c
-  __shared__ int rows_cells[2];                     // how many of them are cells
-  __shared__ uint2 key_mask[8];                     // the resolver is up to four tiles ahead of the softmax
-  __shared__ ItemInfo info[kInfoSlots];
-  __shared__ __align__(8) float factor[2][kHeadsPerItem];
-  __shared__ float rescale[kHeadsPerItem];
-  __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag;
-
+  Shared& sh = *reinterpret_cast<Shared*>(p_smem + 2 * kPBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  volatile int* abort = &abort_flag;
+  volatile int* abort = &sh.abort_flag;
   unsigned int* status = p.status;
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles need 1024-byte alignment: never seen otherwise
+    if (threadIdx.x == 0) atomicOr(status, FM_DEV_TIMEOUT);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPairs; ++i) {
-      mbar_init(&kv_full[i], kKvArrivals);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&sh.kv_full[i], kKvArrivals);
+      mbar_init(&sh.kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 2);
-      mbar_init(&s_empty[i], 4);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&pv_done[i], 1);
-      mbar_init(&stat_full[i], 4);
-      mbar_init(&stat_empty[i], 4);
+      mbar_init(&sh.s_full[i], 2);
+      mbar_init(&sh.s_empty[i], kSoftmaxWarps);
+      mbar_init(&sh.p_full[i], kSoftmaxWarps);
+      mbar_init(&sh.pv_done[i], 1);
+      mbar_init(&sh.stat_full[i], 4);
+      mbar_init(&sh.stat_empty[i], 4);
     }
-    mbar_init(&q_full, 1);
-    mbar_init(&q_empty, 1);
-    mbar_init(&o_full, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&o_empty[i], 4);
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.o_full, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.o_empty[i], 4);
     for (int i = 0; i < kInfoSlots; ++i) {
-      mbar_init(&info_full[i], 1);
-      mbar_init(&info_empty[i], kInfoReaders);
+      mbar_init(&sh.info_full[i], 1);
+      mbar_init(&sh.info_empty[i], kInfoReaders);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&rows_full[i], 1);
-      mbar_init(&rows_empty[i], kProducerWarps);
+      mbar_init(&sh.rows_full[i], 1);
+      mbar_init(&sh.rows_empty[i], kProducerWarps);
     }
-    mbar_init(&drain[0], 1);
-    mbar_init(&drain[1], 1);
-    abort_flag = 0;
+    mbar_init(&sh.drain[0], 1);
+    mbar_init(&sh.drain[1], 1);
+    sh.abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1 && lane == 0) tma_prefetch(&tmap_q);
   if (warp == 0) {
-    tmem_alloc(&tmem_slot, kTmemCols);
+    tmem_alloc(&sh.tmem_slot, kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = sh.tmem_slot;
   const int n_mine = (p.items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
 
   if (warp == 1) {
@@ -333,10 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tile = (int)tiles;
         tile_end = tile + 1;
       }
-      if (!warp_wait(&info_empty[slot], ((i / kInfoSlots) & 1) ^ 1, abort, status)) break;
+      if (!warp_wait(&sh.info_empty[slot], ((i / kInfoSlots) & 1) ^ 1, abort, status)) break;
       if (lane == 0) {
-        info[slot] = ItemInfo{t, th % p.head_blocks, p.splits > 1 ? item : -1, tile_end - tile};
-        mbar_arrive(&info_full[slot]);
+        sh.info[slot] = ItemInfo{t, th % p.head_blocks, p.splits > 1 ? item : -1, tile_end - tile};
+        mbar_arrive(&sh.info_full[slot]);
       }
       // The keys' indexes are read a tile ahead of their use.  Lane l resolves
       // keys l and l + 32: `raw` is a cell, or a page with `offset` in it, or -1.
@@ -387,17 +404,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         mask.x = __ballot_sync(0xffffffffu, row[0] >= 0);
         mask.y = __ballot_sync(0xffffffffu, row[1] >= 0);
         if (tile + 1 < tile_end) fetch(tile + 1);
-        if (!(ok = warp_wait(&rows_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
+        if (!(ok = warp_wait(&sh.rows_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
         const int to = (lane >> 4) * 16 + (lane & 1) * 8 + ((lane & 15) >> 1);
-        rows[g & 1][to] = row[0];
-        rows[g & 1][32 + to] = row[1];
+        sh.rows[g & 1][to] = row[0];
+        sh.rows[g & 1][32 + to] = row[1];
         if (lane == 0) {
-          key_mask[g & 7] = mask;
+          sh.key_mask[g & 7] = mask;
           const int left = n_cells - tile * kTileKeys;
-          rows_cells[g & 1] = left < 0 ? 0 : left;
+          sh.rows_cells[g & 1] = left < 0 ? 0 : left;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&rows_full[g & 1]);
+        if (lane == 0) mbar_arrive(&sh.rows_full[g & 1]);
       }
     }
   } else if (warp == 3) {
@@ -405,25 +422,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     int loaded = 0;
     for (int i = 0; i < n_mine; ++i) {
       const int slot = i % kInfoSlots;
-      if (!warp_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
-      const int t = info[slot].t, h0 = info[slot].head_block * kHeadsPerItem;
+      if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
+      const int t = sh.info[slot].t, h0 = sh.info[slot].head_block * kHeadsPerItem;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&info_empty[slot]);
-      if (!warp_wait(&q_empty, (i & 1) ^ 1, abort, status)) break;
+      if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+      if (!warp_wait(&sh.q_empty, (i & 1) ^ 1, abort, status)) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&q_full, kQBytes);
-        for (int c = 0; c < kWidth / 64; ++c) tma_load_3d(q_smem + c * kChunkBytes, &tmap_q, &q_full, 64 * c, h0, t);
+        mbar_arrive_expect_tx(&sh.q_full, kQBytes);
+        for (int c = 0; c < kWidth / 64; ++c) tma_load_3d(q_smem + c * kChunkBytes, &tmap_q, &sh.q_full, 64 * c, h0, t);
       }
       __syncwarp();
       loaded = i + 1;
     }
-    if (lane == 0 && loaded > 0 && *abort) mbar_wait_drain(&q_full, (loaded - 1) & 1);
-  } else if (warp >= 12) {
+    if (lane == 0 && loaded > 0 && *abort) mbar_wait_drain(&sh.q_full, (loaded - 1) & 1);
+  } else if (warp >= 16) {
     // ------------------------------- producers ------------------------------
     // Producer w takes the tile's keys 16 w .. 16 w + 15.  Copy c of a pair moves
     // the rows of keys 2 c and 2 c + 1: lane l < 16 the 16-byte unit l of the
     // first, the others those of the second.
-    const int me = warp - 12, hi = lane >> 4, unit = lane & 15;
+    const int me = warp - 16, hi = lane >> 4, unit = lane & 15;
     const uint32_t lane_dst = smem_u32(ring) + me * kKeysPerProducer * 128 + (unit >> 3) * kChunkBytes + hi * 128 +
                               (((unit & 7) ^ hi) << 4);
     uint32_t at = 0, at_phase = 1, g = 0;
@@ -431,13 +448,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < n_mine && ok; ++i) {
       int tiles = 1;  // learned from the item's first tile: its rows come after its info
       for (int tile = 0; tile < tiles; ++tile, ++g) {
-        if (!(ok = warp_wait(&rows_full[g & 1], (g >> 1) & 1, abort, status))) break;
-        if (tile == 0) tiles = info[i % kInfoSlots].tiles;
-        const int4 r0 = *reinterpret_cast<const int4*>(&rows[g & 1][me * 16 + hi * 8]);
-        const int4 r1 = *reinterpret_cast<const int4*>(&rows[g & 1][me * 16 + hi * 8 + 4]);
-        const int cells = rows_cells[g & 1] - me * 16 - hi;
+        if (!(ok = warp_wait(&sh.rows_full[g & 1], (g >> 1) & 1, abort, status))) break;
+        if (tile == 0) tiles = sh.info[i % kInfoSlots].tiles;
+        const int4 r0 = *reinterpret_cast<const int4*>(&sh.rows[g & 1][me * 16 + hi * 8]);
+        const int4 r1 = *reinterpret_cast<const int4*>(&sh.rows[g & 1][me * 16 + hi * 8 + 4]);
+        const int cells = sh.rows_cells[g & 1] - me * 16 - hi;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&rows_empty[g & 1]);
+        if (lane == 0) mbar_arrive(&sh.rows_empty[g & 1]);
         const int row[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
         const uint8_t* src[8];
         uint32_t bytes[8];
@@ -450,12 +467,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int j = 0; j < kPairsPerTile; ++j) {
-          if (!(ok = warp_wait(&kv_empty[at], at_phase, abort, status))) break;
+          if (!(ok = warp_wait(&sh.kv_empty[at], at_phase, abort, status))) break;
           const uint32_t dst = lane_dst + at * kPairBytes;
 #pragma unroll
           for (int c = 0; c < 8; ++c) cp_async16((dst ^ ((2 * c & 7) << 4)) + c * 256, src[c] + j * 256, bytes[c]);
-          cp_async_arrive(&kv_full[at]);
-          if (lane == 0) mbar_arrive(&kv_full[at]);  // releases the mask
+          cp_async_arrive(&sh.kv_full[at]);
+          if (lane == 0) mbar_arrive(&sh.kv_full[at]);  // releases the mask
           if (++at == (uint32_t)kPairs) {
             at = 0;
             at_phase ^= 1;
@@ -475,16 +492,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int i = 0; i < n_mine && ok; ++i) {
       const int slot = i % kInfoSlots;
-      if (!warp_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
-      const int tiles = info[slot].tiles;
+      if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
+      const int tiles = sh.info[slot].tiles;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&info_empty[slot]);
-      if (!warp_wait(&q_full, i & 1, abort, status)) break;
+      if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+      if (!warp_wait(&sh.q_full, i & 1, abort, status)) break;
       for (int tile = 0; tile < tiles && ok; ++tile, ++g) {
-        if (!(ok = warp_wait(&s_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
+        if (!(ok = warp_wait(&sh.s_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
         const uint32_t d = tmem + kSCol + (g & 1) * kTileKeys;
         for (int j = 0; j < kPairsPerTile; ++j) {
-          if (!(ok = warp_wait(&kv_full[at], at_phase, abort, status))) break;
+          if (!(ok = warp_wait(&sh.kv_full[at], at_phase, abort, status))) break;
           fence_proxy_async();  // the copies were written through the generic proxy
           tc_fence_after();
           const uint64_t a = q_desc + (uint64_t)(j * (kPairBytes >> 4));
@@ -501,14 +518,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         if (one) {
-          umma_commit(&s_full[g & 1]);
-          mbar_arrive(&s_full[g & 1]);  // passes the mask on
+          umma_commit(&sh.s_full[g & 1]);
+          mbar_arrive(&sh.s_full[g & 1]);  // passes the mask on
         }
       }
-      if (ok && one) umma_commit(&q_empty);
+      if (ok && one) umma_commit(&sh.q_empty);
     }
-    if (one) umma_commit(&drain[0]);
-    if (one) mbar_wait_drain(&drain[0], 0);
+    if (one) umma_commit(&sh.drain[0]);
+    if (one) mbar_wait_drain(&sh.drain[0], 0);
   } else if (warp == 2) {
     // ------------------------------- O issuer -------------------------------
     const bool one = elect_one();
@@ -519,190 +536,209 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int i = 0; i < n_mine && ok; ++i) {
       const int slot = i % kInfoSlots;
-      if (!warp_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
-      const int tiles = info[slot].tiles;
+      if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
+      const int tiles = sh.info[slot].tiles;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&info_empty[slot]);
+      if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
       for (int tile = 0; tile < tiles && ok; ++tile, ++g) {
-        if (!(ok = warp_wait(&p_full[g & 1], (g >> 1) & 1, abort, status))) break;
+        if (!(ok = warp_wait(&sh.p_full[g & 1], (g >> 1) & 1, abort, status))) break;
         tc_fence_after();
         const uint64_t b = p_desc + (uint64_t)((g & 1) * (kPBytes >> 4));
         for (int m = 0; m < kPairsPerTile; ++m) {  // a pair of chunks is a block of 128 elements
           if (tile == 0) {  // the block of the last item has been read
-            if (!(ok = warp_wait(&o_empty[m], (i & 1) ^ 1, abort, status))) break;
+            if (!(ok = warp_wait(&sh.o_empty[m], (i & 1) ^ 1, abort, status))) break;
             tc_fence_after();
           }
           const uint64_t a = v_desc + (uint64_t)(at * (kPairBytes >> 4));
 #pragma unroll
           for (int kk = 0; kk < kTileKeys / 16; ++kk)
             if (one) umma_bf16_ss(tmem + m * kHeadsPerItem, a + kk * (2048 >> 4), b + kk * 2, idesc, kk == 0 ? (uint32_t)tile : 1u);
-          if (one) umma_commit(&kv_empty[at]);
+          if (one) umma_commit(&sh.kv_empty[at]);
           if (++at == (uint32_t)kPairs) at = 0;
         }
         if (!ok) break;
-        if (one) umma_commit(&pv_done[g & 1]);
+        if (one) umma_commit(&sh.pv_done[g & 1]);
       }
-      if (ok && one) umma_commit(&o_full);
+      if (ok && one) umma_commit(&sh.o_full);
     }
-    if (one) umma_commit(&drain[1]);
-    if (one) mbar_wait_drain(&drain[1], 0);
-  } else if (warp < 8) {
+    if (one) umma_commit(&sh.drain[1]);
+    if (one) mbar_wait_drain(&sh.drain[1], 0);
+  } else if (warp < 4 + kSoftmaxWarps) {
     // ------------------------------- softmax --------------------------------
-    // Warp quad w holds heads 16 w .. 16 w + 15 of the block (S's rows in the
-    // first 16 lanes of its quadrant); a thread has two of them, r0 and r0 + 8,
-    // and 16 keys of each.
-    const int quad = warp & 3;
+    // Warps quad and quad + 4 hold heads 16 quad .. 16 quad + 15 of the block (S's
+    // rows in the first 16 lanes of TMEM quadrant quad), each 32 of the tile's
+    // keys; a thread has two heads, r0 and r0 + 8, and eight keys of each.
+    const int quad = warp & 3, half = (warp - 4) >> 2;
     const int r0 = quad * 16 + lane / 4;
     const float c = p.scale * kLog2e;
+    // P is K-major in rows (heads) of 128 bytes, SWIZZLE_128B: this lane's row of
+    // the eight 8 x 8 matrices that the warp stores
+    const uint32_t p_dst = smem_u32(p_smem) + (quad * 16 + (lane & 7)) * 128 + (((4 * half + (lane >> 3)) ^ (lane & 7)) << 4);
     uint32_t g = 0;
     bool dead = false;
     for (int i = 0; i < n_mine; ++i) {
       const int slot = i % kInfoSlots;
-      bool ok = !dead && warp_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status);
+      bool ok = !dead && warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status);
       if (softmax_any(!ok)) break;
-      const int tiles = info[slot].tiles;
-      const int t = info[slot].t, h0 = info[slot].head_block * kHeadsPerItem, part = info[slot].part;
+      const int tiles = sh.info[slot].tiles;
+      const int t = sh.info[slot].t, h0 = sh.info[slot].head_block * kHeadsPerItem, part = sh.info[slot].part;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&info_empty[slot]);
+      if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // m in units of S, l of this thread's keys
       bool left = false;
       for (int tile = 0; tile < tiles; ++tile, ++g) {
-        ok = !dead && warp_wait(&s_full[g & 1], (g >> 1) & 1, abort, status);
-        uint32_t raw[32];
-        float top[2] = {-INFINITY, -INFINITY};
-        bool need = false;
+        ok = !dead && warp_wait(&sh.s_full[g & 1], (g >> 1) & 1, abort, status);
+        uint32_t raw[16], w[8];
+        float top[2] = {-INFINITY, -INFINITY}, sum[2];
+        // weights under the maximum in use and their sums
+        auto weigh = [&]() {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float mc = m[r] == -INFINITY ? 0.f : m[r] * c;
+            sum[r] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float a = exp2_fast(fmaf(__uint_as_float(raw[4 * j + 2 * r]), c, -mc));
+              const float b = exp2_fast(fmaf(__uint_as_float(raw[4 * j + 2 * r + 1]), c, -mc));
+              sum[r] += a + b;
+              w[4 * r + j] = pack_bf16(a, b);
+            }
+          }
+        };
+        bool need = false, p_free = false;
         if (ok) {
           tc_fence_after();
-          tmem_ld_16x256b_x8(tmem + ((uint32_t)(quad * 32) << 16) + kSCol + (g & 1) * kTileKeys, raw);
-          const uint2 mask = key_mask[g & 7];
+          tmem_ld_16x256b_x4(tmem + ((uint32_t)(quad * 32) << 16) + kSCol + (g & 1) * kTileKeys + 32 * half, raw);
+          const uint32_t mask = half ? sh.key_mask[g & 7].y : sh.key_mask[g & 7].x;
+          p_free = mbar_test(&sh.pv_done[g & 1], ((g >> 1) & 1) ^ 1);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[g & 1]);
-          if ((mask.x & mask.y) != 0xffffffffu) {
-            const uint32_t lo = mask.x >> (2 * (lane & 3)), hi = mask.y >> (2 * (lane & 3));
+          if (lane == 0) mbar_arrive(&sh.s_empty[g & 1]);
+          if (mask != 0xffffffffu) {
+            const uint32_t seen = mask >> (2 * (lane & 3));
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                if ((((j < 4 ? lo : hi) >> (8 * (j & 3) + e)) & 1u) == 0)
-                  raw[4 * j + e] = raw[4 * j + 2 + e] = 0xFF800000u;  // -inf
+                if (((seen >> (8 * j + e)) & 1u) == 0) raw[4 * j + e] = raw[4 * j + 2 + e] = 0xFF800000u;  // -inf
           }
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
+          for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 4; ++j)
               top[r] = fmaxf(top[r], fmaxf(__uint_as_float(raw[4 * j + 2 * r]), __uint_as_float(raw[4 * j + 2 * r + 1])));
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-          }
           // the maximum in use may be passed by up to 2^8 before the sums so far
           // are rescaled: the weights' bf16 and the fp32 sums lose nothing by it
-          need = tile > 0 && (top[0] * c > m[0] * c + 8.f || top[1] * c > m[1] * c + 8.f);
+          need = top[0] * c > m[0] * c + 8.f || top[1] * c > m[1] * c + 8.f;
+          if (tile > 0) weigh();
         }
-        if (softmax_any(need || !ok)) {
+        if (tile == 0 || softmax_any(need || !ok)) {
+          // a new maximum: the heads' tops over both halves of the keys
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+            if ((lane & 3) == 0) sh.top_half[half][r0 + 8 * r] = top[r];
+          }
           if (softmax_any(!ok)) {
             left = true;
             break;
           }
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float f = 1.f;
-            if (top[r] * c > m[r] * c + 8.f) {
-              f = m[r] == -INFINITY ? 0.f : exp2_fast((m[r] - top[r]) * c);
+            top[r] = fmaxf(top[r], sh.top_half[half ^ 1][r0 + 8 * r]);
+            if (tile == 0) {
               m[r] = top[r];
+            } else {
+              float f = 1.f;
+              if (top[r] * c > m[r] * c + 8.f) {
+                f = m[r] == -INFINITY ? 0.f : exp2_fast((m[r] - top[r]) * c);
+                m[r] = top[r];
+              }
+              l[r] *= f;
+              if (half == 0 && (lane & 3) == 0) sh.rescale[r0 + 8 * r] = f;
             }
-            l[r] *= f;
-            if ((lane & 3) == 0) rescale[r0 + 8 * r] = f;
           }
-          const uint32_t gp = g - 1;
-          ok = warp_wait(&pv_done[gp & 1], (gp >> 1) & 1, abort, status);
-          if (softmax_any(!ok)) {
-            left = true;
-            break;
-          }
-          tc_fence_after();
-          for (int x = 0; x < 8; ++x) {
-            uint32_t o[32];
-            const uint32_t addr = tmem + ((uint32_t)(quad * 32) << 16) + 32 * x;
-            tmem_ld32(addr, o);
-            tmem_ld_wait();
+          if (tile > 0) {
+            const uint32_t gp = g - 1;
+            ok = warp_wait(&sh.pv_done[gp & 1], (gp >> 1) & 1, abort, status);
+            if (softmax_any(!ok)) {
+              left = true;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 4 * half; x < 4 * half + 4; ++x) {
+              uint32_t o[32];
+              const uint32_t addr = tmem + ((uint32_t)(quad * 32) << 16) + 32 * x;
+              tmem_ld32(addr, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < 32; ++h)
-              o[h] = __float_as_uint(__uint_as_float(o[h]) * rescale[(x & 1) * 32 + h]);
-            tmem_st32(addr, o);
+              for (int h = 0; h < 32; ++h)
+                o[h] = __float_as_uint(__uint_as_float(o[h]) * sh.rescale[(x & 1) * 32 + h]);
+              tmem_st32(addr, o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
           }
-          tmem_st_wait();
-          tc_fence_before();
-        } else if (tile == 0) {
-          m[0] = top[0];
-          m[1] = top[1];
+          weigh();
         }
-        // weights, their sums, and P (bf16) in rows of 128 bytes, swizzled
-        const float mc[2] = {m[0] == -INFINITY ? 0.f : m[0] * c, m[1] == -INFINITY ? 0.f : m[1] * c};
-        uint32_t w[16];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float a = exp2_fast(fmaf(__uint_as_float(raw[4 * j + 2 * r]), c, -mc[r]));
-            const float b = exp2_fast(fmaf(__uint_as_float(raw[4 * j + 2 * r + 1]), c, -mc[r]));
-            l[r] += a + b;
-            w[2 * j + r] = pack_bf16(a, b);
-          }
-        if (!warp_wait(&pv_done[g & 1], ((g >> 1) & 1) ^ 1, abort, status)) {
+        l[0] += sum[0];
+        l[1] += sum[1];
+        if (!__all_sync(0xffffffffu, p_free) && !warp_wait(&sh.pv_done[g & 1], ((g >> 1) & 1) ^ 1, abort, status)) {
           dead = true;  // leave together with the others, at the next tile or item
           continue;
         }
-        uint8_t* dst = p_smem + (g & 1) * kPBytes + (lane & 3) * 4;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int row = r0 + 8 * r;
-            *reinterpret_cast<uint32_t*>(dst + row * 128 + ((j ^ (row & 7)) << 4)) = w[2 * j + r];
-          }
+        const uint32_t dst = p_dst + (g & 1) * kPBytes;
+        store_8x8_x4(dst, w[0], w[1], w[2], w[3]);
+        store_8x8_x4(dst + 8 * 128, w[4], w[5], w[6], w[7]);
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[g & 1]);
+        if (lane == 0) mbar_arrive(&sh.p_full[g & 1]);
       }
       if (left) break;
-      if (!dead && !warp_wait(&stat_empty[i & 1], ((i >> 1) & 1) ^ 1, abort, status)) dead = true;
-      if (dead) continue;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float sum = l[r];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const int hl = r0 + 8 * r, h = h0 + hl;
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        if (half == 1 && (lane & 3) == 0) sh.sum_half[r0 + 8 * r] = l[r];
+      }
+      if (!dead && !warp_wait(&sh.stat_empty[i & 1], ((i >> 1) & 1) ^ 1, abort, status)) dead = true;
+      if (softmax_any(dead)) break;
+      if (half == 0) {
         if ((lane & 3) == 0) {
-          if (part >= 0) {
-            factor[i & 1][hl] = 1.f;
-            p.part_ml[(int64_t)part * kHeadsPerItem + hl] = make_float2(m[r] * c, sum);
-          } else {
-            float below = sum;
-            if (p.sink_logit != nullptr && h < p.n_h) below += exp2f(fmaf(__ldg(p.sink_logit + h), kLog2e, -m[r] * c));
-            factor[i & 1][hl] = sum == 0.f ? 0.f : 1.f / below;
-            if (p.lse != nullptr && h < p.n_h)
-              p.lse[(int64_t)t * p.n_h + h] = sum == 0.f ? -INFINITY : m[r] * p.scale + logf(sum);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int hl = r0 + 8 * r, h = h0 + hl;
+            const float total = l[r] + sh.sum_half[hl];
+            if (part >= 0) {
+              p.part_ml[(int64_t)part * kHeadsPerItem + hl] = make_float2(m[r] * c, total);
+            } else {
+              float below = total;
+              if (p.sink_logit != nullptr && h < p.n_h) below += exp2f(fmaf(__ldg(p.sink_logit + h), kLog2e, -m[r] * c));
+              sh.factor[i & 1][hl] = total == 0.f ? 0.f : 1.f / below;
+              if (p.lse != nullptr && h < p.n_h)
+                p.lse[(int64_t)t * p.n_h + h] = total == 0.f ? -INFINITY : m[r] * p.scale + logf(total);
+            }
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.stat_full[i & 1]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&stat_full[i & 1]);
     }
   } else {
     // ------------------------------- epilogue -------------------------------
     const int quad = warp & 3;
     for (int i = 0; i < n_mine; ++i) {
       const int slot = i % kInfoSlots;
-      if (!warp_wait(&info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
-      const int t = info[slot].t, h0 = info[slot].head_block * kHeadsPerItem, part = info[slot].part;
+      if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
+      const int t = sh.info[slot].t, h0 = sh.info[slot].head_block * kHeadsPerItem, part = sh.info[slot].part;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&info_empty[slot]);
-      if (!warp_wait(&stat_full[i & 1], (i >> 1) & 1, abort, status)) break;
-      if (!warp_wait(&o_full, i & 1, abort, status)) break;
+      if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+      if (!warp_wait(&sh.stat_full[i & 1], (i >> 1) & 1, abort, status)) break;
+      if (!warp_wait(&sh.o_full, i & 1, abort, status)) break;
       tc_fence_after();
       const int heads = min(kHeadsPerItem, p.n_h - h0);
       const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
@@ -718,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((x & 1) * 32 + h < heads) dst[h * kWidth] = __uint_as_float(o[h]);
           tc_fence_before();
           __syncwarp();
-          if ((x & 1) && lane == 0) mbar_arrive(&o_empty[x >> 1]);
+          if ((x & 1) && lane == 0) mbar_arrive(&sh.o_empty[x >> 1]);
         }
       } else {
         // A warp has 32 elements (TMEM lanes) of every head.  Eight heads at a
@@ -734,11 +770,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
-          if ((x & 1) && lane == 0) mbar_arrive(&o_empty[x >> 1]);
+          if ((x & 1) && lane == 0) mbar_arrive(&sh.o_empty[x >> 1]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int hl = (x & 1) * 32 + 8 * j;
-            const float2 f = *reinterpret_cast<const float2*>(&factor[i & 1][hl + 2 * (lane & 3)]);
+            const float2 f = *reinterpret_cast<const float2*>(&sh.factor[i & 1][hl + 2 * (lane & 3)]);
             uint32_t e[4];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -769,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&stat_empty[i & 1]);
+      if (lane == 0) mbar_arrive(&sh.stat_empty[i & 1]);
     }
   }
   tc_fence_before();
