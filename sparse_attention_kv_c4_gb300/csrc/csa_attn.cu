@@ -64,6 +64,7 @@ constexpr int kMaxParts = 256;                  // partial results of one call
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
+  const uint16_t* q;
   const uint16_t* kv_pool;
   const uint16_t* cell_pool;
   const int32_t* page_table;
@@ -131,8 +132,12 @@ struct ItemInfo {
 };
 
 // 16 bytes global -> shared, or 16 zero bytes where `bytes` is 0: nothing is read then.
-FM_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+FM_DEV void cp_async16(uint32_t dst, uint64_t src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// Towards L2 (16-byte aligned, a multiple of 16 bytes).
+FM_DEV void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 // Arrive on `bar` when this thread's copies so far have landed.
 FM_DEV void cp_async_arrive(uint64_t* bar) {
@@ -255,14 +260,13 @@ FM_DEV bool elect_one() {
 struct Shared {
   uint64_t kv_full[kPairs], kv_empty[kPairs];
   uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
-  uint64_t q_full, q_empty, o_full, o_empty[4], stat_full[2], stat_empty[2];
+  uint64_t q_full[kPairsPerTile], q_empty[kPairsPerTile], o_full, o_empty[kPairsPerTile], stat_full[2], stat_empty[2];
   uint64_t info_full[kInfoSlots], info_empty[kInfoSlots], rows_full[2], rows_empty[2], drain[2];
   uint2 key_mask[8];                     // the resolver is up to four tiles ahead of the softmax
   ItemInfo info[kInfoSlots];
-  alignas(16) int rows[2][kTileKeys];                // key 16 w + 2 c + x at 16 w + 8 x + c
-  int rows_cells[2];                     // how many of them are cells
+  alignas(16) uint64_t rows[2][kTileKeys];  // addresses: key 16 w + 2 c + x at 16 w + 8 x + c
   alignas(16) float factor[2][kHeadsPerItem];
-  float rescale[kHeadsPerItem], top_half[2][kHeadsPerItem], sum_half[kHeadsPerItem];
+  float rescale[kHeadsPerItem], top_half[2][kHeadsPerItem];
   uint32_t tmem_slot;
   int abort_flag;
 };
@@ -298,10 +302,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.stat_full[i], 4);
       mbar_init(&sh.stat_empty[i], 4);
     }
-    mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.o_full, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.o_empty[i], 4);
+    for (int i = 0; i < kPairsPerTile; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.o_empty[i], 4);
+    }
     for (int i = 0; i < kInfoSlots; ++i) {
       mbar_init(&sh.info_full[i], 1);
       mbar_init(&sh.info_empty[i], kInfoReaders);
@@ -354,7 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         sh.info[slot] = ItemInfo{t, th % p.head_blocks, p.splits > 1 ? item : -1, tile_end - tile};
         mbar_arrive(&sh.info_full[slot]);
+        const int h0 = th % p.head_blocks * kHeadsPerItem;
+        prefetch_l2(p.q + ((int64_t)t * p.n_h + h0) * kWidth, min(kHeadsPerItem, p.n_h - h0) * kWidth * 2);
       }
+      const int tile_begin = tile;
       // The keys' indexes are read a tile ahead of their use.  Lane l resolves
       // keys l and l + 32: `raw` is a cell, or a page with `offset` in it, or -1.
       int raw[2], offset[2];
@@ -385,56 +394,61 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      fetch(tile);
-      for (; tile < tile_end; ++tile, ++g) {
-        int row[2];
+      raw[0] = raw[1] = -1;
+      for (--tile; tile < tile_end; ++tile) {  // the first pass only fetches
+        uint64_t row[2];
+        bool seen[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const bool cell = tile * kTileKeys + 32 * x + lane < n_cells;
-          row[x] = -1;
-          if (raw[x] >= 0) {
-            if (raw[x] >= (cell ? p.cell_limit : p.P))
-              atomicOr(status, FM_DEV_PAGE_RANGE);
-            else
-              row[x] = cell ? (raw[x] / kPage) * (int)p.cell_page_rows + raw[x] % kPage
-                            : raw[x] * (int)p.kv_page_rows + offset[x];
-          }
+          seen[x] = raw[x] >= 0 && raw[x] < (cell ? p.cell_limit : p.P);
+          if (raw[x] >= 0 && !seen[x]) atomicOr(status, FM_DEV_PAGE_RANGE);
+          const int64_t r = cell ? (int64_t)(raw[x] / kPage) * p.cell_page_rows + raw[x] % kPage
+                                 : raw[x] * p.kv_page_rows + offset[x];
+          // any address where nothing is read
+          row[x] = seen[x] ? reinterpret_cast<uint64_t>((cell ? p.cell_pool : p.kv_pool) + r * kWidth)
+                           : reinterpret_cast<uint64_t>(p.pos);
         }
         uint2 mask;
-        mask.x = __ballot_sync(0xffffffffu, row[0] >= 0);
-        mask.y = __ballot_sync(0xffffffffu, row[1] >= 0);
+        mask.x = __ballot_sync(0xffffffffu, seen[0]);
+        mask.y = __ballot_sync(0xffffffffu, seen[1]);
         if (tile + 1 < tile_end) fetch(tile + 1);
+        if (tile < tile_begin) continue;
         if (!(ok = warp_wait(&sh.rows_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
         const int to = (lane >> 4) * 16 + (lane & 1) * 8 + ((lane & 15) >> 1);
         sh.rows[g & 1][to] = row[0];
         sh.rows[g & 1][32 + to] = row[1];
-        if (lane == 0) {
-          sh.key_mask[g & 7] = mask;
-          const int left = n_cells - tile * kTileKeys;
-          sh.rows_cells[g & 1] = left < 0 ? 0 : left;
-        }
+        if (lane == 0) sh.key_mask[g & 7] = mask;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.rows_full[g & 1]);
+        ++g;
       }
     }
   } else if (warp == 3) {
     // ------------------------------- q loader -------------------------------
+    // Pair by pair, as the last tile of the item before is done with it.
     int loaded = 0;
-    for (int i = 0; i < n_mine; ++i) {
+    bool ok = true;
+    for (int i = 0; i < n_mine && ok; ++i) {
       const int slot = i % kInfoSlots;
       if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
       const int t = sh.info[slot].t, h0 = sh.info[slot].head_block * kHeadsPerItem;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
-      if (!warp_wait(&sh.q_empty, (i & 1) ^ 1, abort, status)) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sh.q_full, kQBytes);
-        for (int c = 0; c < kWidth / 64; ++c) tma_load_3d(q_smem + c * kChunkBytes, &tmap_q, &sh.q_full, 64 * c, h0, t);
+      for (int j = 0; j < kPairsPerTile; ++j) {
+        if (!(ok = warp_wait(&sh.q_empty[j], (i & 1) ^ 1, abort, status))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sh.q_full[j], kPairBytes);
+          tma_load_3d(q_smem + j * kPairBytes, &tmap_q, &sh.q_full[j], 128 * j, h0, t);
+          tma_load_3d(q_smem + j * kPairBytes + kChunkBytes, &tmap_q, &sh.q_full[j], 128 * j + 64, h0, t);
+        }
+        __syncwarp();
+        ++loaded;
       }
-      __syncwarp();
-      loaded = i + 1;
     }
-    if (lane == 0 && loaded > 0 && *abort) mbar_wait_drain(&sh.q_full, (loaded - 1) & 1);
+    if (lane == 0 && *abort)  // let copies in flight land before the CTA exits
+      for (int x = loaded > kPairsPerTile ? loaded - kPairsPerTile : 0; x < loaded; ++x)
+        mbar_wait_drain(&sh.q_full[x % kPairsPerTile], (x / kPairsPerTile) & 1);
   } else if (warp >= 16) {
     // ------------------------------- producers ------------------------------
     // Producer w takes the tile's keys 16 w .. 16 w + 15.  Copy c of a pair moves
@@ -444,42 +458,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_dst = smem_u32(ring) + me * kKeysPerProducer * 128 + (unit >> 3) * kChunkBytes + hi * 128 +
                               (((unit & 7) ^ hi) << 4);
     uint32_t at = 0, at_phase = 1, g = 0;
-    bool ok = true;
-    for (int i = 0; i < n_mine && ok; ++i) {
-      int tiles = 1;  // learned from the item's first tile: its rows come after its info
-      for (int tile = 0; tile < tiles; ++tile, ++g) {
-        if (!(ok = warp_wait(&sh.rows_full[g & 1], (g >> 1) & 1, abort, status))) break;
-        if (tile == 0) tiles = sh.info[i % kInfoSlots].tiles;
-        const int4 r0 = *reinterpret_cast<const int4*>(&sh.rows[g & 1][me * 16 + hi * 8]);
-        const int4 r1 = *reinterpret_cast<const int4*>(&sh.rows[g & 1][me * 16 + hi * 8 + 4]);
-        const int cells = sh.rows_cells[g & 1] - me * 16 - hi;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.rows_empty[g & 1]);
-        const int row[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-        const uint8_t* src[8];
-        uint32_t bytes[8];
+    int i = 0, left = 0;  // the current item, its tiles not yet copied
+    uint64_t src[8];
+    uint32_t valid = 0;   // bit 2 c: copy c reads
+    auto take_rows = [&](uint32_t tile) {
+      const ulonglong2* r = reinterpret_cast<const ulonglong2*>(&sh.rows[tile & 1][me * 16 + hi * 8]);
+#pragma unroll
+      for (int c = 0; c < 8; c += 2) {
+        const ulonglong2 x = r[c / 2];
+        src[c] = x.x + unit * 16;
+        src[c + 1] = x.y + unit * 16;
+      }
+      valid = (me & 2 ? sh.key_mask[tile & 7].y : sh.key_mask[tile & 7].x) >> ((me & 1) * 16 + hi);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.rows_empty[tile & 1]);
+    };
+    bool taken = false;
+    // (the loops here stay rolled: unrolled, the roles' code outgrows the instruction cache)
+    while (i < n_mine) {
+      if (!taken) {
+        if (!warp_wait(&sh.rows_full[g & 1], (g >> 1) & 1, abort, status)) break;
+        take_rows(g);
+      }
+      if (left == 0) left = sh.info[i % kInfoSlots].tiles;  // an item's rows come after its info
+      if (--left == 0) ++i;
+      taken = false;
+      bool ok = true;
+      uint64_t from[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) from[c] = src[c];
+      const uint32_t reads = valid;
+      ++g;
+#pragma unroll 1
+      for (int j = 0; j < kPairsPerTile; ++j) {
+        // the next tile's rows, where they are there already, before the last wait
+        if (j == kPairsPerTile - 1 && i < n_mine &&
+            __all_sync(0xffffffffu, mbar_test(&sh.rows_full[g & 1], (g >> 1) & 1))) {
+          take_rows(g);
+          taken = true;
+        }
+        if (!(ok = warp_wait(&sh.kv_empty[at], at_phase, abort, status))) break;
+        const uint32_t dst = lane_dst + at * kPairBytes;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const uint16_t* base = 2 * c < cells ? p.cell_pool : p.kv_pool;
-          bytes[c] = row[c] >= 0 ? 16u : 0u;
-          if (row[c] < 0) base = reinterpret_cast<const uint16_t*>(p.pos);  // any address: nothing is read
-          src[c] = reinterpret_cast<const uint8_t*>(base + (int64_t)(row[c] < 0 ? 0 : row[c]) * kWidth) + unit * 16;
+          cp_async16((dst ^ ((2 * c & 7) << 4)) + c * 256, from[c], (reads >> (2 * c) & 1u) << 4);
+          from[c] += 256;
         }
-#pragma unroll
-        for (int j = 0; j < kPairsPerTile; ++j) {
-          if (!(ok = warp_wait(&sh.kv_empty[at], at_phase, abort, status))) break;
-          const uint32_t dst = lane_dst + at * kPairBytes;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) cp_async16((dst ^ ((2 * c & 7) << 4)) + c * 256, src[c] + j * 256, bytes[c]);
-          cp_async_arrive(&sh.kv_full[at]);
-          if (lane == 0) mbar_arrive(&sh.kv_full[at]);  // releases the mask
-          if (++at == (uint32_t)kPairs) {
-            at = 0;
-            at_phase ^= 1;
-          }
+        cp_async_arrive(&sh.kv_full[at]);
+        if (lane == 0) mbar_arrive(&sh.kv_full[at]);  // releases the mask
+        if (++at == (uint32_t)kPairs) {
+          at = 0;
+          at_phase ^= 1;
         }
-        if (!ok) break;
       }
+      if (!ok) break;
     }
     cp_async_wait_all();
   } else if (warp == 0) {
@@ -496,11 +528,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tiles = sh.info[slot].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
-      if (!warp_wait(&sh.q_full, i & 1, abort, status)) break;
       for (int tile = 0; tile < tiles && ok; ++tile, ++g) {
         if (!(ok = warp_wait(&sh.s_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
         const uint32_t d = tmem + kSCol + (g & 1) * kTileKeys;
         for (int j = 0; j < kPairsPerTile; ++j) {
+          if (tile == 0 && !(ok = warp_wait(&sh.q_full[j], i & 1, abort, status))) break;
           if (!(ok = warp_wait(&sh.kv_full[at], at_phase, abort, status))) break;
           fence_proxy_async();  // the copies were written through the generic proxy
           tc_fence_after();
@@ -511,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t o = (uint64_t)((kk >> 2) * (kChunkBytes >> 4) + (kk & 3) * 2);
             if (one) umma_bf16_ss(d, a + o, b + o, idesc, kk == 0 ? (uint32_t)j : 1u);
           }
+          if (tile == tiles - 1 && one) umma_commit(&sh.q_empty[j]);
           if (++at == (uint32_t)kPairs) {
             at = 0;
             at_phase ^= 1;
@@ -522,7 +555,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sh.s_full[g & 1]);  // passes the mask on
         }
       }
-      if (ok && one) umma_commit(&sh.q_empty);
     }
     if (one) umma_commit(&sh.drain[0]);
     if (one) mbar_wait_drain(&sh.drain[0], 0);
@@ -590,21 +622,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = !dead && warp_wait(&sh.s_full[g & 1], (g >> 1) & 1, abort, status);
         uint32_t raw[16], w[8];
         float top[2] = {-INFINITY, -INFINITY}, sum[2];
-        // weights under the maximum in use and their sums
-        auto weigh = [&]() {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float mc = m[r] == -INFINITY ? 0.f : m[r] * c;
-            sum[r] = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = exp2_fast(fmaf(__uint_as_float(raw[4 * j + 2 * r]), c, -mc));
-              const float b = exp2_fast(fmaf(__uint_as_float(raw[4 * j + 2 * r + 1]), c, -mc));
-              sum[r] += a + b;
-              w[4 * r + j] = pack_bf16(a, b);
-            }
-          }
-        };
         bool need = false, p_free = false;
         if (ok) {
           tc_fence_after();
@@ -631,9 +648,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the maximum in use may be passed by up to 2^8 before the sums so far
           // are rescaled: the weights' bf16 and the fp32 sums lose nothing by it
           need = top[0] * c > m[0] * c + 8.f || top[1] * c > m[1] * c + 8.f;
-          if (tile > 0) weigh();
         }
-        if (tile == 0 || softmax_any(need || !ok)) {
+        // Weights under the maximum in use, before it is known whether that
+        // holds; where it does not, once more under the new one.
+        for (bool renew = tile == 0, last = false;; renew = true) {
+          if (!renew || last) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float mc = m[r] == -INFINITY ? 0.f : m[r] * c;
+              sum[r] = 0.f;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float a = exp2_fast(fmaf(__uint_as_float(raw[4 * j + 2 * r]), c, -mc));
+                const float b = exp2_fast(fmaf(__uint_as_float(raw[4 * j + 2 * r + 1]), c, -mc));
+                sum[r] += a + b;
+                w[4 * r + j] = pack_bf16(a, b);
+              }
+            }
+            if (last || !softmax_any(need || !ok)) break;
+          }
           // a new maximum: the heads' tops over both halves of the keys
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
@@ -641,10 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
             if ((lane & 3) == 0) sh.top_half[half][r0 + 8 * r] = top[r];
           }
-          if (softmax_any(!ok)) {
-            left = true;
-            break;
-          }
+          left = softmax_any(!ok);
+          if (left) break;
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             top[r] = fmaxf(top[r], sh.top_half[half ^ 1][r0 + 8 * r]);
@@ -663,10 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tile > 0) {
             const uint32_t gp = g - 1;
             ok = warp_wait(&sh.pv_done[gp & 1], (gp >> 1) & 1, abort, status);
-            if (softmax_any(!ok)) {
-              left = true;
-              break;
-            }
+            left = softmax_any(!ok);
+            if (left) break;
             tc_fence_after();
 #pragma unroll 1
             for (int x = 4 * half; x < 4 * half + 4; ++x) {
@@ -682,8 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
             tc_fence_before();
           }
-          weigh();
+          last = true;
         }
+        if (left) break;
         l[0] += sum[0];
         l[1] += sum[1];
         if (!__all_sync(0xffffffffu, p_free) && !warp_wait(&sh.pv_done[g & 1], ((g >> 1) & 1) ^ 1, abort, status)) {
@@ -703,16 +733,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = 0; r < 2; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        if (half == 1 && (lane & 3) == 0) sh.sum_half[r0 + 8 * r] = l[r];
       }
       if (!dead && !warp_wait(&sh.stat_empty[i & 1], ((i >> 1) & 1) ^ 1, abort, status)) dead = true;
+      // the upper halves' sums pass through the place of the factors
+      if (!dead && half == 1 && (lane & 3) == 0) {
+        sh.factor[i & 1][r0] = l[0];
+        sh.factor[i & 1][r0 + 8] = l[1];
+      }
       if (softmax_any(dead)) break;
       if (half == 0) {
         if ((lane & 3) == 0) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const int hl = r0 + 8 * r, h = h0 + hl;
-            const float total = l[r] + sh.sum_half[hl];
+            const float total = l[r] + sh.factor[i & 1][hl];
             if (part >= 0) {
               p.part_ml[(int64_t)part * kHeadsPerItem + hl] = make_float2(m[r] * c, total);
             } else {
@@ -940,6 +974,7 @@ fm_status csa_attn(const char* who, bool tree, const uint16_t* q, int T, int n_h
   if (st != FM_OK) return st;
   AttnParams p = {};
   if ((st = status_word(&p.status)) != FM_OK) return st;
+  p.q = q;
   p.kv_pool = kv_pool;
   p.cell_pool = cell_pool;
   p.page_table = page_table;
