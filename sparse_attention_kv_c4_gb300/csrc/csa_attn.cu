@@ -61,7 +61,7 @@ constexpr int kInfoSlots = 4;
 constexpr int kInfoReaders = 1 + 2 + kSoftmaxWarps + 4;       // q loader, issuers, softmax and epilogue warps
 constexpr int kKvArrivals = 33 * kProducerWarps;              // the producers' copies, and their first lanes
 constexpr int kMaxParts = 256;                  // partial results of one call
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
   const uint16_t* q;
@@ -165,14 +165,6 @@ FM_DEV void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
-// Transpose of an 8 x 8 matrix of 16-bit elements: thread i holds row i / 4,
-// columns 2 (i % 4) + {0, 1} of it, before and after.
-FM_DEV uint32_t transpose_8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
 // Descriptor of an MN-major SWIZZLE_128B operand: 64 elements of M or N to a
 // 128-byte row, one row per K; 8-row groups 1024 bytes apart (stride offset),
 // the next 64 elements of M or N a chunk further (leading offset).
@@ -200,6 +192,18 @@ FM_DEV void store_8x8_x4(uint32_t addr, uint32_t x0, uint32_t x1, uint32_t x2, u
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x0), "r"(x1),
                "r"(x2), "r"(x3)
                : "memory");
+}
+
+// The same, each matrix transposed.
+FM_DEV void store_8x8_x4_trans(uint32_t addr, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x0), "r"(x1),
+               "r"(x2), "r"(x3)
+               : "memory");
+}
+FM_DEV uint4 load_shared_16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 
 // Whether the phase with the given parity is complete, without a wait.
@@ -234,11 +238,32 @@ FM_DEV uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// A warp's wait: lane 0 polls, every lane learns the result.
+FM_DEV uint32_t timer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+
+// A warp's wait for a phase, given up after FM_WAIT_LIMIT_NS or when another
+// warp has given up.  Lane 0 polls.  Some twenty copies of this loop share the
+// instruction cache with the roles' own loops, so it is kept small.
 FM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort, status) ? 1 : 0;
+  if ((threadIdx.x & 31) == 0) {
+    const uint32_t t0 = timer_lo();
+#pragma unroll 1
+    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+      if ((n & 31) != 0) continue;
+      const bool late = timer_lo() - t0 > (uint32_t)FM_WAIT_LIMIT_NS;
+      if (late && *abort == 0) atomicOr(status, FM_DEV_TIMEOUT);
+      if (late) *abort = 1;
+      if (*abort != 0) {
+        ok = 0;
+        break;
+      }
+    }
+  }
   ok = __shfl_sync(0xffffffffu, ok, 0);
   __syncwarp();
   return ok != 0;
@@ -260,19 +285,19 @@ FM_DEV bool elect_one() {
 struct Shared {
   uint64_t kv_full[kPairs], kv_empty[kPairs];
   uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
-  uint64_t q_full[kPairsPerTile], q_empty[kPairsPerTile], o_full, o_empty[kPairsPerTile], stat_full[2], stat_empty[2];
+  uint64_t q_full[kPairsPerTile], q_empty[kPairsPerTile], o_full, o_empty[kPairsPerTile], stat_full, stat_empty, stage_free[2];
   uint64_t info_full[kInfoSlots], info_empty[kInfoSlots], rows_full[2], rows_empty[2], drain[2];
   uint2 key_mask[8];                     // the resolver is up to four tiles ahead of the softmax
   ItemInfo info[kInfoSlots];
   alignas(16) uint64_t rows[2][kTileKeys];  // addresses: key 16 w + 2 c + x at 16 w + 8 x + c
-  alignas(16) float factor[2][kHeadsPerItem];
+  float2 stat[kHeadsPerItem];            // maximum in log2 units, sum of an item's heads
   float rescale[kHeadsPerItem], top_half[2][kHeadsPerItem];
   uint32_t tmem_slot;
   int abort_flag;
 };
 constexpr int kSmemBytes = kQBytes + kPairs * kPairBytes + 2 * kPBytes + (int)sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "227 KB of shared memory to a CTA");
-static_assert(offsetof(Shared, rows) % 16 == 0 && offsetof(Shared, factor) % 8 == 0, "vector accesses");
+static_assert(offsetof(Shared, rows) % 16 == 0, "vector accesses");
 
 __global__ void __launch_bounds__(kThreads, 1)
     csa_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ AttnParams p) {
@@ -299,10 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.s_empty[i], kSoftmaxWarps);
       mbar_init(&sh.p_full[i], kSoftmaxWarps);
       mbar_init(&sh.pv_done[i], 1);
-      mbar_init(&sh.stat_full[i], 4);
-      mbar_init(&sh.stat_empty[i], 4);
+      mbar_init(&sh.stage_free[i], 4);
     }
     mbar_init(&sh.o_full, 1);
+    mbar_init(&sh.stat_full, 4);
+    mbar_init(&sh.stat_empty, 4);
     for (int i = 0; i < kPairsPerTile; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
@@ -336,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------- resolver ------------------------------
     bool ok = true;
     uint32_t g = 0;
+#pragma unroll 1
     for (int i = 0; i < n_mine && ok; ++i) {
       const int slot = i % kInfoSlots;
       const int item = (int)blockIdx.x + i * (int)gridDim.x;
@@ -395,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       raw[0] = raw[1] = -1;
+#pragma unroll 1
       for (--tile; tile < tile_end; ++tile) {  // the first pass only fetches
         uint64_t row[2];
         bool seen[2];
@@ -429,12 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Pair by pair, as the last tile of the item before is done with it.
     int loaded = 0;
     bool ok = true;
+#pragma unroll 1
     for (int i = 0; i < n_mine && ok; ++i) {
       const int slot = i % kInfoSlots;
       if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
       const int t = sh.info[slot].t, h0 = sh.info[slot].head_block * kHeadsPerItem;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+#pragma unroll 1
       for (int j = 0; j < kPairsPerTile; ++j) {
         if (!(ok = warp_wait(&sh.q_empty[j], (i & 1) ^ 1, abort, status))) break;
         if (lane == 0) {
@@ -475,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool taken = false;
     // (the loops here stay rolled: unrolled, the roles' code outgrows the instruction cache)
+#pragma unroll 1
     while (i < n_mine) {
       if (!taken) {
         if (!warp_wait(&sh.rows_full[g & 1], (g >> 1) & 1, abort, status)) break;
@@ -522,15 +553,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t k_desc = sdesc_sw128(smem_u32(ring));
     uint32_t g = 0, at = 0, at_phase = 0;
     bool ok = true;
+#pragma unroll 1
     for (int i = 0; i < n_mine && ok; ++i) {
       const int slot = i % kInfoSlots;
       if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
       const int tiles = sh.info[slot].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+#pragma unroll 1
       for (int tile = 0; tile < tiles && ok; ++tile, ++g) {
         if (!(ok = warp_wait(&sh.s_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
         const uint32_t d = tmem + kSCol + (g & 1) * kTileKeys;
+#pragma unroll 1
         for (int j = 0; j < kPairsPerTile; ++j) {
           if (tile == 0 && !(ok = warp_wait(&sh.q_full[j], i & 1, abort, status))) break;
           if (!(ok = warp_wait(&sh.kv_full[at], at_phase, abort, status))) break;
@@ -566,16 +600,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t p_desc = sdesc_sw128(smem_u32(p_smem));
     uint32_t g = 0, at = 0;
     bool ok = true;
+#pragma unroll 1
     for (int i = 0; i < n_mine && ok; ++i) {
       const int slot = i % kInfoSlots;
       if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
       const int tiles = sh.info[slot].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+#pragma unroll 1
       for (int tile = 0; tile < tiles && ok; ++tile, ++g) {
         if (!(ok = warp_wait(&sh.p_full[g & 1], (g >> 1) & 1, abort, status))) break;
         tc_fence_after();
         const uint64_t b = p_desc + (uint64_t)((g & 1) * (kPBytes >> 4));
+#pragma unroll 1
         for (int m = 0; m < kPairsPerTile; ++m) {  // a pair of chunks is a block of 128 elements
           if (tile == 0) {  // the block of the last item has been read
             if (!(ok = warp_wait(&sh.o_empty[m], (i & 1) ^ 1, abort, status))) break;
@@ -607,17 +644,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the eight 8 x 8 matrices that the warp stores
     const uint32_t p_dst = smem_u32(p_smem) + (quad * 16 + (lane & 7)) * 128 + (((4 * half + (lane >> 3)) ^ (lane & 7)) << 4);
     uint32_t g = 0;
+    uint32_t staged = 0;  // bit b: P buffer b is lent to an epilogue; bit 2 + b: the phase it ends with
     bool dead = false;
+#pragma unroll 1
     for (int i = 0; i < n_mine; ++i) {
       const int slot = i % kInfoSlots;
       bool ok = !dead && warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status);
       if (softmax_any(!ok)) break;
       const int tiles = sh.info[slot].tiles;
-      const int t = sh.info[slot].t, h0 = sh.info[slot].head_block * kHeadsPerItem, part = sh.info[slot].part;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // m in units of S, l of this thread's keys
       bool left = false;
+#pragma unroll 1
       for (int tile = 0; tile < tiles; ++tile, ++g) {
         ok = !dead && warp_wait(&sh.s_full[g & 1], (g >> 1) & 1, abort, status);
         uint32_t raw[16], w[8];
@@ -651,6 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // Weights under the maximum in use, before it is known whether that
         // holds; where it does not, once more under the new one.
+#pragma unroll 1
         for (bool renew = tile == 0, last = false;; renew = true) {
           if (!renew || last) {
 #pragma unroll
@@ -720,6 +760,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           dead = true;  // leave together with the others, at the next tile or item
           continue;
         }
+        // an epilogue staged its output in this buffer
+        if (staged >> (g & 1) & 1u) {
+          staged ^= 1u << (g & 1);
+          if (!warp_wait(&sh.stage_free[g & 1], staged >> (2 + (g & 1)) & 1u, abort, status)) {
+            dead = true;
+            continue;
+          }
+          staged ^= 4u << (g & 1);
+        }
         const uint32_t dst = p_dst + (g & 1) * kPBytes;
         store_8x8_x4(dst, w[0], w[1], w[2], w[3]);
         store_8x8_x4(dst + 8 * 128, w[4], w[5], w[6], w[7]);
@@ -734,47 +783,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       }
-      if (!dead && !warp_wait(&sh.stat_empty[i & 1], ((i >> 1) & 1) ^ 1, abort, status)) dead = true;
-      // the upper halves' sums pass through the place of the factors
+      staged |= 1u << ((g - 1) & 1);
+      if (!dead && !warp_wait(&sh.stat_empty, (i & 1) ^ 1, abort, status)) dead = true;
+      // the upper halves' sums pass to the lower ones
       if (!dead && half == 1 && (lane & 3) == 0) {
-        sh.factor[i & 1][r0] = l[0];
-        sh.factor[i & 1][r0 + 8] = l[1];
+        sh.stat[r0].y = l[0];
+        sh.stat[r0 + 8].y = l[1];
       }
       if (softmax_any(dead)) break;
       if (half == 0) {
         if ((lane & 3) == 0) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int hl = r0 + 8 * r, h = h0 + hl;
-            const float total = l[r] + sh.factor[i & 1][hl];
-            if (part >= 0) {
-              p.part_ml[(int64_t)part * kHeadsPerItem + hl] = make_float2(m[r] * c, total);
-            } else {
-              float below = total;
-              if (p.sink_logit != nullptr && h < p.n_h) below += exp2f(fmaf(__ldg(p.sink_logit + h), kLog2e, -m[r] * c));
-              sh.factor[i & 1][hl] = total == 0.f ? 0.f : 1.f / below;
-              if (p.lse != nullptr && h < p.n_h)
-                p.lse[(int64_t)t * p.n_h + h] = total == 0.f ? -INFINITY : m[r] * p.scale + logf(total);
-            }
-          }
+          for (int r = 0; r < 2; ++r) sh.stat[r0 + 8 * r] = make_float2(m[r] * c, l[r] + sh.stat[r0 + 8 * r].y);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.stat_full[i & 1]);
+        if (lane == 0) mbar_arrive(&sh.stat_full);
       }
     }
   } else {
     // ------------------------------- epilogue -------------------------------
+    // A warp has 32 elements (TMEM lanes) of every head.  The output is staged,
+    // transposed, 32 heads x 32 elements at a time in a quarter of the P buffer
+    // that the item's last tile is done with.
     const int quad = warp & 3;
+    uint32_t g = 0;
+#pragma unroll 1
     for (int i = 0; i < n_mine; ++i) {
       const int slot = i % kInfoSlots;
       if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
       const int t = sh.info[slot].t, h0 = sh.info[slot].head_block * kHeadsPerItem, part = sh.info[slot].part;
+      g += (uint32_t)sh.info[slot].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
-      if (!warp_wait(&sh.stat_full[i & 1], (i >> 1) & 1, abort, status)) break;
+      const int heads = min(kHeadsPerItem, p.n_h - h0);
+      float sink[2] = {-INFINITY, -INFINITY};  // of heads lane and lane + 32
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (p.sink_logit != nullptr && lane + 32 * r < heads) sink[r] = __ldg(p.sink_logit + h0 + lane + 32 * r) * kLog2e;
+      if (!warp_wait(&sh.stat_full, i & 1, abort, status)) break;
+      const float2 stat[2] = {sh.stat[lane], sh.stat[lane + 32]};
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.stat_empty);
+      float factor[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        factor[r] = stat[r].y == 0.f ? 0.f : 1.f / (stat[r].y + exp2_fast(sink[r] - stat[r].x));
+        if (quad == 0) {
+          if (part >= 0)
+            p.part_ml[(int64_t)part * kHeadsPerItem + lane + 32 * r] = stat[r];
+          else if (p.lse != nullptr && lane + 32 * r < heads)
+            p.lse[(int64_t)t * p.n_h + h0 + lane + 32 * r] = stat[r].y == 0.f ? -INFINITY : (stat[r].x + log2f(stat[r].y)) * kLn2;
+        }
+      }
       if (!warp_wait(&sh.o_full, i & 1, abort, status)) break;
       tc_fence_after();
-      const int heads = min(kHeadsPerItem, p.n_h - h0);
       const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
       if (part >= 0) {
 #pragma unroll 1
@@ -782,19 +844,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t o[32];
           tmem_ld32(lanes + 32 * x, o);
           tmem_ld_wait();
+          if (x & 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_empty[x >> 1]);
+          }
           float* dst = p.part_o + ((int64_t)part * kHeadsPerItem + (x & 1) * 32) * kWidth + (x >> 1) * 128 + quad * 32 + lane;
 #pragma unroll
           for (int h = 0; h < 32; ++h)
             if ((x & 1) * 32 + h < heads) dst[h * kWidth] = __uint_as_float(o[h]);
-          tc_fence_before();
-          __syncwarp();
-          if ((x & 1) && lane == 0) mbar_arrive(&sh.o_empty[x >> 1]);
         }
       } else {
-        // A warp has 32 elements (TMEM lanes) of every head.  Eight heads at a
-        // time: four 8 x 8 transposes give thread i head i / 4 and elements 8 e +
-        // 2 (i % 4) + {0, 1} for e < 4; a transpose among four threads gives it
-        // elements 8 (i % 4) .. + 7, 16 bytes.
+        const uint32_t stage = smem_u32(p_smem) + ((g - 1) & 1) * kPBytes + quad * 2048;
+        // rows of 64 bytes (32 elements of a head), their 16-byte units swizzled:
+        // unit u of row h at u ^ (h / 2) % 4
+        const uint32_t put = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+        const uint32_t get = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
         uint16_t* dst = p.out + ((int64_t)t * p.n_h + h0 + lane / 4) * kWidth + quad * 32 + (lane & 3) * 8;
 #pragma unroll 1
         for (int x = 0; x < 8; ++x) {
@@ -802,44 +867,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_16x256b_x4(lanes + 32 * x, a);
           tmem_ld_16x256b_x4(lanes + (16u << 16) + 32 * x, b);
           tmem_ld_wait();
-          tc_fence_before();
-          __syncwarp();
-          if ((x & 1) && lane == 0) mbar_arrive(&sh.o_empty[x >> 1]);
+          if (x & 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_empty[x >> 1]);
+          }
+          const float mine = x & 1 ? factor[1] : factor[0];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int hl = (x & 1) * 32 + 8 * j;
-            const float2 f = *reinterpret_cast<const float2*>(&sh.factor[i & 1][hl + 2 * (lane & 3)]);
+            const float f0 = __shfl_sync(0xffffffffu, mine, 8 * j + 2 * (lane & 3));
+            const float f1 = __shfl_sync(0xffffffffu, mine, 8 * j + 2 * (lane & 3) + 1);
             uint32_t e[4];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              e[r] = transpose_8x8(pack_bf16(__uint_as_float(a[4 * j + 2 * r]) * f.x, __uint_as_float(a[4 * j + 2 * r + 1]) * f.y));
-              e[2 + r] = transpose_8x8(pack_bf16(__uint_as_float(b[4 * j + 2 * r]) * f.x, __uint_as_float(b[4 * j + 2 * r + 1]) * f.y));
+              e[r] = pack_bf16(__uint_as_float(a[4 * j + 2 * r]) * f0, __uint_as_float(a[4 * j + 2 * r + 1]) * f1);
+              e[2 + r] = pack_bf16(__uint_as_float(b[4 * j + 2 * r]) * f0, __uint_as_float(b[4 * j + 2 * r + 1]) * f1);
             }
-            // e[k] of lane q is word (k, q): after two exchanges lane q has words (q, 0..3)
-            const bool odd = lane & 1, high = lane & 2;
-#pragma unroll
-            for (int r = 0; r < 4; r += 2) {
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? e[r] : e[r + 1], 1);
-              if (odd)
-                e[r] = got;
-              else
-                e[r + 1] = got;
-            }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? e[r] : e[r + 2], 2);
-              if (high)
-                e[r] = got;
-              else
-                e[r + 2] = got;
-            }
-            if (hl + lane / 4 < heads)
-              *reinterpret_cast<uint4*>(dst + (int64_t)hl * kWidth + (x >> 1) * 128) = make_uint4(e[0], e[1], e[2], e[3]);
+            store_8x8_x4_trans(put + 8 * j * 64, e[0], e[1], e[2], e[3]);
           }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 v = load_shared_16(get + 8 * j * 64);
+            const int hl = (x & 1) * 32 + 8 * j;
+            if (hl + lane / 4 < heads) *reinterpret_cast<uint4*>(dst + (int64_t)hl * kWidth + (x >> 1) * 128) = v;
+          }
+          __syncwarp();
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.stat_empty[i & 1]);
+      if (lane == 0) mbar_arrive(&sh.stage_free[(g - 1) & 1]);
     }
   }
   tc_fence_before();
@@ -879,7 +935,7 @@ __global__ void __launch_bounds__(128) csa_merge_kernel(const __grid_constant__ 
   v.y = pack_bf16(acc.z * f, acc.w * f);
   *reinterpret_cast<uint2*>(p.out + th * kWidth + d) = v;
   if (p.lse != nullptr && threadIdx.x == 0)
-    p.lse[th] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    p.lse[th] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 int head_blocks_of(int n_h) { return (n_h + kHeadsPerItem - 1) / kHeadsPerItem; }
