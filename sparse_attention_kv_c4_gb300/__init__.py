@@ -139,6 +139,9 @@ def _check(status: int) -> None:
 def _stream(stream) -> int:
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle alone: a tenth of the time
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
@@ -386,124 +389,167 @@ def fm_page_recall(mask, S: int, kmax: int, pages_out, density_out=None, n_out=N
                                 _ptr(n_out), _stream(stream)))
 
 
-def _arg(t, name: str, dtypes, shape, device=None, rows=False):
-    """Check one tensor argument: its element type, its shape (None: any size)
-    and that it is dense -- or, with rows, dense but for its first stride."""
+# The wrappers below check every tensor they are given, on each call; a decode step
+# waits for that, so the checks of an accepted tensor are a few attribute reads and
+# the reasons are worked out only for a refused one.
+_BF16 = _BITS = _I32T = _I64T = _F32T = _U8T = frozenset()  # accepted element types, set by _types()
+
+
+def _types():
     import torch
-    names = dtypes if isinstance(dtypes, tuple) else (dtypes,)
-    if t.dtype not in tuple(getattr(torch, n) for n in names):
-        raise ValueError(f"{name}: dtype {t.dtype}, need {' or '.join(names)}")
-    if t.dim() != len(shape) or any(want is not None and want != have for want, have in zip(shape, t.shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {tuple('any' if n is None else n for n in shape)}")
-    dense = 1
-    for i in reversed(range(1 if rows else 0, t.dim())):
-        if t.shape[i] != 1 and t.stride(i) != dense and t.numel():
-            raise ValueError(f"{name}: strides {t.stride()} of shape {tuple(t.shape)}: rows must be dense")
-        dense *= t.shape[i]
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, need {device}")
+    global _BF16, _BITS, _I32T, _I64T, _F32T, _U8T
+    _BITS, _I32T, _I64T = frozenset((torch.int32, torch.uint32)), frozenset((torch.int32,)), frozenset((torch.int64,))
+    _F32T, _U8T = frozenset((torch.float32,)), frozenset((torch.uint8,))
+    _BF16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))  # bf16 tensors, or their bit patterns
 
 
-def _stride0(t, dense: int) -> int:
-    """The first stride, or the dense one where a size of one leaves it open."""
-    return t.stride(0) if t.shape[0] > 1 else dense
+def _refuse(t, name, types, shape, dev, rows):
+    if t.dtype not in types:
+        raise ValueError(f"{name}: dtype {t.dtype}, need {' or '.join(sorted(map(str, types)))}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {shape}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the other tensors are on {'cuda:%d' % dev if dev >= 0 else 'cpu'}")
+    raise ValueError(f"{name}: strides {t.stride()} of shape {shape}: "
+                     f"{'all but the first dimension' if rows else 'the tensor'} must be dense")
 
 
-def _current(t, name: str):
-    """The tensor's device, which must be the current one (the streams' device)."""
-    import torch
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
+def _dense(t, name, types, shape, dev):
+    """Pointer of a dense tensor of these types, this shape and device (-1: CPU)."""
+    if t.dtype in types and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, types, shape, dev, False)
 
 
-_BF16 = ("bfloat16", "int16", "uint16")  # bf16 tensors, or their bit patterns
+def _rows(t, name, types, shape, dev):
+    """Pointer and first stride of a 3-dimensional tensor that is dense but for its
+    first dimension (the dense stride where one row or none leaves it open)."""
+    if t.dtype in types and t.shape == shape and t.get_device() == dev:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1] * shape[2]
+        stride = t.stride()
+        if (stride[2] == 1 and stride[1] == shape[2]) or (shape[0] and t[0].is_contiguous()):
+            return t.data_ptr(), stride[0]
+    _refuse(t, name, types, shape, dev, True)
+
+
+def _device(t, name):
+    """The tensor's device index (-1: CPU), which must be the current device: the
+    call's stream and kernels are that device's."""
+    if not _BF16:
+        _types()
+    dev = t.get_device()
+    if dev >= 0:
+        import torch
+        if dev != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _shape(t, name, dims):
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name}: shape {tuple(shape)}, need {dims} dimensions")
+    return tuple(shape)
 
 
 def fm_qk_norm_rope(pos, q=None, q_gain=None, q_out=None, k=None, k_gain=None, k_out=None, k_pool=None, k_cell=None,
-                    rope_dim: int = 64, eps: float = 1e-6, stream=None, **rope) -> None:
+                    rope_dim: int = 64, eps: float = 1e-6, stream=None, rope_base: float = RETRIEVER_ROPE["rope_base"],
+                    rope_factor: float = RETRIEVER_ROPE["rope_factor"],
+                    rope_orig_len: float = RETRIEVER_ROPE["rope_orig_len"],
+                    rope_beta_fast: float = RETRIEVER_ROPE["rope_beta_fast"],
+                    rope_beta_slow: float = RETRIEVER_ROPE["rope_beta_slow"]) -> None:
     """pos [T] int64; q [T,n_q,d] bf16 (any token stride) -> q_out [T,n_q,d];
     k [T,n_k,d] bf16 (any token stride) -> k_out [T,n_k,d] and/or rows
     k_cell [T] int32 of k_pool [P,64,n_k*d] (any page stride).  q or k may be
     None.  RMSNorm per head with q_gain / k_gain [d] (None: ones), then the
-    rotation of the last rope_dim entries (rope: RETRIEVER_ROPE's parameters)."""
-    cfg = dict(RETRIEVER_ROPE, **rope)
-    if len(cfg) != len(RETRIEVER_ROPE):
-        raise TypeError(f"unknown arguments {sorted(set(cfg) - set(RETRIEVER_ROPE))}")
-    one = q if q is not None else k
-    if one is None:
+    rotation of the last rope_dim entries (YaRN; RETRIEVER_ROPE's parameters)."""
+    if q is None and k is None:
         raise ValueError("q or k is needed")
-    dev = _current(one, "q" if q is not None else "k")
-    T, d = one.shape[0], one.shape[-1]
-    _arg(pos, "pos", "int64", (T,), dev)
-    n_q = n_k = 0
+    dev = _device(pos, "pos")
+    T, _, d = _shape(q if k is None or q is not None else k, "q" if q is not None else "k", 3)
+    n_q = n_k = P = q_stride = k_stride = page_stride = 0
+    q_p = qg_p = qo_p = k_p = kg_p = ko_p = kp_p = kc_p = None
     if q is not None:
         if q_out is None:
             raise ValueError("q needs q_out")
-        _arg(q, "q", _BF16, (T, None, d), dev, rows=True)
-        n_q = q.shape[1]
-        _arg(q_out, "q_out", _BF16, (T, n_q, d), dev)
+        shape = _shape(q, "q", 3)
+        n_q = shape[1]
+        q_p, q_stride = _rows(q, "q", _BF16, (T, n_q, d), dev)
+        qo_p = _dense(q_out, "q_out", _BF16, shape, dev)
+        if q_gain is not None:
+            qg_p = _dense(q_gain, "q_gain", _BF16, (d,), dev)
     if k is not None:
         if k_out is None and k_pool is None:
             raise ValueError("k needs k_out or k_pool")
-        _arg(k, "k", _BF16, (T, None, d), dev, rows=True)
-        n_k = k.shape[1]
+        shape = _shape(k, "k", 3)
+        n_k = shape[1]
+        k_p, k_stride = _rows(k, "k", _BF16, (T, n_k, d), dev)
+        if k_gain is not None:
+            kg_p = _dense(k_gain, "k_gain", _BF16, (d,), dev)
         if k_out is not None:
-            _arg(k_out, "k_out", _BF16, (T, n_k, d), dev)
+            ko_p = _dense(k_out, "k_out", _BF16, shape, dev)
         if k_pool is not None:
             if k_cell is None:
                 raise ValueError("k_pool needs k_cell")
-            _arg(k_pool, "k_pool", _BF16, (None, 64, n_k * d), dev, rows=True)
-            _arg(k_cell, "k_cell", "int32", (T,), dev)
-    for g, name in ((q_gain, "q_gain"), (k_gain, "k_gain")):
-        if g is not None:
-            _arg(g, name, _BF16, (d,), dev)
-    P = 0 if k_pool is None else k_pool.shape[0]
-    _check(lib().fm_qk_norm_rope(_ptr(pos), T, d, rope_dim, cfg["rope_base"], cfg["rope_factor"], cfg["rope_orig_len"],
-                                 cfg["rope_beta_fast"], cfg["rope_beta_slow"], float(eps), _ptr(q),
-                                 0 if q is None else _stride0(q, n_q * d), n_q, _ptr(q_gain), _ptr(q_out), _ptr(k),
-                                 0 if k is None else _stride0(k, n_k * d), n_k, _ptr(k_gain), _ptr(k_out),
-                                 _ptr(k_pool), P, 64 * n_k * d if P == 0 else _stride0(k_pool, 64 * n_k * d),
-                                 _ptr(k_cell), _stream(stream)))
+            P = k_pool.shape[0]
+            kp_p, page_stride = _rows(k_pool, "k_pool", _BF16, (P, 64, n_k * d), dev)
+            kc_p = _dense(k_cell, "k_cell", _I32T, (T,), dev)
+    st = lib().fm_qk_norm_rope(_dense(pos, "pos", _I64T, (T,), dev), T, d, rope_dim, rope_base, rope_factor,
+                               rope_orig_len, rope_beta_fast, rope_beta_slow, eps, q_p, q_stride, n_q, qg_p, qo_p, k_p,
+                               k_stride, n_k, kg_p, ko_p, kp_p, P, page_stride, kc_p, _stream(stream))
+    if st:
+        _check(st)
 
 
 def fm_csa_attn_workspace(T: int, n_h: int) -> int:
     return lib().fm_csa_attn_workspace(T, n_h)
 
 
-def _csa_attn_args(q, kv_pool, page_table, pos, out, seq, window, n_sink, cell_pool, cells, sink_logit, scale, lse_out):
-    dev = _current(q, "q")
-    T, n_h, d = q.shape
-    _arg(q, "q", _BF16, (T, n_h, d), dev)
-    _arg(kv_pool, "kv_pool", _BF16, (None, 64, d), dev, rows=True)
-    _arg(page_table, "page_table", "int32", (None, None), dev)
-    _arg(pos, "pos", "int64", (T,), dev)
-    _arg(out, "out", _BF16, (T, n_h, d), dev)
+def _csa_attn(tree, q, kv_pool, page_table, pos, out, window, n_sink, seq, cell_pool, cells, sink_logit, scale, lse_out,
+              workspace, stream):
+    dev = _device(q, "q")
+    shape = _shape(q, "q", 3)
+    T, n_h, d = shape
+    P = kv_pool.shape[0]
+    kv_p, kv_stride = _rows(kv_pool, "kv_pool", _BF16, (P, 64, d), dev)
+    B, R = _shape(page_table, "page_table", 2)
+    seq_p = sink_p = lse_p = cp_p = cells_p = None
+    k = Pc = 0
+    cp_stride = 64 * d
     if seq is not None:
-        _arg(seq, "seq", "int32", (T,), dev)
-    if (cell_pool is None) != (cells is None):
-        raise ValueError("cell_pool and cells go together")
-    k = 0
+        seq_p = _dense(seq, "seq", _I32T, (T,), dev)
     if cells is not None:
-        _arg(cell_pool, "cell_pool", _BF16, (None, 64, d), dev, rows=True)
-        _arg(cells, "cells", "int32", (T, None), dev)
-        k = cells.shape[1]
+        if cell_pool is None:
+            raise ValueError("cells needs cell_pool")
+        k = _shape(cells, "cells", 2)[1]
+        Pc = cell_pool.shape[0]
+        cp_p, cp_stride = _rows(cell_pool, "cell_pool", _BF16, (Pc, 64, d), dev)
+        cells_p = _dense(cells, "cells", _I32T, (T, k), dev)
+    elif cell_pool is not None:
+        raise ValueError("cell_pool needs cells")
     if sink_logit is not None:
-        _arg(sink_logit, "sink_logit", "float32", (n_h,), dev)
+        sink_p = _dense(sink_logit, "sink_logit", _F32T, (n_h,), dev)
     if lse_out is not None:
-        _arg(lse_out, "lse_out", "float32", (T, n_h), dev)
-    page = 64 * d
-    return (_ptr(q), T, n_h, d, _ptr(kv_pool), kv_pool.shape[0], _stride0(kv_pool, page), _ptr(page_table),
-            page_table.shape[0], page_table.shape[1], _ptr(seq), _ptr(pos), int(window), n_sink, _ptr(cell_pool),
-            0 if cells is None else cell_pool.shape[0], page if cells is None else _stride0(cell_pool, page),
-            _ptr(cells), k, _ptr(sink_logit), float(d ** -0.5 if scale is None else scale))
-
-
-def _workspace(workspace, dev):
-    if workspace is None:
-        return None, 0
-    _arg(workspace, "workspace", "uint8", (None,), dev)
-    return _ptr(workspace) or None, workspace.numel()
+        lse_p = _dense(lse_out, "lse_out", _F32T, (T, n_h), dev)
+    ws_p, ws_bytes = None, 0
+    if workspace is not None:
+        ws_bytes = workspace.shape[0]
+        ws_p = _dense(workspace, "workspace", _U8T, (ws_bytes,), dev) or None
+    args = (_dense(q, "q", _BF16, shape, dev), T, n_h, d, kv_p, P, kv_stride,
+            _dense(page_table, "page_table", _I32T, (B, R), dev), B, R, seq_p, _dense(pos, "pos", _I64T, (T,), dev),
+            window, n_sink, cp_p, Pc, cp_stride, cells_p, k, sink_p, d ** -0.5 if scale is None else scale)
+    out_p = _dense(out, "out", _BF16, shape, dev)
+    if tree is None:
+        st = lib().fm_csa_attn(*args, out_p, lse_p, ws_p, ws_bytes, _stream(stream))
+    else:
+        tree_mask, tree_base = tree
+        words = _shape(tree_mask, "tree_mask", 2)[1]
+        st = lib().fm_csa_attn_tree(*args, _dense(tree_mask, "tree_mask", _BITS, (T, words), dev), words,
+                                    _dense(tree_base, "tree_base", _I64T, (B,), dev), out_p, lse_p, ws_p, ws_bytes,
+                                    _stream(stream))
+    if st:
+        _check(st)
 
 
 def fm_csa_attn(q, kv_pool, page_table, pos, out, window: int, n_sink: int = 0, seq=None, cell_pool=None, cells=None,
@@ -512,11 +558,10 @@ def fm_csa_attn(q, kv_pool, page_table, pos, out, window: int, n_sink: int = 0, 
     [B,R] int32, pos [T] int64, seq [T] int32 (None: token t is row t), cells
     [T,k] int32 rows of cell_pool [Pc,64,512] (both None: none), sink_logit
     [n_h] fp32 or None, scale (None: 512 ** -0.5) -> out [T,n_h,512] bf16,
-    lse_out [T,n_h] fp32 or None; workspace >= fm_csa_attn_workspace(T, n_h)."""
-    args = _csa_attn_args(q, kv_pool, page_table, pos, out, seq, window, n_sink, cell_pool, cells, sink_logit, scale,
-                          lse_out)
-    ws, ws_bytes = _workspace(workspace, q.device)
-    _check(lib().fm_csa_attn(*args, _ptr(out), _ptr(lse_out), ws, ws_bytes, _stream(stream)))
+    lse_out [T,n_h] fp32 or None; workspace uint8 [>= fm_csa_attn_workspace(T,
+    n_h)]."""
+    _csa_attn(None, q, kv_pool, page_table, pos, out, window, n_sink, seq, cell_pool, cells, sink_logit, scale, lse_out,
+              workspace, stream)
 
 
 def fm_csa_attn_tree(q, kv_pool, page_table, pos, out, window: int, tree_mask, tree_base, n_sink: int = 0, seq=None,
@@ -525,10 +570,5 @@ def fm_csa_attn_tree(q, kv_pool, page_table, pos, out, window: int, tree_mask, t
     """fm_csa_attn for drafted tokens: sequence b's drafted token i is in cache
     slot tree_base[b] + i (tree_base [B] int64); tree_mask [T, words] int32 or
     uint32 has bit i & 31 of word i >> 5 set where token t sees it."""
-    args = _csa_attn_args(q, kv_pool, page_table, pos, out, seq, window, n_sink, cell_pool, cells, sink_logit, scale,
-                          lse_out)
-    _arg(tree_mask, "tree_mask", ("int32", "uint32"), (q.shape[0], None), q.device)
-    _arg(tree_base, "tree_base", "int64", (page_table.shape[0],), q.device)
-    ws, ws_bytes = _workspace(workspace, q.device)
-    _check(lib().fm_csa_attn_tree(*args, _ptr(tree_mask), tree_mask.shape[1], _ptr(tree_base), _ptr(out),
-                                  _ptr(lse_out), ws, ws_bytes, _stream(stream)))
+    _csa_attn((tree_mask, tree_base), q, kv_pool, page_table, pos, out, window, n_sink, seq, cell_pool, cells, sink_logit,
+              scale, lse_out, workspace, stream)

@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_slot;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // csa_merge_kernel may get ready: it waits
   const int n_mine = (p.items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
 
   if (warp == 1) {
@@ -911,6 +912,7 @@ __global__ void __launch_bounds__(128) csa_merge_kernel(const __grid_constant__ 
   const int h = (int)(th % p.n_h), hl = h % kHeadsPerItem;
   const int64_t t = th / p.n_h;
   const int64_t part0 = (t * p.head_blocks + h / kHeadsPerItem) * p.splits;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the partial results
   float top = -INFINITY;
   for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_ml[(part0 + s) * kHeadsPerItem + hl].x);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -955,7 +957,7 @@ fm_status launch_attn(AttnParams& p, const uint16_t* q, int sms, void* workspace
   // tiles that a token can have at most
   const int64_t held = (int64_t)p.R * kPage;
   const int64_t slots = (p.window < held ? p.window : held) + (p.n_sink < held ? p.n_sink : held) + p.k +
-                        (p.tree_mask != nullptr ? 32 * p.tree_words : 0) + 12;
+                        (p.tree_mask != nullptr ? 32 * p.tree_words : 0);
   const int64_t max_tiles = (slots + kTileKeys - 1) / kTileKeys;
   int64_t splits = items <= kMaxParts / 2 ? (sms < kMaxParts ? sms : kMaxParts) / items : 1;
   if (splits > max_tiles) splits = max_tiles;
@@ -979,8 +981,17 @@ fm_status launch_attn(AttnParams& p, const uint16_t* q, int sms, void* workspace
   if ((e = cudaGetLastError()) != cudaSuccess)
     return set_error(FM_ERR_CUDA, "fm_csa_attn: launch: %s", cudaGetErrorString(e));
   if (p.splits > 1) {
-    csa_merge_kernel<<<(unsigned)((int64_t)p.T * p.n_h), 128, 0, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess)
+    // programmatic dependent launch: the launch overlaps the kernel before it
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)p.T * p.n_h));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, csa_merge_kernel, (const AttnParams)p)) != cudaSuccess)
       return set_error(FM_ERR_CUDA, "fm_csa_attn: merge launch: %s", cudaGetErrorString(e));
   }
   return FM_OK;

@@ -70,42 +70,66 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
   const int row_end = min(rows, (chunk + 1) * p.rows_per_chunk);
   const int nvec = p.d >> 3;
 
-  // (cos, sin) of the lane's pairs; c = 1, s = 0 before the rotated part
-  float cs[VPL][4], sn[VPL][4];
-  bool turns[VPL];
-  const uint64_t position = (uint64_t)__ldg(p.pos + t);
+  // The warp's first row is on its way before anything else is done.
+  const int first = chunk * p.rows_per_chunk + warp * kRowsPerWarp + lane / LPR;
+  constexpr int kStep = kWarps * kRowsPerWarp;
+  uint4 next[VPL];
+  auto fetch = [&](int r) {
+    const uint16_t* src = r < p.n_q ? p.q + t * p.q_stride_t + (int64_t)r * p.d
+                                    : p.k + t * p.k_stride_t + (int64_t)(r - p.n_q) * p.d;
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int e0 = 8 * (l + j * LPR);
-    turns[j] = e0 + 8 > p.rope_start && e0 < p.d;
+    for (int j = 0; j < VPL; ++j) {
+      const int v = l + j * LPR;
+      next[j] = make_uint4(0, 0, 0, 0);
+      if (r < row_end && v < nvec) next[j] = *reinterpret_cast<const uint4*>(src + 8 * v);
+    }
+  };
+  fetch(first);
+
+  // (cos, sin) of the lane's pairs; c = 1, s = 0 before the rotated part.  Lane i
+  // works out pairs i, i + 32, ..., and the ones it needs come by shuffle.
+  float cs[VPL][4], sn[VPL][4];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       cs[j][i] = 1.f;
       sn[j][i] = 0.f;
-      const int e = e0 + 2 * i;
-      if (e >= p.rope_start && e < p.d) {
-        const uint64_t phase = position * p.turn[(e - p.rope_start) >> 1];
-        // the signed top word counts half turns in units of 2^-31
-        sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &sn[j][i], &cs[j][i]);
-      }
     }
+  const int pairs = (p.d - p.rope_start) >> 1;
+  const uint64_t position = (uint64_t)__ldg(p.pos + t);
+  for (int base = 0; base < pairs; base += 32) {
+    float c = 1.f, s = 0.f;
+    if (base + lane < pairs) {
+      const uint64_t phase = position * p.turn[base + lane];
+      // the signed top word counts half turns in units of 2^-31
+      sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &s, &c);
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = 8 * (l + j * LPR) + 2 * i - p.rope_start;  // even
+        const int pair = (e >> 1) - base;
+        const float cc = __shfl_sync(0xffffffffu, c, pair & 31), ss = __shfl_sync(0xffffffffu, s, pair & 31);
+        if (e >= 0 && pair >= 0 && pair < 32) {
+          cs[j][i] = cc;
+          sn[j][i] = ss;
+        }
+      }
   }
 
-  for (int r0 = chunk * p.rows_per_chunk + warp * kRowsPerWarp; r0 < row_end; r0 += kWarps * kRowsPerWarp) {
+  for (int r0 = first - lane / LPR; r0 < row_end; r0 += kStep) {
     const int r = r0 + lane / LPR;
     const bool live = r < row_end;
     const bool is_q = r < p.n_q;
     const int head = is_q ? r : r - p.n_q;
-    const uint16_t* src = is_q ? p.q + t * p.q_stride_t : p.k + t * p.k_stride_t;
     const uint16_t* gain = is_q ? p.q_gain : p.k_gain;
-    src += (int64_t)head * p.d;
     uint4 x[VPL];
     float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      const int v = l + j * LPR;
-      x[j] = make_uint4(0, 0, 0, 0);
-      if (live && v < nvec) x[j] = *reinterpret_cast<const uint4*>(src + 8 * v);
+      x[j] = next[j];
       const uint32_t u[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -113,6 +137,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
         ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
       }
     }
+    fetch(r + kStep);
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if (!live) continue;
@@ -145,9 +170,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
         const float2 f = unpack2(u[i]), gg = unpack2(w[i]);
         const float a = f.x * inv * gg.x, b = f.y * inv * gg.y;
         // the unrotated part is written as it is: 0 * inf would make it NaN
-        y[i] = turns[j] && 8 * v + 2 * i >= p.rope_start
-                   ? pack2(a * cs[j][i] - b * sn[j][i], a * sn[j][i] + b * cs[j][i])
-                   : pack2(a, b);
+        y[i] = 8 * v + 2 * i >= p.rope_start ? pack2(a * cs[j][i] - b * sn[j][i], a * sn[j][i] + b * cs[j][i])
+                                             : pack2(a, b);
       }
       const uint4 o = make_uint4(y[0], y[1], y[2], y[3]);
       if (dst0 != nullptr) *reinterpret_cast<uint4*>(dst0 + 8 * v) = o;
