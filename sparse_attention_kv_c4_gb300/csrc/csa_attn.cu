@@ -27,10 +27,15 @@
 // TMEM: O^T 4 x 64 columns, two S buffers of 64.  The output is kept transposed
 // (rows = elements) because 64 rows of heads x 512 columns would fill TMEM.
 //
-// Few tokens: the keys of an item are split over several CTAs, which write
-// unnormalised fp32 outputs with their maximum and sum; csa_merge_kernel joins
-// them in a fixed order.
+// Few tokens: the keys of an item are split over several CTAs.  Up to eight of
+// them are a cluster and join their outputs through distributed shared memory:
+// each CTA scales its own by its share of the common softmax and sends every
+// other one that one's slice of the 512 elements.  More than eight (few tokens
+// with long key lists) write unnormalised fp32 outputs with their maximum and
+// sum, and csa_merge_kernel joins those.  Both in a fixed order.
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "fm_common.cuh"
 #include "fm_internal.h"
@@ -58,9 +63,10 @@ constexpr int kKeysPerProducer = kTileKeys / kProducerWarps;
 constexpr int kTmemCols = 512;                  // allocations are powers of two
 constexpr int kSCol = 256;                      // the S buffers behind O^T's 256 columns
 constexpr int kInfoSlots = 4;
-constexpr int kInfoReaders = 1 + 2 + kSoftmaxWarps + 4;       // q loader, issuers, softmax and epilogue warps
+constexpr int kInfoReaders = 2 + kSoftmaxWarps + 4;           // issuers, softmax and epilogue warps
 constexpr int kKvArrivals = 33 * kProducerWarps;              // the producers' copies, and their first lanes
 constexpr int kMaxParts = 256;                  // partial results of one call
+constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
@@ -84,6 +90,7 @@ struct AttnParams {
   int64_t cell_limit;                    // Pc * 64
   int T, n_h, P, B, R, k, n_sink, tree_words;
   int head_blocks, splits, items;        // items = T * head_blocks * splits
+  int cluster;                           // the splits of an item are a cluster
   float scale;
 };
 
@@ -95,10 +102,8 @@ struct TokenKeys {
   int n_first, n_win, n_tree;
 };
 
-FM_DEV TokenKeys token_keys(const AttnParams& p, int64_t t) {
+FM_DEV TokenKeys token_keys(const AttnParams& p, int64_t b, int64_t pos) {
   TokenKeys r = {0, 0, -1, 0, 0, 0};
-  const int64_t b = p.seq != nullptr ? p.seq[t] : t;
-  const int64_t pos = p.pos[t];
   if (b < 0 || pos < 0) return r;
   if (b >= p.B) {
     atomicOr(p.status, FM_DEV_PAGE_RANGE);
@@ -299,6 +304,77 @@ constexpr int kSmemBytes = kQBytes + kPairs * kPairBytes + 2 * kPBytes + (int)si
 static_assert(kSmemBytes <= 232448, "227 KB of shared memory to a CTA");
 static_assert(offsetof(Shared, rows) % 16 == 0, "vector accesses");
 
+FM_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+FM_DEV uint32_t in_cta(uint32_t smem_addr, uint32_t rank) {  // the same place in another CTA of the cluster
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
+  return a;
+}
+
+// The end of an item whose splits are a cluster, by all threads of its CTAs.
+// CTA r writes elements r * 512 / splits .. of the output; `buf` (the idle ring,
+// the same in every CTA) takes the slices of all CTAs: [split][64 heads][512 / splits].
+FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, uint32_t tmem) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rank = (int)blockIdx.x % p.splits, th = (int)blockIdx.x / p.splits;
+  const int t = th / p.head_blocks, h0 = th % p.head_blocks * kHeadsPerItem;
+  const int heads = min(kHeadsPerItem, p.n_h - h0);
+  const int slice = kWidth / p.splits;
+  cluster_sync();  // every CTA is done with its ring, and its maxima and sums are in place
+  if (threadIdx.x < kHeadsPerItem) {
+    const int h = threadIdx.x;
+    const uint32_t at = smem_u32(&sh.stat[h]);
+    float2 ml[kMaxCluster];
+    float top = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s) {
+      ml[s] = make_float2(-INFINITY, 0.f);
+      if (s < p.splits)
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml[s].x), "=f"(ml[s].y) : "r"(in_cta(at, s)));
+      top = fmaxf(top, ml[s].x);
+    }
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s)
+      if (ml[s].y != 0.f) total = fmaf(ml[s].y, exp2_fast(ml[s].x - top), total);
+    const float sink = p.sink_logit != nullptr && h < heads ? __ldg(p.sink_logit + h0 + h) * kLog2e : -INFINITY;
+    const float2 mine = sh.stat[h];
+    sh.rescale[h] = mine.y == 0.f ? 0.f : exp2_fast(mine.x - top) / (total + exp2_fast(sink - top));
+    if (rank == 0 && p.lse != nullptr && h < heads)
+      p.lse[(int64_t)t * p.n_h + h0 + h] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+  }
+  __syncthreads();
+  // 32 heads x 32 elements at a time, scaled, to the CTA whose slice they are in
+  for (int x = warp >> 2; x < 8; x += kThreads / 128) {
+    const int d = (x >> 1) * 128 + (warp & 3) * 32, to = d / slice;
+    uint32_t o[32];
+    tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + 32 * x, o);
+    tmem_ld_wait();
+    const uint32_t dst = in_cta(smem_u32(buf + (rank * kHeadsPerItem + (x & 1) * 32) * slice + d % slice + lane), to);
+#pragma unroll
+    for (int h = 0; h < 32; ++h)
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + (uint32_t)(h * slice * 4)),
+                   "f"(__uint_as_float(o[h]) * sh.rescale[(x & 1) * 32 + h])
+                   : "memory");
+  }
+  cluster_sync();
+  const int per_head = slice / 4;
+  for (int i = threadIdx.x; i < heads * per_head; i += kThreads) {
+    const int h = i / per_head, d = i % per_head * 4;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < p.splits; ++s) {
+      const float4 v = *reinterpret_cast<const float4*>(buf + (s * kHeadsPerItem + h) * slice + d);
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+    const uint2 v = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+    *reinterpret_cast<uint2*>(p.out + ((int64_t)t * p.n_h + h0 + h) * kWidth + rank * slice + d) = v;
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     csa_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -369,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int item = (int)blockIdx.x + i * (int)gridDim.x;
       const int split = item % p.splits, th = item / p.splits;
       const int t = th / p.head_blocks;
+      const int64_t b = p.seq != nullptr ? __ldg(p.seq + t) : t, pos = __ldg(p.pos + t);
       // listed cells up to the last one that is not empty
       int last = -1;
       const int32_t* cells = p.cells + (int64_t)t * p.k;
@@ -376,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = lane; c < p.k; c += 32)
         if (__ldg(cells + c) >= 0) last = c;
       const int n_cells = __reduce_max_sync(0xffffffffu, last) + 1;
-      const TokenKeys tk = token_keys(p, t);
+      const TokenKeys tk = token_keys(p, b, pos);
       const int end_first = n_cells + tk.n_first, end_win = end_first + tk.n_win, end = end_win + tk.n_tree;
       const int64_t tiles = (end + kTileKeys - 1) / kTileKeys;
       int tile = (int)(tiles * split / p.splits), tile_end = (int)(tiles * (split + 1) / p.splits);
@@ -386,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!warp_wait(&sh.info_empty[slot], ((i / kInfoSlots) & 1) ^ 1, abort, status)) break;
       if (lane == 0) {
-        sh.info[slot] = ItemInfo{t, th % p.head_blocks, p.splits > 1 ? item : -1, tile_end - tile};
+        sh.info[slot] = ItemInfo{t, th % p.head_blocks, p.splits > 1 && !p.cluster ? item : -1, tile_end - tile};
         mbar_arrive(&sh.info_full[slot]);
         const int h0 = th % p.head_blocks * kHeadsPerItem;
         prefetch_l2(p.q + ((int64_t)t * p.n_h + h0) * kWidth, min(kHeadsPerItem, p.n_h - h0) * kWidth * 2);
@@ -460,11 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < n_mine && ok; ++i) {
-      const int slot = i % kInfoSlots;
-      if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
-      const int t = sh.info[slot].t, h0 = sh.info[slot].head_block * kHeadsPerItem;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+      const int th = ((int)blockIdx.x + i * (int)gridDim.x) / p.splits;
+      const int t = th / p.head_blocks, h0 = th % p.head_blocks * kHeadsPerItem;
 #pragma unroll 1
       for (int j = 0; j < kPairsPerTile; ++j) {
         if (!(ok = warp_wait(&sh.q_empty[j], (i & 1) ^ 1, abort, status))) break;
@@ -822,6 +896,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = 0; r < 2; ++r)
         if (p.sink_logit != nullptr && lane + 32 * r < heads) sink[r] = __ldg(p.sink_logit + h0 + lane + 32 * r) * kLog2e;
       if (!warp_wait(&sh.stat_full, i & 1, abort, status)) break;
+      if (p.cluster) {  // the whole CTA sees to it, below
+        (void)warp_wait(&sh.o_full, i & 1, abort, status);
+        break;
+      }
       const float2 stat[2] = {sh.stat[lane], sh.stat[lane + 32]};
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.stat_empty);
@@ -902,6 +980,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.cluster) join_cluster(p, sh, reinterpret_cast<float*>(ring), tmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
@@ -918,10 +1000,10 @@ __global__ void __launch_bounds__(128) csa_merge_kernel(const __grid_constant__ 
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
   const int d = 4 * threadIdx.x;
+#pragma unroll 8
   for (int s = 0; s < p.splits; ++s) {
     const float2 ml = p.part_ml[(part0 + s) * kHeadsPerItem + hl];
-    if (ml.y == 0.f) continue;  // a split without keys
-    const float w = exp2f(ml.x - top);
+    const float w = ml.y == 0.f ? 0.f : exp2_fast(ml.x - top);  // a split without keys holds zeros
     sum = fmaf(w, ml.y, sum);
     const float4 o = *reinterpret_cast<const float4*>(p.part_o + ((part0 + s) * kHeadsPerItem + hl) * kWidth + d);
     acc.x = fmaf(w, o.x, acc.x);
@@ -949,7 +1031,35 @@ size_t attn_workspace_bytes(int T, int n_h) {
   return (size_t)parts * kHeadsPerItem * (kWidth * sizeof(float) + sizeof(float2));
 }
 
+// Clusters of c CTAs of the attention kernel that fit the current device at once.
+// (Asked once per device and size: it does not change.)
+int max_clusters(int c) {
+  static std::atomic<int> known[64][kMaxCluster + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  std::atomic<int>* slot = dev < 64 ? &known[dev][c] : nullptr;
+  if (slot != nullptr && slot->load(std::memory_order_relaxed) > 0) return slot->load(std::memory_order_relaxed);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)c);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)c, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, csa_attn_kernel, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  if (slot != nullptr) slot->store(n, std::memory_order_relaxed);
+  return n;
+}
+
 fm_status launch_attn(AttnParams& p, const uint16_t* q, int sms, void* workspace, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(csa_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return set_error(FM_ERR_CUDA, "fm_csa_attn: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   p.head_blocks = head_blocks_of(p.n_h);
   const int64_t items = (int64_t)p.T * p.head_blocks;
   if (items * kMaxParts >= (int64_t(1) << 31))
@@ -959,9 +1069,21 @@ fm_status launch_attn(AttnParams& p, const uint16_t* q, int sms, void* workspace
   const int64_t slots = (p.window < held ? p.window : held) + (p.n_sink < held ? p.n_sink : held) + p.k +
                         (p.tree_mask != nullptr ? 32 * p.tree_words : 0);
   const int64_t max_tiles = (slots + kTileKeys - 1) / kTileKeys;
-  int64_t splits = items <= kMaxParts / 2 ? (sms < kMaxParts ? sms : kMaxParts) / items : 1;
-  if (splits > max_tiles) splits = max_tiles;
+  const int64_t free_sms = items <= kMaxParts / 2 ? (sms < kMaxParts ? sms : kMaxParts) / items : 1;
+  int64_t splits = free_sms < max_tiles ? free_sms : max_tiles;
   if (splits < 1) splits = 1;
+  p.cluster = 0;
+  if (splits > 1) {
+    // As a cluster where that costs a CTA at most eight tiles more than the split
+    // over all SMs: a tile is some 0.8 us, the partial results' way through
+    // memory and the second kernel some 7 us.
+    int c = kMaxCluster;
+    while (c > 2 && (c > splits || max_clusters(c) < items)) c /= 2;
+    if (c <= splits && (max_tiles + c - 1) / c <= (max_tiles + splits - 1) / splits + 8) {
+      p.cluster = 1;
+      splits = c;
+    }
+  }
   p.splits = (int)splits;
   p.items = (int)(items * splits);
   const size_t parts = (size_t)p.items;
@@ -974,22 +1096,27 @@ fm_status launch_attn(AttnParams& p, const uint16_t* q, int sms, void* workspace
   const uint32_t qb[3] = {64, kHeadsPerItem, 1};
   fm_status st = make_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != FM_OK) return st;
-  cudaError_t e = cudaFuncSetAttribute(csa_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return set_error(FM_ERR_CUDA, "fm_csa_attn: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-  const int grid = p.items < sms ? p.items : sms;
-  csa_attn_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tq, p);
-  if ((e = cudaGetLastError()) != cudaSuccess)
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)(p.cluster || p.items < sms ? p.items : sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  if (p.cluster) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)p.splits, 1, 1};
+    cfg.numAttrs = 1;
+  }
+  if ((e = cudaLaunchKernelEx(&cfg, csa_attn_kernel, tq, (const AttnParams)p)) != cudaSuccess)
     return set_error(FM_ERR_CUDA, "fm_csa_attn: launch: %s", cudaGetErrorString(e));
-  if (p.splits > 1) {
+  if (p.splits > 1 && !p.cluster) {
     // programmatic dependent launch: the launch overlaps the kernel before it
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)p.T * p.n_h));
     cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cfg.dynamicSmemBytes = 0;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, csa_merge_kernel, (const AttnParams)p)) != cudaSuccess)
       return set_error(FM_ERR_CUDA, "fm_csa_attn: merge launch: %s", cudaGetErrorString(e));
