@@ -296,7 +296,8 @@ struct Shared {
   ItemInfo info[kInfoSlots];
   alignas(16) uint64_t rows[2][kTileKeys];  // addresses: key 16 w + 2 c + x at 16 w + 8 x + c
   float2 stat[kHeadsPerItem];            // maximum in log2 units, sum of an item's heads
-  float rescale[kHeadsPerItem], top_half[2][kHeadsPerItem];
+  alignas(16) float rescale[kHeadsPerItem];
+  float top_half[2][kHeadsPerItem];
   uint32_t tmem_slot;
   int abort_flag;
 };
@@ -995,21 +996,47 @@ __global__ void __launch_bounds__(128) csa_merge_kernel(const __grid_constant__ 
   const int64_t t = th / p.n_h;
   const int64_t part0 = (t * p.head_blocks + h / kHeadsPerItem) * p.splits;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for the partial results
-  float top = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_ml[(part0 + s) * kHeadsPerItem + hl].x);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // the splits' weights, a thread each
+  __shared__ float weight[kMaxParts], warp_top[4], warp_sum[4];
+  static_assert(kMaxParts <= 2 * 128, "two splits to a thread");
+  const int tid = threadIdx.x, warp = tid / 32;
+  float2 ml[2] = {make_float2(-INFINITY, 0.f), make_float2(-INFINITY, 0.f)};
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    if (tid + 128 * x < p.splits) ml[x] = p.part_ml[(part0 + tid + 128 * x) * kHeadsPerItem + hl];
+  float top = fmaxf(ml[0].x, ml[1].x);
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (tid % 32 == 0) warp_top[warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(warp_top[0], warp_top[1]), fmaxf(warp_top[2], warp_top[3]));
   float sum = 0.f;
-  const int d = 4 * threadIdx.x;
-#pragma unroll 8
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = p.part_ml[(part0 + s) * kHeadsPerItem + hl];
-    const float w = ml.y == 0.f ? 0.f : exp2_fast(ml.x - top);  // a split without keys holds zeros
-    sum = fmaf(w, ml.y, sum);
-    const float4 o = *reinterpret_cast<const float4*>(p.part_o + ((part0 + s) * kHeadsPerItem + hl) * kWidth + d);
-    acc.x = fmaf(w, o.x, acc.x);
-    acc.y = fmaf(w, o.y, acc.y);
-    acc.z = fmaf(w, o.z, acc.z);
-    acc.w = fmaf(w, o.w, acc.w);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const float w = ml[x].y == 0.f ? 0.f : exp2_fast(ml[x].x - top);  // a split without keys holds zeros
+    sum = fmaf(w, ml[x].y, sum);
+    if (tid + 128 * x < kMaxParts) weight[tid + 128 * x] = w;
+  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (tid % 32 == 0) warp_sum[warp] = sum;
+  __syncthreads();
+  sum = warp_sum[0] + warp_sum[1] + warp_sum[2] + warp_sum[3];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int d = 4 * tid;
+  const float* from = p.part_o + (part0 * kHeadsPerItem + hl) * kWidth + d;
+  for (int s0 = 0; s0 < p.splits; s0 += 8) {
+    float4 o[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      o[s] = s0 + s < p.splits ? *reinterpret_cast<const float4*>(from + (int64_t)(s0 + s) * kHeadsPerItem * kWidth)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const float w = weight[(s0 + s) % kMaxParts];
+      acc.x = fmaf(w, o[s].x, acc.x);
+      acc.y = fmaf(w, o[s].y, acc.y);
+      acc.z = fmaf(w, o[s].z, acc.z);
+      acc.w = fmaf(w, o[s].w, acc.w);
+    }
   }
   float below = sum;
   if (p.sink_logit != nullptr) below += exp2f(fmaf(p.sink_logit[h], kLog2e, -top));
