@@ -8,24 +8,30 @@
 // unit of work is one token's block of 64 heads against tiles of 64 keys
 // (131 kFLOP per key of 1 KB).  A persistent CTA per SM walks its items (token,
 // head block, split of the keys):
-//   resolver    (warp 1)  each item's key ranges, and each tile's 64 pool rows
-//               and mask (a key that is none is row -1 and a zero bit)
-//   q loader    (warp 3)  the item's 64 query rows by TMA: eight SWIZZLE_128B
-//               chunks [64 heads x 64 elements] of 8 KB
-//   producers   (warps 16-19)  the rows by 16-byte cp.async, 16 keys to a warp,
-//               swizzled as TMA would (a TMA gather of four rows costs its warp
-//               some 90 cycles to issue, 128 of them a tile).  The ring holds
-//               nine pairs of chunks [64 keys x 64 elements], four pairs to a
-//               tile; a key that is none is filled with zeros without a read
+//   resolver    (warp 1)  each item's key ranges, and each tile's 64 row addresses
+//               and mask (a key that is none is a zero bit).  An item's first tile
+//               is its 64 query rows
+//   producers   (warps 16-19)  the rows by 16-byte cp.async, 16 rows to a warp,
+//               into SWIZZLE_128B chunks [64 rows x 64 elements] (a TMA gather of
+//               four rows costs its warp some 90 cycles to issue, 128 of them a
+//               tile).  The ring holds three tiles and is freed in quarters; a key
+//               that is none is filled with zeros without a read
 //   S issuer    (warp 0)  S = Q C^T: tcgen05 M64 N64, 32 steps of K16
 //   O issuer    (warp 2)  O^T += C^T P^T: M128 N64, four blocks of 128 elements x
 //               four steps of K16.  The cell tile is read twice from shared
 //               memory, K-major as keys and MN-major as values, and loaded once
 //   softmax     (warps 4-11)  S from TMEM, the running maximum and sum, P in
 //               bf16 to shared memory: 16 heads x 32 keys to a warp
-//   epilogue    (warps 12-15)  O^T from TMEM, times 1 / (sum + sink), to out
-// TMEM: O^T 4 x 64 columns, two S buffers of 64.  The output is kept transposed
-// (rows = elements) because 64 rows of heads x 512 columns would fill TMEM.
+//   epilogue    (warps 12-15)  O^T from TMEM, times 1 / (sum + sink), to out; and
+//               the next item's queries from the ring to their place
+// TMEM: O^T 4 x 64 columns, S 64, three quarters of Q 192.  The output is kept
+// transposed (rows = elements) because 64 rows of heads x 512 columns would fill
+// TMEM.
+// What bounds it: a tile's chain (copies, S, softmax, O) is some 5500 cycles, and the
+// ring holds three tiles; shared memory at 128 bytes a cycle: S reads 64 KB of
+// cells and 16 KB of queries, O 64 KB of cells and 32 KB of weights, the copies write
+// 64 KB, 1900 cycles a tile against 1024 + 512 of the tensor cores.  With all of Q
+// in shared memory the ring held 2.25 tiles.
 //
 // Few tokens: the keys of an item are split over several CTAs.  Up to eight of
 // them are a cluster and join their outputs through distributed shared memory:
@@ -53,15 +59,17 @@ constexpr int kTileKeys = 64;
 constexpr int kChunkBytes = 64 * 128;           // 64 rows x 64 elements
 constexpr int kPairBytes = 2 * kChunkBytes;
 constexpr int kPairsPerTile = kWidth / 128;     // 4
-constexpr int kPairs = 9;
-constexpr int kQBytes = kHeadsPerItem * kWidth * 2;
+constexpr int kTileSlots = 3;
+constexpr int kPairs = kTileSlots * kPairsPerTile;
+constexpr int kQBytes = kPairBytes;             // the first quarter of Q; the rest is in TMEM
 constexpr int kPBytes = kHeadsPerItem * kTileKeys * 2;
 constexpr int kThreads = 20 * 32;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kProducerWarps = 4;
 constexpr int kKeysPerProducer = kTileKeys / kProducerWarps;
 constexpr int kTmemCols = 512;                  // allocations are powers of two
-constexpr int kSCol = 256;                      // the S buffers behind O^T's 256 columns
+constexpr int kSCol = 256;                      // S behind O^T's 256 columns
+constexpr int kQCol = 320;                      // and three quarters of Q, 32 columns to a chunk of 64 elements
 constexpr int kInfoSlots = 4;
 constexpr int kInfoReaders = 2 + kSoftmaxWarps + 4;           // issuers, softmax and epilogue warps
 constexpr int kKvArrivals = 33 * kProducerWarps;              // the producers' copies, and their first lanes
@@ -133,16 +141,12 @@ FM_DEV TokenKeys token_keys(const AttnParams& p, int64_t b, int64_t pos) {
 struct ItemInfo {
   int t, head_block;
   int part;   // index of the partial result, -1 = whole
-  int tiles;  // at least one
+  int tiles;  // of keys, at least one; the tile of queries before them is not counted
 };
 
 // 16 bytes global -> shared, or 16 zero bytes where `bytes` is 0: nothing is read then.
 FM_DEV void cp_async16(uint32_t dst, uint64_t src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// Towards L2 (16-byte aligned, a multiple of 16 bytes).
-FM_DEV void prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 // Arrive on `bar` when this thread's copies so far have landed.
 FM_DEV void cp_async_arrive(uint64_t* bar) {
@@ -150,14 +154,6 @@ FM_DEV void cp_async_arrive(uint64_t* bar) {
 }
 FM_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 FM_DEV void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-FM_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
 // 16 lanes x 32 columns: thread i gets, of columns 8j + 2 (i % 4) + {0, 1}, lane
 // i / 4 in r[4j], r[4j + 1] and lane i / 4 + 8 in r[4j + 2], r[4j + 3].
 FM_DEV void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
@@ -204,6 +200,9 @@ FM_DEV void store_8x8_x4_trans(uint32_t addr, uint32_t x0, uint32_t x1, uint32_t
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x0), "r"(x1),
                "r"(x2), "r"(x3)
                : "memory");
+}
+FM_DEV void store_shared_16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 FM_DEV uint4 load_shared_16(uint32_t addr) {
   uint4 v;
@@ -288,9 +287,9 @@ FM_DEV bool elect_one() {
 
 // What the roles share besides the tiles.
 struct Shared {
-  uint64_t kv_full[kPairs], kv_empty[kPairs];
-  uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
-  uint64_t q_full[kPairsPerTile], q_empty[kPairsPerTile], o_full, o_empty[kPairsPerTile], stat_full, stat_empty, stage_free[2];
+  uint64_t kv_full[kTileSlots], kv_empty[kPairs];
+  uint64_t s_full, s_empty, p_full[2], pv_done[2];
+  uint64_t q_full, q_empty, o_full, o_empty[kPairsPerTile], stat_full, stat_empty, stage_free[2];
   uint64_t info_full[kInfoSlots], info_empty[kInfoSlots], rows_full[2], rows_empty[2], drain[2];
   uint2 key_mask[8];                     // the resolver is up to four tiles ahead of the softmax
   ItemInfo info[kInfoSlots];
@@ -377,7 +376,7 @@ FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, uint32_t t
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    csa_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ AttnParams p) {
+    csa_attn_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* q_smem = smem;
   uint8_t* ring = smem + kQBytes;
@@ -392,25 +391,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kPairs; ++i) {
-      mbar_init(&sh.kv_full[i], kKvArrivals);
-      mbar_init(&sh.kv_empty[i], 1);
-    }
+    for (int i = 0; i < kTileSlots; ++i) mbar_init(&sh.kv_full[i], kKvArrivals);
+    for (int i = 0; i < kPairs; ++i) mbar_init(&sh.kv_empty[i], 1);
+    mbar_init(&sh.s_full, 2);
+    mbar_init(&sh.s_empty, kSoftmaxWarps);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.s_full[i], 2);
-      mbar_init(&sh.s_empty[i], kSoftmaxWarps);
       mbar_init(&sh.p_full[i], kSoftmaxWarps);
       mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.stage_free[i], 4);
     }
+    mbar_init(&sh.q_full, 4);
+    mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.o_full, 1);
     mbar_init(&sh.stat_full, 4);
     mbar_init(&sh.stat_empty, 4);
-    for (int i = 0; i < kPairsPerTile; ++i) {
-      mbar_init(&sh.q_full[i], 1);
-      mbar_init(&sh.q_empty[i], 1);
-      mbar_init(&sh.o_empty[i], 4);
-    }
+    for (int i = 0; i < kPairsPerTile; ++i) mbar_init(&sh.o_empty[i], 4);
     for (int i = 0; i < kInfoSlots; ++i) {
       mbar_init(&sh.info_full[i], 1);
       mbar_init(&sh.info_empty[i], kInfoReaders);
@@ -424,7 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1 && lane == 0) tma_prefetch(&tmap_q);
   if (warp == 0) {
     tmem_alloc(&sh.tmem_slot, kTmemCols);
     tmem_relinquish();
@@ -440,6 +434,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------- resolver ------------------------------
     bool ok = true;
     uint32_t g = 0;
+    // the addresses and the mask of the next tile: rows lane and lane + 32
+    auto publish = [&](const uint64_t (&row)[2], const bool (&seen)[2]) -> bool {
+      uint2 mask;
+      mask.x = __ballot_sync(0xffffffffu, seen[0]);
+      mask.y = __ballot_sync(0xffffffffu, seen[1]);
+      if (!warp_wait(&sh.rows_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status)) return false;
+      const int to = (lane >> 4) * 16 + (lane & 1) * 8 + ((lane & 15) >> 1);
+      sh.rows[g & 1][to] = row[0];
+      sh.rows[g & 1][32 + to] = row[1];
+      if (lane == 0) sh.key_mask[g & 7] = mask;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.rows_full[g & 1]);
+      ++g;
+      return true;
+    };
 #pragma unroll 1
     for (int i = 0; i < n_mine && ok; ++i) {
       const int slot = i % kInfoSlots;
@@ -447,6 +456,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int split = item % p.splits, th = item / p.splits;
       const int t = th / p.head_blocks;
       const int64_t b = p.seq != nullptr ? __ldg(p.seq + t) : t, pos = __ldg(p.pos + t);
+      // the tile of queries
+      uint64_t row[2];
+      bool seen[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int h = th % p.head_blocks * kHeadsPerItem + 32 * x + lane;
+        seen[x] = h < p.n_h;
+        row[x] = reinterpret_cast<uint64_t>(p.q + ((int64_t)t * p.n_h + (seen[x] ? h : 0)) * kWidth);
+      }
+      if (!(ok = publish(row, seen))) break;
       // listed cells up to the last one that is not empty
       int last = -1;
       const int32_t* cells = p.cells + (int64_t)t * p.k;
@@ -466,8 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         sh.info[slot] = ItemInfo{t, th % p.head_blocks, p.splits > 1 && !p.cluster ? item : -1, tile_end - tile};
         mbar_arrive(&sh.info_full[slot]);
-        const int h0 = th % p.head_blocks * kHeadsPerItem;
-        prefetch_l2(p.q + ((int64_t)t * p.n_h + h0) * kWidth, min(kHeadsPerItem, p.n_h - h0) * kWidth * 2);
       }
       const int tile_begin = tile;
       // The keys' indexes are read a tile ahead of their use.  Lane l resolves
@@ -503,8 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       raw[0] = raw[1] = -1;
 #pragma unroll 1
       for (--tile; tile < tile_end; ++tile) {  // the first pass only fetches
-        uint64_t row[2];
-        bool seen[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const bool cell = tile * kTileKeys + 32 * x + lane < n_cells;
@@ -516,45 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           row[x] = seen[x] ? reinterpret_cast<uint64_t>((cell ? p.cell_pool : p.kv_pool) + r * kWidth)
                            : reinterpret_cast<uint64_t>(p.pos);
         }
-        uint2 mask;
-        mask.x = __ballot_sync(0xffffffffu, seen[0]);
-        mask.y = __ballot_sync(0xffffffffu, seen[1]);
         if (tile + 1 < tile_end) fetch(tile + 1);
-        if (tile < tile_begin) continue;
-        if (!(ok = warp_wait(&sh.rows_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
-        const int to = (lane >> 4) * 16 + (lane & 1) * 8 + ((lane & 15) >> 1);
-        sh.rows[g & 1][to] = row[0];
-        sh.rows[g & 1][32 + to] = row[1];
-        if (lane == 0) sh.key_mask[g & 7] = mask;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.rows_full[g & 1]);
-        ++g;
+        if (tile >= tile_begin && !(ok = publish(row, seen))) break;
       }
     }
-  } else if (warp == 3) {
-    // ------------------------------- q loader -------------------------------
-    // Pair by pair, as the last tile of the item before is done with it.
-    int loaded = 0;
-    bool ok = true;
-#pragma unroll 1
-    for (int i = 0; i < n_mine && ok; ++i) {
-      const int th = ((int)blockIdx.x + i * (int)gridDim.x) / p.splits;
-      const int t = th / p.head_blocks, h0 = th % p.head_blocks * kHeadsPerItem;
-#pragma unroll 1
-      for (int j = 0; j < kPairsPerTile; ++j) {
-        if (!(ok = warp_wait(&sh.q_empty[j], (i & 1) ^ 1, abort, status))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&sh.q_full[j], kPairBytes);
-          tma_load_3d(q_smem + j * kPairBytes, &tmap_q, &sh.q_full[j], 128 * j, h0, t);
-          tma_load_3d(q_smem + j * kPairBytes + kChunkBytes, &tmap_q, &sh.q_full[j], 128 * j + 64, h0, t);
-        }
-        __syncwarp();
-        ++loaded;
-      }
-    }
-    if (lane == 0 && *abort)  // let copies in flight land before the CTA exits
-      for (int x = loaded > kPairsPerTile ? loaded - kPairsPerTile : 0; x < loaded; ++x)
-        mbar_wait_drain(&sh.q_full[x % kPairsPerTile], (x / kPairsPerTile) & 1);
   } else if (warp >= 16) {
     // ------------------------------- producers ------------------------------
     // Producer w takes the tile's keys 16 w .. 16 w + 15.  Copy c of a pair moves
@@ -564,6 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_dst = smem_u32(ring) + me * kKeysPerProducer * 128 + (unit >> 3) * kChunkBytes + hi * 128 +
                               (((unit & 7) ^ hi) << 4);
     uint32_t at = 0, at_phase = 1, g = 0;
+    int tile_slot = 0;
     int i = 0, left = 0;  // the current item, its tiles not yet copied
     uint64_t src[8];
     uint32_t valid = 0;   // bit 2 c: copy c reads
@@ -587,8 +568,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(&sh.rows_full[g & 1], (g >> 1) & 1, abort, status)) break;
         take_rows(g);
       }
-      if (left == 0) left = sh.info[i % kInfoSlots].tiles;  // an item's rows come after its info
-      if (--left == 0) ++i;
+      if (left == 0) {  // the item's tile of queries: its info may come later
+        left = -1;
+      } else {
+        if (left < 0) left = sh.info[i % kInfoSlots].tiles;
+        if (--left == 0) ++i;
+      }
       taken = false;
       bool ok = true;
       uint64_t from[8];
@@ -611,14 +596,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           cp_async16((dst ^ ((2 * c & 7) << 4)) + c * 256, from[c], (reads >> (2 * c) & 1u) << 4);
           from[c] += 256;
         }
-        cp_async_arrive(&sh.kv_full[at]);
-        if (lane == 0) mbar_arrive(&sh.kv_full[at]);  // releases the mask
         if (++at == (uint32_t)kPairs) {
           at = 0;
           at_phase ^= 1;
         }
       }
       if (!ok) break;
+      cp_async_arrive(&sh.kv_full[tile_slot]);
+      if (lane == 0) mbar_arrive(&sh.kv_full[tile_slot]);  // passes the mask on
+      if (++tile_slot == kTileSlots) tile_slot = 0;
     }
     cp_async_wait_all();
   } else if (warp == 0) {
@@ -627,7 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc = idesc_bf16_f32(64, kTileKeys);
     const uint64_t q_desc = sdesc_sw128(smem_u32(q_smem));
     const uint64_t k_desc = sdesc_sw128(smem_u32(ring));
-    uint32_t g = 0, at = 0, at_phase = 0;
+    uint32_t g = 0;                // key tiles
+    uint32_t at = 0, at_phase = 0; // the current tile's slot in the ring, query tiles among them
     bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < n_mine && ok; ++i) {
@@ -636,34 +623,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tiles = sh.info[slot].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+      if (!warp_wait(&sh.q_full, i & 1, abort, status)) break;
+      if (one)  // they have left the ring
+        for (int j = 0; j < kPairsPerTile; ++j) mbar_arrive(&sh.kv_empty[at * kPairsPerTile + j]);
 #pragma unroll 1
-      for (int tile = 0; tile < tiles && ok; ++tile, ++g) {
-        if (!(ok = warp_wait(&sh.s_empty[g & 1], ((g >> 1) & 1) ^ 1, abort, status))) break;
-        const uint32_t d = tmem + kSCol + (g & 1) * kTileKeys;
+      for (int tile = 0; tile < tiles; ++tile, ++g) {
+        if (++at == kTileSlots) {
+          at = 0;
+          at_phase ^= 1;
+        }
+        // (one wait to a tile: four of them cost the issuer more than the later start)
+        if (!(ok = warp_wait(&sh.kv_full[at], at_phase, abort, status))) break;
+        if (!(ok = warp_wait(&sh.s_empty, (g & 1) ^ 1, abort, status))) break;
+        fence_proxy_async();  // the copies were written through the generic proxy
+        tc_fence_after();
+        uint64_t b = k_desc + (uint64_t)(at * (kPairsPerTile * kPairBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t o = (uint64_t)((kk >> 2) * (kChunkBytes >> 4) + (kk & 3) * 2);
+          if (one) umma_bf16_ss(tmem + kSCol, q_desc + o, b + o, idesc, kk == 0 ? 0u : 1u);
+        }
+        uint32_t a = tmem + kQCol;
 #pragma unroll 1
-        for (int j = 0; j < kPairsPerTile; ++j) {
-          if (tile == 0 && !(ok = warp_wait(&sh.q_full[j], i & 1, abort, status))) break;
-          if (!(ok = warp_wait(&sh.kv_full[at], at_phase, abort, status))) break;
-          fence_proxy_async();  // the copies were written through the generic proxy
-          tc_fence_after();
-          const uint64_t a = q_desc + (uint64_t)(j * (kPairBytes >> 4));
-          const uint64_t b = k_desc + (uint64_t)(at * (kPairBytes >> 4));
+        for (int j = 1; j < kPairsPerTile; ++j) {
+          b += (uint64_t)(kPairBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint64_t o = (uint64_t)((kk >> 2) * (kChunkBytes >> 4) + (kk & 3) * 2);
-            if (one) umma_bf16_ss(d, a + o, b + o, idesc, kk == 0 ? (uint32_t)j : 1u);
+            if (one) umma_bf16_ts(tmem + kSCol, a + 8 * kk, b + o, idesc, 1u);
           }
-          if (tile == tiles - 1 && one) umma_commit(&sh.q_empty[j]);
-          if (++at == (uint32_t)kPairs) {
-            at = 0;
-            at_phase ^= 1;
-          }
+          a += 64;
         }
-        if (!ok) break;
         if (one) {
-          umma_commit(&sh.s_full[g & 1]);
-          mbar_arrive(&sh.s_full[g & 1]);  // passes the mask on
+          umma_commit(&sh.s_full);
+          mbar_arrive(&sh.s_full);  // passes the mask on
         }
+      }
+      if (ok && one) umma_commit(&sh.q_empty);
+      if (++at == kTileSlots) {  // the next item's queries
+        at = 0;
+        at_phase ^= 1;
       }
     }
     if (one) umma_commit(&sh.drain[0]);
@@ -683,6 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tiles = sh.info[slot].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+      at += kPairsPerTile;  // the tile of queries
+      if (at == (uint32_t)kPairs) at = 0;
 #pragma unroll 1
       for (int tile = 0; tile < tiles && ok; ++tile, ++g) {
         if (!(ok = warp_wait(&sh.p_full[g & 1], (g >> 1) & 1, abort, status))) break;
@@ -708,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (one) umma_commit(&sh.drain[1]);
     if (one) mbar_wait_drain(&sh.drain[1], 0);
-  } else if (warp < 4 + kSoftmaxWarps) {
+  } else if (warp >= 4 && warp < 4 + kSoftmaxWarps) {
     // ------------------------------- softmax --------------------------------
     // Warps quad and quad + 4 hold heads 16 quad .. 16 quad + 15 of the block (S's
     // rows in the first 16 lanes of TMEM quadrant quad), each 32 of the tile's
@@ -734,19 +735,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool left = false;
 #pragma unroll 1
       for (int tile = 0; tile < tiles; ++tile, ++g) {
-        ok = !dead && warp_wait(&sh.s_full[g & 1], (g >> 1) & 1, abort, status);
+        ok = !dead && warp_wait(&sh.s_full, g & 1, abort, status);
         uint32_t raw[16], w[8];
         float top[2] = {-INFINITY, -INFINITY}, sum[2];
         bool need = false, p_free = false;
         if (ok) {
           tc_fence_after();
-          tmem_ld_16x256b_x4(tmem + ((uint32_t)(quad * 32) << 16) + kSCol + (g & 1) * kTileKeys + 32 * half, raw);
-          const uint32_t mask = half ? sh.key_mask[g & 7].y : sh.key_mask[g & 7].x;
+          tmem_ld_16x256b_x4(tmem + ((uint32_t)(quad * 32) << 16) + kSCol + 32 * half, raw);
+          const uint32_t mask = half ? sh.key_mask[(g + i + 1) & 7].y : sh.key_mask[(g + i + 1) & 7].x;
           p_free = mbar_test(&sh.pv_done[g & 1], ((g >> 1) & 1) ^ 1);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.s_empty[g & 1]);
+          if (lane == 0) mbar_arrive(&sh.s_empty);
           if (mask != 0xffffffffu) {
             const uint32_t seen = mask >> (2 * (lane & 3));
 #pragma unroll
@@ -876,19 +877,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sh.stat_full);
       }
     }
-  } else {
+  } else if (warp >= 12) {  // (warp 3 has no role)
     // ------------------------------- epilogue -------------------------------
     // A warp has 32 elements (TMEM lanes) of every head.  The output is staged,
     // transposed, 32 heads x 32 elements at a time in a quarter of the P buffer
     // that the item's last tile is done with.
     const int quad = warp & 3;
     uint32_t g = 0;
+    int at = 0;  // the current item's tile of queries: its number in the ring's stream
+    // The queries of item i, from the ring to their place: the first two chunks to
+    // shared memory as they are, the others to TMEM: heads 16 quad .. 16 quad + 15,
+    // head r in lanes r and r + 16 of the quadrant (an M of 64 has its rows in 16
+    // lanes of each quadrant), elements 2 x and 2 x + 1 of a chunk in its column x.
+    auto queries = [&](int i) -> bool {
+      const int tile = at % kTileSlots;
+      // (in this order: the slot's phases before this one, which these warps do not
+      // wait for, are over once the last item's scores are)
+      if (!warp_wait(&sh.q_empty, (i & 1) ^ 1, abort, status)) return false;
+      if (!warp_wait(&sh.kv_full[tile], (at / kTileSlots) & 1, abort, status)) return false;
+      tc_fence_after();
+      const uint32_t from = smem_u32(ring) + tile * kPairsPerTile * kPairBytes;
+      const uint32_t copy = (quad * 32 + lane) * 16;
+#pragma unroll
+      for (int x = 0; x < kQBytes / 2048; ++x) store_shared_16(smem_u32(q_smem) + copy + x * 2048, load_shared_16(from + copy + x * 2048));
+      const int row = quad * 16 + (lane & 15);
 #pragma unroll 1
-    for (int i = 0; i < n_mine; ++i) {
+      for (int c = 2; c < 8; ++c) {
+        uint32_t v[32];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const uint4 u = load_shared_16(from + c * kChunkBytes + row * 128 + ((x ^ (row & 7)) << 4));
+          v[4 * x] = u.x;
+          v[4 * x + 1] = u.y;
+          v[4 * x + 2] = u.z;
+          v[4 * x + 3] = u.w;
+        }
+        tmem_st32(tmem + ((uint32_t)(quad * 32) << 16) + kQCol + 32 * (c - 2), v);
+      }
+      tmem_st_wait();
+      fence_proxy_async();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full);
+      return true;
+    };
+    bool ok = n_mine == 0 || queries(0);
+#pragma unroll 1
+    for (int i = 0; i < n_mine && ok; ++i) {
       const int slot = i % kInfoSlots;
       if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
       const int t = sh.info[slot].t, h0 = sh.info[slot].head_block * kHeadsPerItem, part = sh.info[slot].part;
       g += (uint32_t)sh.info[slot].tiles;
+      at += 1 + sh.info[slot].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
       const int heads = min(kHeadsPerItem, p.n_h - h0);
@@ -896,6 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int r = 0; r < 2; ++r)
         if (p.sink_logit != nullptr && lane + 32 * r < heads) sink[r] = __ldg(p.sink_logit + h0 + lane + 32 * r) * kLog2e;
+      if (i + 1 < n_mine && !(ok = queries(i + 1))) break;
       if (!warp_wait(&sh.stat_full, i & 1, abort, status)) break;
       if (p.cluster) {  // the whole CTA sees to it, below
         (void)warp_wait(&sh.o_full, i & 1, abort, status);
@@ -1084,7 +1125,7 @@ int max_clusters(int c) {
   return n;
 }
 
-fm_status launch_attn(AttnParams& p, const uint16_t* q, int sms, void* workspace, cudaStream_t stream) {
+fm_status launch_attn(AttnParams& p, int sms, void* workspace, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(csa_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return set_error(FM_ERR_CUDA, "fm_csa_attn: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   p.head_blocks = head_blocks_of(p.n_h);
@@ -1117,12 +1158,6 @@ fm_status launch_attn(AttnParams& p, const uint16_t* q, int sms, void* workspace
   p.part_ml = static_cast<float2*>(workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + parts * kHeadsPerItem * sizeof(float2));
 
-  CUtensorMap tq;
-  const uint64_t qd[3] = {(uint64_t)kWidth, (uint64_t)p.n_h, (uint64_t)p.T};
-  const uint64_t qs[2] = {(uint64_t)kWidth * 2, (uint64_t)kWidth * 2 * p.n_h};
-  const uint32_t qb[3] = {64, kHeadsPerItem, 1};
-  fm_status st = make_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st != FM_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3((unsigned)(p.cluster || p.items < sms ? p.items : sms));
@@ -1135,7 +1170,7 @@ fm_status launch_attn(AttnParams& p, const uint16_t* q, int sms, void* workspace
     attr[0].val.clusterDim = {(unsigned)p.splits, 1, 1};
     cfg.numAttrs = 1;
   }
-  if ((e = cudaLaunchKernelEx(&cfg, csa_attn_kernel, tq, (const AttnParams)p)) != cudaSuccess)
+  if ((e = cudaLaunchKernelEx(&cfg, csa_attn_kernel, (const AttnParams)p)) != cudaSuccess)
     return set_error(FM_ERR_CUDA, "fm_csa_attn: launch: %s", cudaGetErrorString(e));
   if (p.splits > 1 && !p.cluster) {
     // programmatic dependent launch: the launch overlaps the kernel before it
@@ -1220,7 +1255,7 @@ fm_status csa_attn(const char* who, bool tree, const uint16_t* q, int T, int n_h
   p.n_sink = n_sink;
   p.tree_words = tree_words;
   p.scale = scale;
-  return launch_attn(p, q, sms, workspace, stream);
+  return launch_attn(p, sms, workspace, stream);
 }
 
 }  // namespace
