@@ -487,12 +487,13 @@ fm_status fm_qk_norm_rope(const int64_t* pos, int T, int d, int rope_dim, double
  * (sink_logit NULL: no second term).  A token without keys gets out = 0 and
  * lse = -inf.  Rows that are no keys are never read.
  *
- *   q           [T, n_h, 512] bf16, 16-byte aligned; 1 <= n_h <= 1024
+ *   q           [T, n_h, 512] bf16, 16-byte aligned; 1 <= n_h <= 1024,
+ *               T * ceil(n_h / 64) < 2^23
  *   kv_pool     [P, 64, 512] bf16 pages, kv_page_stride elements from page to
  *               page: a multiple of 512, >= 64 * 512 (layers may lie between);
  *               16-byte aligned; NULL with P = 0
- *   page_table  [B, R] int32; an entry at or past P is skipped and flagged
- *               FM_DEVERR_PAGE_RANGE, as is a position at or past R * 64
+ *   page_table  [B, R] int32, R <= 2^19; an entry at or past P is skipped and
+ *               flagged FM_DEVERR_PAGE_RANGE, as is a token at or past R * 64
  *   seq         [T] int32 rows of page_table, or NULL (token t is row t, T <= B);
  *               a negative one (and a negative position) sees no cached tokens,
  *               one at or past B neither, and is flagged

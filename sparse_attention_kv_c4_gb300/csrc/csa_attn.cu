@@ -54,6 +54,7 @@ namespace {
 constexpr int kWidth = 512;
 constexpr int kPage = 64;
 constexpr int kMaxCells = 1024;
+constexpr int kMaxTable = 1 << 19;              // pages of a sequence: its 2^25 tokens take less than a wait's limit
 constexpr int kHeadsPerItem = 64;
 constexpr int kTileKeys = 64;
 constexpr int kChunkBytes = 64 * 128;           // 64 rows x 64 elements
@@ -75,6 +76,7 @@ constexpr int kInfoReaders = 2 + kSoftmaxWarps + 4;           // issuers, softma
 constexpr int kKvArrivals = 33 * kProducerWarps;              // the producers' copies, and their first lanes
 constexpr int kMaxParts = 256;                  // partial results of one call
 constexpr int kMaxCluster = 8;
+constexpr int64_t kMaxItems = int64_t(1) << 23;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
@@ -117,20 +119,20 @@ FM_DEV TokenKeys token_keys(const AttnParams& p, int64_t b, int64_t pos) {
     atomicOr(p.status, FM_DEV_PAGE_RANGE);
     return r;
   }
-  int64_t end = pos + 1;  // cached tokens below end
+  int64_t last = pos;  // the last cached token that is not after the query
   if (p.tree_mask != nullptr) {
     r.base = p.tree_base[b];
     if (r.base < 0) return r;
-    if (r.base < end) end = r.base;
+    if (r.base <= last) last = r.base - 1;
+    if (r.base > int64_t(1) << 62) r.base = int64_t(1) << 62;  // past every table, and sums stay in 64 bits
     r.n_tree = 32 * p.tree_words;
   }
   r.b = (int)b;
+  // the window has tokens past the table, or the first tokens reach past it
   const int64_t held = (int64_t)p.R * kPage;
-  if (end > held) {
-    end = held;
-    atomicOr(p.status, FM_DEV_PAGE_RANGE);
-  }
-  r.low = p.window > pos ? 0 : pos + 1 - p.window;
+  if (last >= held && (pos - last < p.window || p.n_sink > held)) atomicOr(p.status, FM_DEV_PAGE_RANGE);
+  const int64_t end = (last < held ? last : held - 1) + 1;
+  r.low = p.window > pos ? 0 : p.window == 0 ? end : pos - p.window + 1;
   if (r.low > end) r.low = end;
   r.n_first = (int)(p.n_sink < r.low ? p.n_sink : r.low);
   r.n_win = (int)(end - r.low);
@@ -884,17 +886,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // that the item's last tile is done with.
     const int quad = warp & 3;
     uint32_t g = 0;
-    int at = 0;  // the current item's tile of queries: its number in the ring's stream
+    uint32_t at = 0;  // the current item's tile of queries: its number in the ring's stream, modulo 2 * kTileSlots
     // The queries of item i, from the ring to their place: the first two chunks to
     // shared memory as they are, the others to TMEM: heads 16 quad .. 16 quad + 15,
     // head r in lanes r and r + 16 of the quadrant (an M of 64 has its rows in 16
     // lanes of each quadrant), elements 2 x and 2 x + 1 of a chunk in its column x.
     auto queries = [&](int i) -> bool {
-      const int tile = at % kTileSlots;
+      const uint32_t tile = at % kTileSlots;
       // (in this order: the slot's phases before this one, which these warps do not
       // wait for, are over once the last item's scores are)
       if (!warp_wait(&sh.q_empty, (i & 1) ^ 1, abort, status)) return false;
-      if (!warp_wait(&sh.kv_full[tile], (at / kTileSlots) & 1, abort, status)) return false;
+      if (!warp_wait(&sh.kv_full[tile], at / kTileSlots, abort, status)) return false;
       tc_fence_after();
       const uint32_t from = smem_u32(ring) + tile * kPairsPerTile * kPairBytes;
       const uint32_t copy = (quad * 32 + lane) * 16;
@@ -928,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
       const int t = sh.info[slot].t, h0 = sh.info[slot].head_block * kHeadsPerItem, part = sh.info[slot].part;
       g += (uint32_t)sh.info[slot].tiles;
-      at += 1 + sh.info[slot].tiles;
+      at = (at + 1u + (uint32_t)sh.info[slot].tiles) % (2 * kTileSlots);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
       const int heads = min(kHeadsPerItem, p.n_h - h0);
@@ -1130,8 +1132,6 @@ fm_status launch_attn(AttnParams& p, int sms, void* workspace, cudaStream_t stre
   if (e != cudaSuccess) return set_error(FM_ERR_CUDA, "fm_csa_attn: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   p.head_blocks = head_blocks_of(p.n_h);
   const int64_t items = (int64_t)p.T * p.head_blocks;
-  if (items * kMaxParts >= (int64_t(1) << 31))
-    return set_error(FM_ERR_INVALID_ARG, "fm_csa_attn: T=%d n_h=%d: too many head blocks", p.T, p.n_h);
   // tiles that a token can have at most
   const int64_t held = (int64_t)p.R * kPage;
   const int64_t slots = (p.window < held ? p.window : held) + (p.n_sink < held ? p.n_sink : held) + p.k +
@@ -1142,13 +1142,13 @@ fm_status launch_attn(AttnParams& p, int sms, void* workspace, cudaStream_t stre
   if (splits < 1) splits = 1;
   p.cluster = 0;
   if (splits > 1) {
-    // As a cluster where that costs a CTA at most eight tiles more than the split
-    // over all SMs: a tile is some 0.8 us, the partial results' way through
-    // memory and the second kernel some 7 us.
+    // The largest cluster of which enough fit at once; the split over all SMs
+    // through memory where it saves a CTA more than eight tiles: a tile is some
+    // 1.1 us, the partial results' way through memory and the second kernel some 8 us.
     int c = kMaxCluster;
-    while (c > 2 && (c > splits || max_clusters(c) < items)) c /= 2;
-    if (c <= splits && (max_tiles + c - 1) / c <= (max_tiles + splits - 1) / splits + 8) {
-      p.cluster = 1;
+    while (c > 1 && (c > splits || max_clusters(c) < items)) c /= 2;
+    if ((max_tiles + c - 1) / c <= (max_tiles + splits - 1) / splits + 8) {
+      p.cluster = c > 1;
       splits = c;
     }
   }
@@ -1193,11 +1193,12 @@ fm_status csa_attn(const char* who, bool tree, const uint16_t* q, int T, int n_h
                    const uint32_t* tree_mask, int tree_words, const int64_t* tree_base, uint16_t* out, float* lse_out,
                    void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (d != kWidth) return set_error(FM_ERR_INVALID_ARG, "%s: d=%d (need 512)", who, d);
-  if (T < 0 || n_h < 1 || n_h > 1024 || (int64_t)T * n_h >= (int64_t(1) << 31))
-    return set_error(FM_ERR_INVALID_ARG, "%s: bad sizes T=%d n_h=%d (1 <= n_h <= 1024, T * n_h < 2^31)", who, T, n_h);
-  if (B < 0 || R < 0 || R > (1 << 24) || window < 0 || n_sink < 0 || k < 0 || k > kMaxCells)
+  if (T < 0 || n_h < 1 || n_h > 1024 || (int64_t)T * head_blocks_of(n_h) >= kMaxItems)
+    return set_error(FM_ERR_INVALID_ARG, "%s: bad sizes T=%d n_h=%d (1 <= n_h <= 1024, T * ceil(n_h / 64) < 2^23)", who,
+                     T, n_h);
+  if (B < 0 || R < 0 || R > kMaxTable || window < 0 || n_sink < 0 || k < 0 || k > kMaxCells)
     return set_error(FM_ERR_INVALID_ARG,
-                     "%s: bad sizes B=%d R=%d window=%lld n_sink=%d k=%d (R <= 2^24, 0 <= k <= 1024)", who, B, R,
+                     "%s: bad sizes B=%d R=%d window=%lld n_sink=%d k=%d (R <= 2^19, 0 <= k <= 1024)", who, B, R,
                      (long long)window, n_sink, k);
   if (!(scale > 0.0f) || isinf(scale)) return set_error(FM_ERR_INVALID_ARG, "%s: scale=%g", who, (double)scale);
   if (tree && (tree_words < 1 || tree_words > 32))

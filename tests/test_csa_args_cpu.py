@@ -54,8 +54,8 @@ def test_attention_refusals(fm):
         first = f(*a.values(), *z.values())
         assert ft(*a.values(), *tree.values(), *z.values()) == first  # both entry points refuse alike
         return first
-    for bad in (dict(d=128), dict(T=-1), dict(H=0), dict(H=1025), dict(T=1 << 30, H=2), dict(B=-1), dict(R=-1),
-                dict(R=(1 << 24) + 1), dict(window=-1), dict(n_sink=-1), dict(k=-1), dict(k=1025), dict(scale=0.0),
+    for bad in (dict(d=128), dict(T=-1), dict(H=0), dict(H=1025), dict(T=1 << 23, H=2), dict(T=1 << 22, H=65), dict(B=-1), dict(R=-1),
+                dict(R=(1 << 19) + 1), dict(window=-1), dict(n_sink=-1), dict(k=-1), dict(k=1025), dict(scale=0.0),
                 dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(P=-1), dict(kv=None),
                 dict(kv=FAKE + 8), dict(kvs=page - 512), dict(kvs=page + 8), dict(P=1 << 25), dict(kvs=1 << 45),
                 dict(Pc=-1), dict(cp=None), dict(cps=page + 64), dict(Pc=1 << 25), dict(seq=None, T=5), dict(q=None),

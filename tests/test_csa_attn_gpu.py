@@ -339,3 +339,170 @@ def test_wider_pool_views_and_default_rows(torch_dev):
     b.kw["seq"] = None
     b.call()
     b.check(torch)
+
+
+def test_many_short_items(torch_dev):
+    """Far more tokens than SMs, each with none to three tiles of keys, so that a
+    CTA goes from item to item all the time: right, and the same bits each time."""
+    torch, dev = torch_dev
+    seqs = [(int(n), int(n) - 1 + 7 * i) for i, n in enumerate(np.random.default_rng(3).integers(1, 60, 60))]
+    b = Batch(21, seqs, 3, 40, 70, 2, Pc=4, pads=5, holes=True).device(torch, dev)
+    b.call()
+    b.check(torch)
+    want = b.d["out"].clone()
+    for _ in range(20):
+        b.d["out"].zero_()
+        b.call()
+        torch.cuda.synchronize()
+        assert torch.equal(want, b.d["out"])
+
+
+@pytest.mark.parametrize("tokens", [1, 9, 19, 38, 60, 77])
+def test_every_way_of_splitting(torch_dev, tokens):
+    """Clusters of eight, four and two CTAs, partial results through memory, and no
+    split: each with tokens whose keys leave some of the splits empty."""
+    torch, dev = torch_dev
+    seqs = [(1, 5000 if i % 5 == 0 else 31 * i) for i in range(tokens)]
+    for window in (300, 5001):
+        b = Batch(30 + tokens, seqs, 5, 16, window, 4, pads=1).device(torch, dev)
+        b.call()
+        b.check(torch, tokens=list(range(0, b.T, max(1, b.T // 9))) + [b.T - 1])
+
+
+def test_partial_results_in_a_graph(torch_dev):
+    """The split through memory (two kernels): captured, replayed on new inputs,
+    and the same bits as the eager call."""
+    torch, dev = torch_dev
+    b = Batch(40, [(1, 7000), (1, 6500)], 64, 0, 6800, 4).device(torch, dev)
+    b.call()
+    b.check(torch)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.call()
+    c = Batch(41, [(1, 7000), (1, 6500)], 64, 0, 6800, 4).device(torch, dev)
+    for key in ("q", "kv_pool", "page_table"):
+        b.d[key].copy_(c.d[key])
+    b.kw["sink_logit"].copy_(c.kw["sink_logit"])
+    c.call()
+    for _ in range(3):
+        b.d["out"].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(b.d["out"], c.d["out"]) and torch.equal(b.kw["lse_out"], c.kw["lse_out"])
+    c.check(torch)
+
+
+def test_extreme_positions_windows_and_sinks(torch_dev):
+    """Nothing overflows at the ends of the types, and only tokens that a call can
+    see past the table are flagged."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    b = Batch(50, [(1, 300)], 8, 20, 0, 0, sink=False).device(torch, dev)
+    for pos, window, n_sink, flag in ((2 ** 63 - 1, 0, 0, 0), (2 ** 63 - 1, 0, 3, 0), (2 ** 63 - 1, 1, 0, 1),
+                                      (2 ** 63 - 1, 2 ** 63 - 1, 0, 1), (b.R * PAGE - 1, 5, 2 ** 31 - 1, 0),
+                                      (b.R * PAGE, 0, 2 ** 31 - 1, 1), (b.R * PAGE + 9, 3, 4, 1)):
+        slots = [j for j in range(b.R * PAGE) if j <= pos and (j < n_sink or j > pos - window)]
+        rows = [int(b.table[0, j // PAGE]) * PAGE + j % PAGE for j in slots]
+        b.kv[rows] = ref.bf16(np.random.default_rng(1).standard_normal((len(rows), D)))
+        b.d["kv_pool"].copy_(torch.from_numpy(b.kv.view(np.int16).reshape(-1, PAGE, D)).to(dev))
+        b.d["pos"].fill_(pos)
+        b.kw.update(window=window, n_sink=n_sink)
+        b.rows = [rows]
+        b.call()
+        torch.cuda.synchronize()
+        assert fm.fm_device_status(reset=True) == (fm.FM_DEVERR_PAGE_RANGE if flag else 0), (pos, window, n_sink)
+        b.check(torch)
+    # a tree whose base is past everything sees its window's tokens of the table, and flags the others
+    t = Batch(51, [(4, 100)], 8, 0, 40, 0, tree=True).device(torch, dev)
+    t.kw["tree_base"].fill_(2 ** 63 - 1)
+    t.call()
+    torch.cuda.synchronize()
+    assert fm.fm_device_status(reset=True) == fm.FM_DEVERR_PAGE_RANGE
+
+
+def test_not_finite_keys_that_are_seen(torch_dev):
+    """An infinite element of a visible cell makes the heads that weigh it
+    infinite or NaN, and no other token's rows."""
+    torch, dev = torch_dev
+    b = Batch(60, [(6, 300)], 64, 32, 64, 4).device(torch, dev)
+    b.call()
+    b.check(torch)
+    clean = b.d["out"].clone()
+    row = int(b.cells[2][b.cells[2] >= 0][0])
+    users = [t for t in range(b.T) if row in b.cells[t]]
+    b.kw["cell_pool"].view(-1, D)[row, 5] = 0x7F80  # +inf
+    b.call()
+    torch.cuda.synchronize()
+    out = b.d["out"]
+    for t in range(b.T):
+        if t in users:
+            assert not torch.isfinite(out[t].view(torch.bfloat16)).all()
+        else:
+            assert torch.equal(out[t], clean[t])
+
+
+def test_the_layer_from_selection_to_output(torch_dev):
+    """As a decode step runs it: the indexer's top-k picks cells (reserve cells), the
+    norm and rotation make the queries and write the token's own cell, and the
+    attention reads both -- one stream, no synchronisation in between."""
+    torch, dev = torch_dev
+    import gen
+    import sparse_attention_kv_c4_gb300 as fm
+    rng = np.random.default_rng(70)
+    t = lambda a, dt=None: torch.from_numpy(np.ascontiguousarray(a if dt is None else a.view(dt))).to(dev)
+    pc = gen.PagedCfg("layer", requests=5, layers=1, n_pages=30, R=9, seed=gen.BASE_SEED + 300)
+    logical, phys, owner = gen.paged_tables(pc)
+    pq, pw = gen.paged_qw(pc)
+    k8, scale = gen.paged_pool_host(pc, owner)
+    Q, H, window, n_sink = pc.Q, 64, 128, 4
+    cells = torch.empty((Q, 128), dtype=torch.int32, device=dev)
+    ws = torch.empty(fm.fm_native_topk_paged_workspace(Q, pc.R), dtype=torch.uint8, device=dev)
+    pos = 200 + 97 * np.arange(Q)
+    R = int(pos.max()) // PAGE + 1
+    table = rng.permutation(Q * R).reshape(Q, R).astype(np.int32)
+    kv = ref.bf16(rng.standard_normal((Q * R, PAGE, D)))
+    pool = ref.bf16(rng.standard_normal((k8.shape[0], PAGE, D)))
+    q, k = ref.bf16(rng.standard_normal((Q, H, D))), ref.bf16(rng.standard_normal((Q, 1, D)))
+    qg, kg = ref.bf16(1 + 0.1 * rng.standard_normal(D)), ref.bf16(1 + 0.1 * rng.standard_normal(D))
+    own = table[np.arange(Q), pos // PAGE] * PAGE + pos % PAGE
+    kv_d, q_out = t(kv, np.int16), torch.empty((Q, H, D), dtype=torch.int16, device=dev)
+    out, lse = torch.empty_like(q_out), torch.empty((Q, H), device=dev)
+    aws = torch.empty(fm.fm_csa_attn_workspace(Q, H), dtype=torch.uint8, device=dev)
+    args = [t(pq, np.int16), t(pw), t(k8), t(scale), t(phys), t(logical)]
+    q_d, k_d, qg_d, kg_d, pos_d, own_d, tab_d, pool_d = (t(q, np.int16), t(k, np.int16), t(qg, np.int16),
+                                                          t(kg, np.int16), t(pos), t(own.astype(np.int32)), t(table),
+                                                          t(pool, np.int16))
+    sink = torch.zeros(H, device=dev)
+
+    def step():
+        fm.fm_native_topk_paged_ex(*args, 128, cells, id_mode=1, workspace=ws)
+        fm.fm_qk_norm_rope(pos_d, q=q_d, q_gain=qg_d, q_out=q_out, k=k_d, k_gain=kg_d, k_pool=kv_d, k_cell=own_d)
+        fm.fm_csa_attn(q_out, kv_d, tab_d, pos_d, out, window=window, n_sink=n_sink, cell_pool=pool_d, cells=cells,
+                       sink_logit=sink, lse_out=lse, workspace=aws)
+    step()
+    torch.cuda.synchronize()
+    assert fm.fm_device_status(reset=True) == 0
+    eager = out.clone()
+    # the attention's own inputs are the bits that the steps before wrote
+    got_q = ref.f64(q_out.cpu().numpy().view(np.uint16))
+    want_q, tol_q = ref.norm_rope(ref.f64(q), ref.f64(qg), pos, 64, 1e-6)
+    assert (np.abs(got_q - want_q) <= tol_q).all()
+    kv_now = kv_d.cpu().numpy().view(np.uint16).reshape(-1, D)
+    want_k, tol_k = ref.norm_rope(ref.f64(k), ref.f64(kg), pos, 64, 1e-6)
+    assert (np.abs(ref.f64(kv_now[own]) - want_k[:, 0]) <= tol_k[:, 0]).all()
+    chosen, got = cells.cpu().numpy(), ref.f64(out.cpu().numpy().view(np.uint16))
+    assert (chosen >= 0).sum(1).min() == 128
+    for i in range(Q):
+        slots = ref.visible(int(pos[i]), window, n_sink, int(pos[i]) + 1)
+        rows = [int(table[i, j // PAGE]) * PAGE + j % PAGE for j in slots]
+        keys = np.concatenate([kv_now[rows], pool.reshape(-1, D)[chosen[i]]])
+        w, w_lse, tol, ltol = ref.attend(got_q[i], ref.f64(keys), np.zeros(H), D ** -0.5)
+        assert (np.abs(got[i] - w) <= tol).all() and (np.abs(lse[i].cpu().numpy() - w_lse) <= ltol).all()
+    # the whole step captured and replayed
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, eager) and fm.fm_device_status(reset=True) == 0
