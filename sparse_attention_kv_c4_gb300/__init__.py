@@ -139,9 +139,6 @@ def _check(status: int) -> None:
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle alone: a tenth of the time
-        if raw is not None:
-            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
@@ -393,11 +390,16 @@ def fm_page_recall(mask, S: int, kmax: int, pages_out, density_out=None, n_out=N
 # waits for that, so the checks of an accepted tensor are a few attribute reads and
 # the reasons are worked out only for a refused one.
 _BF16 = _BITS = _I32T = _I64T = _F32T = _U8T = frozenset()  # accepted element types, set by _types()
+_current_device = _raw_stream = None
 
 
 def _types():
     import torch
-    global _BF16, _BITS, _I32T, _I64T, _F32T, _U8T
+    global _BF16, _BITS, _I32T, _I64T, _F32T, _U8T, _current_device, _raw_stream
+    _current_device = torch.cuda.current_device
+    # the current stream's handle alone: a tenth of the time of current_stream()
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
     _BITS, _I32T, _I64T = frozenset((torch.int32, torch.uint32)), frozenset((torch.int32,)), frozenset((torch.int64,))
     _F32T, _U8T = frozenset((torch.float32,)), frozenset((torch.uint8,))
     _BF16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))  # bf16 tensors, or their bit patterns
@@ -439,10 +441,8 @@ def _device(t, name):
     if not _BF16:
         _types()
     dev = t.get_device()
-    if dev >= 0:
-        import torch
-        if dev != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if dev >= 0 and dev != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
     return dev
 
 
@@ -497,7 +497,7 @@ def fm_qk_norm_rope(pos, q=None, q_gain=None, q_out=None, k=None, k_gain=None, k
             kc_p = _dense(k_cell, "k_cell", _I32T, (T,), dev)
     st = lib().fm_qk_norm_rope(_dense(pos, "pos", _I64T, (T,), dev), T, d, rope_dim, rope_base, rope_factor,
                                rope_orig_len, rope_beta_fast, rope_beta_slow, eps, q_p, q_stride, n_q, qg_p, qo_p, k_p,
-                               k_stride, n_k, kg_p, ko_p, kp_p, P, page_stride, kc_p, _stream(stream))
+                               k_stride, n_k, kg_p, ko_p, kp_p, P, page_stride, kc_p, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
 
@@ -541,13 +541,13 @@ def _csa_attn(tree, q, kv_pool, page_table, pos, out, window, n_sink, seq, cell_
             window, n_sink, cp_p, Pc, cp_stride, cells_p, k, sink_p, d ** -0.5 if scale is None else scale)
     out_p = _dense(out, "out", _BF16, shape, dev)
     if tree is None:
-        st = lib().fm_csa_attn(*args, out_p, lse_p, ws_p, ws_bytes, _stream(stream))
+        st = lib().fm_csa_attn(*args, out_p, lse_p, ws_p, ws_bytes, _raw_stream(dev) if stream is None else _stream(stream))
     else:
         tree_mask, tree_base = tree
         words = _shape(tree_mask, "tree_mask", 2)[1]
         st = lib().fm_csa_attn_tree(*args, _dense(tree_mask, "tree_mask", _BITS, (T, words), dev), words,
                                     _dense(tree_base, "tree_base", _I64T, (B,), dev), out_p, lse_p, ws_p, ws_bytes,
-                                    _stream(stream))
+                                    _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
 
