@@ -306,6 +306,9 @@ constexpr int kSmemBytes = kQBytes + kPairs * kPairBytes + 2 * kPBytes + (int)si
 static_assert(kSmemBytes <= 232448, "227 KB of shared memory to a CTA");
 static_assert(offsetof(Shared, rows) % 16 == 0, "vector accesses");
 
+FM_DEV void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+FM_DEV void grid_dep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 FM_DEV void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -429,7 +432,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_slot;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // csa_merge_kernel may get ready: it waits
+  // What is above overlaps the kernel before this one; what it wrote is read from
+  // here on.  The kernel after may get ready likewise.
+  grid_dep_wait();
+  grid_dep_launch_dependents();
   const int n_mine = (p.items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
 
   if (warp == 1) {
@@ -1038,7 +1044,7 @@ __global__ void __launch_bounds__(128) csa_merge_kernel(const __grid_constant__ 
   const int h = (int)(th % p.n_h), hl = h % kHeadsPerItem;
   const int64_t t = th / p.n_h;
   const int64_t part0 = (t * p.head_blocks + h / kHeadsPerItem) * p.splits;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the partial results
+  grid_dep_wait();  // for the partial results
   // the splits' weights, a thread each
   __shared__ float weight[kMaxParts], warp_top[4], warp_sum[4];
   static_assert(kMaxParts <= 2 * 128, "two splits to a thread");
@@ -1158,28 +1164,28 @@ fm_status launch_attn(AttnParams& p, int sms, void* workspace, cudaStream_t stre
   p.part_ml = static_cast<float2*>(workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + parts * kHeadsPerItem * sizeof(float2));
 
+  // programmatic dependent launch: a kernel's set-up overlaps the one before it
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)(p.cluster || p.items < sms ? p.items : sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
+  cfg.numAttrs = 1;
   if (p.cluster) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)p.splits, 1, 1};
-    cfg.numAttrs = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)p.splits, 1, 1};
+    cfg.numAttrs = 2;
   }
   if ((e = cudaLaunchKernelEx(&cfg, csa_attn_kernel, (const AttnParams)p)) != cudaSuccess)
     return set_error(FM_ERR_CUDA, "fm_csa_attn: launch: %s", cudaGetErrorString(e));
   if (p.splits > 1 && !p.cluster) {
-    // programmatic dependent launch: the launch overlaps the kernel before it
     cfg.gridDim = dim3((unsigned)((int64_t)p.T * p.n_h));
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, csa_merge_kernel, (const AttnParams)p)) != cudaSuccess)
       return set_error(FM_ERR_CUDA, "fm_csa_attn: merge launch: %s", cudaGetErrorString(e));
   }

@@ -69,6 +69,10 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
   const int rows = p.n_q + p.n_k;
   const int row_end = min(rows, (chunk + 1) * p.rows_per_chunk);
   const int nvec = p.d >> 3;
+  // programmatic dependent launch: this kernel's launch overlaps the one before
+  // it, whose output may be read from here on; the kernel after may get ready
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // The warp's first row is on its way before anything else is done.
   const int first = chunk * p.rows_per_chunk + warp * kRowsPerWarp + lane / LPR;
@@ -191,8 +195,16 @@ cudaError_t launch(NormRopeParams& p, int T, int sms, cudaStream_t stream) {
   if (chunks > steps) chunks = steps;
   p.rows_per_chunk = (steps + chunks - 1) / chunks * kStep;
   p.chunks = (rows + p.rows_per_chunk - 1) / p.rows_per_chunk;
-  qk_norm_rope_kernel<LPR, VPL><<<(unsigned)((int64_t)T * p.chunks), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)((int64_t)T * p.chunks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<LPR, VPL>, (const NormRopeParams)p);
 }
 
 }  // namespace
