@@ -306,6 +306,65 @@ constexpr int kSmemBytes = kQBytes + kPairs * kPairBytes + 2 * kPBytes + (int)si
 static_assert(kSmemBytes <= 232448, "227 KB of shared memory to a CTA");
 static_assert(offsetof(Shared, rows) % 16 == 0, "vector accesses");
 
+// The output of an item, 32 heads x 32 elements (of TMEM quadrant `quad`) at a time:
+// half block x has heads 32 (x % 2) .. of the 128 elements x / 2.
+constexpr int kStageBytes = 32 * 32 * 2;
+struct Output {
+  const AttnParams& p;
+  uint32_t tmem, stage;  // stage: kStageBytes of shared memory of the warp's own
+  int t, h0, part;
+
+  // Scaled by the heads' factors (f[2 j + e]: of head 8 j + 2 (lane % 4) + e), to
+  // bf16, transposed through `stage`; `loaded` runs once TMEM has been read.
+  template <typename Loaded>
+  FM_DEV void half_block(int x, int quad, int lane, const float (&f)[8], Loaded loaded) const {
+    const int heads = min(kHeadsPerItem, p.n_h - h0);
+    // rows of 64 bytes (32 elements of a head), their 16-byte units swizzled: unit u
+    // of row h at u ^ (h / 2) % 4
+    const uint32_t put = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+    const uint32_t get = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    uint16_t* dst = p.out + ((int64_t)t * p.n_h + h0 + (x & 1) * 32 + lane / 4) * kWidth + (x >> 1) * 128 + quad * 32 +
+                    (lane & 3) * 8;
+    const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + 32 * x;
+    uint32_t a[16], b[16];
+    tmem_ld_16x256b_x4(from, a);
+    tmem_ld_16x256b_x4(from + (16u << 16), b);
+    tmem_ld_wait();
+    tc_fence_before();
+    __syncwarp();
+    loaded();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t e[4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        e[r] = pack_bf16(__uint_as_float(a[4 * j + 2 * r]) * f[2 * j], __uint_as_float(a[4 * j + 2 * r + 1]) * f[2 * j + 1]);
+        e[2 + r] = pack_bf16(__uint_as_float(b[4 * j + 2 * r]) * f[2 * j], __uint_as_float(b[4 * j + 2 * r + 1]) * f[2 * j + 1]);
+      }
+      store_8x8_x4_trans(put + 8 * j * 64, e[0], e[1], e[2], e[3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 v = load_shared_16(get + 8 * j * 64);
+      if ((x & 1) * 32 + 8 * j + lane / 4 < heads) *reinterpret_cast<uint4*>(dst + 8 * j * kWidth) = v;
+    }
+    __syncwarp();
+  }
+
+  // As it is, fp32, to the partial results.
+  FM_DEV void half_block_partial(int x, int quad, int lane) const {
+    const int heads = min(kHeadsPerItem, p.n_h - h0);
+    uint32_t o[32];
+    tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + 32 * x, o);
+    tmem_ld_wait();
+    float* dst = p.part_o + ((int64_t)part * kHeadsPerItem + (x & 1) * 32) * kWidth + (x >> 1) * 128 + quad * 32 + lane;
+#pragma unroll
+    for (int h = 0; h < 32; ++h)
+      if ((x & 1) * 32 + h < heads) dst[h * kWidth] = __uint_as_float(o[h]);
+  }
+};
+
 FM_DEV void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 FM_DEV void grid_dep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -965,64 +1024,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!warp_wait(&sh.o_full, i & 1, abort, status)) break;
+      if (i == n_mine - 1) {  // the whole CTA stores the last item, below
+        if (quad == 0) {
+          sh.rescale[lane] = factor[0];
+          sh.rescale[lane + 32] = factor[1];
+        }
+        break;
+      }
       tc_fence_after();
-      const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-      if (part >= 0) {
+      const Output out = {p, tmem, smem_u32(p_smem) + ((g - 1) & 1) * kPBytes + quad * kStageBytes, t, h0, -1};
 #pragma unroll 1
-        for (int x = 0; x < 8; ++x) {
-          uint32_t o[32];
-          tmem_ld32(lanes + 32 * x, o);
-          tmem_ld_wait();
-          if (x & 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.o_empty[x >> 1]);
-          }
-          float* dst = p.part_o + ((int64_t)part * kHeadsPerItem + (x & 1) * 32) * kWidth + (x >> 1) * 128 + quad * 32 + lane;
+      for (int x = 0; x < 8; ++x) {
+        const float mine = x & 1 ? factor[1] : factor[0];
+        float f[8];
 #pragma unroll
-          for (int h = 0; h < 32; ++h)
-            if ((x & 1) * 32 + h < heads) dst[h * kWidth] = __uint_as_float(o[h]);
-        }
-      } else {
-        const uint32_t stage = smem_u32(p_smem) + ((g - 1) & 1) * kPBytes + quad * 2048;
-        // rows of 64 bytes (32 elements of a head), their 16-byte units swizzled:
-        // unit u of row h at u ^ (h / 2) % 4
-        const uint32_t put = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
-        const uint32_t get = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
-        uint16_t* dst = p.out + ((int64_t)t * p.n_h + h0 + lane / 4) * kWidth + quad * 32 + (lane & 3) * 8;
-#pragma unroll 1
-        for (int x = 0; x < 8; ++x) {
-          uint32_t a[16], b[16];
-          tmem_ld_16x256b_x4(lanes + 32 * x, a);
-          tmem_ld_16x256b_x4(lanes + (16u << 16) + 32 * x, b);
-          tmem_ld_wait();
-          if (x & 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.o_empty[x >> 1]);
-          }
-          const float mine = x & 1 ? factor[1] : factor[0];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float f0 = __shfl_sync(0xffffffffu, mine, 8 * j + 2 * (lane & 3));
-            const float f1 = __shfl_sync(0xffffffffu, mine, 8 * j + 2 * (lane & 3) + 1);
-            uint32_t e[4];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              e[r] = pack_bf16(__uint_as_float(a[4 * j + 2 * r]) * f0, __uint_as_float(a[4 * j + 2 * r + 1]) * f1);
-              e[2 + r] = pack_bf16(__uint_as_float(b[4 * j + 2 * r]) * f0, __uint_as_float(b[4 * j + 2 * r + 1]) * f1);
-            }
-            store_8x8_x4_trans(put + 8 * j * 64, e[0], e[1], e[2], e[3]);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 v = load_shared_16(get + 8 * j * 64);
-            const int hl = (x & 1) * 32 + 8 * j;
-            if (hl + lane / 4 < heads) *reinterpret_cast<uint4*>(dst + (int64_t)hl * kWidth + (x >> 1) * 128) = v;
-          }
-          __syncwarp();
-        }
+        for (int j = 0; j < 8; ++j) f[j] = __shfl_sync(0xffffffffu, mine, 8 * (j >> 1) + 2 * (lane & 3) + (j & 1));
+        out.half_block(x, quad, lane, f, [&] {
+          if ((x & 1) && lane == 0) mbar_arrive(&sh.o_empty[x >> 1]);
+        });
       }
       if (lane == 0) mbar_arrive(&sh.stage_free[(g - 1) & 1]);
     }
@@ -1030,7 +1049,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (p.cluster) join_cluster(p, sh, reinterpret_cast<float*>(ring), tmem);
+  if (p.cluster) {
+    join_cluster(p, sh, reinterpret_cast<float*>(ring), tmem);
+  } else if (n_mine > 0 && sh.abort_flag == 0) {
+    // the last item, by all warps: a half block of its output at a time each
+    const ItemInfo f = sh.info[(n_mine - 1) % kInfoSlots];
+    const Output out = {p, tmem, smem_u32(ring) + warp * kStageBytes, f.t, f.head_block * kHeadsPerItem, f.part};
+#pragma unroll 1
+    for (int x = warp >> 2; x < 8; x += kThreads / 128) {
+      float fac[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) fac[j] = sh.rescale[(x & 1) * 32 + 8 * (j >> 1) + 2 * (lane & 3) + (j & 1)];
+      if (f.part >= 0)
+        out.half_block_partial(x, warp & 3, lane);
+      else
+        out.half_block(x, warp & 3, lane, fac, [] {});
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
