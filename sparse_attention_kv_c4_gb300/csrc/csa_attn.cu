@@ -1073,64 +1073,77 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the splits of one (token, head): out = sum_s 2^(m_s - M) O_s / (sum_s
-// 2^(m_s - M) l_s + sink), the splits in order.
-__global__ void __launch_bounds__(128) csa_merge_kernel(const __grid_constant__ AttnParams p) {
+// 2^(m_s - M) l_s + sink).  Four groups of 128 threads (four elements to a thread)
+// take every fourth split, eight of them in flight; their sums meet in shared
+// memory.  The order of all sums is fixed.
+constexpr int kMergeGroups = 4;
+constexpr int kMergeThreads = 128 * kMergeGroups;
+__global__ void __launch_bounds__(kMergeThreads) csa_merge_kernel(const __grid_constant__ AttnParams p) {
+  __shared__ float weight[kMaxParts], warp_top[kMaxParts / 32], warp_sum[kMaxParts / 32];
+  __shared__ float4 group_sum[kMergeGroups - 1][128];
+  static_assert(kMaxParts <= kMergeThreads, "a split to a thread");
   const int64_t th = blockIdx.x;
   const int h = (int)(th % p.n_h), hl = h % kHeadsPerItem;
   const int64_t t = th / p.n_h;
   const int64_t part0 = (t * p.head_blocks + h / kHeadsPerItem) * p.splits;
+  const int tid = threadIdx.x, group = tid / 128, d = 4 * (tid % 128);
+  const float sink = p.sink_logit != nullptr ? __ldg(p.sink_logit + h) * kLog2e : -INFINITY;
   grid_dep_wait();  // for the partial results
-  // the splits' weights, a thread each
-  __shared__ float weight[kMaxParts], warp_top[4], warp_sum[4];
-  static_assert(kMaxParts <= 2 * 128, "two splits to a thread");
-  const int tid = threadIdx.x, warp = tid / 32;
-  float2 ml[2] = {make_float2(-INFINITY, 0.f), make_float2(-INFINITY, 0.f)};
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-    if (tid + 128 * x < p.splits) ml[x] = p.part_ml[(part0 + tid + 128 * x) * kHeadsPerItem + hl];
-  float top = fmaxf(ml[0].x, ml[1].x);
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (tid % 32 == 0) warp_top[warp] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(warp_top[0], warp_top[1]), fmaxf(warp_top[2], warp_top[3]));
-  float sum = 0.f;
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const float w = ml[x].y == 0.f ? 0.f : exp2_fast(ml[x].x - top);  // a split without keys holds zeros
-    sum = fmaf(w, ml[x].y, sum);
-    if (tid + 128 * x < kMaxParts) weight[tid + 128 * x] = w;
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (tid < p.splits) ml = p.part_ml[(part0 + tid) * kHeadsPerItem + hl];
+  if (tid < kMaxParts) {
+    float top = ml.x;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (tid % 32 == 0) warp_top[tid / 32] = top;
   }
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (tid % 32 == 0) warp_sum[warp] = sum;
   __syncthreads();
-  sum = warp_sum[0] + warp_sum[1] + warp_sum[2] + warp_sum[3];
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxParts / 32; ++i) top = fmaxf(top, warp_top[i]);
+  if (tid < kMaxParts) {
+    const float w = ml.y == 0.f ? 0.f : exp2_fast(ml.x - top);  // a split without keys holds zeros
+    weight[tid] = w;
+    float part = w * ml.y;
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (tid % 32 == 0) warp_sum[tid / 32] = part;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kMaxParts / 32; ++i) sum += warp_sum[i];
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int d = 4 * tid;
   const float* from = p.part_o + (part0 * kHeadsPerItem + hl) * kWidth + d;
-  for (int s0 = 0; s0 < p.splits; s0 += 8) {
+  for (int s0 = group; s0 < p.splits; s0 += 8 * kMergeGroups) {
     float4 o[8];
 #pragma unroll
-    for (int s = 0; s < 8; ++s)
-      o[s] = s0 + s < p.splits ? *reinterpret_cast<const float4*>(from + (int64_t)(s0 + s) * kHeadsPerItem * kWidth)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < 8; ++x) {
+      const int s = s0 + x * kMergeGroups;
+      o[x] = s < p.splits ? *reinterpret_cast<const float4*>(from + (int64_t)s * kHeadsPerItem * kWidth)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const float w = weight[(s0 + s) % kMaxParts];
-      acc.x = fmaf(w, o[s].x, acc.x);
-      acc.y = fmaf(w, o[s].y, acc.y);
-      acc.z = fmaf(w, o[s].z, acc.z);
-      acc.w = fmaf(w, o[s].w, acc.w);
+    for (int x = 0; x < 8; ++x) {
+      const float w = weight[(s0 + x * kMergeGroups) % kMaxParts];  // (past the last split: of zeros)
+      acc.x = fmaf(w, o[x].x, acc.x);
+      acc.y = fmaf(w, o[x].y, acc.y);
+      acc.z = fmaf(w, o[x].z, acc.z);
+      acc.w = fmaf(w, o[x].w, acc.w);
     }
   }
-  float below = sum;
-  if (p.sink_logit != nullptr) below += exp2f(fmaf(p.sink_logit[h], kLog2e, -top));
-  const float f = sum == 0.f ? 0.f : 1.f / below;
-  uint2 v;
-  v.x = pack_bf16(acc.x * f, acc.y * f);
-  v.y = pack_bf16(acc.z * f, acc.w * f);
+  if (group > 0) group_sum[group - 1][tid % 128] = acc;
+  __syncthreads();
+  if (group > 0) return;
+#pragma unroll
+  for (int g = 0; g < kMergeGroups - 1; ++g) {
+    const float4 v = group_sum[g][tid];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+  }
+  const float f = sum == 0.f ? 0.f : 1.f / (sum + exp2_fast(sink - top));
+  const uint2 v = make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
   *reinterpret_cast<uint2*>(p.out + th * kWidth + d) = v;
-  if (p.lse != nullptr && threadIdx.x == 0)
-    p.lse[th] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  if (p.lse != nullptr && tid == 0) p.lse[th] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 int head_blocks_of(int n_h) { return (n_h + kHeadsPerItem - 1) / kHeadsPerItem; }
@@ -1219,7 +1232,7 @@ fm_status launch_attn(AttnParams& p, int sms, void* workspace, cudaStream_t stre
     return set_error(FM_ERR_CUDA, "fm_csa_attn: launch: %s", cudaGetErrorString(e));
   if (p.splits > 1 && !p.cluster) {
     cfg.gridDim = dim3((unsigned)((int64_t)p.T * p.n_h));
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
     if ((e = cudaLaunchKernelEx(&cfg, csa_merge_kernel, (const AttnParams)p)) != cudaSuccess)
       return set_error(FM_ERR_CUDA, "fm_csa_attn: merge launch: %s", cudaGetErrorString(e));
