@@ -77,7 +77,7 @@ constexpr int kKvArrivals = 33 * kProducerWarps;              // the producers' 
 constexpr int kMaxParts = 256;                  // partial results of one call
 constexpr int kMaxCluster = 8;
 constexpr int64_t kMaxItems = int64_t(1) << 23;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
   const uint16_t* q;
@@ -93,7 +93,7 @@ struct AttnParams {
   uint16_t* out;
   float* lse;
   float* part_o;                         // [parts][64][512] unnormalised outputs
-  float2* part_ml;                       // [parts][64] (maximum in log2 units, sum)
+  float2* part_ml;                       // [parts][64] (maximum in units of S, sum)
   unsigned int* status;
   int64_t kv_page_rows, cell_page_rows;  // rows (of 512 elements) from page to page
   int64_t window;
@@ -296,7 +296,7 @@ struct Shared {
   uint2 key_mask[8];                     // the resolver is up to four tiles ahead of the softmax
   ItemInfo info[kInfoSlots];
   alignas(16) uint64_t rows[2][kTileKeys];  // addresses: key 16 w + 2 c + x at 16 w + 8 x + c
-  float2 stat[kHeadsPerItem];            // maximum in log2 units, sum of an item's heads
+  float2 stat[kHeadsPerItem];            // maximum in units of S, sum of an item's heads
   alignas(16) float rescale[kHeadsPerItem];
   float top_half[2][kHeadsPerItem];
   uint32_t tmem_slot;
@@ -386,6 +386,7 @@ FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, uint32_t t
   const int t = th / p.head_blocks, h0 = th % p.head_blocks * kHeadsPerItem;
   const int heads = min(kHeadsPerItem, p.n_h - h0);
   const int slice = kWidth / p.splits;
+  const float c = p.scale * kLog2e;
   cluster_sync();  // every CTA is done with its ring, and its maxima and sums are in place
   if (threadIdx.x < kHeadsPerItem) {
     const int h = threadIdx.x;
@@ -401,12 +402,12 @@ FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, uint32_t t
     }
 #pragma unroll
     for (int s = 0; s < kMaxCluster; ++s)
-      if (ml[s].y != 0.f) total = fmaf(ml[s].y, exp2_fast(ml[s].x - top), total);
+      if (ml[s].y != 0.f) total = fmaf(ml[s].y, exp2_fast((ml[s].x - top) * c), total);
     const float sink = p.sink_logit != nullptr && h < heads ? __ldg(p.sink_logit + h0 + h) * kLog2e : -INFINITY;
     const float2 mine = sh.stat[h];
-    sh.rescale[h] = mine.y == 0.f ? 0.f : exp2_fast(mine.x - top) / (total + exp2_fast(sink - top));
+    sh.rescale[h] = mine.y == 0.f ? 0.f : exp2_fast((mine.x - top) * c) / (total + exp2_fast(fmaf(-c, top, sink)));
     if (rank == 0 && p.lse != nullptr && h < heads)
-      p.lse[(int64_t)t * p.n_h + h0 + h] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+      p.lse[(int64_t)t * p.n_h + h0 + h] = total == 0.f ? -INFINITY : fmaf(top, p.scale, logf(total));
   }
   __syncthreads();
   // 32 heads x 32 elements at a time, scaled, to the CTA whose slice they are in
@@ -938,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (half == 0) {
         if ((lane & 3) == 0) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) sh.stat[r0 + 8 * r] = make_float2(m[r] * c, l[r] + sh.stat[r0 + 8 * r].y);
+          for (int r = 0; r < 2; ++r) sh.stat[r0 + 8 * r] = make_float2(m[r], l[r] + sh.stat[r0 + 8 * r].y);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.stat_full);
@@ -950,6 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // transposed, 32 heads x 32 elements at a time in a quarter of the P buffer
     // that the item's last tile is done with.
     const int quad = warp & 3;
+    const float c = p.scale * kLog2e;
     uint32_t g = 0;
     uint32_t at = 0;  // the current item's tile of queries: its number in the ring's stream, modulo 2 * kTileSlots
     // The queries of item i, from the ring to their place: the first two chunks to
@@ -1015,12 +1017,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       float factor[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        factor[r] = stat[r].y == 0.f ? 0.f : 1.f / (stat[r].y + exp2_fast(sink[r] - stat[r].x));
+        factor[r] = stat[r].y == 0.f ? 0.f : 1.f / (stat[r].y + exp2_fast(fmaf(-c, stat[r].x, sink[r])));
         if (quad == 0) {
           if (part >= 0)
             p.part_ml[(int64_t)part * kHeadsPerItem + lane + 32 * r] = stat[r];
           else if (p.lse != nullptr && lane + 32 * r < heads)
-            p.lse[(int64_t)t * p.n_h + h0 + lane + 32 * r] = stat[r].y == 0.f ? -INFINITY : (stat[r].x + log2f(stat[r].y)) * kLn2;
+            p.lse[(int64_t)t * p.n_h + h0 + lane + 32 * r] = 
+                stat[r].y == 0.f ? -INFINITY : fmaf(stat[r].x, p.scale, logf(stat[r].y));
         }
       }
       if (!warp_wait(&sh.o_full, i & 1, abort, status)) break;
@@ -1087,7 +1090,7 @@ __global__ void __launch_bounds__(kMergeThreads) csa_merge_kernel(const __grid_c
   const int64_t t = th / p.n_h;
   const int64_t part0 = (t * p.head_blocks + h / kHeadsPerItem) * p.splits;
   const int tid = threadIdx.x, group = tid / 128, d = 4 * (tid % 128);
-  const float sink = p.sink_logit != nullptr ? __ldg(p.sink_logit + h) * kLog2e : -INFINITY;
+  const float c = p.scale * kLog2e;
   grid_dep_wait();  // for the partial results
   float2 ml = make_float2(-INFINITY, 0.f);
   if (tid < p.splits) ml = p.part_ml[(part0 + tid) * kHeadsPerItem + hl];
@@ -1101,7 +1104,7 @@ __global__ void __launch_bounds__(kMergeThreads) csa_merge_kernel(const __grid_c
 #pragma unroll
   for (int i = 0; i < kMaxParts / 32; ++i) top = fmaxf(top, warp_top[i]);
   if (tid < kMaxParts) {
-    const float w = ml.y == 0.f ? 0.f : exp2_fast(ml.x - top);  // a split without keys holds zeros
+    const float w = ml.y == 0.f ? 0.f : exp2_fast((ml.x - top) * c);  // a split without keys holds zeros
     weight[tid] = w;
     float part = w * ml.y;
     for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
@@ -1110,6 +1113,7 @@ __global__ void __launch_bounds__(kMergeThreads) csa_merge_kernel(const __grid_c
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kMaxParts / 32; ++i) sum += warp_sum[i];
+  const float sink = p.sink_logit != nullptr ? __ldg(p.sink_logit + h) * kLog2e : -INFINITY;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const float* from = p.part_o + (part0 * kHeadsPerItem + hl) * kWidth + d;
   for (int s0 = group; s0 < p.splits; s0 += 8 * kMergeGroups) {
@@ -1140,10 +1144,10 @@ __global__ void __launch_bounds__(kMergeThreads) csa_merge_kernel(const __grid_c
     acc.z += v.z;
     acc.w += v.w;
   }
-  const float f = sum == 0.f ? 0.f : 1.f / (sum + exp2_fast(sink - top));
+  const float f = sum == 0.f ? 0.f : 1.f / (sum + exp2_fast(fmaf(-c, top, sink)));
   const uint2 v = make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
   *reinterpret_cast<uint2*>(p.out + th * kWidth + d) = v;
-  if (p.lse != nullptr && tid == 0) p.lse[th] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  if (p.lse != nullptr && tid == 0) p.lse[th] = sum == 0.f ? -INFINITY : fmaf(top, p.scale, logf(sum));
 }
 
 int head_blocks_of(int n_h) { return (n_h + kHeadsPerItem - 1) / kHeadsPerItem; }
