@@ -251,10 +251,9 @@ FM_DEV uint32_t timer_lo() {
 }
 
 // A warp's wait for a phase, given up after FM_WAIT_LIMIT_NS or when another
-// warp has given up.  Lane 0 polls.  Some twenty copies of this loop share the
-// instruction cache with the roles' own loops, so it is kept small.
-FM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+// warp has given up.  Lane 0 polls.  A function of its own: some twenty copies
+// of this loop would not leave the roles' loops room in the instruction cache.
+__device__ __noinline__ bool warp_wait_poll(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
   int ok = 1;
   if ((threadIdx.x & 31) == 0) {
     const uint32_t t0 = timer_lo();
@@ -273,6 +272,11 @@ FM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsig
   ok = __shfl_sync(0xffffffffu, ok, 0);
   __syncwarp();
   return ok != 0;
+}
+__device__ __noinline__ void wait_drain(uint64_t* bar) { mbar_wait_drain(bar, 0); }
+FM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait_poll(bar, parity, abort, status);
 }
 
 // The issuers' warps run as a whole and elect the lane that issues, so that the
@@ -382,10 +386,10 @@ FM_DEV uint32_t in_cta(uint32_t smem_addr, uint32_t rank) {  // the same place i
 // the same in every CTA) takes the slices of all CTAs: [split][64 heads][512 / splits].
 FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, uint32_t tmem) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int rank = (int)blockIdx.x % p.splits, th = (int)blockIdx.x / p.splits;
+  const int rank = (int)blockIdx.x & (p.splits - 1), th = (int)blockIdx.x >> (__ffs(p.splits) - 1);
   const int t = th / p.head_blocks, h0 = th % p.head_blocks * kHeadsPerItem;
   const int heads = min(kHeadsPerItem, p.n_h - h0);
-  const int slice = kWidth / p.splits;
+  const int log_splits = __ffs(p.splits) - 1, slice = kWidth >> log_splits;  // (a power of two)
   const float c = p.scale * kLog2e;
   cluster_sync();  // every CTA is done with its ring, and its maxima and sums are in place
   if (threadIdx.x < kHeadsPerItem) {
@@ -411,12 +415,14 @@ FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, uint32_t t
   }
   __syncthreads();
   // 32 heads x 32 elements at a time, scaled, to the CTA whose slice they are in
+#pragma unroll 1
   for (int x = warp >> 2; x < 8; x += kThreads / 128) {
-    const int d = (x >> 1) * 128 + (warp & 3) * 32, to = d / slice;
+    if ((x & 1) && heads <= 32) continue;
+    const int d = (x >> 1) * 128 + (warp & 3) * 32, to = d >> (9 - log_splits);
     uint32_t o[32];
     tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + 32 * x, o);
     tmem_ld_wait();
-    const uint32_t dst = in_cta(smem_u32(buf + (rank * kHeadsPerItem + (x & 1) * 32) * slice + d % slice + lane), to);
+    const uint32_t dst = in_cta(smem_u32(buf + (rank * kHeadsPerItem + (x & 1) * 32) * slice + (d & (slice - 1)) + lane), to);
 #pragma unroll
     for (int h = 0; h < 32; ++h)
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + (uint32_t)(h * slice * 4)),
@@ -424,10 +430,11 @@ FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, uint32_t t
                    : "memory");
   }
   cluster_sync();
-  const int per_head = slice / 4;
-  for (int i = threadIdx.x; i < heads * per_head; i += kThreads) {
-    const int h = i / per_head, d = i % per_head * 4;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < heads * slice / 4; i += kThreads) {
+    const int h = i >> (7 - log_splits), d = (i * 4) & (slice - 1);
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
     for (int s = 0; s < p.splits; ++s) {
       const float4 v = *reinterpret_cast<const float4*>(buf + (s * kHeadsPerItem + h) * slice + d);
       sum.x += v.x;
@@ -543,8 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_cells = __reduce_max_sync(0xffffffffu, last) + 1;
       const TokenKeys tk = token_keys(p, b, pos);
       const int end_first = n_cells + tk.n_first, end_win = end_first + tk.n_win, end = end_win + tk.n_tree;
-      const int64_t tiles = (end + kTileKeys - 1) / kTileKeys;
-      int tile = (int)(tiles * split / p.splits), tile_end = (int)(tiles * (split + 1) / p.splits);
+      const uint32_t tiles = (uint32_t)(end + kTileKeys - 1) / kTileKeys;  // < 2^20, and at most 2^8 splits
+      int tile = (int)(tiles * (uint32_t)split / (uint32_t)p.splits);
+      int tile_end = (int)(tiles * (uint32_t)(split + 1) / (uint32_t)p.splits);
       if (tile == tile_end) {  // a split without keys still runs one tile, of no keys
         tile = (int)tiles;
         tile_end = tile + 1;
@@ -579,8 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (seen && at >= (int64_t)p.R * kPage) {
               atomicOr(status, FM_DEV_PAGE_RANGE);
             } else if (seen) {
-              raw[x] = __ldg(p.page_table + (int64_t)tk.b * p.R + at / kPage);
-              offset[x] = (int)(at % kPage);
+              raw[x] = __ldg(p.page_table + (int64_t)tk.b * p.R + (uint32_t)at / kPage);
+              offset[x] = (int)((uint32_t)at % kPage);
             }
           }
         }
@@ -593,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool cell = tile * kTileKeys + 32 * x + lane < n_cells;
           seen[x] = raw[x] >= 0 && raw[x] < (cell ? p.cell_limit : p.P);
           if (raw[x] >= 0 && !seen[x]) atomicOr(status, FM_DEV_PAGE_RANGE);
-          const int64_t r = cell ? (int64_t)(raw[x] / kPage) * p.cell_page_rows + raw[x] % kPage
+          const int64_t r = cell ? (int64_t)((uint32_t)raw[x] / kPage) * p.cell_page_rows + (uint32_t)raw[x] % kPage
                                  : raw[x] * p.kv_page_rows + offset[x];
           // any address where nothing is read
           row[x] = seen[x] ? reinterpret_cast<uint64_t>((cell ? p.cell_pool : p.kv_pool) + r * kWidth)
@@ -611,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int me = warp - 16, hi = lane >> 4, unit = lane & 15;
     const uint32_t lane_dst = smem_u32(ring) + me * kKeysPerProducer * 128 + (unit >> 3) * kChunkBytes + hi * 128 +
                               (((unit & 7) ^ hi) << 4);
-    uint32_t at = 0, at_phase = 1, g = 0;
+    uint32_t at_phase = 1, g = 0;
     int tile_slot = 0;
     int i = 0, left = 0;  // the current item, its tiles not yet copied
     uint64_t src[8];
@@ -645,9 +653,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       taken = false;
       bool ok = true;
       uint64_t from[8];
+      uint32_t size[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) from[c] = src[c];
-      const uint32_t reads = valid;
+      for (int c = 0; c < 8; ++c) {
+        from[c] = src[c];
+        size[c] = (valid >> (2 * c) & 1u) << 4;
+      }
+      // (only these four addresses and constant offsets: the issue of the copies is
+      // one of the two things that bound a tile)
+      const uint32_t slot_dst = lane_dst + tile_slot * (kPairsPerTile * kPairBytes);
+      const uint32_t dst[4] = {slot_dst, slot_dst ^ 32, slot_dst ^ 64, slot_dst ^ 96};
       ++g;
 #pragma unroll 1
       for (int j = 0; j < kPairsPerTile; ++j) {
@@ -657,22 +672,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           take_rows(g);
           taken = true;
         }
-        if (!(ok = warp_wait(&sh.kv_empty[at], at_phase, abort, status))) break;
-        const uint32_t dst = lane_dst + at * kPairBytes;
+        if (!(ok = warp_wait(&sh.kv_empty[tile_slot * kPairsPerTile + j], at_phase, abort, status))) break;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          cp_async16((dst ^ ((2 * c & 7) << 4)) + c * 256, from[c], (reads >> (2 * c) & 1u) << 4);
-          from[c] += 256;
-        }
-        if (++at == (uint32_t)kPairs) {
-          at = 0;
-          at_phase ^= 1;
-        }
+        for (int c = 0; c < 8; ++c) cp_async16(dst[c & 3] + c * 256 + j * kPairBytes, from[c] + 256 * j, size[c]);
       }
       if (!ok) break;
       cp_async_arrive(&sh.kv_full[tile_slot]);
       if (lane == 0) mbar_arrive(&sh.kv_full[tile_slot]);  // passes the mask on
-      if (++tile_slot == kTileSlots) tile_slot = 0;
+      if (++tile_slot == kTileSlots) {
+        tile_slot = 0;
+        at_phase ^= 1;
+      }
     }
     cp_async_wait_all();
   } else if (warp == 0) {
@@ -734,11 +744,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (one) umma_commit(&sh.drain[0]);
-    if (one) mbar_wait_drain(&sh.drain[0], 0);
+    if (one) wait_drain(&sh.drain[0]);
   } else if (warp == 2) {
     // ------------------------------- O issuer -------------------------------
     const bool one = elect_one();
-    const uint32_t idesc = idesc_bf16_f32(128, kHeadsPerItem) | kAIsMnMajor;
     const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring));
     const uint64_t p_desc = sdesc_sw128(smem_u32(p_smem));
     uint32_t g = 0, at = 0;
@@ -747,7 +756,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < n_mine && ok; ++i) {
       const int slot = i % kInfoSlots;
       if (!warp_wait(&sh.info_full[slot], (i / kInfoSlots) & 1, abort, status)) break;
-      const int tiles = sh.info[slot].tiles;
+      const int tiles = sh.info[slot].tiles, heads = min(kHeadsPerItem, p.n_h - sh.info[slot].head_block * kHeadsPerItem);
+      // N: the heads there are, to a multiple of 16 (a reduction's result is a uniform
+      // value, and an MMA whose operands are not costs its issuer twice the time)
+      const uint32_t idesc = (idesc_bf16_f32(128, 0) | kAIsMnMajor) | ((uint32_t)__reduce_max_sync(0xffffffffu, (heads + 15) / 16) << 18);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
       at += kPairsPerTile;  // the tile of queries
@@ -757,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = warp_wait(&sh.p_full[g & 1], (g >> 1) & 1, abort, status))) break;
         tc_fence_after();
         const uint64_t b = p_desc + (uint64_t)((g & 1) * (kPBytes >> 4));
-#pragma unroll 1
+#pragma unroll
         for (int m = 0; m < kPairsPerTile; ++m) {  // a pair of chunks is a block of 128 elements
           if (tile == 0) {  // the block of the last item has been read
             if (!(ok = warp_wait(&sh.o_empty[m], (i & 1) ^ 1, abort, status))) break;
@@ -776,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && one) umma_commit(&sh.o_full);
     }
     if (one) umma_commit(&sh.drain[1]);
-    if (one) mbar_wait_drain(&sh.drain[1], 0);
+    if (one) wait_drain(&sh.drain[1]);
   } else if (warp >= 4 && warp < 4 + kSoftmaxWarps) {
     // ------------------------------- softmax --------------------------------
     // Warps quad and quad + 4 hold heads 16 quad .. 16 quad + 15 of the block (S's
@@ -1038,6 +1050,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Output out = {p, tmem, smem_u32(p_smem) + ((g - 1) & 1) * kPBytes + quad * kStageBytes, t, h0, -1};
 #pragma unroll 1
       for (int x = 0; x < 8; ++x) {
+        if ((x & 1) && heads <= 32) {
+          if (lane == 0) mbar_arrive(&sh.o_empty[x >> 1]);
+          continue;
+        }
         const float mine = x & 1 ? factor[1] : factor[0];
         float f[8];
 #pragma unroll
@@ -1060,6 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Output out = {p, tmem, smem_u32(ring) + warp * kStageBytes, f.t, f.head_block * kHeadsPerItem, f.part};
 #pragma unroll 1
     for (int x = warp >> 2; x < 8; x += kThreads / 128) {
+      if ((x & 1) && p.n_h - out.h0 <= 32) continue;
       float fac[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) fac[j] = sh.rescale[(x & 1) * 32 + 8 * (j >> 1) + 2 * (lane & 3) + (j & 1)];
