@@ -27,11 +27,24 @@
 // TMEM: O^T 4 x 64 columns, S 64, three quarters of Q 192.  The output is kept
 // transposed (rows = elements) because 64 rows of heads x 512 columns would fill
 // TMEM.
-// What bounds it: a tile's chain (copies, S, softmax, O) is some 5500 cycles, and the
-// ring holds three tiles; shared memory at 128 bytes a cycle: S reads 64 KB of
-// cells and 16 KB of queries, O 64 KB of cells and 32 KB of weights, the copies write
-// 64 KB, 1900 cycles a tile against 1024 + 512 of the tensor cores.  With all of Q
-// in shared memory the ring held 2.25 tiles.
+// What bounds it: a tile takes some 2200 cycles (2400 where its cells are scattered).
+// Timing copies of the kernel with one part removed shows two bounds of about that
+// length, side by side: the copies (128 cp.async of 512 bytes a tile: 31 bytes a
+// cycle, with four and with eight producer warps alike, and without the reads), and
+// the products (S 32 steps of 32 cycles; O 16 steps of at least 48, as it takes 64 KB
+// of cells and 32 KB of weights from shared memory at 128 bytes a cycle; and the
+// switches between the two).  Without both it is the softmax, 1650.  Between items
+// another 3900 cycles: the queries hold a third of the ring, and the item's second
+// tile waits for the slot of the last item's last one.  What all roles pay for is
+// code: a kernel of 107 KB (the waits' loops inlined, 64-bit divisions) took 3 to 9%
+// longer than this one of 80.  With all of Q in shared memory the ring held 2.25
+// tiles (515 us for the prefill below).
+// Measured, alone on the device: 4096 tokens x 64 heads x 644 keys 399 us (866
+// TFLOP/s, 44% of the burst peak of a library's product); 2 x 61 drafted tokens over
+// a window of 4096 76.5 us (766 TFLOP/s on 122 of the 152 SMs); 3065 tokens x 20
+// heads x 186 keys on average 114 us (items of three tiles, and the scores' product
+// is padded to 64 heads); 30 tokens x 644 keys 16.9 us; 76 tokens x 128 heads x 644
+// keys 24.4 us; 8 tokens x 32832 keys 59.4 us (4.5 TB/s); one token x 37 keys 8.5 us.
 //
 // Few tokens: the keys of an item are split over several CTAs.  Up to eight of
 // them are a cluster and join their outputs through distributed shared memory:
