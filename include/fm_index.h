@@ -502,7 +502,7 @@ fm_status fm_qk_norm_rope(const int64_t* pos, int T, int d, int rope_dim, double
  *   cell_pool   [Pc, 64, 512] bf16 with cell_page_stride as kv_pool; cells
  *               [T, k] int32 (dense), 0 <= k <= 1024; an entry at or past Pc * 64 is
  *               skipped and flagged; k = 0: both ignored
- *   sink_logit  [n_h] fp32 or NULL;  scale  > 0, 512^-1/2 as a rule
+ *   sink_logit  [n_h] fp32 or NULL;  scale  > 0 (scale * log2 e finite), 512^-1/2 as a rule
  *   out         [T, n_h, 512] bf16, 16-byte aligned;  lse_out [T, n_h] fp32 or NULL
  *   workspace   >= fm_csa_attn_workspace(T, n_h) bytes, 256-byte aligned (may be
  *               NULL when that is 0): the partial results of tokens whose keys

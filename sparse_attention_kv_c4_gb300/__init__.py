@@ -495,6 +495,8 @@ def fm_qk_norm_rope(pos, q=None, q_gain=None, q_out=None, k=None, k_gain=None, k
             P = k_pool.shape[0]
             kp_p, page_stride = _rows(k_pool, "k_pool", _BF16, (P, 64, n_k * d), dev)
             kc_p = _dense(k_cell, "k_cell", _I32T, (T,), dev)
+    if dev < 0:
+        raise ValueError("the tensors are on the CPU")
     st = lib().fm_qk_norm_rope(_dense(pos, "pos", _I64T, (T,), dev), T, d, rope_dim, rope_base, rope_factor,
                                rope_orig_len, rope_beta_fast, rope_beta_slow, eps, q_p, q_stride, n_q, qg_p, qo_p, k_p,
                                k_stride, n_k, kg_p, ko_p, kp_p, P, page_stride, kc_p, _raw_stream(dev) if stream is None else _stream(stream))
@@ -540,14 +542,16 @@ def _csa_attn(tree, q, kv_pool, page_table, pos, out, window, n_sink, seq, cell_
             _dense(page_table, "page_table", _I32T, (B, R), dev), B, R, seq_p, _dense(pos, "pos", _I64T, (T,), dev),
             window, n_sink, cp_p, Pc, cp_stride, cells_p, k, sink_p, d ** -0.5 if scale is None else scale)
     out_p = _dense(out, "out", _BF16, shape, dev)
-    if tree is None:
-        st = lib().fm_csa_attn(*args, out_p, lse_p, ws_p, ws_bytes, _raw_stream(dev) if stream is None else _stream(stream))
-    else:
+    f, tree_args = lib().fm_csa_attn, ()
+    if tree is not None:
         tree_mask, tree_base = tree
         words = _shape(tree_mask, "tree_mask", 2)[1]
-        st = lib().fm_csa_attn_tree(*args, _dense(tree_mask, "tree_mask", _BITS, (T, words), dev), words,
-                                    _dense(tree_base, "tree_base", _I64T, (B,), dev), out_p, lse_p, ws_p, ws_bytes,
-                                    _raw_stream(dev) if stream is None else _stream(stream))
+        f = lib().fm_csa_attn_tree
+        tree_args = (_dense(tree_mask, "tree_mask", _BITS, (T, words), dev), words,
+                     _dense(tree_base, "tree_base", _I64T, (B,), dev))
+    if dev < 0:
+        raise ValueError("the tensors are on the CPU")
+    st = f(*args, *tree_args, out_p, lse_p, ws_p, ws_bytes, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
 

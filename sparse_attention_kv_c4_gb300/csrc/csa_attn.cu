@@ -420,7 +420,7 @@ FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, uint32_t t
 #pragma unroll
     for (int s = 0; s < kMaxCluster; ++s)
       if (ml[s].y != 0.f) total = fmaf(ml[s].y, exp2_fast((ml[s].x - top) * c), total);
-    const float sink = p.sink_logit != nullptr && h < heads ? __ldg(p.sink_logit + h0 + h) * kLog2e : -INFINITY;
+    const float sink = p.sink_logit != nullptr && h < heads ? p.sink_logit[h0 + h] * kLog2e : -INFINITY;
     const float2 mine = sh.stat[h];
     sh.rescale[h] = mine.y == 0.f ? 0.f : exp2_fast((mine.x - top) * c) / (total + exp2_fast(fmaf(-c, top, sink)));
     if (rank == 0 && p.lse != nullptr && h < heads)
@@ -513,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem_slot;
   // What is above overlaps the kernel before this one; what it wrote is read from
-  // here on.  The kernel after may get ready likewise.
+  // here on (by plain loads: a read-only one is for what no kernel before this one
+  // can still be writing).  The kernel after may get ready likewise.
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int n_mine = (p.items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int item = (int)blockIdx.x + i * (int)gridDim.x;
       const int split = item % p.splits, th = item / p.splits;
       const int t = th / p.head_blocks;
-      const int64_t b = p.seq != nullptr ? __ldg(p.seq + t) : t, pos = __ldg(p.pos + t);
+      const int64_t b = p.seq != nullptr ? p.seq[t] : t, pos = p.pos[t];
       // the tile of queries
       uint64_t row[2];
       bool seen[2];
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* cells = p.cells + (int64_t)t * p.k;
 #pragma unroll 8
       for (int c = lane; c < p.k; c += 32)
-        if (__ldg(cells + c) >= 0) last = c;
+        if (cells[c] >= 0) last = c;
       const int n_cells = __reduce_max_sync(0xffffffffu, last) + 1;
       const TokenKeys tk = token_keys(p, b, pos);
       const int end_first = n_cells + tk.n_first, end_win = end_first + tk.n_win, end = end_win + tk.n_tree;
@@ -586,13 +587,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           raw[x] = -1;
           offset[x] = 0;
           if (s < n_cells) {
-            raw[x] = __ldg(cells + s);
+            raw[x] = cells[s];
           } else if (s < end) {
             int64_t at = s - n_cells;
             bool seen = true;
             if (s >= end_win) {
               const int d = s - end_win;
-              seen = (__ldg(p.tree_mask + (int64_t)t * p.tree_words + (d >> 5)) >> (d & 31)) & 1u;
+              seen = (p.tree_mask[(int64_t)t * p.tree_words + (d >> 5)] >> (d & 31)) & 1u;
               at = tk.base + d;
             } else if (s >= end_first) {
               at = tk.low + (s - end_first);
@@ -600,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (seen && at >= (int64_t)p.R * kPage) {
               atomicOr(status, FM_DEV_PAGE_RANGE);
             } else if (seen) {
-              raw[x] = __ldg(p.page_table + (int64_t)tk.b * p.R + (uint32_t)at / kPage);
+              raw[x] = p.page_table[(int64_t)tk.b * p.R + (uint32_t)at / kPage];
               offset[x] = (int)((uint32_t)at % kPage);
             }
           }
@@ -1029,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sink[2] = {-INFINITY, -INFINITY};  // of heads lane and lane + 32
 #pragma unroll
       for (int r = 0; r < 2; ++r)
-        if (p.sink_logit != nullptr && lane + 32 * r < heads) sink[r] = __ldg(p.sink_logit + h0 + lane + 32 * r) * kLog2e;
+        if (p.sink_logit != nullptr && lane + 32 * r < heads) sink[r] = p.sink_logit[h0 + lane + 32 * r] * kLog2e;
       if (i + 1 < n_mine && !(ok = queries(i + 1))) break;
       if (!warp_wait(&sh.stat_full, i & 1, abort, status)) break;
       if (p.cluster) {  // the whole CTA sees to it, below
@@ -1143,7 +1144,7 @@ __global__ void __launch_bounds__(kMergeThreads) csa_merge_kernel(const __grid_c
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kMaxParts / 32; ++i) sum += warp_sum[i];
-  const float sink = p.sink_logit != nullptr ? __ldg(p.sink_logit + h) * kLog2e : -INFINITY;
+  const float sink = p.sink_logit != nullptr ? p.sink_logit[h] * kLog2e : -INFINITY;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const float* from = p.part_o + (part0 * kHeadsPerItem + hl) * kWidth + d;
   for (int s0 = group; s0 < p.splits; s0 += 8 * kMergeGroups) {
@@ -1288,7 +1289,7 @@ fm_status csa_attn(const char* who, bool tree, const uint16_t* q, int T, int n_h
     return set_error(FM_ERR_INVALID_ARG,
                      "%s: bad sizes B=%d R=%d window=%lld n_sink=%d k=%d (R <= 2^19, 0 <= k <= 1024)", who, B, R,
                      (long long)window, n_sink, k);
-  if (!(scale > 0.0f) || isinf(scale)) return set_error(FM_ERR_INVALID_ARG, "%s: scale=%g", who, (double)scale);
+  if (!(scale > 0.0f) || isinf(scale * kLog2e)) return set_error(FM_ERR_INVALID_ARG, "%s: scale=%g", who, (double)scale);
   if (tree && (tree_words < 1 || tree_words > 32))
     return set_error(FM_ERR_INVALID_ARG, "%s: tree_words=%d (1..32)", who, tree_words);
   // a pool's rows are counted in 31 bits

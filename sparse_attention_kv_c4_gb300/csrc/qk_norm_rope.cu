@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
       sn[j][i] = 0.f;
     }
   const int pairs = (p.d - p.rope_start) >> 1;
-  const uint64_t position = (uint64_t)__ldg(p.pos + t);
+  const uint64_t position = (uint64_t)p.pos[t];
   for (int base = 0; base < pairs; base += 32) {
     float c = 1.f, s = 0.f;
     if (base + lane < pairs) {
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
     } else {
       if (p.k_out != nullptr) dst0 = p.k_out + (t * p.n_k + head) * p.d;
       if (p.k_pool != nullptr) {
-        const int64_t cell = __ldg(p.k_cell + t);
+        const int64_t cell = p.k_cell[t];
         if (cell >= p.pool_rows) {
           if (l == 0 && head == 0) atomicOr(p.status, FM_DEV_PAGE_RANGE);
         } else if (cell >= 0) {
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
       const int v = l + j * LPR;
       if (v >= nvec) continue;
       uint4 g = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);  // ones
-      if (gain != nullptr) g = __ldg(reinterpret_cast<const uint4*>(gain + 8 * v));
+      if (gain != nullptr) g = *reinterpret_cast<const uint4*>(gain + 8 * v);
       const uint32_t u[4] = {x[j].x, x[j].y, x[j].z, x[j].w}, w[4] = {g.x, g.y, g.z, g.w};
       uint32_t y[4];
 #pragma unroll
@@ -233,7 +233,8 @@ FM_API fm_status fm_qk_norm_rope(const int64_t* pos, int T, int d, int rope_dim,
                      "%s: d=%d rope_dim=%d (d: a multiple of 8 up to 1024; rope_dim: even, up to min(d, 256))", who, d,
                      rope_dim);
   if (rope_dim > 0 && (!(rope_base > 1.0) || !(rope_factor >= 1.0) || !(rope_orig_len > 0.0) ||
-                       !(rope_beta_fast > rope_beta_slow)))
+                       !(rope_beta_fast > rope_beta_slow) || isinf(rope_base) || isinf(rope_factor) ||
+                       isinf(rope_orig_len) || isinf(rope_beta_fast - rope_beta_slow)))
     return set_error(FM_ERR_INVALID_ARG, "%s: bad rotary parameters", who);
   if (!(eps >= 0.0f)) return set_error(FM_ERR_INVALID_ARG, "%s: eps=%g", who, (double)eps);
   if (T == 0 || n_q + n_k == 0) return FM_OK;

@@ -4,6 +4,7 @@ strides."""
 import pytest
 
 FAKE = 4096  # never dereferenced: validation fails first
+NOT_THE_DEVICE = "^(?!the tensors are on the CPU)"  # refused for another reason than that
 
 
 @pytest.fixture(scope="module")
@@ -28,7 +29,9 @@ def test_norm_rope_refusals(fm):
         return f(*dict(good, **new).values())
     for bad in (dict(T=-1), dict(nq=-1), dict(nq=4096), dict(d=0), dict(d=12), dict(d=1032), dict(rope=-2), dict(rope=3),
                 dict(rope=258), dict(d=32, rope=34), dict(base=1.0), dict(factor=0.5), dict(orig=0.0), dict(fast=1.0),
-                dict(base=float("nan")), dict(eps=-1.0), dict(eps=float("nan")), dict(pos=None), dict(q=None),
+                dict(base=float("nan")),
+                dict(base=float("inf")), dict(factor=float("inf")), dict(orig=float("inf")), dict(fast=float("inf")),
+                dict(slow=float("-inf")), dict(eps=-1.0), dict(eps=float("nan")), dict(pos=None), dict(q=None),
                 dict(qo=None), dict(k=None), dict(kp=None), dict(kc=None), dict(P=-1), dict(P=(1 << 25) + 1),
                 dict(kps=64 * 512 - 8), dict(kps=64 * 512 + 4), dict(qs=64 * 512 - 8), dict(qs=64 * 512 + 4),
                 dict(ks=504), dict(ks=513), dict(pos=FAKE + 4), dict(q=FAKE + 8), dict(qo=FAKE + 2), dict(qg=FAKE + 2),
@@ -56,7 +59,7 @@ def test_attention_refusals(fm):
         return first
     for bad in (dict(d=128), dict(T=-1), dict(H=0), dict(H=1025), dict(T=1 << 23, H=2), dict(T=1 << 22, H=65), dict(B=-1), dict(R=-1),
                 dict(R=(1 << 19) + 1), dict(window=-1), dict(n_sink=-1), dict(k=-1), dict(k=1025), dict(scale=0.0),
-                dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(P=-1), dict(kv=None),
+                dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(P=-1), dict(kv=None),
                 dict(kv=FAKE + 8), dict(kvs=page - 512), dict(kvs=page + 8), dict(P=1 << 25), dict(kvs=1 << 45),
                 dict(Pc=-1), dict(cp=None), dict(cps=page + 64), dict(Pc=1 << 25), dict(seq=None, T=5), dict(q=None),
                 dict(pos=None), dict(out=None), dict(cells=None), dict(pt=None), dict(q=FAKE + 8), dict(out=FAKE + 2),
@@ -85,18 +88,31 @@ def test_python_wrappers_check_their_tensors(fm):
                 dict(cells=i32(2, 5)), dict(cell_pool=bf(3, 64, 512)), dict(cell_pool=bf(3, 64, 512), cells=i32(3, 5)),
                 dict(cell_pool=bf(3, 64, 512), cells=i32(5, 2).t()), dict(sink_logit=torch.zeros(3)),
                 dict(lse_out=torch.zeros(2, 5)), dict(workspace=i32(64))):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match=NOT_THE_DEVICE):
             fm.fm_csa_attn(**dict(good, **bad), stream=0)
     for bad in (dict(tree_mask=i32(3, 1)), dict(tree_base=i32(2)), dict(tree_mask=torch.zeros(2, 1))):
         args = dict(good, tree_mask=i32(2, 1), tree_base=torch.zeros(2, dtype=torch.int64))
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match=NOT_THE_DEVICE):
             fm.fm_csa_attn_tree(**dict(args, **bad), stream=0)
     pos = torch.zeros(2, dtype=torch.int64)
     for bad in (dict(), dict(q=bf(2, 4, 64)), dict(q=bf(2, 4, 64), q_out=bf(2, 4, 32)), dict(k=bf(2, 1, 64)),
                 dict(k=bf(2, 1, 64), k_pool=bf(2, 64, 64)), dict(k=bf(2, 1, 64), k_pool=bf(2, 32, 64), k_cell=i32(2)),
                 dict(q=bf(2, 64, 4).transpose(1, 2), q_out=bf(2, 4, 64)),
                 dict(q=bf(2, 4, 64), q_out=bf(2, 4, 64), q_gain=bf(32))):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match=NOT_THE_DEVICE):
             fm.fm_qk_norm_rope(pos, **bad, stream=0)
     with pytest.raises(TypeError):
         fm.fm_qk_norm_rope(pos, q=bf(2, 4, 64), q_out=bf(2, 4, 64), rope_size=3)
+
+
+def test_python_wrappers_refuse_tensors_of_the_cpu(fm):
+    import torch
+    q, pos = torch.zeros((2, 4, 512), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int64)
+    args = dict(q=q, kv_pool=torch.zeros((3, 64, 512), dtype=torch.bfloat16), pos=pos, out=q.clone(), window=8,
+                page_table=torch.zeros((2, 2), dtype=torch.int32))
+    with pytest.raises(ValueError, match="on the CPU"):
+        fm.fm_csa_attn(**args, stream=0)
+    with pytest.raises(ValueError, match="on the CPU"):
+        fm.fm_csa_attn_tree(**args, tree_mask=torch.zeros((2, 1), dtype=torch.int32), tree_base=pos, stream=0)
+    with pytest.raises(ValueError, match="on the CPU"):
+        fm.fm_qk_norm_rope(pos, q=q, q_out=q.clone(), stream=0)
