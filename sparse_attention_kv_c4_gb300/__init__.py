@@ -396,7 +396,7 @@ _current_device = _raw_stream = None
 def _types():
     import torch
     global _BF16, _BITS, _I32T, _I64T, _F32T, _U8T, _current_device, _raw_stream
-    _current_device = torch.cuda.current_device
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     # the current stream's handle alone: a tenth of the time of current_stream()
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -408,11 +408,11 @@ def _types():
 def _refuse(t, name, types, shape, dev, rows):
     if t.dtype not in types:
         raise ValueError(f"{name}: dtype {t.dtype}, need {' or '.join(sorted(map(str, types)))}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {tuple(shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the other tensors are on {'cuda:%d' % dev if dev >= 0 else 'cpu'}")
-    raise ValueError(f"{name}: strides {t.stride()} of shape {shape}: "
+    raise ValueError(f"{name}: strides {t.stride()} of shape {tuple(shape)}: "
                      f"{'all but the first dimension' if rows else 'the tensor'} must be dense")
 
 
@@ -450,7 +450,7 @@ def _shape(t, name, dims):
     shape = t.shape
     if len(shape) != dims:
         raise ValueError(f"{name}: shape {tuple(shape)}, need {dims} dimensions")
-    return tuple(shape)
+    return shape
 
 
 def fm_qk_norm_rope(pos, q=None, q_gain=None, q_out=None, k=None, k_gain=None, k_out=None, k_pool=None, k_cell=None,
@@ -467,13 +467,13 @@ def fm_qk_norm_rope(pos, q=None, q_gain=None, q_out=None, k=None, k_gain=None, k
     if q is None and k is None:
         raise ValueError("q or k is needed")
     dev = _device(pos, "pos")
-    T, _, d = _shape(q if k is None or q is not None else k, "q" if q is not None else "k", 3)
+    T, _, d = _shape(k, "k", 3) if q is None else _shape(q, "q", 3)
     n_q = n_k = P = q_stride = k_stride = page_stride = 0
     q_p = qg_p = qo_p = k_p = kg_p = ko_p = kp_p = kc_p = None
     if q is not None:
         if q_out is None:
             raise ValueError("q needs q_out")
-        shape = _shape(q, "q", 3)
+        shape = q.shape
         n_q = shape[1]
         q_p, q_stride = _rows(q, "q", _BF16, (T, n_q, d), dev)
         qo_p = _dense(q_out, "q_out", _BF16, shape, dev)
