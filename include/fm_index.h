@@ -454,6 +454,8 @@ fm_status fm_index_prefill_topk(const uint16_t* q, const float* w, const int64_t
  *   T >= 0; n_q, n_k >= 0 (0: that side's pointers are ignored), n_q + n_k <= 4096
  *   d         a multiple of 8, 8 <= d <= 1024
  *   rope_dim  even, 0 <= rope_dim <= min(d, 256); 0: norm only
+ *   rotation  rope_base > 1, rope_factor >= 1, rope_orig_len > 0, rope_beta_fast >
+ *             rope_beta_slow, all finite;  eps >= 0
  *   strides   multiples of 8 elements, q_stride_t >= n_q * d, k_stride_t >=
  *             n_k * d, k_page_stride >= 64 * n_k * d; q, k, the gains and the
  *             outputs 16-byte aligned

@@ -27,29 +27,32 @@
 // TMEM: O^T 4 x 64 columns, S 64, three quarters of Q 192.  The output is kept
 // transposed (rows = elements) because 64 rows of heads x 512 columns would fill
 // TMEM.
-// What bounds it: a tile takes some 2200 cycles (2400 where its cells are scattered).
-// Timing copies of the kernel with one part removed shows two bounds of about that
-// length, side by side: the copies (128 cp.async of 512 bytes a tile: 31 bytes a
-// cycle, with four and with eight producer warps alike, and without the reads), and
-// the products (S 32 steps of 32 cycles; O 16 steps of at least 48, as it takes 64 KB
-// of cells and 32 KB of weights from shared memory at 128 bytes a cycle; and the
-// switches between the two).  Without both it is the softmax, 1650.  Between items
+// What bounds it: a tile takes some 2200 cycles (2400 where its cells are scattered),
+// a third of what its slot of the ring goes through: the copies (128 cp.async of 512
+// bytes, 16 cycles of the SM each with four and with eight producer warps alike, and
+// not much less without the reads: 2080), S (32 steps of 32 cycles), the softmax
+// (some 1500) and O (16 steps of at least 48: it takes 64 KB of cells and 32 KB of
+// weights from shared memory at 128 bytes a cycle).  Copies of the kernel with a part
+// removed (2 x 61 drafted tokens, 77 us): three quarters of O and half of S gone 72,
+// half of the copies gone too 65, all copies gone 55, only the copies gone 81 (S and O
+// then interleave more, and each switch between the two costs).  Between items
 // another 3900 cycles: the queries hold a third of the ring, and the item's second
 // tile waits for the slot of the last item's last one.  What all roles pay for is
 // code: a kernel of 107 KB (the waits' loops inlined, 64-bit divisions) took 3 to 9%
 // longer than this one of 80.  With all of Q in shared memory the ring held 2.25
 // tiles (515 us for the prefill below).
-// Measured, alone on the device: 4096 tokens x 64 heads x 644 keys 399 us (866
+// Measured, calls queued on a stream: 4096 tokens x 64 heads x 644 keys 399 us (866
 // TFLOP/s, 44% of the burst peak of a library's product); 2 x 61 drafted tokens over
 // a window of 4096 76.5 us (766 TFLOP/s on 122 of the 152 SMs); 3065 tokens x 20
 // heads x 186 keys on average 114 us (items of three tiles, and the scores' product
-// is padded to 64 heads); 30 tokens x 644 keys 16.9 us; 76 tokens x 128 heads x 644
-// keys 24.4 us; 8 tokens x 32832 keys 59.4 us (4.5 TB/s); one token x 37 keys 8.5 us.
+// is padded to 64 heads); 30 tokens x 644 keys 16.1 us; 76 tokens x 128 heads x 644
+// keys 21.2 us; 8 tokens x 32832 keys 59.4 us (4.5 TB/s); one token x 37 keys 8.2 us.
 //
 // Few tokens: the keys of an item are split over several CTAs.  Up to eight of
 // them are a cluster and join their outputs through distributed shared memory:
-// each CTA scales its own by its share of the common softmax and sends every
-// other one that one's slice of the 512 elements.  More than eight (few tokens
+// each CTA sends every other one that one's slice of the 512 elements of its output,
+// and sums the slices that it gets by the splits' shares of the common softmax, worked
+// out beside the sends (30 tokens: 16.3 -> 16.05 us).  More than eight (few tokens
 // with long key lists) write unnormalised fp32 outputs with their maximum and
 // sum, and csa_merge_kernel joins those.  Both in a fixed order.
 #include <cuda_bf16.h>
@@ -396,8 +399,9 @@ FM_DEV uint32_t in_cta(uint32_t smem_addr, uint32_t rank) {  // the same place i
 
 // The end of an item whose splits are a cluster, by all threads of its CTAs.
 // CTA r writes elements r * 512 / splits .. of the output; `buf` (the idle ring,
-// the same in every CTA) takes the slices of all CTAs: [split][64 heads][512 / splits].
-FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, uint32_t tmem) {
+// the same in every CTA) takes the slices of all CTAs: [split][64 heads][512 / splits],
+// and `share` (an idle P buffer) the splits' shares [split][64].
+FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, float* share, uint32_t tmem) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = (int)blockIdx.x & (p.splits - 1), th = (int)blockIdx.x >> (__ffs(p.splits) - 1);
   const int t = th / p.head_blocks, h0 = th % p.head_blocks * kHeadsPerItem;
@@ -405,8 +409,22 @@ FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, uint32_t t
   const int log_splits = __ffs(p.splits) - 1, slice = kWidth >> log_splits;  // (a power of two)
   const float c = p.scale * kLog2e;
   cluster_sync();  // every CTA is done with its ring, and its maxima and sums are in place
-  if (threadIdx.x < kHeadsPerItem) {
-    const int h = threadIdx.x;
+  // 32 heads x 32 elements at a time to the CTA whose slice they are in
+#pragma unroll 1
+  for (int x = warp >> 2; x < 8; x += kThreads / 128) {
+    if ((x & 1) && heads <= 32) continue;
+    const int d = (x >> 1) * 128 + (warp & 3) * 32, to = d >> (9 - log_splits);
+    uint32_t o[32];
+    tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + 32 * x, o);
+    tmem_ld_wait();
+    const uint32_t dst = in_cta(smem_u32(buf + (rank * kHeadsPerItem + (x & 1) * 32) * slice + (d & (slice - 1)) + lane), to);
+#pragma unroll
+    for (int h = 0; h < 32; ++h)
+      asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst + (uint32_t)(h * slice * 4)), "r"(o[h]) : "memory");
+  }
+  // each split's share of the common softmax
+  if (warp >= 16 && warp < 18) {  // (which have the least to send)
+    const int h = threadIdx.x - 16 * 32;
     const uint32_t at = smem_u32(&sh.stat[h]);
     float2 ml[kMaxCluster];
     float top = -INFINITY, total = 0.f;
@@ -421,26 +439,12 @@ FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, uint32_t t
     for (int s = 0; s < kMaxCluster; ++s)
       if (ml[s].y != 0.f) total = fmaf(ml[s].y, exp2_fast((ml[s].x - top) * c), total);
     const float sink = p.sink_logit != nullptr && h < heads ? p.sink_logit[h0 + h] * kLog2e : -INFINITY;
-    const float2 mine = sh.stat[h];
-    sh.rescale[h] = mine.y == 0.f ? 0.f : exp2_fast((mine.x - top) * c) / (total + exp2_fast(fmaf(-c, top, sink)));
+    const float norm = 1.f / (total + exp2_fast(fmaf(-c, top, sink)));
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s)
+      share[s * kHeadsPerItem + h] = ml[s].y == 0.f ? 0.f : exp2_fast((ml[s].x - top) * c) * norm;
     if (rank == 0 && p.lse != nullptr && h < heads)
       p.lse[(int64_t)t * p.n_h + h0 + h] = total == 0.f ? -INFINITY : fmaf(top, p.scale, logf(total));
-  }
-  __syncthreads();
-  // 32 heads x 32 elements at a time, scaled, to the CTA whose slice they are in
-#pragma unroll 1
-  for (int x = warp >> 2; x < 8; x += kThreads / 128) {
-    if ((x & 1) && heads <= 32) continue;
-    const int d = (x >> 1) * 128 + (warp & 3) * 32, to = d >> (9 - log_splits);
-    uint32_t o[32];
-    tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + 32 * x, o);
-    tmem_ld_wait();
-    const uint32_t dst = in_cta(smem_u32(buf + (rank * kHeadsPerItem + (x & 1) * 32) * slice + (d & (slice - 1)) + lane), to);
-#pragma unroll
-    for (int h = 0; h < 32; ++h)
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + (uint32_t)(h * slice * 4)),
-                   "f"(__uint_as_float(o[h]) * sh.rescale[(x & 1) * 32 + h])
-                   : "memory");
   }
   cluster_sync();
 #pragma unroll 1
@@ -450,10 +454,11 @@ FM_DEV void join_cluster(const AttnParams& p, Shared& sh, float* buf, uint32_t t
 #pragma unroll 2
     for (int s = 0; s < p.splits; ++s) {
       const float4 v = *reinterpret_cast<const float4*>(buf + (s * kHeadsPerItem + h) * slice + d);
-      sum.x += v.x;
-      sum.y += v.y;
-      sum.z += v.z;
-      sum.w += v.w;
+      const float f = share[s * kHeadsPerItem + h];
+      sum.x = fmaf(f, v.x, sum.x);
+      sum.y = fmaf(f, v.y, sum.y);
+      sum.z = fmaf(f, v.z, sum.z);
+      sum.w = fmaf(f, v.w, sum.w);
     }
     const uint2 v = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
     *reinterpret_cast<uint2*>(p.out + ((int64_t)t * p.n_h + h0 + h) * kWidth + rank * slice + d) = v;
@@ -724,7 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           at = 0;
           at_phase ^= 1;
         }
-        // (one wait to a tile: four of them cost the issuer more than the later start)
+        // (one wait to a tile: with one to each half or quarter the scores start earlier,
+        // but the two issuers' products interleave more: tree of 61 tokens 77 -> 87 us)
         if (!(ok = warp_wait(&sh.kv_full[at], at_phase, abort, status))) break;
         if (!(ok = warp_wait(&sh.s_empty, (g & 1) ^ 1, abort, status))) break;
         fence_proxy_async();  // the copies were written through the generic proxy
@@ -1083,7 +1089,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (p.cluster) {
-    join_cluster(p, sh, reinterpret_cast<float*>(ring), tmem);
+    join_cluster(p, sh, reinterpret_cast<float*>(ring), reinterpret_cast<float*>(p_smem), tmem);
   } else if (n_mine > 0 && sh.abort_flag == 0) {
     // the last item, by all warps: a half block of its output at a time each
     const ItemInfo f = sh.info[(n_mine - 1) % kInfoSlots];
