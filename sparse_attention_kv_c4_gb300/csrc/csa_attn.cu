@@ -41,7 +41,7 @@
 // code: a kernel of 107 KB (the waits' loops inlined, 64-bit divisions) took 3 to 9%
 // longer than this one of 80.  With all of Q in shared memory the ring held 2.25
 // tiles (515 us for the prefill below).
-// Measured, calls queued on a stream: 4096 tokens x 64 heads x 644 keys 399 us (866
+// Measured, calls on the same inputs queued on a stream: 4096 tokens x 64 heads x 644 keys 399 us (866
 // TFLOP/s, 44% of the burst peak of a library's product); 2 x 61 drafted tokens over
 // a window of 4096 76.5 us (766 TFLOP/s on 122 of the 152 SMs); 3065 tokens x 20
 // heads x 186 keys on average 114 us (items of three tiles, and the scores' product

@@ -15,7 +15,7 @@
 // row that it handles, so their sines are worked out once per token, a pair to a
 // lane, passed by shuffle and kept in registers.
 //
-// Measured (4096 tokens x 65 heads x 512, 545 MB): 90 us, 6.0 TB/s, 89% of the
+// Measured (4096 tokens x 65 heads x 512, 545 MB): 87.5 us, 6.2 TB/s, 92% of the
 // measured copy rate.  What it took: the next row's load ahead of the current
 // row's sums (107 -> 92 us with the sines below), and few registers -- the gains held
 // in registers as well cost an occupancy step and 16 us.
