@@ -506,3 +506,16 @@ def test_the_layer_from_selection_to_output(torch_dev):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, eager) and fm.fm_device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("H", [2, 15, 17, 31, 32, 33, 48, 49, 63, 80, 97])
+@pytest.mark.parametrize("seqs,window", [([(1, 2600)], 2601),    # through memory
+                                         ([(30, 300)], 150),     # by clusters
+                                         ([(200, 230)], 100)])   # several items to a CTA
+def test_head_counts(torch_dev, H, seqs, window):
+    """Head blocks that are not full, with a maximum that moves: nothing of the
+    heads that are not there gets into the others."""
+    torch, dev = torch_dev
+    b = Batch(500 + H + window, seqs, H, 40, window, 2, magnitude=6.0).device(torch, dev)
+    b.call()
+    b.check(torch)
