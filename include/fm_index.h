@@ -469,6 +469,30 @@ fm_status fm_qk_norm_rope(const int64_t* pos, int T, int d, int rope_dim, double
                           uint16_t* k_pool, int64_t P, int64_t k_page_stride, const int32_t* k_cell,
                           fm_stream_t stream);
 
+/* The same call with its arguments in a struct, for callers that pay for each
+ * argument that crosses a language's border (ctypes: 0.1 us each). */
+typedef struct fm_qk_norm_rope_args {
+  const int64_t* pos;
+  int T, d, rope_dim;
+  double rope_base, rope_factor, rope_orig_len, rope_beta_fast, rope_beta_slow;
+  float eps;
+  const uint16_t* q;
+  int64_t q_stride_t;
+  int n_q;
+  const uint16_t* q_gain;
+  uint16_t* q_out;
+  const uint16_t* k;
+  int64_t k_stride_t;
+  int n_k;
+  const uint16_t* k_gain;
+  uint16_t* k_out;
+  uint16_t* k_pool;
+  int64_t P, k_page_stride;
+  const int32_t* k_cell;
+  fm_stream_t stream;
+} fm_qk_norm_rope_args;
+fm_status fm_qk_norm_rope_packed(const fm_qk_norm_rope_args* args);
+
 /*
  * Attention of a CSA layer: one softmax over the selected chunk cells, the
  * first tokens of the sequence and a sliding window of its last tokens ([V4]
@@ -541,6 +565,37 @@ fm_status fm_csa_attn_tree(const uint16_t* q, int T, int n_h, int d, const uint1
                            int64_t cell_page_stride, const int32_t* cells, int k, const float* sink_logit, float scale,
                            const uint32_t* tree_mask, int tree_words, const int64_t* tree_base, uint16_t* out,
                            float* lse_out, void* workspace, size_t workspace_bytes, fm_stream_t stream);
+
+/* Both calls with their arguments in a struct: fm_csa_attn_tree where tree != 0,
+ * else fm_csa_attn, which ignores the three fields behind it. */
+typedef struct fm_csa_attn_args {
+  const uint16_t* q;
+  int T, n_h, d;
+  const uint16_t* kv_pool;
+  int64_t P, kv_page_stride;
+  const int32_t* page_table;
+  int B, R;
+  const int32_t* seq;
+  const int64_t* pos;
+  int64_t window;
+  int n_sink;
+  const uint16_t* cell_pool;
+  int64_t Pc, cell_page_stride;
+  const int32_t* cells;
+  int k;
+  const float* sink_logit;
+  float scale;
+  int tree;
+  const uint32_t* tree_mask;
+  int tree_words;
+  const int64_t* tree_base;
+  uint16_t* out;
+  float* lse_out;
+  void* workspace;
+  size_t workspace_bytes;
+  fm_stream_t stream;
+} fm_csa_attn_args;
+fm_status fm_csa_attn_packed(const fm_csa_attn_args* args);
 
 /*
  * Device status word of the current device: the OR of FM_DEVERR_* bits set by

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "FmError", "lib", "fm_version", "fm_last_error", "fm_device_status", "fm_check_device_status", "fm_memindex_score_mask",
@@ -111,7 +112,8 @@ def lib() -> ctypes.CDLL:
             _D = ctypes.c_double
             L.fm_qk_norm_rope.argtypes = [_VP, _I32, _I32, _I32, _D, _D, _D, _D, _D, _F, _VP, _I64, _I32, _VP, _VP, _VP,
                                           _I64, _I32, _VP, _VP, _VP, _I64, _I64, _VP, _VP]
-            L.fm_qk_norm_rope.restype = ctypes.c_int
+            L.fm_qk_norm_rope.restype = L.fm_qk_norm_rope_packed.restype = ctypes.c_int
+            L.fm_qk_norm_rope_packed.argtypes = [ctypes.c_char_p]
         if hasattr(L, "fm_csa_attn"):
             L.fm_csa_attn_workspace.argtypes = [_I32, _I32]
             L.fm_csa_attn_workspace.restype = _SZ
@@ -120,7 +122,8 @@ def lib() -> ctypes.CDLL:
             tail = [_VP, _VP, _VP, _SZ, _VP]
             L.fm_csa_attn.argtypes = head + tail
             L.fm_csa_attn_tree.argtypes = head + [_VP, _I32, _VP] + tail
-            L.fm_csa_attn.restype = L.fm_csa_attn_tree.restype = ctypes.c_int
+            L.fm_csa_attn_packed.argtypes = [ctypes.c_char_p]
+            L.fm_csa_attn.restype = L.fm_csa_attn_tree.restype = L.fm_csa_attn_packed.restype = ctypes.c_int
         if hasattr(L, "fm_page_recall"):
             L.fm_page_recall.argtypes = [_VP, _I32, _I64, _I64, _I64, _I32, _VP, _VP, _VP, _VP]
         for name in ("fm_memindex_score_mask", "fm_topk_select", "fm_native_topk_paged", "fm_index_prefill_topk",
@@ -389,6 +392,9 @@ def fm_page_recall(mask, S: int, kmax: int, pages_out, density_out=None, n_out=N
 # The wrappers below check every tensor they are given, on each call; a decode step
 # waits for that, so the checks of an accepted tensor are a few attribute reads and
 # the reasons are worked out only for a refused one.
+# fm_qk_norm_rope_args and fm_csa_attn_args: one argument through ctypes instead of 25
+_QK_ARGS = struct.Struct("@P3i5dfPqi3Pqi3P2q2P")
+_ATTN_ARGS = struct.Struct("@P3iP2qP2i2PqiP2qPiPfiPi4PNP")
 _BF16 = _BITS = _I32T = _I64T = _F32T = _U8T = frozenset()  # accepted element types, set by _types()
 _current_device = _raw_stream = None
 
@@ -469,7 +475,7 @@ def fm_qk_norm_rope(pos, q=None, q_gain=None, q_out=None, k=None, k_gain=None, k
     dev = _device(pos, "pos")
     T, _, d = _shape(k, "k", 3) if q is None else _shape(q, "q", 3)
     n_q = n_k = P = q_stride = k_stride = page_stride = 0
-    q_p = qg_p = qo_p = k_p = kg_p = ko_p = kp_p = kc_p = None
+    q_p = qg_p = qo_p = k_p = kg_p = ko_p = kp_p = kc_p = 0
     if q is not None:
         if q_out is None:
             raise ValueError("q needs q_out")
@@ -495,11 +501,16 @@ def fm_qk_norm_rope(pos, q=None, q_gain=None, q_out=None, k=None, k_gain=None, k
             P = k_pool.shape[0]
             kp_p, page_stride = _rows(k_pool, "k_pool", _BF16, (P, 64, n_k * d), dev)
             kc_p = _dense(k_cell, "k_cell", _I32T, (T,), dev)
+    pos_p = _dense(pos, "pos", _I64T, (T,), dev)
     if dev < 0:
         raise ValueError("the tensors are on the CPU")
-    st = lib().fm_qk_norm_rope(_dense(pos, "pos", _I64T, (T,), dev), T, d, rope_dim, rope_base, rope_factor,
-                               rope_orig_len, rope_beta_fast, rope_beta_slow, eps, q_p, q_stride, n_q, qg_p, qo_p, k_p,
-                               k_stride, n_k, kg_p, ko_p, kp_p, P, page_stride, kc_p, _raw_stream(dev) if stream is None else _stream(stream))
+    try:
+        args = _QK_ARGS.pack(pos_p, T, d, rope_dim, rope_base, rope_factor, rope_orig_len, rope_beta_fast, rope_beta_slow,
+                             eps, q_p, q_stride, n_q, qg_p, qo_p, k_p, k_stride, n_k, kg_p, ko_p, kp_p, P, page_stride,
+                             kc_p, _raw_stream(dev) if stream is None else _stream(stream))
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"fm_qk_norm_rope: {e}") from None
+    st = lib().fm_qk_norm_rope_packed(args)
     if st:
         _check(st)
 
@@ -516,7 +527,7 @@ def _csa_attn(tree, q, kv_pool, page_table, pos, out, window, n_sink, seq, cell_
     P = kv_pool.shape[0]
     kv_p, kv_stride = _rows(kv_pool, "kv_pool", _BF16, (P, 64, d), dev)
     B, R = _shape(page_table, "page_table", 2)
-    seq_p = sink_p = lse_p = cp_p = cells_p = None
+    seq_p = sink_p = lse_p = cp_p = cells_p = 0
     k = Pc = 0
     cp_stride = 64 * d
     if seq is not None:
@@ -534,24 +545,28 @@ def _csa_attn(tree, q, kv_pool, page_table, pos, out, window, n_sink, seq, cell_
         sink_p = _dense(sink_logit, "sink_logit", _F32T, (n_h,), dev)
     if lse_out is not None:
         lse_p = _dense(lse_out, "lse_out", _F32T, (T, n_h), dev)
-    ws_p, ws_bytes = None, 0
+    ws_p = ws_bytes = 0
     if workspace is not None:
         ws_bytes = workspace.shape[0]
-        ws_p = _dense(workspace, "workspace", _U8T, (ws_bytes,), dev) or None
-    args = (_dense(q, "q", _BF16, shape, dev), T, n_h, d, kv_p, P, kv_stride,
-            _dense(page_table, "page_table", _I32T, (B, R), dev), B, R, seq_p, _dense(pos, "pos", _I64T, (T,), dev),
-            window, n_sink, cp_p, Pc, cp_stride, cells_p, k, sink_p, d ** -0.5 if scale is None else scale)
-    out_p = _dense(out, "out", _BF16, shape, dev)
-    f, tree_args = lib().fm_csa_attn, ()
+        ws_p = _dense(workspace, "workspace", _U8T, (ws_bytes,), dev)
+    mask_p = base_p = words = 0
     if tree is not None:
         tree_mask, tree_base = tree
         words = _shape(tree_mask, "tree_mask", 2)[1]
-        f = lib().fm_csa_attn_tree
-        tree_args = (_dense(tree_mask, "tree_mask", _BITS, (T, words), dev), words,
-                     _dense(tree_base, "tree_base", _I64T, (B,), dev))
+        mask_p = _dense(tree_mask, "tree_mask", _BITS, (T, words), dev)
+        base_p = _dense(tree_base, "tree_base", _I64T, (B,), dev)
+    q_p, out_p = _dense(q, "q", _BF16, shape, dev), _dense(out, "out", _BF16, shape, dev)
+    table_p, pos_p = _dense(page_table, "page_table", _I32T, (B, R), dev), _dense(pos, "pos", _I64T, (T,), dev)
     if dev < 0:
         raise ValueError("the tensors are on the CPU")
-    st = f(*args, *tree_args, out_p, lse_p, ws_p, ws_bytes, _raw_stream(dev) if stream is None else _stream(stream))
+    try:
+        args = _ATTN_ARGS.pack(q_p, T, n_h, d, kv_p, P, kv_stride, table_p, B, R, seq_p, pos_p, window, n_sink, cp_p, Pc,
+                               cp_stride, cells_p, k, sink_p, d ** -0.5 if scale is None else scale, tree is not None,
+                               mask_p, words, base_p, out_p, lse_p, ws_p, ws_bytes,
+                               _raw_stream(dev) if stream is None else _stream(stream))
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"fm_csa_attn: {e}") from None
+    st = lib().fm_csa_attn_packed(args)
     if st:
         _check(st)
 

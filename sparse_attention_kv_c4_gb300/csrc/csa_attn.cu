@@ -1384,3 +1384,13 @@ FM_API fm_status fm_csa_attn_tree(const uint16_t* q, int T, int n_h, int d, cons
                       window, n_sink, cell_pool, Pc, cell_page_stride, cells, k, sink_logit, scale, tree_mask, tree_words,
                       tree_base, out, lse_out, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
+
+FM_API fm_status fm_csa_attn_packed(const fm_csa_attn_args* a) {
+  if (!a) return fm::set_error(FM_ERR_INVALID_ARG, "fm_csa_attn_packed: args is NULL");
+  const bool tree = a->tree != 0;
+  return fm::csa_attn(tree ? "fm_csa_attn_tree" : "fm_csa_attn", tree, a->q, a->T, a->n_h, a->d, a->kv_pool, a->P,
+                      a->kv_page_stride, a->page_table, a->B, a->R, a->seq, a->pos, a->window, a->n_sink, a->cell_pool,
+                      a->Pc, a->cell_page_stride, a->cells, a->k, a->sink_logit, a->scale, tree ? a->tree_mask : nullptr,
+                      tree ? a->tree_words : 0, tree ? a->tree_base : nullptr, a->out, a->lse_out, a->workspace,
+                      a->workspace_bytes, reinterpret_cast<cudaStream_t>(a->stream));
+}

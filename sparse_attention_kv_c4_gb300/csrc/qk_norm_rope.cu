@@ -320,3 +320,11 @@ FM_API fm_status fm_qk_norm_rope(const int64_t* pos, int T, int d, int rope_dim,
   if (e != cudaSuccess) return set_error(FM_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
   return FM_OK;
 }
+
+FM_API fm_status fm_qk_norm_rope_packed(const fm_qk_norm_rope_args* a) {
+  if (!a) return set_error(FM_ERR_INVALID_ARG, "fm_qk_norm_rope_packed: args is NULL");
+  return fm_qk_norm_rope(a->pos, a->T, a->d, a->rope_dim, a->rope_base, a->rope_factor, a->rope_orig_len,
+                         a->rope_beta_fast, a->rope_beta_slow, a->eps, a->q, a->q_stride_t, a->n_q, a->q_gain, a->q_out,
+                         a->k, a->k_stride_t, a->n_k, a->k_gain, a->k_out, a->k_pool, a->P, a->k_page_stride, a->k_cell,
+                         a->stream);
+}

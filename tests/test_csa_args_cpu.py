@@ -116,3 +116,35 @@ def test_python_wrappers_refuse_tensors_of_the_cpu(fm):
         fm.fm_csa_attn_tree(**args, tree_mask=torch.zeros((2, 1), dtype=torch.int32), tree_base=pos, stream=0)
     with pytest.raises(ValueError, match="on the CPU"):
         fm.fm_qk_norm_rope(pos, q=q, q_out=q.clone(), stream=0)
+
+
+def test_packed_arguments_are_the_same_call(fm):
+    """The struct forms refuse what the calls refuse, with the same words: every
+    field is where the struct's reader expects it."""
+    L, page = fm.lib(), 64 * 512
+    words = lambda call, args: (call(*args), fm.fm_last_error())
+    none = lambda args: [0 if a is None else a for a in args]
+    good = [FAKE, 4, 512, 64, 160000.0, 16.0, 65536.0, 32.0, 1.0, 1e-6, FAKE, page, 64, FAKE, FAKE, FAKE, 512, 1, FAKE,
+            FAKE, FAKE, 4, page, FAKE, None]
+    for at, bad in ((0, None), (0, FAKE + 4), (1, -7), (2, 12), (3, 3), (4, 1.0), (5, 0.5), (6, 0.0), (7, 1.0), (8, 32.0),
+                    (9, -1.0), (10, None), (11, 8), (12, -5), (13, FAKE + 2), (14, None), (15, FAKE + 2), (16, 504),
+                    (17, 4095), (18, FAKE + 8), (19, FAKE + 8), (20, FAKE + 8), (21, -1), (22, page + 4), (23, None)):
+        args = good[:at] + [bad] + good[at + 1:]
+        want = words(L.fm_qk_norm_rope, args)
+        assert want[0] == 1 and words(L.fm_qk_norm_rope_packed, [fm._QK_ARGS.pack(*none(args))]) == want, (at, bad)
+    head = [FAKE, 4, 64, 512, FAKE, 9, page, FAKE, 4, 3, FAKE, FAKE, 128, 4, FAKE, 9, page, FAKE, 512, FAKE, 0.04]
+    tree, tail = [FAKE, 1, FAKE], [FAKE, FAKE, 256, 8, None]
+    flat = head + tree + tail
+    for at, bad in ((0, None), (1, -1), (2, 2000), (3, 128), (4, FAKE + 8), (5, -1), (6, page + 8), (7, FAKE + 2), (8, -2),
+                    (9, 1 << 20), (10, FAKE + 1), (11, None), (12, -9), (13, -3), (14, None), (15, -1), (16, 64), (17, None),
+                    (18, 1025), (19, FAKE + 2), (20, -2.0), (21, None), (22, 33), (23, FAKE + 4), (24, None), (25, FAKE + 2),
+                    (26, 128), (27, 9)):
+        args = flat[:at] + [bad] + flat[at + 1:]
+        want = words(L.fm_csa_attn_tree, args)
+        assert want[0] in (1, 5)
+        pack = fm._ATTN_ARGS.pack
+        assert words(L.fm_csa_attn_packed, [pack(*none(args[:21] + [1] + args[21:]))]) == want, (at, bad)
+        if not 21 <= at <= 23:
+            want = words(L.fm_csa_attn, args[:21] + args[24:])
+            assert words(L.fm_csa_attn_packed, [pack(*none(args[:21] + [0] + args[21:]))]) == want, (at, bad)
+    assert L.fm_qk_norm_rope_packed(None) == 1 and L.fm_csa_attn_packed(None) == 1

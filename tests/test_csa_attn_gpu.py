@@ -519,3 +519,16 @@ def test_head_counts(torch_dev, H, seqs, window):
     b = Batch(500 + H + window, seqs, H, 40, window, 2, magnitude=6.0).device(torch, dev)
     b.call()
     b.check(torch)
+
+
+def test_numbers_past_their_type_are_refused(torch_dev):
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    q, pos = torch.zeros((2, 4, D), dtype=torch.bfloat16, device=dev), torch.zeros(2, dtype=torch.int64, device=dev)
+    with pytest.raises(ValueError):
+        fm.fm_qk_norm_rope(pos, q=q, q_out=q.clone(), rope_dim=1 << 40)
+    args = dict(q=q, kv_pool=torch.zeros((3, PAGE, D), dtype=torch.bfloat16, device=dev), pos=pos, out=q.clone(),
+                page_table=torch.zeros((2, 2), dtype=torch.int32, device=dev))
+    for bad in (dict(window=1 << 70), dict(window=8, n_sink=1 << 40)):
+        with pytest.raises(ValueError):
+            fm.fm_csa_attn(**args, **bad)
