@@ -529,7 +529,8 @@ fm_status fm_qk_norm_rope_packed(const fm_qk_norm_rope_args* args);
  *               [T, k] int32 (dense), 0 <= k <= 1024; an entry at or past Pc * 64 is
  *               skipped and flagged; k = 0: both ignored
  *   sink_logit  [n_h] fp32 or NULL;  scale  > 0 (scale * log2 e finite), 512^-1/2 as a rule
- *   out         [T, n_h, 512] bf16, 16-byte aligned;  lse_out [T, n_h] fp32 or NULL
+ *   out         [T, n_h, 512] bf16, 16-byte aligned; may be q itself;  lse_out
+ *               [T, n_h] fp32 or NULL
  *   workspace   >= fm_csa_attn_workspace(T, n_h) bytes, 256-byte aligned (may be
  *               NULL when that is 0): the partial results of tokens whose keys
  *               are split over several SMs.  Calls that overlap on the GPU need

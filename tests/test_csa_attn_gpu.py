@@ -532,3 +532,13 @@ def test_numbers_past_their_type_are_refused(torch_dev):
     for bad in (dict(window=1 << 70), dict(window=8, n_sink=1 << 40)):
         with pytest.raises(ValueError):
             fm.fm_csa_attn(**args, **bad)
+
+
+@pytest.mark.parametrize("seqs,H,window", [([(1, 2600)], 64, 2601), ([(30, 300)], 80, 150), ([(200, 230)], 64, 100)])
+def test_output_over_the_queries(torch_dev, seqs, H, window):
+    """out may be q: through memory, by clusters, several items to a CTA."""
+    torch, dev = torch_dev
+    b = Batch(900 + H + window, seqs, H, 40, window, 2).device(torch, dev)
+    b.d["out"] = b.d["q"]
+    b.call()
+    b.check(torch)
