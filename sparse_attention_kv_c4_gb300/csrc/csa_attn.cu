@@ -622,9 +622,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (raw[x] >= 0 && !seen[x]) atomicOr(status, FM_DEV_PAGE_RANGE);
           const int64_t r = cell ? (int64_t)((uint32_t)raw[x] / kPage) * p.cell_page_rows + (uint32_t)raw[x] % kPage
                                  : raw[x] * p.kv_page_rows + offset[x];
-          // any address where nothing is read
+          // where nothing is read, an address all the same: a copy's source is on a
+          // 16-byte border whatever its size, and q is the one input that is never
+          // NULL and on such a border
           row[x] = seen[x] ? reinterpret_cast<uint64_t>((cell ? p.cell_pool : p.kv_pool) + r * kWidth)
-                           : reinterpret_cast<uint64_t>(p.pos);
+                           : reinterpret_cast<uint64_t>(p.q);
         }
         if (tile + 1 < tile_end) fetch(tile + 1);
         if (tile >= tile_begin && !(ok = publish(row, seen))) break;
