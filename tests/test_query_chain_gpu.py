@@ -146,3 +146,66 @@ def test_query_chain_layers_match_oracle(torch_dev, orc, L, T, n_h, dim, r):
         q_ref, w_ref = orc.query_chain(hidden, wq_a, q_norm, wq_b, w_proj, pos, n_h=n_h)
         _check(q_ref, w_ref, qb_all[:, l], q32[:, l].cpu().numpy().astype(np.float64),
                w[:, l].cpu().numpy().astype(np.float64))
+
+
+@pytest.mark.parametrize("maker", ["norm", "attention"])
+def test_weights_that_the_kernel_before_writes(torch_dev, maker):
+    """Every input of the chain may be the output of the call before it on the
+    stream, the second projection's weights too, which it prefetches: written by
+    the norm or the attention, whose kernels let the next one start early."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    r, n_h = 512, 128
+    rows = n_h * 128
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a.view(np.int16) if a.dtype == np.uint16 else a)).to(dev)
+    hidden, wq_a, q_norm, _, w_proj, pos = map(t, gen.query_chain_inputs(4, dim=1024, r=r, n_h=n_h, seed=gen.BASE_SEED + 590))
+    g = torch.Generator(device=dev).manual_seed(1)
+    made = torch.zeros((rows, r), dtype=torch.bfloat16, device=dev)
+    if maker == "norm":
+        raw = [torch.randn((rows // 8, 8, r), generator=g, device=dev).bfloat16() for _ in range(2)]
+        at = torch.zeros(rows // 8, dtype=torch.int64, device=dev)
+
+        def make(i, out):
+            fm.fm_qk_norm_rope(at, q=raw[i], q_out=out.view(rows // 8, 8, r), rope_dim=0)
+    else:
+        T = rows // 64
+        q = torch.randn((T, 64, r), generator=g, device=dev).bfloat16()
+        pool = [torch.randn((T, 64, r), generator=g, device=dev).bfloat16() for _ in range(2)]
+        table = torch.arange(T, dtype=torch.int32, device=dev).view(T, 1)
+        at = torch.arange(T, device=dev) % 64
+
+        def make(i, out):
+            fm.fm_csa_attn(q, pool[i], table, at, out.view(T, 64, r), window=64)
+    ws = torch.empty(fm.fm_query_chain_workspace(4, r, n_h), dtype=torch.uint8, device=dev)
+    outs = lambda: (torch.zeros((4, n_h, 128), dtype=torch.int16, device=dev), torch.zeros((4, n_h), device=dev))
+
+    def chain(wq_b, to):
+        fm.fm_query_chain(hidden, wq_a, q_norm, wq_b.view(torch.int16), w_proj, pos, *to, workspace=ws)
+    want = []
+    for i in range(2):
+        w = torch.empty_like(made)
+        make(i, w)
+        torch.cuda.synchronize()
+        want.append(outs())
+        chain(w, want[-1])
+        torch.cuda.synchronize()
+    assert not torch.equal(want[0][0], want[1][0])
+    got = [outs() for _ in range(40)]
+    for i, to in enumerate(got):
+        make(i % 2, made)
+        chain(made, to)
+    torch.cuda.synchronize()
+    for i, to in enumerate(got):
+        assert torch.equal(to[0], want[i % 2][0]) and torch.equal(to[1], want[i % 2][1]), i
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(2):
+            make(i, made)
+            chain(made, got[i])
+    for x in got[0] + got[1]:
+        x.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(got[i][0], want[i][0]) and torch.equal(got[i][1], want[i][1])
+    assert fm.fm_device_status(reset=True) == 0
