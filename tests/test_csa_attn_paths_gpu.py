@@ -34,3 +34,63 @@ def test_arguments_on_their_own_borders_only(torch_dev, seqs, window, tree):
                 assert args[name].data_ptr() % (2 * args[name].element_size()) != 0
     b.call()
     b.check(torch)
+
+
+MARK = 0xA5
+
+
+def call_by(torch, b, way):
+    """One call, and proof of the way it took.  Whole items and clusters leave the
+    workspace as it was; partial results fill exactly [parts, 64] maxima and sums
+    and the [parts, 64, 512] outputs behind them."""
+    ws = b.kw["workspace"]
+    ws.fill_(MARK)
+    b.call()
+    torch.cuda.synchronize()
+    items = b.T * ((b.H + 63) // 64)
+    if way != "memory":
+        assert items > 128 if way == "whole" else items <= 76
+        assert ws.numel() == 0 or bool((ws == MARK).all())
+        return
+    slots = min(b.window, b.R * PAGE) + min(b.n_sink, b.R * PAGE) + b.k + 32 * b.words
+    sms = torch.cuda.get_device_properties(ws.device).multi_processor_count
+    splits = min(min(sms, 256) // items, -(-slots // 64))
+    parts = items * splits
+    assert splits > 1
+    assert bool((ws[:parts * 512].view(-1, 8) != MARK).any(1).all())  # a maximum and a sum for each part's 64 heads
+    outs = ws[parts * 512:parts * (512 + 64 * 2048)].view(parts, 64, 2048)
+    last = b.H - 64 * ((b.H + 63) // 64 - 1)
+    assert bool((outs[:, :last] != MARK).any(-1).all())
+    assert bool((ws[parts * (512 + 64 * 2048):] == MARK).all())
+
+
+@pytest.mark.parametrize("H", [2, 33, 64, 80, 130, 320])
+@pytest.mark.parametrize("holes", [False, True])
+def test_through_memory(torch_dev, H, holes):
+    """Partial results of one to five blocks of heads, the last one full and not, of a
+    long token and of one that leaves most of its splits without keys; a maximum
+    that moves."""
+    torch, dev = torch_dev
+    seqs = [(1, 7000)] if H > 130 else [(1, 7000), (1, 31)]
+    b = Batch(1300 + H, seqs, H, 40, 7001, 2, magnitude=6.0, holes=holes).device(torch, dev)
+    call_by(torch, b, "memory")
+    b.check(torch)
+
+
+@pytest.mark.parametrize("H", [5, 64, 80])
+@pytest.mark.parametrize("holes", [False, True])
+def test_tree_through_memory(torch_dev, H, holes):
+    torch, dev = torch_dev
+    b = Batch(1400 + H, [(2, 7000)], H, 40, 7001, 2, magnitude=6.0, holes=holes, tree=True).device(torch, dev)
+    call_by(torch, b, "memory")
+    b.check(torch)
+
+
+@pytest.mark.parametrize("H", [33, 64, 80])
+@pytest.mark.parametrize("tree", [False, True])
+def test_output_over_the_queries_through_memory(torch_dev, H, tree):
+    torch, dev = torch_dev
+    b = Batch(1500 + H, [(2, 7000)], H, 40, 7001, 2, tree=tree).device(torch, dev)
+    b.d["out"] = b.d["q"]
+    call_by(torch, b, "memory")
+    b.check(torch)
