@@ -94,3 +94,54 @@ def test_output_over_the_queries_through_memory(torch_dev, H, tree):
     b.d["out"] = b.d["q"]
     call_by(torch, b, "memory")
     b.check(torch)
+
+
+COUNTED = [
+    # way, tree, seqs, H, k, window, n_sink
+    ("whole", False, [(160, 3100)], 20, 30, 2991, 5),
+    ("whole", True, [(150, 3100)], 20, 0, 2991, 5),
+    ("cluster", False, [(3, 4000), (1, 3333), (1, 12)], 64, 70, 3001, 65),     # of eight
+    ("cluster", False, [(30, 3200)], 64, 512, 2500, 4),                        # of four
+    ("cluster", False, [(60, 3200)], 20, 512, 600, 4),                         # of two
+    ("cluster", True, [(16, 4100)], 64, 33, 3333, 4),
+    ("memory", False, [(1, 7000)], 64, 0, 6990, 3),
+    ("memory", False, [(2, 6999)], 80, 100, 6500, 66),
+    ("memory", True, [(3, 6900)], 64, 10, 6800, 4),
+]
+
+
+@pytest.mark.parametrize("way,tree,seqs,H,k,window,n_sink", COUNTED)
+@pytest.mark.parametrize("holes", [False, True])
+def test_no_key_is_lost_or_doubled(torch_dev, way, tree, seqs, H, k, window, n_sink, holes):
+    """Queries near zero: every key weighs the same, lse is the logarithm of their
+    number, good to 2^-18 * (2 + lse) or so, and each key raises one element of the
+    output by 1024 / number.  A key more or less at the edge of a window, a page, a
+    tile or a split moves lse by 1 / 7000 at least, nearly four times its tolerance, and
+    that element by seven times its own."""
+    torch, dev = torch_dev
+    b = Batch(1600 + H + k, seqs, H, k, window, n_sink, tree=tree, holes=holes, magnitude=2.0 ** -20, sink=False)
+    for pool in (b.kv, b.cp):
+        used = np.flatnonzero(pool[:, 0] != 0x7FC1)
+        pool[used, used * 37 % D] = ref.bf16(np.float32(1024.0))
+    b.device(torch, dev)
+    call_by(torch, b, way)
+    b.check(torch, tokens=None if b.T < 40 else sorted(set(range(0, b.T, 9)) | {b.T - 1}))
+
+
+def test_tree_with_a_base_past_every_table(torch_dev):
+    """Its drafted slots are past the table: no keys, and flagged.  Its committed
+    tokens are those of its window, and they are attended to."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    b = Batch(1700, [(4, 100)], 8, 10, 40, 3, tree=True)
+    b.rows = []
+    for p in b.pos:
+        rows = [int(b.table[0, j // PAGE]) * PAGE + j % PAGE for j in ref.visible(p, b.window, b.n_sink, p + 1)]
+        b.kv[rows] = ref.bf16(np.random.default_rng(p).standard_normal((len(rows), D)))
+        b.rows.append(rows)
+    b.device(torch, dev)
+    b.kw["tree_base"].fill_(2 ** 63 - 1)
+    b.call()
+    torch.cuda.synchronize()
+    assert fm.fm_device_status(reset=True) == fm.FM_DEVERR_PAGE_RANGE
+    b.check(torch)
