@@ -145,3 +145,85 @@ def test_tree_with_a_base_past_every_table(torch_dev):
     torch.cuda.synchronize()
     assert fm.fm_device_status(reset=True) == fm.FM_DEVERR_PAGE_RANGE
     b.check(torch)
+
+
+def test_a_layer_without_cached_tokens(torch_dev):
+    """Selected cells alone: a pool of no pages and a table of no columns, with
+    positions like any other, and nothing flagged."""
+    torch, dev = torch_dev
+    b = Batch(1800, [(3, 900), (1, 40)], 64, 200, 0, 0).device(torch, dev)
+    b.d.update(kv_pool=torch.empty((0, PAGE, D), dtype=torch.int16, device=dev),
+               page_table=torch.empty((b.B, 0), dtype=torch.int32, device=dev))
+    b.call()
+    b.check(torch)
+
+
+def test_most_heads_and_cells(torch_dev):
+    torch, dev = torch_dev
+    b = Batch(1900, [(2, 1000)], 1024, 1024, 65, 4).device(torch, dev)
+    b.call()
+    b.check(torch)
+
+
+def test_widest_tree(torch_dev):
+    """1024 drafted tokens, 32 words of mask."""
+    torch, dev = torch_dev
+    b = Batch(1901, [(1024, 300)], 20, 8, 64, 4, tree=True)
+    assert b.words == 32
+    b.device(torch, dev).call()
+    b.check(torch, tokens=[0, 1, 31, 32, 33, 500, 1000, 1022, 1023])
+
+
+@pytest.mark.parametrize("tokens,way", [(1, "memory"), (130, "whole")])
+def test_longest_table(torch_dev, tokens, way):
+    """The most pages of a table, 2^25 visible tokens, split and not.  All pages are one
+    page, and the queries are zero, so every weight is 1 and every partial sum an
+    integer that is exact in fp32 up to 2^24: lse is log 2^25, and the output the page's
+    mean.  (One element's mean is 1/2: its sums reach 2^24 and pass it by less than 64
+    within the last pages, so each of their last steps is off by 1 at most, 2^-19 of
+    the mean together.)"""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    R, H = 1 << 19, 3
+    g = torch.Generator(device=dev).manual_seed(3)
+    page = (torch.randint(0, 2, (1, PAGE, D), generator=g, device=dev) * 2 - 1).bfloat16()
+    mean = page[0].double().mean(0)
+    assert float(mean.abs().max()) * (1 << 25) <= 1 << 24
+    out = torch.empty((tokens, H, D), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((tokens, H), device=dev)
+    ws = torch.full((fm.fm_csa_attn_workspace(tokens, H),), MARK, dtype=torch.uint8, device=dev)
+    fm.fm_csa_attn(torch.zeros_like(out), page, torch.zeros((1, R), dtype=torch.int32, device=dev),
+                   torch.full((tokens,), R * PAGE - 1, device=dev), out, R * PAGE,
+                   seq=torch.zeros(tokens, dtype=torch.int32, device=dev), lse_out=lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert fm.fm_device_status(reset=True) == 0
+    assert (way == "memory") == bool((ws != MARK).any())
+    n = 25 * np.log(2.0)
+    assert float((lse.double() - n).abs().max()) <= 2.0 ** -18 * (1 + n)
+    assert bool(((out.double() - mean).abs() <= ref.HALF_BF16 * mean.abs() * (1 + 2.0 ** -8) + 2.0 ** -16).all())
+
+
+def test_queries_and_outputs_past_32_bit_offsets(torch_dev):
+    """More than 2^32 elements of queries and outputs (8.6 GB each)."""
+    torch, dev = torch_dev
+    T, H = (1 << 32) // (64 * D) + 30, 64
+    b = Batch(1902, [(3, 200)], H, 20, 100, 4).device(torch, dev)
+    far = [0, T // 2 + 1, T - 1]  # the batch's three tokens; the others are padding
+    q = torch.zeros((T, H, D), dtype=torch.int16, device=dev)
+    out, lse = torch.full_like(q, 0x7FC1), torch.full((T, H), float("nan"), device=dev)
+    seq, pos = torch.full((T,), -1, dtype=torch.int32, device=dev), torch.zeros(T, dtype=torch.int64, device=dev)
+    cells = torch.full((T, 20), -1, dtype=torch.int32, device=dev)
+    for i, t in enumerate(far):
+        q[t], seq[t], pos[t], cells[t] = b.d["q"][i], 0, b.d["pos"][i], b.kw["cells"][i]
+    small = b.d["out"], b.kw["lse_out"]
+    b.d.update(q=q, out=out, pos=pos)
+    b.kw.update(seq=seq, cells=cells, lse_out=lse, workspace=None)
+    b.call()
+    torch.cuda.synchronize()
+    pad = torch.ones(T, dtype=torch.bool, device=dev)
+    pad[far] = False
+    assert int((out != 0).any(-1).any(-1).sum()) == 3 and bool(torch.isneginf(lse[pad]).all())
+    for i, t in enumerate(far):
+        small[0][i], small[1][i] = out[t], lse[t]
+    b.d["out"], b.kw["lse_out"] = small
+    b.check(torch)

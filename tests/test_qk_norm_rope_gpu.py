@@ -138,3 +138,42 @@ def test_graph_replay_takes_new_inputs(torch_dev):
     fm.fm_qk_norm_rope(pos, q=xs[1], q_out=out)
     torch.cuda.synchronize()
     assert torch.equal(got, out)
+
+
+def test_offsets_past_32_bits_and_most_heads(torch_dev):
+    """More than 2^32 elements of queries, and of the pool; the most heads and the
+    widest one."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    T, H, K, d = 1060, 4000, 96, 1024
+    g = torch.Generator(device=dev).manual_seed(6)
+    q = torch.randn((T, H, d), generator=g, device=dev, dtype=torch.bfloat16)
+    k = torch.randn((T, K, d), generator=g, device=dev, dtype=torch.bfloat16)
+    assert q.numel() > 1 << 32
+    P = (1 << 32) // (PAGE * K * d) + 2
+    pool = torch.zeros((P, PAGE, K * d), dtype=torch.bfloat16, device=dev)
+    pos = torch.arange(T, device=dev) * 997
+    cell = (P * PAGE - 1 - torch.arange(T, device=dev)).int()
+    out = torch.empty_like(q)
+    fm.fm_qk_norm_rope(pos, q=q, q_out=out, k=k, k_pool=pool, k_cell=cell, rope_dim=256)
+    torch.cuda.synchronize()
+    assert fm.fm_device_status(reset=True) == 0
+    rows = pool.view(P * PAGE, K, d)
+    for t in (0, T // 2, T - 1):
+        at = np.array([t * 997])
+        for x, y in ((q[t], out[t]), (k[t], rows[int(cell[t])])):
+            want, tol = ref.norm_rope(x[None].double().cpu().numpy(), None, at, 256, 1e-6)
+            assert (np.abs(y[None].double().cpu().numpy() - want) <= tol).all()
+
+
+def test_many_tokens(torch_dev):
+    """More than two million tokens of one narrow head."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    T = (1 << 21) + 5
+    x = torch.randn((T, 1, 8), generator=torch.Generator(device=dev).manual_seed(7), device=dev, dtype=torch.bfloat16)
+    pos, out = torch.arange(T, device=dev), torch.empty_like(x)
+    fm.fm_qk_norm_rope(pos, q=x, q_out=out, rope_dim=8)
+    torch.cuda.synchronize()
+    want, tol = ref.norm_rope(x.double().cpu().numpy(), None, pos.cpu().numpy(), 8, 1e-6)
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
