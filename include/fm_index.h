@@ -438,7 +438,10 @@ fm_status fm_index_prefill_topk(const uint16_t* q, const float* w, const int64_t
  * angle pos[t] * theta'_i, with theta'_i the YaRN frequency of fm_query_chain
  * (base^(-2i/rope_dim), rope_factor, rope_orig_len, rope_beta_fast / _slow;
  * rope_factor 1 is the plain rotary embedding).  fp32 throughout, the angle's
- * fraction of a turn in 64-bit fixed point; one rounding, to bf16.
+ * fraction of a turn in 64-bit fixed point; one rounding, to bf16.  The sum of
+ * squares is fp32's too: a row whose sum passes its range (elements of some 10^18
+ * at d = 512) comes out as zeros, and with eps = 0 one below its range (elements
+ * of some 10^-23) as infinities or NaN.
  *
  *   pos       [T] int64 token positions
  *   q         [T, n_q, d] bf16, token stride q_stride_t elements (a slice of a
@@ -511,7 +514,10 @@ fm_status fm_qk_norm_rope_packed(const fm_qk_norm_rope_args* args);
  *     out[t, h] = sum_j exp(s_j) c_j / (Z + exp(sink_logit[h]))
  *     lse[t, h] = log Z
  * (sink_logit NULL: no second term).  A token without keys gets out = 0 and
- * lse = -inf.  Rows that are no keys are never read.
+ * lse = -inf.  Rows that are no keys are never read.  A cell is its own value: where
+ * the cells' last entries were turned by their positions (fm_qk_norm_rope), the
+ * output's are sums of turned entries; a model that turns them back by the
+ * query's position does so itself.
  *
  *   q           [T, n_h, 512] bf16, 16-byte aligned; 1 <= n_h <= 1024,
  *               T * ceil(n_h / 64) < 2^23
@@ -533,11 +539,13 @@ fm_status fm_qk_norm_rope_packed(const fm_qk_norm_rope_args* args);
  *               [T, n_h] fp32 or NULL
  *   workspace   >= fm_csa_attn_workspace(T, n_h) bytes, 256-byte aligned (may be
  *               NULL when that is 0): the partial results of tokens whose keys
- *               are split over several SMs.  Calls that overlap on the GPU need
- *               a workspace each.
- * Scores, softmax statistics and sums are fp32; the softmax weights are rounded
- * to bf16 for the tensor cores' second product.  The result does not depend on
- * scheduling.
+ *               are split over several SMs.  The size goes by T and n_h alone, so
+ *               a call of T * ceil(n_h / 64) <= 128 needs it whether its keys turn out
+ *               to be split that way or not.  Calls that overlap on the GPU need a
+ *               workspace each.
+ * Scores (scale * log2 e included), softmax statistics and sums are fp32; the
+ * softmax weights are rounded to bf16 for the tensor cores' second product.  The
+ * result does not depend on scheduling.
  * Errors: FM_ERR_INVALID_ARG, FM_ERR_WORKSPACE, FM_ERR_CUDA.
  */
 size_t fm_csa_attn_workspace(int T, int n_h);

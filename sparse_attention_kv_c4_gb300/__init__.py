@@ -578,7 +578,8 @@ def fm_csa_attn(q, kv_pool, page_table, pos, out, window: int, n_sink: int = 0, 
     [T,k] int32 rows of cell_pool [Pc,64,512] (both None: none), sink_logit
     [n_h] fp32 or None, scale (None: 512 ** -0.5) -> out [T,n_h,512] bf16,
     lse_out [T,n_h] fp32 or None; workspace uint8 [>= fm_csa_attn_workspace(T,
-    n_h)]."""
+    n_h)].  A layer without cached tokens passes a kv_pool of no pages and a
+    page_table [T,0]."""
     _csa_attn(None, q, kv_pool, page_table, pos, out, window, n_sink, seq, cell_pool, cells, sink_logit, scale, lse_out,
               workspace, stream)
 
