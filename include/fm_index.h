@@ -607,6 +607,172 @@ typedef struct fm_csa_attn_args {
 fm_status fm_csa_attn_packed(const fm_csa_attn_args* args);
 
 /*
+ * A dense layer of grouped heads, held in 8 bits: fm_prompt_attn (a whole
+ * prompt's attention), fm_kv_append_fp8 (its keys and values, and later each
+ * step's, into the cache) and fm_kv_attn_fp8 (attention over the cache).  n_h
+ * query heads share n_k key and value heads, n_h a multiple of n_k and
+ * n_h / n_k <= 128: query head h reads key head h / (n_h / n_k).  d is a
+ * multiple of 16, 16 <= d <= 128.  Sequences are packed: sequence b has the
+ * tokens cu[b] .. cu[b + 1] - 1 of the call's T; cu is non-decreasing with
+ * cu[0] = 0 and cu[B] <= T.  Rows behind the last sequence (a padded batch) are
+ * neither read nor written.  An offset outside 0 .. T is read as the nearer of the
+ * two, and a sequence whose end is before its begin as empty.
+ *
+ * The cache: pages of 64 tokens, k_pool and v_pool [P, n_k, 64, d] E4M3 codes and
+ * k_scale, v_scale [P, n_k, 4] fp32, one for each block of 16 tokens of a page and
+ * head: an entry is e4m3(code) * scale.  Token position j of sequence b is row
+ * j % 64 of page page_table[b, j / 64].  page_stride is the bytes from page to page
+ * of either pool (layers may lie between): a multiple of 16, at least n_k * 64 * d;
+ * scale_stride the floats from page to page of either scale array: a multiple of 4,
+ * at least 4 n_k.  Pools and scales are 16-byte aligned.  page_table [B, R] int32, R <= 2^19: a
+ * negative entry is a page that is not held, one at or past P is skipped and flagged
+ * FM_DEVERR_PAGE_RANGE, as is a token at or past R * 64.
+ *
+ * The rotation ([RM] "Hyperparameters": YaRN), where there is one, is
+ * fm_qk_norm_rope's: the pairs of the last rope_dim elements turn by position *
+ * theta'_i.
+ *
+ * fm_kv_append_fp8: token i of sequence b gets position p = start[b] + i.  Its keys are
+ * turned (fp32, the angle's fraction of a turn in 64-bit fixed point), its values
+ * taken as they are, and both written to the cell of position p; where q is given, its
+ * queries are turned alike into q_out (bf16).
+ *   Scales: with amax the largest magnitude of the call's entries of a block and head,
+ * need is the least power of two >= 2^-100 with amax <= 448 * need.  A block whose first
+ * position this call writes (or precedes) starts anew with scale need.  One that holds
+ * earlier tokens keeps the larger of its scale and need; where that is need, its
+ * earlier codes c become e4m3(e4m3(c) * old / need).  An entry x becomes
+ * e4m3(x * (1 / scale)), rounded once from fp32, ties to even.  Infinities and NaN do not
+ * count for amax and are stored as NaN (0x7F).
+ *   A page that several sequences share may be appended to by one of them only.
+ *   A negative start[b] leaves sequence b out; a token whose page is not held or out
+ * of range is left out.
+ *
+ *   k, v       [T, n_k, d] bf16, token strides k_stride_t, v_stride_t elements
+ *   q          [T, n_h, d] bf16, token stride q_stride_t, or NULL (n_h is ignored);
+ *              q_out [T, n_h, d] bf16 dense, may be q where that is dense
+ *   start      [B] int64: the tokens that sequence b has in the cache already
+ *   cu_tokens  [B + 1] int32, or NULL: T = B, one token a sequence
+ *   rope_dim   even, 0 <= rope_dim <= d; 0: no rotation; the other rotary
+ *              parameters as for fm_qk_norm_rope
+ *   strides multiples of 8 elements that hold the heads; k, v, q, q_out 16-byte aligned
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_CUDA.
+ */
+#define FM_KV_PAGE 64  /* tokens of a cache page */
+#define FM_KV_BLOCK 16 /* tokens that share a scale */
+
+typedef struct fm_kv_append_fp8_args {
+  const uint16_t* k;
+  int64_t k_stride_t;
+  const uint16_t* v;
+  int64_t v_stride_t;
+  int T, n_k, d, n_h;
+  const uint16_t* q;
+  int64_t q_stride_t;
+  uint16_t* q_out;
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  float* k_scale;
+  float* v_scale;
+  int64_t P, page_stride, scale_stride;
+  const int32_t* page_table;
+  int B, R;
+  const int64_t* start;
+  const int32_t* cu_tokens;
+  double rope_base, rope_factor, rope_orig_len, rope_beta_fast, rope_beta_slow;
+  int rope_dim;
+  fm_stream_t stream;
+} fm_kv_append_fp8_args;
+fm_status fm_kv_append_fp8(const fm_kv_append_fp8_args* args);
+
+/*
+ * Attention over that cache: token i of sequence b, at position p = start[b] + i,
+ * attends to the cached positions j of its sequence with p - window < j <= p on held pages
+ * (its own among them: append first).  For query head h and s_j = scale * (q . k_j):
+ *     out = sum_j exp(s_j) v_j / (Z + exp(sink_logit[h])),  lse = log Z,  Z = sum_j exp(s_j)
+ * (sink_logit NULL: no second term).  A token without keys gets out = 0 and lse = -inf.
+ * Cells that are no keys of a token have no part in its result, whatever they hold.
+ *
+ *   q          [T, n_h, d] bf16, token stride q_stride_t; 1 <= n_h <= 1024
+ *   start      [B] int64, cu_tokens [B + 1] or NULL, as for fm_kv_append_fp8
+ *   window     >= 0 (0: no keys); INT64_MAX: no limit
+ *   scales     positive and finite; any fp32 ones, powers of two or not
+ *   scale      > 0 (scale * log2 e finite), d^-1/2 as a rule
+ *   out        [T, n_h, d] bf16 dense, may be q where that is dense; lse_out [T, n_h] fp32 or NULL
+ *   workspace  >= fm_kv_attn_fp8_workspace(T, n_h, n_k, d) bytes, 256-byte aligned;
+ *              calls that overlap on the GPU need one each
+ *   q, out 16-byte aligned
+ * Scores, softmax statistics and sums are fp32; queries and softmax weights are fp16
+ * operands, scaled by powers of two so that no row leaves fp16's range.  The result does
+ * not depend on scheduling.
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_WORKSPACE, FM_ERR_CUDA.
+ */
+typedef struct fm_kv_attn_fp8_args {
+  const uint16_t* q;
+  int64_t q_stride_t;
+  int T, n_h, n_k, d;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t P, page_stride, scale_stride;
+  const int32_t* page_table;
+  int B, R;
+  const int64_t* start;
+  const int32_t* cu_tokens;
+  int64_t window;
+  const float* sink_logit;
+  float scale;
+  uint16_t* out;
+  float* lse_out;
+  void* workspace;
+  size_t workspace_bytes;
+  fm_stream_t stream;
+} fm_kv_attn_fp8_args;
+size_t fm_kv_attn_fp8_workspace(int T, int n_h, int n_k, int d);
+fm_status fm_kv_attn_fp8(const fm_kv_attn_fp8_args* args);
+
+/*
+ * Attention over whole prompts ([RM] "Two-level recall algorithm": the prompt is
+ * prefilled densely), causal, packed sequences.  Sequence b has the nq queries
+ * cu_q[b] .. cu_q[b + 1] - 1 of T and the nk keys cu_k[b] .. cu_k[b + 1] - 1 of Tk; its
+ * queries are the last nq of the nk tokens (nk > nq: a prefix whose keys are at hand).
+ * Query i sees the keys j with i + nk - nq - window < j <= i + nk - nq, and
+ * out and lse are fm_kv_attn_fp8's.  A query without keys (nk < nq) gets out = 0 and lse = -inf.
+ * Keys and values that a query does not see have no part in its result, whatever
+ * they hold.
+ *
+ *   q       [T, n_h, d] bf16, token stride q_stride_t; k, v [Tk, n_k, d], k_stride_t,
+ *           v_stride_t; 1 <= n_h <= 1024; strides multiples of 8 elements that hold
+ *           the heads; T, Tk < 2^30
+ *   cu_q    [B + 1] int32, or NULL: one sequence of T queries (B = 1)
+ *   cu_k    [B + 1] int32, or NULL: cu_q's (T = Tk), or with cu_q NULL one sequence of Tk keys
+ *   window  >= 0; INT64_MAX: no limit;  sink_logit [n_h] fp32 or NULL;  scale as above
+ *   out     [T, n_h, d] bf16 dense;  lse_out [T, n_h] fp32 or NULL
+ *   q, k, v, out 16-byte aligned
+ * Scores, softmax statistics and sums are fp32; the softmax weights are rounded to
+ * bf16 for the tensor cores' second product.  The result does not depend on scheduling.
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_CUDA.
+ */
+typedef struct fm_prompt_attn_args {
+  const uint16_t* q;
+  int64_t q_stride_t;
+  const uint16_t* k;
+  int64_t k_stride_t;
+  const uint16_t* v;
+  int64_t v_stride_t;
+  int T, Tk, n_h, n_k, d, B;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int64_t window;
+  const float* sink_logit;
+  float scale;
+  uint16_t* out;
+  float* lse_out;
+  fm_stream_t stream;
+} fm_prompt_attn_args;
+fm_status fm_prompt_attn(const fm_prompt_attn_args* args);
+
+/*
  * Device status word of the current device: the OR of FM_DEVERR_* bits set by
  * kernels since the last reset.  Synchronises `stream` before reading.  When
  * reset != 0 the word is cleared after reading.  status_out is HOST memory.

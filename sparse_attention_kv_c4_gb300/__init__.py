@@ -21,7 +21,8 @@ __all__ = [
     "fm_native_topk_paged_ex", "fm_memindex_fp8_workspace", "fm_memindex_score_mask_fp8",
     "fm_index_prefill_scores", "fm_retriever_workspace", "fm_retriever_score_mask", "fm_query_chain_workspace",
     "fm_query_chain", "fm_query_chain_layers_workspace", "fm_query_chain_layers", "fm_qk_norm_rope",
-    "fm_csa_attn_workspace", "fm_csa_attn", "fm_csa_attn_tree", "LIB_PATH",
+    "fm_csa_attn_workspace", "fm_csa_attn", "fm_csa_attn_tree", "fm_prompt_attn", "fm_kv_append_fp8",
+    "fm_kv_attn_fp8_workspace", "fm_kv_attn_fp8", "LIB_PATH",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -124,6 +125,12 @@ def lib() -> ctypes.CDLL:
             L.fm_csa_attn_tree.argtypes = head + [_VP, _I32, _VP] + tail
             L.fm_csa_attn_packed.argtypes = [ctypes.c_char_p]
             L.fm_csa_attn.restype = L.fm_csa_attn_tree.restype = L.fm_csa_attn_packed.restype = ctypes.c_int
+        if hasattr(L, "fm_kv_attn_fp8"):
+            L.fm_kv_attn_fp8_workspace.argtypes = [_I32, _I32, _I32, _I32]
+            L.fm_kv_attn_fp8_workspace.restype = _SZ
+            for name in ("fm_prompt_attn", "fm_kv_append_fp8", "fm_kv_attn_fp8"):
+                getattr(L, name).argtypes = [ctypes.c_char_p]
+                getattr(L, name).restype = ctypes.c_int
         if hasattr(L, "fm_page_recall"):
             L.fm_page_recall.argtypes = [_VP, _I32, _I64, _I64, _I64, _I32, _VP, _VP, _VP, _VP]
         for name in ("fm_memindex_score_mask", "fm_topk_select", "fm_native_topk_paged", "fm_index_prefill_topk",
@@ -395,19 +402,25 @@ def fm_page_recall(mask, S: int, kmax: int, pages_out, density_out=None, n_out=N
 # fm_qk_norm_rope_args and fm_csa_attn_args: one argument through ctypes instead of 25
 _QK_ARGS = struct.Struct("@P3i5dfPqi3Pqi3P2q2P")
 _ATTN_ARGS = struct.Struct("@P3iP2qP2i2PqiP2qPiPfiPi4PNP")
-_BF16 = _BITS = _I32T = _I64T = _F32T = _U8T = frozenset()  # accepted element types, set by _types()
+# fm_kv_append_fp8_args, fm_kv_attn_fp8_args, fm_prompt_attn_args
+_APPEND_ARGS = struct.Struct("@PqPq4iPqP4P3qP2i2P5diP")
+_KV_ATTN_ARGS = struct.Struct("@Pq4i4P3qP2i2PqPf3PNP")
+_PROMPT_ARGS = struct.Struct("@PqPqPq6i2PqPf3P")
+_NO_WINDOW = (1 << 63) - 1
+_BF16 = _BITS = _I32T = _I64T = _F32T = _U8T = _E4M3 = frozenset()  # accepted element types, set by _types()
 _current_device = _raw_stream = None
 
 
 def _types():
     import torch
-    global _BF16, _BITS, _I32T, _I64T, _F32T, _U8T, _current_device, _raw_stream
+    global _BF16, _BITS, _I32T, _I64T, _F32T, _U8T, _E4M3, _current_device, _raw_stream
     _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     # the current stream's handle alone: a tenth of the time of current_stream()
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
     _BITS, _I32T, _I64T = frozenset((torch.int32, torch.uint32)), frozenset((torch.int32,)), frozenset((torch.int64,))
     _F32T, _U8T = frozenset((torch.float32,)), frozenset((torch.uint8,))
+    _E4M3 = frozenset((torch.uint8, torch.float8_e4m3fn))  # codes, or the values that they are
     _BF16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))  # bf16 tensors, or their bit patterns
 
 
@@ -592,3 +605,162 @@ def fm_csa_attn_tree(q, kv_pool, page_table, pos, out, window: int, tree_mask, t
     uint32 has bit i & 31 of word i >> 5 set where token t sees it."""
     _csa_attn((tree_mask, tree_base), q, kv_pool, page_table, pos, out, window, n_sink, seq, cell_pool, cells, sink_logit,
               scale, lse_out, workspace, stream)
+
+
+def _pages(t, name, types, shape, dev):
+    """Pointer and first stride of a 4-dimensional pool that is dense but for its first
+    dimension, as _rows."""
+    if t.dtype in types and t.shape == shape and t.get_device() == dev:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1] * shape[2] * shape[3]
+        if shape[0] and t[0].is_contiguous():
+            return t.data_ptr(), t.stride(0)
+    _refuse(t, name, types, shape, dev, True)
+
+
+def _cache(k_pool, v_pool, k_scale, v_scale, n_k, d, dev):
+    """Pointers and strides of the 8-bit cache's four arrays: (k, v, k_scale, v_scale,
+    P, page_stride, scale_stride)."""
+    P = k_pool.shape[0]
+    k_p, page = _pages(k_pool, "k_pool", _E4M3, (P, n_k, 64, d), dev)
+    v_p, v_page = _pages(v_pool, "v_pool", _E4M3, (P, n_k, 64, d), dev)
+    ks_p, stride = _rows(k_scale, "k_scale", _F32T, (P, n_k, 4), dev)
+    vs_p, v_stride = _rows(v_scale, "v_scale", _F32T, (P, n_k, 4), dev)
+    if P > 1 and (page != v_page or stride != v_stride):
+        raise ValueError(f"k_pool and v_pool, and k_scale and v_scale, need the same stride from page to page: "
+                         f"{page} and {v_page}, {stride} and {v_stride}")
+    return k_p, v_p, ks_p, vs_p, P, page, stride
+
+
+def _packed(T, page_table, start, cu_tokens, dev):
+    """(B, R, page_table, start, cu_tokens) of a call over cached sequences."""
+    B, R = _shape(page_table, "page_table", 2)
+    table_p = _dense(page_table, "page_table", _I32T, (B, R), dev)
+    start_p = _dense(start, "start", _I64T, (B,), dev)
+    cu_p = 0
+    if cu_tokens is not None:
+        cu_p = _dense(cu_tokens, "cu_tokens", _I32T, (B + 1,), dev)
+    elif T != B:
+        raise ValueError(f"without cu_tokens every sequence has one token: {T} tokens, {B} rows of page_table")
+    return B, R, table_p, start_p, cu_p
+
+
+def fm_kv_append_fp8(k, v, k_pool, v_pool, k_scale, v_scale, page_table, start, cu_tokens=None, q=None, q_out=None,
+                     rope_dim: int = 64, stream=None, rope_base: float = RETRIEVER_ROPE["rope_base"],
+                     rope_factor: float = RETRIEVER_ROPE["rope_factor"],
+                     rope_orig_len: float = RETRIEVER_ROPE["rope_orig_len"],
+                     rope_beta_fast: float = RETRIEVER_ROPE["rope_beta_fast"],
+                     rope_beta_slow: float = RETRIEVER_ROPE["rope_beta_slow"]) -> None:
+    """k, v [T,n_k,d] bf16 (any token stride) into the 8-bit cache k_pool, v_pool
+    [P,n_k,64,d] uint8 or float8_e4m3fn and k_scale, v_scale [P,n_k,4] fp32 (any page
+    stride), a scale for each 16 positions and head; page_table [B,R] int32, start [B]
+    int64 the tokens that a sequence has already, cu_tokens [B+1] int32 the packed
+    sequences' offsets (None: one token each).  The last rope_dim entries of k are turned by
+    their positions on the way (0: none), and those of q [T,n_h,d] into q_out."""
+    dev = _device(k, "k")
+    T, n_k, d = _shape(k, "k", 3)
+    k_p, k_stride = _rows(k, "k", _BF16, (T, n_k, d), dev)
+    v_p, v_stride = _rows(v, "v", _BF16, (T, n_k, d), dev)
+    n_h = q_p = q_stride = qo_p = 0
+    if q is not None:
+        if q_out is None:
+            raise ValueError("q needs q_out")
+        shape = _shape(q, "q", 3)
+        n_h = shape[1]
+        q_p, q_stride = _rows(q, "q", _BF16, (T, n_h, d), dev)
+        qo_p = _dense(q_out, "q_out", _BF16, shape, dev)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    cache = _cache(k_pool, v_pool, k_scale, v_scale, n_k, d, dev)
+    B, R, table_p, start_p, cu_p = _packed(T, page_table, start, cu_tokens, dev)
+    if dev < 0:
+        raise ValueError("the tensors are on the CPU")
+    try:
+        args = _APPEND_ARGS.pack(k_p, k_stride, v_p, v_stride, T, n_k, d, n_h, q_p, q_stride, qo_p, *cache, table_p, B, R,
+                                 start_p, cu_p, rope_base, rope_factor, rope_orig_len, rope_beta_fast, rope_beta_slow,
+                                 rope_dim, _raw_stream(dev) if stream is None else _stream(stream))
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"fm_kv_append_fp8: {e}") from None
+    st = lib().fm_kv_append_fp8(args)
+    if st:
+        _check(st)
+
+
+def fm_kv_attn_fp8_workspace(T: int, n_h: int, n_k: int, d: int) -> int:
+    return lib().fm_kv_attn_fp8_workspace(T, n_h, n_k, d)
+
+
+def fm_kv_attn_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, start, out, cu_tokens=None, window=None,
+                   sink_logit=None, scale=None, lse_out=None, workspace=None, stream=None) -> None:
+    """q [T,n_h,d] bf16 (any token stride) over the 8-bit cache (fm_kv_append_fp8's
+    arrays): token i of sequence b is at position start[b] + i and attends to the cached
+    positions up to its own, the last `window` of them (None: all); sink_logit [n_h] fp32
+    or None, scale (None: d ** -0.5) -> out [T,n_h,d] bf16, lse_out [T,n_h] fp32 or
+    None; workspace uint8 [>= fm_kv_attn_fp8_workspace(T, n_h, n_k, d)]."""
+    dev = _device(q, "q")
+    shape = _shape(q, "q", 3)
+    T, n_h, d = shape
+    n_k = _shape(k_pool, "k_pool", 4)[1]
+    q_p, q_stride = _rows(q, "q", _BF16, shape, dev)
+    out_p = _dense(out, "out", _BF16, shape, dev)
+    cache = _cache(k_pool, v_pool, k_scale, v_scale, n_k, d, dev)
+    B, R, table_p, start_p, cu_p = _packed(T, page_table, start, cu_tokens, dev)
+    sink_p = lse_p = ws_p = ws_bytes = 0
+    if sink_logit is not None:
+        sink_p = _dense(sink_logit, "sink_logit", _F32T, (n_h,), dev)
+    if lse_out is not None:
+        lse_p = _dense(lse_out, "lse_out", _F32T, (T, n_h), dev)
+    if workspace is not None:
+        ws_bytes = workspace.shape[0]
+        ws_p = _dense(workspace, "workspace", _U8T, (ws_bytes,), dev)
+    if dev < 0:
+        raise ValueError("the tensors are on the CPU")
+    try:
+        args = _KV_ATTN_ARGS.pack(q_p, q_stride, T, n_h, n_k, d, *cache, table_p, B, R, start_p, cu_p,
+                                  _NO_WINDOW if window is None else window, sink_p, d ** -0.5 if scale is None else scale,
+                                  out_p, lse_p, ws_p, ws_bytes, _raw_stream(dev) if stream is None else _stream(stream))
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"fm_kv_attn_fp8: {e}") from None
+    st = lib().fm_kv_attn_fp8(args)
+    if st:
+        _check(st)
+
+
+def fm_prompt_attn(q, k, v, out, cu_q=None, cu_k=None, window=None, sink_logit=None, scale=None, lse_out=None,
+                   stream=None) -> None:
+    """Causal attention over whole prompts: q [T,n_h,d], k, v [Tk,n_k,d] bf16 (any token
+    strides), packed sequences with offsets cu_q [B+1] int32 (None: one sequence) and cu_k
+    (None: cu_q's); a sequence's queries are the last of its keys.  window (None: no
+    limit), sink_logit [n_h] fp32 or None, scale (None: d ** -0.5) -> out [T,n_h,d] bf16,
+    lse_out [T,n_h] fp32 or None."""
+    dev = _device(q, "q")
+    shape = _shape(q, "q", 3)
+    T, n_h, d = shape
+    Tk, n_k, _ = _shape(k, "k", 3)
+    q_p, q_stride = _rows(q, "q", _BF16, shape, dev)
+    k_p, k_stride = _rows(k, "k", _BF16, (Tk, n_k, d), dev)
+    v_p, v_stride = _rows(v, "v", _BF16, (Tk, n_k, d), dev)
+    out_p = _dense(out, "out", _BF16, shape, dev)
+    B, cuq_p, cuk_p, sink_p, lse_p = 1, 0, 0, 0, 0
+    if cu_q is not None:
+        B = _shape(cu_q, "cu_q", 1)[0] - 1
+        cuq_p = _dense(cu_q, "cu_q", _I32T, (B + 1,), dev)
+    if cu_k is not None:
+        if cu_q is None:
+            raise ValueError("cu_k needs cu_q")
+        cuk_p = _dense(cu_k, "cu_k", _I32T, (B + 1,), dev)
+    if sink_logit is not None:
+        sink_p = _dense(sink_logit, "sink_logit", _F32T, (n_h,), dev)
+    if lse_out is not None:
+        lse_p = _dense(lse_out, "lse_out", _F32T, (T, n_h), dev)
+    if dev < 0:
+        raise ValueError("the tensors are on the CPU")
+    try:
+        args = _PROMPT_ARGS.pack(q_p, q_stride, k_p, k_stride, v_p, v_stride, T, Tk, n_h, n_k, d, B, cuq_p, cuk_p,
+                                 _NO_WINDOW if window is None else window, sink_p, d ** -0.5 if scale is None else scale,
+                                 out_p, lse_p, _raw_stream(dev) if stream is None else _stream(stream))
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"fm_prompt_attn: {e}") from None
+    st = lib().fm_prompt_attn(args)
+    if st:
+        _check(st)

@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfm_index.so")
 SOURCES = ["fm_api.cu", "memindex.cu", "memindex_fp8.cu", "retriever.cu", "topk.cu", "paged.cu", "prefill.cu", "noalloc.cu",
-           "recall.cu", "query_chain.cu", "qk_norm_rope.cu", "csa_attn.cu"]
+           "recall.cu", "query_chain.cu", "qk_norm_rope.cu", "csa_attn.cu", "kv_append.cu", "kv_attn_fp8.cu",
+           "prompt_attn.cu"]
 ARCH = ["-gencode=arch=compute_103a,code=sm_103a"]
 CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 NVCC = os.path.join(CUDA_HOME, "bin", "nvcc")

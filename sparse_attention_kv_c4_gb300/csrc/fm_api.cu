@@ -71,6 +71,31 @@ fm_status make_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const
   return FM_OK;
 }
 
+void rope_turns(int rope_dim, double base, double factor, double orig_len, double beta_fast, double beta_slow,
+                uint64_t* turn) {
+  struct Table {
+    int rope_dim;
+    double base, factor, orig_len, beta_fast, beta_slow;
+    uint64_t turn[kMaxRopePairs];
+  };
+  static thread_local Table kept = {};
+  if (rope_dim > 0 && (kept.rope_dim != rope_dim || kept.base != base || kept.factor != factor ||
+                       kept.orig_len != orig_len || kept.beta_fast != beta_fast || kept.beta_slow != beta_slow)) {
+    kept.rope_dim = 0;
+    for (int i = 0; i < rope_dim / 2; ++i) {
+      const double f = yarn_freq(i, rope_dim, base, factor, orig_len, beta_fast, beta_slow);
+      kept.turn[i] = (uint64_t)ldexp(f / 6.283185307179586476925286766559, 64);  // f <= 1: at most 2^61.4
+    }
+    kept.base = base;
+    kept.factor = factor;
+    kept.orig_len = orig_len;
+    kept.beta_fast = beta_fast;
+    kept.beta_slow = beta_slow;
+    kept.rope_dim = rope_dim;
+  }
+  for (int i = 0; i < rope_dim / 2; ++i) turn[i] = kept.turn[i];
+}
+
 }  // namespace fm
 
 using namespace fm;

@@ -43,6 +43,12 @@ inline double yarn_freq(int i, int rope_dim, double base, double factor, double 
   return (1.0 - gamma) * theta / factor + gamma * theta;
 }
 
+// theta'_i / 2 pi in units of 2^-64 turns for the rope_dim / 2 pairs (at most
+// kMaxRopePairs).  The last parameters' table is kept per thread: 32 powers take 2 us.
+constexpr int kMaxRopePairs = 128;
+void rope_turns(int rope_dim, double base, double factor, double orig_len, double beta_fast, double beta_slow,
+                uint64_t* turn);
+
 // ---- launchers (arguments already validated) -------------------------------
 struct MemindexArgs {
   const uint16_t* q;

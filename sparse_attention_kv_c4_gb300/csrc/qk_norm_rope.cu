@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxPairs = 128;
+constexpr int kMaxPairs = kMaxRopePairs;
 constexpr int kPage = 64;
 
 struct NormRopeParams {
@@ -279,29 +279,7 @@ FM_API fm_status fm_qk_norm_rope(const int64_t* pos, int T, int d, int rope_dim,
   p.rope_start = d - rope_dim;
   p.inv_d = 1.0f / (float)d;
   p.eps = eps;
-  // the frequencies of this thread's last parameters are kept: 32 powers take 2 us
-  struct Table {
-    int rope_dim;
-    double base, factor, orig_len, beta_fast, beta_slow;
-    uint64_t turn[kMaxPairs];
-  };
-  static thread_local Table kept = {};
-  if (rope_dim > 0 && (kept.rope_dim != rope_dim || kept.base != rope_base || kept.factor != rope_factor ||
-                       kept.orig_len != rope_orig_len || kept.beta_fast != rope_beta_fast ||
-                       kept.beta_slow != rope_beta_slow)) {
-    kept.rope_dim = 0;
-    for (int i = 0; i < rope_dim / 2; ++i) {
-      const double f = yarn_freq(i, rope_dim, rope_base, rope_factor, rope_orig_len, rope_beta_fast, rope_beta_slow);
-      kept.turn[i] = (uint64_t)ldexp(f / 6.283185307179586476925286766559, 64);  // f <= 1: at most 2^61.4
-    }
-    kept.base = rope_base;
-    kept.factor = rope_factor;
-    kept.orig_len = rope_orig_len;
-    kept.beta_fast = rope_beta_fast;
-    kept.beta_slow = rope_beta_slow;
-    kept.rope_dim = rope_dim;
-  }
-  for (int i = 0; i < rope_dim / 2; ++i) p.turn[i] = kept.turn[i];
+  rope_turns(rope_dim, rope_base, rope_factor, rope_orig_len, rope_beta_fast, rope_beta_slow, p.turn);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int nvec = d / 8;
   cudaError_t e;

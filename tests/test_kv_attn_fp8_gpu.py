@@ -1,0 +1,236 @@
+"""fm_kv_attn_fp8 against the fp64 formula: lengths from nothing to many pages, groups, windows, sinks, drafted
+tokens, garbage in every cell that is no key, strides, padded batches, graphs."""
+import numpy as np
+import pytest
+
+import attn_ref as ref
+import grouped_ref as gr
+
+pytestmark = pytest.mark.gpu
+FOREVER = 1 << 62
+
+
+@pytest.fixture(scope="module")
+def torch_dev():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch, torch.device("cuda:0")
+
+
+def up(torch, dev, a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(dev)
+
+
+def make(rng, lens, starts, H, K, d, layers=1, spread=0.3, drop=(), free=0):
+    """A cache with NaN codes and NaN scales in every cell and block that holds no token, and its fp64 values."""
+    B = len(lens)
+    ends = [max(s + n, 0) for n, s in zip(lens, starts)]
+    R = max([(e + 63) // 64 for e in ends] + [1]) + free
+    P = B * R + 2
+    table = rng.permutation(P)[:B * R].reshape(B, R).astype(np.int32)
+    codes = np.full((2, P, layers, K, 64, d), 0x7F, np.uint8)
+    scales = np.full((2, P, layers, K, 4), np.nan, np.float32)
+    mid = layers // 2
+    k, v, size, scale_of, held = [], [], [], [], []
+    for b in range(B):
+        m = ends[b]
+        c = rng.integers(0, 256, (2, R * 64, K, d)).astype(np.uint8)
+        c[(c & 127) == 127] = 0
+        normal = gr.e4m3_codes(np.clip(100 * rng.standard_normal((2, R * 64, K, d)), -448, 448))
+        c = np.where(rng.random((2, R * 64, K, 1)) < 0.1, c, normal)
+        s = (np.exp(spread * rng.standard_normal((2, R * 4, K))) * 0.01).astype(np.float32)
+        ok = np.ones(m, bool)
+        for page in range(R):
+            if (b, page) in drop:
+                ok[page * 64:(page + 1) * 64] = False
+                table[b, page] = -1
+                continue
+            at = table[b, page]
+            for row in range(64):
+                if page * 64 + row < m:
+                    codes[:, at, mid, :, row] = c[:, page * 64 + row]
+            for blk in range(4):
+                if page * 64 + blk * 16 < m:
+                    scales[:, at, mid, :, blk] = s[:, page * 4 + blk]
+        j = np.arange(m)
+        x = gr.VALUES[c[:, :m]] * s.astype(np.float64)[:, j // 16][..., None]
+        k.append(x[0])
+        v.append(x[1])
+        size.append(np.abs(gr.VALUES[c[1, :m]]))
+        scale_of.append(s[1].astype(np.float64)[j // 16][..., None])
+        held.append(ok)
+    return table, codes, scales, k, v, size, scale_of, held
+
+
+def check(torch, dev, rng, lens, starts, H, K, d, window=None, sink=False, layers=1, pad=0, offsets=True, scale=None, **kw):
+    import sparse_attention_kv_c4_gb300 as fm
+    flags = kw.pop("flags", 0)
+    q_size = kw.pop("q_size", 1.0)
+    table, codes, scales, k, v, size, scale_of, held = make(rng, lens, starts, H, K, d, layers, **kw)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T = int(cu[-1]) + pad
+    fused = ref.bf16(q_size * rng.standard_normal((T, H * d + 16)))
+    q = up(torch, dev, fused.view(np.int16))[:, :H * d].view(T, H, d)
+    cd, sd = up(torch, dev, codes), up(torch, dev, scales)
+    mid = layers // 2
+    sinks = rng.standard_normal(H).astype(np.float32) if sink else None
+    out = torch.full((T, H, d), 77, dtype=torch.int16, device=dev)
+    lse = torch.full((T, H), 77.0, device=dev)
+    ws = torch.empty(max(fm.fm_kv_attn_fp8_workspace(T, H, K, d), 1), dtype=torch.uint8, device=dev)
+    ws.fill_(0xFF)
+    fm.fm_kv_attn_fp8(q, cd[0][:, mid], cd[1][:, mid], sd[0][:, mid], sd[1][:, mid], up(torch, dev, table),
+                      up(torch, dev, np.array(starts, np.int64)), out, cu_tokens=up(torch, dev, cu) if offsets else None, window=window,
+                      sink_logit=None if sinks is None else up(torch, dev, sinks), scale=scale, lse_out=lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert fm.fm_device_status(reset=True) == flags
+    got, got_lse = out.cpu().numpy().view(np.uint16), lse.cpu().numpy().astype(np.float64)
+    assert (got[cu[-1]:] == 77).all() and (got_lse[cu[-1]:] == 77).all()
+    qf = ref.f64(fused[:, :H * d]).reshape(T, H, d)
+    for b, (n, s) in enumerate(zip(lens, starts)):
+        rows = slice(cu[b], cu[b + 1])
+        want, want_lse, tol, ltol = gr.attend(qf[rows], k[b], v[b], s, FOREVER if window is None else window, sinks,
+                                              d ** -0.5 if scale is None else scale, held[b], gr.HALF_FP16, (size[b], scale_of[b]))
+        g, gl = ref.f64(got[rows]), got_lse[rows]
+        empty = np.isneginf(want_lse)
+        assert (np.isneginf(gl) == empty).all() and (g[empty] == 0).all()
+        assert (np.abs(gl[~empty] - want_lse[~empty]) <= ltol[~empty]).all(), b
+        assert (np.abs(g - want) <= tol).all(), (b, np.abs(g - want).max())
+
+
+@pytest.mark.parametrize("lens,starts,H,K,d,window,sink", [
+    ([1], [0], 1, 1, 16, None, False), ([1], [36], 32, 8, 128, None, False), ([1] * 5, [0, 15, 16, 63, 64], 8, 8, 64, None, True),
+    ([1] * 7, [127, 300, 1, 700, 64, 65, 2000], 20, 4, 96, None, True), ([1] * 3, [900, 77, 4000], 64, 8, 128, 129, False),
+    ([1] * 3, [900, 77, 4000], 5, 1, 128, 1, True), ([1, 1], [50, 60], 4, 2, 32, 0, True), ([5] * 4, [0, 60, 123, 1000], 40, 8, 64, None, True),
+    ([3, 0, 8, 1], [10, 4, 300, 129], 6, 2, 112, 70, False), ([17, 2], [40, 500], 16, 1, 48, None, False), ([2, 130], [1, 5], 12, 4, 128, 65, True),
+    ([1], [9000], 128, 1, 128, None, False), ([1, 4], [33000, 900], 8, 2, 80, None, True), ([7], [20], 128, 1, 64, 9, True)])
+def test_matches_formula(torch_dev, lens, starts, H, K, d, window, sink):
+    torch, dev = torch_dev
+    check(torch, dev, np.random.default_rng(H + d + len(lens)), lens, starts, H, K, d, window, sink)
+
+
+def test_padded_batch_layers_between_and_no_offsets(torch_dev):
+    torch, dev = torch_dev
+    check(torch, dev, np.random.default_rng(1), [1, 3, 1], [200, 100, 30], 8, 2, 64, layers=3, pad=5)
+    check(torch, dev, np.random.default_rng(2), [1] * 9, [31 * b for b in range(9)], 8, 2, 128, layers=2, offsets=False)
+
+
+def test_pages_not_held_and_out_of_range(torch_dev):
+    torch, dev = torch_dev
+    rng = np.random.default_rng(3)
+    check(torch, dev, rng, [1, 2, 1, 1], [300, 200, 70, 64], 8, 2, 64, drop={(0, 1), (0, 3), (1, 0), (2, 0), (2, 1), (3, 1)}, free=1)
+    check(torch, dev, rng, [2, 1], [-2, -1], 4, 2, 64)
+
+
+def test_tables_that_are_too_short_or_name_no_page_are_flagged(torch_dev):
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    rng = np.random.default_rng(4)
+    table, codes, scales, k, v, size, scale_of, held = make(rng, [1, 1], [150, 20], 4, 2, 64)
+    table[0, 1] = codes.shape[1] + 7
+    held[0][64:128] = False
+    q = ref.bf16(rng.standard_normal((2, 4, 64)))
+    out, ws = torch.zeros((2, 4, 64), dtype=torch.int16, device=dev), torch.empty(max(1, fm.fm_kv_attn_fp8_workspace(2, 4, 2, 64)), dtype=torch.uint8, device=dev)
+    cd, sd = up(torch, dev, codes), up(torch, dev, scales)
+    for start in ([150, 20], [5 * 64, 20], [1 << 61, 20]):  # the first sequence's last tokens lie past the table
+        st = torch.tensor(start, device=dev)
+        fm.fm_kv_attn_fp8(up(torch, dev, q.view(np.int16)), cd[0][:, 0], cd[1][:, 0], sd[0][:, 0], sd[1][:, 0], up(torch, dev, table), st, out, workspace=ws)
+        assert fm.fm_device_status(reset=True) == 1
+    got = ref.f64(out.cpu().numpy().view(np.uint16))
+    want, _, tol, _ = gr.attend(ref.f64(q)[1:], k[1], v[1], 20, FOREVER, None, 0.125, held[1], gr.HALF_FP16, (size[1], scale_of[1]))
+    assert (np.abs(got[1:] - want) <= tol).all()
+
+
+def test_scales_of_every_size(torch_dev):
+    """Values whose blocks' scales differ by e^30, scores of hundreds, queries near the ends of bf16."""
+    torch, dev = torch_dev
+    check(torch, dev, np.random.default_rng(5), [1, 3], [500, 90], 8, 2, 64, spread=8.0, scale=1e-6)
+    check(torch, dev, np.random.default_rng(6), [1, 3], [500, 90], 8, 2, 64, scale=60.0)
+    check(torch, dev, np.random.default_rng(7), [1, 3], [500, 90], 8, 2, 64, q_size=1e30, scale=1e-30)
+    check(torch, dev, np.random.default_rng(8), [1, 3], [500, 90], 8, 2, 64, q_size=1e-30, scale=1e30)
+
+
+def test_a_drafted_token_does_not_see_what_a_later_one_holds(torch_dev):
+    """The last draft's cell and scale are NaN: the earlier drafts' rows are as without it, its own row is NaN."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    rng = np.random.default_rng(11)
+    for start in (64, 40, 60, 15):  # the drafts within a block, over a block's and a page's border
+        table, codes, scales, k, v, size, scale_of, held = make(rng, [4], [start], 8, 2, 64)
+        last = start + 3
+        codes[1, table[0, last // 64], 0, 1, last % 64, 5] = 0x7F
+        q = ref.bf16(rng.standard_normal((4, 8, 64)))
+        out, ws = torch.zeros((4, 8, 64), dtype=torch.int16, device=dev), torch.empty(max(1, fm.fm_kv_attn_fp8_workspace(4, 8, 2, 64)), dtype=torch.uint8, device=dev)
+        cd, sd = up(torch, dev, codes), up(torch, dev, scales)
+        fm.fm_kv_attn_fp8(up(torch, dev, q.view(np.int16)), cd[0][:, 0], cd[1][:, 0], sd[0][:, 0], sd[1][:, 0], up(torch, dev, table),
+                          torch.tensor([start], device=dev), out, cu_tokens=torch.tensor([0, 4], dtype=torch.int32, device=dev), workspace=ws)
+        got = ref.f64(out.cpu().numpy().view(np.uint16))
+        assert np.isnan(got[3, 4:, 5]).all() and np.isnan(got).sum() == 4
+        want, _, tol, _ = gr.attend(ref.f64(q)[:3], k[0], v[0], start, FOREVER, None, 0.125, held[0], gr.HALF_FP16, (size[0], scale_of[0]))
+        assert (np.abs(got[:3] - want) <= tol).all()
+
+
+def test_long_caches_see_every_key(torch_dev):
+    """One long sequence beside short ones: a single key of another value among equal ones is found at every
+    place where the work may be split."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    d, K, H, m = 64, 2, 8, 40000
+    R = (m + 63) // 64
+    codes = torch.zeros((2, R + 1, K, 64, d), dtype=torch.uint8, device=dev)
+    scales = torch.full((2, R + 1, K, 4), 2.0, device=dev)
+    table = torch.stack([torch.randperm(R), torch.cat([torch.tensor([R]), torch.full((R - 1,), -1)])]).int().to(dev)
+    start = torch.tensor([m - 1, 10], device=dev)
+    q = torch.randn((2, H, d), device=dev).bfloat16()
+    out, lse = torch.empty((2, H, d), dtype=torch.bfloat16, device=dev), torch.empty((2, H), device=dev)
+    ws = torch.empty(max(1, fm.fm_kv_attn_fp8_workspace(2, H, K, d)), dtype=torch.uint8, device=dev)
+    places = sorted({0, 1, 15, 16, 63, 64, 65, m - 1, m - 2} | {int(x) for x in np.random.default_rng(0).integers(0, m, 60)})
+    for j in places:
+        page, row = int(table[0, j // 64]), j % 64
+        codes[1, page, :, row] = 0x7E  # 448
+        fm.fm_kv_attn_fp8(q, codes[0], codes[1], scales[0], scales[1], table, start, out, lse_out=lse, workspace=ws)
+        codes[1, page, :, row] = 0
+        want = 448 * 2.0 / m  # weights are equal: keys are zero
+        got = out[0].double().cpu().numpy()
+        assert (np.abs(got - want) <= want * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -9)).all(), j
+        assert (out[1] == 0).all().item()
+    assert np.abs(lse.cpu().numpy()[0] - np.log(m)).max() <= 2.0 ** -19 * 11 + m * 2.0 ** -24
+
+
+def test_two_calls_at_once_graph_and_same_results(torch_dev):
+    """The result is the same bits eager, replayed on another stream, and beside another call with a workspace
+    of its own; out may be q."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    rng = np.random.default_rng(12)
+    cases = []
+    for starts, H, K, d in (([5000, 100, 7000], 16, 4, 128), ([300, 9000], 8, 8, 64)):
+        table, codes, scales = make(rng, [1] * len(starts), starts, H, K, d)[:3]
+        T = len(starts)
+        cd, sd = up(torch, dev, codes), up(torch, dev, scales)
+        q = torch.randn((T, H, d), device=dev).bfloat16()
+        args = (cd[0][:, 0], cd[1][:, 0], sd[0][:, 0], sd[1][:, 0], up(torch, dev, table), torch.tensor(starts, device=dev))
+        ws = torch.empty(max(1, fm.fm_kv_attn_fp8_workspace(T, H, K, d)), dtype=torch.uint8, device=dev)
+        want = torch.empty_like(q)
+        fm.fm_kv_attn_fp8(q, *args, want, workspace=ws)
+        cases.append((q, args, ws, want))
+    streams = [torch.cuda.Stream(dev) for _ in cases]
+    graphs, outs = [], []
+    torch.cuda.synchronize()
+    for (q, args, ws, want), s in zip(cases, streams):
+        g, out = torch.cuda.CUDAGraph(), q.clone()
+        with torch.cuda.graph(g, stream=s):
+            fm.fm_kv_attn_fp8(out, *args, out, workspace=ws)
+        graphs.append(g)
+        outs.append(out)
+    for _ in range(5):
+        for (q, *_), out in zip(cases, outs):
+            out.copy_(q)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, _, _, want), out in zip(cases, outs):
+            assert (out.view(torch.int16) == want.view(torch.int16)).all()
+    assert fm.fm_device_status(reset=True) == 0
