@@ -1,43 +1,750 @@
-// kv_attn_fp8.cu -- attention of grouped heads over the paged 8-bit cache.
+// kv_attn_fp8.cu -- attention of grouped heads over the paged 8-bit cache: decode
+// steps and a few (drafted) tokens a sequence ("FlashMemory-DeepSeek-V4" README,
+// "compressed_k format": E4M3 codes with fp32 scales).
+//     s_j = scale (q . k_j),  out = sum_j e^{s_j} v_j / (sum_j e^{s_j} + e^{sink}),
+// k_j = e4m3(code) * scale of its block of 16 tokens and head, v_j alike.
+//
+// A cell is read once for all rows (token, query head) that share its head: 2 d bytes
+// for 4 d flops a row, so the kernel is bound by HBM up to some 30 rows.
+//
+// The work is the list of units (sequence, key head, row tile, page of 64 tokens), cut into
+// as many equal runs as there are SMs whatever the sequences' lengths; a CTA works
+// out its run from the offsets by itself.  In a CTA one warp brings pages in by TMA (a
+// ring of stages, 128-byte swizzle) and seven warps take a page each in turn:
+//   S^T = K Q^T   m16n8k16, 16 keys (one block of scales) x 8 rows, fp16 operands:
+//                 E4M3 is exact in fp16, queries are scaled to 2^14 by row
+//   softmax       against a running reference that moves only when a score
+//                 passes it by 2^8: most tiles need no reduction over lanes
+//   O^T += V^T P^T  the weights times the block's scale of V in fp16, kept in its range by
+//                 a reference of their own (the largest weight times scale)
+// The transposed products take rows in eights, and their operands come from the
+// cache's rows as they lie: a lane's 16 bytes of a key are four steps of K16 (the order of
+// the contraction is free), ldmatrix transposes V by pairs of bytes.  mma.sync, not tcgen05:
+// codes have to pass through registers to become fp16, and a few rows leave either idle.
+// A segment's seven partial results are joined through shared memory; an item that spans
+// CTAs by kv_join_kernel, in a fixed order.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "attn_plain.cuh"
+#include <atomic>
+
+#include "grouped.cuh"
 
 #define FM_API extern "C" __attribute__((visibility("default")))
 
 namespace fm {
 namespace {
 
-struct CacheSource {
-  const uint8_t *k_pool, *v_pool;
-  const float *k_scale, *v_scale;
-  int64_t P, page_stride, scale_stride;
-  const int32_t* table;
-  int R, d;
-  const int64_t* start;
-  unsigned int* status;
-  FM_DEV int64_t past(int b, int n) const {  // a position past 2^62 sees nothing, as a negative one
-    const int64_t s = start[b];
-    return s < 0 || s >= (int64_t(1) << 62) ? -(int64_t)n : s;
-  }
-  FM_DEV int64_t clamp(int64_t j) const {
-    if (j < (int64_t)R * kKvPage) return j;
-    atomicOr(status, FM_DEV_PAGE_RANGE);
-    return (int64_t)R * kKvPage - 1;
-  }
-  FM_DEV bool held(int b, int64_t j) const {
-    const int page = table[(int64_t)b * R + j / kKvPage];
-    if (page >= P) atomicOr(status, FM_DEV_PAGE_RANGE);
-    return page >= 0 && page < P;
-  }
-  FM_DEV float value(int b, int64_t j, int head, int e, bool is_k) const {
-    const int64_t page = table[(int64_t)b * R + j / kKvPage];
-    const int row = (int)(j % kKvPage);
-    const uint8_t c = (is_k ? k_pool : v_pool)[page * page_stride + ((int64_t)head * kKvPage + row) * d + e];
-    const float s = (is_k ? k_scale : v_scale)[page * scale_stride + head * kBlocksPerPage + row / kKvBlock];
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3))) * s;
-  }
+constexpr int kConsumers = 7;            // eight warps: two to a scheduler have 255 registers each
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kMaxCtas = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLow = -1e30f;          // below every score
+constexpr float kSlack = 8.f;           // how far a score (in log2) may pass its reference
+
+template <int D>
+struct Layout {
+  static constexpr int kTile = kKvPage * D;  // bytes of a page and head
+  static constexpr int kStages = D == 128 ? 11 : 16;
+  static constexpr int kPitch = D + 4;       // floats: rows 2c of a join are 8 banks apart
 };
+
+struct KvParams {
+  const uint16_t* q;
+  const float *k_scale, *v_scale, *sink;
+  const int32_t *page_table, *cu;
+  const int64_t* start;
+  uint16_t* out;
+  float* lse;
+  float* part_o;      // [2 CTAs][rows][D] unnormalised outputs
+  float4* part_ml;    // [2 CTAs][rows] (reference of scores, of weights times scales, sum)
+  int4* part_item;    // [CTAs] (sequence, head, row tile, CTAs that follow) of a CTA's begun item
+  int64_t q_stride_t, scale_stride, window;
+  int T, n_h, n_k, d, G, P, B, R;
+  float scale;
+  unsigned int* status;
+};
+
+template <int D, int NT>
+struct Smem {
+  uint8_t kv[Layout<D>::kStages][2][Layout<D>::kTile];  // 1024-byte aligned
+  float scales[Layout<D>::kStages][2][kBlocksPerPage];
+  float join[kConsumers][8][Layout<D>::kPitch];
+  float3 stats[kConsumers][8 * NT];
+  int held[Layout<D>::kStages];
+  uint64_t full[Layout<D>::kStages], empty[Layout<D>::kStages];
+  int64_t scan[kThreads / 32 + 1];
+  int64_t found;                                        // units before the run's first sequence
+  int seq;
+  int abort;
+};
+
+// A sequence of the call and the pages that its rows see.
+struct Seq {
+  int64_t start;
+  int begin, n, tiles, low, pages;  // low page, number of pages (at least one unit: a row without keys is written too)
+  bool none;                        // no page at all
+};
+
+template <int NT>
+FM_DEV Seq sequence(const KvParams& p, int b) {
+  Seq s;
+  s.begin = b;
+  s.n = 1;
+  if (p.cu) {
+    s.begin = offset_at(p.cu, b, p.T);
+    s.n = max(offset_at(p.cu, b + 1, p.T) - s.begin, 0);
+  }
+  s.start = p.start[b];
+  s.tiles = (int)(((int64_t)s.n * p.G + 8 * NT - 1) / (8 * NT));
+  const int64_t last = s.start + s.n - 1, limit = (int64_t)p.R * kKvPage;
+  const int64_t low = s.start < p.window ? 0 : s.start - p.window + 1;
+  s.none = s.start < 0 || s.start >= (int64_t(1) << 62) || p.window == 0 || low >= limit || p.R == 0;
+  s.low = s.none ? 0 : (int)(low / kKvPage);
+  s.pages = s.none ? 1 : (int)((last < limit ? last : limit - 1) / kKvPage) - s.low + 1;
+  return s;
+}
+template <int NT>
+FM_DEV int64_t units_of(const KvParams& p, int b) {
+  const Seq s = sequence<NT>(p, b);
+  return (int64_t)s.tiles * p.n_k * s.pages;
+}
+
+// First unit of CTA c's run.
+FM_DEV int64_t run_begin(int64_t units, int c, int ctas) {
+  const int64_t each = units / ctas, more = units % ctas;
+  return c * each + min((int64_t)c, more);
+}
+
+FM_DEV uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+FM_DEV uint32_t floats_half2(float a, float b) { return half2_bits(__floats2half2_rn(a, b)); }
+FM_DEV uint32_t codes_half2(uint32_t c) {  // of the low two codes
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xFFFFu), __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+FM_DEV float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+FM_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+FM_DEV uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+FM_DEV void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+FM_DEV uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+FM_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Row r of eight in a fragment is key row_key(r) of its eight keys, and a cell's 16-byte
+// chunk lies where the TMA's swizzle put it: with this order the eight lanes of a
+// 16-byte load, and the eight rows of an ldmatrix, meet eight different chunks.
+template <int D>
+FM_DEV int row_key(int r) { return D == 128 ? (r >> 1) | ((r & 1) << 2) : r; }
+template <int D>
+FM_DEV uint32_t chunk_at(int key, int chunk) {
+  return key * D + 16 * (D == 128 ? chunk ^ (key & 7) : chunk ^ ((key >> 1) & 3));
+}
+
+// ---------------------------------------------------------------------------------------
+// consumers
+
+template <int D, int NT>
+struct Rows {
+  uint32_t q[D / 16][NT][2];    // B fragments: row g of each eight, elements of the lane's chunks
+  float f[NT][2];               // columns 2c, 2c + 1: factor from q . code to scores in log2 (times K's scale)
+  int pos[NT][2], low[NT][2];   // the last and the first position that they see (last below first: no row)
+  float m[NT][2], mv[NT][2], l[NT][2];
+  float o[D / 16][NT][4];       // (d = 16 j + 2 g, column 2c), (.., 2c + 1), (d + 1, 2c), (d + 1, 2c + 1)
+  int least, most, low_least, low_most;  // of the tile's first and last row
+};
+
+template <int D, int NT>
+FM_DEV void load_rows(const KvParams& p, const Seq& s, int head, int tile, Rows<D, NT>& w) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int rows = s.n * p.G, row0 = tile * 8 * NT;
+  // positions past the table's reach are alike: 2^30 is one
+  auto last_of = [&](int row) { return (int)max(min(s.start + row / p.G, (int64_t)1 << 30), (int64_t)-1); };
+  auto low_of = [&](int row) {
+    const int64_t pos = s.start + row / p.G;
+    return pos < p.window ? 0 : (int)min(pos - p.window + 1, (int64_t)1 << 30);
+  };
+  const int row1 = min(rows, row0 + 8 * NT) - 1;
+  w.least = last_of(row0);
+  w.most = last_of(row1);
+  w.low_least = low_of(row0);
+  w.low_most = low_of(row1);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = row0 + 8 * nt + g;
+    const bool in = r < rows;
+    const int t = in ? r / p.G : 0;
+    const uint16_t* src = p.q + (int64_t)(s.begin + t) * p.q_stride_t + (head * p.G + (in ? r - t * p.G : 0)) * p.d;
+    uint32_t raw[D / 64][8];
+    float top = 0.f;
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {
+      const int e = 16 * (c + 4 * h);
+      uint4 a = make_uint4(0, 0, 0, 0), b = a;
+      if (in && e < p.d) {
+        a = *reinterpret_cast<const uint4*>(src + e);
+        b = *reinterpret_cast<const uint4*>(src + e + 8);
+      }
+      const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        raw[h][i] = u[i];
+        const float2 x = bf16x2_floats(u[i]);
+        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+      }
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // 2^(14 - exponent) brings the row's largest to [2^14, 2^15); the two factors of a scaling by
+    // more than 2^127 are applied one after the other
+    int e = top > 0.f && top < INFINITY ? (int)(__float_as_uint(top) >> 23) - 127 : 14;
+    e = max(e, -110) - 14;
+    const float down = __uint_as_float((uint32_t)(127 - (e >> 1)) << 23), down2 = __uint_as_float((uint32_t)(127 - (e - (e >> 1))) << 23);
+    const float up = __uint_as_float((uint32_t)(127 + (e >> 1)) << 23), up2 = __uint_as_float((uint32_t)(127 + (e - (e >> 1))) << 23);
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 x = bf16x2_floats(raw[h][i]);
+        w.q[4 * h + (i >> 1)][nt][i & 1] = floats_half2(x.x * down * down2, x.y * down * down2);
+      }
+    const float factor = p.scale * kLog2e * up * up2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w.f[nt][i] = __shfl_sync(0xffffffffu, factor, 4 * (2 * c + i));
+      const int row = row0 + 8 * nt + 2 * c + i;
+      w.pos[nt][i] = row < rows ? last_of(row) : -1;
+      w.low[nt][i] = row < rows ? low_of(row) : 0;
+      w.m[nt][i] = w.mv[nt][i] = kLow;
+      w.l[nt][i] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w.o[j][nt][i] = 0.f;
+}
+
+// O^T += V^T P^T over a block of 16 keys.  keep0, keep1: which of the lane's keys of V (bytes: two of the
+// first, two of the second) are read as they are, the others as zeros.
+template <int D, int NT, bool Masked, class Use>
+FM_DEV void values_block(uint32_t v_smem, int block, uint32_t keep0, uint32_t keep1, Use use) {
+  const int lane = threadIdx.x & 31;
+  // lanes 0-7 address the rows of the matrix (keys 0-7, chunk 2j), 8-15 (8-15, 2j), 16-23 (0-7, 2j + 1), 24-31
+  const int key = 16 * block + 8 * ((lane >> 3) & 1) + row_key<D>(lane & 7);
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    uint32_t r[4];
+    ldmatrix4_trans(r, v_smem + chunk_at<D>(key, 2 * j + (lane >> 4)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t x0 = r[2 * i], x1 = r[2 * i + 1];
+      if (Masked) {
+        x0 &= keep0;
+        x1 &= keep1;
+      }
+      x0 = __byte_perm(x0, 0, 0x3120);
+      x1 = __byte_perm(x1, 0, 0x3120);
+      use(2 * j + i, codes_half2(x0), codes_half2(x0 >> 16), codes_half2(x1), codes_half2(x1 >> 16));
+    }
+  }
+}
+
+// `Blocks` blocks of 16 keys from block `at` of a page on.
+template <int D, int NT, int Blocks, bool Partial>
+FM_DEV void key_blocks(const KvParams& p, const uint8_t* kv, const float (*scales)[kBlocksPerPage], int at, int page_first,
+                       Rows<D, NT>& w) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const uint32_t k_smem = smem_u32(kv) + 16 * at * D, v_smem = k_smem + Layout<D>::kTile;  // 16 rows keep the swizzle's phase
+  const int first = page_first + 16 * at;
+  float s[Blocks][NT][4];
+#pragma unroll
+  for (int block = 0; block < Blocks; ++block) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[block][nt][i] = 0.f;
+    const int key = 16 * block + row_key<D>(g);
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {
+      const uint4 lo = lds16(k_smem + chunk_at<D>(key, c + 4 * h)), hi = lds16(k_smem + chunk_at<D>(key + 8, c + 4 * h));
+      const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a0 = codes_half2(a[i]), a1 = codes_half2(b[i]), a2 = codes_half2(a[i] >> 16), a3 = codes_half2(b[i] >> 16);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(s[block][nt], a0, a1, a2, a3, w.q[4 * h + i][nt][0], w.q[4 * h + i][nt][1]);
+      }
+    }
+  }
+  float ks[Blocks], vs[Blocks];
+#pragma unroll
+  for (int block = 0; block < Blocks; ++block) {
+    ks[block] = scales[0][at + block];
+    vs[block] = scales[1][at + block];
+  }
+  // scores in log2; how far they pass their references
+  bool passes = false;
+  float top[NT][2], topv[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      top[nt][i] = topv[nt][i] = -INFINITY;
+#pragma unroll
+      for (int block = 0; block < Blocks; ++block) {
+        const float f = ks[block] * w.f[nt][i];
+        float a = s[block][nt][i] * f, b = s[block][nt][i + 2] * f;
+        if (Partial) {
+          const int j = first + 16 * block + row_key<D>(g);
+          if (j > w.pos[nt][i] || j < w.low[nt][i]) a = -INFINITY;
+          if (j + 8 > w.pos[nt][i] || j + 8 < w.low[nt][i]) b = -INFINITY;
+        }
+        s[block][nt][i] = a;
+        s[block][nt][i + 2] = b;
+        const float x = fmaxf(a, b);
+        top[nt][i] = fmaxf(top[nt][i], x);
+        topv[nt][i] = fmaxf(topv[nt][i], x + __log2f(vs[block]));
+      }
+      passes |= top[nt][i] > w.m[nt][i] + kSlack || topv[nt][i] > w.mv[nt][i] + kSlack;
+    }
+  if (__any_sync(0xffffffffu, passes)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          top[nt][i] = fmaxf(top[nt][i], __shfl_xor_sync(0xffffffffu, top[nt][i], o));
+          topv[nt][i] = fmaxf(topv[nt][i], __shfl_xor_sync(0xffffffffu, topv[nt][i], o));
+        }
+        const float m = fmaxf(w.m[nt][i], top[nt][i]), mv = fmaxf(w.mv[nt][i], topv[nt][i]);
+        w.l[nt][i] *= exp2_fast(w.m[nt][i] - m);
+        const float keep = exp2_fast(w.mv[nt][i] - mv);
+        w.m[nt][i] = m;
+        w.mv[nt][i] = mv;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          w.o[j][nt][i] *= keep;
+          w.o[j][nt][i + 2] *= keep;
+        }
+      }
+  }
+  // weights, their sums, and the weights times V's scale in fp16 as the second product's operand
+  uint32_t pt[Blocks][NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float shift[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) shift[i] = exp2_fast(fminf(w.m[nt][i] - w.mv[nt][i], 126.f));
+#pragma unroll
+    for (int block = 0; block < Blocks; ++block) {
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = exp2_fast(s[block][nt][i] - w.m[nt][i & 1]);
+        w.l[nt][i & 1] += e;
+        x[i] = e * (vs[block] * shift[i & 1]);
+        if (Partial && s[block][nt][i] == -INFINITY) x[i] = 0.f;  // a block's scale may be anything where no key is
+      }
+      pt[block][nt][0] = transpose8x8(floats_half2(x[0], x[1]));
+      pt[block][nt][1] = transpose8x8(floats_half2(x[2], x[3]));
+    }
+  }
+  auto plain = [&](int block) {
+    return [&w, &pt, block](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_f16(w.o[j][nt], a0, a1, a2, a3, pt[block][nt][0], pt[block][nt][1]);
+    };
+  };
+  if (!Partial) {
+#pragma unroll
+    for (int block = 0; block < Blocks; ++block) values_block<D, NT, false>(v_smem, block, 0, 0, plain(block));
+    return;
+  }
+  // Cells that are no keys of any row are taken as zeros: they may hold NaN, and zero times that is NaN.
+  auto keep_of = [&](int block, int half, int lo, int hi) {
+    const int j0 = first + 16 * block + 8 * half + row_key<D>(2 * c), j1 = first + 16 * block + 8 * half + row_key<D>(2 * c + 1);
+    return (j0 >= lo && j0 <= hi ? 0xFFFFu : 0u) | (j1 >= lo && j1 <= hi ? 0xFFFF0000u : 0u);
+  };
+  // NaN among the keys that some rows see and others do not
+  bool bad = false;
+  if (w.least != w.most) {
+#pragma unroll
+    for (int block = 0; block < Blocks; ++block) {
+      const uint32_t k0 = keep_of(block, 0, w.low_least, w.most) & ~keep_of(block, 0, w.low_most, w.least);
+      const uint32_t k1 = keep_of(block, 1, w.low_least, w.most) & ~keep_of(block, 1, w.low_most, w.least);
+      const int key = 16 * block + 8 * ((lane >> 3) & 1) + row_key<D>(lane & 7);
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        uint32_t r[4];
+        ldmatrix4_trans(r, v_smem + chunk_at<D>(key, 2 * j + (lane >> 4)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bad |= (((r[i] & (i & 1 ? k1 : k0) & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+      }
+    }
+    bad = __any_sync(0xffffffffu, bad);
+  }
+  if (!bad) {
+#pragma unroll
+    for (int block = 0; block < Blocks; ++block)
+      values_block<D, NT, true>(v_smem, block, keep_of(block, 0, w.low_least, w.most), keep_of(block, 1, w.low_least, w.most), plain(block));
+    return;
+  }
+  // one token at a time: a product with the keys that it sees, added to its own columns
+  for (int pos = w.least; pos <= w.most; ++pos) {
+    const int lo = w.low_most > 0 ? max(w.low_most - (w.most - pos), 0) : 0;
+#pragma unroll
+    for (int block = 0; block < Blocks; ++block)
+      values_block<D, NT, true>(v_smem, block, keep_of(block, 0, lo, pos), keep_of(block, 1, lo, pos),
+                                [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                                  for (int nt = 0; nt < NT; ++nt) {
+                                    float x[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma_f16(x, a0, a1, a2, a3, pt[block][nt][0], pt[block][nt][1]);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                      if (w.pos[nt][i & 1] == pos) w.o[j][nt][i] += x[i];
+                                  }
+                                });
+  }
+}
+
+// A page: all of its keys at once where registers allow, else in halves.
+template <int D, int NT, bool Partial>
+FM_DEV void page_tile(const KvParams& p, const uint8_t* kv, const float (*scales)[kBlocksPerPage], int first, Rows<D, NT>& w) {
+  constexpr int kBlocks = D * NT <= 256 ? 4 : 2;
+#pragma unroll 1
+  for (int at = 0; at < kBlocksPerPage; at += kBlocks) key_blocks<D, NT, kBlocks, Partial>(p, kv, scales, at, first, w);
+}
+
+FM_DEV void store_output(const KvParams& p, int64_t at, int e, float x) {
+  if (e < p.d) p.out[at * p.d + e] = (uint16_t)(floats_bf16x2(x, 0.f) & 0xFFFFu);
+}
+
+// A row's factor from its sum of weights times codes to the output, and its log-sum-exp.
+FM_DEV float row_factor(const KvParams& p, int h, float m, float mv, float l) {
+  if (l == 0.f) return 0.f;
+  const float z = p.sink ? l + exp2_fast(p.sink[h] * kLog2e - m) : l;
+  return exp2_fast(mv - m) / z;
+}
+FM_DEV float row_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f; }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_constant__ CUtensorMap k_map,
+                                                              const __grid_constant__ CUtensorMap v_map,
+                                                              const __grid_constant__ KvParams p) {
+  using L = Layout<D>;
+  extern __shared__ __align__(1024) uint8_t raw_smem[];
+  Smem<D, NT>& sh = *reinterpret_cast<Smem<D, NT>*>(raw_smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    tma_prefetch(&k_map);
+    tma_prefetch(&v_map);
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  // programmatic dependent launch: what a kernel before wrote may be read from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // the run of this CTA: units of all sequences, then the sequence that holds the run's first
+  int64_t mine = 0;
+  for (int b = tid; b < p.B; b += kThreads) mine += units_of<NT>(p, b);
+  const int64_t own = p.B <= kThreads ? mine : 0;
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sh.scan[warp] = mine;
+  __syncthreads();
+  int64_t units = 0;
+  for (int i = 0; i < kThreads / 32; ++i) units += sh.scan[i];
+  const int64_t u0 = run_begin(units, blockIdx.x, gridDim.x), u1 = run_begin(units, blockIdx.x + 1, gridDim.x);
+  if (tid == 0) p.part_item[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (u0 >= u1) return;
+  int64_t before = 0;  // units of the sequences before this round's
+  for (int base = 0; base < p.B; base += kThreads) {
+    const int b = base + tid;
+    const int64_t mine_b = p.B <= kThreads ? own : b < p.B ? units_of<NT>(p, b) : 0;
+    int64_t incl = mine_b;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    __syncthreads();
+    if (lane == 31) sh.scan[warp] = incl;
+    __syncthreads();
+    int64_t at = before;
+    for (int i = 0; i < warp; ++i) at += sh.scan[i];
+    for (int i = 0; i < kThreads / 32; ++i) before += sh.scan[i];
+    at += incl - mine_b;
+    if (mine_b > 0 && at <= u0 && u0 < at + mine_b) {
+      sh.found = at;
+      sh.seq = b;
+    }
+    if (before > u0) break;  // the same for every thread
+  }
+  __syncthreads();
+  int b = sh.seq;
+  int64_t local = u0 - sh.found;  // the unit's place in its sequence
+
+  if (warp == kConsumers) {
+    // ---------------------------------------------------------------- producer
+    int64_t u = u0;
+    int n = 0;
+    bool ok = true;
+    for (; ok && u < u1; ++b, local = 0) {
+      const Seq s = sequence<NT>(p, b);
+      const int64_t all = (int64_t)s.tiles * p.n_k * s.pages;
+      if (all == 0) continue;
+      if (lane == 0 && !s.none && s.start + s.n - 1 >= (int64_t)p.R * kKvPage) atomicOr(p.status, FM_DEV_PAGE_RANGE);
+      if (lane == 0 && s.none && s.start >= 0 && p.window > 0) atomicOr(p.status, FM_DEV_PAGE_RANGE);
+      int64_t item = local / s.pages;
+      int page_at = (int)(local - item * s.pages);
+      int listed = -1;   // lane i: the table's entry of page page_from + i
+      int page_from = -64;
+      for (; ok && item < (int64_t)s.tiles * p.n_k && u < u1; ++item, page_at = 0) {
+        const int head = (int)(item / s.tiles);
+        for (; page_at < s.pages && u < u1; ++page_at, ++u, ++n) {
+          if (page_at < page_from || page_at >= page_from + 32) {
+            page_from = page_at;
+            listed = -1;
+            if (!s.none && page_at + lane < s.pages) listed = p.page_table[(int64_t)b * p.R + s.low + page_at + lane];
+            if (listed >= p.P) {
+              atomicOr(p.status, FM_DEV_PAGE_RANGE);
+              listed = -1;
+            }
+          }
+          const int page = __shfl_sync(0xffffffffu, listed, page_at - page_from);
+          const int stage = n % L::kStages, turn = n / L::kStages;
+          if (turn > 0) ok = mbar_wait(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            sh.held[stage] = page >= 0;
+            if (page >= 0) {
+              mbar_arrive_expect_tx(&sh.full[stage], 2 * L::kTile + 2 * kBlocksPerPage * 4);
+              tma_load_3d(sh.kv[stage][0], &k_map, &sh.full[stage], 0, head * kKvPage, page);
+              tma_load_3d(sh.kv[stage][1], &v_map, &sh.full[stage], 0, head * kKvPage, page);
+              bulk_load(sh.scales[stage][0], p.k_scale + page * p.scale_stride + head * kBlocksPerPage, 16, &sh.full[stage]);
+              bulk_load(sh.scales[stage][1], p.v_scale + page * p.scale_stride + head * kBlocksPerPage, 16, &sh.full[stage]);
+            } else {
+              mbar_arrive(&sh.full[stage]);
+            }
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0)  // gave up: the copies in flight land before the CTA's memory is another's
+      for (int i = max(n - L::kStages, 0); i < n; ++i) mbar_wait_drain(&sh.full[i % L::kStages], (i / L::kStages) & 1);
+    return;
+  }
+
+  // ------------------------------------------------------------------ consumers
+  Rows<D, NT> w;
+  int64_t u = u0;
+  for (; u < u1; ++b, local = 0) {
+    const Seq s = sequence<NT>(p, b);
+    if (s.tiles == 0) continue;
+    int64_t item = local / s.pages;
+    int page0 = (int)(local - item * s.pages);
+    for (; item < (int64_t)s.tiles * p.n_k && u < u1; ++item, page0 = 0) {
+      const int head = (int)(item / s.tiles), tile = (int)(item - (int64_t)head * s.tiles);
+      const int64_t from = u;
+      const int pages = (int)min((int64_t)(s.pages - page0), u1 - u);  // of this segment
+      u += pages;
+      load_rows<D, NT>(p, s, head, tile, w);
+      for (int i = 0; i < pages; ++i) {
+        const int64_t n = from + i - u0;
+        if ((int)(n % kConsumers) != warp) continue;
+        const int stage = (int)(n % L::kStages);
+        const bool ok = mbar_wait(&sh.full[stage], (uint32_t)(n / L::kStages) & 1, &sh.abort, p.status);
+        const int first = (s.low + page0 + i) * kKvPage;
+        const bool some = ok && sh.held[stage] && first <= w.most && first + kKvPage > w.low_least;
+        if (__all_sync(0xffffffffu, some)) {
+          if (first + kKvPage - 1 <= w.least && first >= w.low_most)
+            page_tile<D, NT, false>(p, sh.kv[stage][0], sh.scales[stage], first, w);
+          else
+            page_tile<D, NT, true>(p, sh.kv[stage][0], sh.scales[stage], first, w);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[stage]);
+      }
+      // join the warps' results
+      const bool begins = page0 == 0, ends = page0 + pages == s.pages;
+      const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float l = w.l[nt][i];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+          if (g == 0) sh.stats[warp][8 * nt + 2 * c + i] = make_float3(w.m[nt][i], w.mv[nt][i], l);
+        }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (nt > 0) named_bar_sync(1, kConsumers * 32);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float2*>(&sh.join[warp][2 * c + i][16 * j + 2 * g]) = make_float2(w.o[j][nt][i], w.o[j][nt][i + 2]);
+        named_bar_sync(1, kConsumers * 32);
+        for (int i8 = warp; i8 < 8; i8 += kConsumers) {  // a row to a warp
+          const int row = 8 * nt + i8, r = tile * 8 * NT + row;
+          float m = kLow, mv = kLow, l = 0.f, f[kConsumers];
+#pragma unroll
+          for (int i = 0; i < kConsumers; ++i) {
+            m = fmaxf(m, sh.stats[i][row].x);
+            mv = fmaxf(mv, sh.stats[i][row].y);
+          }
+#pragma unroll
+          for (int i = 0; i < kConsumers; ++i) {
+            l += sh.stats[i][row].z * exp2_fast(sh.stats[i][row].x - m);
+            f[i] = exp2_fast(sh.stats[i][row].y - mv);
+          }
+          const bool in = r < s.n * p.G, whole = begins && ends;
+          const int t = in ? r / p.G : 0;
+          const int64_t at = (int64_t)(s.begin + t) * p.n_h + head * p.G + (r - t * p.G);  // the output's row
+          const int64_t part = ((int64_t)2 * blockIdx.x + begins) * 8 * NT + row;
+          const float factor = in && whole ? row_factor(p, head * p.G + r - t * p.G, m, mv, l) : 1.f;
+          for (int e = lane; e < D; e += 32) {
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < kConsumers; ++i) x = fmaf(sh.join[i][i8][e], f[i], x);
+            if (!whole)
+              p.part_o[part * D + e] = x;
+            else if (in)
+              store_output(p, at, e, l == 0.f ? 0.f : x * factor);
+          }
+          if (lane == 0) {
+            if (!whole)
+              p.part_ml[part] = make_float4(m, mv, l, 0.f);
+            else if (in && p.lse)
+              p.lse[at] = row_lse(m, l);
+          }
+        }
+      }
+      if (begins && !ends && warp == 0 && lane == 0) {
+        // the CTAs that have the rest of the item: up to the one with its last unit
+        const int64_t last = from + s.pages - 1;
+        const int64_t each = units / gridDim.x, more = units % gridDim.x;
+        const int64_t cta = last < more * (each + 1) ? last / (each + 1) : more + (last - more * (each + 1)) / each;
+        p.part_item[blockIdx.x] = make_int4(b, head, tile, (int)(cta - blockIdx.x));
+      }
+      named_bar_sync(1, kConsumers * 32);  // join and stats are free again
+    }
+  }
+}
+
+// Joins the parts of the items that span CTAs: block (c, row) the item that CTA c began.
+template <int D, int NT>
+__global__ void __launch_bounds__(D) kv_join_kernel(const __grid_constant__ KvParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int cta = blockIdx.x, row = blockIdx.y, e = threadIdx.x;
+  const int4 item = p.part_item[cta];
+  if (item.x < 0) return;
+  const int begin = p.cu ? offset_at(p.cu, item.x, p.T) : item.x;
+  const int n = p.cu ? offset_at(p.cu, item.x + 1, p.T) - begin : 1;
+  const int r = item.z * 8 * NT + row;
+  if (r >= n * p.G) return;
+  auto part = [&](int i) { return ((int64_t)2 * (cta + i) + (i == 0)) * 8 * NT + row; };
+  float m = kLow, mv = kLow;
+  for (int i = 0; i <= item.w; ++i) {
+    const float4 s = p.part_ml[part(i)];
+    m = fmaxf(m, s.x);
+    mv = fmaxf(mv, s.y);
+  }
+  float l = 0.f, x = 0.f;
+  for (int i = 0; i <= item.w; ++i) {
+    const float4 s = p.part_ml[part(i)];
+    l += s.z * exp2_fast(s.x - m);
+    x = fmaf(p.part_o[part(i) * D + e], exp2_fast(s.y - mv), x);
+  }
+  const int t = r / p.G, h = item.y * p.G + r - t * p.G;
+  const int64_t at = (int64_t)(begin + t) * p.n_h + h;
+  store_output(p, at, e, l == 0.f ? 0.f : x * row_factor(p, h, m, mv, l));
+  if (e == 0 && p.lse) p.lse[at] = row_lse(m, l);
+}
+
+// Rows in eights to a tile: those that a sequence's tokens have on average, so that its pages are read
+// once, or equal parts of them; at most what registers hold.
+int row_eights(int64_t rows, int d) {
+  const int64_t most = d <= 64 ? 4 : 3, eights = (rows + 7) / 8, tiles = (eights + most - 1) / most;
+  const int64_t need = (eights + tiles - 1) / tiles;
+  return d <= 64 && need == 3 ? 4 : (int)need;
+}
+
+size_t workspace_bytes(int eights, int d) {
+  return (size_t)kMaxCtas * (sizeof(int4) + 2 * 8 * (size_t)eights * (sizeof(float4) + (d <= 64 ? 64 : 128) * sizeof(float)));
+}
+
+template <int D, int NT>
+cudaError_t launch(KvParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, int sms, uint8_t* workspace, cudaStream_t stream) {
+  p.part_o = reinterpret_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float4*>(workspace + (size_t)kMaxCtas * 2 * 8 * NT * D * sizeof(float));
+  p.part_item = reinterpret_cast<int4*>(p.part_ml + (size_t)kMaxCtas * 2 * 8 * NT);
+  static_assert(sizeof(Smem<D, NT>) <= 227 * 1024, "shared memory of an SM");
+  const int smem = (int)sizeof(Smem<D, NT>);
+  static std::atomic<uint64_t> prepared{0};  // devices whose kernel has its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(prepared.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(kv_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) prepared.fetch_or(uint64_t(1) << dev);
+  }
+  const int64_t most = (int64_t)p.T * p.n_h * (p.R > 0 ? p.R : 1);  // units
+  int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  if (most < ctas) ctas = (int)most;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, NT>, k_map, v_map, (const KvParams)p)) != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)ctas, 8 * NT);
+  cfg.blockDim = dim3(D);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT>, (const KvParams)p);
+}
 
 }  // namespace
 }  // namespace fm
@@ -46,7 +753,7 @@ using namespace fm;
 
 FM_API size_t fm_kv_attn_fp8_workspace(int T, int n_h, int n_k, int d) {
   if (T < 0 || bad_heads(n_h, n_k, d)) return 0;
-  return 0;
+  return workspace_bytes(d <= 64 ? 4 : 3, d);
 }
 
 FM_API fm_status fm_kv_attn_fp8(const fm_kv_attn_fp8_args* a) {
@@ -73,12 +780,54 @@ FM_API fm_status fm_kv_attn_fp8(const fm_kv_attn_fp8_args* a) {
   const size_t need = fm_kv_attn_fp8_workspace(a->T, a->n_h, a->n_k, a->d);
   if (need > 0 && (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < need))
     return set_error(FM_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 256-byte aligned", who, need);
-  fm_status st = check_device(nullptr);
+  int sms = 0;
+  fm_status st = check_device(&sms);
   if (st != FM_OK) return st;
-  CacheSource src = {a->k_pool, a->v_pool, a->k_scale, a->v_scale, a->P, a->page_stride, a->scale_stride, a->page_table, a->R, a->d, a->start, nullptr};
-  if ((st = status_word(&src.status)) != FM_OK) return st;
-  PlainParams p = {a->q, a->q_stride_t, a->cu_tokens, a->out, a->lse_out, a->sink_logit, a->window, a->scale, a->T, a->n_h, a->n_k, a->d, a->B};
-  const cudaError_t e = launch_plain(p, src, reinterpret_cast<cudaStream_t>(a->stream));
+  KvParams p = {};
+  if ((st = status_word(&p.status)) != FM_OK) return st;
+  const int D = a->d <= 64 ? 64 : 128;
+  CUtensorMap k_map, v_map;
+  const uint64_t dims[3] = {(uint64_t)a->d, (uint64_t)a->n_k * kKvPage, a->P > 0 ? (uint64_t)a->P : 1};
+  const uint64_t strides[2] = {(uint64_t)a->d, (uint64_t)a->page_stride};
+  const uint32_t box[3] = {(uint32_t)D, kKvPage, 1};
+  const CUtensorMapSwizzle swizzle = D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  // without pages nothing is read: any address will do for the maps
+  const void *k_base = a->P > 0 ? (const void*)a->k_pool : a->q, *v_base = a->P > 0 ? (const void*)a->v_pool : a->q;
+  if ((st = make_tmap(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, k_base, dims, strides, box, swizzle)) != FM_OK) return st;
+  if ((st = make_tmap(&v_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, v_base, dims, strides, box, swizzle)) != FM_OK) return st;
+  p.q = a->q;
+  p.q_stride_t = a->q_stride_t;
+  p.k_scale = a->k_scale;
+  p.v_scale = a->v_scale;
+  p.scale_stride = a->scale_stride;
+  p.sink = a->sink_logit;
+  p.page_table = a->page_table;
+  p.cu = a->cu_tokens;
+  p.start = a->start;
+  p.out = a->out;
+  p.lse = a->lse_out;
+  p.window = a->window;
+  p.T = a->T;
+  p.n_h = a->n_h;
+  p.n_k = a->n_k;
+  p.d = a->d;
+  p.G = a->n_h / a->n_k;
+  p.P = (int)a->P;
+  p.B = a->B;
+  p.R = a->R;
+  p.scale = a->scale;
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(a->stream);
+  const int eights = row_eights(((int64_t)a->T + a->B - 1) / a->B * p.G, a->d);
+  cudaError_t e;
+  if (D == 64)
+    e = eights == 1   ? launch<64, 1>(p, k_map, v_map, sms, ws, stream)
+        : eights == 2 ? launch<64, 2>(p, k_map, v_map, sms, ws, stream)
+                      : launch<64, 4>(p, k_map, v_map, sms, ws, stream);
+  else
+    e = eights == 1   ? launch<128, 1>(p, k_map, v_map, sms, ws, stream)
+        : eights == 2 ? launch<128, 2>(p, k_map, v_map, sms, ws, stream)
+                      : launch<128, 3>(p, k_map, v_map, sms, ws, stream);
   if (e != cudaSuccess) return set_error(FM_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
   return FM_OK;
 }
