@@ -1,26 +1,512 @@
-// prompt_attn.cu -- causal attention of grouped heads over packed prompts.
-#include "attn_plain.cuh"
+// prompt_attn.cu -- causal attention of grouped heads over packed prompts
+// ("FlashMemory-DeepSeek-V4" README, "Two-level recall algorithm": the prompt's dense pass).
+//     s_j = scale (q . k_j),  out = sum_j e^{s_j} v_j / (sum_j e^{s_j} + e^{sink}),  keys up to the query's own
+//
+// 4 d flops for each query head and key that it sees: bound by the tensor cores.  A CTA
+// has two tiles of 128 rows of one key head against tiles of 128 keys.  A row is a (token, head of
+// the group), tokens first: a tile spans 128 / G tokens, so that short prompts fill it, the
+// diagonal cuts few of its key tiles, and keys are read once for a group.
+//   producer   (warp 8)  Q by 3-D TMA boxes [128 / G tokens, G heads, 64 elements]; keys and values in
+//              turn into a ring of tiles (SWIZZLE_128B)
+//   issuers    (warps 9, 10)  one to a row tile: S = Q K^T (tcgen05 M128 N128 K16), then
+//              O += P V with P from TMEM.  P takes the place of S, so the next S of a tile waits
+//              for its O; the other tile's products fill that gap
+//   softmax    (warps 0-3, 4-7)  one row to a thread: scores from TMEM, a running reference
+//              that moves only when a score passes it by 2^8 (O is scaled in TMEM then), weights in
+//              bf16 back to TMEM.  Sums are taken of the weights before they are rounded
+//   checker    (warp 11)  tiles of keys that some rows do not see: an infinity or NaN among the
+//              values would reach those rows as 0 * inf, so it is zeroed in shared memory and added
+//              by the epilogue to the rows that do see it
+// TMEM: S and P 2 x 128 columns, O 2 x D.
+#include <atomic>
+
+#include "grouped.cuh"
 
 #define FM_API extern "C" __attribute__((visibility("default")))
 
 namespace fm {
 namespace {
 
-struct RowSource {
-  const uint16_t *k, *v;
-  int64_t k_stride_t, v_stride_t;
-  const int32_t* cu_k;
-  int Tk, d;
-  FM_DEV int begin(int b) const { return cu_k ? offset_at(cu_k, b, Tk) : 0; }
-  FM_DEV int keys(int b) const { return max((cu_k ? offset_at(cu_k, b + 1, Tk) : Tk) - begin(b), 0); }
-  FM_DEV int64_t past(int b, int n) const { return (int64_t)keys(b) - n; }
-  FM_DEV int64_t clamp(int64_t j) const { return j; }
-  FM_DEV bool held(int, int64_t) const { return true; }
-  FM_DEV float value(int b, int64_t j, int head, int e, bool is_k) const {
-    const uint16_t* x = is_k ? k + (begin(b) + j) * k_stride_t : v + (begin(b) + j) * v_stride_t;
-    return __uint_as_float((uint32_t)x[head * d + e] << 16);
-  }
+constexpr int kRows = 128;       // of a tile
+constexpr int kKeys = 128;
+constexpr int kThreads = 12 * 32;
+constexpr int kChunkBytes = 128 * 128;  // 128 rows x 64 elements
+constexpr int kTmemCols = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLow = -1e30f;   // below every score
+constexpr float kSlack = 8.f;    // how far a score (in log2) may pass its reference
+constexpr int kMaxEdge = 16;     // tiles of an item that the mask cuts: at most 2 (256 + 127) / 128 + 2
+constexpr uint32_t kBIsMnMajor = 1u << 16;
+
+struct PromptParams {
+  const uint16_t* v;
+  const int32_t *cu_q, *cu_k;
+  const float* sink;
+  uint16_t* out;
+  float* lse;
+  int64_t v_stride_t, window;
+  int T, Tk, n_h, n_k, d, G, B, tokens, slots;  // tokens of a row tile
+  float scale;
+  unsigned int* status;
 };
+
+template <int D>
+struct Smem {
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  uint8_t q[2][D / 64][kChunkBytes];           // 1024-byte aligned
+  uint8_t kv[kStages][D / 64][kChunkBytes];
+  uint64_t q_full, full[kStages], ready[kStages], empty[kStages];  // ready: full and checked
+  uint64_t s_full[2], p_full[2], o_done[2], drain[2];
+  int bad_tile[kMaxEdge];                      // key tiles that held an infinity or NaN
+  int bad;
+  uint32_t tmem;
+  int abort;
+};
+
+FM_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// Descriptor of an MN-major SWIZZLE_128B operand: 64 elements of N to a 128-byte row, one row per K;
+// 8-row groups 1024 bytes apart (stride offset), the next 64 elements of N a chunk further (leading offset).
+FM_DEV uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(kChunkBytes >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+FM_DEV float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+FM_DEV float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+FM_DEV float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+FM_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// A row tile: its tokens in the sequence and the key tiles that they see.
+struct Tile {
+  int t0, tokens;     // first token, number (0: an empty tile)
+  int j0, j1;         // key tiles [j0, j1)
+};
+struct Item {
+  int q0, k0, nk;     // the sequence's first query and key rows, its keys
+  int head;
+  int shift;          // nk - nq: query i is at position i + shift
+  Tile tile[2];
+  int j0, j1;         // of both
+};
+
+FM_DEV int last_key(const Item& w, int token) { return token + w.shift; }
+FM_DEV int first_key(const PromptParams& p, const Item& w, int token) {
+  const int pos = token + w.shift;
+  return pos < p.window ? 0 : (int)(pos - p.window + 1);
+}
+// Whether the mask or the sequence's end cuts key tile j for a row of either tile.
+FM_DEV bool cut(const PromptParams& p, const Item& w, int j) {
+  bool some = false;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const Tile& t = w.tile[i];
+    if (j < t.j0 || j >= t.j1) continue;
+    some |= j * kKeys + kKeys - 1 > last_key(w, t.t0) || j * kKeys < first_key(p, w, t.t0 + t.tokens - 1);
+  }
+  return some;
+}
+
+// The item of this block; false where the slot is empty.
+FM_DEV bool find_item(const PromptParams& p, Item& w) {
+  const int slot = p.slots - 1 - (int)(blockIdx.x / p.n_k);  // later tokens, which see more keys, go first
+  w.head = blockIdx.x % p.n_k;
+  const int pair = 2 * p.tokens;
+  int b = 0, nq = p.T;
+  w.q0 = w.k0 = 0;
+  w.nk = p.Tk;
+  if (p.cu_q) {
+    b = warp_find(p.B, slot, [&](int i) { return (int64_t)(offset_at(p.cu_q, i, p.T) / pair) + i; });
+    w.q0 = offset_at(p.cu_q, b, p.T);
+    nq = offset_at(p.cu_q, b + 1, p.T) - w.q0;
+    w.k0 = offset_at(p.cu_k, b, p.Tk);
+    w.nk = max(offset_at(p.cu_k, b + 1, p.Tk) - w.k0, 0);
+  }
+  const int first = (slot - (p.cu_q ? w.q0 / pair + b : 0)) * pair;
+  if (first < 0 || first >= nq) return false;
+  w.shift = w.nk - nq;
+  w.j0 = 1 << 30;
+  w.j1 = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    Tile& t = w.tile[i];
+    t.t0 = first + i * p.tokens;
+    t.tokens = max(min(p.tokens, nq - t.t0), 0);
+    t.j0 = t.j1 = 0;
+    if (t.tokens == 0) continue;
+    const int last = last_key(w, t.t0 + t.tokens - 1);
+    const int low = max(first_key(p, w, max(t.t0, -w.shift)), 0);
+    if (last < low) continue;
+    t.j0 = low / kKeys;
+    t.j1 = last / kKeys + 1;
+    w.j0 = min(w.j0, t.j0);
+    w.j1 = max(w.j1, t.j1);
+  }
+  return true;
+}
+
+template <int D>
+FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uint32_t tmem, int which) {
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+  const Tile& tile = w.tile[which];
+  const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+  const uint32_t s_at = tmem + lanes + which * kKeys, o_at = tmem + lanes + 2 * kKeys + which * D;
+  const int r = 32 * quarter + lane;
+  const int t = r / p.G;
+  const bool live = t < tile.tokens;
+  const int token = tile.t0 + t;
+  const int last = live ? last_key(w, token) : -1, first = live ? first_key(p, w, token) : 0;
+  const float c = p.scale * kLog2e;
+  float m = kLow;          // the reference, in log2 units
+  float2 l = make_float2(0.f, 0.f);
+  bool ok = true;
+  for (int j = tile.j0; j < tile.j1; ++j) {
+    const int n = j - tile.j0;
+    if (ok) ok = mbar_wait(&sh.s_full[which], n & 1, &sh.abort, p.status);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    tc_fence_after();
+    uint32_t s[4][32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s[i]);
+    tmem_ld_wait();
+    const int lo = first - j * kKeys, hi = last - j * kKeys;  // the row's keys in the tile: lo .. hi
+    if (__any_sync(0xffffffffu, lo > 0 || hi < kKeys - 1)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (32 * i + e < lo || 32 * i + e > hi) s[i][e] = 0xFF800000u;  // -inf
+    }
+    float top[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+    for (int e = 1; e < 32; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], __uint_as_float(s[i][e]));
+    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+    if (__any_sync(0xffffffffu, most > m + kSlack)) {
+      const float next = fmaxf(m, most);
+      const float keep = exp2_fast(m - next);
+      m = next;
+      l.x *= keep;
+      l.y *= keep;
+      if (n > 0) {  // the products so far, in TMEM
+        if (!mbar_wait(&sh.o_done[which], (n - 1) & 1, &sh.abort, p.status)) ok = false;
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          tmem_ld32(o_at + 32 * i, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+          tmem_st32(o_at + 32 * i, o);
+        }
+      }
+    }
+    const float2 cc = make_float2(c, c), mm = make_float2(-m, -m);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t packed[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const uint32_t* x = s[2 * half + e / 16];
+        const int at = 2 * (e % 16);
+        float2 y = fma2(make_float2(__uint_as_float(x[at]), __uint_as_float(x[at + 1])), cc, mm);
+        y = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+        l = add2(l, y);
+        packed[e] = floats_bf16x2(y.x, y.y);
+      }
+      tmem_st32(s_at + 32 * half, packed);
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.p_full[which]);
+  }
+  // epilogue
+  const int n = tile.j1 - tile.j0;
+  if (n > 0 && ok) {
+    if (!mbar_wait(&sh.o_done[which], (n - 1) & 1, &sh.abort, p.status)) ok = false;
+    tc_fence_after();
+  }
+  if (!__all_sync(0xffffffffu, ok)) return;
+  const float sum = l.x + l.y;
+  const int h = w.head * p.G + r - t * p.G;
+  float z = sum;
+  if (live && p.sink) z += exp2_fast(p.sink[h] * kLog2e - m);
+  const bool some = n > 0 && sum != 0.f;  // the row sees a key
+  const float inv = some ? 1.f / z : 0.f;
+  const int64_t at = (int64_t)(w.q0 + token) * p.n_h + h;
+  const int bad = sh.bad;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    uint32_t o[32];
+    if (n > 0) {
+      tmem_ld32(o_at + 32 * i, o);
+      tmem_ld_wait();
+    }
+    if (live && some && bad) {  // infinities and NaN of tiles that the mask cuts
+      for (int x = 0; x < kMaxEdge; ++x) {
+        if (!(bad >> x & 1)) continue;
+        const int j = sh.bad_tile[x];
+        for (int key = max(first, j * kKeys); key <= min(last, j * kKeys + kKeys - 1); ++key)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            if (32 * i + e >= p.d) continue;
+            const uint32_t v = (uint32_t)p.v[(int64_t)(w.k0 + key) * p.v_stride_t + w.head * p.d + 32 * i + e] << 16;
+            if ((v & 0x7F800000u) == 0x7F800000u) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(v));
+          }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+      if (!live || 32 * i + e >= p.d) continue;
+      uint32_t y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        y[k] = some ? floats_bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv) : 0u;
+      *reinterpret_cast<uint4*>(p.out + at * p.d + 32 * i + e) = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+    __syncwarp();  // the next load from TMEM is the whole warp's
+  }
+  if (live && p.lse) p.lse[at] = some ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ CUtensorMap q_map,
+                                                                  const __grid_constant__ CUtensorMap k_map,
+                                                                  const __grid_constant__ CUtensorMap v_map,
+                                                                  const __grid_constant__ PromptParams p) {
+  using S = Smem<D>;
+  extern __shared__ __align__(1024) uint8_t raw_smem[];
+  S& sh = *reinterpret_cast<S*>(raw_smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&sh.q_full, 1);
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.ready[i], 1);
+      mbar_init(&sh.empty[i], 3);  // both issuers and the checker
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.o_done[i], 1);
+      mbar_init(&sh.drain[i], 1);
+    }
+    sh.bad = 0;
+    sh.abort = 0;
+    fence_mbar_init();
+    tma_prefetch(&q_map);
+    tma_prefetch(&k_map);
+    tma_prefetch(&v_map);
+  }
+  // programmatic dependent launch: what a kernel before wrote may be read from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Item w;
+  if (!find_item(p, w)) return;  // the whole block
+  if (warp == 8) {
+    tmem_alloc(&sh.tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    softmax_warps<D>(p, sh, w, tmem, warp >> 2);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8 && lane == 0) {
+      // ------------------------------------------------------------ producer
+      bool ok = true;
+      if (w.j1 > w.j0) {
+        const int tiles = w.tile[1].tokens > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(&sh.q_full, tiles * (D / 64) * p.tokens * p.G * 128);
+        for (int i = 0; i < tiles; ++i)
+          for (int x = 0; x < D / 64; ++x) tma_load_3d(sh.q[i][x], &q_map, &sh.q_full, 64 * x, w.head * p.G, w.q0 + w.tile[i].t0);
+      }
+      int n = 0;
+      for (int j = w.j0; ok && j < w.j1; ++j)
+        for (int v = 0; v < 2; ++v, ++n) {
+          const int stage = n % S::kStages, turn = n / S::kStages;
+          if (turn > 0 && !(ok = mbar_wait(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status))) break;
+          mbar_arrive_expect_tx(&sh.full[stage], (D / 64) * kChunkBytes);
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_3d(sh.kv[stage][x], v ? &v_map : &k_map, &sh.full[stage], 64 * x, w.head, w.k0 + j * kKeys);
+        }
+      // the issuers' last arrivals come before the block ends
+      for (int i = max(n - S::kStages, 0); ok && i < n; ++i)
+        ok = mbar_wait(&sh.empty[i % S::kStages], (i / S::kStages) & 1, &sh.abort, p.status);
+      if (!ok) {  // gave up: the copies in flight land before the block's memory is another's
+        mbar_wait_drain(&sh.q_full, 0);
+        for (int i = max(n - S::kStages, 0); i < n; ++i) mbar_wait_drain(&sh.full[i % S::kStages], (i / S::kStages) & 1);
+      }
+    } else if ((warp == 9 || warp == 10) && lane == 0) {
+      // ------------------------------------------------------------ issuers
+      const int which = warp - 9;
+      const Tile& tile = w.tile[which];
+      const uint32_t s_at = tmem + which * kKeys, o_at = tmem + 2 * kKeys + which * D;
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sh.q[which][0]));
+      const uint32_t s_idesc = idesc_bf16_f32(kRows, kKeys), o_idesc = idesc_bf16_f32(kRows, D) | kBIsMnMajor;
+      bool ok = w.j1 <= w.j0 || mbar_wait(&sh.q_full, 0, &sh.abort, p.status);
+      int n = 0;
+      for (int j = w.j0; ok && j < w.j1; ++j, n += 2) {
+        const int ks = n % S::kStages, vs = (n + 1) % S::kStages;
+        if (j < tile.j0 || j >= tile.j1) {  // the other row tile's alone
+          // each phase is waited for all the same: a wait tells only the last phase from the one before
+          if (!(ok = mbar_wait(&sh.full[ks], (n / S::kStages) & 1, &sh.abort, p.status))) break;
+          if (!(ok = mbar_wait(&sh.full[vs], ((n + 1) / S::kStages) & 1, &sh.abort, p.status))) break;
+          mbar_arrive(&sh.empty[ks]);
+          mbar_arrive(&sh.empty[vs]);
+          continue;
+        }
+        const int at = j - tile.j0;
+        if (!(ok = mbar_wait(&sh.full[ks], (n / S::kStages) & 1, &sh.abort, p.status))) break;
+        if (at > 0 && !(ok = mbar_wait(&sh.o_done[which], (at - 1) & 1, &sh.abort, p.status))) break;
+        tc_fence_after();
+        const uint64_t k_desc = sdesc_sw128(smem_u32(sh.kv[ks][0]));
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint64_t o = (uint64_t)((i / 4) * (kChunkBytes >> 4) + (i % 4) * 2);
+          umma_bf16_ss(s_at, q_desc + o, k_desc + o, s_idesc, i > 0);
+        }
+        umma_commit(&sh.empty[ks]);
+        umma_commit(&sh.s_full[which]);
+        if (!(ok = mbar_wait(&sh.full[vs], ((n + 1) / S::kStages) & 1, &sh.abort, p.status))) break;
+        if (cut(p, w, j) && !(ok = mbar_wait(&sh.ready[vs], ((n + 1) / S::kStages) & 1, &sh.abort, p.status))) break;
+        if (!(ok = mbar_wait(&sh.p_full[which], at & 1, &sh.abort, p.status))) break;
+        tc_fence_after();
+        const uint64_t v_desc = sdesc_mn_sw128(smem_u32(sh.kv[vs][0]));
+#pragma unroll
+        for (int i = 0; i < kKeys / 16; ++i)
+          umma_bf16_ts(o_at, s_at + 8 * i, v_desc + (uint64_t)(i * (2048 >> 4)), o_idesc, at > 0 || i > 0);
+        umma_commit(&sh.empty[vs]);
+        umma_commit(&sh.o_done[which]);
+      }
+      if (!ok) {  // gave up: the products in flight end before TMEM is freed
+        umma_commit(&sh.drain[which]);
+        mbar_wait_drain(&sh.drain[which], 0);
+      }
+    } else if (warp == 11) {
+      // ------------------------------------------------------------ checker
+      // Every stage of the ring passes through its hands, keys too, so that its barriers keep step
+      // with the ring's.
+      const int items = 2 * max(w.j1 - w.j0, 0);
+      int edges = 0;
+      for (int n = 0; n < items; ++n) {
+        const int vs = n % S::kStages, j = w.j0 + n / 2;
+        const bool ok = mbar_wait(&sh.full[vs], (n / S::kStages) & 1, &sh.abort, p.status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (n % 2 == 0 || !cut(p, w, j)) {
+          if (lane == 0) {
+            mbar_arrive(&sh.ready[vs]);
+            mbar_arrive(&sh.empty[vs]);
+          }
+          continue;
+        }
+        bool bad = false;
+        for (int x = 0; x < D / 64; ++x) {
+          uint4* cells = reinterpret_cast<uint4*>(sh.kv[vs][x]);
+#pragma unroll 4
+          for (int i = lane; i < kChunkBytes / 16; i += 32) {
+            const uint4 u = cells[i];
+            const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // a carry out of an all-ones exponent, of either half
+              bad |= (((a[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) != 0;
+          }
+        }
+        if (__any_sync(0xffffffffu, bad)) {
+          for (int x = 0; x < D / 64; ++x) {
+            uint16_t* cells = reinterpret_cast<uint16_t*>(sh.kv[vs][x]);
+            for (int i = lane; i < kChunkBytes / 2; i += 32)
+              if ((cells[i] & 0x7F80u) == 0x7F80u) cells[i] = 0;
+          }
+          if (lane == 0) {
+            sh.bad_tile[edges] = j;
+            sh.bad |= 1 << edges;
+          }
+          fence_async_smem();
+        }
+        __syncwarp();
+        ++edges;
+        if (lane == 0) {
+          mbar_arrive(&sh.ready[vs]);
+          mbar_arrive(&sh.empty[vs]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch(const PromptParams& p, const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                   cudaStream_t stream) {
+  constexpr int smem = (int)sizeof(Smem<D>);
+  static_assert(smem <= 227 * 1024, "shared memory of an SM");
+  static std::atomic<uint64_t> prepared{0};  // devices whose kernel has its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(prepared.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(prompt_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) prepared.fetch_or(uint64_t(1) << dev);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)((int64_t)p.slots * p.n_k));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_attn_kernel<D>, q_map, k_map, v_map, p);
+}
 
 }  // namespace
 }  // namespace fm
@@ -50,12 +536,45 @@ FM_API fm_status fm_prompt_attn(const fm_prompt_attn_args* a) {
   if (!a->out || !aligned(a->out, 16) || !aligned(a->lse_out, 4) || !aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) ||
       !aligned(a->sink_logit, 4))
     return set_error(FM_ERR_INVALID_ARG, "%s: out is NULL, or a pointer misaligned", who);
+  PromptParams p = {};
+  p.G = a->n_h / a->n_k;
+  p.tokens = kRows / p.G;
+  const int64_t slots = a->cu_q ? (int64_t)a->T / (2 * p.tokens) + a->B : (a->T + 2 * p.tokens - 1) / (2 * p.tokens);
+  if (slots * a->n_k >= int64_t(1) << 31)
+    return set_error(FM_ERR_INVALID_ARG, "%s: T=%d B=%d are too many for %d heads", who, a->T, a->B, a->n_h);
   fm_status st = check_device(nullptr);
   if (st != FM_OK) return st;
-  RowSource src = {a->k, a->v, a->k_stride_t, a->v_stride_t, a->cu_k ? a->cu_k : a->cu_q, a->Tk, a->d};
-  PlainParams p = {a->q, a->q_stride_t, a->cu_q, a->out, a->lse_out, a->sink_logit, a->window, a->scale, a->T, a->n_h, a->n_k, a->d, 1};
-  if (a->cu_q) p.B = a->B;
-  const cudaError_t e = launch_plain(p, src, reinterpret_cast<cudaStream_t>(a->stream));
+  if ((st = status_word(&p.status)) != FM_OK) return st;
+  const int D = a->d <= 64 ? 64 : 128;
+  CUtensorMap maps[3];
+  for (int i = 0; i < 3; ++i) {
+    const bool q = i == 0, none = !q && a->Tk == 0;  // without keys nothing is read: any address will do
+    const void* base = q || none ? a->q : i == 1 ? a->k : a->v;
+    const int64_t stride = q || none ? a->q_stride_t : i == 1 ? a->k_stride_t : a->v_stride_t;
+    const uint64_t dims[3] = {(uint64_t)a->d, (uint64_t)(q || none ? a->n_h : a->n_k), (uint64_t)(q || none ? a->T : a->Tk)};
+    const uint64_t strides[2] = {(uint64_t)a->d * 2, (uint64_t)stride * 2};
+    const uint32_t box[3] = {64, (uint32_t)(q ? p.G : 1), (uint32_t)(q ? p.tokens : kKeys)};
+    if ((st = make_tmap(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) != FM_OK)
+      return st;
+  }
+  p.v = a->v;
+  p.v_stride_t = a->v_stride_t;
+  p.cu_q = a->cu_q;
+  p.cu_k = a->cu_k ? a->cu_k : a->cu_q;
+  p.sink = a->sink_logit;
+  p.out = a->out;
+  p.lse = a->lse_out;
+  p.window = a->window;
+  p.T = a->T;
+  p.Tk = a->Tk;
+  p.n_h = a->n_h;
+  p.n_k = a->n_k;
+  p.d = a->d;
+  p.B = a->B;
+  p.slots = (int)slots;
+  p.scale = a->scale;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(a->stream);
+  const cudaError_t e = D == 64 ? launch<64>(p, maps[0], maps[1], maps[2], stream) : launch<128>(p, maps[0], maps[1], maps[2], stream);
   if (e != cudaSuccess) return set_error(FM_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
   return FM_OK;
 }
