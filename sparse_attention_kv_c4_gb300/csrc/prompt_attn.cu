@@ -8,16 +8,16 @@
 // diagonal cuts few of its key tiles, and keys are read once for a group.
 //   producer   (warp 8)  Q by 3-D TMA boxes [128 / G tokens, G heads, 64 elements]; keys and values in
 //              turn into a ring of tiles (SWIZZLE_128B)
-//   issuers    (warps 9, 10)  one to a row tile: S = Q K^T (tcgen05 M128 N128 K16), then
-//              O += P V with P from TMEM.  P takes the place of S, so the next S of a tile waits
-//              for its O; the other tile's products fill that gap
+//   issuer     (warp 9)  S = Q K^T (tcgen05 M128 N128 K16), then O += P V with P from TMEM, in two halves;
+//              one row tile's products run while the other's softmax does.  At D = 128 P takes
+//              the place of S, so the next S of a tile waits for its O
 //   softmax    (warps 0-3, 4-7)  one row to a thread: scores from TMEM, a running reference
-//              that moves only when a score passes it by 2^8 (O is scaled in TMEM then), weights in
+//              that moves only after a score has passed it by 2^8 (O is scaled in TMEM then), weights in
 //              bf16 back to TMEM.  Sums are taken of the weights before they are rounded
 //   checker    (warp 11)  tiles of keys that some rows do not see: an infinity or NaN among the
 //              values would reach those rows as 0 * inf, so it is zeroed in shared memory and added
 //              by the epilogue to the rows that do see it
-// TMEM: S and P 2 x 128 columns, O 2 x D.
+// TMEM: S 2 x 128 columns, O 2 x D, P 2 x 64 (at D = 128 in S's place).
 #include <atomic>
 
 #include "grouped.cuh"
@@ -34,7 +34,8 @@ constexpr int kChunkBytes = 128 * 128;  // 128 rows x 64 elements
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLow = -1e30f;   // below every score
-constexpr float kSlack = 8.f;    // how far a score (in log2) may pass its reference
+constexpr float kSlack = 8.f;    // how far a score (in log2) may pass its reference for long,
+constexpr float kFar = 64.f;     // and at all
 constexpr int kMaxEdge = 16;     // tiles of an item that the mask cuts: at most 2 (256 + 127) / 128 + 2
 constexpr uint32_t kBIsMnMajor = 1u << 16;
 
@@ -50,13 +51,19 @@ struct PromptParams {
   unsigned int* status;
 };
 
+// Columns of P: its own where TMEM has room, else those of S.
+template <int D>
+constexpr bool kOwnP = D == 64;
+template <int D>
+FM_DEV uint32_t p_column(int i) { return kOwnP<D> ? 2 * kKeys + 2 * D + i * (kKeys / 2) : i * kKeys; }
+
 template <int D>
 struct Smem {
   static constexpr int kStages = D == 128 ? 5 : 8;
   uint8_t q[2][D / 64][kChunkBytes];           // 1024-byte aligned
   uint8_t kv[kStages][D / 64][kChunkBytes];
   uint64_t q_full, full[kStages], ready[kStages], empty[kStages];  // ready: full and checked
-  uint64_t s_full[2], p_full[2], o_done[2], drain[2];
+  uint64_t s_full[2], s_read[2], p_full[2][2], o_done[2], drain;  // p_full: of the first 64 keys' weights, of the others'
   int bad_tile[kMaxEdge];                      // key tiles that held an infinity or NaN
   int bad;
   uint32_t tmem;
@@ -86,6 +93,11 @@ FM_DEV float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+FM_DEV float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 FM_DEV float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
   asm("{\n\t.reg .b64 x, y, z, w;\n\t"
@@ -104,12 +116,19 @@ FM_DEV float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+// One lane of a warp that runs as a whole.
+FM_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 x;\n\telect.sync x|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+  return r != 0;
+}
 FM_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // A row tile: its tokens in the sequence and the key tiles that they see.
 struct Tile {
   int t0, tokens;     // first token, number (0: an empty tile)
   int j0, j1;         // key tiles [j0, j1)
+  int whole0, whole1; // those of them that every row sees whole
 };
 struct Item {
   int q0, k0, nk;     // the sequence's first query and key rows, its keys
@@ -125,15 +144,9 @@ FM_DEV int first_key(const PromptParams& p, const Item& w, int token) {
   return pos < p.window ? 0 : (int)(pos - p.window + 1);
 }
 // Whether the mask or the sequence's end cuts key tile j for a row of either tile.
-FM_DEV bool cut(const PromptParams& p, const Item& w, int j) {
-  bool some = false;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const Tile& t = w.tile[i];
-    if (j < t.j0 || j >= t.j1) continue;
-    some |= j * kKeys + kKeys - 1 > last_key(w, t.t0) || j * kKeys < first_key(p, w, t.t0 + t.tokens - 1);
-  }
-  return some;
+FM_DEV bool cut(const Item& w, int j) {
+  auto one = [j](const Tile& t) { return j >= t.j0 && j < t.j1 && (j < t.whole0 || j >= t.whole1); };
+  return one(w.tile[0]) || one(w.tile[1]);
 }
 
 // The item of this block; false where the slot is empty.
@@ -161,13 +174,15 @@ FM_DEV bool find_item(const PromptParams& p, Item& w) {
     Tile& t = w.tile[i];
     t.t0 = first + i * p.tokens;
     t.tokens = max(min(p.tokens, nq - t.t0), 0);
-    t.j0 = t.j1 = 0;
+    t.j0 = t.j1 = t.whole0 = t.whole1 = 0;
     if (t.tokens == 0) continue;
     const int last = last_key(w, t.t0 + t.tokens - 1);
     const int low = max(first_key(p, w, max(t.t0, -w.shift)), 0);
     if (last < low) continue;
     t.j0 = low / kKeys;
     t.j1 = last / kKeys + 1;
+    t.whole0 = (first_key(p, w, t.t0 + t.tokens - 1) + kKeys - 1) / kKeys;
+    t.whole1 = (max(last_key(w, t.t0), -1) + 1) / kKeys;
     w.j0 = min(w.j0, t.j0);
     w.j1 = max(w.j1, t.j1);
   }
@@ -180,6 +195,7 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
   const Tile& tile = w.tile[which];
   const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
   const uint32_t s_at = tmem + lanes + which * kKeys, o_at = tmem + lanes + 2 * kKeys + which * D;
+  const uint32_t p_at = tmem + lanes + p_column<D>(which);
   const int r = 32 * quarter + lane;
   const int t = r / p.G;
   const bool live = t < tile.tokens;
@@ -187,6 +203,8 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
   const int last = live ? last_key(w, token) : -1, first = live ? first_key(p, w, token) : 0;
   const float c = p.scale * kLog2e;
   float m = kLow;          // the reference, in log2 units
+  float last_most = kLow;  // the last tile's largest
+  bool behind = false;     // some row's last tile passed its reference by more than kSlack
   float2 l = make_float2(0.f, 0.f);
   bool ok = true;
   for (int j = tile.j0; j < tile.j1; ++j) {
@@ -198,6 +216,11 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
 #pragma unroll
     for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s[i]);
     tmem_ld_wait();
+    if (kOwnP<D>) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.s_read[which]);
+    }
     const int lo = first - j * kKeys, hi = last - j * kKeys;  // the row's keys in the tile: lo .. hi
     if (__any_sync(0xffffffffu, lo > 0 || hi < kKeys - 1)) {
 #pragma unroll
@@ -208,14 +231,19 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
     }
     float top[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(s[i][0]);
+    for (int i = 0; i < 4; ++i) {
+      top[i] = __uint_as_float(s[i][0]);
 #pragma unroll
-    for (int e = 1; e < 32; ++e)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], __uint_as_float(s[i][e]));
-    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-    if (__any_sync(0xffffffffu, most > m + kSlack)) {
-      const float next = fmaxf(m, most);
+      for (int e = 1; e + 1 < 32; e += 2) top[i] = max3(top[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
+      top[i] = fmaxf(top[i], __uint_as_float(s[i][31]));
+    }
+    const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
+    // The reference moves before this tile's weights where they would leave fp32's range, and after
+    // them where they are merely large: floating point loses nothing by it, and O is not
+    // waited for.
+    const bool must = __any_sync(0xffffffffu, most > m + kFar);
+    if (must || behind) {
+      const float next = must ? fmaxf(m, most) : fmaxf(m, last_most);
       const float keep = exp2_fast(m - next);
       m = next;
       l.x *= keep;
@@ -235,7 +263,10 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
         }
       }
     }
+    behind = __any_sync(0xffffffffu, most > m + kSlack);
+    last_most = most;
     const float2 cc = make_float2(c, c), mm = make_float2(-m, -m);
+    float2 sums[4] = {l, make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint32_t packed[32];
@@ -245,15 +276,21 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
         const int at = 2 * (e % 16);
         float2 y = fma2(make_float2(__uint_as_float(x[at]), __uint_as_float(x[at + 1])), cc, mm);
         y = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-        l = add2(l, y);
+        sums[e % 4] = add2(sums[e % 4], y);
         packed[e] = floats_bf16x2(y.x, y.y);
       }
-      tmem_st32(s_at + 32 * half, packed);
+      if (kOwnP<D> && half == 0 && n > 0) {  // the product that reads the last weights is over
+        if (!mbar_wait(&sh.o_done[which], (n - 1) & 1, &sh.abort, p.status)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+      }
+      tmem_st32(p_at + 32 * half, packed);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_full[which][half]);
     }
-    tmem_st_wait();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.p_full[which]);
+    l = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
   }
   // epilogue
   const int n = tile.j1 - tile.j0;
@@ -304,6 +341,114 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
   if (live && p.lse) p.lse[at] = some ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
+// One thread issues both row tiles' products in a fixed order, one tile's while the other's softmax
+// runs.  (An issuer for each tile: their products mix and end together, the tiles fall into step and
+// the tensor cores idle through both softmaxes.)
+// A place in the ring.
+template <int Stages>
+struct Place {
+  int stage = 0;
+  uint32_t turn = 0;  // parity of the round
+  FM_DEV void next(int by) {
+    stage += by;
+    if (stage >= Stages) {
+      stage -= Stages;
+      turn ^= 1;
+    }
+  }
+};
+
+// A value that is the same in all lanes, in a form that the compiler knows to be: an MMA whose operands
+// are not takes its issuer several times as long.
+FM_DEV uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
+template <int D>
+FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, const Item& w) {
+  constexpr int kStages = Smem<D>::kStages;
+  constexpr uint32_t s_idesc = idesc_bf16_f32(kRows, kKeys), o_idesc = idesc_bf16_f32(kRows, D) | kBIsMnMajor;
+  constexpr uint32_t kTileStep = (D / 64) * (kChunkBytes >> 4);
+  const bool one = elect_one();
+  const uint32_t tmem = uniform(sh.tmem);
+  const int tiles = (int)uniform((uint32_t)max(w.j1 - w.j0, 0));
+  const int first[2] = {(int)uniform(max(w.tile[0].j0 - w.j0, 0)), (int)uniform(max(w.tile[1].j0 - w.j0, 0))};
+  const int end[2] = {(int)uniform(max(w.tile[0].j1 - w.j0, 0)), (int)uniform(max(w.tile[1].j1 - w.j0, 0))};
+  const uint64_t q_desc = sdesc_sw128(smem_u32(sh.q[0][0])), k_desc = sdesc_sw128(smem_u32(sh.kv[0][0])),
+                 v_desc = sdesc_mn_sw128(smem_u32(sh.kv[0][0]));
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, &sh.abort, p.status));
+  };
+  if (tiles == 0) return;
+  // S of key tile j, whose keys are in stage `at`, for row tile i.  The stage's phase is waited for even where
+  // the row tile does not see the keys: a wait tells only the last phase from the one before.
+  auto scores = [&](int i, int j, const Place<kStages>& at) {
+    if (!wait(&sh.full[at.stage], at.turn)) return false;
+    const int done = j - first[i];
+    if (done < 0 || j >= end[i]) {
+      if (one) mbar_arrive(&sh.empty[at.stage]);
+      return true;
+    }
+    // S is free: its last scores are read, or, where P lies in its place, the product that reads P is over
+    if (done > 0 && !wait(kOwnP<D> ? &sh.s_read[i] : &sh.o_done[i], (done - 1) & 1)) return false;
+    tc_fence_after();
+    const uint64_t a = q_desc + i * kTileStep, b = k_desc + at.stage * kTileStep;
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x) {
+      const uint64_t o = (uint64_t)((x / 4) * (kChunkBytes >> 4) + (x % 4) * 2);
+      if (one) umma_bf16_ss(tmem + i * kKeys, a + o, b + o, s_idesc, x > 0);
+    }
+    if (one) {
+      umma_commit(&sh.empty[at.stage]);
+      umma_commit(&sh.s_full[i]);
+    }
+    return true;
+  };
+  // O += P V, half of the keys as soon as their weights are there.
+  auto values = [&](int i, int j, const Place<kStages>& at) {
+    if (!wait(&sh.full[at.stage], at.turn)) return false;
+    const int done = j - first[i];
+    if (done < 0 || j >= end[i]) {
+      if (one) mbar_arrive(&sh.empty[at.stage]);
+      return true;
+    }
+    if (cut(w, w.j0 + j) && !wait(&sh.ready[at.stage], at.turn)) return false;
+    const uint64_t b = v_desc + at.stage * kTileStep;
+    const uint32_t o_at = tmem + 2 * kKeys + i * D, p_at = tmem + p_column<D>(i);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (!wait(&sh.p_full[i][half], done & 1)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int x = 0; x < kKeys / 32; ++x) {
+        const int k = half * (kKeys / 32) + x;
+        if (one) umma_bf16_ts(o_at, p_at + 8 * k, b + (uint64_t)(k * (2048 >> 4)), o_idesc, done > 0 || k > 0);
+      }
+    }
+    if (one) {
+      umma_commit(&sh.empty[at.stage]);
+      umma_commit(&sh.o_done[i]);
+    }
+    return true;
+  };
+  Place<kStages> k_at, v_at;  // of the keys after, and of the values of, tile j
+  v_at.next(1);
+  bool ok = wait(&sh.q_full, 0);
+#pragma unroll 1
+  for (int j = -1; ok && j < tiles; ++j) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (kOwnP<D> && ok && j + 1 < tiles) ok = scores(i, j + 1, k_at);
+      if (ok && j >= 0) ok = values(i, j, v_at);
+      if (!kOwnP<D> && ok && j + 1 < tiles) ok = scores(i, j + 1, k_at);
+    }
+    k_at.next(2);
+    if (j >= 0) v_at.next(2);
+  }
+  if (!ok && one) {  // gave up: the products in flight end before TMEM is freed
+    umma_commit(&sh.drain);
+    mbar_wait_drain(&sh.drain, 0);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                                                                   const __grid_constant__ CUtensorMap k_map,
@@ -318,14 +463,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.ready[i], 1);
-      mbar_init(&sh.empty[i], 3);  // both issuers and the checker
+      mbar_init(&sh.empty[i], 3);  // both row tiles and the checker
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_full[i][0], 4);
+      mbar_init(&sh.p_full[i][1], 4);
+      mbar_init(&sh.s_read[i], 4);
       mbar_init(&sh.o_done[i], 1);
-      mbar_init(&sh.drain[i], 1);
     }
+    mbar_init(&sh.drain, 1);
     sh.bad = 0;
     sh.abort = 0;
     fence_mbar_init();
@@ -377,52 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         mbar_wait_drain(&sh.q_full, 0);
         for (int i = max(n - S::kStages, 0); i < n; ++i) mbar_wait_drain(&sh.full[i % S::kStages], (i / S::kStages) & 1);
       }
-    } else if ((warp == 9 || warp == 10) && lane == 0) {
-      // ------------------------------------------------------------ issuers
-      const int which = warp - 9;
-      const Tile& tile = w.tile[which];
-      const uint32_t s_at = tmem + which * kKeys, o_at = tmem + 2 * kKeys + which * D;
-      const uint64_t q_desc = sdesc_sw128(smem_u32(sh.q[which][0]));
-      const uint32_t s_idesc = idesc_bf16_f32(kRows, kKeys), o_idesc = idesc_bf16_f32(kRows, D) | kBIsMnMajor;
-      bool ok = w.j1 <= w.j0 || mbar_wait(&sh.q_full, 0, &sh.abort, p.status);
-      int n = 0;
-      for (int j = w.j0; ok && j < w.j1; ++j, n += 2) {
-        const int ks = n % S::kStages, vs = (n + 1) % S::kStages;
-        if (j < tile.j0 || j >= tile.j1) {  // the other row tile's alone
-          // each phase is waited for all the same: a wait tells only the last phase from the one before
-          if (!(ok = mbar_wait(&sh.full[ks], (n / S::kStages) & 1, &sh.abort, p.status))) break;
-          if (!(ok = mbar_wait(&sh.full[vs], ((n + 1) / S::kStages) & 1, &sh.abort, p.status))) break;
-          mbar_arrive(&sh.empty[ks]);
-          mbar_arrive(&sh.empty[vs]);
-          continue;
-        }
-        const int at = j - tile.j0;
-        if (!(ok = mbar_wait(&sh.full[ks], (n / S::kStages) & 1, &sh.abort, p.status))) break;
-        if (at > 0 && !(ok = mbar_wait(&sh.o_done[which], (at - 1) & 1, &sh.abort, p.status))) break;
-        tc_fence_after();
-        const uint64_t k_desc = sdesc_sw128(smem_u32(sh.kv[ks][0]));
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint64_t o = (uint64_t)((i / 4) * (kChunkBytes >> 4) + (i % 4) * 2);
-          umma_bf16_ss(s_at, q_desc + o, k_desc + o, s_idesc, i > 0);
-        }
-        umma_commit(&sh.empty[ks]);
-        umma_commit(&sh.s_full[which]);
-        if (!(ok = mbar_wait(&sh.full[vs], ((n + 1) / S::kStages) & 1, &sh.abort, p.status))) break;
-        if (cut(p, w, j) && !(ok = mbar_wait(&sh.ready[vs], ((n + 1) / S::kStages) & 1, &sh.abort, p.status))) break;
-        if (!(ok = mbar_wait(&sh.p_full[which], at & 1, &sh.abort, p.status))) break;
-        tc_fence_after();
-        const uint64_t v_desc = sdesc_mn_sw128(smem_u32(sh.kv[vs][0]));
-#pragma unroll
-        for (int i = 0; i < kKeys / 16; ++i)
-          umma_bf16_ts(o_at, s_at + 8 * i, v_desc + (uint64_t)(i * (2048 >> 4)), o_idesc, at > 0 || i > 0);
-        umma_commit(&sh.empty[vs]);
-        umma_commit(&sh.o_done[which]);
-      }
-      if (!ok) {  // gave up: the products in flight end before TMEM is freed
-        umma_commit(&sh.drain[which]);
-        mbar_wait_drain(&sh.drain[which], 0);
-      }
+    } else if (warp == 9) {
+      issue_products<D>(p, sh, w);
     } else if (warp == 11) {
       // ------------------------------------------------------------ checker
       // Every stage of the ring passes through its hands, keys too, so that its barriers keep step
@@ -433,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         const int vs = n % S::kStages, j = w.j0 + n / 2;
         const bool ok = mbar_wait(&sh.full[vs], (n / S::kStages) & 1, &sh.abort, p.status);
         if (!__all_sync(0xffffffffu, ok)) break;
-        if (n % 2 == 0 || !cut(p, w, j)) {
+        if (n % 2 == 0 || !cut(w, j)) {
           if (lane == 0) {
             mbar_arrive(&sh.ready[vs]);
             mbar_arrive(&sh.empty[vs]);
