@@ -22,6 +22,22 @@ FM_DEV uint32_t floats_bf16x2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// mbar_wait in few instructions: these kernels wait in many places, and what leaves the instruction cache
+// costs every role (the tensor-core kernel with mbar_wait's unrolled polls was 120 KB of code).
+FM_DEV bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+#pragma unroll 1
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if ((n & 31) != 0) continue;
+    const bool late = globaltimer() - t0 > FM_WAIT_LIMIT_NS;
+    if (late && *abort == 0) atomicOr(status, FM_DEV_TIMEOUT);
+    if (late) *abort = 1;
+    if (*abort != 0) return false;
+  }
+  return true;
+}
+
 // Offset i of packed sequences, kept within the call's rows whatever it holds.
 FM_DEV int offset_at(const int32_t* cu, int i, int rows) { return min(max(cu[i], 0), rows); }
 

@@ -8,9 +8,9 @@
 // diagonal cuts few of its key tiles, and keys are read once for a group.
 //   producer   (warp 8)  Q by 3-D TMA boxes [128 / G tokens, G heads, 64 elements]; keys and values in
 //              turn into a ring of tiles (SWIZZLE_128B)
-//   issuer     (warp 9)  S = Q K^T (tcgen05 M128 N128 K16), then O += P V with P from TMEM, in two halves;
-//              one row tile's products run while the other's softmax does.  At D = 128 P takes
-//              the place of S, so the next S of a tile waits for its O
+//   issuers    (warps 9, 10)  one to a row tile: S = Q K^T (tcgen05 M128 N128 K16), then O += P V with P
+//              from TMEM, in two halves; one row tile's products run while the other's softmax
+//              does.  At D = 128 P takes the place of S, so the next S of a tile waits for its O
 //   softmax    (warps 0-3, 4-7)  one row to a thread: scores from TMEM, a running reference
 //              that moves only after a score has passed it by 2^8 (O is scaled in TMEM then), weights in
 //              bf16 back to TMEM.  Sums are taken of the weights before they are rounded
@@ -63,7 +63,7 @@ struct Smem {
   uint8_t q[2][D / 64][kChunkBytes];           // 1024-byte aligned
   uint8_t kv[kStages][D / 64][kChunkBytes];
   uint64_t q_full, full[kStages], ready[kStages], empty[kStages];  // ready: full and checked
-  uint64_t s_full[2], s_read[2], p_full[2][2], o_done[2], drain;  // p_full: of the first 64 keys' weights, of the others'
+  uint64_t s_full[2], s_read[2], p_full[2][2], o_done[2], turn[2], drain[2];  // p_full: of the first 64 keys' weights, of the others'
   int bad_tile[kMaxEdge];                      // key tiles that held an infinity or NaN
   int bad;
   uint32_t tmem;
@@ -209,7 +209,7 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
   bool ok = true;
   for (int j = tile.j0; j < tile.j1; ++j) {
     const int n = j - tile.j0;
-    if (ok) ok = mbar_wait(&sh.s_full[which], n & 1, &sh.abort, p.status);
+    if (ok) ok = wait_bar(&sh.s_full[which], n & 1, &sh.abort, p.status);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after();
     uint32_t s[4][32];
@@ -249,10 +249,10 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
       l.x *= keep;
       l.y *= keep;
       if (n > 0) {  // the products so far, in TMEM
-        if (!mbar_wait(&sh.o_done[which], (n - 1) & 1, &sh.abort, p.status)) ok = false;
+        if (!wait_bar(&sh.o_done[which], (n - 1) & 1, &sh.abort, p.status)) ok = false;
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
           uint32_t o[32];
           tmem_ld32(o_at + 32 * i, o);
@@ -280,7 +280,7 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
         packed[e] = floats_bf16x2(y.x, y.y);
       }
       if (kOwnP<D> && half == 0 && n > 0) {  // the product that reads the last weights is over
-        if (!mbar_wait(&sh.o_done[which], (n - 1) & 1, &sh.abort, p.status)) ok = false;
+        if (!wait_bar(&sh.o_done[which], (n - 1) & 1, &sh.abort, p.status)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
       }
@@ -295,7 +295,7 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
   // epilogue
   const int n = tile.j1 - tile.j0;
   if (n > 0 && ok) {
-    if (!mbar_wait(&sh.o_done[which], (n - 1) & 1, &sh.abort, p.status)) ok = false;
+    if (!wait_bar(&sh.o_done[which], (n - 1) & 1, &sh.abort, p.status)) ok = false;
     tc_fence_after();
   }
   if (!__all_sync(0xffffffffu, ok)) return;
@@ -306,26 +306,13 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
   const bool some = n > 0 && sum != 0.f;  // the row sees a key
   const float inv = some ? 1.f / z : 0.f;
   const int64_t at = (int64_t)(w.q0 + token) * p.n_h + h;
-  const int bad = sh.bad;
-#pragma unroll
+  uint16_t* out = p.out + at * p.d;
+#pragma unroll 1
   for (int i = 0; i < D / 32; ++i) {
     uint32_t o[32];
     if (n > 0) {
       tmem_ld32(o_at + 32 * i, o);
       tmem_ld_wait();
-    }
-    if (live && some && bad) {  // infinities and NaN of tiles that the mask cuts
-      for (int x = 0; x < kMaxEdge; ++x) {
-        if (!(bad >> x & 1)) continue;
-        const int j = sh.bad_tile[x];
-        for (int key = max(first, j * kKeys); key <= min(last, j * kKeys + kKeys - 1); ++key)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (32 * i + e >= p.d) continue;
-            const uint32_t v = (uint32_t)p.v[(int64_t)(w.k0 + key) * p.v_stride_t + w.head * p.d + 32 * i + e] << 16;
-            if ((v & 0x7F800000u) == 0x7F800000u) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(v));
-          }
-      }
     }
 #pragma unroll
     for (int e = 0; e < 32; e += 8) {
@@ -334,16 +321,31 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         y[k] = some ? floats_bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv) : 0u;
-      *reinterpret_cast<uint4*>(p.out + at * p.d + 32 * i + e) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(out + 32 * i + e) = make_uint4(y[0], y[1], y[2], y[3]);
     }
     __syncwarp();  // the next load from TMEM is the whole warp's
+  }
+  const int bad = sh.bad;
+  if (live && some && bad) {  // infinities and NaN of tiles that the mask cuts, in the keys that the row sees
+#pragma unroll 1
+    for (int x = 0; x < kMaxEdge; ++x) {
+      if (!(bad >> x & 1)) continue;
+      const int j = sh.bad_tile[x];
+#pragma unroll 1
+      for (int key = max(first, j * kKeys); key <= min(last, j * kKeys + kKeys - 1); ++key) {
+        const uint16_t* v = p.v + (int64_t)(w.k0 + key) * p.v_stride_t + w.head * p.d;
+#pragma unroll 1
+        for (int e = 0; e < p.d; ++e) {
+          if ((v[e] & 0x7F80u) != 0x7F80u) continue;
+          const float sum_e = __uint_as_float((uint32_t)out[e] << 16) + __uint_as_float((uint32_t)v[e] << 16);
+          out[e] = (uint16_t)(floats_bf16x2(sum_e, 0.f) & 0xFFFFu);
+        }
+      }
+    }
   }
   if (live && p.lse) p.lse[at] = some ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-// One thread issues both row tiles' products in a fixed order, one tile's while the other's softmax
-// runs.  (An issuer for each tile: their products mix and end together, the tiles fall into step and
-// the tensor cores idle through both softmaxes.)
 // A place in the ring.
 template <int Stages>
 struct Place {
@@ -362,60 +364,65 @@ struct Place {
 // are not takes its issuer several times as long.
 FM_DEV uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
 
-template <int D>
+// One warp issues a row tile's products.  Where a tile's S waits for its O, the two warps take turns, a tile's
+// O and next S at a time: left to themselves the tiles fall into step, their products mix and end
+// together, and the tensor cores idle through both softmaxes.  (One warp for both tiles: the hundred
+// instructions between two products are then nobody else's time, 2 x 800 cycles of a step of 4000.)
+template <int D, int I>
 FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, const Item& w) {
   constexpr int kStages = Smem<D>::kStages;
   constexpr uint32_t s_idesc = idesc_bf16_f32(kRows, kKeys), o_idesc = idesc_bf16_f32(kRows, D) | kBIsMnMajor;
   constexpr uint32_t kTileStep = (D / 64) * (kChunkBytes >> 4);
   const bool one = elect_one();
-  const uint32_t tmem = uniform(sh.tmem);
+  const uint32_t tmem = uniform(sh.tmem), s_at = tmem + I * kKeys, o_at = tmem + 2 * kKeys + I * D, p_at = tmem + p_column<D>(I);
   const int tiles = (int)uniform((uint32_t)max(w.j1 - w.j0, 0));
-  const int first[2] = {(int)uniform(max(w.tile[0].j0 - w.j0, 0)), (int)uniform(max(w.tile[1].j0 - w.j0, 0))};
-  const int end[2] = {(int)uniform(max(w.tile[0].j1 - w.j0, 0)), (int)uniform(max(w.tile[1].j1 - w.j0, 0))};
-  const uint64_t q_desc = sdesc_sw128(smem_u32(sh.q[0][0])), k_desc = sdesc_sw128(smem_u32(sh.kv[0][0])),
+  const int first = (int)uniform(max(w.tile[I].j0 - w.j0, 0)), end = (int)uniform(max(w.tile[I].j1 - w.j0, 0));
+  const uint64_t q_desc = sdesc_sw128(smem_u32(sh.q[I][0])), k_desc = sdesc_sw128(smem_u32(sh.kv[0][0])),
                  v_desc = sdesc_mn_sw128(smem_u32(sh.kv[0][0]));
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, &sh.abort, p.status));
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, &sh.abort, p.status));
   };
   if (tiles == 0) return;
-  // S of key tile j, whose keys are in stage `at`, for row tile i.  The stage's phase is waited for even where
-  // the row tile does not see the keys: a wait tells only the last phase from the one before.
-  auto scores = [&](int i, int j, const Place<kStages>& at) {
+  // S of key tile j, whose keys are in stage `at`.  The stage's phase is waited for even where the row tile
+  // does not see the keys: a wait tells only the last phase from the one before.
+  auto scores = [&](int j, const Place<kStages>& at) {
     if (!wait(&sh.full[at.stage], at.turn)) return false;
-    const int done = j - first[i];
-    if (done < 0 || j >= end[i]) {
+    const int done = j - first;
+    if (done < 0 || j >= end) {
       if (one) mbar_arrive(&sh.empty[at.stage]);
       return true;
     }
+    const uint64_t b = k_desc + at.stage * kTileStep;
     // S is free: its last scores are read, or, where P lies in its place, the product that reads P is over
-    if (done > 0 && !wait(kOwnP<D> ? &sh.s_read[i] : &sh.o_done[i], (done - 1) & 1)) return false;
+    if (done > 0 && !wait(kOwnP<D> ? &sh.s_read[I] : &sh.o_done[I], (done - 1) & 1)) return false;
     tc_fence_after();
-    const uint64_t a = q_desc + i * kTileStep, b = k_desc + at.stage * kTileStep;
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
       const uint64_t o = (uint64_t)((x / 4) * (kChunkBytes >> 4) + (x % 4) * 2);
-      if (one) umma_bf16_ss(tmem + i * kKeys, a + o, b + o, s_idesc, x > 0);
+      if (one) umma_bf16_ss(s_at, q_desc + o, b + o, s_idesc, x > 0);
     }
     if (one) {
       umma_commit(&sh.empty[at.stage]);
-      umma_commit(&sh.s_full[i]);
+      umma_commit(&sh.s_full[I]);
     }
     return true;
   };
   // O += P V, half of the keys as soon as their weights are there.
-  auto values = [&](int i, int j, const Place<kStages>& at) {
+  auto values = [&](int j, const Place<kStages>& at) {
     if (!wait(&sh.full[at.stage], at.turn)) return false;
-    const int done = j - first[i];
-    if (done < 0 || j >= end[i]) {
+    const int done = j - first;
+    const bool sees = done >= 0 && j < end;
+    if (sees && cut(w, w.j0 + j) && !wait(&sh.ready[at.stage], at.turn)) return false;
+    if (sees && !wait(&sh.p_full[I][0], done & 1)) return false;
+    if (!kOwnP<D> && !wait(&sh.turn[I], j & 1)) return false;
+    if (!sees) {
       if (one) mbar_arrive(&sh.empty[at.stage]);
       return true;
     }
-    if (cut(w, w.j0 + j) && !wait(&sh.ready[at.stage], at.turn)) return false;
     const uint64_t b = v_desc + at.stage * kTileStep;
-    const uint32_t o_at = tmem + 2 * kKeys + i * D, p_at = tmem + p_column<D>(i);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      if (!wait(&sh.p_full[i][half], done & 1)) return false;
+      if (half == 1 && !wait(&sh.p_full[I][1], done & 1)) return false;
       tc_fence_after();
 #pragma unroll
       for (int x = 0; x < kKeys / 32; ++x) {
@@ -425,7 +432,7 @@ FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, const Item& w) {
     }
     if (one) {
       umma_commit(&sh.empty[at.stage]);
-      umma_commit(&sh.o_done[i]);
+      umma_commit(&sh.o_done[I]);
     }
     return true;
   };
@@ -434,18 +441,18 @@ FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, const Item& w) {
   bool ok = wait(&sh.q_full, 0);
 #pragma unroll 1
   for (int j = -1; ok && j < tiles; ++j) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (kOwnP<D> && ok && j + 1 < tiles) ok = scores(i, j + 1, k_at);
-      if (ok && j >= 0) ok = values(i, j, v_at);
-      if (!kOwnP<D> && ok && j + 1 < tiles) ok = scores(i, j + 1, k_at);
+    if (kOwnP<D> && j + 1 < tiles) ok = scores(j + 1, k_at);
+    if (ok && j >= 0) ok = values(j, v_at);
+    if (!kOwnP<D>) {
+      if (ok && j + 1 < tiles) ok = scores(j + 1, k_at);
+      if (one && (I == 0 || j + 1 < tiles) && j + I >= 0) mbar_arrive(&sh.turn[1 - I]);
     }
     k_at.next(2);
     if (j >= 0) v_at.next(2);
   }
   if (!ok && one) {  // gave up: the products in flight end before TMEM is freed
-    umma_commit(&sh.drain);
-    mbar_wait_drain(&sh.drain, 0);
+    umma_commit(&sh.drain[I]);
+    mbar_wait_drain(&sh.drain[I], 0);
   }
 }
 
@@ -471,8 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       mbar_init(&sh.p_full[i][1], 4);
       mbar_init(&sh.s_read[i], 4);
       mbar_init(&sh.o_done[i], 1);
+      mbar_init(&sh.turn[i], 1);
+      mbar_init(&sh.drain[i], 1);
     }
-    mbar_init(&sh.drain, 1);
     sh.bad = 0;
     sh.abort = 0;
     fence_mbar_init();
@@ -512,20 +520,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       for (int j = w.j0; ok && j < w.j1; ++j)
         for (int v = 0; v < 2; ++v, ++n) {
           const int stage = n % S::kStages, turn = n / S::kStages;
-          if (turn > 0 && !(ok = mbar_wait(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status))) break;
+          if (turn > 0 && !(ok = wait_bar(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status))) break;
           mbar_arrive_expect_tx(&sh.full[stage], (D / 64) * kChunkBytes);
           for (int x = 0; x < D / 64; ++x)
             tma_load_3d(sh.kv[stage][x], v ? &v_map : &k_map, &sh.full[stage], 64 * x, w.head, w.k0 + j * kKeys);
         }
       // the issuers' last arrivals come before the block ends
       for (int i = max(n - S::kStages, 0); ok && i < n; ++i)
-        ok = mbar_wait(&sh.empty[i % S::kStages], (i / S::kStages) & 1, &sh.abort, p.status);
+        ok = wait_bar(&sh.empty[i % S::kStages], (i / S::kStages) & 1, &sh.abort, p.status);
       if (!ok) {  // gave up: the copies in flight land before the block's memory is another's
         mbar_wait_drain(&sh.q_full, 0);
         for (int i = max(n - S::kStages, 0); i < n; ++i) mbar_wait_drain(&sh.full[i % S::kStages], (i / S::kStages) & 1);
       }
     } else if (warp == 9) {
-      issue_products<D>(p, sh, w);
+      issue_products<D, 0>(p, sh, w);
+    } else if (warp == 10) {
+      issue_products<D, 1>(p, sh, w);
     } else if (warp == 11) {
       // ------------------------------------------------------------ checker
       // Every stage of the ring passes through its hands, keys too, so that its barriers keep step
@@ -534,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       int edges = 0;
       for (int n = 0; n < items; ++n) {
         const int vs = n % S::kStages, j = w.j0 + n / 2;
-        const bool ok = mbar_wait(&sh.full[vs], (n / S::kStages) & 1, &sh.abort, p.status);
+        const bool ok = wait_bar(&sh.full[vs], (n / S::kStages) & 1, &sh.abort, p.status);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (n % 2 == 0 || !cut(w, j)) {
           if (lane == 0) {
