@@ -38,6 +38,14 @@ FM_DEV bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, unsign
   return true;
 }
 
+// The same with its loop out of line, for roles that have registers to spare at a call.
+static __device__ __noinline__ bool wait_poll(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
+  return wait_bar(bar, parity, abort, status);
+}
+FM_DEV bool wait_call(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
+  return mbar_try_wait(bar, parity) || wait_poll(bar, parity, abort, status);
+}
+
 // Offset i of packed sequences, kept within the call's rows whatever it holds.
 FM_DEV int offset_at(const int32_t* cu, int i, int rows) { return min(max(cu[i], 0), rows); }
 

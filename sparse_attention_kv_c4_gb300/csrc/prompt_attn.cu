@@ -368,19 +368,20 @@ FM_DEV uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); 
 // O and next S at a time: left to themselves the tiles fall into step, their products mix and end
 // together, and the tensor cores idle through both softmaxes.  (One warp for both tiles: the hundred
 // instructions between two products are then nobody else's time, 2 x 800 cycles of a step of 4000.)
-template <int D, int I>
-FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, const Item& w) {
+template <int D>
+FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, const Item& w, uint32_t I) {
   constexpr int kStages = Smem<D>::kStages;
   constexpr uint32_t s_idesc = idesc_bf16_f32(kRows, kKeys), o_idesc = idesc_bf16_f32(kRows, D) | kBIsMnMajor;
   constexpr uint32_t kTileStep = (D / 64) * (kChunkBytes >> 4);
   const bool one = elect_one();
+  const Tile& tile = w.tile[I];
   const uint32_t tmem = uniform(sh.tmem), s_at = tmem + I * kKeys, o_at = tmem + 2 * kKeys + I * D, p_at = tmem + p_column<D>(I);
   const int tiles = (int)uniform((uint32_t)max(w.j1 - w.j0, 0));
-  const int first = (int)uniform(max(w.tile[I].j0 - w.j0, 0)), end = (int)uniform(max(w.tile[I].j1 - w.j0, 0));
+  const int first = (int)uniform(max(tile.j0 - w.j0, 0)), end = (int)uniform(max(tile.j1 - w.j0, 0));
   const uint64_t q_desc = sdesc_sw128(smem_u32(sh.q[I][0])), k_desc = sdesc_sw128(smem_u32(sh.kv[0][0])),
                  v_desc = sdesc_mn_sw128(smem_u32(sh.kv[0][0]));
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_bar(bar, parity, &sh.abort, p.status));
+    return __all_sync(0xffffffffu, wait_call(bar, parity, &sh.abort, p.status));
   };
   if (tiles == 0) return;
   // S of key tile j, whose keys are in stage `at`.  The stage's phase is waited for even where the row tile
@@ -445,7 +446,7 @@ FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, const Item& w) {
     if (ok && j >= 0) ok = values(j, v_at);
     if (!kOwnP<D>) {
       if (ok && j + 1 < tiles) ok = scores(j + 1, k_at);
-      if (one && (I == 0 || j + 1 < tiles) && j + I >= 0) mbar_arrive(&sh.turn[1 - I]);
+      if (one && (I == 0 || j + 1 < tiles) && j + (int)I >= 0) mbar_arrive(&sh.turn[1 - I]);
     }
     k_at.next(2);
     if (j >= 0) v_at.next(2);
@@ -520,22 +521,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       for (int j = w.j0; ok && j < w.j1; ++j)
         for (int v = 0; v < 2; ++v, ++n) {
           const int stage = n % S::kStages, turn = n / S::kStages;
-          if (turn > 0 && !(ok = wait_bar(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status))) break;
+          if (turn > 0 && !(ok = wait_call(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status))) break;
           mbar_arrive_expect_tx(&sh.full[stage], (D / 64) * kChunkBytes);
           for (int x = 0; x < D / 64; ++x)
             tma_load_3d(sh.kv[stage][x], v ? &v_map : &k_map, &sh.full[stage], 64 * x, w.head, w.k0 + j * kKeys);
         }
       // the issuers' last arrivals come before the block ends
       for (int i = max(n - S::kStages, 0); ok && i < n; ++i)
-        ok = wait_bar(&sh.empty[i % S::kStages], (i / S::kStages) & 1, &sh.abort, p.status);
+        ok = wait_call(&sh.empty[i % S::kStages], (i / S::kStages) & 1, &sh.abort, p.status);
       if (!ok) {  // gave up: the copies in flight land before the block's memory is another's
         mbar_wait_drain(&sh.q_full, 0);
         for (int i = max(n - S::kStages, 0); i < n; ++i) mbar_wait_drain(&sh.full[i % S::kStages], (i / S::kStages) & 1);
       }
-    } else if (warp == 9) {
-      issue_products<D, 0>(p, sh, w);
-    } else if (warp == 10) {
-      issue_products<D, 1>(p, sh, w);
+    } else if (warp == 9 || warp == 10) {
+      issue_products<D>(p, sh, w, uniform(warp - 9));
     } else if (warp == 11) {
       // ------------------------------------------------------------ checker
       // Every stage of the ring passes through its hands, keys too, so that its barriers keep step
@@ -544,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       int edges = 0;
       for (int n = 0; n < items; ++n) {
         const int vs = n % S::kStages, j = w.j0 + n / 2;
-        const bool ok = wait_bar(&sh.full[vs], (n / S::kStages) & 1, &sh.abort, p.status);
+        const bool ok = wait_call(&sh.full[vs], (n / S::kStages) & 1, &sh.abort, p.status);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (n % 2 == 0 || !cut(w, j)) {
           if (lane == 0) {
