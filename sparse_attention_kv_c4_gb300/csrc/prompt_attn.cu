@@ -6,8 +6,8 @@
 // has two tiles of 128 rows of one key head against tiles of 128 keys.  A row is a (token, head of
 // the group), tokens first: a tile spans 128 / G tokens, so that short prompts fill it, the
 // diagonal cuts few of its key tiles, and keys are read once for a group.
-//   producer   (warp 8)  Q by 3-D TMA boxes [128 / G tokens, G heads, 64 elements]; keys and values in
-//              turn into a ring of tiles (SWIZZLE_128B)
+//   producer   (warp 8)  finds the items; Q by 3-D TMA boxes [128 / G tokens, G heads, 64 elements]; keys
+//              and values in turn into a ring of tiles (SWIZZLE_128B)
 //   issuers    (warps 9, 10)  one to a row tile: S = Q K^T (tcgen05 M128 N128 K16), then O += P V with P
 //              from TMEM, in two halves; one row tile's products run while the other's softmax
 //              does.  At D = 128 P takes the place of S, so the next S of a tile waits for its O
@@ -57,15 +57,33 @@ constexpr bool kOwnP = D == 64;
 template <int D>
 FM_DEV uint32_t p_column(int i) { return kOwnP<D> ? 2 * kKeys + 2 * D + i * (kKeys / 2) : i * kKeys; }
 
+// A row tile: its tokens in the sequence and the key tiles that they see.
+struct Tile {
+  int t0, tokens;     // first token, number (0: an empty tile)
+  int j0, j1;         // key tiles [j0, j1)
+  int whole0, whole1; // those of them that every row sees whole
+};
+struct Item {
+  int q0, k0, nk;     // the sequence's first query and key rows, its keys
+  int head;
+  int shift;          // nk - nq: query i is at position i + shift
+  int j0, j1;         // key tiles of both
+  int end;            // no item: the block's work is done
+  Tile tile[2];
+};
+
 template <int D>
 struct Smem {
   static constexpr int kStages = D == 128 ? 5 : 8;
   uint8_t q[2][D / 64][kChunkBytes];           // 1024-byte aligned
   uint8_t kv[kStages][D / 64][kChunkBytes];
-  uint64_t q_full, full[kStages], ready[kStages], empty[kStages];  // ready: full and checked
+  uint64_t q_full, q_empty, full[kStages], ready[kStages], empty[kStages];  // ready: full and checked
   uint64_t s_full[2], s_read[2], p_full[2][2], o_done[2], turn[2], drain[2];  // p_full: of the first 64 keys' weights, of the others'
-  int bad_tile[kMaxEdge];                      // key tiles that held an infinity or NaN
-  int bad;
+  uint64_t item_full[2], item_empty[2], claimed;
+  uint4 claim;                                 // a block of the grid that this one takes over
+  Item item[2];
+  int bad_tile[2][kMaxEdge];                   // an item's key tiles that held an infinity or NaN
+  int bad[2];
   uint32_t tmem;
   int abort;
 };
@@ -122,21 +140,28 @@ FM_DEV bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 x;\n\telect.sync x|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
   return r != 0;
 }
+// Takes over a block of this grid that has not started (cluster launch control); the answer arrives at `bar`.
+FM_DEV void claim_block(uint4* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+constexpr uint32_t kNoBlock = 0xFFFFFFFFu;
+FM_DEV uint32_t claimed_block(const uint4* answer) {
+  uint32_t x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+      "ld.shared.b128 a, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "mov.u32 %0, 0xFFFFFFFF;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, a;\n\t}"
+      : "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return x;
+}
 FM_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// A row tile: its tokens in the sequence and the key tiles that they see.
-struct Tile {
-  int t0, tokens;     // first token, number (0: an empty tile)
-  int j0, j1;         // key tiles [j0, j1)
-  int whole0, whole1; // those of them that every row sees whole
-};
-struct Item {
-  int q0, k0, nk;     // the sequence's first query and key rows, its keys
-  int head;
-  int shift;          // nk - nq: query i is at position i + shift
-  Tile tile[2];
-  int j0, j1;         // of both
-};
 
 FM_DEV int last_key(const Item& w, int token) { return token + w.shift; }
 FM_DEV int first_key(const PromptParams& p, const Item& w, int token) {
@@ -149,10 +174,11 @@ FM_DEV bool cut(const Item& w, int j) {
   return one(w.tile[0]) || one(w.tile[1]);
 }
 
-// The item of this block; false where the slot is empty.
-FM_DEV bool find_item(const PromptParams& p, Item& w) {
-  const int slot = p.slots - 1 - (int)(blockIdx.x / p.n_k);  // later tokens, which see more keys, go first
-  w.head = blockIdx.x % p.n_k;
+// The item of a block of the grid; false where the slot is empty.
+FM_DEV bool find_item(const PromptParams& p, uint32_t block, Item& w) {
+  const int slot = p.slots - 1 - (int)(block / p.n_k);  // later tokens, which see more keys, go first
+  w.head = block % p.n_k;
+  w.end = 0;
   const int pair = 2 * p.tokens;
   int b = 0, nq = p.T;
   w.q0 = w.k0 = 0;
@@ -189,10 +215,12 @@ FM_DEV bool find_item(const PromptParams& p, Item& w) {
   return true;
 }
 
+// One item's softmax and output.  `before`: key tiles of this row tile in the items before.
 template <int D>
-FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uint32_t tmem, int which) {
+FM_DEV bool softmax_item(const PromptParams& p, Smem<D>& sh, int slot, uint32_t tmem, int which, uint32_t before) {
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
-  const Tile& tile = w.tile[which];
+  const Item& w = sh.item[slot];
+  const Tile tile = w.tile[which];
   const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
   const uint32_t s_at = tmem + lanes + which * kKeys, o_at = tmem + lanes + 2 * kKeys + which * D;
   const uint32_t p_at = tmem + lanes + p_column<D>(which);
@@ -209,7 +237,7 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
   bool ok = true;
   for (int j = tile.j0; j < tile.j1; ++j) {
     const int n = j - tile.j0;
-    if (ok) ok = wait_bar(&sh.s_full[which], n & 1, &sh.abort, p.status);
+    if (ok) ok = wait_bar(&sh.s_full[which], (before + n) & 1, &sh.abort, p.status);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after();
     uint32_t s[4][32];
@@ -249,7 +277,7 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
       l.x *= keep;
       l.y *= keep;
       if (n > 0) {  // the products so far, in TMEM
-        if (!wait_bar(&sh.o_done[which], (n - 1) & 1, &sh.abort, p.status)) ok = false;
+        if (!wait_bar(&sh.o_done[which], (before + n - 1) & 1, &sh.abort, p.status)) ok = false;
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
 #pragma unroll 1
@@ -280,7 +308,7 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
         packed[e] = floats_bf16x2(y.x, y.y);
       }
       if (kOwnP<D> && half == 0 && n > 0) {  // the product that reads the last weights is over
-        if (!wait_bar(&sh.o_done[which], (n - 1) & 1, &sh.abort, p.status)) ok = false;
+        if (!wait_bar(&sh.o_done[which], (before + n - 1) & 1, &sh.abort, p.status)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
       }
@@ -295,10 +323,10 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
   // epilogue
   const int n = tile.j1 - tile.j0;
   if (n > 0 && ok) {
-    if (!wait_bar(&sh.o_done[which], (n - 1) & 1, &sh.abort, p.status)) ok = false;
+    if (!wait_bar(&sh.o_done[which], (before + n - 1) & 1, &sh.abort, p.status)) ok = false;
     tc_fence_after();
   }
-  if (!__all_sync(0xffffffffu, ok)) return;
+  if (!__all_sync(0xffffffffu, ok)) return false;
   const float sum = l.x + l.y;
   const int h = w.head * p.G + r - t * p.G;
   float z = sum;
@@ -325,12 +353,12 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
     }
     __syncwarp();  // the next load from TMEM is the whole warp's
   }
-  const int bad = sh.bad;
+  const int bad = sh.bad[slot];
   if (live && some && bad) {  // infinities and NaN of tiles that the mask cuts, in the keys that the row sees
 #pragma unroll 1
     for (int x = 0; x < kMaxEdge; ++x) {
       if (!(bad >> x & 1)) continue;
-      const int j = sh.bad_tile[x];
+      const int j = sh.bad_tile[slot][x];
 #pragma unroll 1
       for (int key = max(first, j * kKeys); key <= min(last, j * kKeys + kKeys - 1); ++key) {
         const uint16_t* v = p.v + (int64_t)(w.k0 + key) * p.v_stride_t + w.head * p.d;
@@ -344,6 +372,7 @@ FM_DEV void softmax_warps(const PromptParams& p, Smem<D>& sh, const Item& w, uin
     }
   }
   if (live && p.lse) p.lse[at] = some ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  return true;
 }
 
 // A place in the ring.
@@ -369,21 +398,19 @@ FM_DEV uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); 
 // together, and the tensor cores idle through both softmaxes.  (One warp for both tiles: the hundred
 // instructions between two products are then nobody else's time, 2 x 800 cycles of a step of 4000.)
 template <int D>
-FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, const Item& w, uint32_t I) {
+FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, uint32_t I) {
   constexpr int kStages = Smem<D>::kStages;
   constexpr uint32_t s_idesc = idesc_bf16_f32(kRows, kKeys), o_idesc = idesc_bf16_f32(kRows, D) | kBIsMnMajor;
   constexpr uint32_t kTileStep = (D / 64) * (kChunkBytes >> 4);
   const bool one = elect_one();
-  const Tile& tile = w.tile[I];
   const uint32_t tmem = uniform(sh.tmem), s_at = tmem + I * kKeys, o_at = tmem + 2 * kKeys + I * D, p_at = tmem + p_column<D>(I);
-  const int tiles = (int)uniform((uint32_t)max(w.j1 - w.j0, 0));
-  const int first = (int)uniform(max(tile.j0 - w.j0, 0)), end = (int)uniform(max(tile.j1 - w.j0, 0));
+  int tiles = 0, first = 0, end = 0, slot = 0;     // of the item; key tiles count from its first
+  uint32_t before = 0, turns = 0, q_turn = 0;      // this row tile's key tiles, all, and items with keys, before it
   const uint64_t q_desc = sdesc_sw128(smem_u32(sh.q[I][0])), k_desc = sdesc_sw128(smem_u32(sh.kv[0][0])),
                  v_desc = sdesc_mn_sw128(smem_u32(sh.kv[0][0]));
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_call(bar, parity, &sh.abort, p.status));
   };
-  if (tiles == 0) return;
   // S of key tile j, whose keys are in stage `at`.  The stage's phase is waited for even where the row tile
   // does not see the keys: a wait tells only the last phase from the one before.
   auto scores = [&](int j, const Place<kStages>& at) {
@@ -395,7 +422,7 @@ FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, const Item& w, ui
     }
     const uint64_t b = k_desc + at.stage * kTileStep;
     // S is free: its last scores are read, or, where P lies in its place, the product that reads P is over
-    if (done > 0 && !wait(kOwnP<D> ? &sh.s_read[I] : &sh.o_done[I], (done - 1) & 1)) return false;
+    if (before + done > 0 && !wait(kOwnP<D> ? &sh.s_read[I] : &sh.o_done[I], (before + done - 1) & 1)) return false;
     tc_fence_after();
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
@@ -413,9 +440,9 @@ FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, const Item& w, ui
     if (!wait(&sh.full[at.stage], at.turn)) return false;
     const int done = j - first;
     const bool sees = done >= 0 && j < end;
-    if (sees && cut(w, w.j0 + j) && !wait(&sh.ready[at.stage], at.turn)) return false;
-    if (sees && !wait(&sh.p_full[I][0], done & 1)) return false;
-    if (!kOwnP<D> && !wait(&sh.turn[I], j & 1)) return false;
+    if (sees && cut(sh.item[slot], sh.item[slot].j0 + j) && !wait(&sh.ready[at.stage], at.turn)) return false;
+    if (sees && !wait(&sh.p_full[I][0], (before + done) & 1)) return false;
+    if (!kOwnP<D> && !wait(&sh.turn[I], (turns + j) & 1)) return false;
     if (!sees) {
       if (one) mbar_arrive(&sh.empty[at.stage]);
       return true;
@@ -423,7 +450,7 @@ FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, const Item& w, ui
     const uint64_t b = v_desc + at.stage * kTileStep;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      if (half == 1 && !wait(&sh.p_full[I][1], done & 1)) return false;
+      if (half == 1 && !wait(&sh.p_full[I][1], (before + done) & 1)) return false;
       tc_fence_after();
 #pragma unroll
       for (int x = 0; x < kKeys / 32; ++x) {
@@ -439,22 +466,68 @@ FM_DEV void issue_products(const PromptParams& p, Smem<D>& sh, const Item& w, ui
   };
   Place<kStages> k_at, v_at;  // of the keys after, and of the values of, tile j
   v_at.next(1);
-  bool ok = wait(&sh.q_full, 0);
+  bool ok = true;
 #pragma unroll 1
-  for (int j = -1; ok && j < tiles; ++j) {
-    if (kOwnP<D> && j + 1 < tiles) ok = scores(j + 1, k_at);
-    if (ok && j >= 0) ok = values(j, v_at);
-    if (!kOwnP<D>) {
-      if (ok && j + 1 < tiles) ok = scores(j + 1, k_at);
-      if (one && (I == 0 || j + 1 < tiles) && j + (int)I >= 0) mbar_arrive(&sh.turn[1 - I]);
+  for (uint32_t k = 0; ok; ++k) {
+    slot = k & 1;
+    if (!(ok = wait(&sh.item_full[slot], (k >> 1) & 1)) || sh.item[slot].end) break;
+    const Item& w = sh.item[slot];
+    tiles = (int)uniform((uint32_t)max(w.j1 - w.j0, 0));
+    first = (int)uniform(max(w.tile[I].j0 - w.j0, 0));
+    end = (int)uniform(max(w.tile[I].j1 - w.j0, 0));
+    if (tiles > 0) ok = wait(&sh.q_full, q_turn++ & 1);
+#pragma unroll 1
+    for (int j = -1; ok && j < tiles; ++j) {
+      const bool more = j + 1 < tiles;
+      if (kOwnP<D> && more) ok = scores(j + 1, k_at);
+      if (ok && j >= 0) ok = values(j, v_at);
+      if (!kOwnP<D> && ok && more) ok = scores(j + 1, k_at);
+      if (one && more && j + 2 == tiles) umma_commit(&sh.q_empty);
+      if (!kOwnP<D> && one && (I == 0 || more) && j + (int)I >= 0) mbar_arrive(&sh.turn[1 - I]);
+      if (more) k_at.next(2);
+      if (j >= 0) v_at.next(2);
     }
-    k_at.next(2);
-    if (j >= 0) v_at.next(2);
+    if (end > first) before += end - first;
+    turns += tiles;
+    __syncwarp();
+    if (one) mbar_arrive(&sh.item_empty[slot]);
   }
   if (!ok && one) {  // gave up: the products in flight end before TMEM is freed
     umma_commit(&sh.drain[I]);
     mbar_wait_drain(&sh.drain[I], 0);
   }
+}
+
+// Zeroes infinities and NaN of the values in a stage; an item's edge number `edge`, key tile j.
+template <int D>
+FM_DEV void check_values(Smem<D>& sh, int stage, int slot, int edge, int j) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+#pragma unroll 1
+  for (int x = 0; x < D / 64; ++x) {
+    const uint4* cells = reinterpret_cast<const uint4*>(sh.kv[stage][x]);
+#pragma unroll 8
+    for (int i = lane; i < kChunkBytes / 16; i += 32) {
+      const uint4 u = cells[i];
+      const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)  // a carry out of an all-ones exponent, of either half
+        bad |= (((a[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) != 0;
+    }
+  }
+  if (!__any_sync(0xffffffffu, bad)) return;
+#pragma unroll 1
+  for (int x = 0; x < D / 64; ++x) {
+    uint16_t* cells = reinterpret_cast<uint16_t*>(sh.kv[stage][x]);
+#pragma unroll 1
+    for (int i = lane; i < kChunkBytes / 2; i += 32)
+      if ((cells[i] & 0x7F80u) == 0x7F80u) cells[i] = 0;
+  }
+  if (lane == 0) {
+    sh.bad_tile[slot][edge] = j;
+    sh.bad[slot] |= 1 << edge;
+  }
+  fence_async_smem();
 }
 
 template <int D>
@@ -468,6 +541,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 2);
+    mbar_init(&sh.claimed, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.item_full[i], 1);
+      mbar_init(&sh.item_empty[i], 11);  // softmax warps, issuers and the checker
+    }
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.ready[i], 1);
@@ -482,18 +561,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       mbar_init(&sh.turn[i], 1);
       mbar_init(&sh.drain[i], 1);
     }
-    sh.bad = 0;
     sh.abort = 0;
     fence_mbar_init();
     tma_prefetch(&q_map);
     tma_prefetch(&k_map);
     tma_prefetch(&v_map);
   }
-  // programmatic dependent launch: what a kernel before wrote may be read from here on
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Item w;
-  if (!find_item(p, w)) return;  // the whole block
   if (warp == 8) {
     tmem_alloc(&sh.tmem, kTmemCols);
     tmem_relinquish();
@@ -501,87 +574,131 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // programmatic dependent launch: what a kernel before wrote may be read from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = sh.tmem;
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    softmax_warps<D>(p, sh, w, tmem, warp >> 2);
+    const int which = warp >> 2;
+    uint32_t before = 0;
+#pragma unroll 1
+    for (uint32_t k = 0;; ++k) {
+      const int slot = k & 1;
+      const bool ok = wait_bar(&sh.item_full[slot], (k >> 1) & 1, &sh.abort, p.status);
+      if (!__all_sync(0xffffffffu, ok) || sh.item[slot].end) break;
+      if (!softmax_item<D>(p, sh, slot, tmem, which, before)) break;
+      before += sh.item[slot].tile[which].j1 - sh.item[slot].tile[which].j0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.item_empty[slot]);
+    }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8 && lane == 0) {
+    if (warp == 8) {
       // ------------------------------------------------------------ producer
+      // It also finds the items: this block's own, then those of blocks that have not started yet, which it
+      // takes over one at a time, so that the last item's output runs beside the next one's first products.
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_call(bar, parity, &sh.abort, p.status));
+      };
       bool ok = true;
-      if (w.j1 > w.j0) {
-        const int tiles = w.tile[1].tokens > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(&sh.q_full, tiles * (D / 64) * p.tokens * p.G * 128);
-        for (int i = 0; i < tiles; ++i)
-          for (int x = 0; x < D / 64; ++x) tma_load_3d(sh.q[i][x], &q_map, &sh.q_full, 64 * x, w.head * p.G, w.q0 + w.tile[i].t0);
-      }
-      int n = 0;
-      for (int j = w.j0; ok && j < w.j1; ++j)
-        for (int v = 0; v < 2; ++v, ++n) {
-          const int stage = n % S::kStages, turn = n / S::kStages;
-          if (turn > 0 && !(ok = wait_call(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status))) break;
-          mbar_arrive_expect_tx(&sh.full[stage], (D / 64) * kChunkBytes);
-          for (int x = 0; x < D / 64; ++x)
-            tma_load_3d(sh.kv[stage][x], v ? &v_map : &k_map, &sh.full[stage], 64 * x, w.head, w.k0 + j * kKeys);
+      uint32_t block = blockIdx.x, claims = 0, items = 0, q_items = 0;
+      int n = 0;  // stages filled
+#pragma unroll 1
+      for (;; ++claims) {
+        Item w;
+        if (find_item(p, block, w)) {
+          const int slot = items & 1;
+          if (items >= 2 && !(ok = wait(&sh.item_empty[slot], ((items >> 1) - 1) & 1))) break;
+          if (lane == 0) {
+            sh.item[slot] = w;
+            sh.bad[slot] = 0;
+            mbar_arrive(&sh.item_full[slot]);
+          }
+          ++items;
+          if (w.j1 > w.j0) {
+            if (q_items > 0 && !(ok = wait(&sh.q_empty, (q_items - 1) & 1))) break;
+            ++q_items;
+            if (lane == 0) {
+              const int tiles = w.tile[1].tokens > 0 ? 2 : 1;
+              mbar_arrive_expect_tx(&sh.q_full, tiles * (D / 64) * p.tokens * p.G * 128);
+              for (int i = 0; i < tiles; ++i)
+                for (int x = 0; x < D / 64; ++x)
+                  tma_load_3d(sh.q[i][x], &q_map, &sh.q_full, 64 * x, w.head * p.G, w.q0 + w.tile[i].t0);
+              for (int j = w.j0; ok && j < w.j1; ++j)
+                for (int v = 0; v < 2; ++v, ++n) {
+                  const int stage = n % S::kStages, turn = n / S::kStages;
+                  if (turn > 0 && !(ok = wait_call(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status))) break;
+                  mbar_arrive_expect_tx(&sh.full[stage], (D / 64) * kChunkBytes);
+                  for (int x = 0; x < D / 64; ++x)
+                    tma_load_3d(sh.kv[stage][x], v ? &v_map : &k_map, &sh.full[stage], 64 * x, w.head, w.k0 + j * kKeys);
+                }
+            }
+            n = __shfl_sync(0xffffffffu, n, 0);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          }
         }
+        // asked for when the item's last copies are under way: asked for before, the first blocks take what
+        // is left whether they finish early or not
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sh.claimed, 16);
+          claim_block(&sh.claim, &sh.claimed);
+        }
+        if (!(ok = wait(&sh.claimed, claims & 1))) break;
+        const uint32_t next = claimed_block(&sh.claim);
+        fence_async_smem();  // the next claim is written through the other proxy
+        if (next == kNoBlock) break;
+        block = next;
+        __syncwarp();
+      }
+      const int slot = items & 1;
+      if (ok && items >= 2) ok = wait(&sh.item_empty[slot], ((items >> 1) - 1) & 1);
+      if (ok && lane == 0) {
+        sh.item[slot].end = 1;
+        mbar_arrive(&sh.item_full[slot]);
+      }
       // the issuers' last arrivals come before the block ends
-      for (int i = max(n - S::kStages, 0); ok && i < n; ++i)
-        ok = wait_call(&sh.empty[i % S::kStages], (i / S::kStages) & 1, &sh.abort, p.status);
-      if (!ok) {  // gave up: the copies in flight land before the block's memory is another's
-        mbar_wait_drain(&sh.q_full, 0);
+      for (int i = max(n - S::kStages, 0); ok && i < n; ++i) ok = wait(&sh.empty[i % S::kStages], (i / S::kStages) & 1);
+      if (ok && q_items > 0) ok = wait(&sh.q_empty, (q_items - 1) & 1);
+      if (!ok && lane == 0) {  // gave up: the copies in flight land before the block's memory is another's
+        if (q_items > 0) mbar_wait_drain(&sh.q_full, (q_items - 1) & 1);
         for (int i = max(n - S::kStages, 0); i < n; ++i) mbar_wait_drain(&sh.full[i % S::kStages], (i / S::kStages) & 1);
       }
     } else if (warp == 9 || warp == 10) {
-      issue_products<D>(p, sh, w, uniform(warp - 9));
-    } else if (warp == 11) {
+      issue_products<D>(p, sh, uniform(warp - 9));
+    } else {
       // ------------------------------------------------------------ checker
       // Every stage of the ring passes through its hands, keys too, so that its barriers keep step
       // with the ring's.
-      const int items = 2 * max(w.j1 - w.j0, 0);
-      int edges = 0;
-      for (int n = 0; n < items; ++n) {
-        const int vs = n % S::kStages, j = w.j0 + n / 2;
-        const bool ok = wait_call(&sh.full[vs], (n / S::kStages) & 1, &sh.abort, p.status);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        if (n % 2 == 0 || !cut(w, j)) {
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_call(bar, parity, &sh.abort, p.status));
+      };
+      Place<S::kStages> at;
+      bool ok = true;
+#pragma unroll 1
+      for (uint32_t k = 0; ok; ++k) {
+        const int slot = k & 1;
+        if (!(ok = wait(&sh.item_full[slot], (k >> 1) & 1)) || sh.item[slot].end) break;
+        const Item& w = sh.item[slot];
+        const int stages = 2 * max(w.j1 - w.j0, 0);
+        int edges = 0;
+#pragma unroll 1
+        for (int n = 0; n < stages; ++n, at.next(1)) {
+          if (!(ok = wait(&sh.full[at.stage], at.turn))) break;
+          const int j = w.j0 + n / 2;
+          if (n % 2 == 1 && cut(w, j)) {
+            check_values<D>(sh, at.stage, slot, edges, j);
+            ++edges;
+          }
+          __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&sh.ready[vs]);
-            mbar_arrive(&sh.empty[vs]);
+            mbar_arrive(&sh.ready[at.stage]);
+            mbar_arrive(&sh.empty[at.stage]);
           }
-          continue;
-        }
-        bool bad = false;
-        for (int x = 0; x < D / 64; ++x) {
-          uint4* cells = reinterpret_cast<uint4*>(sh.kv[vs][x]);
-#pragma unroll 4
-          for (int i = lane; i < kChunkBytes / 16; i += 32) {
-            const uint4 u = cells[i];
-            const uint32_t a[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)  // a carry out of an all-ones exponent, of either half
-              bad |= (((a[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) != 0;
-          }
-        }
-        if (__any_sync(0xffffffffu, bad)) {
-          for (int x = 0; x < D / 64; ++x) {
-            uint16_t* cells = reinterpret_cast<uint16_t*>(sh.kv[vs][x]);
-            for (int i = lane; i < kChunkBytes / 2; i += 32)
-              if ((cells[i] & 0x7F80u) == 0x7F80u) cells[i] = 0;
-          }
-          if (lane == 0) {
-            sh.bad_tile[edges] = j;
-            sh.bad |= 1 << edges;
-          }
-          fence_async_smem();
         }
         __syncwarp();
-        ++edges;
-        if (lane == 0) {
-          mbar_arrive(&sh.ready[vs]);
-          mbar_arrive(&sh.empty[vs]);
-        }
+        if (lane == 0) mbar_arrive(&sh.item_empty[slot]);
       }
     }
   }
