@@ -159,6 +159,8 @@ FM_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
 // Row r of eight in a fragment is key row_key(r) of its eight keys, and a cell's 16-byte
 // chunk lies where the TMA's swizzle put it: with this order the eight lanes of a
 // 16-byte load, and the eight rows of an ldmatrix, meet eight different chunks.
+FM_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 template <int D>
 FM_DEV int row_key(int r) { return D == 128 ? (r >> 1) | ((r & 1) << 2) : r; }
 template <int D>
@@ -252,37 +254,12 @@ FM_DEV void load_rows(const KvParams& p, const Seq& s, int head, int tile, Rows<
       for (int i = 0; i < 4; ++i) w.o[j][nt][i] = 0.f;
 }
 
-// O^T += V^T P^T over a block of 16 keys.  keep0, keep1: which of the lane's keys of V (bytes: two of the
-// first, two of the second) are read as they are, the others as zeros.
-template <int D, int NT, bool Masked, class Use>
-FM_DEV void values_block(uint32_t v_smem, int block, uint32_t keep0, uint32_t keep1, Use use) {
-  const int lane = threadIdx.x & 31;
-  // lanes 0-7 address the rows of the matrix (keys 0-7, chunk 2j), 8-15 (8-15, 2j), 16-23 (0-7, 2j + 1), 24-31
-  const int key = 16 * block + 8 * ((lane >> 3) & 1) + row_key<D>(lane & 7);
-#pragma unroll
-  for (int j = 0; j < D / 32; ++j) {
-    uint32_t r[4];
-    ldmatrix4_trans(r, v_smem + chunk_at<D>(key, 2 * j + (lane >> 4)));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t x0 = r[2 * i], x1 = r[2 * i + 1];
-      if (Masked) {
-        x0 &= keep0;
-        x1 &= keep1;
-      }
-      x0 = __byte_perm(x0, 0, 0x3120);
-      x1 = __byte_perm(x1, 0, 0x3120);
-      use(2 * j + i, codes_half2(x0), codes_half2(x0 >> 16), codes_half2(x1), codes_half2(x1 >> 16));
-    }
-  }
-}
-
-// `Blocks` blocks of 16 keys from block `at` of a page on.
-template <int D, int NT, int Blocks, bool Partial>
-FM_DEV void key_blocks(const KvParams& p, const uint8_t* kv, const float (*scales)[kBlocksPerPage], int at, int page_first,
+// Blocks of 16 keys from block `at` of a page on, `Blocks` of them.  partial: some row does not see some key.
+template <int D, int NT, int Blocks>
+FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], int at, int page_first, bool partial,
                        Rows<D, NT>& w) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const uint32_t k_smem = smem_u32(kv) + 16 * at * D, v_smem = k_smem + Layout<D>::kTile;  // 16 rows keep the swizzle's phase
+  const uint32_t k_smem = kv_smem + 16 * at * D, v_smem = k_smem + Layout<D>::kTile;  // 16 rows keep the swizzle's phase
   const int first = page_first + 16 * at;
   float s[Blocks][NT][4];
 #pragma unroll
@@ -304,13 +281,38 @@ FM_DEV void key_blocks(const KvParams& p, const uint8_t* kv, const float (*scale
       }
     }
   }
-  float ks[Blocks], vs[Blocks];
+  float ks[Blocks], vs[Blocks], log_vs[Blocks];
 #pragma unroll
   for (int block = 0; block < Blocks; ++block) {
     ks[block] = scales[0][at + block];
     vs[block] = scales[1][at + block];
+    // a block that holds no key of any row may have any scale
+    if (partial && (first + 16 * block > w.most || first + 16 * block + 15 < w.low_least)) vs[block] = 0.f;
+    log_vs[block] = __log2f(vs[block]);
   }
-  // scores in log2; how far they pass their references
+  // scores in log2
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int block = 0; block < Blocks; ++block) {
+      const float f0 = ks[block] * w.f[nt][0], f1 = ks[block] * w.f[nt][1];
+      s[block][nt][0] *= f0;
+      s[block][nt][1] *= f1;
+      s[block][nt][2] *= f0;
+      s[block][nt][3] *= f1;
+    }
+  if (partial) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int block = 0; block < Blocks; ++block)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = first + 16 * block + row_key<D>(g) + 8 * (i >> 1);
+          if (j > w.pos[nt][i & 1] || j < w.low[nt][i & 1]) s[block][nt][i] = -INFINITY;
+        }
+  }
+  // how far they, and they plus the scale of V, pass their references
   bool passes = false;
   float top[NT][2], topv[NT][2];
 #pragma unroll
@@ -320,18 +322,9 @@ FM_DEV void key_blocks(const KvParams& p, const uint8_t* kv, const float (*scale
       top[nt][i] = topv[nt][i] = -INFINITY;
 #pragma unroll
       for (int block = 0; block < Blocks; ++block) {
-        const float f = ks[block] * w.f[nt][i];
-        float a = s[block][nt][i] * f, b = s[block][nt][i + 2] * f;
-        if (Partial) {
-          const int j = first + 16 * block + row_key<D>(g);
-          if (j > w.pos[nt][i] || j < w.low[nt][i]) a = -INFINITY;
-          if (j + 8 > w.pos[nt][i] || j + 8 < w.low[nt][i]) b = -INFINITY;
-        }
-        s[block][nt][i] = a;
-        s[block][nt][i + 2] = b;
-        const float x = fmaxf(a, b);
+        const float x = fmaxf(s[block][nt][i], s[block][nt][i + 2]);
         top[nt][i] = fmaxf(top[nt][i], x);
-        topv[nt][i] = fmaxf(topv[nt][i], x + __log2f(vs[block]));
+        topv[nt][i] = fmaxf(topv[nt][i], x + log_vs[block]);
       }
       passes |= top[nt][i] > w.m[nt][i] + kSlack || topv[nt][i] > w.mv[nt][i] + kSlack;
     }
@@ -372,77 +365,75 @@ FM_DEV void key_blocks(const KvParams& p, const uint8_t* kv, const float (*scale
         const float e = exp2_fast(s[block][nt][i] - w.m[nt][i & 1]);
         w.l[nt][i & 1] += e;
         x[i] = e * (vs[block] * shift[i & 1]);
-        if (Partial && s[block][nt][i] == -INFINITY) x[i] = 0.f;  // a block's scale may be anything where no key is
       }
       pt[block][nt][0] = transpose8x8(floats_half2(x[0], x[1]));
       pt[block][nt][1] = transpose8x8(floats_half2(x[2], x[3]));
     }
   }
-  auto plain = [&](int block) {
-    return [&w, &pt, block](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+  // O^T += V^T P^T.  Lanes 0-7 address the rows of the matrix (keys 0-7, chunk 2j), 8-15 (8-15, 2j), 16-23 (0-7,
+  // 2j + 1), 24-31 (8-15, 2j + 1)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_f16(w.o[j][nt], a0, a1, a2, a3, pt[block][nt][0], pt[block][nt][1]);
-    };
-  };
-  if (!Partial) {
+  for (int block = 0; block < Blocks; ++block) {
+    const int key = 16 * block + 8 * ((lane >> 3) & 1) + row_key<D>(lane & 7);
 #pragma unroll
-    for (int block = 0; block < Blocks; ++block) values_block<D, NT, false>(v_smem, block, 0, 0, plain(block));
-    return;
-  }
-  // Cells that are no keys of any row are taken as zeros: they may hold NaN, and zero times that is NaN.
-  auto keep_of = [&](int block, int half, int lo, int hi) {
-    const int j0 = first + 16 * block + 8 * half + row_key<D>(2 * c), j1 = first + 16 * block + 8 * half + row_key<D>(2 * c + 1);
-    return (j0 >= lo && j0 <= hi ? 0xFFFFu : 0u) | (j1 >= lo && j1 <= hi ? 0xFFFF0000u : 0u);
-  };
-  // NaN among the keys that some rows see and others do not
-  bool bad = false;
-  if (w.least != w.most) {
+    for (int j = 0; j < D / 32; ++j) {
+      uint32_t r[4];
+      ldmatrix4_trans(r, v_smem + chunk_at<D>(key, 2 * j + (lane >> 4)));
 #pragma unroll
-    for (int block = 0; block < Blocks; ++block) {
-      const uint32_t k0 = keep_of(block, 0, w.low_least, w.most) & ~keep_of(block, 0, w.low_most, w.least);
-      const uint32_t k1 = keep_of(block, 1, w.low_least, w.most) & ~keep_of(block, 1, w.low_most, w.least);
-      const int key = 16 * block + 8 * ((lane >> 3) & 1) + row_key<D>(lane & 7);
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t x0 = __byte_perm(r[2 * i], 0, 0x3120), x1 = __byte_perm(r[2 * i + 1], 0, 0x3120);
+        const uint32_t a0 = codes_half2(x0), a1 = codes_half2(x0 >> 16), a2 = codes_half2(x1), a3 = codes_half2(x1 >> 16);
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        uint32_t r[4];
-        ldmatrix4_trans(r, v_smem + chunk_at<D>(key, 2 * j + (lane >> 4)));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) bad |= (((r[i] & (i & 1 ? k1 : k0) & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+        for (int nt = 0; nt < NT; ++nt) mma_f16(w.o[2 * j + i][nt], a0, a1, a2, a3, pt[block][nt][0], pt[block][nt][1]);
       }
     }
-    bad = __any_sync(0xffffffffu, bad);
-  }
-  if (!bad) {
-#pragma unroll
-    for (int block = 0; block < Blocks; ++block)
-      values_block<D, NT, true>(v_smem, block, keep_of(block, 0, w.low_least, w.most), keep_of(block, 1, w.low_least, w.most), plain(block));
-    return;
-  }
-  // one token at a time: a product with the keys that it sees, added to its own columns
-  for (int pos = w.least; pos <= w.most; ++pos) {
-    const int lo = w.low_most > 0 ? max(w.low_most - (w.most - pos), 0) : 0;
-#pragma unroll
-    for (int block = 0; block < Blocks; ++block)
-      values_block<D, NT, true>(v_smem, block, keep_of(block, 0, lo, pos), keep_of(block, 1, lo, pos),
-                                [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-                                  for (int nt = 0; nt < NT; ++nt) {
-                                    float x[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma_f16(x, a0, a1, a2, a3, pt[block][nt][0], pt[block][nt][1]);
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                      if (w.pos[nt][i & 1] == pos) w.o[j][nt][i] += x[i];
-                                  }
-                                });
   }
 }
 
-// A page: all of its keys at once where registers allow, else in halves.
-template <int D, int NT, bool Partial>
-FM_DEV void page_tile(const KvParams& p, const uint8_t* kv, const float (*scales)[kBlocksPerPage], int first, Rows<D, NT>& w) {
-  constexpr int kBlocks = D * NT <= 256 ? 4 : 2;
+// Cells of V that are no keys of any row become zeros: they may hold NaN, and zero times that is NaN.  A NaN
+// that some rows see and others do not is made a zero too, and put into the outputs of those that
+// see it (E4M3 has no infinities).
+template <int D, int NT>
+FM_DEV void clean_values(uint8_t* v, int first, Rows<D, NT>& w) {
+  const int lane = threadIdx.x & 31, g = lane >> 2;
+  bool bad = false;
 #pragma unroll 1
-  for (int at = 0; at < kBlocksPerPage; at += kBlocks) key_blocks<D, NT, kBlocks, Partial>(p, kv, scales, at, first, w);
+  for (int i = lane; i < kKvPage * (D / 16); i += 32) {
+    const int key = first + i / (D / 16);
+    uint4* cell = reinterpret_cast<uint4*>(v + 16 * i);  // some chunk of the key's row: the swizzle stays within it
+    if (key > w.most || key < w.low_least) {
+      *cell = make_uint4(0, 0, 0, 0);
+    } else if (key > w.least || key < w.low_most) {
+      const uint4 u = *cell;
+      const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) bad |= (((a[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+    }
+  }
+  __syncwarp();
+  if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+    for (int key = 0; key < kKvPage; ++key) {
+      const int at = first + key;
+      if (at > w.most || at < w.low_least || (at <= w.least && at >= w.low_most)) continue;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint8_t* cell = v + chunk_at<D>(key, j) + 2 * g + k;
+          const bool nan = (*cell & 0x7F) == 0x7F;
+          __syncwarp();
+          if (!nan) continue;
+          *cell = 0;  // of the four lanes that read it, all
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (at <= w.pos[nt][i] && at >= w.low[nt][i]) w.o[j][nt][i + 2 * k] = __int_as_float(0x7FC00000);
+        }
+    }
+  }
+  __syncwarp();
 }
 
 FM_DEV void store_output(const KvParams& p, int64_t at, int e, float x) {
@@ -546,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
           }
           const int page = __shfl_sync(0xffffffffu, listed, page_at - page_from);
           const int stage = n % L::kStages, turn = n / L::kStages;
-          if (turn > 0) ok = mbar_wait(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status);
+          if (turn > 0) ok = wait_bar(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) {
@@ -587,14 +578,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
         const int64_t n = from + i - u0;
         if ((int)(n % kConsumers) != warp) continue;
         const int stage = (int)(n % L::kStages);
-        const bool ok = mbar_wait(&sh.full[stage], (uint32_t)(n / L::kStages) & 1, &sh.abort, p.status);
+        const bool ok = wait_bar(&sh.full[stage], (uint32_t)(n / L::kStages) & 1, &sh.abort, p.status);
         const int first = (s.low + page0 + i) * kKvPage;
         const bool some = ok && sh.held[stage] && first <= w.most && first + kKvPage > w.low_least;
         if (__all_sync(0xffffffffu, some)) {
-          if (first + kKvPage - 1 <= w.least && first >= w.low_most)
-            page_tile<D, NT, false>(p, sh.kv[stage][0], sh.scales[stage], first, w);
-          else
-            page_tile<D, NT, true>(p, sh.kv[stage][0], sh.scales[stage], first, w);
+          const bool partial = first + kKvPage - 1 > w.least || first < w.low_most;
+          if (partial) clean_values<D, NT>(sh.kv[stage][1], first, w);
+          // all keys at once where registers allow, else in halves
+          constexpr int kBlocks = D * NT <= 256 ? 4 : 2;
+#pragma unroll 1
+          for (int block = 0; block < kBlocksPerPage; block += kBlocks)
+            key_blocks<D, NT, kBlocks>(smem_u32(sh.kv[stage][0]), sh.scales[stage], block, first, partial, w);
+          if (partial) fence_async_smem();  // the next page comes through the other proxy
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[stage]);

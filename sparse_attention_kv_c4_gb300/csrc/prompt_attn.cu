@@ -250,7 +250,7 @@ FM_DEV bool softmax_item(const PromptParams& p, Smem<D>& sh, int slot, uint32_t 
       if (lane == 0) mbar_arrive(&sh.s_read[which]);
     }
     const int lo = first - j * kKeys, hi = last - j * kKeys;  // the row's keys in the tile: lo .. hi
-    if (__any_sync(0xffffffffu, lo > 0 || hi < kKeys - 1)) {
+    if (j < tile.whole0 || j >= tile.whole1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
