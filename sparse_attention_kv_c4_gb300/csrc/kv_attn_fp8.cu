@@ -118,9 +118,11 @@ FM_DEV int64_t run_begin(int64_t units, int c, int ctas) {
 
 FM_DEV uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 FM_DEV uint32_t floats_half2(float a, float b) { return half2_bits(__floats2half2_rn(a, b)); }
-FM_DEV uint32_t codes_half2(uint32_t c) {  // of the low two codes
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xFFFFu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four codes as two pairs of fp16 (exact).
+FM_DEV void codes_halves(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(c));
 }
 FM_DEV float exp2_fast(float x) {
   float y;
@@ -275,7 +277,9 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
       const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t a0 = codes_half2(a[i]), a1 = codes_half2(b[i]), a2 = codes_half2(a[i] >> 16), a3 = codes_half2(b[i] >> 16);
+        uint32_t a0, a1, a2, a3;
+        codes_halves(a[i], a0, a2);
+        codes_halves(b[i], a1, a3);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_f16(s[block][nt], a0, a1, a2, a3, w.q[4 * h + i][nt][0], w.q[4 * h + i][nt][1]);
       }
@@ -381,8 +385,9 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
       ldmatrix4_trans(r, v_smem + chunk_at<D>(key, 2 * j + (lane >> 4)));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t x0 = __byte_perm(r[2 * i], 0, 0x3120), x1 = __byte_perm(r[2 * i + 1], 0, 0x3120);
-        const uint32_t a0 = codes_half2(x0), a1 = codes_half2(x0 >> 16), a2 = codes_half2(x1), a3 = codes_half2(x1 >> 16);
+        uint32_t a0, a1, a2, a3;
+        codes_halves(__byte_perm(r[2 * i], 0, 0x3120), a0, a1);
+        codes_halves(__byte_perm(r[2 * i + 1], 0, 0x3120), a2, a3);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_f16(w.o[2 * j + i][nt], a0, a1, a2, a3, pt[block][nt][0], pt[block][nt][1]);
       }
