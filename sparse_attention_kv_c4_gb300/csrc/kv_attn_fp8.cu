@@ -10,7 +10,7 @@
 // The work is the list of units (sequence, key head, row tile, page of 64 tokens), cut into
 // as many equal runs as there are SMs whatever the sequences' lengths; a CTA works
 // out its run from the offsets by itself.  In a CTA one warp brings pages in by TMA (a
-// ring of stages, 128-byte swizzle) and seven warps take a page each in turn:
+// ring of stages, 128-byte swizzle) and six warps take a page each in turn:
 //   S^T = K Q^T   m16n8k16, 16 keys (one block of scales) x 8 rows, fp16 operands:
 //                 E4M3 is exact in fp16, queries are scaled to 2^14 by row
 //   softmax       against a running reference that moves only when a score
@@ -21,7 +21,7 @@
 // cache's rows as they lie: a lane's 16 bytes of a key are four steps of K16 (the order of
 // the contraction is free), ldmatrix transposes V by pairs of bytes.  mma.sync, not tcgen05:
 // codes have to pass through registers to become fp16, and a few rows leave either idle.
-// A segment's seven partial results are joined through shared memory; an item that spans
+// A segment's six partial results are joined through shared memory; an item that spans
 // CTAs by kv_join_kernel, in a fixed order.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -35,9 +35,10 @@
 namespace fm {
 namespace {
 
-constexpr int kConsumers = 7;            // eight warps: two to a scheduler have 255 registers each
+constexpr int kConsumers = 6;            // with the producer at most two warps to a scheduler: 255 registers each
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kMaxCtas = 256;
+constexpr int kBatch = 4;              // units that the producer brings at once
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLow = -1e30f;          // below every score
 constexpr float kSlack = 8.f;           // how far a score (in log2) may pass its reference
@@ -45,7 +46,9 @@ constexpr float kSlack = 8.f;           // how far a score (in log2) may pass it
 template <int D>
 struct Layout {
   static constexpr int kTile = kKvPage * D;  // bytes of a page and head
-  static constexpr int kStages = D == 128 ? 11 : 16;
+  // A multiple of the consumers: a stage is always the same warp's, which then sees every one of its phases.  (A
+  // warp that skipped a round could not tell its end from that of the round before.)
+  static constexpr int kStages = (D == 128 ? 2 : 3) * kConsumers;
   static constexpr int kPitch = D + 4;       // floats: rows 2c of a join are 8 banks apart
 };
 
@@ -515,53 +518,66 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
 
   if (warp == kConsumers) {
     // ---------------------------------------------------------------- producer
+    // Four lanes bring four units at once: one lane's hundred instructions a unit took longer than the copies.
     int64_t u = u0;
-    int n = 0;
+    uint32_t issued = 0;
     bool ok = true;
     for (; ok && u < u1; ++b, local = 0) {
       const Seq s = sequence<NT>(p, b);
       const int64_t all = (int64_t)s.tiles * p.n_k * s.pages;
       if (all == 0) continue;
-      if (lane == 0 && !s.none && s.start + s.n - 1 >= (int64_t)p.R * kKvPage) atomicOr(p.status, FM_DEV_PAGE_RANGE);
-      if (lane == 0 && s.none && s.start >= 0 && p.window > 0) atomicOr(p.status, FM_DEV_PAGE_RANGE);
-      int64_t item = local / s.pages;
-      int page_at = (int)(local - item * s.pages);
-      int listed = -1;   // lane i: the table's entry of page page_from + i
-      int page_from = -64;
-      for (; ok && item < (int64_t)s.tiles * p.n_k && u < u1; ++item, page_at = 0) {
-        const int head = (int)(item / s.tiles);
-        for (; page_at < s.pages && u < u1; ++page_at, ++u, ++n) {
-          if (page_at < page_from || page_at >= page_from + 32) {
-            page_from = page_at;
-            listed = -1;
-            if (!s.none && page_at + lane < s.pages) listed = p.page_table[(int64_t)b * p.R + s.low + page_at + lane];
-            if (listed >= p.P) {
-              atomicOr(p.status, FM_DEV_PAGE_RANGE);
-              listed = -1;
-            }
-          }
-          const int page = __shfl_sync(0xffffffffu, listed, page_at - page_from);
-          const int stage = n % L::kStages, turn = n / L::kStages;
-          if (turn > 0) ok = wait_bar(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) {
-            sh.held[stage] = page >= 0;
-            if (page >= 0) {
-              mbar_arrive_expect_tx(&sh.full[stage], 2 * L::kTile + 2 * kBlocksPerPage * 4);
-              tma_load_3d(sh.kv[stage][0], &k_map, &sh.full[stage], 0, head * kKvPage, page);
-              tma_load_3d(sh.kv[stage][1], &v_map, &sh.full[stage], 0, head * kKvPage, page);
-              bulk_load(sh.scales[stage][0], p.k_scale + page * p.scale_stride + head * kBlocksPerPage, 16, &sh.full[stage]);
-              bulk_load(sh.scales[stage][1], p.v_scale + page * p.scale_stride + head * kBlocksPerPage, 16, &sh.full[stage]);
-            } else {
-              mbar_arrive(&sh.full[stage]);
-            }
-          }
+      if (lane == 0 && p.window > 0 && (s.none ? s.start >= 0 : s.start + s.n - 1 >= (int64_t)p.R * kKvPage))
+        atomicOr(p.status, FM_DEV_PAGE_RANGE);
+      const int count = (int)min(all - local, u1 - u);      // units of this sequence in the run
+      const int item0 = (int)(local / s.pages), page0 = (int)(local - (int64_t)item0 * s.pages);
+      const int32_t* table = p.page_table + (int64_t)b * p.R + s.low;
+      // unit i of them: its key head and its page's number in the pool
+      auto place = [&](int i, int& head) {
+        const uint32_t at = (uint32_t)(page0 + i), item = at / (uint32_t)s.pages;
+        head = (int)(((uint32_t)item0 + item) / (uint32_t)s.tiles);
+        return i < count && !s.none ? table[at - item * s.pages] : -1;
+      };
+      int head = 0, next_head = 0;
+      int next = lane < kBatch ? place(lane, next_head) : -1;
+#pragma unroll 1
+      for (int base = 0; base < count; base += kBatch) {
+        int page = next;
+        head = next_head;
+        const bool live = lane < kBatch && base + lane < count;
+        if (lane < kBatch) next = place(base + kBatch + lane, next_head);
+        if (page >= p.P) {
+          atomicOr(p.status, FM_DEV_PAGE_RANGE);
+          page = -1;
+        }
+        const uint32_t n = (uint32_t)(u - u0) + base + lane;
+        const int stage = n % L::kStages;
+        const uint32_t turn = n / L::kStages;
+        if (live && turn > 0) ok = wait_bar(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        issued = (uint32_t)(u - u0) + base + kBatch;
+        if (!live) continue;
+        uint64_t* full = &sh.full[stage];
+        sh.held[stage] = page >= 0;
+        if (page >= 0) {
+          mbar_arrive_expect_tx(full, 2 * L::kTile + 2 * kBlocksPerPage * 4);
+          tma_load_3d(sh.kv[stage][0], &k_map, full, 0, head * kKvPage, page);
+          tma_load_3d(sh.kv[stage][1], &v_map, full, 0, head * kKvPage, page);
+          const int64_t at = page * p.scale_stride + head * kBlocksPerPage;
+          bulk_load(sh.scales[stage][0], p.k_scale + at, 16, full);
+          bulk_load(sh.scales[stage][1], p.v_scale + at, 16, full);
+        } else {
+          mbar_arrive(full);
         }
       }
+      __syncwarp();
+      u += count;
     }
-    if (!ok && lane == 0)  // gave up: the copies in flight land before the CTA's memory is another's
-      for (int i = max(n - L::kStages, 0); i < n; ++i) mbar_wait_drain(&sh.full[i % L::kStages], (i / L::kStages) & 1);
+    if (!ok && lane == 0) {  // gave up: the copies in flight land before the CTA's memory is another's
+      const uint32_t n = min((int64_t)issued, u1 - u0);
+      for (uint32_t i = n > L::kStages ? n - L::kStages : 0; i < n; ++i)
+        mbar_wait_drain(&sh.full[i % L::kStages], (i / L::kStages) & 1);
+    }
     return;
   }
 
@@ -579,11 +595,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
       const int pages = (int)min((int64_t)(s.pages - page0), u1 - u);  // of this segment
       u += pages;
       load_rows<D, NT>(p, s, head, tile, w);
-      for (int i = 0; i < pages; ++i) {
-        const int64_t n = from + i - u0;
-        if ((int)(n % kConsumers) != warp) continue;
-        const int stage = (int)(n % L::kStages);
-        const bool ok = wait_bar(&sh.full[stage], (uint32_t)(n / L::kStages) & 1, &sh.abort, p.status);
+      const uint32_t n0 = (uint32_t)(from - u0);  // of the run's units, this warp's are n = warp modulo kConsumers
+      for (int i = (int)((warp + kConsumers - n0 % kConsumers) % kConsumers); i < pages; i += kConsumers) {
+        const uint32_t n = n0 + i;
+        const int stage = n % L::kStages;
+        const bool ok = wait_bar(&sh.full[stage], n / L::kStages & 1, &sh.abort, p.status);
         const int first = (s.low + page0 + i) * kKvPage;
         const bool some = ok && sh.held[stage] && first <= w.most && first + kKvPage > w.low_least;
         if (__all_sync(0xffffffffu, some)) {

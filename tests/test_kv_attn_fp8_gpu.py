@@ -197,6 +197,38 @@ def test_long_caches_see_every_key(torch_dev):
     assert np.abs(lse.cpu().numpy()[0] - np.log(m)).max() <= 2.0 ** -19 * 11 + m * 2.0 ** -24
 
 
+@pytest.mark.parametrize("H,K,d,lens,starts,window", [
+    (8, 8, 64, [1, 1, 1], [60000, 35, 47003], None), (32, 4, 128, [1, 2], [70001, 30000], None), (10, 2, 96, [3, 1, 5], [50000, 64000, 9], 40001)])
+def test_many_pages_to_each_sm(torch_dev, H, K, d, lens, starts, window):
+    """Runs of a hundred pages and more that go round the ring many times, several heads and sequences to a run;
+    twenty calls give the same bits."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    rng = np.random.default_rng(H)
+    table, codes, scales, k, v, size, scale_of, held = make(rng, lens, starts, H, K, d)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T = int(cu[-1])
+    q = ref.bf16(rng.standard_normal((T, H, d)))
+    cd, sd = up(torch, dev, codes), up(torch, dev, scales)
+    args = (up(torch, dev, q.view(np.int16)), cd[0][:, 0], cd[1][:, 0], sd[0][:, 0], sd[1][:, 0], up(torch, dev, table), torch.tensor(starts, device=dev))
+    out, lse = torch.zeros((T, H, d), dtype=torch.int16, device=dev), torch.zeros((T, H), device=dev)
+    ws = torch.empty(fm.fm_kv_attn_fp8_workspace(T, H, K, d), dtype=torch.uint8, device=dev)
+    first = None
+    for _ in range(20):
+        out.zero_()
+        fm.fm_kv_attn_fp8(*args, out, cu_tokens=up(torch, dev, cu), window=window, lse_out=lse, workspace=ws)
+        torch.cuda.synchronize()
+        first = out.clone() if first is None else first
+        assert (out == first).all().item()
+    assert fm.fm_device_status(reset=True) == 0
+    got, got_lse = ref.f64(out.cpu().numpy().view(np.uint16)), lse.double().cpu().numpy()
+    for b in range(len(lens)):
+        rows = slice(cu[b], cu[b + 1])
+        want, want_lse, tol, ltol = gr.attend(ref.f64(q)[rows], k[b], v[b], starts[b], FOREVER if window is None else window, None, d ** -0.5,
+                                              held[b], gr.HALF_FP16, (size[b], scale_of[b]))
+        assert (np.abs(got_lse[rows] - want_lse) <= ltol).all() and (np.abs(got[rows] - want) <= tol).all(), b
+
+
 def test_two_calls_at_once_graph_and_same_results(torch_dev):
     """The result is the same bits eager, replayed on another stream, and beside another call with a workspace
     of its own; out may be q."""
