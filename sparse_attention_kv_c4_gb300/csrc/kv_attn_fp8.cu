@@ -8,9 +8,9 @@
 // for 4 d flops a row, so the kernel is bound by HBM up to some 30 rows.
 //
 // The work is the list of units (sequence, key head, row tile, page of 64 tokens), cut into
-// as many equal runs as there are SMs whatever the sequences' lengths; a CTA works
-// out its run from the offsets by itself.  In a CTA one warp brings pages in by TMA (a
-// ring of stages, 128-byte swizzle) and six warps take a page each in turn:
+// as many equal runs as there are warps, eight to an SM, whatever the sequences' lengths;
+// a warp works out its run from the offsets by itself.  It brings its own tiles of 64 x 64 or 32 x 128 by TMA
+// (three stages of 8 KB each, swizzled), and nothing in a CTA waits for another warp:
 //   S^T = K Q^T   m16n8k16, 16 keys (one block of scales) x 8 rows, fp16 operands:
 //                 E4M3 is exact in fp16, queries are scaled to 2^14 by row
 //   softmax       against a running reference that moves only when a score
@@ -21,8 +21,9 @@
 // cache's rows as they lie: a lane's 16 bytes of a key are four steps of K16 (the order of
 // the contraction is free), ldmatrix transposes V by pairs of bytes.  mma.sync, not tcgen05:
 // codes have to pass through registers to become fp16, and a few rows leave either idle.
-// A segment's six partial results are joined through shared memory; an item that spans
-// CTAs by kv_join_kernel, in a fixed order.
+// An item (sequence, key head, row tile) that spans runs is joined by kv_join_kernel, in a fixed order.
+// (With runs for each SM, a producer warp and a join of six warps' results at each item's end, an end cost
+// some 4 us: 30 requests of 1K to 32K took 209 us where 30 of 17K took 164.)
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -35,21 +36,21 @@
 namespace fm {
 namespace {
 
-constexpr int kConsumers = 6;            // with the producer at most two warps to a scheduler: 255 registers each
-constexpr int kThreads = (kConsumers + 1) * 32;
-constexpr int kMaxCtas = 256;
-constexpr int kBatch = 4;              // units that the producer brings at once
+constexpr int kWarps = 8;                // two to a scheduler: 255 registers each
+constexpr int kThreads = kWarps * 32;
+constexpr int kDepth = 3;                // tiles of a warp in shared memory
+constexpr int kMaxCtas = 160;
+constexpr int kMaxRuns = kMaxCtas * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLow = -1e30f;          // below every score
 constexpr float kSlack = 8.f;           // how far a score (in log2) may pass its reference
 
 template <int D>
 struct Layout {
-  static constexpr int kTile = kKvPage * D;  // bytes of a page and head
-  // A multiple of the consumers: a stage is always the same warp's, which then sees every one of its phases.  (A
-  // warp that skipped a round could not tell its end from that of the round before.)
-  static constexpr int kStages = (D == 128 ? 2 : 3) * kConsumers;
-  static constexpr int kPitch = D + 4;       // floats: rows 2c of a join are 8 banks apart
+  static constexpr int kKeys = 4096 / D;     // keys of a tile: a page, or half of one
+  static constexpr int kTiles = kKvPage / kKeys;
+  static constexpr int kTile = 4096;         // bytes of keys, and of values
+  static constexpr int kBlocks = kKeys / kKvBlock;
 };
 
 struct KvParams {
@@ -59,26 +60,22 @@ struct KvParams {
   const int64_t* start;
   uint16_t* out;
   float* lse;
-  float* part_o;      // [2 CTAs][rows][D] unnormalised outputs
-  float4* part_ml;    // [2 CTAs][rows] (reference of scores, of weights times scales, sum)
-  int4* part_item;    // [CTAs] (sequence, head, row tile, CTAs that follow) of a CTA's begun item
+  float* part_o;      // [2 runs][rows][D] unnormalised outputs
+  float4* part_ml;    // [2 runs][rows] (reference of scores, of weights times scales, sum)
+  int4* part_item;    // [runs] (sequence, head, row tile, runs that follow) of the item that a run begins and does not end
   int64_t q_stride_t, scale_stride, window;
-  int T, n_h, n_k, d, G, P, B, R;
+  int T, n_h, n_k, d, G, P, B, R, runs;
   float scale;
   unsigned int* status;
 };
 
-template <int D, int NT>
+template <int D>
 struct Smem {
-  uint8_t kv[Layout<D>::kStages][2][Layout<D>::kTile];  // 1024-byte aligned
-  float scales[Layout<D>::kStages][2][kBlocksPerPage];
-  float join[kConsumers][8][Layout<D>::kPitch];
-  float3 stats[kConsumers][8 * NT];
-  int held[Layout<D>::kStages];
-  uint64_t full[Layout<D>::kStages], empty[Layout<D>::kStages];
-  int64_t scan[kThreads / 32 + 1];
-  int64_t found;                                        // units before the run's first sequence
-  int seq;
+  uint8_t kv[kWarps][kDepth][2][Layout<D>::kTile];  // 1024-byte aligned
+  float scales[kWarps][kDepth][2][kBlocksPerPage];
+  uint64_t full[kWarps][kDepth];
+  int held[kWarps][kDepth];
+  int64_t before[kThreads + 1];                     // units before each thread's sequences
   int abort;
 };
 
@@ -113,10 +110,10 @@ FM_DEV int64_t units_of(const KvParams& p, int b) {
   return (int64_t)s.tiles * p.n_k * s.pages;
 }
 
-// First unit of CTA c's run.
-FM_DEV int64_t run_begin(int64_t units, int c, int ctas) {
-  const int64_t each = units / ctas, more = units % ctas;
-  return c * each + min((int64_t)c, more);
+// First unit of run r.
+FM_DEV int64_t run_begin(int64_t units, int r, int runs) {
+  const int64_t each = units / runs, more = units % runs;
+  return r * each + min((int64_t)r, more);
 }
 
 FM_DEV uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -259,13 +256,13 @@ FM_DEV void load_rows(const KvParams& p, const Seq& s, int head, int tile, Rows<
       for (int i = 0; i < 4; ++i) w.o[j][nt][i] = 0.f;
 }
 
-// Blocks of 16 keys from block `at` of a page on, `Blocks` of them.  partial: some row does not see some key.
+// Blocks of 16 keys from block `at` of a tile on, `Blocks` of them, whose scales are scale_at, ...  partial: some row does not see some key.
 template <int D, int NT, int Blocks>
-FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], int at, int page_first, bool partial,
-                       Rows<D, NT>& w) {
+FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], int at, int scale_at, int tile_first,
+                       bool partial, Rows<D, NT>& w) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const uint32_t k_smem = kv_smem + 16 * at * D, v_smem = k_smem + Layout<D>::kTile;  // 16 rows keep the swizzle's phase
-  const int first = page_first + 16 * at;
+  const int first = tile_first + 16 * at;
   float s[Blocks][NT][4];
 #pragma unroll
   for (int block = 0; block < Blocks; ++block) {
@@ -291,8 +288,8 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
   float ks[Blocks], vs[Blocks], log_vs[Blocks];
 #pragma unroll
   for (int block = 0; block < Blocks; ++block) {
-    ks[block] = scales[0][at + block];
-    vs[block] = scales[1][at + block];
+    ks[block] = scales[0][scale_at + block];
+    vs[block] = scales[1][scale_at + block];
     // a block that holds no key of any row may have any scale
     if (partial && (first + 16 * block > w.most || first + 16 * block + 15 < w.low_least)) vs[block] = 0.f;
     log_vs[block] = __log2f(vs[block]);
@@ -406,7 +403,7 @@ FM_DEV void clean_values(uint8_t* v, int first, Rows<D, NT>& w) {
   const int lane = threadIdx.x & 31, g = lane >> 2;
   bool bad = false;
 #pragma unroll 1
-  for (int i = lane; i < kKvPage * (D / 16); i += 32) {
+  for (int i = lane; i < Layout<D>::kKeys * (D / 16); i += 32) {
     const int key = first + i / (D / 16);
     uint4* cell = reinterpret_cast<uint4*>(v + 16 * i);  // some chunk of the key's row: the swizzle stays within it
     if (key > w.most || key < w.low_least) {
@@ -421,7 +418,7 @@ FM_DEV void clean_values(uint8_t* v, int first, Rows<D, NT>& w) {
   __syncwarp();
   if (__any_sync(0xffffffffu, bad)) {
 #pragma unroll 1
-    for (int key = 0; key < kKvPage; ++key) {
+    for (int key = 0; key < Layout<D>::kKeys; ++key) {
       const int at = first + key;
       if (at > w.most || at < w.low_least || (at <= w.least && at >= w.low_most)) continue;
 #pragma unroll
@@ -444,10 +441,6 @@ FM_DEV void clean_values(uint8_t* v, int first, Rows<D, NT>& w) {
   __syncwarp();
 }
 
-FM_DEV void store_output(const KvParams& p, int64_t at, int e, float x) {
-  if (e < p.d) p.out[at * p.d + e] = (uint16_t)(floats_bf16x2(x, 0.f) & 0xFFFFu);
-}
-
 // A row's factor from its sum of weights times codes to the output, and its log-sum-exp.
 FM_DEV float row_factor(const KvParams& p, int h, float m, float mv, float l) {
   if (l == 0.f) return 0.f;
@@ -456,261 +449,303 @@ FM_DEV float row_factor(const KvParams& p, int h, float m, float mv, float l) {
 }
 FM_DEV float row_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f; }
 
+// Brings a run's tiles one after the other, ahead of their use.
+template <int D, int NT>
+struct Loader {
+  const KvParams& p;
+  const CUtensorMap *k_map, *v_map;
+  Smem<D>& sh;
+  int warp, lane;
+  int64_t left;          // units of the run that have not been asked for
+  int b, item, page, part, entry;   // where the next tile is; entry: its page in the pool
+  int pages, items, tiles, low;
+  bool none;
+  int stage;
+
+  FM_DEV void enter(const Seq& s) {
+    pages = s.pages;
+    tiles = s.tiles;
+    items = s.tiles * p.n_k;
+    low = s.low;
+    none = s.none;
+    if (lane == 0 && p.window > 0 && (s.none ? s.start >= 0 : s.start + s.n - 1 >= (int64_t)p.R * kKvPage))
+      atomicOr(p.status, FM_DEV_PAGE_RANGE);
+  }
+  FM_DEV void look_up() { entry = none ? -1 : p.page_table[(int64_t)b * p.R + low + page]; }
+  FM_DEV void next() {
+    if (left == 0) return;
+    int at = entry;
+    if (at >= p.P) {
+      if (lane == 0) atomicOr(p.status, FM_DEV_PAGE_RANGE);
+      at = -1;
+    }
+    if (lane == 0) {
+      const int head = item / tiles;
+      uint64_t* full = &sh.full[warp][stage];
+      sh.held[warp][stage] = at >= 0;
+      if (at >= 0) {
+        mbar_arrive_expect_tx(full, 2 * Layout<D>::kTile + 2 * kBlocksPerPage * 4);
+        const int row = head * kKvPage + part * Layout<D>::kKeys;
+        tma_load_3d(sh.kv[warp][stage][0], k_map, full, 0, row, at);
+        tma_load_3d(sh.kv[warp][stage][1], v_map, full, 0, row, at);
+        const int64_t s = at * p.scale_stride + head * kBlocksPerPage;
+        bulk_load(sh.scales[warp][stage][0], p.k_scale + s, 16, full);
+        bulk_load(sh.scales[warp][stage][1], p.v_scale + s, 16, full);
+      } else {
+        mbar_arrive(full);
+      }
+    }
+    stage = stage + 1 == kDepth ? 0 : stage + 1;
+    if (++part < Layout<D>::kTiles) return;
+    part = 0;
+    --left;
+    if (++page == pages) {
+      page = 0;
+      if (++item == items && left > 0) {
+        item = 0;
+        Seq s;
+        do s = sequence<NT>(p, ++b);
+        while (s.tiles == 0);
+        enter(s);
+      }
+    }
+    if (left > 0) look_up();
+  }
+};
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_constant__ CUtensorMap k_map,
                                                               const __grid_constant__ CUtensorMap v_map,
                                                               const __grid_constant__ KvParams p) {
   using L = Layout<D>;
   extern __shared__ __align__(1024) uint8_t raw_smem[];
-  Smem<D, NT>& sh = *reinterpret_cast<Smem<D, NT>*>(raw_smem);
+  Smem<D>& sh = *reinterpret_cast<Smem<D>*>(raw_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     tma_prefetch(&k_map);
     tma_prefetch(&v_map);
-    for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
-    }
     sh.abort = 0;
-    fence_mbar_init();
   }
+  if (lane < kDepth) mbar_init(&sh.full[warp][lane], 1);
+  fence_mbar_init();
   // programmatic dependent launch: what a kernel before wrote may be read from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // the run of this CTA: units of all sequences, then the sequence that holds the run's first
-  int64_t mine = 0;
-  for (int b = tid; b < p.B; b += kThreads) mine += units_of<NT>(p, b);
-  const int64_t own = p.B <= kThreads ? mine : 0;
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sh.scan[warp] = mine;
-  __syncthreads();
-  int64_t units = 0;
-  for (int i = 0; i < kThreads / 32; ++i) units += sh.scan[i];
-  const int64_t u0 = run_begin(units, blockIdx.x, gridDim.x), u1 = run_begin(units, blockIdx.x + 1, gridDim.x);
-  if (tid == 0) p.part_item[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  if (u0 >= u1) return;
-  int64_t before = 0;  // units of the sequences before this round's
-  for (int base = 0; base < p.B; base += kThreads) {
-    const int b = base + tid;
-    const int64_t mine_b = p.B <= kThreads ? own : b < p.B ? units_of<NT>(p, b) : 0;
-    int64_t incl = mine_b;
+  // units before each thread's share of the sequences
+  const int share = (p.B + kThreads - 1) / kThreads;
+  {
+    int64_t mine = 0;
+    for (int i = 0; i < share && tid * (int64_t)share + i < p.B; ++i) mine += units_of<NT>(p, tid * share + i);
+    int64_t incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
+    if (lane == 31) sh.before[warp] = incl;
     __syncthreads();
-    if (lane == 31) sh.scan[warp] = incl;
+    for (int i = 0; i < warp; ++i) incl += sh.before[i];
     __syncthreads();
-    int64_t at = before;
-    for (int i = 0; i < warp; ++i) at += sh.scan[i];
-    for (int i = 0; i < kThreads / 32; ++i) before += sh.scan[i];
-    at += incl - mine_b;
-    if (mine_b > 0 && at <= u0 && u0 < at + mine_b) {
-      sh.found = at;
-      sh.seq = b;
-    }
-    if (before > u0) break;  // the same for every thread
+    sh.before[tid + 1] = incl;
+    if (tid == 0) sh.before[0] = 0;
+    __syncthreads();
   }
-  __syncthreads();
-  int b = sh.seq;
-  int64_t local = u0 - sh.found;  // the unit's place in its sequence
+  const int64_t units = sh.before[kThreads];
+  // neighbouring runs go to different SMs
+  const int run = warp * gridDim.x + blockIdx.x;
+  const int64_t u0 = run_begin(units, run, p.runs), u1 = run_begin(units, run + 1, p.runs);
+  if (lane == 0) p.part_item[run] = make_int4(-1, 0, 0, 0);
+  if (u0 >= u1) return;
+  // the sequence that holds the run's first unit
+  int lo = 0;
+  for (int hi = kThreads; hi - lo > 1;) {
+    const int mid = (lo + hi) / 2;
+    (sh.before[mid] <= u0 ? lo : hi) = mid;
+  }
+  int b = lo * share;
+  int64_t local = u0 - sh.before[lo];
+  for (int base = b;; base += 32) {  // 32 of the share's sequences at a time
+    const int64_t mine = lane + base < min(p.B, (lo + 1) * share) ? units_of<NT>(p, lane + base) : 0;
+    int64_t incl = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, incl > local);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      b = base + at;
+      local -= __shfl_sync(0xffffffffu, incl - mine, at);
+      break;
+    }
+    local -= __shfl_sync(0xffffffffu, incl, 31);
+  }
 
-  if (warp == kConsumers) {
-    // ---------------------------------------------------------------- producer
-    // Four lanes bring four units at once: one lane's hundred instructions a unit took longer than the copies.
-    int64_t u = u0;
-    uint32_t issued = 0;
-    bool ok = true;
-    for (; ok && u < u1; ++b, local = 0) {
-      const Seq s = sequence<NT>(p, b);
-      const int64_t all = (int64_t)s.tiles * p.n_k * s.pages;
-      if (all == 0) continue;
-      if (lane == 0 && p.window > 0 && (s.none ? s.start >= 0 : s.start + s.n - 1 >= (int64_t)p.R * kKvPage))
-        atomicOr(p.status, FM_DEV_PAGE_RANGE);
-      const int count = (int)min(all - local, u1 - u);      // units of this sequence in the run
-      const int item0 = (int)(local / s.pages), page0 = (int)(local - (int64_t)item0 * s.pages);
-      const int32_t* table = p.page_table + (int64_t)b * p.R + s.low;
-      // unit i of them: its key head and its page's number in the pool
-      auto place = [&](int i, int& head) {
-        const uint32_t at = (uint32_t)(page0 + i), item = at / (uint32_t)s.pages;
-        head = (int)(((uint32_t)item0 + item) / (uint32_t)s.tiles);
-        return i < count && !s.none ? table[at - item * s.pages] : -1;
-      };
-      int head = 0, next_head = 0;
-      int next = lane < kBatch ? place(lane, next_head) : -1;
+  Seq s = sequence<NT>(p, b);
+  int item = (int)(local / s.pages), page0 = (int)(local - (int64_t)item * s.pages);
+  Loader<D, NT> load = {p, &k_map, &v_map, sh, warp, lane, u1 - u0, b, item, page0, 0, -1};
+  load.stage = 0;
+  load.enter(s);
+  load.look_up();
 #pragma unroll 1
-      for (int base = 0; base < count; base += kBatch) {
-        int page = next;
-        head = next_head;
-        const bool live = lane < kBatch && base + lane < count;
-        if (lane < kBatch) next = place(base + kBatch + lane, next_head);
-        if (page >= p.P) {
-          atomicOr(p.status, FM_DEV_PAGE_RANGE);
-          page = -1;
-        }
-        const uint32_t n = (uint32_t)(u - u0) + base + lane;
-        const int stage = n % L::kStages;
-        const uint32_t turn = n / L::kStages;
-        if (live && turn > 0) ok = wait_bar(&sh.empty[stage], (turn - 1) & 1, &sh.abort, p.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        issued = (uint32_t)(u - u0) + base + kBatch;
-        if (!live) continue;
-        uint64_t* full = &sh.full[stage];
-        sh.held[stage] = page >= 0;
-        if (page >= 0) {
-          mbar_arrive_expect_tx(full, 2 * L::kTile + 2 * kBlocksPerPage * 4);
-          tma_load_3d(sh.kv[stage][0], &k_map, full, 0, head * kKvPage, page);
-          tma_load_3d(sh.kv[stage][1], &v_map, full, 0, head * kKvPage, page);
-          const int64_t at = page * p.scale_stride + head * kBlocksPerPage;
-          bulk_load(sh.scales[stage][0], p.k_scale + at, 16, full);
-          bulk_load(sh.scales[stage][1], p.v_scale + at, 16, full);
-        } else {
-          mbar_arrive(full);
-        }
+  for (int i = 0; i < kDepth; ++i) load.next();
+
+  Rows<D, NT> w;
+  int stage = 0;
+  uint32_t turn = 0;
+  bool ok = true;
+#pragma unroll 1
+  for (int64_t u = u0; u < u1 && ok;) {
+    if (item == s.tiles * p.n_k) {
+      item = 0;
+      do s = sequence<NT>(p, ++b);
+      while (s.tiles == 0);
+    }
+    const int head = item / s.tiles, tile = item - head * s.tiles;
+    const int64_t from = u;
+    const int pages = (int)min((int64_t)(s.pages - page0), u1 - u);  // of this segment
+    u += pages;
+    load_rows<D, NT>(p, s, head, tile, w);
+    const int first0 = (s.low + page0) * kKvPage;
+#pragma unroll 1
+    for (int i = 0; i < pages * L::kTiles; ++i) {
+      ok = wait_bar(&sh.full[warp][stage], turn, &sh.abort, p.status);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const int first = first0 + i * L::kKeys;
+      if (sh.held[warp][stage] && first <= w.most && first + L::kKeys > w.low_least) {
+        const bool partial = first + L::kKeys - 1 > w.least || first < w.low_most;
+        if (partial) clean_values<D, NT>(sh.kv[warp][stage][1], first, w);
+        // all keys at once where registers allow, else in halves
+        constexpr int kBlocks = D * NT <= 128 ? L::kBlocks : 2;
+#pragma unroll 1
+        for (int block = 0; block < L::kBlocks; block += kBlocks)
+          key_blocks<D, NT, kBlocks>(smem_u32(sh.kv[warp][stage][0]), sh.scales[warp][stage], block,
+                                     (i % L::kTiles) * L::kBlocks + block, first, partial, w);
+        if (partial) fence_async_smem();  // the next tile comes through the other proxy
       }
       __syncwarp();
-      u += count;
+      load.next();
+      stage = stage + 1 == kDepth ? 0 : stage + 1;
+      turn ^= stage == 0;
     }
-    if (!ok && lane == 0) {  // gave up: the copies in flight land before the CTA's memory is another's
-      const uint32_t n = min((int64_t)issued, u1 - u0);
-      for (uint32_t i = n > L::kStages ? n - L::kStages : 0; i < n; ++i)
-        mbar_wait_drain(&sh.full[i % L::kStages], (i / L::kStages) & 1);
+    if (!ok) break;
+    // the item's rows: out, or to the workspace where other runs have a part
+    const bool begins = page0 == 0, ends = page0 + pages == s.pages;
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) w.l[nt][i] += __shfl_xor_sync(0xffffffffu, w.l[nt][i], o);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float l = w.l[nt][i];
+        const int row = 8 * nt + 2 * c + i, r = tile * 8 * NT + row;
+        if (r >= s.n * p.G) continue;
+        if (begins && ends) {
+          const int t = r / p.G, h = head * p.G + r - t * p.G;
+          const int64_t at = (int64_t)(s.begin + t) * p.n_h + h;
+          const float factor = row_factor(p, h, w.m[nt][i], w.mv[nt][i], l);
+          uint16_t* out = p.out + at * p.d + 2 * g;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j)
+            if (16 * j < p.d)
+              *reinterpret_cast<uint32_t*>(out + 16 * j) =
+                  l == 0.f ? 0u : floats_bf16x2(w.o[j][nt][i] * factor, w.o[j][nt][i + 2] * factor);
+          if (g == 0 && p.lse) p.lse[at] = row_lse(w.m[nt][i], l);
+        } else {
+          const int64_t part = ((int64_t)2 * run + begins) * 8 * NT + row;
+          float* out = p.part_o + part * D + 2 * g;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) *reinterpret_cast<float2*>(out + 16 * j) = make_float2(w.o[j][nt][i], w.o[j][nt][i + 2]);
+          if (g == 0) p.part_ml[part] = make_float4(w.m[nt][i], w.mv[nt][i], l, 0.f);
+        }
+      }
+    __syncwarp();
+    if (begins && !ends && lane == 0) {
+      // the runs that have the rest of the item: up to the one with its last unit
+      const int64_t last = from + s.pages - 1, each = units / p.runs, more = units % p.runs;
+      const int64_t to = last < more * (each + 1) ? last / (each + 1) : more + (last - more * (each + 1)) / each;
+      p.part_item[run] = make_int4(b, head, tile, (int)(to - run));
     }
-    return;
+    ++item;
+    page0 = 0;
   }
-
-  // ------------------------------------------------------------------ consumers
-  Rows<D, NT> w;
-  int64_t u = u0;
-  for (; u < u1; ++b, local = 0) {
-    const Seq s = sequence<NT>(p, b);
-    if (s.tiles == 0) continue;
-    int64_t item = local / s.pages;
-    int page0 = (int)(local - item * s.pages);
-    for (; item < (int64_t)s.tiles * p.n_k && u < u1; ++item, page0 = 0) {
-      const int head = (int)(item / s.tiles), tile = (int)(item - (int64_t)head * s.tiles);
-      const int64_t from = u;
-      const int pages = (int)min((int64_t)(s.pages - page0), u1 - u);  // of this segment
-      u += pages;
-      load_rows<D, NT>(p, s, head, tile, w);
-      const uint32_t n0 = (uint32_t)(from - u0);  // of the run's units, this warp's are n = warp modulo kConsumers
-      for (int i = (int)((warp + kConsumers - n0 % kConsumers) % kConsumers); i < pages; i += kConsumers) {
-        const uint32_t n = n0 + i;
-        const int stage = n % L::kStages;
-        const bool ok = wait_bar(&sh.full[stage], n / L::kStages & 1, &sh.abort, p.status);
-        const int first = (s.low + page0 + i) * kKvPage;
-        const bool some = ok && sh.held[stage] && first <= w.most && first + kKvPage > w.low_least;
-        if (__all_sync(0xffffffffu, some)) {
-          const bool partial = first + kKvPage - 1 > w.least || first < w.low_most;
-          if (partial) clean_values<D, NT>(sh.kv[stage][1], first, w);
-          // all keys at once where registers allow, else in halves
-          constexpr int kBlocks = D * NT <= 256 ? 4 : 2;
-#pragma unroll 1
-          for (int block = 0; block < kBlocksPerPage; block += kBlocks)
-            key_blocks<D, NT, kBlocks>(smem_u32(sh.kv[stage][0]), sh.scales[stage], block, first, partial, w);
-          if (partial) fence_async_smem();  // the next page comes through the other proxy
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[stage]);
-      }
-      // join the warps' results
-      const bool begins = page0 == 0, ends = page0 + pages == s.pages;
-      const int g = lane >> 2, c = lane & 3;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float l = w.l[nt][i];
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-          if (g == 0) sh.stats[warp][8 * nt + 2 * c + i] = make_float3(w.m[nt][i], w.mv[nt][i], l);
-        }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (nt > 0) named_bar_sync(1, kConsumers * 32);
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float2*>(&sh.join[warp][2 * c + i][16 * j + 2 * g]) = make_float2(w.o[j][nt][i], w.o[j][nt][i + 2]);
-        named_bar_sync(1, kConsumers * 32);
-        for (int i8 = warp; i8 < 8; i8 += kConsumers) {  // a row to a warp
-          const int row = 8 * nt + i8, r = tile * 8 * NT + row;
-          float m = kLow, mv = kLow, l = 0.f, f[kConsumers];
-#pragma unroll
-          for (int i = 0; i < kConsumers; ++i) {
-            m = fmaxf(m, sh.stats[i][row].x);
-            mv = fmaxf(mv, sh.stats[i][row].y);
-          }
-#pragma unroll
-          for (int i = 0; i < kConsumers; ++i) {
-            l += sh.stats[i][row].z * exp2_fast(sh.stats[i][row].x - m);
-            f[i] = exp2_fast(sh.stats[i][row].y - mv);
-          }
-          const bool in = r < s.n * p.G, whole = begins && ends;
-          const int t = in ? r / p.G : 0;
-          const int64_t at = (int64_t)(s.begin + t) * p.n_h + head * p.G + (r - t * p.G);  // the output's row
-          const int64_t part = ((int64_t)2 * blockIdx.x + begins) * 8 * NT + row;
-          const float factor = in && whole ? row_factor(p, head * p.G + r - t * p.G, m, mv, l) : 1.f;
-          for (int e = lane; e < D; e += 32) {
-            float x = 0.f;
-#pragma unroll
-            for (int i = 0; i < kConsumers; ++i) x = fmaf(sh.join[i][i8][e], f[i], x);
-            if (!whole)
-              p.part_o[part * D + e] = x;
-            else if (in)
-              store_output(p, at, e, l == 0.f ? 0.f : x * factor);
-          }
-          if (lane == 0) {
-            if (!whole)
-              p.part_ml[part] = make_float4(m, mv, l, 0.f);
-            else if (in && p.lse)
-              p.lse[at] = row_lse(m, l);
-          }
-        }
-      }
-      if (begins && !ends && warp == 0 && lane == 0) {
-        // the CTAs that have the rest of the item: up to the one with its last unit
-        const int64_t last = from + s.pages - 1;
-        const int64_t each = units / gridDim.x, more = units % gridDim.x;
-        const int64_t cta = last < more * (each + 1) ? last / (each + 1) : more + (last - more * (each + 1)) / each;
-        p.part_item[blockIdx.x] = make_int4(b, head, tile, (int)(cta - blockIdx.x));
-      }
-      named_bar_sync(1, kConsumers * 32);  // join and stats are free again
+  if (!ok)  // gave up: the copies in flight land before the CTA's memory is another's
+    for (int i = 0; i < kDepth; ++i, turn ^= stage == 0) {
+      if (lane == 0) mbar_wait_drain(&sh.full[warp][stage], turn);
+      stage = stage + 1 == kDepth ? 0 : stage + 1;
     }
-  }
 }
 
-// Joins the parts of the items that span CTAs: block (c, row) the item that CTA c began.
-template <int D, int NT>
-__global__ void __launch_bounds__(D) kv_join_kernel(const __grid_constant__ KvParams p) {
+// Joins the parts of the items that span runs: block (x, row) the x-th such item.  Groups of D threads take
+// parts in turn and are summed in order.
+template <int D, int NT, int Groups>
+__global__ void __launch_bounds__(D * Groups) kv_join_kernel(const __grid_constant__ KvParams p) {
+  __shared__ int count[D * Groups / 32], found;
+  __shared__ float sum[Groups][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y;
+  constexpr int kThreadsJ = D * Groups;
+  if (tid == 0) found = -1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int cta = blockIdx.x, row = blockIdx.y, e = threadIdx.x;
-  const int4 item = p.part_item[cta];
-  if (item.x < 0) return;
+  // the x-th run that begins such an item
+  int before = 0;
+  for (int base = 0; base < p.runs; base += kThreadsJ) {
+    const bool is = base + tid < p.runs && p.part_item[base + tid].x >= 0;
+    const uint32_t vote = __ballot_sync(0xffffffffu, is);
+    if (lane == 0) count[warp] = __popc(vote);
+    __syncthreads();
+    int at = before + __popc(vote & ((1u << lane) - 1u));
+    for (int i = 0; i < kThreadsJ / 32; ++i) {
+      if (i < warp) at += count[i];
+      before += count[i];
+    }
+    if (is && at == (int)blockIdx.x) found = base + tid;
+    __syncthreads();
+    if (before > (int)blockIdx.x) break;
+  }
+  const int run = found;
+  if (run < 0) return;
+  const int4 item = p.part_item[run];
   const int begin = p.cu ? offset_at(p.cu, item.x, p.T) : item.x;
   const int n = p.cu ? offset_at(p.cu, item.x + 1, p.T) - begin : 1;
   const int r = item.z * 8 * NT + row;
   if (r >= n * p.G) return;
-  auto part = [&](int i) { return ((int64_t)2 * (cta + i) + (i == 0)) * 8 * NT + row; };
+  auto part = [&](int i) { return ((int64_t)2 * (run + i) + (i == 0)) * 8 * NT + row; };
   float m = kLow, mv = kLow;
-  for (int i = 0; i <= item.w; ++i) {
+  for (int i = lane; i <= item.w; i += 32) {
     const float4 s = p.part_ml[part(i)];
     m = fmaxf(m, s.x);
     mv = fmaxf(mv, s.y);
   }
-  float l = 0.f, x = 0.f;
-  for (int i = 0; i <= item.w; ++i) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+  }
+  float l = 0.f;
+  for (int i = lane; i <= item.w; i += 32) {
     const float4 s = p.part_ml[part(i)];
     l += s.z * exp2_fast(s.x - m);
-    x = fmaf(p.part_o[part(i) * D + e], exp2_fast(s.y - mv), x);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const int e = tid % D, group = tid / D;
+  float x = 0.f;
+#pragma unroll 8
+  for (int i = group; i <= item.w; i += Groups) x = fmaf(p.part_o[part(i) * D + e], exp2_fast(p.part_ml[part(i)].y - mv), x);
+  sum[group][e] = x;
+  __syncthreads();
+  if (group > 0) return;
+#pragma unroll
+  for (int i = 1; i < Groups; ++i) x += sum[i][e];
   const int t = r / p.G, h = item.y * p.G + r - t * p.G;
   const int64_t at = (int64_t)(begin + t) * p.n_h + h;
-  store_output(p, at, e, l == 0.f ? 0.f : x * row_factor(p, h, m, mv, l));
+  if (e < p.d) p.out[at * p.d + e] = (uint16_t)(floats_bf16x2(l == 0.f ? 0.f : x * row_factor(p, h, m, mv, l), 0.f) & 0xFFFFu);
   if (e == 0 && p.lse) p.lse[at] = row_lse(m, l);
 }
 
@@ -723,16 +758,16 @@ int row_eights(int64_t rows, int d) {
 }
 
 size_t workspace_bytes(int eights, int d) {
-  return (size_t)kMaxCtas * (sizeof(int4) + 2 * 8 * (size_t)eights * (sizeof(float4) + (d <= 64 ? 64 : 128) * sizeof(float)));
+  return (size_t)kMaxRuns * (sizeof(int4) + 2 * 8 * (size_t)eights * (sizeof(float4) + (d <= 64 ? 64 : 128) * sizeof(float)));
 }
 
 template <int D, int NT>
 cudaError_t launch(KvParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, int sms, uint8_t* workspace, cudaStream_t stream) {
   p.part_o = reinterpret_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float4*>(workspace + (size_t)kMaxCtas * 2 * 8 * NT * D * sizeof(float));
-  p.part_item = reinterpret_cast<int4*>(p.part_ml + (size_t)kMaxCtas * 2 * 8 * NT);
-  static_assert(sizeof(Smem<D, NT>) <= 227 * 1024, "shared memory of an SM");
-  const int smem = (int)sizeof(Smem<D, NT>);
+  p.part_ml = reinterpret_cast<float4*>(workspace + (size_t)kMaxRuns * 2 * 8 * NT * D * sizeof(float));
+  p.part_item = reinterpret_cast<int4*>(p.part_ml + (size_t)kMaxRuns * 2 * 8 * NT);
+  static_assert(sizeof(Smem<D>) <= 227 * 1024, "shared memory of an SM");
+  const int smem = (int)sizeof(Smem<D>);
   static std::atomic<uint64_t> prepared{0};  // devices whose kernel has its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -745,6 +780,7 @@ cudaError_t launch(KvParams& p, const CUtensorMap& k_map, const CUtensorMap& v_m
   const int64_t most = (int64_t)p.T * p.n_h * (p.R > 0 ? p.R : 1);  // units
   int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   if (most < ctas) ctas = (int)most;
+  p.runs = ctas * kWarps;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -756,10 +792,16 @@ cudaError_t launch(KvParams& p, const CUtensorMap& k_map, const CUtensorMap& v_m
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, NT>, k_map, v_map, (const KvParams)p)) != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)ctas, 8 * NT);
-  cfg.blockDim = dim3(D);
+  if (p.R <= 1) return cudaSuccess;  // items of one page are one run's
+  // At most as many items are split as there are runs, or items at all.  Where few items share the runs an
+  // item has many parts, which eight groups of threads sum.
+  const int64_t items = ((int64_t)p.T * p.G / (8 * NT) + p.B) * p.n_k;
+  const bool long_items = p.runs > 32 * items;
+  cfg.gridDim = dim3((unsigned)(items < p.runs ? items : p.runs), 8 * NT);
+  cfg.blockDim = dim3(long_items ? 8 * D : 2 * D);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT>, (const KvParams)p);
+  return long_items ? cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, 8>, (const KvParams)p)
+                    : cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, 2>, (const KvParams)p);
 }
 
 }  // namespace
@@ -769,7 +811,8 @@ using namespace fm;
 
 FM_API size_t fm_kv_attn_fp8_workspace(int T, int n_h, int n_k, int d) {
   if (T < 0 || bad_heads(n_h, n_k, d)) return 0;
-  return workspace_bytes(d <= 64 ? 4 : 3, d);
+  const int64_t most = d <= 64 ? 4 : 3, eights = ((int64_t)T * (n_h / n_k) + 7) / 8;
+  return workspace_bytes((int)(eights < most ? eights < 1 ? 1 : eights : most), d);
 }
 
 FM_API fm_status fm_kv_attn_fp8(const fm_kv_attn_fp8_args* a) {
@@ -805,7 +848,7 @@ FM_API fm_status fm_kv_attn_fp8(const fm_kv_attn_fp8_args* a) {
   CUtensorMap k_map, v_map;
   const uint64_t dims[3] = {(uint64_t)a->d, (uint64_t)a->n_k * kKvPage, a->P > 0 ? (uint64_t)a->P : 1};
   const uint64_t strides[2] = {(uint64_t)a->d, (uint64_t)a->page_stride};
-  const uint32_t box[3] = {(uint32_t)D, kKvPage, 1};
+  const uint32_t box[3] = {(uint32_t)D, (uint32_t)(4096 / D), 1};
   const CUtensorMapSwizzle swizzle = D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   // without pages nothing is read: any address will do for the maps
   const void *k_base = a->P > 0 ? (const void*)a->k_pool : a->q, *v_base = a->P > 0 ? (const void*)a->v_pool : a->q;
