@@ -41,6 +41,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kDepth = 3;                // tiles of a warp in shared memory
 constexpr int kMaxCtas = 160;
 constexpr int kMaxRuns = kMaxCtas * kWarps;
+constexpr int kRunsPerBlock = 8;        // of the join
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLow = -1e30f;          // below every score
 constexpr float kSlack = 8.f;           // how far a score (in log2) may pass its reference
@@ -458,7 +459,7 @@ struct Loader {
   int warp, lane;
   int64_t left;          // units of the run that have not been asked for
   int b, item, page, part, entry;   // where the next tile is; entry: its page in the pool
-  int pages, items, tiles, low;
+  int pages, items, tiles, low, row;  // row: the head's first in a page
   bool none;
   int stage;
 
@@ -480,15 +481,14 @@ struct Loader {
       at = -1;
     }
     if (lane == 0) {
-      const int head = item / tiles;
       uint64_t* full = &sh.full[warp][stage];
       sh.held[warp][stage] = at >= 0;
       if (at >= 0) {
         mbar_arrive_expect_tx(full, 2 * Layout<D>::kTile + 2 * kBlocksPerPage * 4);
-        const int row = head * kKvPage + part * Layout<D>::kKeys;
-        tma_load_3d(sh.kv[warp][stage][0], k_map, full, 0, row, at);
-        tma_load_3d(sh.kv[warp][stage][1], v_map, full, 0, row, at);
-        const int64_t s = at * p.scale_stride + head * kBlocksPerPage;
+        const int y = row + part * Layout<D>::kKeys;
+        tma_load_3d(sh.kv[warp][stage][0], k_map, full, 0, y, at);
+        tma_load_3d(sh.kv[warp][stage][1], v_map, full, 0, y, at);
+        const int64_t s = at * p.scale_stride + row / kKvBlock;
         bulk_load(sh.scales[warp][stage][0], p.k_scale + s, 16, full);
         bulk_load(sh.scales[warp][stage][1], p.v_scale + s, 16, full);
       } else {
@@ -508,6 +508,7 @@ struct Loader {
         while (s.tiles == 0);
         enter(s);
       }
+      row = item / tiles * kKvPage;
     }
     if (left > 0) look_up();
   }
@@ -553,8 +554,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
   const int64_t units = sh.before[kThreads];
   // neighbouring runs go to different SMs
   const int run = warp * gridDim.x + blockIdx.x;
-  const int64_t u0 = run_begin(units, run, p.runs), u1 = run_begin(units, run + 1, p.runs);
   if (lane == 0) p.part_item[run] = make_int4(-1, 0, 0, 0);
+  // an item's part costs a run as much as a page: no more runs than make four pages each, if the SMs have one
+  const int runs = (int)min((int64_t)p.runs, max(units / 4, (int64_t)gridDim.x));
+  if (run >= runs) return;
+  const int64_t u0 = run_begin(units, run, runs), u1 = run_begin(units, run + 1, runs);
   if (u0 >= u1) return;
   // the sequence that holds the run's first unit
   int lo = 0;
@@ -586,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
   Loader<D, NT> load = {p, &k_map, &v_map, sh, warp, lane, u1 - u0, b, item, page0, 0, -1};
   load.stage = 0;
   load.enter(s);
+  load.row = item / s.tiles * kKvPage;
   load.look_up();
 #pragma unroll 1
   for (int i = 0; i < kDepth; ++i) load.next();
@@ -667,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
     __syncwarp();
     if (begins && !ends && lane == 0) {
       // the runs that have the rest of the item: up to the one with its last unit
-      const int64_t last = from + s.pages - 1, each = units / p.runs, more = units % p.runs;
+      const int64_t last = from + s.pages - 1, each = units / runs, more = units % runs;
       const int64_t to = last < more * (each + 1) ? last / (each + 1) : more + (last - more * (each + 1)) / each;
       p.part_item[run] = make_int4(b, head, tile, (int)(to - run));
     }
@@ -681,72 +686,67 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
     }
 }
 
-// Joins the parts of the items that span runs: block (x, row) the x-th such item.  Groups of D threads take
-// parts in turn and are summed in order.
-template <int D, int NT, int Groups>
-__global__ void __launch_bounds__(D * Groups) kv_join_kernel(const __grid_constant__ KvParams p) {
-  __shared__ int count[D * Groups / 32], found;
-  __shared__ float sum[Groups][D];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y;
-  constexpr int kThreadsJ = D * Groups;
-  if (tid == 0) found = -1;
+// Joins the parts of the items that span runs: block (x, row) those that runs 8 x, ... , 8 x + 7 begin.  Eight
+// groups of threads take an item's parts in turn, four elements to a thread; their sums are added in order.
+template <int D, int NT>
+__global__ void __launch_bounds__(2 * D) kv_join_kernel(const __grid_constant__ KvParams p) {
+  constexpr int kGroups = 8, kLanes = D / 4;
+  __shared__ float4 sums[kGroups][kLanes];
+  const int tid = threadIdx.x, lane = tid & 31, row = blockIdx.y, group = tid / kLanes, e = 4 * (tid % kLanes);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // the x-th run that begins such an item
-  int before = 0;
-  for (int base = 0; base < p.runs; base += kThreadsJ) {
-    const bool is = base + tid < p.runs && p.part_item[base + tid].x >= 0;
-    const uint32_t vote = __ballot_sync(0xffffffffu, is);
-    if (lane == 0) count[warp] = __popc(vote);
-    __syncthreads();
-    int at = before + __popc(vote & ((1u << lane) - 1u));
-    for (int i = 0; i < kThreadsJ / 32; ++i) {
-      if (i < warp) at += count[i];
-      before += count[i];
+  const int run0 = blockIdx.x * kRunsPerBlock;
+  const int follow = lane < kRunsPerBlock && run0 + lane < p.runs && p.part_item[run0 + lane].x >= 0;
+  for (uint32_t todo = __ballot_sync(0xffffffffu, follow); todo != 0; todo &= todo - 1) {
+    const int run = run0 + __ffs(todo) - 1;
+    const int4 item = p.part_item[run];
+    const int begin = p.cu ? offset_at(p.cu, item.x, p.T) : item.x;
+    const int n = p.cu ? offset_at(p.cu, item.x + 1, p.T) - begin : 1;
+    const int r = item.z * 8 * NT + row;
+    if (r >= n * p.G) continue;  // the whole block
+    auto part = [&](int i) { return ((int64_t)2 * (run + i) + (i == 0)) * 8 * NT + row; };
+    float m = kLow, mv = kLow;
+    for (int i = lane; i <= item.w; i += 32) {
+      const float4 s = p.part_ml[part(i)];
+      m = fmaxf(m, s.x);
+      mv = fmaxf(mv, s.y);
     }
-    if (is && at == (int)blockIdx.x) found = base + tid;
-    __syncthreads();
-    if (before > (int)blockIdx.x) break;
-  }
-  const int run = found;
-  if (run < 0) return;
-  const int4 item = p.part_item[run];
-  const int begin = p.cu ? offset_at(p.cu, item.x, p.T) : item.x;
-  const int n = p.cu ? offset_at(p.cu, item.x + 1, p.T) - begin : 1;
-  const int r = item.z * 8 * NT + row;
-  if (r >= n * p.G) return;
-  auto part = [&](int i) { return ((int64_t)2 * (run + i) + (i == 0)) * 8 * NT + row; };
-  float m = kLow, mv = kLow;
-  for (int i = lane; i <= item.w; i += 32) {
-    const float4 s = p.part_ml[part(i)];
-    m = fmaxf(m, s.x);
-    mv = fmaxf(mv, s.y);
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-  }
-  float l = 0.f;
-  for (int i = lane; i <= item.w; i += 32) {
-    const float4 s = p.part_ml[part(i)];
-    l += s.z * exp2_fast(s.x - m);
-  }
+    for (int o = 16; o > 0; o >>= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+    }
+    float l = 0.f;
+    for (int i = lane; i <= item.w; i += 32) {
+      const float4 s = p.part_ml[part(i)];
+      l += s.z * exp2_fast(s.x - m);
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const int e = tid % D, group = tid / D;
-  float x = 0.f;
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int i = group; i <= item.w; i += Groups) x = fmaf(p.part_o[part(i) * D + e], exp2_fast(p.part_ml[part(i)].y - mv), x);
-  sum[group][e] = x;
-  __syncthreads();
-  if (group > 0) return;
+    for (int i = group; i <= item.w; i += kGroups) {
+      const float f = exp2_fast(p.part_ml[part(i)].y - mv);
+      const float4 y = *reinterpret_cast<const float4*>(p.part_o + part(i) * D + e);
+      x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+    }
+    sums[group][e / 4] = x;
+    __syncthreads();
+    if (group == 0 && e < p.d) {
 #pragma unroll
-  for (int i = 1; i < Groups; ++i) x += sum[i][e];
-  const int t = r / p.G, h = item.y * p.G + r - t * p.G;
-  const int64_t at = (int64_t)(begin + t) * p.n_h + h;
-  if (e < p.d) p.out[at * p.d + e] = (uint16_t)(floats_bf16x2(l == 0.f ? 0.f : x * row_factor(p, h, m, mv, l), 0.f) & 0xFFFFu);
-  if (e == 0 && p.lse) p.lse[at] = row_lse(m, l);
+      for (int i = 1; i < kGroups; ++i) {
+        const float4 y = sums[i][e / 4];
+        x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+      }
+      const int t = r / p.G, h = item.y * p.G + r - t * p.G;
+      const int64_t at = (int64_t)(begin + t) * p.n_h + h;
+      const float f = row_factor(p, h, m, mv, l);
+      *reinterpret_cast<uint2*>(p.out + at * p.d + e) =
+          l == 0.f ? make_uint2(0u, 0u) : make_uint2(floats_bf16x2(x.x * f, x.y * f), floats_bf16x2(x.z * f, x.w * f));
+      if (e == 0 && p.lse) p.lse[at] = row_lse(m, l);
+    }
+    __syncthreads();
+  }
 }
 
 // Rows in eights to a tile: those that a sequence's tokens have on average, so that its pages are read
@@ -793,15 +793,10 @@ cudaError_t launch(KvParams& p, const CUtensorMap& k_map, const CUtensorMap& v_m
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, NT>, k_map, v_map, (const KvParams)p)) != cudaSuccess) return e;
   if (p.R <= 1) return cudaSuccess;  // items of one page are one run's
-  // At most as many items are split as there are runs, or items at all.  Where few items share the runs an
-  // item has many parts, which eight groups of threads sum.
-  const int64_t items = ((int64_t)p.T * p.G / (8 * NT) + p.B) * p.n_k;
-  const bool long_items = p.runs > 32 * items;
-  cfg.gridDim = dim3((unsigned)(items < p.runs ? items : p.runs), 8 * NT);
-  cfg.blockDim = dim3(long_items ? 8 * D : 2 * D);
+  cfg.gridDim = dim3((unsigned)((p.runs + kRunsPerBlock - 1) / kRunsPerBlock), 8 * NT);
+  cfg.blockDim = dim3(2 * D);
   cfg.dynamicSmemBytes = 0;
-  return long_items ? cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, 8>, (const KvParams)p)
-                    : cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, 2>, (const KvParams)p);
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT>, (const KvParams)p);
 }
 
 }  // namespace
