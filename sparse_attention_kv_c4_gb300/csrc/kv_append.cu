@@ -29,7 +29,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = 64;
-constexpr int kQVectors = 4 * kThreads;  // 16-byte vectors of queries to a CTA
+constexpr int kQVectors = 8 * kThreads;  // 16-byte vectors of queries to a CTA
 constexpr int kQTokens = 16;
 
 struct AppendParams {
@@ -165,26 +165,29 @@ FM_DEV void append_block(const AppendParams& p, Shared& sh) {
   __syncthreads();
   if (!live) return;
 
-  float x[4][16];
+  // entries 2 m and 2 m + 1 of the lane's chunk i, turned.  Worked out twice, for the largest and for the codes: 64
+  // of them kept would halve the blocks of an SM.
+  auto entry = [&](int i, int m) {
+    const uint4 u = raw[i][m / 4];
+    const uint32_t v = m % 4 == 0 ? u.x : m % 4 == 1 ? u.y : m % 4 == 2 ? u.z : u.w;
+    float2 f = bf16x2_floats(v);
+    const int e = 16 * (lane + 32 * i - row[i] * chunks) + 2 * m - p.rope_start;  // even
+    if (is_k && e >= 0) {
+      const float2 t = sh.cs[row[i]][e >> 1];
+      f = make_float2(f.x * t.x - f.y * t.y, f.x * t.y + f.y * t.x);
+    }
+    return f;
+  };
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t u[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
-                           raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
-    const int e = 16 * (lane + 32 * i - max(row[i], 0) * chunks);
+  for (int i = 0; i < 4; ++i)
+    if (row[i] >= lo) {
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      float2 f = bf16x2_floats(u[m]);
-      const int pair = (e + 2 * m - p.rope_start) / 2;  // e + 2 m - rope_start is even
-      if (is_k && row[i] >= lo && e + 2 * m >= p.rope_start) {
-        const float2 t = sh.cs[row[i]][pair];
-        f = make_float2(f.x * t.x - f.y * t.y, f.x * t.y + f.y * t.x);
+      for (int m = 0; m < 8; ++m) {
+        const float2 f = entry(i, m);
+        amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
       }
-      x[i][2 * m] = f.x;
-      x[i][2 * m + 1] = f.y;
-      if (row[i] >= lo) amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
     }
-  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const float need = need_scale(amax);
@@ -198,11 +201,13 @@ FM_DEV void append_block(const AppendParams& p, Shared& sh) {
     const int e = 16 * (lane + 32 * i - row[i] * chunks);
     uint4 out;
     if (row[i] >= lo) {
-      float* y = x[i];
+      uint32_t w[4];
 #pragma unroll
-      for (int m = 0; m < 16; ++m) y[m] *= inv;
-      out = make_uint4(codes4(y[0], y[1], y[2], y[3]), codes4(y[4], y[5], y[6], y[7]),
-                       codes4(y[8], y[9], y[10], y[11]), codes4(y[12], y[13], y[14], y[15]));
+      for (int m = 0; m < 4; ++m) {
+        const float2 a = entry(i, 2 * m), c = entry(i, 2 * m + 1);
+        w[m] = codes4(a.x * inv, a.y * inv, c.x * inv, c.y * inv);
+      }
+      out = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       uint32_t w[4] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w};
 #pragma unroll
@@ -266,7 +271,7 @@ FM_DEV void turn_queries(const AppendParams& p, Shared& sh, int block) {
   }
 }
 
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ Shared sh;
   if (threadIdx.x < ((p.d - p.rope_start) >> 1)) sh.turn[threadIdx.x] = p.turn[threadIdx.x];
   // programmatic dependent launch: what a kernel before wrote may be read from here on
