@@ -47,6 +47,7 @@ struct PromptParams {
   float* lse;
   int64_t v_stride_t, window;
   int T, Tk, n_h, n_k, d, G, B, tokens, slots;  // tokens of a row tile
+  int more;                                     // there are more blocks than SMs
   float scale;
   unsigned int* status;
 };
@@ -250,12 +251,16 @@ FM_DEV bool softmax_item(const PromptParams& p, Smem<D>& sh, int slot, uint32_t 
       if (lane == 0) mbar_arrive(&sh.s_read[which]);
     }
     const int lo = first - j * kKeys, hi = last - j * kKeys;  // the row's keys in the tile: lo .. hi
-    if (j < tile.whole0 || j >= tile.whole1) {
+    if (j < tile.whole0 || j >= tile.whole1) {  // the mask cuts the tile
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        const int from = lo - 32 * i, to = hi - 32 * i;  // bits from .. to of the word are keys that the row sees
+        const uint32_t below = to >= 31 ? 0xFFFFFFFFu : to < 0 ? 0u : (2u << to) - 1u;
+        const uint32_t seen = from > 31 ? 0u : from <= 0 ? below : below & (0xFFFFFFFFu << from);
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-          if (32 * i + e < lo || 32 * i + e > hi) s[i][e] = 0xFF800000u;  // -inf
+          if (!(seen >> e & 1)) s[i][e] = 0xFF800000u;  // -inf
+      }
     }
     float top[4];
 #pragma unroll
@@ -639,6 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
           }
         }
+        if (!p.more) break;
         // asked for when the item's last copies are under way: asked for before, the first blocks take what
         // is left whether they finish early or not
         if (lane == 0) {
@@ -771,7 +777,8 @@ FM_API fm_status fm_prompt_attn(const fm_prompt_attn_args* a) {
   const int64_t slots = a->cu_q ? (int64_t)a->T / (2 * p.tokens) + a->B : (a->T + 2 * p.tokens - 1) / (2 * p.tokens);
   if (slots * a->n_k >= int64_t(1) << 31)
     return set_error(FM_ERR_INVALID_ARG, "%s: T=%d B=%d are too many for %d heads", who, a->T, a->B, a->n_h);
-  fm_status st = check_device(nullptr);
+  int sms = 0;
+  fm_status st = check_device(&sms);
   if (st != FM_OK) return st;
   if ((st = status_word(&p.status)) != FM_OK) return st;
   const int D = a->d <= 64 ? 64 : 128;
@@ -801,6 +808,7 @@ FM_API fm_status fm_prompt_attn(const fm_prompt_attn_args* a) {
   p.d = a->d;
   p.B = a->B;
   p.slots = (int)slots;
+  p.more = slots * a->n_k > sms;
   p.scale = a->scale;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(a->stream);
   const cudaError_t e = D == 64 ? launch<64>(p, maps[0], maps[1], maps[2], stream) : launch<128>(p, maps[0], maps[1], maps[2], stream);
