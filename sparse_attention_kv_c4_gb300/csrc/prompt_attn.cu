@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   const uint32_t tmem = sh.tmem;
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int which = warp >> 2;
     uint32_t before = 0;
 #pragma unroll 1
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       if (lane == 0) mbar_arrive(&sh.item_empty[slot]);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8) {
       // ------------------------------------------------------------ producer
       // It also finds the items: this block's own, then those of blocks that have not started yet, which it
