@@ -80,6 +80,21 @@ FM_DEV float need_scale(float amax) {
   return __uint_as_float((uint32_t)e << 23);
 }
 
+// Whether y may lie on the other side of the middle between two E4M3 values if it is off by `off`.
+FM_DEV bool near_middle(float y, float off) {
+  y = fabsf(y);
+  const uint32_t exponent = max(__float_as_uint(y) & 0x7F800000u, 121u << 23);  // the steps below 2^-6 are those of 2^-6
+  const float per_step = __uint_as_float(((254u << 23) - exponent) + (3u << 23));  // 2^3 / 2^e
+  const float q = y * per_step;
+  return fabsf(q - floorf(q) - 0.5f) <= off * per_step;
+}
+// A pair of bf16 entries turned in 64 bits: cos and sin of the phase in units of 2^-64 turns.
+__device__ __noinline__ float2 turn_exactly(float a, float b, uint64_t phase, float times) {
+  double s, c;
+  sincospi((double)(int64_t)phase * 1.0842021724855044e-19, &s, &c);
+  return make_float2((float)((a * c - b * s) * times), (float)((a * s + b * c) * times));
+}
+
 FM_DEV uint32_t codes4(float a, float b, float c, float d) {
   auto fix = [](float x) { return isinf(x) ? __int_as_float(0x7FC00000) : x; };  // the conversion would make it 448
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(fix(a), fix(b)), __NV_SATFINITE, __NV_E4M3);
@@ -195,6 +210,22 @@ FM_DEV void append_block(const AppendParams& p, Shared& sh) {
   const float scale = keep ? old : need;
   const float inv = 1.f / scale;
   const float shrink = old * inv;
+  // Entries over the scale.  One that the turn's rounding in 32 bits (under 2^-21 of the pair) may have carried over a
+  // middle between two codes, some 1 of 10^5, is turned again in 64.
+  auto scaled = [&](int i, int m) {
+    float2 f = entry(i, m);
+    f = make_float2(f.x * inv, f.y * inv);
+    const int e = 16 * (lane + 32 * i - row[i] * chunks) + 2 * m - p.rope_start;
+    if (is_k && e >= 0) {
+      const float off = (fabsf(f.x) + fabsf(f.y)) * 4.76837158e-7f;
+      if (near_middle(f.x, off) || near_middle(f.y, off)) {
+        const uint4 u = raw[i][m / 4];
+        const float2 x = bf16x2_floats(m % 4 == 0 ? u.x : m % 4 == 1 ? u.y : m % 4 == 2 ? u.z : u.w);
+        f = turn_exactly(x.x, x.y, (uint64_t)sh.pos[row[i]] * sh.turn[e >> 1], inv);
+      }
+    }
+    return f;
+  };
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (row[i] < 0 || (row[i] < lo && keep)) continue;
@@ -204,8 +235,8 @@ FM_DEV void append_block(const AppendParams& p, Shared& sh) {
       uint32_t w[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const float2 a = entry(i, 2 * m), c = entry(i, 2 * m + 1);
-        w[m] = codes4(a.x * inv, a.y * inv, c.x * inv, c.y * inv);
+        const float2 a = scaled(i, 2 * m), c = scaled(i, 2 * m + 1);
+        w[m] = codes4(a.x, a.y, c.x, c.y);
       }
       out = make_uint4(w[0], w[1], w[2], w[3]);
     } else {

@@ -201,7 +201,7 @@ def test_long_caches_see_every_key(torch_dev):
 
 
 @pytest.mark.parametrize("H,K,d,lens,starts,window", [
-    (8, 8, 64, [1, 1, 1], [40000, 35, 37003], None), (8, 8, 128, [1, 2], [30001, 20000], None), (10, 2, 96, [3, 1, 5], [50000, 34000, 9], 40001)])
+    (8, 8, 64, [1, 1, 1], [24000, 35, 21003], None), (8, 8, 128, [1, 2], [18001, 9000], None), (10, 2, 96, [2, 1, 5], [24000, 30000, 9], 20001)])
 def test_many_pages_to_each_sm(torch_dev, H, K, d, lens, starts, window):
     """Runs that go round their stages many times, several heads and sequences to a run; twenty calls give
     the same bits."""
