@@ -107,3 +107,79 @@ def test_the_append_turns_what_the_norm_would(torch_dev):
         # one key: the output is its value
         want = np.repeat(got_v, H // K, 0)
         assert (np.abs(out[b].double().cpu().numpy() - want) <= 2.0 ** -7 * np.abs(want)).all()
+
+
+def test_offsets_past_32_bits(torch_dev):
+    """A layer among a thousand: its pages are 16 MB apart, the last ones past 2^32 bytes."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    H, K, d, L, P = 4, 2, 128, 1024, 300
+    pools = [torch.zeros((P, L, K, 64, d), dtype=torch.uint8, device=dev) for _ in "kv"]
+    scales = [torch.ones((P, L, K, 4), device=dev) for _ in "kv"]
+    assert pools[0].numel() > 1 << 32
+    (kp, vp), (ks, vs) = ([t[:, 1000] for t in x] for x in (pools, scales))
+    table = torch.tensor([[299, 0, 298]], dtype=torch.int32, device=dev)
+    n = 150
+    g = torch.Generator(device=dev).manual_seed(1)
+    q, k, v = (torch.randn((n, h, d), generator=g, device=dev).bfloat16() for h in (H, K, K))
+    cu, start = torch.tensor([0, n], dtype=torch.int32, device=dev), torch.zeros(1, dtype=torch.int64, device=dev)
+    fm.fm_kv_append_fp8(k, v, kp, vp, ks, vs, table, start, cu_tokens=cu, rope_dim=0)
+    out = torch.empty((1, H, d), dtype=torch.bfloat16, device=dev)
+    ws = torch.empty(fm.fm_kv_attn_fp8_workspace(1, H, K, d), dtype=torch.uint8, device=dev)
+    fm.fm_kv_attn_fp8(q[-1:].contiguous(), kp, vp, ks, vs, table, start + n - 1, out, workspace=ws)
+    torch.cuda.synchronize()
+    assert fm.fm_device_status(reset=True) == 0
+    assert all(int(p[:, :1000].sum()) == 0 and int(p[:, 1001:].sum()) == 0 for p in pools)
+    codes = np.stack([gr.VALUES[x.cpu().numpy()] for x in (kp, vp)])
+    sc = np.stack([x.double().cpu().numpy() for x in (ks, vs)])
+    j = np.arange(n)
+    page = table[0].cpu().numpy()[j // 64]
+    cells = [codes[i][page, :, j % 64] * sc[i][page, :, j % 64 // 16][..., None] for i in (0, 1)]
+    for i, x in ((0, k), (1, v)):
+        x = x.double().cpu().numpy()
+        block = np.stack([np.abs(x[lo:lo + 16]).max((0, 2)) for lo in range(0, n, 16)])[j // 16][..., None]
+        assert (np.abs(cells[i] - x) <= 2.0 ** -4 * np.abs(x) + 2.0 ** -9 * block / 224).all()
+    want, _, tol, _ = gr.attend(q[-1:].double().cpu().numpy(), cells[0], cells[1], n - 1, 1 << 60, None, d ** -0.5, None, gr.HALF_FP16,
+                                (np.abs(codes[1][page, :, j % 64]), sc[1][page, :, j % 64 // 16][..., None]))
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+
+
+def test_arguments_on_their_own_borders_only(torch_dev):
+    """Every tensor begins 16 bytes (or one element, where that is allowed) into a larger one, and rows lie apart."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    n, H, K, d = 70, 6, 3, 80
+    g = torch.Generator(device=dev).manual_seed(2)
+
+    def inside(t, skip):
+        flat = torch.zeros(t.numel() + 64, dtype=t.dtype, device=dev)[skip:skip + t.numel()].view(t.shape)
+        return flat.copy_(t)
+    rows = lambda h: torch.randn((n, h * d + 24), generator=g, device=dev).bfloat16()[:, 8:8 + h * d].unflatten(1, (h, d))
+    q, k, v = rows(H), rows(K), rows(K)
+    ints = lambda x, t: inside(torch.tensor(x, dtype=t, device=dev), 1)
+    cu, table, start = ints([0, 30, n], torch.int32), ints([[1, 3], [0, 2]], torch.int32), ints([0, 9], torch.int64)
+    pool = [inside(torch.zeros((4, K, 64, d), dtype=torch.uint8, device=dev), 16) for _ in "kv"]
+    scale = [inside(torch.ones((4, K, 4), device=dev), 4) for _ in "kv"]
+    sink, lse, lse2 = ints([0.5] * H, torch.float32), inside(torch.zeros((n, H), device=dev), 1), inside(torch.zeros((n, H), device=dev), 3)
+    out, out2 = (inside(torch.zeros((n, H, d), dtype=torch.bfloat16, device=dev), 8) for _ in "ab")
+    fm.fm_kv_append_fp8(k, v, *pool, *scale, table, start, cu_tokens=cu, rope_dim=0)
+    ws = torch.empty(fm.fm_kv_attn_fp8_workspace(n, H, K, d), dtype=torch.uint8, device=dev)
+    fm.fm_kv_attn_fp8(q, *pool, *scale, table, start, out, cu_tokens=cu, window=20, sink_logit=sink, lse_out=lse, workspace=ws)
+    fm.fm_prompt_attn(q, k, v, out2, cu_q=cu, window=20, sink_logit=sink, lse_out=lse2)
+    torch.cuda.synchronize()
+    assert fm.fm_device_status(reset=True) == 0
+    qf, kf, vf = (t.double().cpu().numpy() for t in (q, k, v))
+    for b, (lo, hi) in enumerate(((0, 30), (30, n))):
+        want, wl, tol, lt = gr.attend(qf[lo:hi], kf[lo:hi], vf[lo:hi], 0, 20, np.full(H, 0.5), d ** -0.5)
+        assert (np.abs(out2[lo:hi].double().cpu().numpy() - want) <= tol).all()
+        assert (np.abs(lse2[lo:hi].double().cpu().numpy() - wl) <= lt).all()
+        s = int(start[b])
+        j = np.arange(s, s + hi - lo)
+        page = table[b].cpu().numpy()[j // 64]
+        codes = [gr.VALUES[x.cpu().numpy()][page, :, j % 64] for x in pool]
+        sc = [x.double().cpu().numpy()[page, :, j % 64 // 16][..., None] for x in scale]
+        if s == 0:  # the second sequence's first nine cells were never written: zeros, with weight
+            want, wl, tol, lt = gr.attend(qf[lo:hi], codes[0] * sc[0], codes[1] * sc[1], 0, 20, np.full(H, 0.5), d ** -0.5, None, gr.HALF_FP16,
+                                          (np.abs(codes[1]), sc[1]))
+            assert (np.abs(out[lo:hi].double().cpu().numpy() - want) <= tol).all()
+            assert (np.abs(lse[lo:hi].double().cpu().numpy() - wl) <= lt).all()
