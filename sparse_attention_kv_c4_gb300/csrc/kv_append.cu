@@ -43,6 +43,7 @@ struct AppendParams {
   int T, n_k, d, n_h, B, R, rope_start;
   int slots, slot_ctas;              // CTAs to a slot
   int q_tokens, q_chunks;            // tokens to a CTA, or CTAs to a token
+  uint32_t by_pairs, by_chunks, by_token, by_head;  // ceil(2^32 / divisor): of pairs, of 16-element chunks of a head, of a token's and a head's vectors
   unsigned int* status;
   uint64_t turn[kMaxPairs];          // theta'_i / 2 pi in units of 2^-64 turns
 };
@@ -53,11 +54,14 @@ struct Shared {
   int64_t pos[kQTokens];
 };
 
+// x / divisor for x < 2^16 and divisors up to 2^14 (0: 1): the product's excess stays below 2^32 / divisor.
+FM_DEV int quotient(int x, uint32_t by) { return by == 0 ? x : (int)__umulhi((uint32_t)x, by); }
+
 // (cos, sin) of `rows` tokens at sh.pos (negative: left out), by the whole CTA.
 FM_DEV void fill_turns(const AppendParams& p, Shared& sh, int rows) {
   const int pairs = (p.d - p.rope_start) >> 1;
   for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
-    const int r = i / pairs, j = i - r * pairs;
+    const int r = quotient(i, p.by_pairs), j = i - r * pairs;
     if (sh.pos[r] < 0) continue;
     const uint64_t phase = (uint64_t)sh.pos[r] * sh.turn[j];
     float c, s;
@@ -160,7 +164,7 @@ FM_DEV void append_block(const AppendParams& p, Shared& sh) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int c = lane + 32 * i;
-    row[i] = c / chunks;
+    row[i] = quotient(c, p.by_chunks);
     const int e = 16 * (c - row[i] * chunks);
     raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
     if (!live || row[i] >= hi) {
@@ -266,7 +270,7 @@ FM_DEV void turn_queries(const AppendParams& p, Shared& sh, int block) {
     const int v = v0 + threadIdx.x + i * kThreads;
     raw[i] = make_uint4(0, 0, 0, 0);
     if (v - v0 < vectors) {
-      const int t = v / per;
+      const int t = quotient(v, p.by_token);
       raw[i] = load16(p.q + (int64_t)(t0 + t) * p.q_stride_t + 8 * (v - t * per));
     }
   }
@@ -288,9 +292,10 @@ FM_DEV void turn_queries(const AppendParams& p, Shared& sh, int block) {
   for (int i = 0; i < kQVectors / kThreads; ++i) {
     const int v = v0 + threadIdx.x + i * kThreads;
     if (v - v0 >= vectors) continue;
-    const int t = v / per;
+    const int t = quotient(v, p.by_token);
     if (sh.pos[t] < 0) continue;
-    const int e = 8 * ((v - t * per) % (p.d >> 3));
+    const int in = v - t * per;  // the vector's place in its token, then in its head
+    const int e = 8 * (in - quotient(in, p.by_head) * (p.d >> 3));
     uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -385,6 +390,11 @@ FM_API fm_status fm_kv_append_fp8(const fm_kv_append_fp8_args* a) {
   p.B = a->B;
   p.R = a->R;
   p.rope_start = a->d - a->rope_dim;
+  auto by = [](int divisor) { return divisor <= 1 ? 0u : (uint32_t)(((uint64_t(1) << 32) + divisor - 1) / divisor); };
+  p.by_pairs = by(a->rope_dim / 2);
+  p.by_chunks = by(a->d / 16);
+  p.by_token = by((int)per);
+  p.by_head = by(a->d / 8);
   rope_turns(a->rope_dim, a->rope_base, a->rope_factor, a->rope_orig_len, a->rope_beta_fast, a->rope_beta_slow, p.turn);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
