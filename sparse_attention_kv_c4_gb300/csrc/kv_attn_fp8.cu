@@ -8,9 +8,9 @@
 // for 4 d flops a row, so the kernel is bound by HBM up to some 30 rows.
 //
 // The work is the list of units (sequence, key head, row tile, page of 64 tokens), cut into
-// as many equal runs as there are warps, eight to an SM, whatever the sequences' lengths;
-// a warp works out its run from the offsets by itself.  It brings its own tiles of 64 x 64 or 32 x 128 by TMA
-// (three stages of 8 KB each, swizzled), and nothing in a CTA waits for another warp:
+// as many equal runs as there are warps, seven to an SM, whatever the sequences' lengths;
+// a warp works out its run from the offsets by itself, and a lane of the CTA's eighth warp brings its tiles
+// of 64 x 64 or 32 x 128 by TMA (three stages of 8 KB each, swizzled):
 //   S^T = K Q^T   m16n8k16, 16 keys (one block of scales) x 8 rows, fp16 operands:
 //                 E4M3 is exact in fp16, queries are scaled to 2^14 by row
 //   softmax       against a running reference that moves only when a score
@@ -36,8 +36,8 @@
 namespace fm {
 namespace {
 
-constexpr int kWarps = 8;                // two to a scheduler: 255 registers each
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = 7;                // with the producer two to a scheduler: 255 registers each
+constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kDepth = 3;                // tiles of a warp in shared memory
 constexpr int kMaxCtas = 160;
 constexpr int kMaxRuns = kMaxCtas * kWarps;
@@ -74,7 +74,7 @@ template <int D>
 struct Smem {
   uint8_t kv[kWarps][kDepth][2][Layout<D>::kTile];  // 1024-byte aligned
   float scales[kWarps][kDepth][2][kBlocksPerPage];
-  uint64_t full[kWarps][kDepth];
+  uint64_t full[kWarps][kDepth], empty[kWarps][kDepth];
   int held[kWarps][kDepth];
   int64_t before[kThreads + 1];                     // units before each thread's sequences
   int abort;
@@ -450,69 +450,124 @@ FM_DEV float row_factor(const KvParams& p, int h, float m, float mv, float l) {
 }
 FM_DEV float row_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f; }
 
-// Brings a run's tiles one after the other, ahead of their use.
-template <int D, int NT>
-struct Loader {
-  const KvParams& p;
-  const CUtensorMap *k_map, *v_map;
-  Smem<D>& sh;
-  int warp, lane;
-  int64_t left;          // units of the run that have not been asked for
-  int b, item, page, part, entry;   // where the next tile is; entry: its page in the pool
-  int pages, items, tiles, low, row;  // row: the head's first in a page
-  bool none;
-  int stage;
+// Whether the phase with the given parity is complete, without a wait.
+FM_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
-  FM_DEV void enter(const Seq& s) {
-    pages = s.pages;
-    tiles = s.tiles;
-    items = s.tiles * p.n_k;
-    low = s.low;
-    none = s.none;
-    if (lane == 0 && p.window > 0 && (s.none ? s.start >= 0 : s.start + s.n - 1 >= (int64_t)p.R * kKvPage))
+// The producer: lane w brings the tiles of warp w's run, as they become free.
+template <int D, int NT>
+FM_DEV void bring_tiles(const KvParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, Smem<D>& sh, int64_t units, int runs,
+                        int share) {
+  using L = Layout<D>;
+  const int warp = threadIdx.x & 31;   // whose tiles the lane brings
+  const int run = warp * gridDim.x + blockIdx.x;
+  int64_t left = 0, local = 0;
+  int b = 0;
+  Seq s = {};
+  auto enter = [&]() {
+    s = sequence<NT>(p, b);
+    if (s.tiles > 0 && p.window > 0 && (s.none ? s.start >= 0 : s.start + s.n - 1 >= (int64_t)p.R * kKvPage))
       atomicOr(p.status, FM_DEV_PAGE_RANGE);
-  }
-  FM_DEV void look_up() { entry = none ? -1 : p.page_table[(int64_t)b * p.R + low + page]; }
-  FM_DEV void next() {
-    if (left == 0) return;
-    int at = entry;
-    if (at >= p.P) {
-      if (lane == 0) atomicOr(p.status, FM_DEV_PAGE_RANGE);
-      at = -1;
+  };
+  if (warp < kWarps && run < runs) {
+    const int64_t u0 = run_begin(units, run, runs);
+    left = run_begin(units, run + 1, runs) - u0;
+    if (left > 0) {
+      int lo = 0;
+      for (int hi = kThreads; hi - lo > 1;) {
+        const int mid = (lo + hi) / 2;
+        (sh.before[mid] <= u0 ? lo : hi) = mid;
+      }
+      b = lo * share;
+      local = u0 - sh.before[lo];
+      for (int64_t mine; local >= (mine = units_of<NT>(p, b)); ++b) local -= mine;
+      enter();
     }
-    if (lane == 0) {
+  }
+  int item = 0, page = 0, row = 0, entry = -1, part = 0, stage = 0;
+  uint32_t round = 0, issued = 0;
+  auto look_up = [&]() { entry = s.none ? -1 : p.page_table[(int64_t)b * p.R + s.low + page]; };
+  if (left > 0) {
+    item = (int)(local / s.pages);
+    page = (int)(local - (int64_t)item * s.pages);
+    row = item / s.tiles * kKvPage;
+    look_up();
+  }
+  uint64_t since = 0;
+  bool ok = true;
+#pragma unroll 1
+  for (uint32_t idle = 0; __any_sync(0xffffffffu, left > 0);) {
+    const bool ready = left > 0 && (issued < kDepth || mbar_test(&sh.empty[warp][stage], round ^ 1));
+    if (ready) {
+      int at = entry;
+      if (at >= p.P) {
+        atomicOr(p.status, FM_DEV_PAGE_RANGE);
+        at = -1;
+      }
       uint64_t* full = &sh.full[warp][stage];
       sh.held[warp][stage] = at >= 0;
       if (at >= 0) {
-        mbar_arrive_expect_tx(full, 2 * Layout<D>::kTile + 2 * kBlocksPerPage * 4);
-        const int y = row + part * Layout<D>::kKeys;
-        tma_load_3d(sh.kv[warp][stage][0], k_map, full, 0, y, at);
-        tma_load_3d(sh.kv[warp][stage][1], v_map, full, 0, y, at);
-        const int64_t s = at * p.scale_stride + row / kKvBlock;
-        bulk_load(sh.scales[warp][stage][0], p.k_scale + s, 16, full);
-        bulk_load(sh.scales[warp][stage][1], p.v_scale + s, 16, full);
+        mbar_arrive_expect_tx(full, 2 * L::kTile + 2 * kBlocksPerPage * 4);
+        const int y = row + part * L::kKeys;
+        tma_load_3d(sh.kv[warp][stage][0], &k_map, full, 0, y, at);
+        tma_load_3d(sh.kv[warp][stage][1], &v_map, full, 0, y, at);
+        const int64_t x = at * p.scale_stride + row / kKvBlock;
+        bulk_load(sh.scales[warp][stage][0], p.k_scale + x, 16, full);
+        bulk_load(sh.scales[warp][stage][1], p.v_scale + x, 16, full);
       } else {
         mbar_arrive(full);
       }
-    }
-    stage = stage + 1 == kDepth ? 0 : stage + 1;
-    if (++part < Layout<D>::kTiles) return;
-    part = 0;
-    --left;
-    if (++page == pages) {
-      page = 0;
-      if (++item == items && left > 0) {
-        item = 0;
-        Seq s;
-        do s = sequence<NT>(p, ++b);
-        while (s.tiles == 0);
-        enter(s);
+      ++issued;
+      stage = stage + 1 == kDepth ? 0 : stage + 1;
+      round ^= stage == 0;
+      if (++part == L::kTiles) {
+        part = 0;
+        --left;
+        if (++page == s.pages) {
+          page = 0;
+          if (++item == s.tiles * p.n_k && left > 0) {
+            item = 0;
+            do {
+              ++b;
+              enter();
+            } while (s.tiles == 0);
+          }
+          row = item / s.tiles * kKvPage;
+        }
+        if (left > 0) look_up();
       }
-      row = item / tiles * kKvPage;
     }
-    if (left > 0) look_up();
+    if (__any_sync(0xffffffffu, ready)) {
+      idle = 0;
+      continue;
+    }
+    __nanosleep(100);  // looking again at once would take issue slots from the warps that work
+    if ((++idle & 63) == 1) {  // a bounded wait, as wait_bar's
+      const uint64_t now = globaltimer();
+      if (idle == 1) since = now;
+      const bool late = now - since > FM_WAIT_LIMIT_NS;
+      if (late && *(volatile int*)&sh.abort == 0) atomicOr(p.status, FM_DEV_TIMEOUT);
+      if (late) *(volatile int*)&sh.abort = 1;
+      if (__any_sync(0xffffffffu, *(volatile int*)&sh.abort != 0)) {
+        ok = false;
+        break;
+      }
+    }
   }
-};
+  if (ok || warp >= kWarps) return;
+  // gave up: the copies in flight land before the CTA's memory is another's
+  for (uint32_t i = issued > kDepth ? issued - kDepth : 0; i < issued; ++i)
+    mbar_wait_drain(&sh.full[warp][i % kDepth], (i / kDepth) & 1);
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_constant__ CUtensorMap k_map,
@@ -527,7 +582,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
     tma_prefetch(&v_map);
     sh.abort = 0;
   }
-  if (lane < kDepth) mbar_init(&sh.full[warp][lane], 1);
+  if (warp < kWarps && lane < kDepth) {
+    mbar_init(&sh.full[warp][lane], 1);
+    mbar_init(&sh.empty[warp][lane], 1);
+  }
   fence_mbar_init();
   // programmatic dependent launch: what a kernel before wrote may be read from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -552,11 +610,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
     __syncthreads();
   }
   const int64_t units = sh.before[kThreads];
+  // an item's part costs a run as much as a page: no more runs than make four pages each, if the SMs have one
+  const int runs = (int)min((int64_t)p.runs, max(units / 4, (int64_t)gridDim.x));
+  if (warp == kWarps) {
+    bring_tiles<D, NT>(p, k_map, v_map, sh, units, runs, share);
+    return;
+  }
   // neighbouring runs go to different SMs
   const int run = warp * gridDim.x + blockIdx.x;
   if (lane == 0) p.part_item[run] = make_int4(-1, 0, 0, 0);
-  // an item's part costs a run as much as a page: no more runs than make four pages each, if the SMs have one
-  const int runs = (int)min((int64_t)p.runs, max(units / 4, (int64_t)gridDim.x));
   if (run >= runs) return;
   const int64_t u0 = run_begin(units, run, runs), u1 = run_begin(units, run + 1, runs);
   if (u0 >= u1) return;
@@ -587,14 +649,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
 
   Seq s = sequence<NT>(p, b);
   int item = (int)(local / s.pages), page0 = (int)(local - (int64_t)item * s.pages);
-  Loader<D, NT> load = {p, &k_map, &v_map, sh, warp, lane, u1 - u0, b, item, page0, 0, -1};
-  load.stage = 0;
-  load.enter(s);
-  load.row = item / s.tiles * kKvPage;
-  load.look_up();
-#pragma unroll 1
-  for (int i = 0; i < kDepth; ++i) load.next();
-
   Rows<D, NT> w;
   int stage = 0;
   uint32_t turn = 0;
@@ -629,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
         if (partial) fence_async_smem();  // the next tile comes through the other proxy
       }
       __syncwarp();
-      load.next();
+      if (lane == 0) mbar_arrive(&sh.empty[warp][stage]);
       stage = stage + 1 == kDepth ? 0 : stage + 1;
       turn ^= stage == 0;
     }
