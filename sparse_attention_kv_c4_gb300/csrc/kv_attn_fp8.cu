@@ -10,7 +10,7 @@
 // The work is the list of units (sequence, key head, row tile, page of 64 tokens), cut into
 // as many equal runs as there are warps, seven to an SM, whatever the sequences' lengths;
 // a warp works out its run from the offsets by itself, and a lane of the CTA's eighth warp brings its tiles
-// of 64 x 64 or 32 x 128 by TMA (three stages of 8 KB each, swizzled):
+// (a page of a head) by TMA (two or three stages each, swizzled):
 //   S^T = K Q^T   m16n8k16, 16 keys (one block of scales) x 8 rows, fp16 operands:
 //                 E4M3 is exact in fp16, queries are scaled to 2^14 by row
 //   softmax       against a running reference that moves only when a score
@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kWarps = 7;                // with the producer two to a scheduler: 255 registers each
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kDepth = 3;                // tiles of a warp in shared memory
+constexpr int kScan = 128;               // parts of the sequences whose units are counted
 constexpr int kMaxCtas = 160;
 constexpr int kMaxRuns = kMaxCtas * kWarps;
 constexpr int kRunsPerBlock = 8;        // of the join
@@ -48,10 +48,8 @@ constexpr float kSlack = 8.f;           // how far a score (in log2) may pass it
 
 template <int D>
 struct Layout {
-  static constexpr int kKeys = 4096 / D;     // keys of a tile: a page, or half of one
-  static constexpr int kTiles = kKvPage / kKeys;
-  static constexpr int kTile = 4096;         // bytes of keys, and of values
-  static constexpr int kBlocks = kKeys / kKvBlock;
+  static constexpr int kTile = kKvPage * D;          // bytes of a page and head's keys, and of its values
+  static constexpr int kDepth = D == 64 ? 3 : 2;     // tiles of a warp in shared memory
 };
 
 struct KvParams {
@@ -72,11 +70,12 @@ struct KvParams {
 
 template <int D>
 struct Smem {
+  static constexpr int kDepth = Layout<D>::kDepth;
   uint8_t kv[kWarps][kDepth][2][Layout<D>::kTile];  // 1024-byte aligned
   float scales[kWarps][kDepth][2][kBlocksPerPage];
   uint64_t full[kWarps][kDepth], empty[kWarps][kDepth];
   int held[kWarps][kDepth];
-  int64_t before[kThreads + 1];                     // units before each thread's sequences
+  int64_t before[kScan + 1];                        // units before each part's sequences
   int abort;
 };
 
@@ -257,13 +256,13 @@ FM_DEV void load_rows(const KvParams& p, const Seq& s, int head, int tile, Rows<
       for (int i = 0; i < 4; ++i) w.o[j][nt][i] = 0.f;
 }
 
-// Blocks of 16 keys from block `at` of a tile on, `Blocks` of them, whose scales are scale_at, ...  partial: some row does not see some key.
+// Blocks of 16 keys from block `at` of a page on, `Blocks` of them.  partial: some row does not see some key.
 template <int D, int NT, int Blocks>
-FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], int at, int scale_at, int tile_first,
-                       bool partial, Rows<D, NT>& w) {
+FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], int at, int page_first, bool partial,
+                       Rows<D, NT>& w) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const uint32_t k_smem = kv_smem + 16 * at * D, v_smem = k_smem + Layout<D>::kTile;  // 16 rows keep the swizzle's phase
-  const int first = tile_first + 16 * at;
+  const int first = page_first + 16 * at;
   float s[Blocks][NT][4];
 #pragma unroll
   for (int block = 0; block < Blocks; ++block) {
@@ -289,8 +288,8 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
   float ks[Blocks], vs[Blocks], log_vs[Blocks];
 #pragma unroll
   for (int block = 0; block < Blocks; ++block) {
-    ks[block] = scales[0][scale_at + block];
-    vs[block] = scales[1][scale_at + block];
+    ks[block] = scales[0][at + block];
+    vs[block] = scales[1][at + block];
     // a block that holds no key of any row may have any scale
     if (partial && (first + 16 * block > w.most || first + 16 * block + 15 < w.low_least)) vs[block] = 0.f;
     log_vs[block] = __log2f(vs[block]);
@@ -404,7 +403,7 @@ FM_DEV void clean_values(uint8_t* v, int first, Rows<D, NT>& w) {
   const int lane = threadIdx.x & 31, g = lane >> 2;
   bool bad = false;
 #pragma unroll 1
-  for (int i = lane; i < Layout<D>::kKeys * (D / 16); i += 32) {
+  for (int i = lane; i < kKvPage * (D / 16); i += 32) {
     const int key = first + i / (D / 16);
     uint4* cell = reinterpret_cast<uint4*>(v + 16 * i);  // some chunk of the key's row: the swizzle stays within it
     if (key > w.most || key < w.low_least) {
@@ -419,7 +418,7 @@ FM_DEV void clean_values(uint8_t* v, int first, Rows<D, NT>& w) {
   __syncwarp();
   if (__any_sync(0xffffffffu, bad)) {
 #pragma unroll 1
-    for (int key = 0; key < Layout<D>::kKeys; ++key) {
+    for (int key = 0; key < kKvPage; ++key) {
       const int at = first + key;
       if (at > w.most || at < w.low_least || (at <= w.least && at >= w.low_most)) continue;
 #pragma unroll
@@ -468,6 +467,7 @@ template <int D, int NT>
 FM_DEV void bring_tiles(const KvParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, Smem<D>& sh, int64_t units, int runs,
                         int share) {
   using L = Layout<D>;
+  constexpr int kDepth = L::kDepth;
   const int warp = threadIdx.x & 31;   // whose tiles the lane brings
   const int run = warp * gridDim.x + blockIdx.x;
   int64_t left = 0, local = 0;
@@ -483,7 +483,7 @@ FM_DEV void bring_tiles(const KvParams& p, const CUtensorMap& k_map, const CUten
     left = run_begin(units, run + 1, runs) - u0;
     if (left > 0) {
       int lo = 0;
-      for (int hi = kThreads; hi - lo > 1;) {
+      for (int hi = kScan; hi - lo > 1;) {
         const int mid = (lo + hi) / 2;
         (sh.before[mid] <= u0 ? lo : hi) = mid;
       }
@@ -493,7 +493,7 @@ FM_DEV void bring_tiles(const KvParams& p, const CUtensorMap& k_map, const CUten
       enter();
     }
   }
-  int item = 0, page = 0, row = 0, entry = -1, part = 0, stage = 0;
+  int item = 0, page = 0, row = 0, entry = -1, stage = 0;
   uint32_t round = 0, issued = 0;
   auto look_up = [&]() { entry = s.none ? -1 : p.page_table[(int64_t)b * p.R + s.low + page]; };
   if (left > 0) {
@@ -517,9 +517,8 @@ FM_DEV void bring_tiles(const KvParams& p, const CUtensorMap& k_map, const CUten
       sh.held[warp][stage] = at >= 0;
       if (at >= 0) {
         mbar_arrive_expect_tx(full, 2 * L::kTile + 2 * kBlocksPerPage * 4);
-        const int y = row + part * L::kKeys;
-        tma_load_3d(sh.kv[warp][stage][0], &k_map, full, 0, y, at);
-        tma_load_3d(sh.kv[warp][stage][1], &v_map, full, 0, y, at);
+        tma_load_3d(sh.kv[warp][stage][0], &k_map, full, 0, row, at);
+        tma_load_3d(sh.kv[warp][stage][1], &v_map, full, 0, row, at);
         const int64_t x = at * p.scale_stride + row / kKvBlock;
         bulk_load(sh.scales[warp][stage][0], p.k_scale + x, 16, full);
         bulk_load(sh.scales[warp][stage][1], p.v_scale + x, 16, full);
@@ -529,22 +528,19 @@ FM_DEV void bring_tiles(const KvParams& p, const CUtensorMap& k_map, const CUten
       ++issued;
       stage = stage + 1 == kDepth ? 0 : stage + 1;
       round ^= stage == 0;
-      if (++part == L::kTiles) {
-        part = 0;
-        --left;
-        if (++page == s.pages) {
-          page = 0;
-          if (++item == s.tiles * p.n_k && left > 0) {
-            item = 0;
-            do {
-              ++b;
-              enter();
-            } while (s.tiles == 0);
-          }
-          row = item / s.tiles * kKvPage;
+      --left;
+      if (++page == s.pages) {
+        page = 0;
+        if (++item == s.tiles * p.n_k && left > 0) {
+          item = 0;
+          do {
+            ++b;
+            enter();
+          } while (s.tiles == 0);
         }
-        if (left > 0) look_up();
+        row = item / s.tiles * kKvPage;
       }
+      if (left > 0) look_up();
     }
     if (__any_sync(0xffffffffu, ready)) {
       idle = 0;
@@ -573,7 +569,7 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_constant__ CUtensorMap k_map,
                                                               const __grid_constant__ CUtensorMap v_map,
                                                               const __grid_constant__ KvParams p) {
-  using L = Layout<D>;
+  constexpr int kDepth = Layout<D>::kDepth;
   extern __shared__ __align__(1024) uint8_t raw_smem[];
   Smem<D>& sh = *reinterpret_cast<Smem<D>*>(raw_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -591,9 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // units before each thread's share of the sequences
-  const int share = (p.B + kThreads - 1) / kThreads;
-  {
+  // units before each of kScan shares of the sequences
+  const int share = (p.B + kScan - 1) / kScan;
+  if (warp < kScan / 32) {
     int64_t mine = 0;
     for (int i = 0; i < share && tid * (int64_t)share + i < p.B; ++i) mine += units_of<NT>(p, tid * share + i);
     int64_t incl = mine;
@@ -602,14 +598,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
       if (lane >= o) incl += x;
     }
     if (lane == 31) sh.before[warp] = incl;
-    __syncthreads();
+    named_bar_sync(1, kScan);
     for (int i = 0; i < warp; ++i) incl += sh.before[i];
-    __syncthreads();
+    named_bar_sync(1, kScan);
     sh.before[tid + 1] = incl;
     if (tid == 0) sh.before[0] = 0;
-    __syncthreads();
   }
-  const int64_t units = sh.before[kThreads];
+  __syncthreads();
+  const int64_t units = sh.before[kScan];
   // an item's part costs a run as much as a page: no more runs than make four pages each, if the SMs have one
   const int runs = (int)min((int64_t)p.runs, max(units / 4, (int64_t)gridDim.x));
   if (warp == kWarps) {
@@ -624,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
   if (u0 >= u1) return;
   // the sequence that holds the run's first unit
   int lo = 0;
-  for (int hi = kThreads; hi - lo > 1;) {
+  for (int hi = kScan; hi - lo > 1;) {
     const int mid = (lo + hi) / 2;
     (sh.before[mid] <= u0 ? lo : hi) = mid;
   }
@@ -667,19 +663,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
     load_rows<D, NT>(p, s, head, tile, w);
     const int first0 = (s.low + page0) * kKvPage;
 #pragma unroll 1
-    for (int i = 0; i < pages * L::kTiles; ++i) {
+    for (int i = 0; i < pages; ++i) {
       ok = wait_bar(&sh.full[warp][stage], turn, &sh.abort, p.status);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      const int first = first0 + i * L::kKeys;
-      if (sh.held[warp][stage] && first <= w.most && first + L::kKeys > w.low_least) {
-        const bool partial = first + L::kKeys - 1 > w.least || first < w.low_most;
+      const int first = first0 + i * kKvPage;
+      if (sh.held[warp][stage] && first <= w.most && first + kKvPage > w.low_least) {
+        const bool partial = first + kKvPage - 1 > w.least || first < w.low_most;
         if (partial) clean_values<D, NT>(sh.kv[warp][stage][1], first, w);
         // all keys at once where registers allow, else in halves
-        constexpr int kBlocks = D * NT <= 128 ? L::kBlocks : 2;
+        constexpr int kBlocks = D * NT < 256 || (D == 128 && NT == 2) ? 4 : 2;
 #pragma unroll 1
-        for (int block = 0; block < L::kBlocks; block += kBlocks)
-          key_blocks<D, NT, kBlocks>(smem_u32(sh.kv[warp][stage][0]), sh.scales[warp][stage], block,
-                                     (i % L::kTiles) * L::kBlocks + block, first, partial, w);
+        for (int block = 0; block < kBlocksPerPage; block += kBlocks)
+          key_blocks<D, NT, kBlocks>(smem_u32(sh.kv[warp][stage][0]), sh.scales[warp][stage], block, first, partial, w);
         if (partial) fence_async_smem();  // the next tile comes through the other proxy
       }
       __syncwarp();
@@ -897,7 +892,7 @@ FM_API fm_status fm_kv_attn_fp8(const fm_kv_attn_fp8_args* a) {
   CUtensorMap k_map, v_map;
   const uint64_t dims[3] = {(uint64_t)a->d, (uint64_t)a->n_k * kKvPage, a->P > 0 ? (uint64_t)a->P : 1};
   const uint64_t strides[2] = {(uint64_t)a->d, (uint64_t)a->page_stride};
-  const uint32_t box[3] = {(uint32_t)D, (uint32_t)(4096 / D), 1};
+  const uint32_t box[3] = {(uint32_t)D, kKvPage, 1};
   const CUtensorMapSwizzle swizzle = D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   // without pages nothing is read: any address will do for the maps
   const void *k_base = a->P > 0 ? (const void*)a->k_pool : a->q, *v_base = a->P > 0 ? (const void*)a->v_pool : a->q;
