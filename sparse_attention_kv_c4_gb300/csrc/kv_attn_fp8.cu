@@ -41,7 +41,7 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kScan = 128;               // parts of the sequences whose units are counted
 constexpr int kMaxCtas = 160;
 constexpr int kMaxRuns = kMaxCtas * kWarps;
-constexpr int kRunsPerBlock = 8;        // of the join
+constexpr int kRunsPerBlock = 4;        // of the join
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLow = -1e30f;          // below every score
 constexpr float kSlack = 8.f;           // how far a score (in log2) may pass its reference
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
     }
 }
 
-// Joins the parts of the items that span runs: block (x, row) those that runs 8 x, ... , 8 x + 7 begin.  Eight
+// Joins the parts of the items that span runs: block (x, row) those that runs 4 x, ... , 4 x + 3 begin.  Eight
 // groups of threads take an item's parts in turn, four elements to a thread; their sums are added in order.
 template <int D, int NT>
 __global__ void __launch_bounds__(2 * D) kv_join_kernel(const __grid_constant__ KvParams p) {
@@ -749,13 +749,18 @@ __global__ void __launch_bounds__(2 * D) kv_join_kernel(const __grid_constant__ 
   for (uint32_t todo = __ballot_sync(0xffffffffu, follow); todo != 0; todo &= todo - 1) {
     const int run = run0 + __ffs(todo) - 1;
     const int4 item = p.part_item[run];
+    auto part = [&](int i) { return ((int64_t)2 * (run + i) + (i == 0)) * 8 * NT + row; };
+    // one round of loads: what most items need is under way at once
+    float4 mine = make_float4(kLow, kLow, 0.f, 0.f), x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (lane <= item.w) mine = p.part_ml[part(lane)];
+    if (group <= item.w) x = *reinterpret_cast<const float4*>(p.part_o + part(group) * D + e);
+    const float x_mv = group <= item.w ? p.part_ml[part(group)].y : kLow;
     const int begin = p.cu ? offset_at(p.cu, item.x, p.T) : item.x;
     const int n = p.cu ? offset_at(p.cu, item.x + 1, p.T) - begin : 1;
     const int r = item.z * 8 * NT + row;
     if (r >= n * p.G) continue;  // the whole block
-    auto part = [&](int i) { return ((int64_t)2 * (run + i) + (i == 0)) * 8 * NT + row; };
-    float m = kLow, mv = kLow;
-    for (int i = lane; i <= item.w; i += 32) {
+    float m = mine.x, mv = mine.y;
+    for (int i = lane + 32; i <= item.w; i += 32) {
       const float4 s = p.part_ml[part(i)];
       m = fmaxf(m, s.x);
       mv = fmaxf(mv, s.y);
@@ -765,16 +770,17 @@ __global__ void __launch_bounds__(2 * D) kv_join_kernel(const __grid_constant__ 
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
     }
-    float l = 0.f;
-    for (int i = lane; i <= item.w; i += 32) {
+    float l = mine.z * exp2_fast(mine.x - m);
+    for (int i = lane + 32; i <= item.w; i += 32) {
       const float4 s = p.part_ml[part(i)];
       l += s.z * exp2_fast(s.x - m);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float f0 = exp2_fast(x_mv - mv);
+    x = make_float4(x.x * f0, x.y * f0, x.z * f0, x.w * f0);
 #pragma unroll 8
-    for (int i = group; i <= item.w; i += kGroups) {
+    for (int i = group + kGroups; i <= item.w; i += kGroups) {
       const float f = exp2_fast(p.part_ml[part(i)].y - mv);
       const float4 y = *reinterpret_cast<const float4*>(p.part_o + part(i) * D + e);
       x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
