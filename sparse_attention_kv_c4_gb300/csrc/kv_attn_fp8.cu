@@ -815,6 +815,12 @@ int row_eights(int64_t rows, int d) {
   return d <= 64 && need == 3 ? 4 : (int)need;
 }
 
+// The most that row_eights gives for up to that many rows.
+int most_eights(int64_t rows, int d) {
+  const int64_t eights = (rows + 7) / 8;
+  return eights >= 3 ? (d <= 64 ? 4 : 3) : eights < 1 ? 1 : (int)eights;
+}
+
 size_t workspace_bytes(int eights, int d) {
   return (size_t)kMaxRuns * (sizeof(int4) + 2 * 8 * (size_t)eights * (sizeof(float4) + (d <= 64 ? 64 : 128) * sizeof(float)));
 }
@@ -864,8 +870,7 @@ using namespace fm;
 
 FM_API size_t fm_kv_attn_fp8_workspace(int T, int n_h, int n_k, int d) {
   if (T < 0 || bad_heads(n_h, n_k, d)) return 0;
-  const int64_t most = d <= 64 ? 4 : 3, eights = ((int64_t)T * (n_h / n_k) + 7) / 8;
-  return workspace_bytes((int)(eights < most ? eights < 1 ? 1 : eights : most), d);
+  return workspace_bytes(most_eights((int64_t)T * (n_h / n_k), d), d);
 }
 
 FM_API fm_status fm_kv_attn_fp8(const fm_kv_attn_fp8_args* a) {

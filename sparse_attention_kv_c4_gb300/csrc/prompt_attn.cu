@@ -42,7 +42,7 @@ constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLow = -1e30f;   // below every score
 constexpr float kSlack = 8.f;    // how far a score (in log2) may pass its reference for long,
-constexpr float kFar = 64.f;     // and at all
+constexpr float kFar = 16.f;     // and at all: weights of up to 2^16 leave values room in fp32
 constexpr int kMaxEdge = 16;     // tiles of an item that the mask cuts: at most 2 (256 + 127) / 128 + 2
 constexpr uint32_t kBIsMnMajor = 1u << 16;
 

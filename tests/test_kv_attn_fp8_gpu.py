@@ -232,6 +232,28 @@ def test_many_pages_to_each_sm(torch_dev, H, K, d, lens, starts, window):
         assert (np.abs(got_lse[rows] - want_lse) <= ltol).all() and (np.abs(got[rows] - want) <= tol).all(), b
 
 
+@pytest.mark.parametrize("T,H,K,d", [(1, 24, 1, 64), (3, 8, 1, 48), (1, 17, 1, 64), (1, 24, 1, 128), (2, 9, 1, 128), (1, 128, 1, 64), (5, 5, 1, 64)])
+def test_the_workspace_holds_what_is_written(torch_dev, T, H, K, d):
+    """Rows that do not fill their eights, split over every SM: nothing is written behind the workspace's end."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    rng = np.random.default_rng(T + H)
+    starts = [9000] * T
+    table, codes, scales, k, v, size, scale_of, held = make(rng, [1] * T, starts, H, K, d, quick=True)
+    need = fm.fm_kv_attn_fp8_workspace(T, H, K, d)
+    ws = torch.full((need + (1 << 24),), 0xA5, dtype=torch.uint8, device=dev)
+    cd, sd = up(torch, dev, codes), up(torch, dev, scales)
+    q = ref.bf16(rng.standard_normal((T, H, d)))
+    out = torch.zeros((T, H, d), dtype=torch.int16, device=dev)
+    fm.fm_kv_attn_fp8(up(torch, dev, q.view(np.int16)), cd[0][:, 0], cd[1][:, 0], sd[0][:, 0], sd[1][:, 0], up(torch, dev, table),
+                      torch.tensor(starts, device=dev), out, workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert (ws[need:] == 0xA5).all().item() and fm.fm_device_status(reset=True) == 0
+    got = ref.f64(out.cpu().numpy().view(np.uint16))
+    want, _, tol, _ = gr.attend(ref.f64(q)[:1, :4], k[0], v[0], 9000, FOREVER, None, d ** -0.5, held[0], gr.HALF_FP16, (size[0], scale_of[0]))
+    assert (np.abs(got[:1, :4] - want) <= tol).all()
+
+
 def test_two_calls_at_once_graph_and_same_results(torch_dev):
     """The result is the same bits eager, replayed on another stream, and beside another call with a workspace
     of its own; out may be q."""

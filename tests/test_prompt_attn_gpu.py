@@ -101,6 +101,19 @@ def test_scores_that_rise_by_thousands(torch_dev):
     assert (np.abs(ref.f64(got) - want) <= tol).all() and (np.abs(lse - want_lse) <= ltol).all()
 
 
+def test_large_values_under_rising_scores(torch_dev):
+    """Values of 10^30 while the scores rise from key to key: no product leaves fp32's range."""
+    torch, dev = torch_dev
+    rng = np.random.default_rng(15)
+    n, H, K, d = 500, 4, 2, 128
+    q = ref.bf16(np.abs(rng.standard_normal((n, H, d))))
+    k = ref.bf16(np.abs(rng.standard_normal((n, K, d))) * np.linspace(0.05, 6, n)[:, None, None])
+    v = ref.bf16(1e30 * rng.standard_normal((n, K, d)))
+    got, lse, cu, _ = call(torch, dev, q, k, v, [n], [0], None, None, None, 0)
+    want, want_lse, tol, ltol = gr.attend(ref.f64(q), ref.f64(k), ref.f64(v), 0, FOREVER, None, d ** -0.5)
+    assert (np.abs(ref.f64(got) - want) <= tol).all() and (np.abs(lse - want_lse) <= ltol).all()
+
+
 @pytest.mark.parametrize("G", [1, 3, 8])
 def test_infinities_and_nan_reach_only_the_queries_that_see_them(torch_dev, G):
     """A token's bad values and keys show in its own and later rows of its sequence, within the window, and nowhere else."""
