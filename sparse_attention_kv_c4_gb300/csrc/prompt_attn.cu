@@ -14,7 +14,7 @@
 //   softmax    (warps 0-3, 4-7)  one row to a thread: scores from TMEM, a running reference
 //              that moves only after a score has passed it by 2^8 (O is scaled in TMEM then), weights in
 //              bf16 back to TMEM.  Sums are taken of the weights before they are rounded
-//   checker    (warp 11)  tiles of keys that some rows do not see: an infinity or NaN among the
+//   sweeper    (warp 11)  tiles of keys that some rows do not see: an infinity or NaN among the
 //              values would reach those rows as 0 * inf, so it is zeroed in shared memory and added
 //              by the epilogue to the rows that do see it
 // TMEM: S 2 x 128 columns, O 2 x D, P 2 x 64 (at D = 128 in S's place).
@@ -557,12 +557,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     mbar_init(&sh.claimed, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_empty[i], 11);  // softmax warps, issuers and the checker
+      mbar_init(&sh.item_empty[i], 11);  // softmax warps, issuers and the sweeper
     }
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.ready[i], 1);
-      mbar_init(&sh.empty[i], 3);  // both row tiles and the checker
+      mbar_init(&sh.empty[i], 3);  // both row tiles and the sweeper
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     } else if (warp == 9 || warp == 10) {
       issue_products<D>(p, sh, uniform(warp - 9));
     } else {
-      // ------------------------------------------------------------ checker
+      // ------------------------------------------------------------ sweeper
       // Every stage of the ring passes through its hands, keys too, so that its barriers keep step
       // with the ring's.
       auto wait = [&](uint64_t* bar, uint32_t parity) {
