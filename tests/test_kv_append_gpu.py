@@ -22,11 +22,15 @@ def up(torch, dev, a):
 
 
 def tables(rng, lens, starts, extra=2):
-    """A page table in a random order with room behind each sequence's end, and the number of pages."""
-    B = len(lens)
+    """A page table that holds, in a random order, the pages from each sequence's first new token on, with room behind
+    its end, and the number of pages."""
     R = max((s + n + 63) // 64 for n, s in zip(lens, starts)) + 1
-    P = B * R + extra
-    return rng.permutation(P)[:B * R].reshape(B, R).astype(np.int32), P
+    table, at = np.full((len(lens), R), -1, np.int32), 0
+    for b, s in enumerate(starts):
+        table[b, s // 64:] = np.arange(at, at + R - s // 64)
+        at += R - s // 64
+    order = rng.permutation(at + extra).astype(np.int32)
+    return np.where(table < 0, -1, order[table]), at + extra
 
 
 def check_pool(got, before, want, written, exact, size, what):
