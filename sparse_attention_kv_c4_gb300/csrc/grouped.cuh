@@ -4,6 +4,8 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "fm_common.cuh"
 #include "fm_internal.h"
 
@@ -91,6 +93,27 @@ inline const char* bad_cache(const void* k_pool, const void* v_pool, const void*
     return "pools and scales must be 16-byte aligned";
   if ((B > 0 && R > 0 && !table) || !aligned(table, 4)) return "page_table is NULL or misaligned";
   return nullptr;
+}
+
+// Launches a kernel that needs `smem` bytes of shared memory, which has to be said once in a device's context
+// (1.3 us a time).  `said` has a bit for each device where it was; a launch that is refused all the same (a
+// reset has ended that context) says it again.
+template <class... Params, class... Args>
+cudaError_t launch_with_smem(std::atomic<uint64_t>& said, int smem, const cudaLaunchConfig_t& cfg, void (*kernel)(Params...),
+                             const Args&... args) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  for (bool again = dev < 64 && (said.load() >> dev & 1) != 0;; again = false) {
+    if (!again) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) said.fetch_or(uint64_t(1) << dev);
+    }
+    e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaErrorInvalidValue || !again) return e;
+    cudaGetLastError();
+  }
 }
 
 }  // namespace fm

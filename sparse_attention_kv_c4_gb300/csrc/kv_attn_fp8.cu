@@ -30,8 +30,6 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include <atomic>
-
 #include "grouped.cuh"
 
 #define FM_API extern "C" __attribute__((visibility("default")))
@@ -832,15 +830,7 @@ cudaError_t launch(KvParams& p, const CUtensorMap& k_map, const CUtensorMap& v_m
   p.part_item = reinterpret_cast<int4*>(p.part_ml + (size_t)kMaxRuns * 2 * 8 * NT);
   static_assert(sizeof(Smem<D>) <= 227 * 1024, "shared memory of an SM");
   const int smem = (int)sizeof(Smem<D>);
-  static std::atomic<uint64_t> prepared{0};  // devices whose kernel has its shared memory
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(prepared.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(kv_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) prepared.fetch_or(uint64_t(1) << dev);
-  }
+  static std::atomic<uint64_t> said{0};
   const int64_t most = (int64_t)p.T * p.n_h * (p.R > 0 ? p.R : 1);  // units
   int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   if (most < ctas) ctas = (int)most;
@@ -855,7 +845,8 @@ cudaError_t launch(KvParams& p, const CUtensorMap& k_map, const CUtensorMap& v_m
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, NT>, k_map, v_map, (const KvParams)p)) != cudaSuccess) return e;
+  const cudaError_t e = launch_with_smem(said, smem, cfg, kv_attn_kernel<D, NT>, k_map, v_map, p);
+  if (e != cudaSuccess) return e;
   if (p.R <= 1) return cudaSuccess;  // items of one page are one run's
   cfg.gridDim = dim3((unsigned)((p.runs + kRunsPerBlock - 1) / kRunsPerBlock), 8 * NT);
   cfg.blockDim = dim3(2 * D);

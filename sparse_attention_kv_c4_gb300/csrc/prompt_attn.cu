@@ -25,8 +25,6 @@
 // Measured, calls queued on a stream, inputs in rotation: 8192 tokens x 32 heads x 128 391 us (1.41 PFLOP/s,
 // 75% of a library product's burst rate), 4 x up to 4096 x 32 x 64 in a window of 1021 168 us, 2935 tokens of
 // five prompts x 20 x 96 25 us, 37 tokens 8 us.
-#include <atomic>
-
 #include "grouped.cuh"
 
 #define FM_API extern "C" __attribute__((visibility("default")))
@@ -728,15 +726,7 @@ cudaError_t launch(const PromptParams& p, const CUtensorMap& q_map, const CUtens
                    cudaStream_t stream) {
   constexpr int smem = (int)sizeof(Smem<D>);
   static_assert(smem <= 227 * 1024, "shared memory of an SM");
-  static std::atomic<uint64_t> prepared{0};  // devices whose kernel has its shared memory
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(prepared.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(prompt_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) prepared.fetch_or(uint64_t(1) << dev);
-  }
+  static std::atomic<uint64_t> said{0};
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -747,7 +737,7 @@ cudaError_t launch(const PromptParams& p, const CUtensorMap& q_map, const CUtens
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prompt_attn_kernel<D>, q_map, k_map, v_map, p);
+  return launch_with_smem(said, smem, cfg, prompt_attn_kernel<D>, q_map, k_map, v_map, p);
 }
 
 }  // namespace
