@@ -615,7 +615,7 @@ fm_status fm_csa_attn_packed(const fm_csa_attn_args* args);
  * multiple of 16, 16 <= d <= 128.  Sequences are packed: sequence b has the
  * tokens cu[b] .. cu[b + 1] - 1 of the call's T; cu is non-decreasing with
  * cu[0] = 0 and cu[B] <= T.  Rows behind the last sequence (a padded batch) are
- * neither read nor written.  An offset outside 0 .. T is read as the nearer of the
+ * not written and, like the other sequences' rows, have no part in a sequence's result.  An offset outside 0 .. T is read as the nearer of the
  * two, and a sequence whose end is before its begin as empty.
  *
  * The cache: pages of 64 tokens, k_pool and v_pool [P, n_k, 64, d] E4M3 codes and
@@ -752,7 +752,8 @@ fm_status fm_kv_attn_fp8(const fm_kv_attn_fp8_args* args);
  *   out     [T, n_h, d] bf16 dense;  lse_out [T, n_h] fp32 or NULL
  *   q, k, v, out 16-byte aligned
  * Scores, softmax statistics and sums are fp32; the softmax weights are rounded to
- * bf16 for the tensor cores' second product.  The result does not depend on scheduling.
+ * bf16 for the tensor cores' second product.  A sequence's bits depend neither on scheduling
+ * nor on the call's other sequences.
  * Errors: FM_ERR_INVALID_ARG, FM_ERR_CUDA.
  */
 typedef struct fm_prompt_attn_args {

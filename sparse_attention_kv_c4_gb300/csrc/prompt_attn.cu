@@ -278,8 +278,9 @@ FM_DEV bool softmax_item(const PromptParams& p, Smem<D>& sh, int slot, uint32_t 
     const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
     // The reference moves before this tile's weights where they would leave fp32's range, and after
     // them where they are merely large: floating point loses nothing by it, and O is not
-    // waited for.
-    const bool must = __any_sync(0xffffffffu, most > m + kFar);
+    // waited for.  The tile's other rows have no vote: the next sequence's, what lies behind the last, or what shared
+    // memory held where the group's tokens do not fill 128 rows.
+    const bool must = __any_sync(0xffffffffu, live && most > m + kFar);
     if (must || behind) {
       const float next = must ? fmaxf(m, most) : fmaxf(m, last_most);
       const float keep = exp2_fast(m - next);
@@ -301,7 +302,7 @@ FM_DEV bool softmax_item(const PromptParams& p, Smem<D>& sh, int slot, uint32_t 
         }
       }
     }
-    behind = __any_sync(0xffffffffu, most > m + kSlack);
+    behind = __any_sync(0xffffffffu, live && most > m + kSlack);
     last_most = most;
     const float2 cc = make_float2(c, c), mm = make_float2(-m, -m);
     float2 sums[4] = {l, make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};

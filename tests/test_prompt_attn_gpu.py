@@ -183,3 +183,36 @@ def test_graph_and_streams_give_the_same_bits(torch_dev):
         torch.cuda.synchronize()
         assert (out.view(torch.int16) == want.view(torch.int16)).all() and (other.view(torch.int16) == want.view(torch.int16)).all()
     assert fm.fm_device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("G,d", [(3, 64), (5, 64), (5, 128), (7, 128), (9, 64), (24, 128)])
+def test_other_rows_of_a_tile_have_no_part_in_a_sequences_bits(torch_dev, G, d):
+    """A sequence alone, before another one of large queries, before rows behind the last sequence, and after a call that left
+    large numbers in shared memory: the same bits."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    K, n, past, other = 2, 50, 700, 77
+    H, rng = K * G, np.random.default_rng(G + d)
+    q, k, v = (up(torch, dev, ref.bf16(rng.standard_normal(s)).view(np.int16)) for s in ((n, H, d), (n + past, K, d), (n + past, K, d)))
+    large, zero = up(torch, dev, ref.bf16(60 * rng.standard_normal((other, H, d))).view(np.int16)), torch.zeros((other, H, d), dtype=torch.int16, device=dev)
+    full = [up(torch, dev, ref.bf16(60 * rng.standard_normal((38912, 1, d))).view(np.int16)), torch.zeros((38912, 1, d), dtype=torch.int16, device=dev)]
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)
+    kv = torch.zeros((other, K, d), dtype=torch.int16, device=dev)
+    results = []
+    for behind in (None, large, zero):
+        for sequences in ((1,) if behind is None else (1, 2)):
+            for before in full:  # a tile of 128 tokens of one head: every row of Q's shared memory
+                fm.fm_prompt_attn(before, full[1][:128], full[1][:128], torch.empty_like(before), cu_q=i32(0, 38912), cu_k=i32(0, 128), window=1)
+                qq = q if behind is None else torch.cat([q, behind])
+                kk, vv = (x if behind is None else torch.cat([x, kv]) for x in (k, v))
+                ends = ((0, n), (0, n + past)) if sequences == 1 else ((0, n, n + other), (0, n + past, n + past + other))
+                out, lse = torch.empty_like(qq), torch.empty(qq.shape[:2], device=dev)
+                fm.fm_prompt_attn(qq, kk, vv, out, cu_q=i32(*ends[0]), cu_k=i32(*ends[1]), lse_out=lse)
+                results.append((out[:n].clone(), lse[:n].clone()))
+    torch.cuda.synchronize()
+    assert fm.fm_device_status(reset=True) == 0
+    for out, lse in results[1:]:
+        assert (out == results[0][0]).all().item() and (lse == results[0][1]).all().item()
+    want, _, tol, _ = gr.attend(ref.f64(q.cpu().numpy().view(np.uint16)), ref.f64(k.cpu().numpy().view(np.uint16)),
+                                ref.f64(v.cpu().numpy().view(np.uint16)), past, FOREVER, None, d ** -0.5)
+    assert (np.abs(ref.f64(results[0][0].cpu().numpy().view(np.uint16)) - want) <= tol).all()
