@@ -703,9 +703,10 @@ fm_status fm_kv_append_fp8(const fm_kv_append_fp8_args* args);
  *   workspace  >= fm_kv_attn_fp8_workspace(T, n_h, n_k, d) bytes, 256-byte aligned;
  *              calls that overlap on the GPU need one each
  *   q, out 16-byte aligned
- * Scores, softmax statistics and sums are fp32; queries and softmax weights are fp16
- * operands, scaled by powers of two so that no row leaves fp16's range.  The result does
- * not depend on scheduling.
+ * Scores, softmax statistics and sums are fp32; queries and softmax weights times the values' scales are fp16
+ * operands.  Queries are scaled by their row's largest; a weight times scale is off by 2^-11 of itself, or by 2^-22 of the
+ * largest of its page of 64 tokens if that is more (other pages' weights, however large, cost it nothing).
+ * The result does not depend on scheduling.
  * Errors: FM_ERR_INVALID_ARG, FM_ERR_WORKSPACE, FM_ERR_CUDA.
  */
 typedef struct fm_kv_attn_fp8_args {

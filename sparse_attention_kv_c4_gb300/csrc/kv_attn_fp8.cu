@@ -16,7 +16,7 @@
 //   softmax       against a running reference that moves only when a score
 //                 passes it by 2^8: most tiles need no reduction over lanes
 //   O^T += V^T P^T  the weights times the block's scale of V in fp16, kept in its range by
-//                 a reference of their own (the largest weight times scale)
+//                 a reference of their own, which follows the tiles' largest weight times scale up and down
 // The transposed products take rows in eights, and their operands come from the
 // cache's rows as they lie: a lane's 16 bytes of a key are four steps of K16 (the order of
 // the contraction is free), ldmatrix transposes V by pairs of bytes.  mma.sync, not tcgen05:
@@ -26,7 +26,7 @@
 // of 1K to 32K took 209 us where 30 of 17K took 164.)
 // Measured, calls queued on a stream, inputs in rotation: 30 tokens x 64 heads over 1K to 32K cells of 8 x 128
 // 173 us (6.0 TB/s; 161 us the first kernel, 96% of the measured copy rate), one token x 32 heads over 1M cells of
-// 4 x 128 177 us, 8 x 5 drafted tokens x 40 heads over 8191 cells of 8 x 64 39 us, 37 cells 10 us.
+// 4 x 128 177 us, 8 x 5 drafted tokens x 40 heads over 8191 cells of 8 x 64 42 us, 37 cells 10 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -46,6 +46,12 @@ constexpr int kRunsPerBlock = 4;        // of the join
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLow = -1e30f;          // below every score
 constexpr float kSlack = 8.f;           // how far a score (in log2) may pass its reference
+// Weights times V's scale go to fp16 as 2^(x - rv).  A reference rv starts 11 to 12 below a tile's largest x and moves,
+// up or down and by whole numbers, when a tile's largest weight passes 2^15 (fp16 ends at 65504) or stays below 2^-3: each
+// is then off by 2^-11 of itself or 2^-22 of its tile's largest (half of fp16's smallest step).  (With a reference at the largest of all tiles, a
+// key e^16 over the others whose value was zero left them to fp16's subnormals: 12% off.)  O, in fp32, is in units of
+// 2^rv; a reference goes down no further than leaves O below 2^kTop.
+constexpr float kLead = 11.f, kMost = 15.f, kLeast = -3.f, kTop = 100.f;
 
 template <int D>
 struct Layout {
@@ -61,7 +67,7 @@ struct KvParams {
   uint16_t* out;
   float* lse;
   float* part_o;      // [2 runs][rows][D] unnormalised outputs
-  float4* part_ml;    // [2 runs][rows] (reference of scores, of weights times scales, sum)
+  float4* part_ml;    // [2 runs][rows] (reference of scores, of weights times V's scales, sum)
   int4* part_item;    // [runs] (sequence, head, row tile, runs that follow) of the item that a run begins and does not end
   int64_t q_stride_t, scale_stride, window;
   int T, n_h, n_k, d, G, P, B, R, runs;
@@ -179,7 +185,7 @@ struct Rows {
   uint32_t q[D / 16][NT][2];    // B fragments: row g of each eight, elements of the lane's chunks
   float f[NT][2];               // columns 2c, 2c + 1: factor from q . code to scores in log2 (times K's scale)
   int pos[NT][2], low[NT][2];   // the last and the first position that they see (last below first: no row)
-  float m[NT][2], mv[NT][2], l[NT][2];
+  float m[NT][2], rv[NT][2], l[NT][2];
   float o[D / 16][NT][4];       // (d = 16 j + 2 g, column 2c), (.., 2c + 1), (d + 1, 2c), (d + 1, 2c + 1)
   int least, most, low_least, low_most;  // of the tile's first and last row
 };
@@ -245,7 +251,7 @@ FM_DEV void load_rows(const KvParams& p, const Seq& s, int head, int tile, Rows<
       const int row = row0 + 8 * nt + 2 * c + i;
       w.pos[nt][i] = row < rows ? last_of(row) : -1;
       w.low[nt][i] = row < rows ? low_of(row) : 0;
-      w.m[nt][i] = w.mv[nt][i] = kLow;
+      w.m[nt][i] = w.rv[nt][i] = kLow;
       w.l[nt][i] = 0.f;
     }
   }
@@ -317,8 +323,8 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
           if (j > w.pos[nt][i & 1] || j < w.low[nt][i & 1]) s[block][nt][i] = -INFINITY;
         }
   }
-  // how far they, and they plus the scale of V, pass their references
-  bool passes = false;
+  // how far they, and they plus the scale of V, are from their references
+  bool passes = false, low = false;
   float top[NT][2], topv[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -331,37 +337,79 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
         top[nt][i] = fmaxf(top[nt][i], x);
         topv[nt][i] = fmaxf(topv[nt][i], x + log_vs[block]);
       }
-      passes |= top[nt][i] > w.m[nt][i] + kSlack || topv[nt][i] > w.mv[nt][i] + kSlack;
+      passes |= top[nt][i] > w.m[nt][i] + kSlack || topv[nt][i] > w.rv[nt][i] + kMost;
+      low |= topv[nt][i] < w.rv[nt][i] + kLeast;
     }
-  if (__any_sync(0xffffffffu, passes)) {
+  if (__any_sync(0xffffffffu, passes || low)) {
+    if (__any_sync(0xffffffffu, low)) {  // the lane's keys are; the column's?
+      uint32_t some = 0, near = 0;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          top[nt][i] = fmaxf(top[nt][i], __shfl_xor_sync(0xffffffffu, top[nt][i], o));
-          topv[nt][i] = fmaxf(topv[nt][i], __shfl_xor_sync(0xffffffffu, topv[nt][i], o));
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t bit = 1u << (8 * nt + 4 * i);
+          some |= topv[nt][i] > -INFINITY ? bit : 0u;
+          near |= topv[nt][i] >= w.rv[nt][i] + kLeast ? bit : 0u;
         }
-        const float m = fmaxf(w.m[nt][i], top[nt][i]), mv = fmaxf(w.mv[nt][i], topv[nt][i]);
-        w.l[nt][i] *= exp2_fast(w.m[nt][i] - m);
-        const float keep = exp2_fast(w.mv[nt][i] - mv);
-        w.m[nt][i] = m;
-        w.mv[nt][i] = mv;
+      some = __reduce_or_sync(0xffffffffu, some << c);
+      near = __reduce_or_sync(0xffffffffu, near << c);
+      if ((some & ~near) != 0) {
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          w.o[j][nt][i] *= keep;
-          w.o[j][nt][i + 2] *= keep;
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float x = topv[nt][i], most = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) most = fmaxf(most, fmaxf(fabsf(w.o[j][nt][i]), fabsf(w.o[j][nt][i + 2])));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+              most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            }
+            const float rv = w.rv[nt][i];
+            if (x > -INFINITY && x < rv + kLeast)
+              w.rv[nt][i] = fmaxf(floorf(x - kLead), rv + ceilf(fminf(__log2f(most) - kTop, 0.f)));
+            // 2^fall may pass 2^127 where O is small; where O is zero any factor will do
+            const float fall = rv - w.rv[nt][i], half = floorf(0.5f * fall);
+            const float keep = exp2_fast(fminf(half, 126.f)), keep2 = exp2_fast(fminf(fall - half, 126.f));
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              w.o[j][nt][i] = w.o[j][nt][i] * keep * keep2;
+              w.o[j][nt][i + 2] = w.o[j][nt][i + 2] * keep * keep2;
+            }
+          }
       }
+    }
+    if (__any_sync(0xffffffffu, passes)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            top[nt][i] = fmaxf(top[nt][i], __shfl_xor_sync(0xffffffffu, top[nt][i], o));
+            topv[nt][i] = fmaxf(topv[nt][i], __shfl_xor_sync(0xffffffffu, topv[nt][i], o));
+          }
+          const float m = fmaxf(w.m[nt][i], top[nt][i]), rv = fmaxf(w.rv[nt][i], floorf(topv[nt][i] - kLead));
+          w.l[nt][i] *= exp2_fast(w.m[nt][i] - m);
+          const float keep = exp2_fast(w.rv[nt][i] - rv);
+          w.m[nt][i] = m;
+          w.rv[nt][i] = rv;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            w.o[j][nt][i] *= keep;
+            w.o[j][nt][i + 2] *= keep;
+          }
+        }
+    }
   }
   // weights, their sums, and the weights times V's scale in fp16 as the second product's operand
   uint32_t pt[Blocks][NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float shift[2];
+    float shift[2];  // half of the way from one reference to the other: the whole may pass 2^127
 #pragma unroll
-    for (int i = 0; i < 2; ++i) shift[i] = exp2_fast(fminf(w.m[nt][i] - w.mv[nt][i], 126.f));
+    for (int i = 0; i < 2; ++i) shift[i] = exp2_fast(fminf(0.5f * (w.m[nt][i] - w.rv[nt][i]), 126.f));
 #pragma unroll
     for (int block = 0; block < Blocks; ++block) {
       float x[4];
@@ -369,7 +417,7 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
       for (int i = 0; i < 4; ++i) {
         const float e = exp2_fast(s[block][nt][i] - w.m[nt][i & 1]);
         w.l[nt][i & 1] += e;
-        x[i] = e * (vs[block] * shift[i & 1]);
+        x[i] = e * (vs[block] * shift[i & 1] * shift[i & 1]);
       }
       pt[block][nt][0] = transpose8x8(floats_half2(x[0], x[1]));
       pt[block][nt][1] = transpose8x8(floats_half2(x[2], x[3]));
@@ -442,11 +490,13 @@ FM_DEV void clean_values(uint8_t* v, int first, Rows<D, NT>& w) {
   __syncwarp();
 }
 
-// A row's factor from its sum of weights times codes to the output, and its log-sum-exp.
-FM_DEV float row_factor(const KvParams& p, int h, float m, float mv, float l) {
-  if (l == 0.f) return 0.f;
+// A row's factors from its sum of weights times codes to the output, one after the other (the product may leave fp32's
+// range), and its log-sum-exp.
+FM_DEV float2 row_factors(const KvParams& p, int h, float m, float rv, float l) {
+  if (l == 0.f) return make_float2(0.f, 0.f);
   const float z = p.sink ? l + exp2_fast(p.sink[h] * kLog2e - m) : l;
-  return exp2_fast(mv - m) / z;
+  const float half = exp2_fast(0.5f * (rv - m));
+  return make_float2(half, half / z);
 }
 FM_DEV float row_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f; }
 
@@ -703,20 +753,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
         if (begins && ends) {
           const int t = r / p.G, h = head * p.G + r - t * p.G;
           const int64_t at = (int64_t)(s.begin + t) * p.n_h + h;
-          const float factor = row_factor(p, h, w.m[nt][i], w.mv[nt][i], l);
+          const float2 f = row_factors(p, h, w.m[nt][i], w.rv[nt][i], l);
           uint16_t* out = p.out + at * p.d + 2 * g;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j)
             if (16 * j < p.d)
               *reinterpret_cast<uint32_t*>(out + 16 * j) =
-                  l == 0.f ? 0u : floats_bf16x2(w.o[j][nt][i] * factor, w.o[j][nt][i + 2] * factor);
+                  l == 0.f ? 0u : floats_bf16x2(w.o[j][nt][i] * f.x * f.y, w.o[j][nt][i + 2] * f.x * f.y);
           if (g == 0 && p.lse) p.lse[at] = row_lse(w.m[nt][i], l);
         } else {
           const int64_t part = ((int64_t)2 * run + begins) * 8 * NT + row;
           float* out = p.part_o + part * D + 2 * g;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) *reinterpret_cast<float2*>(out + 16 * j) = make_float2(w.o[j][nt][i], w.o[j][nt][i + 2]);
-          if (g == 0) p.part_ml[part] = make_float4(w.m[nt][i], w.mv[nt][i], l, 0.f);
+          if (g == 0) p.part_ml[part] = make_float4(w.m[nt][i], w.rv[nt][i], l, 0.f);
         }
       }
     __syncwarp();
@@ -755,21 +805,21 @@ __global__ void __launch_bounds__(2 * D) kv_join_kernel(const __grid_constant__ 
     float4 mine = make_float4(kLow, kLow, 0.f, 0.f), x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (lane <= item.w) mine = p.part_ml[part(lane)];
     if (group <= item.w) x = *reinterpret_cast<const float4*>(p.part_o + part(group) * D + e);
-    const float x_mv = group <= item.w ? p.part_ml[part(group)].y : kLow;
+    const float x_rv = group <= item.w ? p.part_ml[part(group)].y : kLow;
     const int begin = p.cu ? offset_at(p.cu, item.x, p.T) : item.x;
     const int n = p.cu ? offset_at(p.cu, item.x + 1, p.T) - begin : 1;
     const int r = item.z * 8 * NT + row;
     if (r >= n * p.G) continue;  // the whole block
-    float m = mine.x, mv = mine.y;
+    float m = mine.x, rv = mine.y;
     for (int i = lane + 32; i <= item.w; i += 32) {
       const float4 s = p.part_ml[part(i)];
       m = fmaxf(m, s.x);
-      mv = fmaxf(mv, s.y);
+      rv = fmaxf(rv, s.y);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+      rv = fmaxf(rv, __shfl_xor_sync(0xffffffffu, rv, o));
     }
     float l = mine.z * exp2_fast(mine.x - m);
     for (int i = lane + 32; i <= item.w; i += 32) {
@@ -778,11 +828,11 @@ __global__ void __launch_bounds__(2 * D) kv_join_kernel(const __grid_constant__ 
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float f0 = exp2_fast(x_mv - mv);
+    const float f0 = exp2_fast(x_rv - rv);
     x = make_float4(x.x * f0, x.y * f0, x.z * f0, x.w * f0);
 #pragma unroll 8
     for (int i = group + kGroups; i <= item.w; i += kGroups) {
-      const float f = exp2_fast(p.part_ml[part(i)].y - mv);
+      const float f = exp2_fast(p.part_ml[part(i)].y - rv);
       const float4 y = *reinterpret_cast<const float4*>(p.part_o + part(i) * D + e);
       x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
     }
@@ -796,9 +846,10 @@ __global__ void __launch_bounds__(2 * D) kv_join_kernel(const __grid_constant__ 
       }
       const int t = r / p.G, h = item.y * p.G + r - t * p.G;
       const int64_t at = (int64_t)(begin + t) * p.n_h + h;
-      const float f = row_factor(p, h, m, mv, l);
+      const float2 f = row_factors(p, h, m, rv, l);
       *reinterpret_cast<uint2*>(p.out + at * p.d + e) =
-          l == 0.f ? make_uint2(0u, 0u) : make_uint2(floats_bf16x2(x.x * f, x.y * f), floats_bf16x2(x.z * f, x.w * f));
+          l == 0.f ? make_uint2(0u, 0u)
+                   : make_uint2(floats_bf16x2(x.x * f.x * f.y, x.y * f.x * f.y), floats_bf16x2(x.z * f.x * f.y, x.w * f.x * f.y));
       if (e == 0 && p.lse) p.lse[at] = row_lse(m, l);
     }
     __syncthreads();

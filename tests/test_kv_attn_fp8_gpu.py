@@ -291,3 +291,121 @@ def test_two_calls_at_once_graph_and_same_results(torch_dev):
         for (_, _, _, want), out in zip(cases, outs):
             assert (out.view(torch.int16) == want.view(torch.int16)).all()
     assert fm.fm_device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("B,K,G,n,d", [(133, 8, 1, 1, 64), (133, 8, 2, 1, 128), (70, 16, 16, 1, 64), (70, 16, 2, 8, 128),
+                                       (36, 16, 6, 4, 128), (36, 16, 8, 4, 64)])
+@pytest.mark.parametrize("above,place", [(12.0, 0), (17.5, 0), (17.5, 2000), (17.5, 4080), (60.0, 0), (60.0, 2000)])
+def test_keys_under_one_that_takes_nearly_all_of_the_weight(torch_dev, B, K, G, n, d, above, place):
+    """A key whose score is `above` nats over the others' and whose value is zero, by itself and in a block of 64 times the
+    scale: the output is that of the others.  Requests share their 64 pages, so that each warp has all of a request's.
+
+    Values are positive, so that bounds are relative: a weight times scale is off by 2^-11 of itself, or by 2^-22 of the largest
+    of its page but by no more than itself; scores and sums as in grouped_ref.attend; half a step of bf16."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    m, H, T = 4096, K * G, B * n
+    g = torch.Generator(device=dev).manual_seed(B + d)
+    k = (32 * torch.randn((64, K, 64, d), generator=g, device=dev) * 0.5).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    k[..., 0] = 0
+    k[place // 64, :, place % 64] = 0
+    k[place // 64, :, place % 64, 0] = 0x7E  # 448
+    v = torch.randint(0x60, 0x70, (64, K, 64, d), generator=g, device=dev, dtype=torch.uint8)  # 32 .. 60
+    v[place // 64, :, place % 64] = 0
+    table = torch.randperm(64, generator=g, device=dev).int()
+    inverse = torch.empty_like(table)
+    inverse[table.long()] = torch.arange(64, device=dev, dtype=torch.int32)
+    q = torch.randn((T, H, d), generator=g, device=dev)
+    q[..., 0] = above * d ** 0.5 / (448 / 32)
+    q = q.bfloat16()
+    out, lse = torch.empty_like(q), torch.empty((T, H), device=dev)
+    ws = torch.empty(fm.fm_kv_attn_fp8_workspace(T, H, K, d), dtype=torch.uint8, device=dev)
+    for times in (1.0, 64.0):
+        ks, vs = torch.full((64, K, 4), 2.0 ** -5, device=dev), torch.full((64, K, 4), 2.0 ** -6, device=dev)
+        vs[place // 64, :, place % 64 // 16] *= times
+        order = inverse.long()
+        fm.fm_kv_attn_fp8(q, k[order], v[order], ks[order], vs[order], table.expand(B, 64).contiguous(), torch.full((B,), m - n, device=dev), out,
+                          cu_tokens=torch.arange(B + 1, device=dev, dtype=torch.int32) * n, lse_out=lse, workspace=ws)
+        value = lambda c, s: (c.view(torch.float8_e4m3fn).double() * s.double().repeat_interleave(16, -1)[..., None]).transpose(1, 2).reshape(m, K, d)
+        kf, vf = value(k, ks), value(v, vs)
+        seen = torch.arange(m, device=dev) <= torch.arange(m - n, m, device=dev)[:, None]
+        for h in range(K):
+            rows = q.view(B, n, K, G, d)[:, :, h].transpose(1, 2).reshape(B * G, n, d).double()
+            score = (rows @ kf[:, h].T * d ** -0.5).masked_fill(~seen, -float("inf"))
+            size = (rows.abs() @ kf[:, h].abs().T * d ** -0.5).amax()
+            w = score.softmax(-1)
+            weighed = w * vs[:, h].double().repeat_interleave(16, -1).view(m)
+            page = weighed.view(B * G, n, 64, 64).amax(-1, keepdim=True)
+            lost = torch.minimum(2.0 ** -22 * page.expand(-1, -1, -1, 64).reshape(weighed.shape), weighed)
+            codes = v[:, h].view(torch.float8_e4m3fn).double().view(m, d)
+            want = w @ vf[:, h]
+            rel = 2 * ((d + 8) * 2.0 ** -24 * size + 2.0 ** -22 * above) + 2.0 ** -20 + m * 2.0 ** -24
+            tol = want * (2 * rel + 2.0 ** -11 + 2.0 ** -8) + lost @ codes
+            got = out.view(B, n, K, G, d)[:, :, h].transpose(1, 2).reshape(B * G, n, d).double()
+            assert ((got - want).abs() <= tol).all().item(), (times, h, ((got - want).norm() / want.norm()).item())
+            got_lse = lse.view(B, n, K, G)[:, :, h].transpose(1, 2).reshape(B * G, n).double()
+            assert ((got_lse - score.logsumexp(-1)).abs() <= 2 * rel + 2.0 ** -21 * (above + 10)).all().item()
+    assert fm.fm_device_status(reset=True) == 0
+
+
+def one_call(torch, dev, q, codes, scales, table, lens, starts, d, scale=None):
+    """One call over arrays as make's; out and lse in fp64."""
+    import sparse_attention_kv_c4_gb300 as fm
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T, H, K = int(cu[-1]), q.shape[1], codes.shape[3]
+    cd, sd = up(torch, dev, codes), up(torch, dev, scales)
+    out, lse = torch.zeros((T, H, d), dtype=torch.int16, device=dev), torch.zeros((T, H), device=dev)
+    ws = torch.empty(fm.fm_kv_attn_fp8_workspace(T, H, K, d), dtype=torch.uint8, device=dev)
+    fm.fm_kv_attn_fp8(up(torch, dev, q.view(np.int16)), cd[0][:, 0], cd[1][:, 0], sd[0][:, 0], sd[1][:, 0], up(torch, dev, table),
+                      torch.tensor(starts, device=dev), out, cu_tokens=up(torch, dev, cu), scale=scale, lse_out=lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert fm.fm_device_status(reset=True) == 0
+    return ref.f64(out.cpu().numpy().view(np.uint16)), lse.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("d,K,G", [(64, 2, 1), (128, 2, 2), (64, 2, 30)])
+def test_values_that_shrink_from_page_to_page(torch_dev, d, K, G):
+    """Scales of V from 2^90 down to 2^-100, the larger ones' values zero up to a page: the outputs are those of the first
+    page that has values, whatever the references went through; and from 2^-40 up to 2^30, the later pages' zero."""
+    torch, dev = torch_dev
+    rng, m = np.random.default_rng(d + G), 640
+    for first in (0, 3, 9):
+        for turned in (False, True):
+            # each request has all ten pages in one run where there are enough requests; they share them
+            B = 133 * 8 // K
+            table, codes, scales, k, v, size, scale_of, held = make(rng, [1], [m - 1], K * G, K, d)
+            at = np.arange(m) // 64
+            power = 2.0 ** (np.linspace(-40, 30, 10) if turned else np.linspace(90, -100, 10)).astype(int)
+            empty = np.arange(10)[::-1 if turned else 1] < first
+            scales[1][table[0]] = power[:, None, None, None]
+            codes[1][table[0][empty]] = 0
+            size, scale_of = size[0] * ~empty[at][:, None, None], power[at][:, None, None] * np.ones((1, K, 1))
+            q = ref.bf16(rng.standard_normal((1, K * G, d))).repeat(B, 0)
+            got, lse = one_call(torch, dev, q, codes, scales, table.repeat(B, 0), [1] * B, [m - 1] * B, d)
+            want, want_lse, _, ltol = gr.attend(ref.f64(q)[:1], k[0], size * np.sign(v[0]) * scale_of, m - 1, FOREVER, None, d ** -0.5, held[0])
+            # the page of the largest scale with values: its weights' bound for all
+            top = np.flatnonzero(power * ~empty == (power * ~empty).max())[0]
+            mean = size * scale_of
+            s = np.einsum("hd,mhd->hm", ref.f64(q)[0], k[0].repeat(G, 1)) * d ** -0.5
+            w = np.exp(s - want_lse.T)
+            a = np.einsum("hm,mhd->hd", w, mean.repeat(G, 1))
+            tol = a * (2.0 ** -11 + 2 * 2.0 ** -15) + 64 * 2.0 ** -22 * 448 * (w * scale_of.repeat(G, 1)[:, :, 0].T).reshape(-1, m)[:, at == top].max(1)[:, None]
+            assert (np.abs(got - want) <= tol + 2.0 ** -8 * np.abs(want)).all(), (first, turned)
+            assert (np.abs(lse - want_lse) <= ltol).all()
+
+
+@pytest.mark.parametrize("size", [1e-36, 1e35])
+def test_outputs_at_the_ends_of_the_types(torch_dev, size):
+    """Scales of 2^-126 and of 2^110: outputs as small, and as large."""
+    torch, dev = torch_dev
+    K, G, d, rng = 2, 2, 64, np.random.default_rng(1)
+    table, codes, scales, k, v, sizes, scale_of, held = make(rng, [1], [300], K * G, K, d)
+    s = np.float32(2.0 ** np.floor(np.log2(size)) / 64)
+    scales[1] = np.where(np.isnan(scales[1]), scales[1], s)
+    scale_of = np.full_like(scale_of[0], s, dtype=np.float64)
+    q = ref.bf16(rng.standard_normal((1, K * G, d)))
+    got, lse = one_call(torch, dev, q, codes, scales, table, [1], [300], d)
+    want, want_lse, tol, ltol = gr.attend(ref.f64(q), k[0], sizes[0] * np.sign(v[0]) * s, 300, FOREVER, None, d ** -0.5, held[0], gr.HALF_FP16,
+                                          (sizes[0], scale_of))
+    # grouped_ref's absolute term of 2^-120 is these outputs' size: bf16's smallest step instead
+    assert (np.abs(got - want) <= tol - 2.0 ** -120 + 2.0 ** -133).all() and (np.abs(lse - want_lse) <= ltol).all()
