@@ -706,6 +706,7 @@ fm_status fm_kv_append_fp8(const fm_kv_append_fp8_args* args);
  * Scores, softmax statistics and sums are fp32; queries and softmax weights times the values' scales are fp16
  * operands.  Queries are scaled by their row's largest; a weight times scale is off by 2^-11 of itself, or by 2^-22 of the
  * largest of its page of 64 tokens if that is more (other pages' weights, however large, cost it nothing).
+ * A key whose score is 77 or more below its row's largest may count for less than its weight, down to nothing.
  * The result does not depend on scheduling.
  * Errors: FM_ERR_INVALID_ARG, FM_ERR_WORKSPACE, FM_ERR_CUDA.
  */

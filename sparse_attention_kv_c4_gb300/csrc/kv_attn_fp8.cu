@@ -412,12 +412,16 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
     for (int i = 0; i < 2; ++i) shift[i] = exp2_fast(fminf(0.5f * (w.m[nt][i] - w.rv[nt][i]), 126.f));
 #pragma unroll
     for (int block = 0; block < Blocks; ++block) {
-      float x[4];
+      float x[4], unit[2];
+      // Rounded towards zero, so that what passes fp32 ends at its largest number: the weight it then meets is
+      // below 2^-112 of the row's largest, or zero, and zero times infinity is no zero.
+#pragma unroll
+      for (int i = 0; i < 2; ++i) unit[i] = __fmul_rz(__fmul_rz(vs[block], shift[i]), shift[i]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float e = exp2_fast(s[block][nt][i] - w.m[nt][i & 1]);
         w.l[nt][i & 1] += e;
-        x[i] = e * (vs[block] * shift[i & 1] * shift[i & 1]);
+        x[i] = e * unit[i & 1];
       }
       pt[block][nt][0] = transpose8x8(floats_half2(x[0], x[1]));
       pt[block][nt][1] = transpose8x8(floats_half2(x[2], x[3]));

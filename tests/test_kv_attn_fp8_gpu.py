@@ -409,3 +409,32 @@ def test_outputs_at_the_ends_of_the_types(torch_dev, size):
                                           (sizes[0], scale_of))
     # grouped_ref's absolute term of 2^-120 is these outputs' size: bf16's smallest step instead
     assert (np.abs(got - want) <= tol - 2.0 ** -120 + 2.0 ** -133).all() and (np.abs(lse - want_lse) <= ltol).all()
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 4), (128, 2), (128, 5)])
+def test_scales_far_apart(torch_dev, d, G):
+    """Values' scales of 2^-100 (a block of zeros, as the append stores it) and of 2^40: a key that a row does not see, and one
+    whose weight is none in fp32, have no part in it."""
+    torch, dev = torch_dev
+    K, rng = 2, np.random.default_rng(d + G)
+    for n, start, border in ((4, 13, 16), (4, 62, 64), (1, 127, 64)):
+        table, codes, scales, k, v, size, scale_of, held = make(rng, [n], [start], K * G, K, d)
+        q = ref.bf16(rng.standard_normal((n, K * G, d)))
+        m = start + n
+        at = np.arange(m)
+        scale_of[0] = np.where(at < border, 2.0 ** -100, 2.0 ** 40)[:, None, None] * np.ones((1, K, 1))
+        for b in range((m + 15) // 16):
+            scales[1, table[0, b // 4], 0, :, b % 4] = 2.0 ** (-100 if 16 * b < border else 40)
+        if n == 1:  # the far keys' scores lie 120 nats below
+            q[..., 0] = ref.bf16(np.full(1, 120 * d ** 0.5))
+            for j in range(m):
+                codes[0, table[0, j // 64], 0, :, j % 64, 0] = 0 if j < border else 0xB8  # -1
+                k[0][j, :, 0] = 0.0 if j < border else -1.0
+            scales[0] = np.where(np.isnan(scales[0]), scales[0], 1.0)
+            k[0] = gr.VALUES[codes[0][table[0, at // 64], 0, :, at % 64]]
+            q[..., 1:] = ref.bf16(0.01 * rng.standard_normal((1, K * G, d - 1)))
+        value = size[0] * np.sign(v[0]) * scale_of[0]
+        got, lse = one_call(torch, dev, q, codes, scales, table, [n], [start], d)
+        want, want_lse, tol, ltol = gr.attend(ref.f64(q), k[0], value, start, FOREVER, None, d ** -0.5, held[0], gr.HALF_FP16, (size[0], scale_of[0]))
+        assert np.isfinite(got).all() and (np.abs(got - want) <= tol).all(), (n, start, np.abs(got - want).max())
+        assert (np.abs(lse - want_lse) <= ltol).all()
