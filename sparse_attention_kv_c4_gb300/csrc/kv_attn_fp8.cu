@@ -297,8 +297,6 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
   for (int block = 0; block < Blocks; ++block) {
     ks[block] = scales[0][at + block];
     vs[block] = scales[1][at + block];
-    // a block that holds no key of any row may have any scale
-    if (partial && (first + 16 * block > w.most || first + 16 * block + 15 < w.low_least)) vs[block] = 0.f;
     log_vs[block] = __log2f(vs[block]);
   }
   // scores in log2
@@ -450,9 +448,10 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
 
 // Cells of V that are no keys of any row become zeros: they may hold NaN, and zero times that is NaN.  A NaN
 // that some rows see and others do not is made a zero too, and put into the outputs of those that
-// see it (E4M3 has no infinities).
+// see it (E4M3 has no infinities).  The same for the scales of V: a block that is no row's may have any scale, and one that is
+// no number stays with the rows that see the block.
 template <int D, int NT>
-FM_DEV void clean_values(uint8_t* v, int first, Rows<D, NT>& w) {
+FM_DEV void clean_values(uint8_t* v, float* scales, int first, Rows<D, NT>& w) {
   const int lane = threadIdx.x & 31, g = lane >> 2;
   bool bad = false;
 #pragma unroll 1
@@ -490,6 +489,22 @@ FM_DEV void clean_values(uint8_t* v, int first, Rows<D, NT>& w) {
               if (at <= w.pos[nt][i] && at >= w.low[nt][i]) w.o[j][nt][i + 2 * k] = __int_as_float(0x7FC00000);
         }
     }
+  }
+#pragma unroll 1
+  for (int block = 0; block < kBlocksPerPage; ++block) {
+    const int at = first + kKvBlock * block, end = at + kKvBlock - 1;
+    const bool none = at > w.most || end < w.low_least;
+    if (!none && fabsf(scales[block]) < INFINITY) continue;  // the same in all lanes
+    __syncwarp();
+    scales[block] = 0.f;
+    if (none) continue;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (at <= w.pos[nt][i] && end >= w.low[nt][i])
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) w.o[j][nt][i] = w.o[j][nt][i + 2] = __int_as_float(0x7FC00000);
   }
   __syncwarp();
 }
@@ -724,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
       const int first = first0 + i * kKvPage;
       if (sh.held[warp][stage] && first <= w.most && first + kKvPage > w.low_least) {
         const bool partial = first + kKvPage - 1 > w.least || first < w.low_most;
-        if (partial) clean_values<D, NT>(sh.kv[warp][stage][1], first, w);
+        if (partial) clean_values<D, NT>(sh.kv[warp][stage][1], sh.scales[warp][stage][1], first, w);
         // all keys at once where registers allow, else in halves
         constexpr int kBlocks = D * NT < 256 || (D == 128 && NT == 2) ? 4 : 2;
 #pragma unroll 1

@@ -438,3 +438,23 @@ def test_scales_far_apart(torch_dev, d, G):
         want, want_lse, tol, ltol = gr.attend(ref.f64(q), k[0], value, start, FOREVER, None, d ** -0.5, held[0], gr.HALF_FP16, (size[0], scale_of[0]))
         assert np.isfinite(got).all() and (np.abs(got - want) <= tol).all(), (n, start, np.abs(got - want).max())
         assert (np.abs(lse - want_lse) <= ltol).all()
+
+
+@pytest.mark.parametrize("which,bad", [(0, np.nan), (1, np.nan), (0, np.inf), (1, np.inf)])
+def test_a_later_drafts_scale_does_not_reach_the_earlier_rows(torch_dev, which, bad):
+    """A block that only the later drafts see has a scale that is no number: the rows that do not see it are as without."""
+    torch, dev = torch_dev
+    rng = np.random.default_rng(21)
+    for start, d in ((15, 64), (62, 64), (31, 128)):
+        table, codes, scales, k, v, size, scale_of, held = make(rng, [4], [start], 8, 2, d)
+        border = (start // 16 + 1) * 16
+        scales[which, table[0, border // 64], 0, 1, border % 64 // 16] = bad
+        q = ref.bf16(rng.standard_normal((4, 8, d)))
+        got, _ = one_call(torch, dev, q, codes, scales, table, [4], [start], d)
+        want, _, tol, _ = gr.attend(ref.f64(q), k[0], v[0], start, FOREVER, None, d ** -0.5, held[0], gr.HALF_FP16, (size[0], scale_of[0]))
+        sees = np.arange(start, start + 4) >= border
+        clean = np.ones(got.shape, bool)
+        clean[np.ix_(sees, range(4, 8))] = False
+        assert (np.abs(got - want) <= tol)[clean].all(), (start, d)
+        if np.isnan(bad):
+            assert np.isnan(got[~clean]).all()
