@@ -642,7 +642,8 @@ fm_status fm_csa_attn_packed(const fm_csa_attn_args* args);
  * earlier tokens keeps the larger of its scale and need; where that is need, its
  * earlier codes c become e4m3(e4m3(c) * old / need).  An entry x becomes
  * e4m3(x * (1 / scale)), rounded once from fp32, ties to even; a turned pair that fp32's rounding may
- * have carried over the middle between two codes is turned in fp64.  Infinities and NaN do not
+ * have carried over the middle between two codes, or a block's largest entry over 448 times a power of two, is turned in
+ * fp64.  Infinities and NaN do not
  * count for amax and are stored as NaN (0x7F).
  *   A page that several sequences share may be appended to by one of them only, and a call's
  * tokens are on pages that differ (a table that names one page twice leaves its cells unspecified).

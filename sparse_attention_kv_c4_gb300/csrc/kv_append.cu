@@ -94,12 +94,22 @@ FM_DEV bool near_middle(float y, float off) {
   return fabsf(q - floorf(q) - 0.5f) <= off * per_step;
 }
 // A pair of bf16 entries turned in 64 bits: cos and sin of the phase in units of 2^-64 turns.
-__device__ __noinline__ float2 turn_exactly(float a, float b, uint64_t phase, float times) {
+FM_DEV double2 turned(float a, float b, uint64_t phase) {
   double s, c;
   sincospi((double)(int64_t)phase * 1.0842021724855044e-19, &s, &c);
-  return make_float2((float)((a * c - b * s) * times), (float)((a * s + b * c) * times));
+  return make_double2(a * c - b * s, a * s + b * c);
+}
+__device__ __noinline__ float2 turn_exactly(float a, float b, uint64_t phase, float times) {
+  const double2 x = turned(a, b, phase);
+  return make_float2((float)(x.x * times), (float)(x.y * times));
 }
 
+// Whether fp32's rounding of the turn, under 2^-20 of the largest entry (2^-21 of a pair's two, and neither is more than
+// 1.42 times the larger turned one), may have carried a block's largest over a border between two scales.
+FM_DEV bool near_border(float amax) {
+  const int from = (int)(__float_as_uint(amax) & 0x7FFFFFu) - 0x600000;  // in units of 2^-23 of its power of two
+  return from >= -16 && from <= 16;  // 2^-20 of 1.75 are 14.7
+}
 FM_DEV uint32_t codes4(float a, float b, float c, float d) {
   auto fix = [](float x) { return isinf(x) ? __int_as_float(0x7FC00000) : x; };  // the conversion would make it 448
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(fix(a), fix(b)), __NV_SATFINITE, __NV_E4M3);
@@ -110,6 +120,56 @@ FM_DEV uint32_t codes4(float a, float b, float c, float d) {
 FM_DEV float2 code2_floats(uint32_t c) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xFFFFu), __NV_E4M3);
   return __half22float2(__half2(h));
+}
+
+// A block of keys whose largest entry is a turned one within fp32's error of a border: whether some entry is over it is found
+// with the turns in 64 bits, then all is as in append_block.  By a whole warp, from memory; row 0 would be token `t`.  Some
+// block in 10^5 needs it.
+__device__ __noinline__ void append_at_border(const AppendParams& p, const Shared& sh, int t, int head, int lo, int hi, uint8_t* cells,
+                                              float* scale_at, float amax) {
+  const int pairs = p.d / 2, lane = threadIdx.x & 31;
+  const uint16_t* x = p.k + (int64_t)t * p.k_stride_t + head * p.d;
+  const float border = __uint_as_float((__float_as_uint(amax) & 0x7F800000u) | 0x600000u);
+  bool over = false;
+#pragma unroll 1
+  for (int i = lo * pairs + lane; i < hi * pairs; i += 32) {
+    const int row = i / pairs, e = 2 * (i - row * pairs);
+    const float2 f = bf16x2_floats(*reinterpret_cast<const uint32_t*>(x + row * p.k_stride_t + e));
+    const float a = f.x / border, b = f.y / border;
+    double2 y = make_double2(f.x, f.y);
+    if (e >= p.rope_start) {
+      if (!(a * a + b * b > 0.999f)) continue;  // no turned entry is larger than the pair
+      y = turned(f.x, f.y, (uint64_t)sh.pos[row] * sh.turn[(e - p.rope_start) >> 1]);
+    }
+    over |= (finite_abs((float)y.x) > 0.f && fabs(y.x) > border) || (finite_abs((float)y.y) > 0.f && fabs(y.y) > border);
+  }
+  const float need = need_scale(__any_sync(0xffffffffu, over) ? __uint_as_float(__float_as_uint(border) + 1) : border);
+  const float old = lo > 0 ? *scale_at : 0.f;
+  const bool keep = lo > 0 && old >= need;
+  const float scale = keep ? old : need, inv = 1.f / scale, shrink = old * inv;
+#pragma unroll 1
+  for (int i = (keep ? lo : 0) * pairs + lane; i < hi * pairs; i += 32) {
+    const int row = i / pairs, e = 2 * (i - row * pairs);
+    uint16_t* cell = reinterpret_cast<uint16_t*>(cells + row * p.d + e);
+    float2 f;
+    if (row < lo) {
+      f = code2_floats(*cell);
+      f = make_float2(f.x * shrink, f.y * shrink);
+    } else {
+      const float2 v = bf16x2_floats(*reinterpret_cast<const uint32_t*>(x + row * p.k_stride_t + e));
+      f = make_float2(v.x * inv, v.y * inv);
+      if (e >= p.rope_start) {
+        const float2 c = sh.cs[row][(e - p.rope_start) >> 1];
+        f = make_float2((v.x * c.x - v.y * c.y) * inv, (v.x * c.y + v.y * c.x) * inv);
+        const float off = (fabsf(f.x) + fabsf(f.y)) * 4.76837158e-7f;
+        if (near_middle(f.x, off) || near_middle(f.y, off))
+          f = turn_exactly(v.x, v.y, (uint64_t)sh.pos[row] * sh.turn[(e - p.rope_start) >> 1], inv);
+      }
+    }
+    *cell = (uint16_t)codes4(f.x, f.y, 0.f, 0.f);
+  }
+  __syncwarp();
+  if (lane == 0 && !keep) *scale_at = scale;
 }
 
 FM_DEV uint4 load16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
@@ -198,18 +258,26 @@ FM_DEV void append_block(const AppendParams& p, Shared& sh) {
     }
     return f;
   };
-  float amax = 0.f;
+  float amax = 0.f, turned_amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (row[i] >= lo) {
+      float x = 0.f;
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
         const float2 f = entry(i, m);
-        amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+        x = fmaxf(x, fmaxf(finite_abs(f.x), finite_abs(f.y)));
       }
+      amax = fmaxf(amax, x);
+      if (16 * (lane + 32 * i - row[i] * chunks) + 14 >= p.rope_start) turned_amax = fmaxf(turned_amax, x);
     }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const bool at_border = is_k && __any_sync(0xffffffffu, near_border(turned_amax) && turned_amax > 0.99f * amax);
+  if (at_border) {  // nothing of the warp's is used behind the call, which so costs the others no registers
+    append_at_border(p, sh, begin + (int)(first - start), head, lo, hi, cells, scale_at, amax);
+    return;
+  }
   const float need = need_scale(amax);
   const bool keep = lo > 0 && old >= need;  // the block's earlier codes stay as they are
   const float scale = keep ? old : need;

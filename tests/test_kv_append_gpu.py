@@ -223,3 +223,33 @@ def test_no_offsets_in_place_queries_streams_and_graph(torch_dev):
     pos = start.cpu().numpy()
     want = gr.rotate(q.double().cpu().numpy(), pos, 64)
     assert (np.abs(q_plain.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -17).all()
+
+
+@pytest.mark.parametrize("inside,d,K", [(0, 64, 1), (5, 64, 1), (0, 96, 2), (5, 128, 1)])
+def test_a_turned_pair_at_the_border_of_a_scale(torch_dev, inside, d, K):
+    """Pairs whose larger turned entry lies within 2^-24 of 448 times a power of two, on either side: fp32's rounding of the turn
+    would put some on the other side, and with it all of their block's codes."""
+    torch, dev = torch_dev
+    rope = 64
+    pos = 16 * np.arange(0, 256) + inside
+    angle = pos[:, None] * ref.freqs(rope)[None, :]
+    c, s = np.cos(angle)[..., None], np.sin(angle)[..., None]
+    a = (128 + np.arange(128)) / 128.0 * np.ones(c.shape)
+    border = 1.75
+    with np.errstate(divide="ignore", invalid="ignore"):
+        b = ref.f64(ref.bf16((a * c - border) / s))
+        x, y = a * c - b * s, a * s + b * c
+        near = np.abs(x / border - 1)
+    # farther than fp64's own errors, and the larger of the two
+    t, i, j = np.nonzero((near < 2.0 ** -24) & (near > 1e-10) & (np.abs(y) < 1.5))
+    assert len(t) >= 32 and (x[t, i, j] > border).any() and (x[t, i, j] < border).any()
+    T = len(t)
+    rng = np.random.default_rng(5)
+    k = ref.bf16(0.1 * rng.standard_normal((T, K, d)))
+    at = np.arange(T)
+    k[at, K - 1, d - rope + 2 * i], k[at, K - 1, d - rope + 2 * i + 1] = ref.bf16(a[t, i, j]), ref.bf16(b[t, i, j])
+    starts = [int(p) for p in pos[t]]
+    table, at = np.full((T, max(starts) // 64 + 1), -1, np.int32), np.arange(T)
+    table[at, np.array(starts) // 64] = at
+    pools, scales = np.zeros((2, T, 1, K, 64, d), np.uint8), np.full((2, T, 1, K, 4), 2.0 ** -20, np.float32)
+    run(torch, dev, rng, [1] * T, starts, K, d, 0, rope, k=k, table=table, P=T, pools=pools, scales=scales, gaps=False)
