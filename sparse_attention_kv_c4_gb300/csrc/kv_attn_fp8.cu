@@ -46,12 +46,13 @@ constexpr int kRunsPerBlock = 4;        // of the join
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLow = -1e30f;          // below every score
 constexpr float kSlack = 8.f;           // how far a score (in log2) may pass its reference
-// Weights times V's scale go to fp16 as 2^(x - rv).  A reference rv starts 11 to 12 below a tile's largest x and moves,
-// up or down and by whole numbers, when a tile's largest weight passes 2^15 (fp16 ends at 65504) or stays below 2^-3: each
-// is then off by 2^-11 of itself or 2^-22 of its tile's largest (half of fp16's smallest step).  (With a reference at the largest of all tiles, a
+// Weights times V's scale go to fp16 as 2^(x - rv).  A reference rv starts 12 below a tile's largest x, so that the
+// heaviest weight is a power of two and loses nothing, and moves, up or down, when a tile's largest weight passes 2^15 (fp16
+// ends at 65504) or stays below 2^-3: each is then off by 2^-11 of itself or 2^-22 of its tile's largest (half of fp16's
+// smallest step).  (With a reference at the largest of all tiles, a
 // key e^16 over the others whose value was zero left them to fp16's subnormals: 12% off.)  O, in fp32, is in units of
 // 2^rv; a reference goes down no further than leaves O below 2^kTop.
-constexpr float kLead = 11.f, kMost = 15.f, kLeast = -3.f, kTop = 100.f;
+constexpr float kLead = 12.f, kMost = 15.f, kLeast = -3.f, kTop = 100.f;
 
 template <int D>
 struct Layout {
@@ -366,14 +367,13 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
             }
             const float rv = w.rv[nt][i];
             if (x > -INFINITY && x < rv + kLeast)
-              w.rv[nt][i] = fmaxf(floorf(x - kLead), rv + ceilf(fminf(__log2f(most) - kTop, 0.f)));
+              w.rv[nt][i] = fmaxf(x - kLead, rv + fminf(__log2f(most) - kTop, 0.f));
             // 2^fall may pass 2^127 where O is small; where O is zero any factor will do
-            const float fall = rv - w.rv[nt][i], half = floorf(0.5f * fall);
-            const float keep = exp2_fast(fminf(half, 126.f)), keep2 = exp2_fast(fminf(fall - half, 126.f));
+            const float keep = exp2_fast(fminf(0.5f * (rv - w.rv[nt][i]), 126.f));
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
-              w.o[j][nt][i] = w.o[j][nt][i] * keep * keep2;
-              w.o[j][nt][i + 2] = w.o[j][nt][i + 2] * keep * keep2;
+              w.o[j][nt][i] = w.o[j][nt][i] * keep * keep;
+              w.o[j][nt][i + 2] = w.o[j][nt][i + 2] * keep * keep;
             }
           }
       }
@@ -388,7 +388,7 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
             top[nt][i] = fmaxf(top[nt][i], __shfl_xor_sync(0xffffffffu, top[nt][i], o));
             topv[nt][i] = fmaxf(topv[nt][i], __shfl_xor_sync(0xffffffffu, topv[nt][i], o));
           }
-          const float m = fmaxf(w.m[nt][i], top[nt][i]), rv = fmaxf(w.rv[nt][i], floorf(topv[nt][i] - kLead));
+          const float m = fmaxf(w.m[nt][i], top[nt][i]), rv = fmaxf(w.rv[nt][i], topv[nt][i] - kLead);
           w.l[nt][i] *= exp2_fast(w.m[nt][i] - m);
           const float keep = exp2_fast(w.rv[nt][i] - rv);
           w.m[nt][i] = m;
