@@ -44,15 +44,16 @@ constexpr int kMaxCtas = 160;
 constexpr int kMaxRuns = kMaxCtas * kWarps;
 constexpr int kRunsPerBlock = 4;        // of the join
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLow = -1e30f;          // below every score
 constexpr float kSlack = 8.f;           // how far a score (in log2) may pass its reference
-// Weights times V's scale go to fp16 as 2^(x - rv).  A reference rv starts 12 below a tile's largest x, so that the
-// heaviest weight is a power of two and loses nothing, and moves, up or down, when a tile's largest weight passes 2^15 (fp16
-// ends at 65504) or stays below 2^-3: each is then off by 2^-11 of itself or 2^-22 of its tile's largest (half of fp16's
-// smallest step).  (With a reference at the largest of all tiles, a
-// key e^16 over the others whose value was zero left them to fp16's subnormals: 12% off.)  O, in fp32, is in units of
-// 2^rv; a reference goes down no further than leaves O below 2^kTop.
+// Weights times V's scale go to fp16 as 2^(x + g), x the logarithm of such a product relative to the row's reference of
+// scores.  A row's g puts a tile's largest at 2^12, so that the heaviest weight is a power of two and loses nothing, and
+// moves, up or down, when a tile's largest passes 2^15 (fp16 ends at 65504) or stays below 2^-3: each is then off by 2^-11
+// of itself or 2^-22 of its tile's largest (half of fp16's smallest step).  (With a range that only went up, a key e^16
+// over the others whose value was zero left them to fp16's subnormals: 12% off.)  O, in fp32, is in units of 2^-g; g goes
+// up no further than leaves O below 2^kTop.  All of it is relative: scores of 10^9 lose fp32's digits, but no range.
 constexpr float kLead = 12.f, kMost = 15.f, kLeast = -3.f, kTop = 100.f;
+constexpr float kUnset = 3e38f;         // g of a row that has not met a key
+constexpr float kNoKey = -3.402823466e38f;  // a part's reference where it has none
 
 template <int D>
 struct Layout {
@@ -68,7 +69,7 @@ struct KvParams {
   uint16_t* out;
   float* lse;
   float* part_o;      // [2 runs][rows][D] unnormalised outputs
-  float4* part_ml;    // [2 runs][rows] (reference of scores, of weights times V's scales, sum)
+  float4* part_ml;    // [2 runs][rows] (reference of scores, g, sum)
   int4* part_item;    // [runs] (sequence, head, row tile, runs that follow) of the item that a run begins and does not end
   int64_t q_stride_t, scale_stride, window;
   int T, n_h, n_k, d, G, P, B, R, runs;
@@ -186,7 +187,7 @@ struct Rows {
   uint32_t q[D / 16][NT][2];    // B fragments: row g of each eight, elements of the lane's chunks
   float f[NT][2];               // columns 2c, 2c + 1: factor from q . code to scores in log2 (times K's scale)
   int pos[NT][2], low[NT][2];   // the last and the first position that they see (last below first: no row)
-  float m[NT][2], rv[NT][2], l[NT][2];
+  float m[NT][2], g[NT][2], l[NT][2];  // reference of scores, unit of the weights, sum
   float o[D / 16][NT][4];       // (d = 16 j + 2 g, column 2c), (.., 2c + 1), (d + 1, 2c), (d + 1, 2c + 1)
   int least, most, low_least, low_most;  // of the tile's first and last row
 };
@@ -252,7 +253,8 @@ FM_DEV void load_rows(const KvParams& p, const Seq& s, int head, int tile, Rows<
       const int row = row0 + 8 * nt + 2 * c + i;
       w.pos[nt][i] = row < rows ? last_of(row) : -1;
       w.low[nt][i] = row < rows ? low_of(row) : 0;
-      w.m[nt][i] = w.rv[nt][i] = kLow;
+      w.m[nt][i] = 0.f;
+      w.g[nt][i] = kUnset;
       w.l[nt][i] = 0.f;
     }
   }
@@ -298,19 +300,15 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
   for (int block = 0; block < Blocks; ++block) {
     ks[block] = scales[0][at + block];
     vs[block] = scales[1][at + block];
-    log_vs[block] = __log2f(vs[block]);
+    log_vs[block] = fmaxf(__log2f(vs[block]), -200.f);  // a scale of zero has one too
   }
-  // scores in log2
+  // scores in log2, relative to their references
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int block = 0; block < Blocks; ++block) {
-      const float f0 = ks[block] * w.f[nt][0], f1 = ks[block] * w.f[nt][1];
-      s[block][nt][0] *= f0;
-      s[block][nt][1] *= f1;
-      s[block][nt][2] *= f0;
-      s[block][nt][3] *= f1;
-    }
+    for (int block = 0; block < Blocks; ++block)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[block][nt][i] = fmaf(s[block][nt][i], ks[block] * w.f[nt][i & 1], -w.m[nt][i & 1]);
   if (partial) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -322,7 +320,7 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
           if (j > w.pos[nt][i & 1] || j < w.low[nt][i & 1]) s[block][nt][i] = -INFINITY;
         }
   }
-  // how far they, and they plus the scale of V, are from their references
+  // the largest of the lane's, and of them times V's scale
   bool passes = false, low = false;
   float top[NT][2], topv[NT][2];
 #pragma unroll
@@ -336,8 +334,9 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
         top[nt][i] = fmaxf(top[nt][i], x);
         topv[nt][i] = fmaxf(topv[nt][i], x + log_vs[block]);
       }
-      passes |= top[nt][i] > w.m[nt][i] + kSlack || topv[nt][i] > w.rv[nt][i] + kMost;
-      low |= topv[nt][i] < w.rv[nt][i] + kLeast;
+      const float x = topv[nt][i] + w.g[nt][i];
+      passes |= top[nt][i] > kSlack || x > kMost;
+      low |= x < kLeast;
     }
   if (__any_sync(0xffffffffu, passes || low)) {
     if (__any_sync(0xffffffffu, low)) {  // the lane's keys are; the column's?
@@ -348,7 +347,7 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
         for (int i = 0; i < 2; ++i) {
           const uint32_t bit = 1u << (8 * nt + 4 * i);
           some |= topv[nt][i] > -INFINITY ? bit : 0u;
-          near |= topv[nt][i] >= w.rv[nt][i] + kLeast ? bit : 0u;
+          near |= topv[nt][i] + w.g[nt][i] >= kLeast ? bit : 0u;
         }
       some = __reduce_or_sync(0xffffffffu, some << c);
       near = __reduce_or_sync(0xffffffffu, near << c);
@@ -365,11 +364,11 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
               most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
             }
-            const float rv = w.rv[nt][i];
-            if (x > -INFINITY && x < rv + kLeast)
-              w.rv[nt][i] = fmaxf(x - kLead, rv + fminf(__log2f(most) - kTop, 0.f));
-            // 2^fall may pass 2^127 where O is small; where O is zero any factor will do
-            const float keep = exp2_fast(fminf(0.5f * (rv - w.rv[nt][i]), 126.f));
+            float up = 0.f;
+            if (x > -INFINITY && x + w.g[nt][i] < kLeast) up = fminf(kLead - x - w.g[nt][i], fmaxf(kTop - __log2f(most), 0.f));
+            w.g[nt][i] += up;
+            // 2^up may pass 2^127 where O is small; where O is zero any factor will do
+            const float keep = exp2_fast(fminf(0.5f * up, 126.f));
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
               w.o[j][nt][i] = w.o[j][nt][i] * keep * keep;
@@ -383,16 +382,26 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          float x = top[nt][i];
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            top[nt][i] = fmaxf(top[nt][i], __shfl_xor_sync(0xffffffffu, top[nt][i], o));
-            topv[nt][i] = fmaxf(topv[nt][i], __shfl_xor_sync(0xffffffffu, topv[nt][i], o));
+          for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+          // The reference of scores becomes the largest so far; of the row's first keys even if it is below zero.  The
+          // tile's scores move by what lies between, not by the rounded references' difference: the largest is at zero.
+          const bool first_keys = w.g[nt][i] == kUnset && x > -INFINITY;
+          const float by = x > 0.f || first_keys ? x : 0.f;
+          float xv = -INFINITY;
+#pragma unroll
+          for (int block = 0; block < Blocks; ++block) {
+            s[block][nt][i] -= by;
+            s[block][nt][i + 2] -= by;
+            xv = fmaxf(xv, fmaxf(s[block][nt][i], s[block][nt][i + 2]) + log_vs[block]);
           }
-          const float m = fmaxf(w.m[nt][i], top[nt][i]), rv = fmaxf(w.rv[nt][i], topv[nt][i] - kLead);
-          w.l[nt][i] *= exp2_fast(w.m[nt][i] - m);
-          const float keep = exp2_fast(w.rv[nt][i] - rv);
-          w.m[nt][i] = m;
-          w.rv[nt][i] = rv;
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) xv = fmaxf(xv, __shfl_xor_sync(0xffffffffu, xv, o));
+          const float from = first_keys ? INFINITY : w.g[nt][i] + by, to = fminf(from, kLead - xv), keep = exp2_fast(to - from);
+          w.l[nt][i] *= first_keys ? 0.f : exp2_fast(-by);
+          w.m[nt][i] += by;
+          w.g[nt][i] = to;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             w.o[j][nt][i] *= keep;
@@ -405,19 +414,19 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
   uint32_t pt[Blocks][NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float shift[2];  // half of the way from one reference to the other: the whole may pass 2^127
+    float half[2];  // of the way to the weights' unit: the whole may pass 2^127
 #pragma unroll
-    for (int i = 0; i < 2; ++i) shift[i] = exp2_fast(fminf(0.5f * (w.m[nt][i] - w.rv[nt][i]), 126.f));
+    for (int i = 0; i < 2; ++i) half[i] = exp2_fast(fminf(0.5f * w.g[nt][i], 126.f));
 #pragma unroll
     for (int block = 0; block < Blocks; ++block) {
       float x[4], unit[2];
       // Rounded towards zero, so that what passes fp32 ends at its largest number: the weight it then meets is
       // below 2^-112 of the row's largest, or zero, and zero times infinity is no zero.
 #pragma unroll
-      for (int i = 0; i < 2; ++i) unit[i] = __fmul_rz(__fmul_rz(vs[block], shift[i]), shift[i]);
+      for (int i = 0; i < 2; ++i) unit[i] = __fmul_rz(__fmul_rz(vs[block], half[i]), half[i]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = exp2_fast(s[block][nt][i] - w.m[nt][i & 1]);
+        const float e = exp2_fast(s[block][nt][i]);
         w.l[nt][i & 1] += e;
         x[i] = e * unit[i & 1];
       }
@@ -509,12 +518,12 @@ FM_DEV void clean_values(uint8_t* v, float* scales, int first, Rows<D, NT>& w) {
   __syncwarp();
 }
 
-// A row's factors from its sum of weights times codes to the output, one after the other (the product may leave fp32's
-// range), and its log-sum-exp.
-FM_DEV float2 row_factors(const KvParams& p, int h, float m, float rv, float l) {
+// A row's factors from its sum of weights times codes, in units of 2^e relative to the reference m, to the output, one after
+// the other (the product may leave fp32's range), and its log-sum-exp.
+FM_DEV float2 row_factors(const KvParams& p, int h, float m, float e, float l) {
   if (l == 0.f) return make_float2(0.f, 0.f);
   const float z = p.sink ? l + exp2_fast(p.sink[h] * kLog2e - m) : l;
-  const float half = exp2_fast(0.5f * (rv - m));
+  const float half = exp2_fast(0.5f * e);
   return make_float2(half, half / z);
 }
 FM_DEV float row_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f; }
@@ -772,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
         if (begins && ends) {
           const int t = r / p.G, h = head * p.G + r - t * p.G;
           const int64_t at = (int64_t)(s.begin + t) * p.n_h + h;
-          const float2 f = row_factors(p, h, w.m[nt][i], w.rv[nt][i], l);
+          const float2 f = row_factors(p, h, w.m[nt][i], -w.g[nt][i], l);
           uint16_t* out = p.out + at * p.d + 2 * g;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j)
@@ -785,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
           float* out = p.part_o + part * D + 2 * g;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) *reinterpret_cast<float2*>(out + 16 * j) = make_float2(w.o[j][nt][i], w.o[j][nt][i + 2]);
-          if (g == 0) p.part_ml[part] = make_float4(w.m[nt][i], w.rv[nt][i], l, 0.f);
+          if (g == 0) p.part_ml[part] = make_float4(l == 0.f ? kNoKey : w.m[nt][i], w.g[nt][i], l, 0.f);
         }
       }
     __syncwarp();
@@ -821,37 +830,35 @@ __global__ void __launch_bounds__(2 * D) kv_join_kernel(const __grid_constant__ 
     const int4 item = p.part_item[run];
     auto part = [&](int i) { return ((int64_t)2 * (run + i) + (i == 0)) * 8 * NT + row; };
     // one round of loads: what most items need is under way at once
-    float4 mine = make_float4(kLow, kLow, 0.f, 0.f), x = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 mine = make_float4(kNoKey, kUnset, 0.f, 0.f), x_ml = mine, x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (lane <= item.w) mine = p.part_ml[part(lane)];
-    if (group <= item.w) x = *reinterpret_cast<const float4*>(p.part_o + part(group) * D + e);
-    const float x_rv = group <= item.w ? p.part_ml[part(group)].y : kLow;
+    if (group <= item.w) x = *reinterpret_cast<const float4*>(p.part_o + part(group) * D + e), x_ml = p.part_ml[part(group)];
     const int begin = p.cu ? offset_at(p.cu, item.x, p.T) : item.x;
     const int n = p.cu ? offset_at(p.cu, item.x + 1, p.T) - begin : 1;
     const int r = item.z * 8 * NT + row;
     if (r >= n * p.G) continue;  // the whole block
-    float m = mine.x, rv = mine.y;
-    for (int i = lane + 32; i <= item.w; i += 32) {
-      const float4 s = p.part_ml[part(i)];
-      m = fmaxf(m, s.x);
-      rv = fmaxf(rv, s.y);
-    }
+    float m = mine.x;
+    for (int i = lane + 32; i <= item.w; i += 32) m = fmaxf(m, p.part_ml[part(i)].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      rv = fmaxf(rv, __shfl_xor_sync(0xffffffffu, rv, o));
-    }
-    float l = mine.z * exp2_fast(mine.x - m);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // a part's unit relative to the common reference; the highest becomes the common unit
+    auto unit = [&](const float4& s) { return s.x - m - s.y; };
+    float l = mine.z * exp2_fast(mine.x - m), high = unit(mine);
     for (int i = lane + 32; i <= item.w; i += 32) {
       const float4 s = p.part_ml[part(i)];
       l += s.z * exp2_fast(s.x - m);
+      high = fmaxf(high, unit(s));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float f0 = exp2_fast(x_rv - rv);
+    for (int o = 16; o > 0; o >>= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, o);
+      high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+    }
+    const float f0 = exp2_fast(unit(x_ml) - high);
     x = make_float4(x.x * f0, x.y * f0, x.z * f0, x.w * f0);
 #pragma unroll 8
     for (int i = group + kGroups; i <= item.w; i += kGroups) {
-      const float f = exp2_fast(p.part_ml[part(i)].y - rv);
+      const float f = exp2_fast(unit(p.part_ml[part(i)]) - high);
       const float4 y = *reinterpret_cast<const float4*>(p.part_o + part(i) * D + e);
       x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
     }
@@ -865,7 +872,7 @@ __global__ void __launch_bounds__(2 * D) kv_join_kernel(const __grid_constant__ 
       }
       const int t = r / p.G, h = item.y * p.G + r - t * p.G;
       const int64_t at = (int64_t)(begin + t) * p.n_h + h;
-      const float2 f = row_factors(p, h, m, rv, l);
+      const float2 f = row_factors(p, h, m, high, l);
       *reinterpret_cast<uint2*>(p.out + at * p.d + e) =
           l == 0.f ? make_uint2(0u, 0u)
                    : make_uint2(floats_bf16x2(x.x * f.x * f.y, x.y * f.x * f.y), floats_bf16x2(x.z * f.x * f.y, x.w * f.x * f.y));

@@ -458,3 +458,52 @@ def test_a_later_drafts_scale_does_not_reach_the_earlier_rows(torch_dev, which, 
         assert (np.abs(got - want) <= tol)[clean].all(), (start, d)
         if np.isnan(bad):
             assert np.isnan(got[~clean]).all()
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 5)])
+def test_scores_near_the_least_number(torch_dev, d, G):
+    """Keys whose scores are -10^31 and less are keys: equal ones share the weight, the larger one has it all."""
+    torch, dev = torch_dev
+    K, rng = 2, np.random.default_rng(3)
+    table, codes, scales, k, v, size, scale_of, held = make(rng, [1, 3], [4, 200], K * G, K, d)
+    codes[0] = np.where(codes[0] == 0x7F, 0x7F, 0x40)  # 2
+    scales[0] = np.where(np.isnan(scales[0]), scales[0], np.float32(1e16))
+    q = ref.bf16(np.full((4, K * G, d), -1e16))
+    got, lse = one_call(torch, dev, q, codes, scales, table, [1, 3], [4, 200], d)
+    score = float(ref.f64(q)[0, 0, 0]) * 2 * float(np.float32(1e16)) * d * d ** -0.5
+    assert (np.abs(lse / score - 1) <= 2.0 ** -18).all()
+    for b, rows in ((0, range(1)), (1, range(1, 4))):
+        for i, r in enumerate(rows):
+            seen = v[b][:(4, 200)[b] + i + 1].repeat(G, 1)
+            tol = 2.0 ** -8 * np.abs(seen.mean(0)) + (2.0 ** -11 + 2.0 ** -14) * np.abs(seen).mean(0)
+            assert (np.abs(got[r] - seen.mean(0)) <= tol).all(), r
+    for j in (0, 130):  # one key's score of half the size is the largest by far
+        codes[0, table[1, j // 64], 0, :, j % 64] = 0x38  # 1
+        got, lse = one_call(torch, dev, q, codes, scales, table, [1, 3], [4, 200], d)
+        want = v[1][j].repeat(G, 0)
+        assert (np.abs(got[1:] - want) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(want)).all() and (np.abs(lse[1:] / score - 0.5) <= 2.0 ** -18).all()
+        codes[0, table[1, j // 64], 0, :, j % 64] = 0x40
+
+
+@pytest.mark.parametrize("size", [1e6, 3e8, 1e12])
+@pytest.mark.parametrize("d,G,m", [(64, 1, 40), (64, 30, 3000), (128, 2, 300), (128, 20, 3000)])
+def test_scores_of_millions(torch_dev, size, d, G, m):
+    """Scores whose spacing in fp32 is coarser than the weights' range, in one run and in many: out is the mean of some of the
+    values, by weights that are each their own within the rounding of the score: those of the largest alone where it stands out."""
+    torch, dev = torch_dev
+    K, rng = 2, np.random.default_rng(int(np.log2(size)) + d + m)
+    table, codes, scales, k, v, sizes, scale_of, held = make(rng, [1], [m - 1], K * G, K, d)
+    scales[0] = np.where(np.isnan(scales[0]), scales[0], np.float32(size))
+    at = np.arange(m)
+    k[0] = gr.VALUES[codes[0][table[0, at // 64], 0, :, at % 64]] * np.float64(np.float32(size))
+    q = ref.bf16(rng.standard_normal((1, K * G, d)))
+    got, lse = one_call(torch, dev, q, codes, scales, table, [1], [m - 1], d)
+    score = np.einsum("hd,mhd->hm", ref.f64(q)[0], k[0].repeat(G, 1)) * d ** -0.5
+    bound = (d + 8) * 2.0 ** -23 * (np.einsum("hd,mhd->hm", np.abs(ref.f64(q)[0]), np.abs(k[0]).repeat(G, 1)) * d ** -0.5).max(1)
+    top = score.max(1)
+    assert np.isfinite(got).all() and (np.abs(lse[0] - top) <= bound + np.log(m) + 2.0 ** -21 * np.abs(top)).all()
+    for h in range(K * G):
+        close = score[h] >= top[h] - 2 * bound[h] - 20  # all that may be the largest, and what e^-20 leaves
+        x = v[0][close, h // G]
+        slack = 2.0 ** -7 * np.abs(v[0][:, h // G]).max(0) + 2.0 ** -120
+        assert (got[0, h] >= x.min(0) - slack).all() and (got[0, h] <= x.max(0) + slack).all(), h
