@@ -522,8 +522,13 @@ FM_DEV void clean_values(uint8_t* v, float* scales, int first, Rows<D, NT>& w) {
 // the other (the product may leave fp32's range), and its log-sum-exp.
 FM_DEV float2 row_factors(const KvParams& p, int h, float m, float e, float l) {
   if (l == 0.f) return make_float2(0.f, 0.f);
-  const float z = p.sink ? l + exp2_fast(p.sink[h] * kLog2e - m) : l;
-  const float half = exp2_fast(0.5f * e);
+  float z = l, down = 0.f;
+  if (p.sink) {  // it may be far over the scores, or far below
+    const float sink = p.sink[h] * kLog2e - m;
+    down = fmaxf(sink, 0.f);
+    z = l * exp2_fast(-down) + exp2_fast(sink > 0.f ? 0.f : sink);
+  }
+  const float half = exp2_fast(0.5f * (e - down));
   return make_float2(half, half / z);
 }
 FM_DEV float row_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f; }

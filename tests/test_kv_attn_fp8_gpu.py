@@ -507,3 +507,27 @@ def test_scores_of_millions(torch_dev, size, d, G, m):
         x = v[0][close, h // G]
         slack = 2.0 ** -7 * np.abs(v[0][:, h // G]).max(0) + 2.0 ** -120
         assert (got[0, h] >= x.min(0) - slack).all() and (got[0, h] <= x.max(0) + slack).all(), h
+
+
+@pytest.mark.parametrize("d,G,m", [(64, 1, 40), (128, 2, 700), (64, 30, 700)])
+def test_a_sink_far_over_the_scores(torch_dev, d, G, m):
+    """A sink 60 to 100 nats over every score: the output is as much smaller, to the end of fp32's range, and lse is unchanged."""
+    torch, dev = torch_dev
+    import sparse_attention_kv_c4_gb300 as fm
+    K, rng = 2, np.random.default_rng(d + m)
+    table, codes, scales, k, v, sizes, scale_of, held = make(rng, [1], [m - 1], K * G, K, d)
+    q, H = ref.bf16(rng.standard_normal((1, K * G, d))), K * G
+    cd, sd = up(torch, dev, codes), up(torch, dev, scales)
+    out, lse = torch.zeros((1, H, d), dtype=torch.int16, device=dev), torch.zeros((1, H), device=dev)
+    ws = torch.empty(fm.fm_kv_attn_fp8_workspace(1, H, K, d), dtype=torch.uint8, device=dev)
+    for over in (60.0, 88.0, 95.0, np.inf):
+        sinks = np.full(H, over, np.float32)
+        fm.fm_kv_attn_fp8(up(torch, dev, q.view(np.int16)), cd[0][:, 0], cd[1][:, 0], sd[0][:, 0], sd[1][:, 0], up(torch, dev, table),
+                          torch.tensor([m - 1], device=dev), out, sink_logit=up(torch, dev, sinks), lse_out=lse, workspace=ws)
+        want, want_lse, tol, ltol = gr.attend(ref.f64(q), k[0], v[0] * 1e3, m - 1, FOREVER, sinks, d ** -0.5, held[0], gr.HALF_FP16,
+                                              (sizes[0], scale_of[0] * 1e3))
+        got = ref.f64(out.cpu().numpy().view(np.uint16)) * 1e3
+        # grouped_ref's absolute term of 2^-120 is these outputs' size: a step of bf16's subnormals instead; an exponential of
+        # an argument of 100 is off by 2^-16
+        assert (np.abs(got - want) <= tol - 2.0 ** -120 + 2.0 ** -15 * np.abs(want) + 1e3 * 2.0 ** -133).all(), over
+        assert (np.abs(lse.double().cpu().numpy() - want_lse) <= ltol).all()
