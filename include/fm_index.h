@@ -755,8 +755,9 @@ fm_status fm_kv_attn_fp8(const fm_kv_attn_fp8_args* args);
  *   out     [T, n_h, d] bf16 dense;  lse_out [T, n_h] fp32 or NULL
  *   q, k, v, out 16-byte aligned
  * Scores, softmax statistics and sums are fp32; the softmax weights are rounded to
- * bf16 for the tensor cores' second product.  A sequence's bits depend neither on scheduling
- * nor on the call's other sequences.
+ * bf16 for the tensor cores' second product.  Results for scores beyond 2^24 in magnitude (which fp32 tells apart by
+ * whole units) and for finite values beyond 2^100 are unspecified.  A sequence's bits depend neither on scheduling nor on the
+ * call's other sequences.
  * Errors: FM_ERR_INVALID_ARG, FM_ERR_CUDA.
  */
 typedef struct fm_prompt_attn_args {

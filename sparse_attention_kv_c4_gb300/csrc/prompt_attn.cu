@@ -38,7 +38,7 @@ constexpr int kThreads = 12 * 32;
 constexpr int kChunkBytes = 128 * 128;  // 128 rows x 64 elements
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLow = -1e30f;   // below every score
+constexpr float kLow = -1e30f;   // below every score (past 2^24 a reference's own rounding shows in the weights)
 constexpr float kSlack = 8.f;    // how far a score (in log2) may pass its reference for long,
 constexpr float kFar = 16.f;     // and at all: weights of up to 2^16 leave values room in fp32
 constexpr int kMaxEdge = 16;     // tiles of an item that the mask cuts: at most 2 (256 + 127) / 128 + 2

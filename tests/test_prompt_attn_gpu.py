@@ -216,3 +216,26 @@ def test_other_rows_of_a_tile_have_no_part_in_a_sequences_bits(torch_dev, G, d):
     want, _, tol, _ = gr.attend(ref.f64(q.cpu().numpy().view(np.uint16)), ref.f64(k.cpu().numpy().view(np.uint16)),
                                 ref.f64(v.cpu().numpy().view(np.uint16)), past, FOREVER, None, d ** -0.5)
     assert (np.abs(ref.f64(results[0][0].cpu().numpy().view(np.uint16)) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("size", [100.0, 600.0])
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 5)])
+def test_scores_of_millions(torch_dev, size, d, G):
+    """Scores of up to 2^23, whose spacing in fp32 is coarse: out is finite and a mean of the values whose scores may be the
+    largest."""
+    torch, dev = torch_dev
+    K, n, rng = 2, 300, np.random.default_rng(int(np.log2(size)) + d)
+    q, k, v = ref.bf16(size * rng.standard_normal((n, K * G, d))), ref.bf16(size * rng.standard_normal((n, K, d))), ref.bf16(rng.standard_normal((n, K, d)))
+    got, lse, _, _ = call(torch, dev, q, k, v, [n], [0], None, None, None, 0)
+    f, qf, kf, vf = ref.f64(got), ref.f64(q), ref.f64(k), ref.f64(v)
+    assert np.isfinite(f).all()
+    for h in range(K * G):
+        score = qf[:, h] @ kf[:, h // G].T * d ** -0.5
+        score[np.triu_indices(n, 1)] = -np.inf
+        bound = ((d + 8) * 2.0 ** -23 * (np.abs(qf[:, h]) @ np.abs(kf[:, h // G]).T) * d ** -0.5 * np.tri(n)).max(1)
+        top = score.max(1)
+        assert (np.abs(lse[:, h] - top) <= bound + np.log(n) + 2.0 ** -21 * np.abs(top)).all()
+        for i in range(n):
+            x = vf[score[i] >= top[i] - 2 * bound[i] - 20, h // G]
+            slack = 2.0 ** -6 * np.abs(vf[:, h // G]).max(0)
+            assert (f[i, h] >= x.min(0) - slack).all() and (f[i, h] <= x.max(0) + slack).all(), (h, i)
