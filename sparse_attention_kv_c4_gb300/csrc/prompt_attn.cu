@@ -340,10 +340,14 @@ FM_DEV bool softmax_item(const PromptParams& p, Smem<D>& sh, int slot, uint32_t 
   if (!__all_sync(0xffffffffu, ok)) return false;
   const float sum = l.x + l.y;
   const int h = w.head * p.G + r - t * p.G;
-  float z = sum;
-  if (live && p.sink) z += exp2_fast(p.sink[h] * kLog2e - m);
+  float z = sum, half = 1.f;
+  if (live && p.sink) {  // it may be far over the scores: the output is then scaled in two steps
+    const float sink = p.sink[h] * kLog2e - m, down = fmaxf(sink, 0.f);
+    half = exp2_fast(-0.5f * down);
+    z = sum * exp2_fast(-down) + exp2_fast(sink > 0.f ? 0.f : sink);
+  }
   const bool some = n > 0 && sum != 0.f;  // the row sees a key
-  const float inv = some ? 1.f / z : 0.f;
+  const float inv = some ? half / z : 0.f;
   const int64_t at = (int64_t)(w.q0 + token) * p.n_h + h;
   uint16_t* out = p.out + at * p.d;
 #pragma unroll 1
@@ -359,7 +363,7 @@ FM_DEV bool softmax_item(const PromptParams& p, Smem<D>& sh, int slot, uint32_t 
       uint32_t y[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        y[k] = some ? floats_bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv) : 0u;
+        y[k] = some ? floats_bf16x2(__uint_as_float(o[e + 2 * k]) * half * inv, __uint_as_float(o[e + 2 * k + 1]) * half * inv) : 0u;
       *reinterpret_cast<uint4*>(out + 32 * i + e) = make_uint4(y[0], y[1], y[2], y[3]);
     }
     __syncwarp();  // the next load from TMEM is the whole warp's

@@ -239,3 +239,19 @@ def test_scores_of_millions(torch_dev, size, d, G):
             x = vf[score[i] >= top[i] - 2 * bound[i] - 20, h // G]
             slack = 2.0 ** -6 * np.abs(vf[:, h // G]).max(0)
             assert (f[i, h] >= x.min(0) - slack).all() and (f[i, h] <= x.max(0) + slack).all(), (h, i)
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 5)])
+def test_a_sink_far_over_the_scores(torch_dev, d, G):
+    """A sink 60 to 100 nats over every score: the output is as much smaller, to the end of fp32's range, and lse is unchanged."""
+    torch, dev = torch_dev
+    K, n, rng = 2, 300, np.random.default_rng(d)
+    q, k, v = (ref.bf16(rng.standard_normal(s)) for s in ((n, K * G, d), (n, K, d), (n, K, d)))
+    for over in (60.0, 88.0, 95.0, np.inf):
+        sinks = np.full(K * G, over, np.float32)
+        got, lse, _, _ = call(torch, dev, q, k, v, [n], [0], None, sinks, None, 0)
+        want, want_lse, tol, ltol = gr.attend(ref.f64(q), ref.f64(k), ref.f64(v) * 2.0 ** 60, 0, FOREVER, sinks, d ** -0.5)
+        # grouped_ref's absolute term of 2^-120 is these outputs' size, so values are 2^60 times as large there; a step of
+        # bf16's subnormals; an exponential of an argument of 100 is off by 2^-16
+        assert (np.abs(ref.f64(got) * 2.0 ** 60 - want) <= tol + 2.0 ** -15 * np.abs(want) + 2.0 ** (60 - 133)).all(), over
+        assert (np.abs(lse - want_lse) <= ltol).all()
