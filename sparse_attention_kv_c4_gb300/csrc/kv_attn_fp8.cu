@@ -50,7 +50,8 @@ constexpr float kSlack = 8.f;           // how far a score (in log2) may pass it
 // moves, up or down, when a tile's largest passes 2^15 (fp16 ends at 65504) or stays below 2^-3: each is then off by 2^-11
 // of itself or 2^-22 of its tile's largest (half of fp16's smallest step).  (With a range that only went up, a key e^16
 // over the others whose value was zero left them to fp16's subnormals: 12% off.)  O, in fp32, is in units of 2^-g; g goes
-// up no further than leaves O below 2^kTop.  All of it is relative: scores of 10^9 lose fp32's digits, but no range.
+// up no further than leaves O below 2^kTop.  All of it is relative to the reference: scores of 10^9 lose
+// fp32's digits, but no range.
 constexpr float kLead = 12.f, kMost = 15.f, kLeast = -3.f, kTop = 100.f;
 constexpr float kUnset = 3e38f;         // g of a row that has not met a key
 constexpr float kNoKey = -3.402823466e38f;  // a part's reference where it has none
@@ -302,13 +303,13 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
     vs[block] = scales[1][at + block];
     log_vs[block] = fmaxf(__log2f(vs[block]), -200.f);  // a scale of zero has one too
   }
-  // scores in log2, relative to their references
+  // scores in log2
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int block = 0; block < Blocks; ++block)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[block][nt][i] = fmaf(s[block][nt][i], ks[block] * w.f[nt][i & 1], -w.m[nt][i & 1]);
+      for (int i = 0; i < 4; ++i) s[block][nt][i] *= ks[block] * w.f[nt][i & 1];
   if (partial) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -320,7 +321,7 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
           if (j > w.pos[nt][i & 1] || j < w.low[nt][i & 1]) s[block][nt][i] = -INFINITY;
         }
   }
-  // the largest of the lane's, and of them times V's scale
+  // the largest of the lane's over their references, and of them times V's scale
   bool passes = false, low = false;
   float top[NT][2], topv[NT][2];
 #pragma unroll
@@ -330,7 +331,7 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
       top[nt][i] = topv[nt][i] = -INFINITY;
 #pragma unroll
       for (int block = 0; block < Blocks; ++block) {
-        const float x = fmaxf(s[block][nt][i], s[block][nt][i + 2]);
+        const float x = fmaxf(s[block][nt][i], s[block][nt][i + 2]) - w.m[nt][i];
         top[nt][i] = fmaxf(top[nt][i], x);
         topv[nt][i] = fmaxf(topv[nt][i], x + log_vs[block]);
       }
@@ -382,25 +383,21 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float x = top[nt][i];
+          float x = -INFINITY, xv = -INFINITY;
+#pragma unroll
+          for (int block = 0; block < Blocks; ++block) x = fmaxf(x, fmaxf(s[block][nt][i], s[block][nt][i + 2]));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-          // The reference of scores becomes the largest so far; of the row's first keys even if it is below zero.  The
-          // tile's scores move by what lies between, not by the rounded references' difference: the largest is at zero.
+          // the reference of scores: the largest so far; of the row's first keys even if it is below zero
           const bool first_keys = w.g[nt][i] == kUnset && x > -INFINITY;
-          const float by = x > 0.f || first_keys ? x : 0.f;
-          float xv = -INFINITY;
+          const float m = first_keys ? x : fmaxf(w.m[nt][i], x), by = m - w.m[nt][i];
 #pragma unroll
-          for (int block = 0; block < Blocks; ++block) {
-            s[block][nt][i] -= by;
-            s[block][nt][i + 2] -= by;
-            xv = fmaxf(xv, fmaxf(s[block][nt][i], s[block][nt][i + 2]) + log_vs[block]);
-          }
+          for (int block = 0; block < Blocks; ++block) xv = fmaxf(xv, fmaxf(s[block][nt][i], s[block][nt][i + 2]) - m + log_vs[block]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) xv = fmaxf(xv, __shfl_xor_sync(0xffffffffu, xv, o));
           const float from = first_keys ? INFINITY : w.g[nt][i] + by, to = fminf(from, kLead - xv), keep = exp2_fast(to - from);
           w.l[nt][i] *= first_keys ? 0.f : exp2_fast(-by);
-          w.m[nt][i] += by;
+          w.m[nt][i] = m;
           w.g[nt][i] = to;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
@@ -426,7 +423,7 @@ FM_DEV void key_blocks(uint32_t kv_smem, const float (*scales)[kBlocksPerPage], 
       for (int i = 0; i < 2; ++i) unit[i] = __fmul_rz(__fmul_rz(vs[block], half[i]), half[i]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = exp2_fast(s[block][nt][i]);
+        const float e = exp2_fast(s[block][nt][i] - w.m[nt][i & 1]);
         w.l[nt][i & 1] += e;
         x[i] = e * unit[i & 1];
       }

@@ -531,3 +531,21 @@ def test_a_sink_far_over_the_scores(torch_dev, d, G, m):
         # an argument of 100 is off by 2^-16
         assert (np.abs(got - want) <= tol - 2.0 ** -120 + 2.0 ** -15 * np.abs(want) + 1e3 * 2.0 ** -133).all(), over
         assert (np.abs(lse.double().cpu().numpy() - want_lse) <= ltol).all()
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 2), (64, 30)])
+@pytest.mark.parametrize("far", [2000.0, 1e6])
+def test_scores_that_rise_from_far_below_keep_their_digits(torch_dev, d, G, far):
+    """The first pages' scores lie `far` below the others', in one run: the others' weights and lse are as exact as without them."""
+    torch, dev = torch_dev
+    K, m, B, rng = 2, 640, 532, np.random.default_rng(int(far) + d)
+    table, codes, scales, k, v, size, scale_of, held = make(rng, [1], [m - 1], K * G, K, d)
+    q, at = ref.bf16(rng.standard_normal((1, K * G, d))), np.arange(m)
+    q[..., 0] = ref.bf16(np.full(1, far * d ** 0.5 / 4))
+    codes[0][table[0], 0, :, :, 0] = 0
+    codes[0][table[0][:3], 0, :, :, 0] = 0xC8  # -4, with a scale of 1 beside it
+    scales[0][table[0][:3]] = 1.0
+    k[0] = gr.VALUES[codes[0][table[0, at // 64], 0, :, at % 64]] * scales[0][table[0, at // 64], 0, :, at % 64 // 16].astype(np.float64)[..., None]
+    got, lse = one_call(torch, dev, q.repeat(B, 0), codes, scales, table.repeat(B, 0), [1] * B, [m - 1] * B, d)
+    want, want_lse, tol, ltol = gr.attend(ref.f64(q), k[0], v[0], m - 1, FOREVER, None, d ** -0.5, held[0], gr.HALF_FP16, (size[0], scale_of[0]))
+    assert (np.abs(got - want) <= tol).all() and (np.abs(lse - want_lse) <= ltol).all()
