@@ -643,8 +643,7 @@ fm_status fm_csa_attn_packed(const fm_csa_attn_args* args);
  * earlier codes c become e4m3(e4m3(c) * old / need).  An entry x becomes
  * e4m3(x * (1 / scale)), rounded once from fp32, ties to even; a turned pair that fp32's rounding may
  * have carried over the middle between two codes, or a block's largest entry over 448 times a power of two, is turned in
- * fp64.  Infinities and NaN do not
- * count for amax and are stored as NaN (0x7F).
+ * fp64.  Infinities and NaN do not count for amax and are stored as NaN (0x7F).
  *   A page that several sequences share may be appended to by one of them only, and a call's
  * tokens are on pages that differ (a table that names one page twice leaves its cells unspecified).
  *   A negative start[b] leaves sequence b out; a token whose page is not held or out
@@ -696,7 +695,7 @@ fm_status fm_kv_append_fp8(const fm_kv_append_fp8_args* args);
  * Cells that are no keys of a token have no part in its result, whatever they hold.
  *
  *   q          [T, n_h, d] bf16, token stride q_stride_t; 1 <= n_h <= 1024
- *   start      [B] int64, cu_tokens [B + 1] or NULL, as for fm_kv_append_fp8
+ *   start      [B] int64, cu_tokens [B + 1] or NULL, as for fm_kv_append_fp8 (a negative start: tokens without keys)
  *   window     >= 0 (0: no keys); INT64_MAX: no limit
  *   scales     positive and finite; any fp32 ones, powers of two or not
  *   scale      > 0 (scale * log2 e finite), d^-1/2 as a rule
@@ -708,7 +707,8 @@ fm_status fm_kv_append_fp8(const fm_kv_append_fp8_args* args);
  * operands.  Queries are scaled by their row's largest; a weight times scale is off by 2^-11 of itself, or by 2^-22 of the
  * largest of its page of 64 tokens if that is more (other pages' weights, however large, cost it nothing).
  * A key whose score is 77 or more below its row's largest may count for less than its weight, down to nothing.
- * The result does not depend on scheduling.
+ * The result does not depend on scheduling; where a sequence's work is cut, and so its rounding, depends on the
+ * call's other sequences.
  * Errors: FM_ERR_INVALID_ARG, FM_ERR_WORKSPACE, FM_ERR_CUDA.
  */
 typedef struct fm_kv_attn_fp8_args {

@@ -70,7 +70,7 @@ FM_DEV int warp_find(int n, int64_t x, Key key) {
   return lo;
 }
 
-// The kinds of argument that the three calls have in common; "" or what is wrong.
+// The kinds of argument that the three calls have in common; nullptr or what is wrong.
 inline const char* bad_heads(int n_h, int n_k, int d) {
   if (n_h < 1 || n_h > 1024 || n_k < 1 || n_h % n_k != 0 || n_h / n_k > 128)
     return "1 <= n_h <= 1024, n_h a multiple of n_k, n_h / n_k <= 128";

@@ -15,7 +15,8 @@
 // magnitude is one shuffle tree.  The block's (cos, sin) are worked out once per CTA
 // for its eight heads, from a 64-bit fixed-point fraction of a turn (as in
 // qk_norm_rope.cu: the wrap of one integer product is the reduction).
-// Measured: 4096 tokens x (64 + 2 x 8) heads x 128 38 us (4.2 TB/s; bound by issue, 67% of the slots), one token 4.3 us.
+// Measured: 4096 tokens x (64 + 2 x 8) heads x 128 39.5 us (4.0 TB/s; 66% of the issue slots, then waits for shared memory: more
+// than half of the loads' wavefronts are bank conflicts, of the sines), one token 4.4 us.
 // A CTA finds its block by itself: sequence b's blocks begin at slot cu[b] / 16 + 2 b,
 // which leaves room for the two blocks that a sequence may touch beyond n / 16.
 #include <cuda_fp8.h>

@@ -4,8 +4,8 @@
 //     s_j = scale (q . k_j),  out = sum_j e^{s_j} v_j / (sum_j e^{s_j} + e^{sink}),
 // k_j = e4m3(code) * scale of its block of 16 tokens and head, v_j alike.
 //
-// A cell is read once for all rows (token, query head) that share its head: 2 d bytes
-// for 4 d flops a row, so the kernel is bound by HBM up to some 30 rows.
+// A cell is read once for each tile of up to 24 (d <= 64: 32) of the rows (token, query head) that share
+// its head, 2 d bytes for 4 d flops a row: bound by HBM up to 16 rows, by the warps' own work beyond.
 //
 // The work is the list of units (sequence, key head, row tile, page of 64 tokens), cut into
 // as many equal runs as there are warps, seven to an SM, whatever the sequences' lengths;
@@ -14,9 +14,9 @@
 //   S^T = K Q^T   m16n8k16, 16 keys (one block of scales) x 8 rows, fp16 operands:
 //                 E4M3 is exact in fp16, queries are scaled to 2^14 by row
 //   softmax       against a running reference that moves only when a score
-//                 passes it by 2^8: most tiles need no reduction over lanes
+//                 passes it by 8 (in log2): most tiles need no reduction over lanes
 //   O^T += V^T P^T  the weights times the block's scale of V in fp16, kept in its range by
-//                 a reference of their own, which follows the tiles' largest weight times scale up and down
+//                 a unit of their own, which follows the tiles' largest weight times scale up and down
 // The transposed products take rows in eights, and their operands come from the
 // cache's rows as they lie: a lane's 16 bytes of a key are four steps of K16 (the order of
 // the contraction is free), ldmatrix transposes V by pairs of bytes.  mma.sync, not tcgen05:
@@ -26,7 +26,7 @@
 // of 1K to 32K took 209 us where 30 of 17K took 164.)
 // Measured, calls queued on a stream, inputs in rotation: 30 tokens x 64 heads over 1K to 32K cells of 8 x 128
 // 173 us (6.0 TB/s; 161 us the first kernel, 96% of the measured copy rate), one token x 32 heads over 1M cells of
-// 4 x 128 177 us, 8 x 5 drafted tokens x 40 heads over 8191 cells of 8 x 64 42 us, 37 cells 10 us.
+// 4 x 128 176 us, 8 x 5 drafted tokens x 40 heads over 8191 cells of 8 x 64 43.5 us, 37 cells 10 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -168,11 +168,11 @@ FM_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
       : "memory");
 }
 
+FM_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // Row r of eight in a fragment is key row_key(r) of its eight keys, and a cell's 16-byte
 // chunk lies where the TMA's swizzle put it: with this order the eight lanes of a
 // 16-byte load, and the eight rows of an ldmatrix, meet eight different chunks.
-FM_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
 template <int D>
 FM_DEV int row_key(int r) { return D == 128 ? (r >> 1) | ((r & 1) << 2) : r; }
 template <int D>

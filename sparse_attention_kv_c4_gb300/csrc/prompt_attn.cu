@@ -20,8 +20,9 @@
 // TMEM: S 2 x 128 columns, O 2 x D, P 2 x 64 (at D = 128 in S's place).
 // A block takes over the items of blocks that have not started (cluster launch control).
 // What bounds it: at D = 128 a step of both row tiles takes 2940 cycles, 2048 of them products; S starts some 450
-// after the O before it has ended (its end has to be known, as P lies in S's place), twice a step.  At D =
-// 64 the exponentials take as long as the products, 1024 cycles a step.
+// after the O before it has ended (its end has to be known, as P lies in S's place), twice a step.  At D = 64 a
+// step takes some 3000, three times what its products or its exponentials need: the softmax warps' chain (scores from
+// TMEM, all maxima, then all exponentials, then the stores), one tile after the other.
 // Measured, calls queued on a stream, inputs in rotation: 8192 tokens x 32 heads x 128 391 us (1.41 PFLOP/s,
 // 75% of a library product's burst rate), 4 x up to 4096 x 32 x 64 in a window of 1021 168 us, 2935 tokens of
 // five prompts x 20 x 96 25 us, 37 tokens 8 us.
